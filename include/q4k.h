@@ -69,7 +69,8 @@ typedef enum {
     Q4K_ERR_DEVICE = 5,
     Q4K_ERR_CUDA = 6,
     Q4K_ERR_TIMEOUT = 7,
-    Q4K_ERR_ROUTING = 8
+    Q4K_ERR_ROUTING = 8,
+    Q4K_ERR_INDEX = 10 /* 9 is not assigned */
 } q4k_status;
 
 /* Static English text for a status code; never NULL. */
@@ -88,8 +89,10 @@ int q4k_version(void);
 /* Synchronizes `stream`, then reads and clears the device status word that the
  * kernels set when a bounded wait gives up (Q4K_ERR_TIMEOUT) or when a call of
  * q4k_moe_grouped_gemm_reuse_routing found no routing for its shape in its
- * workspace (Q4K_ERR_ROUTING; a timeout is reported first).  Returns Q4K_OK,
- * one of those two, or Q4K_ERR_CUDA if the synchronization itself failed. */
+ * workspace (Q4K_ERR_ROUTING), or when a call on a paged cache read an index from
+ * device memory that is out of range (Q4K_ERR_INDEX).  The first of these, in this
+ * order, that was recorded since the last check is reported.  Returns Q4K_OK, one
+ * of those three, or Q4K_ERR_CUDA if the synchronization itself failed. */
 q4k_status q4k_check_device(void *stream);
 
 /* Declares whether the weight matrices read by the small-M calls (q4k_gemv,
@@ -407,6 +410,171 @@ q4k_status q4k_moe_ffn(const void *w_gate, const void *w_up, const void *w_down,
 q4k_status q4k_moe_grouped_gemm_noalloc(const void *w_experts, int32_t n_experts, int64_t N, int64_t K,
                                         const uint16_t *x, int x_mode, const int32_t *topk_ids, const float *gates,
                                         int64_t T, int32_t topk, float *y, int y_mode, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The operators between a decode step's weight products: closing one block and
+ * opening the next (q4k_norm_residual), writing new keys and values into a paged
+ * cache (q4k_kv_append), attention of the new tokens over that cache
+ * (q4k_attn_decode), shrinking a cache to a budget (q4k_kv_evict) and drawing the
+ * next tokens (q4k_sample).  Their fp32 inputs are what the weight products write,
+ * and their bf16 outputs what those read.
+ *
+ * A sequence's cache is a list of SLOTS 0 .. len - 1, one per cached token, kept in
+ * pages of page_size slots.  Slot j of sequence b lies in page
+ * page_table[b*ld_table + j / page_size] at row j % page_size; the D values of KV
+ * head h there start at element
+ *     page*page_stride + h*head_stride + (j % page_size)*slot_stride
+ * of both pools, which covers [page][head][slot][D], [page][slot][head][D] and pools
+ * that interleave keys and values.  Slots carry no order: rotary positions are in
+ * the keys, and the caller may keep each slot's position (and the attention weight
+ * it received) in the arrays `positions` and `weights` [batch][n_kv_heads][ld_meta].
+ *
+ * Indices read from device memory are checked in the kernels: a page id outside
+ * [0, n_pages), a length above max_pages*page_size, a sequence, slot or position out
+ * of range records Q4K_ERR_INDEX for q4k_check_device, and the slot or token that it
+ * belongs to is left out (a length counts as clamped to what the table or the
+ * metadata can hold). Negative lengths count as 0. Two sequences may share pages
+ * that neither writes. */
+
+#define Q4K_KV_BF16 0 /* cache of bf16 */
+#define Q4K_KV_E4M3 1 /* cache of e4m3 (fp8): the value stands for itself times k_scale or v_scale */
+
+typedef struct {
+    void *k, *v;               /* pools: 16-byte aligned device pointers */
+    const int32_t *page_table; /* device, [batch][ld_table] */
+    int64_t ld_table;          /* >= max_pages */
+    int64_t n_pages;           /* pages in each pool */
+    int64_t page_stride, head_stride, slot_stride; /* in elements, >= 1, multiples of 16 bytes */
+    int32_t batch;             /* sequences, 1 .. 65535 */
+    int32_t max_pages;         /* table entries per sequence; max_pages*page_size < 2^31 */
+    int32_t page_size;         /* slots per page, >= 1 */
+    int32_t n_kv_heads;        /* 1 .. 1024 */
+    int32_t head_dim;          /* D: 64, 128 or 256 */
+    int32_t dtype;             /* Q4K_KV_BF16 or Q4K_KV_E4M3 */
+    float k_scale, v_scale;    /* > 0; 1 for a plain cache */
+} q4k_kv_cache;
+
+#define Q4K_ROPE_HALF 0  /* value i pairs with value i + rope_dim/2 */
+#define Q4K_ROPE_PAIRS 1 /* value 2i pairs with value 2i + 1 */
+
+/* Rotary embedding of T new tokens' queries and keys, and the write of their keys
+ * and values into the cache: for token t of sequence seq[t], slot slot[t],
+ *     (a, b) -> (a*cos - b*sin, b*cos + a*sin)   over the first rope_dim values of
+ * each q and k head, each product and sum rounded to fp32, cos and sin from row
+ * pos[t] of `rope`; q is rounded once to bf16 into q_out, k/k_scale and v/v_scale
+ * (computed as a product with the fp32 reciprocal) once to the cache's type.  For
+ * e4m3, values beyond +-448 become +-448 and NaN stays NaN.
+ *   q [T][ldq], k [T][ldk], v [T][ldv]: fp32, heads consecutive in a row, 4-byte
+ *     aligned.  They may be columns of one product's output.
+ *   seq, slot, pos: int32 [T]; no two tokens with the same (seq, slot).
+ *   rope: fp32 [n_pos][rope_dim], row = rope_dim/2 cosines, then rope_dim/2 sines;
+ *     rope_dim even, 0 .. D; 0: no rotation (rope may be NULL, pos is then only
+ *     written to positions).  With rope_dim > 0, pos[t] must be in [0, n_pos).
+ *   q_out bf16 [T][ldqo].  q and q_out may both be NULL (keys and values only).
+ *   weights, positions (each may be NULL): slot[t]'s entry of every head becomes
+ *     0 and pos[t]; with either, slot[t] must be < ld_meta.
+ * A token with an index out of range is recorded (Q4K_ERR_INDEX) and leaves the
+ * cache, weights and positions alone; its q_out row becomes 0. */
+q4k_status q4k_kv_append(const q4k_kv_cache *cache, int64_t T, int32_t n_heads, const float *q, int64_t ldq,
+                         const float *k, int64_t ldk, const float *v, int64_t ldv, const int32_t *seq,
+                         const int32_t *slot, const int32_t *pos, const float *rope, int64_t n_pos, int32_t rope_dim,
+                         int rope_mode, uint16_t *q_out, int64_t ldqo, float *weights, int32_t *positions,
+                         int64_t ld_meta, void *stream);
+
+/* Attention of the last n_q tokens of every sequence over its cache.
+ *   s[r][j] = scale * k_scale * q[r] . k[j]   (with softcap c > 0: c*tanh(s/c))
+ *   o[r]    = v_scale * sum_j softmax_j(s[r])[j] * v[j]
+ * Row r is query token i (0 <= i < n_q) and head hq of sequence b; it reads KV head
+ * hq / (n_heads/n_kv_heads) at slots [max(0, e - window), e), e = len - n_q + 1 + i
+ * (window 0: all of [0, e)).  len = seq_lens[b] counts the n_q tokens themselves
+ * (q4k_kv_append writes them first).  A row that reads nothing (e <= 0) gives 0.  A slot outside a
+ * row's range has no part in it, whatever its key and value hold.
+ *   q, o: bf16 [batch*n_q][ldq], [batch*n_q][ldo], row b*n_q + i, heads of D
+ *     consecutive; 16-byte aligned, ldq and ldo multiples of 8.
+ *   n_heads: a multiple of n_kv_heads; n_q 1 .. 64.
+ *   weights (may be NULL): fp32 [batch][n_kv_heads][ld_weights], updated for every
+ *     slot j < len:  weights[b][h][j] = decay*weights[b][h][j] + sum of
+ *     softmax(s[r])[j] over the rows r of head h.  len must be <= ld_weights.
+ * Products are exact and sums, maxima and the joined softmax fp32; the weights p
+ * enter the product with v as the sum of two 16-bit values (to about 2^-16), and o is
+ * rounded once.  The length is split over the whole GPU by the lengths of the batch,
+ * and the parts are joined in slot order: the same call repeats its bits, but a
+ * sequence's last bits may depend on the other lengths of its batch, also in
+ * batch-invariant mode.
+ * Workspace: q4k_attn_decode_workspace_size(cache, n_heads, n_q, ld_weights, or 0
+ * without weights) bytes, 256-byte aligned; 0 is returned for arguments that the call
+ * would refuse. */
+size_t q4k_attn_decode_workspace_size(const q4k_kv_cache *cache, int32_t n_heads, int32_t n_q, int64_t ld_weights);
+q4k_status q4k_attn_decode(const q4k_kv_cache *cache, const int32_t *seq_lens, const uint16_t *q, int64_t ldq,
+                           int32_t n_heads, int32_t n_q, float scale, float softcap, int64_t window, uint16_t *o,
+                           int64_t ldo, float *weights, int64_t ld_weights, float decay, void *ws, size_t ws_bytes,
+                           void *stream);
+
+/* Eviction: every sequence longer than `budget` slots is cut to budget, each KV head
+ * by its own weights.  Of a head's slots, the len - budget ones with the smallest
+ * weight go (equal weights: the lowest slot first; NaN counts as larger than all),
+ * among those that are not protected; protected are positions < sinks and positions
+ * > newest - recent, newest being the head's largest position.  (Should more than
+ * budget slots be protected, protected ones go too, by the same order.)  The slots
+ * freed below budget are filled, in increasing order, with the kept slots at or above
+ * it, in increasing order; the other kept slots stay where they are.  So pages from
+ * ceil(budget/page_size) on are free afterwards, and pages must not be shared between
+ * sequences below that.
+ *   weights, positions: [batch][n_kv_heads][ld_meta]; weights_out and positions_out
+ *     receive the entries of the slots < new length (each may be the input array;
+ *     otherwise they must not overlap it).
+ *   new_lens[b] = min(len, budget); may be seq_lens.  len must be <= ld_meta.
+ *   1 <= budget; 0 <= sinks, recent; sinks + recent <= budget.
+ * Workspace: q4k_kv_evict_workspace_size(cache, ld_meta) bytes, 256-byte aligned. */
+size_t q4k_kv_evict_workspace_size(const q4k_kv_cache *cache, int64_t ld_meta);
+q4k_status q4k_kv_evict(const q4k_kv_cache *cache, const int32_t *seq_lens, int32_t *new_lens, int64_t budget,
+                        int64_t sinks, int64_t recent, const float *weights, const int32_t *positions,
+                        float *weights_out, int32_t *positions_out, int64_t ld_meta, void *ws, size_t ws_bytes,
+                        void *stream);
+
+#define Q4K_NORM_NONE 0
+#define Q4K_NORM_RMS 1   /* x / sqrt(mean(x^2) + eps) * w + b */
+#define Q4K_NORM_LAYER 2 /* the same of x - mean(x) */
+#define Q4K_RES_FP32 0
+#define Q4K_RES_BF16 1
+
+/* The end of one block and the start of the next, for M rows of D values:
+ *     h = r_in + scale * gate * post(y)      r_out = h      x = bf16(pre(h))
+ * post and pre are norms over a row (kinds above); y fp32 [M][ldy], may be NULL (h =
+ * r_in).  *_w and *_b fp32 [D], each may be NULL (1 and 0); not read for
+ * Q4K_NORM_NONE.  gate fp32 [M][ld_gate], or one row for all with ld_gate = 0, or
+ * NULL (1).  r_in and r_out [M][ldr] of type r_dtype; r_out may be r_in, or NULL (not
+ * kept).  x bf16 [M][ldx], may be NULL if r_out is not (pre is then not computed).
+ * Everything is fp32 until r_out and x are rounded once each; x comes from h before
+ * r_out's rounding.  1 <= D <= 2^20; pointers aligned to their element. */
+q4k_status q4k_norm_residual(int64_t M, int64_t D, const float *y, int64_t ldy, int post, const float *post_w,
+                             const float *post_b, float post_eps, const float *gate, int64_t ld_gate, float scale,
+                             const void *r_in, void *r_out, int64_t ldr, int r_dtype, int pre, const float *pre_w,
+                             const float *pre_b, float pre_eps, uint16_t *x, int64_t ldx, void *stream);
+
+/* Draws token[m] from row m of logits [M][ldl] (fp32, V values) with the given random
+ * number u[m] in [0, 1).  Per row: temperature, top_k, top_p and min_p (device arrays
+ * [M]; each may be NULL: 1, off, off, off).
+ *   NaN logits count as -inf.  Tokens are ranked by logit, equal ones by index.
+ *   Weights are whole numbers, so that every sum and comparison below is exact and the
+ *   token depends on no order of summation: with z the largest logit and
+ *     d = (z - logit) * ((1/temperature) * log2(e)) in fp32, left to right,
+ *     w = floor(P(d) * 2^40), where 2^-d = 2^-n 2^-f, n = floor(d), and P is 2^-n times
+ *   the fp32 Horner form of the series of 2^-f about f = 1/2 to the 7th power (each
+ *   product and sum rounded); w = 0 from d >= 41 on.
+ *   top_k > 0 keeps the top_k first in rank.  top_p < 1 keeps the shortest run of
+ *   these, in rank, whose weights reach floor(S*floor(top_p*2^24)/2^24), S the sum of what top_k
+ *   kept, and at least one.  min_p > 0 keeps the tokens whose weight is at least
+ *   floor(W*floor(min_p*2^24)/2^24), W the largest weight.  Over the kept tokens by
+ *   index, token is the first whose running sum exceeds floor(S'*floor(u*2^24)/2^24),
+ *   S' being their sum.  prob[m] (may be NULL) = w/S'.
+ *   temperature <= 0 or NaN: the first in rank, prob 1.  A row without any logit above
+ *   -inf: token -1, prob 0.  top_p and min_p are clamped to [0, 1], u to [0, 1 -
+ *   2^-24]; NaN counts as off (0 for u).
+ * 1 <= V <= 2^22, ldl >= V; pointers aligned to their element. */
+q4k_status q4k_sample(const float *logits, int64_t M, int64_t V, int64_t ldl, const float *temperature,
+                      const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *token,
+                      float *prob, void *stream);
 
 #ifdef __cplusplus
 }

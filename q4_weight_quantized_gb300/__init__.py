@@ -16,8 +16,13 @@ LIB_PATH = os.path.join(_PKG, "libq4k.so")
 
 Q4K_OK, Q4K_ERR_NULL, Q4K_ERR_SHAPE, Q4K_ERR_ALIGN = 0, 1, 2, 3
 Q4K_ERR_WORKSPACE, Q4K_ERR_DEVICE, Q4K_ERR_CUDA, Q4K_ERR_TIMEOUT, Q4K_ERR_ROUTING = 4, 5, 6, 7, 8
+Q4K_ERR_INDEX = 10
 Q4K_MOE_X_PER_TOKEN, Q4K_MOE_X_PER_SLOT = 0, 1
 Q4K_MOE_Y_PER_SLOT, Q4K_MOE_Y_COMBINE = 0, 1
+Q4K_KV_BF16, Q4K_KV_E4M3 = 0, 1
+Q4K_ROPE_HALF, Q4K_ROPE_PAIRS = 0, 1
+Q4K_NORM_NONE, Q4K_NORM_RMS, Q4K_NORM_LAYER = 0, 1, 2
+Q4K_RES_FP32, Q4K_RES_BF16 = 0, 1
 
 BLOCK_BYTES = 144
 QK = 256
@@ -29,10 +34,37 @@ EXPORTS = (
     "q4k_moe_route", "q4k_moe_workspace_size", "q4k_moe_grouped_gemm", "q4k_moe_grouped_gemm_reuse_routing",
     "q4k_moe_grouped_gemm_noalloc", "q4k_moe_ffn_workspace_size", "q4k_moe_ffn", "q4k_quantize_x8", "q4k_gemm_x8_workspace_size", "q4k_gemm_x8",
     "q4k_nvfp4_dequant", "q4k_nvfp4_gemm",
+    "q4k_kv_append", "q4k_attn_decode_workspace_size", "q4k_attn_decode", "q4k_kv_evict_workspace_size", "q4k_kv_evict",
+    "q4k_norm_residual", "q4k_sample",
 )
 
 # fixed scratch capacity of q4k_moe_grouped_gemm_noalloc (Q4K_MOE_NOALLOC_SCRATCH_BYTES)
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
+
+
+class KvCache(ctypes.Structure):
+    """q4k_kv_cache of include/q4k.h.  kv_cache() fills one from tensors."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("ld_table", ctypes.c_int64), ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
+
+
+def kv_cache(k, v, page_table, k_scale: float = 1.0, v_scale: float = 1.0) -> KvCache:
+    """Descriptor of a paged cache: k and v [n_pages][n_kv_heads][page_size][head_dim] (bf16 or float8_e4m3fn, any
+    strides with unit stride last, the same for both), page_table int32 [batch][max_pages].  It holds addresses only:
+    the caller keeps the tensors."""
+    import torch
+    if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4 or k.stride(3) != 1:
+        raise ValueError("k and v must be 4-D with the same shape, strides and type, and unit stride last")
+    types = {torch.bfloat16: Q4K_KV_BF16, torch.float8_e4m3fn: Q4K_KV_E4M3}
+    if k.dtype not in types or page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise ValueError("k and v are bfloat16 or float8_e4m3fn, page_table int32 [batch][max_pages]")
+    return KvCache(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), max(page_table.stride(0), page_table.shape[1]),
+                   k.shape[0], k.stride(0), k.stride(1), k.stride(2), page_table.shape[0], page_table.shape[1],
+                   k.shape[2], k.shape[1], k.shape[3], types[k.dtype], k_scale, v_scale)
 
 
 class Q4KError(RuntimeError):
@@ -55,6 +87,7 @@ def load(path: str | None = None):
         raise ImportError(f"{p} is missing; build it with q4_weight_quantized_gb300.build.build_library()")
     lib = ctypes.CDLL(p)
     P, i64, i32, sz, st = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int
+    f32, C = ctypes.c_float, ctypes.POINTER(KvCache)
     sig = {
         "q4k_status_string": ([st], ctypes.c_char_p),
         "q4k_last_cuda_error": ([], st),
@@ -81,6 +114,14 @@ def load(path: str | None = None):
         "q4k_gemm_x8": ([P, i64, i64, P, P, i64, P, i64, P, sz, P], st),
         "q4k_nvfp4_dequant": ([P, ctypes.c_float, i64, i64, P, P], st),
         "q4k_nvfp4_gemm": ([P, ctypes.c_float, i64, i64, P, i64, i64, P, i64, P], st),
+        "q4k_kv_append": ([C, i64, i32, P, i64, P, i64, P, i64, P, P, P, P, i64, i32, st, P, i64, P, P, i64, P], st),
+        "q4k_attn_decode_workspace_size": ([C, i32, i32, i64], sz),
+        "q4k_attn_decode": ([C, P, P, i64, i32, i32, f32, f32, i64, P, i64, P, i64, f32, P, sz, P], st),
+        "q4k_kv_evict_workspace_size": ([C, i64], sz),
+        "q4k_kv_evict": ([C, P, P, i64, i64, i64, P, P, P, P, i64, P, sz, P], st),
+        "q4k_norm_residual": ([i64, i64, P, i64, st, P, P, f32, P, i64, f32, P, P, i64, st, st, P, P, f32, P, i64, P],
+                              st),
+        "q4k_sample": ([P, i64, i64, i64, P, P, P, P, P, P, P, P], st),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -252,3 +293,59 @@ def q4k_nvfp4_dequant(w, g: float, N: int, K: int, out, stream=None) -> None:
 def q4k_nvfp4_gemm(w, g: float, N: int, K: int, x, M: int, ldx: int, y, ldy: int, stream=None) -> None:
     """y = x . W^T with NVFP4 weights (tensor cores, any M >= 1)."""
     _check(load().q4k_nvfp4_gemm(_ptr(w), g, N, K, _ptr(x), M, ldx, _ptr(y), ldy, _stream(stream)), "q4k_nvfp4_gemm")
+
+
+def _cache(c):
+    return None if c is None else ctypes.byref(c)
+
+
+def q4k_kv_append(cache, T: int, n_heads: int, q, ldq: int, k, ldk: int, v, ldv: int, seq, slot, pos, rope, n_pos: int,
+                  rope_dim: int, rope_mode: int, q_out, ldqo: int, weights=None, positions=None, ld_meta: int = 0,
+                  stream=None) -> None:
+    """Rotary embedding of new queries and keys, and the write of new keys and values into the paged cache
+    (a KvCache); q, k, v fp32, q_out bf16."""
+    _check(load().q4k_kv_append(_cache(cache), T, n_heads, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(seq),
+                                _ptr(slot), _ptr(pos), _ptr(rope), n_pos, rope_dim, rope_mode, _ptr(q_out), ldqo,
+                                _ptr(weights), _ptr(positions), ld_meta, _stream(stream)), "q4k_kv_append")
+
+
+def q4k_attn_decode_workspace_size(cache, n_heads: int, n_q: int, ld_weights: int = 0) -> int:
+    return load().q4k_attn_decode_workspace_size(_cache(cache), n_heads, n_q, ld_weights)
+
+
+def q4k_attn_decode(cache, seq_lens, q, ldq: int, n_heads: int, n_q: int, scale: float, softcap: float, window: int,
+                    o, ldo: int, weights, ld_weights: int, decay: float, ws, ws_bytes: int, stream=None) -> None:
+    """Attention of the last n_q tokens of every sequence over its paged cache; q, o bf16 [batch*n_q][ld].  With
+    `weights` (fp32 [batch][n_kv_heads][ld_weights]) it also adds up the weight each cached slot received."""
+    _check(load().q4k_attn_decode(_cache(cache), _ptr(seq_lens), _ptr(q), ldq, n_heads, n_q, scale, softcap, window,
+                                  _ptr(o), ldo, _ptr(weights), ld_weights, decay, _ptr(ws), ws_bytes,
+                                  _stream(stream)), "q4k_attn_decode")
+
+
+def q4k_kv_evict_workspace_size(cache, ld_meta: int) -> int:
+    return load().q4k_kv_evict_workspace_size(_cache(cache), ld_meta)
+
+
+def q4k_kv_evict(cache, seq_lens, new_lens, budget: int, sinks: int, recent: int, weights, positions, weights_out,
+                 positions_out, ld_meta: int, ws, ws_bytes: int, stream=None) -> None:
+    """Cuts every sequence of the cache to at most `budget` slots, each KV head dropping its least attended ones."""
+    _check(load().q4k_kv_evict(_cache(cache), _ptr(seq_lens), _ptr(new_lens), budget, sinks, recent, _ptr(weights),
+                               _ptr(positions), _ptr(weights_out), _ptr(positions_out), ld_meta, _ptr(ws), ws_bytes,
+                               _stream(stream)), "q4k_kv_evict")
+
+
+def q4k_norm_residual(M: int, D: int, y, ldy: int, post: int, post_w, post_b, post_eps: float, gate, ld_gate: int,
+                      scale: float, r_in, r_out, ldr: int, r_dtype: int, pre: int, pre_w, pre_b, pre_eps: float, x,
+                      ldx: int, stream=None) -> None:
+    """h = r_in + scale * gate * post(y); r_out = h; x = bf16(pre(h))."""
+    _check(load().q4k_norm_residual(M, D, _ptr(y), ldy, post, _ptr(post_w), _ptr(post_b), post_eps, _ptr(gate),
+                                    ld_gate, scale, _ptr(r_in), _ptr(r_out), ldr, r_dtype, pre, _ptr(pre_w),
+                                    _ptr(pre_b), pre_eps, _ptr(x), ldx, _stream(stream)), "q4k_norm_residual")
+
+
+def q4k_sample(logits, M: int, V: int, ldl: int, temperature, top_k, top_p, min_p, u, token, prob=None,
+               stream=None) -> None:
+    """Draws a token for each row of fp32 logits [M][ldl] with the given random numbers u; per-row settings, each
+    may be None."""
+    _check(load().q4k_sample(_ptr(logits), M, V, ldl, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                             _ptr(u), _ptr(token), _ptr(prob), _stream(stream)), "q4k_sample")

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "q4k.h"
+#include "q4k_api.h"
 #include "q4k_internal.h"
 #include "q4k_ptx.cuh"
 
@@ -27,11 +28,6 @@ namespace {
 
 thread_local int t_last_cuda_error = 0;
 
-q4k_status cuda_fail(cudaError_t e) {
-    t_last_cuda_error = (int)e;
-    return Q4K_ERR_CUDA;
-}
-
 constexpr int kMaxDevices = 64;
 std::mutex g_dev_mutex;
 bool g_dev_ready[kMaxDevices];
@@ -45,11 +41,14 @@ PFN_cuCtxGetCurrent_v4000 g_ctx_current = nullptr;
 PFN_cuCtxGetId_v12000 g_ctx_id = nullptr;
 std::once_flag g_ctx_once;
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 bool k_ok(int64_t K) { return K > 0 && K % kQK == 0 && K <= (int64_t)1 << 30; }
 
 }  // namespace
+
+q4k_status cuda_fail(cudaError_t e) {
+    t_last_cuda_error = (int)e;
+    return Q4K_ERR_CUDA;
+}
 
 unsigned long long context_id() {
     std::call_once(g_ctx_once, [] {
@@ -205,12 +204,6 @@ cudaError_t make_act_tmap_sw128(CUtensorMap *m, const void *x, int64_t rows, int
     return encode_cached(m, k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-}  // namespace q4k
-
-using namespace q4k;
-
-namespace {
-
 // Common device gate: a cc 10.3 device must be current.
 q4k_status check_device(DeviceInfo *di) {
     cudaError_t e = device_info(di);
@@ -225,7 +218,9 @@ q4k_status check_device(DeviceInfo *di) {
     return Q4K_OK;
 }
 
-}  // namespace
+}  // namespace q4k
+
+using namespace q4k;
 
 extern "C" {
 
@@ -240,6 +235,7 @@ const char *q4k_status_string(int status) {
         case Q4K_ERR_CUDA: return "a CUDA runtime call failed";
         case Q4K_ERR_TIMEOUT: return "a kernel gave up waiting on a barrier";
         case Q4K_ERR_ROUTING: return "a call reusing a routing found one made for another shape";
+        case Q4K_ERR_INDEX: return "an index read from device memory is out of range";
         default: return "unknown status";
     }
 }
@@ -267,7 +263,7 @@ q4k_status q4k_check_device(void *stream) {
     if (v != 0) {
         const unsigned int zero = 0;
         if ((e = cudaMemcpyToSymbol(g_status_word, &zero, sizeof(zero))) != cudaSuccess) return cuda_fail(e);
-        return (v & kDevTimeout) ? Q4K_ERR_TIMEOUT : Q4K_ERR_ROUTING;
+        return (v & kDevTimeout) ? Q4K_ERR_TIMEOUT : (v & kDevRouting) ? Q4K_ERR_ROUTING : Q4K_ERR_INDEX;
     }
     return Q4K_OK;
 }

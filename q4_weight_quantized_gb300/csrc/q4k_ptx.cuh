@@ -14,6 +14,7 @@ namespace q4k {
 
 constexpr unsigned int kDevTimeout = 1u;         // status bit: a bounded wait gave up
 constexpr unsigned int kDevRouting = 2u;         // status bit: a reused routing was made for another call shape
+constexpr unsigned int kDevIndex = 4u;           // status bit: an index read from device memory is out of range
 // Written by the routing kernel after the tile count, with (E, item count): a
 // call that reuses the routing checks that it was made for its own shape.
 constexpr int kRoutingStamp = 0x5134524B;
