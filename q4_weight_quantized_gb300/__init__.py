@@ -133,17 +133,30 @@ def load(path: str | None = None):
 
 
 def _ptr(a):
-    if a is None:
-        return None
-    if isinstance(a, int):
+    if a is None or type(a) is int:
         return a
-    return a.data_ptr()
+    return int(a) if isinstance(a, int) else a.data_ptr()
+
+
+_current_stream = None
+
+
+def _torch_stream():
+    """The handle of torch's current stream, found without building a Stream object (a third of a small call's host
+    time)."""
+    global _current_stream
+    if _current_stream is None:
+        import torch
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        device, raw = torch.cuda.current_device, getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _current_stream()
 
 
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _torch_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -295,41 +308,37 @@ def q4k_nvfp4_gemm(w, g: float, N: int, K: int, x, M: int, ldx: int, y, ldy: int
     _check(load().q4k_nvfp4_gemm(_ptr(w), g, N, K, _ptr(x), M, ldx, _ptr(y), ldy, _stream(stream)), "q4k_nvfp4_gemm")
 
 
-def _cache(c):
-    return None if c is None else ctypes.byref(c)
-
-
 def q4k_kv_append(cache, T: int, n_heads: int, q, ldq: int, k, ldk: int, v, ldv: int, seq, slot, pos, rope, n_pos: int,
                   rope_dim: int, rope_mode: int, q_out, ldqo: int, weights=None, positions=None, ld_meta: int = 0,
                   stream=None) -> None:
     """Rotary embedding of new queries and keys, and the write of new keys and values into the paged cache
     (a KvCache); q, k, v fp32, q_out bf16."""
-    _check(load().q4k_kv_append(_cache(cache), T, n_heads, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(seq),
+    _check(load().q4k_kv_append(cache, T, n_heads, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(seq),
                                 _ptr(slot), _ptr(pos), _ptr(rope), n_pos, rope_dim, rope_mode, _ptr(q_out), ldqo,
                                 _ptr(weights), _ptr(positions), ld_meta, _stream(stream)), "q4k_kv_append")
 
 
 def q4k_attn_decode_workspace_size(cache, n_heads: int, n_q: int, ld_weights: int = 0) -> int:
-    return load().q4k_attn_decode_workspace_size(_cache(cache), n_heads, n_q, ld_weights)
+    return load().q4k_attn_decode_workspace_size(cache, n_heads, n_q, ld_weights)
 
 
 def q4k_attn_decode(cache, seq_lens, q, ldq: int, n_heads: int, n_q: int, scale: float, softcap: float, window: int,
                     o, ldo: int, weights, ld_weights: int, decay: float, ws, ws_bytes: int, stream=None) -> None:
     """Attention of the last n_q tokens of every sequence over its paged cache; q, o bf16 [batch*n_q][ld].  With
     `weights` (fp32 [batch][n_kv_heads][ld_weights]) it also adds up the weight each cached slot received."""
-    _check(load().q4k_attn_decode(_cache(cache), _ptr(seq_lens), _ptr(q), ldq, n_heads, n_q, scale, softcap, window,
+    _check(load().q4k_attn_decode(cache, _ptr(seq_lens), _ptr(q), ldq, n_heads, n_q, scale, softcap, window,
                                   _ptr(o), ldo, _ptr(weights), ld_weights, decay, _ptr(ws), ws_bytes,
                                   _stream(stream)), "q4k_attn_decode")
 
 
 def q4k_kv_evict_workspace_size(cache, ld_meta: int) -> int:
-    return load().q4k_kv_evict_workspace_size(_cache(cache), ld_meta)
+    return load().q4k_kv_evict_workspace_size(cache, ld_meta)
 
 
 def q4k_kv_evict(cache, seq_lens, new_lens, budget: int, sinks: int, recent: int, weights, positions, weights_out,
                  positions_out, ld_meta: int, ws, ws_bytes: int, stream=None) -> None:
     """Cuts every sequence of the cache to at most `budget` slots, each KV head dropping its least attended ones."""
-    _check(load().q4k_kv_evict(_cache(cache), _ptr(seq_lens), _ptr(new_lens), budget, sinks, recent, _ptr(weights),
+    _check(load().q4k_kv_evict(cache, _ptr(seq_lens), _ptr(new_lens), budget, sinks, recent, _ptr(weights),
                                _ptr(positions), _ptr(weights_out), _ptr(positions_out), ld_meta, _ptr(ws), ws_bytes,
                                _stream(stream)), "q4k_kv_evict")
 

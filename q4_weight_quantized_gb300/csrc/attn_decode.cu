@@ -8,19 +8,24 @@
 //     M = max(m_A, m_B),  l = l_A e^(m_A - M) + l_B e^(m_B - M),  o' likewise,
 // which is what lets warps, CTAs and the joining kernel share one row.
 //
-// Bound: every cached key and value is read once, so HBM; with up to 16 rows per KV
-// head (group x new tokens) the tensor work is the same for any row count.  Hence
-//   - The rows of one KV head are the 16 rows of mma.m16n8k16 (more rows: further row
-//     tiles, which find the cache in L2); keys and values go through the MMA straight
-//     from the ring, the two score tiles of a step turn in registers into the
-//     A operand of the second product, and nothing but the cache is ever re-read.
+// Bound: every cached key and value is read once, so HBM.  Hence
+//   - Slots and values are the long sides of the MMAs (m16), the rows of one KV head
+//     their short one (n8 tiles): S^T = K Q^T and O^T = V^T P^T.  A group of up to 8 rows
+//     costs one n tile, so few rows waste little tensor work and few registers; up to 32
+//     rows (16 for D = 256) share one pass over the cache.  The score tile's accumulators
+//     are the second product's B operand after one 8 x 8 transpose in registers.
 //   - The batch's work is one list of tiles (sequence, head, row tile, 4 steps of
 //     slots), cut into equal contiguous shares, one per CTA, whatever the lengths are:
 //     a share may end one unit, hold whole units and begin another.  Whole units are
 //     finished in place; parts leave (m, l, o') in the workspace for join_kernel.
-//   - Each warp owns a ring of stages in shared memory which it fills with 16-byte
-//     asynchronous copies of its own steps, so no barrier lies in the main loop; page
-//     ids are loaded one step before the copies that need them.
+//   - Each warp owns a ring of stages in shared memory and fills it with its own steps by
+//     16-byte asynchronous copies (any page size, any strides; one address for a step
+//     within a page), so no barrier lies in the main loop.  Rows lie RB + 16 bytes
+//     apart: eight rows' 16-byte chunks never share banks.  (A bulk copy per row needs
+//     fewer instructions, but the copy engine takes 12 to 19 cycles for each: 64 sequences
+//     of 2000 to 8192 slots took 320 us.)
+//   - The running maximum only moves when a score exceeds it by 2^8: until then no lane
+//     needs another's scores and o' is not rescaled.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -32,12 +37,13 @@ namespace {
 
 constexpr int kWarps = 4;           // warps of a CTA, each a step of every tile
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;           // rows of a row tile (mma m)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -INFINITY;
+constexpr float kSlack = 8.f;       // how far (log2) a score may exceed the running maximum
 
+// 16 bytes into shared memory, of which the last 16 - bytes become zeros
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -56,10 +62,29 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
+// transpose of an 8 x 8 matrix of 16-bit values held as MMA fragments
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // two e4m3 values (low 16 bits) to two f16 values, exactly
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
@@ -77,40 +102,37 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-
 __device__ __forceinline__ float lo_f32(uint32_t bf16x2) { return __uint_as_float(bf16x2 << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t bf16x2) { return __uint_as_float(bf16x2 & 0xFFFF0000u); }
 
-// floats of one part: (m, l) of 16 rows, then o' [16][D]
-__host__ __device__ constexpr int part_floats(int D) { return 2 * kRows + kRows * D; }
-// p of an e4m3 cache is kept as 2^15 p, in o' and l alike (see the kernel)
-__host__ __device__ constexpr float lift(bool e4m3) { return e4m3 ? 15.f : 0.f; }
+// p of an e4m3 cache is kept as 2^7 p, in o' and l alike (see the kernel)
+__host__ __device__ constexpr float lift(bool e4m3) { return e4m3 ? 7.f : 0.f; }
 
-template <int D_, bool E4M3_>
+// Floats of one part of NR row octets: (m, l) of 8 NR rows, then o' as MMA fragments
+// [octet][D / 16][lane][4].
+__host__ __device__ constexpr int part_floats(int D, int nr) { return 16 * nr + 8 * nr * D; }
+
+template <int D_, bool E4M3_, int NR_>
 struct Cfg {
-    static constexpr int D = D_;
+    static constexpr int D = D_, NR = NR_;                     // values of a head; octets of rows of a unit
     static constexpr bool E4M3 = E4M3_;
     static constexpr int RB = D * (E4M3 ? 1 : 2);              // bytes of a cached row
-    static constexpr int TOK = RB <= 128 ? 32 : 16;            // slots of a step
-    static constexpr int CT = kWarps * TOK;                    // slots of a tile
+    static constexpr int PITCH = RB + 16;
     static constexpr int CHUNKS = RB / 16;                     // 16-byte chunks of a row
-    static constexpr int STAGE = 2 * TOK * RB;                 // bytes of a stage: keys, then values
-    static constexpr int STAGES = STAGE <= 4096 ? 4 : 3;
-    static constexpr bool QSMEM = D > 128;                     // queries in shared memory: no registers left for them
-    static constexpr int KS = D / 16;                          // k steps of the first product
+    static constexpr int TOK = RB <= 128 && NR < 4 ? 32 : 16;  // slots of a step
+    static constexpr int MT = TOK / 16;
+    static constexpr int CT = kWarps * TOK;                    // slots of a tile
+    static constexpr int STAGE = 2 * TOK * PITCH;              // bytes of a stage: keys, then values
+    static constexpr int KS = D / 16;
+    static constexpr bool QSMEM = KS * NR >= 32;               // queries in shared memory where registers run out
+    static constexpr int QBYTES = QSMEM ? KS * NR * 32 * 8 : 0;
+    // a ring of what shared memory holds: two CTAs on an SM, or one where a stage is too large
+    static constexpr int HALF = (112 * 1024 - QBYTES) / (kWarps * STAGE), ALL = (222 * 1024 - QBYTES) / (kWarps * STAGE);
+    static constexpr int PER_SM = HALF >= 3 ? 2 : 1;
+    static constexpr int STAGES = PER_SM == 2 ? (HALF < 6 ? HALF : 6) : (ALL < 6 ? ALL : 6);
     static constexpr int RING = kWarps * STAGES * STAGE;
-    static constexpr int MERGE = kRows * D * 4;                // o' of the CTA
-    static constexpr int QBYTES = QSMEM ? KS * 32 * 16 : 0;
-    static constexpr int SMEM = RING + MERGE + QBYTES;
-    // rows alternate over the 128-byte bank lines so that eight rows' chunks (bf16,
-    // ldmatrix) or two neighbouring rows' four chunks (e4m3 keys) never share banks
-    static __device__ __forceinline__ uint32_t chunk_at(uint32_t row, uint32_t chunk) {
-        if constexpr (E4M3) {
-            if constexpr (RB == 64) return row * RB + (chunk ^ ((row >> 1) & 3)) * 16;
-            return row * RB + (chunk ^ (((row & 1) << 2) | ((row >> 1) & 3))) * 16;
-        }
-        return row * RB + (chunk ^ (row & 7)) * 16;
-    }
+    static constexpr int SMEM = RING + QBYTES;
+    static_assert(STAGES >= 3 && KS * 512 <= STAGE, "a stage holds a warp's fragments of one octet");
 };
 
 // A position in the list of tiles: tile `tile` of `tiles` of unit (b, hr = head * row
@@ -153,482 +175,597 @@ __device__ __forceinline__ void row_range(const AttnArgs &a, int r, int len, int
     begin = a.window > 0 ? (int)max((int64_t)0, (int64_t)end - a.window) : 0;
 }
 
+// This CTA's share of the list, tiles [t0, t1), and where it begins (if it is not empty); CTA 0
+// also writes the prefix sums over the sequences for the joining kernel.
+template <int CT>
+__device__ __forceinline__ void share_of_list(const AttnArgs &a, int64_t &t0, int64_t &t1, Pos &start, int64_t *scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.c.batch + kThreads - 1) / kThreads;
+    const int lo = min(tid * per, a.c.batch), hi = min(lo + per, a.c.batch);
+    int64_t sum = 0;
+    for (int b = lo; b < hi; ++b) {
+        int begin, len;
+        if (blockIdx.x == 0 && __ldg(a.seq_lens + b) > a.cap) atomicOr(a.c.status, kDevIndex);
+        seq_range(a, b, begin, len);
+        sum += (len - begin + CT - 1) / CT;
+    }
+    sum *= a.unit_heads;
+    int64_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    int64_t before = inc - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += scratch[w];
+        total += scratch[w];
+    }
+    const int64_t shares = min((int64_t)a.ctas, total);  // none of them empty
+    t0 = blockIdx.x < shares ? total * blockIdx.x / shares : total;
+    t1 = blockIdx.x < shares ? total * (blockIdx.x + 1) / shares : total;
+    if (t0 < t1 && before <= t0 && t0 < before + sum) {
+        // this thread's sequences hold the share's first tile
+        Pos p;
+        int64_t at = before;
+        for (p.b = lo;; ++p.b) {
+            seq_range(a, p.b, p.begin, p.end);
+            p.tiles = (p.end - p.begin + CT - 1) / CT;
+            if (t0 < at + (int64_t)p.tiles * a.unit_heads) break;
+            at += (int64_t)p.tiles * a.unit_heads;
+        }
+        p.hr = (int)((t0 - at) / p.tiles);
+        p.tile = (int)((t0 - at) - (int64_t)p.hr * p.tiles);
+        start = p;
+    }
+    if (blockIdx.x == 0) {
+        int64_t at = before;
+        for (int b = lo; b < hi; ++b) {
+            int begin, len;
+            a.prefix[b] = at;
+            seq_range(a, b, begin, len);
+            at += (int64_t)((len - begin + CT - 1) / CT) * a.unit_heads;
+        }
+        if (tid == 0) a.prefix[a.c.batch] = total;
+    }
+    __syncthreads();
+}
+
 template <typename C>
-__global__ void __launch_bounds__(kThreads, C::D == 256 && !C::E4M3 ? 1 : 2) attn_kernel(const AttnArgs a) {
-    constexpr int D = C::D, TOK = C::TOK, NT = TOK / 8, KS = C::KS;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
-    __shared__ uint32_t sm_mask[kWarps][C::STAGES];
-    __shared__ int64_t sm_scan[kWarps + 2];
+__global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArgs a) {
+    constexpr int D = C::D, TOK = C::TOK, MT = C::MT, KS = C::KS, NR = C::NR;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float sm_m[kWarps][8 * NR], sm_l[kWarps][8 * NR];
+    __shared__ int64_t sm_scan[kWarps];
+    __shared__ uint32_t sm_stage[kWarps];
     __shared__ Pos sm_pos;
+    __shared__ uint32_t sm_mask[kWarps][C::STAGES];  // slots of a stage that are there
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c4 = lane & 3;
     pdl_wait();
     pdl_trigger();
-
-    // ---- this CTA's share of the list: tiles [t0, t1)
     int64_t t0, t1;
-    {
-        const int per = (a.c.batch + kThreads - 1) / kThreads;
-        const int lo = min(tid * per, a.c.batch), hi = min(lo + per, a.c.batch);
-        int64_t sum = 0;
-        for (int b = lo; b < hi; ++b) {
-            int begin, len;
-            const int raw = __ldg(a.seq_lens + b);
-            if (raw > a.cap && blockIdx.x == 0) atomicOr(a.c.status, kDevIndex);
-            seq_range(a, b, begin, len);
-            sum += (len - begin + C::CT - 1) / C::CT;
-        }
-        sum *= a.unit_heads;
-        int64_t inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) sm_scan[warp] = inc;
-        __syncthreads();
-        int64_t before = inc - sum, total = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += sm_scan[w];
-            total += sm_scan[w];
-        }
-        const int64_t shares = min((int64_t)a.ctas, total);  // none of them empty
-        t0 = blockIdx.x < shares ? total * blockIdx.x / shares : total;
-        t1 = blockIdx.x < shares ? total * (blockIdx.x + 1) / shares : total;
-        if (t0 < t1 && before <= t0 && t0 < before + sum) {
-            // this thread's sequences hold the share's first tile
-            Pos p;
-            int64_t at = before;
-            for (p.b = lo;; ++p.b) {
-                seq_range(a, p.b, p.begin, p.end);
-                p.tiles = (p.end - p.begin + C::CT - 1) / C::CT;
-                if (t0 < at + (int64_t)p.tiles * a.unit_heads) break;
-                at += (int64_t)p.tiles * a.unit_heads;
-            }
-            p.hr = (int)((t0 - at) / p.tiles);
-            p.tile = (int)((t0 - at) % p.tiles);
-            sm_pos = p;
-        }
-        if (blockIdx.x == 0) {
-            int64_t at = before;
-            for (int b = lo; b < hi; ++b) {
-                int begin, len;
-                a.prefix[b] = at;
-                seq_range(a, b, begin, len);
-                at += (int64_t)((len - begin + C::CT - 1) / C::CT) * a.unit_heads;
-            }
-            if (tid == 0) a.prefix[a.c.batch] = total;
-        }
-        if (t0 >= t1) return;
-        __syncthreads();
-    }
+    share_of_list<C::CT>(a, t0, t1, sm_pos, sm_scan);
+    if (t0 >= t1) return;
     Pos cur = sm_pos, nxt = cur;
 
     const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
-    float *merge = reinterpret_cast<float *>(smem + C::RING);
-    uint4 *qs = reinterpret_cast<uint4 *>(smem + C::RING + C::MERGE);
+    const uint32_t qs = smem_u32(smem) + C::RING;
 
-    // ---- copies: the page id of this lane's slot of the next step to be copied is in flight
-    int64_t to_copy = t1 - t0;  // tiles whose copies are still to be issued
+    // ---- copies.  Lane i holds slot i of a step; the page ids of the step to be copied next are in
+    // flight.
+    const int64_t steps = t1 - t0;
+    int64_t copied = 0;
     int32_t page = -1;
     int slot = 0;
     bool in = false;
     auto fetch_page = [&] {
-        if (to_copy > 0) {
-            slot = nxt.begin + (nxt.tile * kWarps + warp) * TOK + lane;
-            in = lane < TOK && slot < nxt.end;
+        if (copied < steps) {
+            slot = nxt.begin + (nxt.tile * kWarps + warp) * TOK + (lane & (TOK - 1));
+            in = slot < nxt.end;
             page = in ? __ldg(a.c.table + nxt.b * a.c.ld_table + page_of(a.c, slot)) : -1;
         }
     };
     auto copy_step = [&](int stage) {
-        if (to_copy > 0) {
+        if (copied < steps) {
+            constexpr uint32_t kFull = TOK == 32 ? 0xFFFFFFFFu : (1u << TOK) - 1;
+            constexpr int ROWS = 32 / C::CHUNKS;  // rows of a warp's copy instruction
             const bool ok = in && page_ok(a.c, page);
             if (in && !ok) atomicOr(a.c.status, kDevIndex);
-            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok) & kFull;
             if (lane == 0) sm_mask[warp][stage] = mask;
-            const int64_t off =
-                ok ? row_bytes_at(a.c, page, nxt.hr / a.row_tiles, (uint32_t)slot - page_of(a.c, slot) * a.c.page_size) : 0;
-            const uint32_t dst = ring + stage * C::STAGE;
+            const int64_t off = ok ? row_bytes_at(a.c, page, (int)((uint32_t)nxt.hr / (uint32_t)a.row_tiles),
+                                                  (uint32_t)slot - page_of(a.c, slot) * a.c.page_size)
+                                   : 0;
+            const int r = lane / C::CHUNKS, ch = lane % C::CHUNKS;
+            const uint32_t to = ring + stage * C::STAGE + r * C::PITCH + ch * 16;
+            const int64_t first = __shfl_sync(0xFFFFFFFFu, off, 0), last = __shfl_sync(0xFFFFFFFFu, off, TOK - 1);
+            if (mask == kFull && last - first == (TOK - 1) * a.c.slot_bytes && __shfl_sync(0xFFFFFFFFu, page, 0) == __shfl_sync(0xFFFFFFFFu, page, TOK - 1)) {
+                // all slots, of one page
+                const uint8_t *k = a.c.k + first + r * a.c.slot_bytes + ch * 16, *v = a.c.v + first + r * a.c.slot_bytes + ch * 16;
 #pragma unroll
-            for (int i = 0; i < TOK * C::CHUNKS / 32; ++i) {
-                const int row = (i * 32 + lane) / C::CHUNKS, ch = lane % C::CHUNKS;
-                const int64_t o = __shfl_sync(0xFFFFFFFFu, off, row) + ch * 16;
-                const uint32_t n = (mask >> row & 1) * 16;  // slots that are not there become zeros
-                cp_async16(dst + C::chunk_at(row, ch), a.c.k + o, n);
-                cp_async16(dst + TOK * C::RB + C::chunk_at(row, ch), a.c.v + o, n);
+                for (int i = 0; i < TOK / ROWS; ++i) {
+                    cp_async16(to + i * ROWS * C::PITCH, k, 16);
+                    cp_async16(to + (TOK + i * ROWS) * C::PITCH, v, 16);
+                    k += ROWS * a.c.slot_bytes, v += ROWS * a.c.slot_bytes;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < TOK / ROWS; ++i) {
+                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, i * ROWS + r) + ch * 16;
+                    const uint32_t n = mask >> (i * ROWS + r) & 1 ? 16 : 0;  // slots that are not there become zeros: 0 * value must be 0
+                    cp_async16(to + i * ROWS * C::PITCH, a.c.k + o, n);
+                    cp_async16(to + (TOK + i * ROWS) * C::PITCH, a.c.v + o, n);
+                }
             }
-            --to_copy;
+            ++copied;
             advance(a, nxt, C::CT);
         }
         cp_async_commit();
         fetch_page();
     };
     fetch_page();
-#pragma unroll
     for (int s = 0; s < C::STAGES - 1; ++s) copy_step(s);
 
-    uint32_t qf[C::QSMEM ? 1 : KS][4];
-    float o[D / 8][4], m[2], l[2], cs[2];
-    int rb[2], re[2];        // slot ranges of rows g and g + 8
-    int in_lo = 0, in_hi = 0;  // slots that every row of the tile reads
-    bool fresh = true;       // the next step begins a unit (or the share)
-    int stage = 0;
+    uint32_t qf[C::QSMEM ? 1 : NR][C::QSMEM ? 1 : KS][2];
+    float o[NR][KS][4], m[NR][2], l[NR][2], cs[NR][2];
+    int in_lo = 0, in_hi = 0;  // slots that every row of the unit reads
 
-    for (int64_t left = t1 - t0; left > 0; --left) {
-        const int head = cur.hr / a.row_tiles, r0 = (cur.hr % a.row_tiles) * kRows;
-        if (fresh) {
-            // queries of rows g, g + 8 as the A operand; e4m3: as f16 scaled by a power of two
-            float mx[2] = {0.f, 0.f};
-            const uint16_t *qrow[2];
+    // Queries of a unit as B operands (row n * 8 + g of the unit; values 2 c4, 2 c4 + 1 and 8 on, or for e4m3
+    // those that ldmatrix leaves in this lane: 4 c4 .. 4 c4 + 3); e4m3: as f16, scaled by a power of two.
+    auto load_queries = [&](const Pos &p) {
+        const int head = (int)((uint32_t)p.hr / (uint32_t)a.row_tiles), r0 = (p.hr - head * a.row_tiles) * 8 * NR;
+        if constexpr (C::QSMEM) __syncthreads();  // the unit before has been read by every warp
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = r0 + g + 8 * h;
-                const int tok = r / a.group, hq = head * a.group + r % a.group;
-                qrow[h] = r < a.rows ? a.q + ((int64_t)cur.b * a.n_q + tok) * a.ldq + (int64_t)hq * D : nullptr;
-                row_range(a, r, cur.end, rb[h], re[h]);
-                m[h] = kNone;
-                l[h] = 0.f;
-            }
-            auto q_at = [&](int h, int ks, int half) -> uint32_t {
-                // the pair of query values that meets key values (k = 2 c4, 2 c4 + 1 | + 8) of k step ks
-                const int d = C::E4M3 ? (ks / 4) * 64 + c4 * 16 + (ks % 4) * 4 + half * 2 : ks * 16 + c4 * 2 + half * 8;
-                return qrow[h] ? __ldg(reinterpret_cast<const uint32_t *>(qrow[h] + d)) : 0u;
-            };
-            float up[2] = {1.f, 1.f};
+        for (int n = 0; n < NR; ++n) {
+            const int r = r0 + n * 8 + g;
+            const int tok = (int)((uint32_t)r / (uint32_t)a.group), hq = head * a.group + r - tok * a.group;
+            const bool there = r < a.rows;
+            const uint16_t *row = a.q + ((int64_t)p.b * a.n_q + (there ? tok : 0)) * a.ldq + (int64_t)(there ? hq : 0) * D;
+            uint32_t v[KS][2];
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    v[ks][f] = there ? __ldg(reinterpret_cast<const uint32_t *>(
+                                           row + ks * 16 + (C::E4M3 ? c4 * 4 + f * 2 : c4 * 2 + f * 8)))
+                                     : 0u;
+            float up = 1.f;
             if constexpr (C::E4M3) {
+                float mx = 0.f;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    for (int ks = 0; ks < KS; ++ks)
-                        for (int f = 0; f < 2; ++f) {
-                            const uint32_t v = q_at(h, ks, f);
-                            mx[h] = fmaxf(mx[h], fmaxf(fabsf(lo_f32(v)), fabsf(hi_f32(v))));
-                        }
-                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
-                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
-                    // 2^(14 - exponent of the largest): f16 then holds bf16's 8 bits of every value
-                    // down to 2^-30 of the largest (exponents are kept where 2^(14 - e) is a float)
-                    const int e = (int)(__float_as_uint(mx[h]) >> 23);
-                    if (e > 14 && e < 255) up[h] = __uint_as_float((uint32_t)(min(127 + 14 + 127 - e, 254)) << 23);
-                }
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) mx = fmaxf(mx, fmaxf(fabsf(lo_f32(v[ks][f])), fabsf(hi_f32(v[ks][f]))));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+                // 2^(14 - exponent of the largest): f16 then holds bf16's 8 bits of every value down to
+                // 2^-28 of the largest
+                const int e = (int)(__float_as_uint(mx) >> 23);
+                if (e > 14 && e < 255) up = __uint_as_float((uint32_t)min(127 + 14 + 127 - e, 254) << 23);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) v[ks][f] = pack_f16(lo_f32(v[ks][f]) * up, hi_f32(v[ks][f]) * up);
             }
-            auto q_frag = [&](int ks, uint32_t (&f)[4]) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t v = q_at(h, ks, half);
-                        f[half * 2 + h] = C::E4M3 ? pack_f16(lo_f32(v) * up[h], hi_f32(v) * up[h]) : v;
-                    }
-            };
+            // scores' factor: of rows n * 8 + 2 c4 and + 1, which other lanes hold as row g
+            const float c = a.scale * kLog2e / up;
+            cs[n][0] = __shfl_sync(0xFFFFFFFFu, c, c4 * 8);
+            cs[n][1] = __shfl_sync(0xFFFFFFFFu, c, c4 * 8 + 4);
             if constexpr (C::QSMEM) {
-                __syncthreads();  // the unit before has been read by every warp
-                for (int ks = warp; ks < KS; ks += kWarps) {
-                    uint32_t f[4];
-                    q_frag(ks, f);
-                    qs[ks * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
-                }
-                __syncthreads();
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+                    if (ks % kWarps == warp)
+                        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(qs + ((n * KS + ks) * 32 + lane) * 8), "r"(v[ks][0]),
+                                     "r"(v[ks][1])
+                                     : "memory");
             } else {
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) q_frag(ks, qf[ks]);
+                for (int ks = 0; ks < KS; ++ks) qf[n][ks][0] = v[ks][0], qf[n][ks][1] = v[ks][1];
             }
-            cs[0] = a.scale / up[0];
-            cs[1] = a.scale / up[1];
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
-            // rows of this tile: first and last token decide what all of them read
-            const int r_last = min(r0 + kRows, a.rows) - 1;
-            int b_, e_;
-            row_range(a, r0, cur.end, b_, in_hi);
-            row_range(a, r_last, cur.end, in_lo, e_);
-            fresh = false;
         }
+        if constexpr (C::QSMEM) __syncthreads();
+    };
+    auto begin_unit = [&](const Pos &p) {
+        const int r0 = p.hr % a.row_tiles * 8 * NR;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            m[n][0] = m[n][1] = kNone;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[n][i][x] = 0.f;
+        }
+        // the first token's rows read the least at the end, the last one's at the begin
+        int other;
+        row_range(a, r0, p.end, other, in_hi);
+        row_range(a, min(r0 + 8 * NR, a.rows) - 1, p.end, in_lo, other);
+    };
+    load_queries(cur);
+    begin_unit(cur);
 
+    int stage = 0;
+    for (int64_t done = 0; done < steps; ++done) {
         cp_async_wait<C::STAGES - 2>();
         __syncwarp();
-        copy_step((stage + C::STAGES - 1) % C::STAGES);
-
-        const uint32_t ks_addr = ring + stage * C::STAGE, vs_addr = ks_addr + TOK * C::RB;
         const uint32_t mask = sm_mask[warp][stage];
+        // every lane has read the step before, whose stage is filled next
+        copy_step(stage == 0 ? C::STAGES - 1 : stage - 1);
+        const uint32_t k_at = ring + stage * C::STAGE, v_at = k_at + TOK * C::PITCH;
         const int j0 = cur.begin + (cur.tile * kWarps + warp) * TOK;  // first slot of the step
         if (mask) {
-            // ---- s = q k^T
-            float s[NT][4];
+            // ---- S^T = K Q^T: slots 16 t + g, + 8 by rows 8 n + 2 c4, + 1
+            float s[MT][NR][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
-            if constexpr (!C::E4M3) {
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t qa[4];
-                    if constexpr (C::QSMEM) {
-                        const uint4 t = qs[ks * 32 + lane];
-                        qa[0] = t.x, qa[1] = t.y, qa[2] = t.z, qa[3] = t.w;
-                    } else {
+                    for (int x = 0; x < 4; ++x) s[t][n][x] = 0.f;
+            auto query = [&](int n, int ks, uint32_t &b0, uint32_t &b1) {
+                if constexpr (C::QSMEM)
+                    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(b0), "=r"(b1) : "r"(qs + ((n * KS + ks) * 32 + lane) * 8) : "memory");
+                else b0 = qf[n][ks][0], b1 = qf[n][ks][1];
+            };
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) qa[i] = qf[ks][i];
+            for (int t = 0; t < MT; ++t) {
+                const uint32_t row = k_at + (t * 16 + (lane & 15)) * C::PITCH + (lane >> 4) * 16;
+                if constexpr (!C::E4M3) {
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        uint32_t kf[4];
+                        ldsm4(kf, row + ks * 32);
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) {
+                            uint32_t b0, b1;
+                            query(n, ks, b0, b1);
+                            mma_bf16(s[t][n], kf[0], kf[1], kf[2], kf[3], b0, b1);
+                        }
                     }
+                } else {
 #pragma unroll
-                    for (int n = 0; n < NT; n += 2) {
-                        uint32_t kb[4];
-                        ldsm4(kb, ks_addr + C::chunk_at(n * 8 + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)));
-                        mma_bf16_16816(s[n], qa, kb[0], kb[1], s[n]);
-                        mma_bf16_16816(s[n + 1], qa, kb[2], kb[3], s[n + 1]);
-                    }
-                }
-            } else {
+                    for (int ks = 0; ks < KS; ks += 2) {
+                        uint32_t kf[4];
+                        ldsm4(kf, row + ks * 16);
 #pragma unroll
-                for (int kq = 0; kq < KS / 4; ++kq) {
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t a0 = e4m3x2_to_f16x2(kf[2 * x]), a1 = e4m3x2_to_f16x2(kf[2 * x + 1]);
+                            const uint32_t a2 = e4m3x2_to_f16x2(kf[2 * x] >> 16), a3 = e4m3x2_to_f16x2(kf[2 * x + 1] >> 16);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const uint4 w = lds128(ks_addr + C::chunk_at(n * 8 + g, 4 * kq + c4));
-                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t qa[4];
-                            if constexpr (C::QSMEM) {
-                                const uint4 t = qs[(kq * 4 + i) * 32 + lane];
-                                qa[0] = t.x, qa[1] = t.y, qa[2] = t.z, qa[3] = t.w;
-                            } else {
-#pragma unroll
-                                for (int x = 0; x < 4; ++x) qa[x] = qf[kq * 4 + i][x];
+                            for (int n = 0; n < NR; ++n) {
+                                uint32_t b0, b1;
+                                query(n, ks + x, b0, b1);
+                                mma_f16(s[t][n], a0, a1, a2, a3, b0, b1);
                             }
-                            mma_f16_16816(s[n], qa, e4m3x2_to_f16x2(ww[i]), e4m3x2_to_f16x2(ww[i] >> 16), s[n]);
                         }
                     }
                 }
             }
             // ---- scores in units of log2, masked
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s[t][n][x] *= cs[n][x & 1];
             if (a.softcap > 0.f) {
+                const float cap = a.softcap * kLog2e;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int t = 0; t < MT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        s[n][i] = a.softcap * kLog2e * tanhf(s[n][i] * cs[i >> 1] / a.softcap);
-            } else {
+                    for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[n][i] *= cs[i >> 1] * kLog2e;
+                        for (int x = 0; x < 4; ++x) s[t][n][x] = cap * tanhf(s[t][n][x] / cap);
             }
             const uint32_t full = TOK == 32 ? 0xFFFFFFFFu : (1u << TOK) - 1;
             const bool inside = j0 >= in_lo && j0 + TOK <= in_hi;
+            const int r0 = cur.hr % a.row_tiles * 8 * NR;
             if (mask != full || !inside) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = n * 8 + c4 * 2 + (i & 1), j = j0 + t, h = i >> 1;
-                        if (!(mask >> t & 1) || j < rb[h] || j >= re[h]) s[n][i] = kNone;
+                    for (int e = 0; e < 2; ++e) {
+                        int begin, end;
+                        row_range(a, r0 + n * 8 + c4 * 2 + e, cur.end, begin, end);
+#pragma unroll
+                        for (int t = 0; t < MT; ++t)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int at = t * 16 + h * 8 + g, j = j0 + at;
+                                if (!(mask >> at & 1) || j < begin || j >= end) s[t][n][h * 2 + e] = kNone;
+                            }
                     }
             }
             if (a.logits) {
+                const int head = (int)((uint32_t)cur.hr / (uint32_t)a.row_tiles);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = r0 + g + 8 * h;
-                    if (r < a.rows) {
-                        float *row = a.logits + (((int64_t)cur.b * a.c.heads + head) * a.rows + r) * a.ld_logits;
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = r0 + n * 8 + c4 * 2 + e;
+                        if (r < a.rows) {
+                            float *row = a.logits + (((int64_t)cur.b * a.c.heads + head) * a.rows + r) * a.ld_logits;
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int j = j0 + n * 8 + c4 * 2 + i;
-                                if (j < cur.end) row[j] = s[n][h * 2 + i];
-                            }
+                            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int j = j0 + t * 16 + h * 8 + g;
+                                    if (j < cur.end) row[j] = s[t][n][h * 2 + e];
+                                }
+                        }
                     }
-                }
             }
-            // ---- running maximum and sum; e4m3: p is 2^15 times itself, in o' and l alike, so that
-            // f16 holds p down to 2^-39
-            constexpr float kLift = lift(C::E4M3);
-            float alpha[2];
+            // ---- running maximum (rows 8 n + 2 c4, + 1: the same in all lanes of a column)
+            float top[NR][2];
+            bool more = false;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float t = kNone;
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) t = fmaxf(t, fmaxf(s[n][h * 2], s[n][h * 2 + 1]));
-                t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
-                t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
-                const float mn = fmaxf(m[h], t);
-                const float base = mn == kNone ? 0.f : mn;
-                alpha[h] = ex2_approx(m[h] - base);
-                m[h] = mn;
-                float sum = 0.f;
+                for (int e = 0; e < 2; ++e) {
+                    top[n][e] = kNone;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int t = 0; t < MT; ++t) top[n][e] = fmaxf(top[n][e], fmaxf(s[t][n][e], s[t][n][2 + e]));
+                    more |= top[n][e] > m[n][e] + kSlack;
+                }
+            if (__any_sync(0xFFFFFFFFu, more)) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float p = ex2_approx(s[n][h * 2 + i] - base + kLift);
-                        s[n][h * 2 + i] = p;
-                        sum += p;
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = top[n][e];
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                        x = fmaxf(x, m[n][e]);
+                        const float alpha = m[n][e] == kNone ? 0.f : ex2_approx(m[n][e] - x);
+                        m[n][e] = x;
+                        l[n][e] *= alpha;
+#pragma unroll
+                        for (int i = 0; i < KS; ++i) {
+                            // (o' is 0 while m is -inf)
+                            o[n][i][e] *= alpha;
+                            o[n][i][2 + e] *= alpha;
+                        }
                     }
-                l[h] = l[h] * alpha[h] + sum;
             }
-            if (__any_sync(0xFFFFFFFFu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+            // ---- p = 2^(s - m), at most 2^8; e4m3: 2^7 times that, so that f16 holds it between 2^15 and
+            // (to 2^-32 in absolute terms) 0
 #pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    o[n][0] *= alpha[0], o[n][1] *= alpha[0];
-                    o[n][2] *= alpha[1], o[n][3] *= alpha[1];
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float base = (m[n][e] == kNone ? 0.f : m[n][e]) - lift(C::E4M3);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float p = ex2_approx(s[t][n][h * 2 + e] - base);
+                            s[t][n][h * 2 + e] = p;
+                            l[n][e] += p;
+                        }
                 }
-            }
             // ---- slots that some rows read and others do not (the new tokens themselves, the window's
-            // edge): 0 * inf must not reach the others, so these are added row by row and then
-            // taken out of the product
+            // edge): a value there that is not finite must not reach the others as 0 * inf, so it
+            // is added row by row and then taken out of the product
             if (!inside && a.n_q > 1) {
-                for (int t = 0; t < TOK; ++t) {
-                    const int j = j0 + t;
-                    if (!(mask >> t & 1) || (j >= in_lo && j < in_hi)) continue;
-                    float p0 = 0.f, p1 = 0.f;
+                for (int at = 0; at < TOK; ++at) {
+                    const int j = j0 + at;
+                    if (!(mask >> at & 1) || (j >= in_lo && j < in_hi)) continue;
+                    const uint32_t v_row = v_at + at * C::PITCH;
+                    bool odd = false;
+                    if (lane * 16 < C::RB) {
+                        const uint4 w = lds128(v_row + lane * 16);
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        if (n == t / 8) {
-                            p0 = t & 1 ? s[n][1] : s[n][0], p1 = t & 1 ? s[n][3] : s[n][2];
-                            if (c4 == (t & 7) / 2) {
-                                if (t & 1) s[n][1] = s[n][3] = 0.f;
-                                else s[n][0] = s[n][2] = 0.f;
-                            }
-                        }
-                    p0 = __shfl_sync(0xFFFFFFFFu, p0, (lane & ~3) | (t & 7) / 2);
-                    p1 = __shfl_sync(0xFFFFFFFFu, p1, (lane & ~3) | (t & 7) / 2);
-                    const bool on0 = j >= rb[0] && j < re[0], on1 = j >= rb[1] && j < re[1];
-#pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        float v0, v1;
-                        if constexpr (C::E4M3) {
-                            const int d = (n / 2) * 16 + c4 * 4 + (n & 1);
-                            const uint32_t at = vs_addr + C::chunk_at(t, d / 16) + d % 16;
-                            uint32_t b0, b1;
-                            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b0) : "r"(at) : "memory");
-                            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b1) : "r"(at + 2) : "memory");
-                            v0 = e4m3_to_f32(b0), v1 = e4m3_to_f32(b1);
-                        } else {
-                            const int d = n * 8 + c4 * 2;
-                            uint32_t v;
-                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(vs_addr + C::chunk_at(t, d / 8) + (d % 8) * 2) : "memory");
-                            v0 = lo_f32(v), v1 = hi_f32(v);
-                        }
-                        if (on0) o[n][0] = fmaf(p0, v0, o[n][0]), o[n][1] = fmaf(p0, v1, o[n][1]);
-                        if (on1) o[n][2] = fmaf(p1, v0, o[n][2]), o[n][3] = fmaf(p1, v1, o[n][3]);
+                        for (int x = 0; x < 4; ++x)
+                            odd |= C::E4M3 ? __vcmpeq4(ws[x] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0
+                                           : __vcmpeq2(ws[x] & 0x7F807F80u, 0x7F807F80u) != 0;
                     }
+                    if (!__any_sync(0xFFFFFFFFu, odd)) continue;
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float p = 0.f;
+#pragma unroll
+                            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    if (at / 8 == t * 2 + h) {
+                                        p = s[t][n][h * 2 + e];
+                                        if ((at & 7) == g) s[t][n][h * 2 + e] = 0.f;
+                                    }
+                            p = __shfl_sync(0xFFFFFFFFu, p, (at & 7) * 4 + c4);
+                            int begin, end;
+                            row_range(a, r0 + n * 8 + c4 * 2 + e, cur.end, begin, end);
+                            if (j >= begin && j < end)
+#pragma unroll
+                                for (int i = 0; i < KS; ++i)
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) {
+                                        float v;
+                                        if constexpr (C::E4M3) {
+                                            uint32_t b;
+                                            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(v_row + i * 16 + 2 * g + h) : "memory");
+                                            v = e4m3_to_f32(b);
+                                        } else {
+                                            uint16_t b;
+                                            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(v_row + (i * 16 + 8 * h + g) * 2) : "memory");
+                                            v = __uint_as_float((uint32_t)b << 16);
+                                        }
+                                        o[n][i][h * 2 + e] = fmaf(p, v, o[n][i][h * 2 + e]);
+                                    }
+                        }
                     __syncwarp();
-                    if (lane < C::CHUNKS)
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(vs_addr + C::chunk_at(t, lane)), "r"(0) : "memory");
+                    if (lane * 16 < C::RB) sts128(v_row + lane * 16, make_uint4(0, 0, 0, 0));
                     __syncwarp();
                 }
             }
-            // ---- o' += p v, p as the sum of two 16-bit values (one alone would cost as much as o's own
-            // rounding)
+            // ---- O^T += V^T P^T.  bf16: p as the sum of two bf16 values (one alone would cost nearly as much
+            // as o's own rounding); e4m3: as one f16 value, 2^-12.
 #pragma unroll
-            for (int kk = 0; kk < TOK / 16; ++kk) {
-                uint32_t ph[4], pl[4];
+            for (int t = 0; t < MT; ++t) {
+                uint32_t ph[NR][2], pl[NR][2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x = s[kk * 2 + (i >> 1)][(i & 1) * 2], y = s[kk * 2 + (i >> 1)][(i & 1) * 2 + 1];
-                    if constexpr (C::E4M3) {
-                        ph[i] = pack_f16(x, y);
-                        const float2 b = __half22float2(*reinterpret_cast<__half2 *>(&ph[i]));
-                        pl[i] = pack_f16(x - b.x, y - b.y);
-                    } else {
-                        ph[i] = pack_bf16(x, y);
-                        pl[i] = pack_bf16(x - lo_f32(ph[i]), y - hi_f32(ph[i]));
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float x = s[t][n][h * 2], y = s[t][n][h * 2 + 1];
+                        if constexpr (C::E4M3) {
+                            ph[n][h] = transpose8(pack_f16(x, y));
+                        } else {
+                            const uint32_t hi = pack_bf16(x, y);
+                            ph[n][h] = transpose8(hi);
+                            pl[n][h] = transpose8(pack_bf16(x - lo_f32(hi), y - hi_f32(hi)));
+                        }
                     }
-                }
+                const uint32_t row = v_at + (t * 16 + (lane & 7) + (C::E4M3 ? lane & 8 : (lane >> 4) * 8)) * C::PITCH +
+                                     (C::E4M3 ? lane >> 4 : lane >> 3 & 1) * 16;
                 if constexpr (!C::E4M3) {
 #pragma unroll
-                    for (int n = 0; n < D / 8; n += 2) {
-                        uint32_t vb[4];
-                        ldsm4_trans(vb, vs_addr + C::chunk_at(kk * 16 + (lane & 15), n + (lane >> 4)));
-                        mma_bf16_16816(o[n], ph, vb[0], vb[1], o[n]);
-                        mma_bf16_16816(o[n + 1], ph, vb[2], vb[3], o[n + 1]);
-                        mma_bf16_16816(o[n], pl, vb[0], vb[1], o[n]);
-                        mma_bf16_16816(o[n + 1], pl, vb[2], vb[3], o[n + 1]);
+                    for (int i = 0; i < KS; ++i) {
+                        uint32_t vf[4];
+                        ldsm4_trans(vf, row + i * 32);
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) {
+                            mma_bf16(o[n][i], vf[0], vf[1], vf[2], vf[3], ph[n][0], ph[n][1]);
+                            mma_bf16(o[n][i], vf[0], vf[1], vf[2], vf[3], pl[n][0], pl[n][1]);
+                        }
                     }
                 } else {
-                    // a transposed 8 x 8 matrix of byte pairs: each register holds values d, d + 1 of two
-                    // slots; tile 2i takes the even d, tile 2i + 1 the odd ones
+                    // a transposed 8 x 8 matrix of byte pairs: a register holds values d, d + 1 of two slots;
+                    // the tile's rows g take the even d, rows g + 8 the odd ones
 #pragma unroll
-                    for (int n = 0; n < D / 8; n += 4) {
-                        uint32_t vb[4];
-                        ldsm4_trans(vb, vs_addr + C::chunk_at(kk * 16 + (lane & 15), n / 2 + (lane >> 4)));
+                    for (int i = 0; i < KS; i += 2) {
+                        uint32_t vf[4];
+                        ldsm4_trans(vf, row + i * 16);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint32_t sel = x & 1 ? 0x31u : 0x20u;
-                            const uint32_t b0 = e4m3x2_to_f16x2(prmt(vb[(x >> 1) * 2], 0, sel));
-                            const uint32_t b1 = e4m3x2_to_f16x2(prmt(vb[(x >> 1) * 2 + 1], 0, sel));
-                            mma_f16_16816(o[n + x], ph, b0, b1, o[n + x]);
-                            mma_f16_16816(o[n + x], pl, b0, b1, o[n + x]);
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t a0 = e4m3x2_to_f16x2(prmt(vf[2 * x], 0, 0x20u)), a1 = e4m3x2_to_f16x2(prmt(vf[2 * x], 0, 0x31u));
+                            const uint32_t a2 = e4m3x2_to_f16x2(prmt(vf[2 * x + 1], 0, 0x20u)), a3 = e4m3x2_to_f16x2(prmt(vf[2 * x + 1], 0, 0x31u));
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) mma_f16(o[n][i + x], a0, a1, a2, a3, ph[n][0], ph[n][1]);
                         }
                     }
                 }
             }
         }
         __syncwarp();
-        stage = (stage + 1) % C::STAGES;
+        const uint32_t read_stage = ring + stage * C::STAGE;  // free until the next step
+        stage = stage + 1 == C::STAGES ? 0 : stage + 1;
 
-        // ---- the unit or the share ends: join the warps
-        if (cur.tile + 1 == cur.tiles || left == 1) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
-                l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
-                if (c4 == 0) sm_m[warp][g + 8 * h] = m[h], sm_l[warp][g + 8 * h] = l[h];
-            }
-            __syncthreads();
-            float f[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float top = kNone;
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm_m[w][g + 8 * h]);
-                f[h] = m[h] == kNone ? 0.f : ex2_approx(m[h] - top);
-            }
-            for (int w = 0; w < kWarps; ++w) {
-                if (w == warp) {
-#pragma unroll
-                    for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int d = C::E4M3 ? (n / 2) * 16 + c4 * 4 + (n & 1) + (i & 1) * 2 : n * 8 + c4 * 2 + (i & 1);
-                            float *at = merge + (g + 8 * (i >> 1)) * D + d;
-                            const float v = f[i >> 1] == 0.f ? 0.f : o[n][i] * f[i >> 1];
-                            *at = w == 0 ? v : *at + v;
-                        }
-                }
-                __syncthreads();
-            }
-            const int rows = min(kRows, a.rows - r0);
-            // of its share's parts, a CTA leaves that of a unit begun before it in slot 0 and that of a
-            // unit that goes on after it in slot 1
-            const bool began = cur.tile <= t1 - t0 - left;
-            const bool whole = began && cur.tile + 1 == cur.tiles;
-            const int64_t unit = (int64_t)cur.b * a.unit_heads + cur.hr;
-            float *part = a.parts + (2 * (int64_t)blockIdx.x + began) * part_floats(D);
-            for (int r = warp; r < rows; r += kWarps) {
-                float top = kNone, sum = 0.f;
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm_m[w][r]);
-                for (int w = 0; w < kWarps; ++w)
-                    if (sm_m[w][r] != kNone) sum += sm_l[w][r] * ex2_approx(sm_m[w][r] - top);
-                if (whole) {
-                    const int rr = r0 + r;
-                    uint16_t *out = a.o + ((int64_t)cur.b * a.n_q + rr / a.group) * a.ldo +
-                                    (int64_t)(head * a.group + rr % a.group) * D;
-                    const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
-                    for (int d = lane * 2; d < D; d += 64)
-                        *reinterpret_cast<uint32_t *>(out + d) = pack_bf16(merge[r * D + d] * inv, merge[r * D + d + 1] * inv);
-                    if (lane == 0) a.unit_ml[unit * kRows + r] = make_float2(top, sum);
-                } else {
-                    for (int d = lane * 4; d < D; d += 128)
-                        *reinterpret_cast<float4 *>(part + 2 * kRows + r * D + d) = *reinterpret_cast<const float4 *>(merge + r * D + d);
-                    if (lane == 0) part[2 * r] = top, part[2 * r + 1] = sum;
-                }
-            }
-            __syncthreads();
-            fresh = true;
+        const bool ends = cur.tile + 1 == cur.tiles;
+        if (!ends && done + 1 < steps) {
+            ++cur.tile;
+            continue;
         }
+        // ---- the unit or the share ends: join the warps
+        Pos was = cur;
         advance(a, cur, C::CT);
+        if (!C::QSMEM && done + 1 < steps) load_queries(cur);  // (on their way during what follows; cs is not needed any more)
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 4);
+                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 8);
+                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 16);
+                if (g == 0) sm_m[warp][n * 8 + c4 * 2 + e] = m[n][e], sm_l[warp][n * 8 + c4 * 2 + e] = l[n][e];
+            }
+        if (lane == 0) sm_stage[warp] = read_stage;
+        __syncthreads();
+        // of its share's parts, a CTA leaves that of a unit begun before it in slot 0 and that of a unit
+        // that goes on after it in slot 1
+        const bool began = was.tile <= done;
+        const bool whole = began && ends;
+        const int head = (int)((uint32_t)was.hr / (uint32_t)a.row_tiles), r0 = (was.hr - head * a.row_tiles) * 8 * NR;
+        float *part = a.parts + (2 * (int64_t)blockIdx.x + began) * part_floats(D, NR);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            float f[2], mt[2], lt[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = n * 8 + c4 * 2 + e;
+                mt[e] = kNone;
+                lt[e] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) mt[e] = fmaxf(mt[e], sm_m[w][r]);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    if (sm_m[w][r] != kNone) lt[e] += sm_l[w][r] * ex2_approx(sm_m[w][r] - mt[e]);
+                f[e] = m[n][e] == kNone ? 0.f : ex2_approx(m[n][e] - mt[e]);
+            }
+            // warps 2 and 3 hand over to 0 and 1, then 1 to 0, through the stage that each has just read
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[n][i][x] *= f[x & 1];
+            auto put = [&] {
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+                    sts128(read_stage + lane * 16 + i * 512, make_uint4(__float_as_uint(o[n][i][0]), __float_as_uint(o[n][i][1]), __float_as_uint(o[n][i][2]),
+                                                     __float_as_uint(o[n][i][3])));
+            };
+            auto add = [&](int from) {
+                const uint32_t at = sm_stage[from] + lane * 16;
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    const uint4 t = lds128(at + i * 512);
+                    o[n][i][0] += __uint_as_float(t.x), o[n][i][1] += __uint_as_float(t.y);
+                    o[n][i][2] += __uint_as_float(t.z), o[n][i][3] += __uint_as_float(t.w);
+                }
+            };
+            if (n > 0) __syncthreads();  // warp 1's stage has been read
+            if (warp >= 2) put();
+            __syncthreads();
+            if (warp < 2) add(warp + 2);
+            if (warp == 1) put();
+            __syncthreads();
+            if (warp == 0) {
+                add(1);
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = r0 + n * 8 + c4 * 2 + e;
+                        if (r < a.rows) {
+                            const int tok = (int)((uint32_t)r / (uint32_t)a.group);
+                            uint16_t *out = a.o + ((int64_t)was.b * a.n_q + tok) * a.ldo + (int64_t)(head * a.group + r - tok * a.group) * D;
+                            const float inv = lt[e] > 0.f || lt[e] != lt[e] ? a.v_scale / lt[e] : 0.f;
+#pragma unroll
+                            for (int i = 0; i < KS; ++i) {
+                                if constexpr (C::E4M3) {
+                                    *reinterpret_cast<uint32_t *>(out + i * 16 + 2 * g) = pack_bf16(o[n][i][e] * inv, o[n][i][2 + e] * inv);
+                                } else {
+                                    const uint32_t t = pack_bf16(o[n][i][e] * inv, o[n][i][2 + e] * inv);
+                                    out[i * 16 + g] = (uint16_t)t;
+                                    out[i * 16 + 8 + g] = (uint16_t)(t >> 16);
+                                }
+                            }
+                            if (a.unit_ml && g == 0)
+                                a.unit_ml[((int64_t)was.b * a.unit_heads + was.hr) * 8 * NR + n * 8 + c4 * 2 + e] = make_float2(mt[e], lt[e]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+                        *reinterpret_cast<float4 *>(part + 16 * NR + ((n * KS + i) * 32 + lane) * 4) =
+                            make_float4(o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]);
+                    if (g == 0)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<float2 *>(part + 2 * (n * 8 + c4 * 2 + e)) = make_float2(mt[e], lt[e]);
+                }
+            }
+        }
+        __syncthreads();
+        if (done + 1 < steps) {
+            if (C::QSMEM) load_queries(cur);
+            begin_unit(cur);
+        }
     }
     cp_async_wait<0>();
 }
@@ -636,33 +773,33 @@ __global__ void __launch_bounds__(kThreads, C::D == 256 && !C::E4M3 ? 1 : 2) att
 // The parts of a unit: those of CTAs [first, last], none if the unit has no slots; one
 // CTA alone has finished the unit (whole).
 struct Parts {
-    int64_t first, last;
+    int first, last;
     bool empty, whole;
 };
 __device__ __forceinline__ Parts parts_of(const AttnArgs &a, int64_t unit) {
-    const int64_t b = unit / a.unit_heads, hr = unit % a.unit_heads;
-    const int64_t p0 = a.prefix[b], p1 = a.prefix[b + 1], total = a.prefix[a.c.batch];
-    const int64_t tiles = (p1 - p0) / a.unit_heads, t = p0 + hr * tiles;
-    Parts r = {0, 0, tiles == 0, false};
+    const int b = (int)(unit / a.unit_heads), hr = (int)(unit - (int64_t)b * a.unit_heads);
+    const int64_t p0 = __ldg(a.prefix + b), p1 = __ldg(a.prefix + b + 1), total = __ldg(a.prefix + a.c.batch);
+    Parts r = {0, 0, p0 == p1, false};
     if (!r.empty) {
+        const int64_t tiles = (p1 - p0) / a.unit_heads, t = p0 + hr * tiles;
         // share i holds the tiles [total i / shares, total (i + 1) / shares)
         const int64_t shares = min((int64_t)a.ctas, total);
-        r.first = ((t + 1) * shares - 1) / total;
-        r.last = ((t + tiles) * shares - 1) / total;
+        r.first = (int)(((t + 1) * shares - 1) / total);
+        r.last = (int)(((t + tiles) * shares - 1) / total);
         r.whole = r.first == r.last;
     }
     return r;
 }
-__device__ __forceinline__ const float *part_at(const AttnArgs &a, const Parts &p, int64_t i) {
-    return a.parts + (2 * i + (i == p.first)) * part_floats(a.c.dim);
+__device__ __forceinline__ const float *part_at(const AttnArgs &a, const Parts &p, int i) {
+    return a.parts + (int64_t)(2 * i + (i == p.first)) * a.part_floats;
 }
 // (m, l) of one row over all its parts; every lane of the warp calls it and gets it.
 __device__ __forceinline__ float2 join_ml(const AttnArgs &a, const Parts &p, int64_t unit, int row) {
     if (p.empty) return make_float2(kNone, 0.f);
-    if (p.whole) return a.unit_ml[unit * kRows + row];
+    if (p.whole) return a.unit_ml[unit * a.tile_rows + row];
     const int lane = threadIdx.x & 31;
     float m = kNone, l = 0.f;
-    for (int64_t i = p.first + lane; i <= p.last; i += 32) {
+    for (int i = p.first + lane; i <= p.last; i += 32) {
         const float2 ml = *reinterpret_cast<const float2 *>(part_at(a, p, i) + 2 * row);
         if (ml.x == kNone) continue;
         const float top = fmaxf(m, ml.x);
@@ -678,101 +815,195 @@ __device__ __forceinline__ float2 join_ml(const AttnArgs &a, const Parts &p, int
     return make_float2(top, l);
 }
 
-constexpr int kChunk = 2048;  // slots of a block that adds up weights
+// Units in several parts, and zeros for units without slots.  A block joins 16 values of the
+// 8 rows of an octet (one fragment: 32 lanes of float4), its warps taking every fourth part.
+__global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a) {
+    __shared__ float4 sm[kWarps][32];
+    __shared__ float2 ml[kMaxAttnCtas][8];  // (m, l) of a part's rows, then (2^(m - M), -)
+    __shared__ float red[kWarps][8], sm_l[kWarps][8];
+    pdl_wait();
+    pdl_trigger();
+    const int D = a.c.dim, ks = D / 16, octets = a.tile_rows / 8;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
+    const int i = blockIdx.x % ks, n = blockIdx.x / ks % octets;
+    const int64_t unit = blockIdx.x / (ks * octets);
+    const Parts p = parts_of(a, unit);
+    if (p.whole) return;
+    const int b = (int)(unit / a.unit_heads), hr = (int)(unit % a.unit_heads), head = hr / a.row_tiles;
+    const int r0 = hr % a.row_tiles * a.tile_rows + n * 8;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l[2] = {0.f, 0.f};
+    if (!p.empty) {
+        // (m, l) of the 8 rows of every part: thread x holds row x % 8 of every 16th part
+        const int parts = p.last - p.first + 1;
+        float top = kNone;
+        for (int x = tid; x < parts * 8; x += kThreads) {
+            const float2 t = *reinterpret_cast<const float2 *>(part_at(a, p, p.first + x / 8) + 2 * (n * 8 + x % 8));
+            ml[x / 8][x % 8] = t;
+            top = fmaxf(top, t.x);
+        }
+        // the fragments of this warp's parts are on their way meanwhile
+        constexpr int kAhead = 8;
+        float4 t[kAhead];
+        const int64_t at = 2 * a.tile_rows + ((n * ks + i) * 32 + lane) * 4;
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y)
+            if (warp + y * kWarps < parts)
+                t[y] = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + warp + y * kWarps) + at);
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+        if (lane < 8) red[warp][lane] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red[w][lane & 7]);
+        float sum = 0.f;
+        for (int x = tid; x < parts * 8; x += kThreads) {
+            const float2 t = ml[x / 8][x % 8];
+            const float f = t.x == kNone ? 0.f : ex2_approx(t.x - top);
+            ml[x / 8][x % 8].x = f;
+            sum = fmaf(f, t.y, sum);
+        }
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+        if (lane < 8) sm_l[warp][lane] = sum;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) l[e] += sm_l[w][c4 * 2 + e];
+        for (int x0 = warp; x0 < parts; x0 += kAhead * kWarps) {
+#pragma unroll
+            for (int y = 0; y < kAhead; ++y) {
+                const int x = x0 + y * kWarps;
+                if (x < parts) {
+                    const float f0 = ml[x][c4 * 2].x, f1 = ml[x][c4 * 2 + 1].x;
+                    v.x = fmaf(f0, t[y].x, v.x), v.y = fmaf(f1, t[y].y, v.y);
+                    v.z = fmaf(f0, t[y].z, v.z), v.w = fmaf(f1, t[y].w, v.w);
+                    if (x + kAhead * kWarps < parts)
+                        t[y] = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + x + kAhead * kWarps) + at);
+                }
+            }
+        }
+        sm[warp][lane] = v;
+        __syncthreads();
+        if (warp > 0) return;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            const float4 x = sm[w][lane];
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+    } else if (warp > 0) {
+        return;
+    }
+    const float lo[2] = {v.x, v.y}, hi[2] = {v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = r0 + c4 * 2 + e;
+        if (r >= a.rows) continue;
+        uint16_t *out = a.o + ((int64_t)b * a.n_q + r / a.group) * a.ldo + (int64_t)(head * a.group + r % a.group) * D + i * 16;
+        const float inv = l[e] > 0.f || l[e] != l[e] ? a.v_scale / l[e] : 0.f;
+        const uint32_t t = pack_bf16(lo[e] * inv, hi[e] * inv);
+        if (a.c.e4m3) {
+            *reinterpret_cast<uint32_t *>(out + 2 * g) = t;
+        } else {
+            out[g] = (uint16_t)t;
+            out[8 + g] = (uint16_t)(t >> 16);
+        }
+    }
+}
 
-// Blocks [0, join_blocks): the rows of units in several parts (a warp a row), and zeros
-// for units without slots.  The others: a chunk of slots of one KV head's weights.
-__global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a, int join_blocks, int chunks) {
+constexpr int kChunk = 1024;  // slots of a block that adds up weights
+
+// A chunk of slots of one KV head's weights: weights <- decay * weights + sum of the rows'
+// 2^(s - m) / l.
+__global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnArgs a, int chunks) {
     __shared__ float sm_m[kMaxAttnRows], sm_r[kMaxAttnRows];
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = a.c.dim;
-    if ((int)blockIdx.x < join_blocks) {
-        const int64_t unit = blockIdx.x / (kRows / kWarps);
-        const int row = (blockIdx.x % (kRows / kWarps)) * kWarps + warp;
-        const int b = (int)(unit / a.unit_heads), hr = (int)(unit % a.unit_heads);
-        const int r = (hr % a.row_tiles) * kRows + row;
-        if (r >= a.rows) return;
-        const Parts p = parts_of(a, unit);
-        if (p.whole) return;
-        uint16_t *out = a.o + ((int64_t)b * a.n_q + r / a.group) * a.ldo +
-                        (int64_t)(hr / a.row_tiles * a.group + r % a.group) * D;
-        const float2 ml = join_ml(a, p, unit, row);
-        const float inv = ml.y > 0.f || ml.y != ml.y ? a.v_scale / ml.y : 0.f;
-        for (int d = lane * 2; d < D; d += 64) {
-            float x = 0.f, y = 0.f;
-            if (!p.empty) {
-#pragma unroll 8
-                for (int64_t i = p.first; i <= p.last; ++i) {
-                    const float *part = part_at(a, p, i);
-                    const float mi = part[2 * row];
-                    const float2 v = *reinterpret_cast<const float2 *>(part + 2 * kRows + row * D + d);
-                    const float f = mi == kNone ? 0.f : ex2_approx(mi - ml.x);
-                    x = fmaf(f, v.x, x), y = fmaf(f, v.y, y);
-                }
-            }
-            *reinterpret_cast<uint32_t *>(out + d) = pack_bf16(x * inv, y * inv);
-        }
-        return;
-    }
-    const int64_t id = blockIdx.x - join_blocks;
-    const int64_t bh = id / chunks;
-    const int b = (int)(bh / a.c.heads), h = (int)(bh % a.c.heads);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t bh = blockIdx.x / chunks;
+    const int b = (int)(bh / a.c.heads), h = (int)(bh - (int64_t)b * a.c.heads);
     int begin, len;
     seq_range(a, b, begin, len);
-    const int lo = (int)(id % chunks) * kChunk, hi = min(lo + kChunk, len);
+    const int lo = (int)(blockIdx.x % chunks) * kChunk, hi = min(lo + kChunk, len);
     if (lo >= len) return;
     if (hi > begin)
         for (int rt = 0; rt < a.row_tiles; ++rt) {
             const int64_t unit = (int64_t)b * a.unit_heads + h * a.row_tiles + rt;
             const Parts p = parts_of(a, unit);
-            for (int row = warp; row < kRows && rt * kRows + row < a.rows; row += kWarps) {
+            for (int row = warp; row < a.tile_rows && rt * a.tile_rows + row < a.rows; row += kWarps) {
                 const float2 ml = join_ml(a, p, unit, row);
                 if (lane == 0) {
-                    sm_m[rt * kRows + row] = ml.x == kNone ? 0.f : ml.x;
-                    sm_r[rt * kRows + row] = ml.y > 0.f || ml.y != ml.y ? ex2_approx(lift(a.c.e4m3 != 0)) / ml.y : 0.f;
+                    sm_m[rt * a.tile_rows + row] = ml.x == kNone ? 0.f : ml.x;
+                    sm_r[rt * a.tile_rows + row] = ml.y > 0.f || ml.y != ml.y ? ex2_approx(lift(a.c.e4m3 != 0)) / ml.y : 0.f;
                 }
             }
         }
     __syncthreads();
     float *w = a.weights + bh * a.ld_weights;
     const float *z = a.logits + bh * a.rows * a.ld_logits;
-    for (int j = lo + threadIdx.x; j < hi; j += kThreads) {
-        float sum = 0.f;
-        if (j >= begin)
-            for (int r = 0; r < a.rows; ++r) {
-                const float s = z[r * a.ld_logits + j];
-                if (s != kNone) sum = fmaf(ex2_approx(s - sm_m[r]), sm_r[r], sum);
+    constexpr int kAt = kChunk / kThreads;  // slots of a thread
+    float sum[kAt];
+#pragma unroll
+    for (int x = 0; x < kAt; ++x) sum[x] = 0.f;
+    for (int r = 0; r < a.rows; ++r) {
+        const float m = sm_m[r], f = sm_r[r];
+#pragma unroll
+        for (int x = 0; x < kAt; ++x) {
+            const int j = lo + x * kThreads + threadIdx.x;
+            if (j >= begin && j < hi) {
+                const float s = __ldg(z + r * a.ld_logits + j);
+                sum[x] = s == kNone ? sum[x] : fmaf(ex2_approx(s - m), f, sum[x]);
             }
-        w[j] = fmaf(w[j], a.decay, sum);
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < kAt; ++x) {
+        const int j = lo + x * kThreads + threadIdx.x;
+        if (j < hi) w[j] = fmaf(w[j], a.decay, sum[x]);
     }
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NR>
 cudaError_t launch(AttnArgs &a, const DeviceInfo &di, cudaStream_t s) {
-    using C = Cfg<D, E4M3>;
+    using C = Cfg<D, E4M3, NR>;
     auto kern = attn_kernel<C>;
     cudaError_t e = ensure_smem((const void *)kern, C::SMEM);
     if (e != cudaSuccess) return e;
     // as many CTAs as are resident at once
-    const int per_sm = C::SMEM <= 112 * 1024 ? 2 : 1;
-    a.ctas = di.sm_count * per_sm < kMaxAttnCtas ? di.sm_count * per_sm : kMaxAttnCtas;
+    a.ctas = di.sm_count * C::PER_SM < kMaxAttnCtas ? di.sm_count * C::PER_SM : kMaxAttnCtas;
+    a.part_floats = part_floats(D, NR);
     e = launch_pdl(kern, dim3(a.ctas), dim3(kThreads), C::SMEM, s, dim3(1), a);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.c.batch * a.unit_heads;
-    const int64_t join_blocks = units * (kRows / kWarps);
-    const int chunks = a.weights ? (a.cap + kChunk - 1) / kChunk : 0;
-    return launch_pdl(join_kernel, dim3((unsigned)(join_blocks + (int64_t)a.c.batch * a.c.heads * chunks)), dim3(kThreads), 0, s,
-                      dim3(1), a, (int)join_blocks, chunks > 0 ? chunks : 1);
+    e = launch_pdl(join_kernel, dim3((unsigned)(units * NR * (D / 16))), dim3(kThreads), 0, s, dim3(1), a);
+    if (e != cudaSuccess || !a.weights) return e;
+    const int chunks = (a.cap + kChunk - 1) / kChunk;
+    return launch_pdl(weigh_kernel, dim3((unsigned)((int64_t)a.c.batch * a.c.heads * chunks)), dim3(kThreads), 0, s, dim3(1), a,
+                      chunks);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_rows(AttnArgs &a, const DeviceInfo &di, cudaStream_t s) {
+    switch (a.tile_rows) {
+        case 8: return launch<D, E4M3, 1>(a, di, s);
+        case 16: return launch<D, E4M3, 2>(a, di, s);
+        default:
+            if constexpr (D <= 128) return launch<D, E4M3, 4>(a, di, s);
+            return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace
 
-int attn_part_floats(int D) { return part_floats(D); }
+// One octet of rows where they fit; otherwise as few row tiles of up to 32 rows (16 for D =
+// 256, whose accumulators fill the registers) as hold them.
+int attn_tile_rows(int D, int rows) { return rows <= 8 ? 8 : rows <= 16 || D == 256 ? 16 : 32; }
+int attn_part_floats(int D, int tile_rows) { return part_floats(D, tile_rows / 8); }
 
 cudaError_t launch_attn_decode(const DeviceInfo &di, AttnArgs &a, cudaStream_t s) {
-    if (a.c.e4m3) return a.c.dim == 64 ? launch<64, true>(a, di, s) : a.c.dim == 128 ? launch<128, true>(a, di, s) : launch<256, true>(a, di, s);
-    return a.c.dim == 64 ? launch<64, false>(a, di, s) : a.c.dim == 128 ? launch<128, false>(a, di, s) : launch<256, false>(a, di, s);
+    if (a.c.e4m3) return a.c.dim == 64 ? launch_rows<64, true>(a, di, s) : a.c.dim == 128 ? launch_rows<128, true>(a, di, s) : launch_rows<256, true>(a, di, s);
+    return a.c.dim == 64 ? launch_rows<64, false>(a, di, s) : a.c.dim == 128 ? launch_rows<128, false>(a, di, s) : launch_rows<256, false>(a, di, s);
 }
 
 }  // namespace q4k

@@ -75,21 +75,24 @@ bool attn_shape_ok(const q4k_kv_cache *c, int32_t n_heads, int32_t n_q) {
     if (!cache_shape_ok(c) || n_heads < 1 || n_heads % c->n_kv_heads || n_q < 1 || n_q > 64) return false;
     const int64_t rows = (int64_t)n_q * (n_heads / c->n_kv_heads);
     if (rows > kMaxAttnRows) return false;
-    const int64_t units = (int64_t)c->batch * c->n_kv_heads * ((rows + 15) / 16);
-    return units * 4 < kInt31 / 2;  // blocks of the joining kernel
+    const int tile = attn_tile_rows(c->head_dim, (int)rows);
+    const int64_t units = (int64_t)c->batch * c->n_kv_heads * ((rows + tile - 1) / tile);
+    // blocks of the joining kernel; tiles times shares in 64 bits
+    return units * (tile / 8) * (c->head_dim / 16) < kInt31;
 }
 
 struct AttnLayout {
     size_t parts, unit_ml, prefix, logits, total;
 };
 AttnLayout attn_layout(const q4k_kv_cache *c, int32_t n_heads, int32_t n_q, int64_t ld_weights) {
-    const size_t rows = (size_t)n_q * (n_heads / c->n_kv_heads), units = (size_t)c->batch * c->n_kv_heads * ((rows + 15) / 16);
+    const size_t rows = (size_t)n_q * (n_heads / c->n_kv_heads);
+    const size_t tile = (size_t)attn_tile_rows(c->head_dim, (int)rows), units = (size_t)c->batch * c->n_kv_heads * ((rows + tile - 1) / tile);
     AttnLayout l;
     size_t at = 0;
     l.parts = at;
-    at += align256((size_t)2 * kMaxAttnCtas * attn_part_floats(c->head_dim) * 4);
+    at += align256((size_t)2 * kMaxAttnCtas * attn_part_floats(c->head_dim, (int)tile) * 4);
     l.unit_ml = at;
-    at += align256(units * 16 * sizeof(float2));
+    if (ld_weights > 0) at += align256(units * tile * sizeof(float2));
     l.prefix = at;
     at += align256(((size_t)c->batch + 1) * 8);
     l.logits = at;
@@ -184,7 +187,8 @@ q4k_status q4k_attn_decode(const q4k_kv_cache *cache, const int32_t *seq_lens, c
     a.n_q = n_q;
     a.group = n_heads / cache->n_kv_heads;
     a.rows = n_q * a.group;
-    a.row_tiles = (a.rows + 15) / 16;
+    a.tile_rows = attn_tile_rows(cache->head_dim, a.rows);
+    a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
     a.unit_heads = cache->n_kv_heads * a.row_tiles;
     a.cap = weights && ld_weights < a.c.capacity ? (int32_t)ld_weights : a.c.capacity;
     a.window = window;
@@ -197,7 +201,7 @@ q4k_status q4k_attn_decode(const q4k_kv_cache *cache, const int32_t *seq_lens, c
     a.logits = weights ? reinterpret_cast<float *>(base + l.logits) : nullptr;
     a.ld_logits = ld_weights;
     a.parts = reinterpret_cast<float *>(base + l.parts);
-    a.unit_ml = reinterpret_cast<float2 *>(base + l.unit_ml);
+    a.unit_ml = weights ? reinterpret_cast<float2 *>(base + l.unit_ml) : nullptr;
     a.prefix = reinterpret_cast<int64_t *>(base + l.prefix);
     return finish(launch_attn_decode(di, a, static_cast<cudaStream_t>(stream)));
 }

@@ -19,7 +19,8 @@ struct AttnArgs {
     uint16_t *o;
     int64_t ldo;
     int32_t n_q, group, rows;        // rows = n_q * group, token-major
-    int32_t row_tiles, unit_heads;   // row tiles of 16 per KV head; units per sequence = heads * row_tiles
+    int32_t tile_rows, row_tiles;    // rows of a row tile (attn_tile_rows), row tiles per KV head
+    int32_t unit_heads;              // units per sequence = heads * row_tiles
     int32_t cap;                     // largest length: of the table, and of the weights if kept
     int64_t window;
     float scale, softcap;            // scale * k_scale
@@ -30,11 +31,13 @@ struct AttnArgs {
     float *logits;                   // [batch * heads][rows][ld_logits], with weights only
     int64_t ld_logits;
     float *parts;                    // [2 * ctas] parts
-    float2 *unit_ml;                 // [batch * unit_heads][16]: (m, l) of units finished by one CTA
+    int32_t part_floats;
+    float2 *unit_ml;                 // [batch * unit_heads][tile_rows]: (m, l) of units finished by one CTA; with weights only
     int64_t *prefix;                 // [batch + 1]: tiles before each sequence
     int32_t ctas;
 };
-int attn_part_floats(int D);
+int attn_tile_rows(int D, int rows);
+int attn_part_floats(int D, int tile_rows);
 cudaError_t launch_attn_decode(const DeviceInfo &di, AttnArgs &a, cudaStream_t s);
 
 struct AppendArgs {
