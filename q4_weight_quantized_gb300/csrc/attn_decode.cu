@@ -135,10 +135,10 @@ struct Cfg {
     static_assert(STAGES >= 3 && KS * 512 <= STAGE, "a stage holds a warp's fragments of one octet");
 };
 
-// A position in the list of tiles: tile `tile` of `tiles` of unit (b, hr = head * row
-// tiles + row tile).
+// A position in the list of tiles: tile `tile` of `tiles` of unit (sequence b, KV head, row
+// tile rt).
 struct Pos {
-    int b, hr, tile, tiles;
+    int b, head, rt, tile, tiles;
     int begin, end;  // slots of the unit: the union of its rows' ranges
 };
 
@@ -159,8 +159,10 @@ __device__ __forceinline__ void enter(const AttnArgs &a, Pos &p, int ct) {
 __device__ __forceinline__ void advance(const AttnArgs &a, Pos &p, int ct) {
     if (++p.tile < p.tiles) return;
     p.tile = 0;
-    if (++p.hr < a.unit_heads) return;
-    p.hr = 0;
+    if (++p.rt < a.row_tiles) return;
+    p.rt = 0;
+    if (++p.head < a.c.heads) return;
+    p.head = 0;
     ++p.b;
     enter(a, p, ct);
 }
@@ -173,6 +175,19 @@ __device__ __forceinline__ void row_range(const AttnArgs &a, int r, int len, int
     }
     end = max(0, len - a.n_q + 1 + r / a.group);
     begin = a.window > 0 ? (int)max((int64_t)0, (int64_t)end - a.window) : 0;
+}
+
+// The list's `total` tiles go to min(ctas, total) shares, none of them empty: share i is
+// [share_begin(i), share_begin(i + 1)), empty from there on.
+__device__ __forceinline__ int64_t share_begin(int64_t total, int ctas, int i) {
+    if (total <= ctas) return min((int64_t)i, total);
+    return total >> 22 ? total * i / ctas : (uint32_t)total * (uint32_t)i / (uint32_t)ctas;  // (ctas <= 2^9)
+}
+// The share that holds tile t.
+__device__ __forceinline__ int share_of(int64_t total, int ctas, int64_t t) {
+    if (total <= ctas) return (int)t;
+    // the largest i with floor(total i / ctas) <= t
+    return total >> 22 ? (int)(((t + 1) * ctas - 1) / total) : (int)(((uint32_t)(t + 1) * (uint32_t)ctas - 1) / (uint32_t)total);
 }
 
 // This CTA's share of the list, tiles [t0, t1), and where it begins (if it is not empty); CTA 0
@@ -204,9 +219,8 @@ __device__ __forceinline__ void share_of_list(const AttnArgs &a, int64_t &t0, in
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
-    const int64_t shares = min((int64_t)a.ctas, total);  // none of them empty
-    t0 = blockIdx.x < shares ? total * blockIdx.x / shares : total;
-    t1 = blockIdx.x < shares ? total * (blockIdx.x + 1) / shares : total;
+    t0 = share_begin(total, a.ctas, blockIdx.x);
+    t1 = share_begin(total, a.ctas, blockIdx.x + 1);
     if (t0 < t1 && before <= t0 && t0 < before + sum) {
         // this thread's sequences hold the share's first tile
         Pos p;
@@ -217,8 +231,11 @@ __device__ __forceinline__ void share_of_list(const AttnArgs &a, int64_t &t0, in
             if (t0 < at + (int64_t)p.tiles * a.unit_heads) break;
             at += (int64_t)p.tiles * a.unit_heads;
         }
-        p.hr = (int)((t0 - at) / p.tiles);
-        p.tile = (int)((t0 - at) - (int64_t)p.hr * p.tiles);
+        const int64_t in = t0 - at;  // (64-bit division is long: only where it must be)
+        const int hr = in >> 31 ? (int)(in / p.tiles) : (int)((uint32_t)in / (uint32_t)p.tiles);
+        p.tile = (int)(in - (int64_t)hr * p.tiles);
+        p.head = (int)((uint32_t)hr / (uint32_t)a.row_tiles);
+        p.rt = hr - p.head * a.row_tiles;
         start = p;
     }
     if (blockIdx.x == 0) {
@@ -239,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
     constexpr int D = C::D, TOK = C::TOK, MT = C::MT, KS = C::KS, NR = C::NR;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sm_m[kWarps][8 * NR], sm_l[kWarps][8 * NR];
+    __shared__ float sm_cs[8 * NR];
     __shared__ int64_t sm_scan[kWarps];
     __shared__ uint32_t sm_stage[kWarps];
     __shared__ Pos sm_pos;
@@ -259,32 +277,41 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
     // flight.
     const int64_t steps = t1 - t0;
     int64_t copied = 0;
-    int32_t page = -1;
-    int slot = 0;
-    bool in = false;
-    auto fetch_page = [&] {
-        if (copied < steps) {
-            slot = nxt.begin + (nxt.tile * kWarps + warp) * TOK + (lane & (TOK - 1));
-            in = slot < nxt.end;
-            page = in ? __ldg(a.c.table + nxt.b * a.c.ld_table + page_of(a.c, slot)) : -1;
-        }
+    int64_t fetched = 0;
+    struct Fetched {
+        int32_t page, head;
+        uint32_t in_page;
+        bool in;
     };
-    auto copy_step = [&](int stage) {
+    auto fetch_page = [&] {
+        Fetched f = {-1, 0, 0, false};
+        if (fetched < steps) {
+            const int slot = nxt.begin + (nxt.tile * kWarps + warp) * TOK + (lane & (TOK - 1));
+            const uint32_t pg = page_of(a.c, slot);
+            f.in = slot < nxt.end;
+            f.in_page = (uint32_t)slot - pg * a.c.page_size;
+            f.head = nxt.head;
+            if (f.in) f.page = __ldg(a.c.table + nxt.b * a.c.ld_table + pg);
+            ++fetched;
+            advance(a, nxt, C::CT);
+        }
+        return f;
+    };
+    auto copy_step = [&](int stage, const Fetched &f) {
         if (copied < steps) {
             constexpr uint32_t kFull = TOK == 32 ? 0xFFFFFFFFu : (1u << TOK) - 1;
             constexpr int ROWS = 32 / C::CHUNKS;  // rows of a warp's copy instruction
-            const bool ok = in && page_ok(a.c, page);
-            if (in && !ok) atomicOr(a.c.status, kDevIndex);
+            const bool ok = f.in && page_ok(a.c, f.page);
+            if (f.in && !ok) atomicOr(a.c.status, kDevIndex);
             const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok) & kFull;
             if (lane == 0) sm_mask[warp][stage] = mask;
-            const int64_t off = ok ? row_bytes_at(a.c, page, (int)((uint32_t)nxt.hr / (uint32_t)a.row_tiles),
-                                                  (uint32_t)slot - page_of(a.c, slot) * a.c.page_size)
-                                   : 0;
+            const int64_t off = ok ? row_bytes_at(a.c, f.page, f.head, f.in_page) : 0;
             const int r = lane / C::CHUNKS, ch = lane % C::CHUNKS;
             const uint32_t to = ring + stage * C::STAGE + r * C::PITCH + ch * 16;
-            const int64_t first = __shfl_sync(0xFFFFFFFFu, off, 0), last = __shfl_sync(0xFFFFFFFFu, off, TOK - 1);
-            if (mask == kFull && last - first == (TOK - 1) * a.c.slot_bytes && __shfl_sync(0xFFFFFFFFu, page, 0) == __shfl_sync(0xFFFFFFFFu, page, TOK - 1)) {
-                // all slots, of one page
+            if (mask == kFull && __shfl_sync(0xFFFFFFFFu, f.in_page, TOK - 1) - __shfl_sync(0xFFFFFFFFu, f.in_page, 0) == TOK - 1 &&
+                __shfl_sync(0xFFFFFFFFu, f.page, TOK - 1) == __shfl_sync(0xFFFFFFFFu, f.page, 0)) {
+                // all slots, consecutive rows of one page
+                const int64_t first = __shfl_sync(0xFFFFFFFFu, off, 0);
                 const uint8_t *k = a.c.k + first + r * a.c.slot_bytes + ch * 16, *v = a.c.v + first + r * a.c.slot_bytes + ch * 16;
 #pragma unroll
                 for (int i = 0; i < TOK / ROWS; ++i) {
@@ -302,75 +329,77 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
                 }
             }
             ++copied;
-            advance(a, nxt, C::CT);
         }
         cp_async_commit();
-        fetch_page();
     };
-    fetch_page();
-    for (int s = 0; s < C::STAGES - 1; ++s) copy_step(s);
+    Fetched ahead[C::STAGES];
+#pragma unroll
+    for (int i = 0; i < C::STAGES; ++i) ahead[i] = fetch_page();
 
-    uint32_t qf[C::QSMEM ? 1 : NR][C::QSMEM ? 1 : KS][2];
+    uint32_t qf[C::QSMEM ? 1 : NR][KS][2];
     float o[NR][KS][4], m[NR][2], l[NR][2], cs[NR][2];
     int in_lo = 0, in_hi = 0;  // slots that every row of the unit reads
 
     // Queries of a unit as B operands (row n * 8 + g of the unit; values 2 c4, 2 c4 + 1 and 8 on, or for e4m3
     // those that ldmatrix leaves in this lane: 4 c4 .. 4 c4 + 3); e4m3: as f16, scaled by a power of two.
-    auto load_queries = [&](const Pos &p) {
-        const int head = (int)((uint32_t)p.hr / (uint32_t)a.row_tiles), r0 = (p.hr - head * a.row_tiles) * 8 * NR;
-        if constexpr (C::QSMEM) __syncthreads();  // the unit before has been read by every warp
+    auto query_octet = [&](const Pos &p, int n, uint32_t (&v)[KS][2]) {
+        const int r = p.rt * 8 * NR + n * 8 + g;
+        const int tok = (int)((uint32_t)r / (uint32_t)a.group), hq = p.head * a.group + r - tok * a.group;
+        const bool there = r < a.rows;
+        const uint16_t *row = a.q + ((int64_t)p.b * a.n_q + (there ? tok : 0)) * a.ldq + (int64_t)(there ? hq : 0) * D;
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            const int r = r0 + n * 8 + g;
-            const int tok = (int)((uint32_t)r / (uint32_t)a.group), hq = head * a.group + r - tok * a.group;
-            const bool there = r < a.rows;
-            const uint16_t *row = a.q + ((int64_t)p.b * a.n_q + (there ? tok : 0)) * a.ldq + (int64_t)(there ? hq : 0) * D;
-            uint32_t v[KS][2];
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+                v[ks][f] = there ? __ldg(reinterpret_cast<const uint32_t *>(row + ks * 16 + (C::E4M3 ? c4 * 4 + f * 2 : c4 * 2 + f * 8)))
+                                 : 0u;
+        float up = 1.f;
+        if constexpr (C::E4M3) {
+            float mx = 0.f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int f = 0; f < 2; ++f)
-                    v[ks][f] = there ? __ldg(reinterpret_cast<const uint32_t *>(
-                                           row + ks * 16 + (C::E4M3 ? c4 * 4 + f * 2 : c4 * 2 + f * 8)))
-                                     : 0u;
-            float up = 1.f;
-            if constexpr (C::E4M3) {
-                float mx = 0.f;
+                for (int f = 0; f < 2; ++f) mx = fmaxf(mx, fmaxf(fabsf(lo_f32(v[ks][f])), fabsf(hi_f32(v[ks][f]))));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+            // 2^(14 - exponent of the largest): f16 then holds bf16's 8 bits of every value down to
+            // 2^-28 of the largest
+            const int e = (int)(__float_as_uint(mx) >> 23);
+            if (e > 14 && e < 255) up = __uint_as_float((uint32_t)min(127 + 14 + 127 - e, 254) << 23);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) v[ks][f] = pack_f16(lo_f32(v[ks][f]) * up, hi_f32(v[ks][f]) * up);
+        }
+        return a.scale * kLog2e / up;  // the scores' factor of row g
+    };
+    auto load_queries = [&](const Pos &p) {
+        if constexpr (C::QSMEM) {
+            __syncthreads();  // the unit before has been read by every warp
+            if (warp < NR) {
+                uint32_t v[KS][2];
+                const float c = query_octet(p, warp, v);
+                if (c4 == 0) sm_cs[warp * 8 + g] = c;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) mx = fmaxf(mx, fmaxf(fabsf(lo_f32(v[ks][f])), fabsf(hi_f32(v[ks][f]))));
-                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-                // 2^(14 - exponent of the largest): f16 then holds bf16's 8 bits of every value down to
-                // 2^-28 of the largest
-                const int e = (int)(__float_as_uint(mx) >> 23);
-                if (e > 14 && e < 255) up = __uint_as_float((uint32_t)min(127 + 14 + 127 - e, 254) << 23);
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) v[ks][f] = pack_f16(lo_f32(v[ks][f]) * up, hi_f32(v[ks][f]) * up);
+                    asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(qs + ((warp * KS + ks) * 32 + lane) * 8), "r"(v[ks][0]), "r"(v[ks][1])
+                                 : "memory");
             }
-            // scores' factor: of rows n * 8 + 2 c4 and + 1, which other lanes hold as row g
-            const float c = a.scale * kLog2e / up;
-            cs[n][0] = __shfl_sync(0xFFFFFFFFu, c, c4 * 8);
-            cs[n][1] = __shfl_sync(0xFFFFFFFFu, c, c4 * 8 + 4);
-            if constexpr (C::QSMEM) {
+            __syncthreads();
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                    if (ks % kWarps == warp)
-                        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(qs + ((n * KS + ks) * 32 + lane) * 8), "r"(v[ks][0]),
-                                     "r"(v[ks][1])
-                                     : "memory");
-            } else {
+            for (int n = 0; n < NR; ++n) cs[n][0] = sm_cs[n * 8 + 2 * c4], cs[n][1] = sm_cs[n * 8 + 2 * c4 + 1];
+        } else {
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) qf[n][ks][0] = v[ks][0], qf[n][ks][1] = v[ks][1];
+            for (int n = 0; n < NR; ++n) {
+                const float c = query_octet(p, n, qf[n]);
+                // of rows n * 8 + 2 c4 and + 1, which other lanes hold as row g
+                cs[n][0] = __shfl_sync(0xFFFFFFFFu, c, c4 * 8);
+                cs[n][1] = __shfl_sync(0xFFFFFFFFu, c, c4 * 8 + 4);
             }
         }
-        if constexpr (C::QSMEM) __syncthreads();
     };
     auto begin_unit = [&](const Pos &p) {
-        const int r0 = p.hr % a.row_tiles * 8 * NR;
+        const int r0 = p.rt * 8 * NR;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             m[n][0] = m[n][1] = kNone;
@@ -386,6 +415,9 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
         row_range(a, min(r0 + 8 * NR, a.rows) - 1, p.end, in_lo, other);
     };
     load_queries(cur);
+#pragma unroll
+    for (int i = 0; i < C::STAGES - 1; ++i) copy_step(i, ahead[i]);
+    Fetched next = ahead[C::STAGES - 1];
     begin_unit(cur);
 
     int stage = 0;
@@ -394,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
         __syncwarp();
         const uint32_t mask = sm_mask[warp][stage];
         // every lane has read the step before, whose stage is filled next
-        copy_step(stage == 0 ? C::STAGES - 1 : stage - 1);
+        copy_step(stage == 0 ? C::STAGES - 1 : stage - 1, next);
+        next = fetch_page();
         const uint32_t k_at = ring + stage * C::STAGE, v_at = k_at + TOK * C::PITCH;
         const int j0 = cur.begin + (cur.tile * kWarps + warp) * TOK;  // first slot of the step
         if (mask) {
@@ -463,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
             }
             const uint32_t full = TOK == 32 ? 0xFFFFFFFFu : (1u << TOK) - 1;
             const bool inside = j0 >= in_lo && j0 + TOK <= in_hi;
-            const int r0 = cur.hr % a.row_tiles * 8 * NR;
+            const int r0 = cur.rt * 8 * NR;
             if (mask != full || !inside) {
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
@@ -481,22 +514,19 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
                     }
             }
             if (a.logits) {
-                const int head = (int)((uint32_t)cur.hr / (uint32_t)a.row_tiles);
+                float *at = a.logits + (((int64_t)cur.b * a.c.heads + cur.head) * a.rows + r0 + c4 * 2) * a.ld_logits + j0 + g;
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int r = r0 + n * 8 + c4 * 2 + e;
-                        if (r < a.rows) {
-                            float *row = a.logits + (((int64_t)cur.b * a.c.heads + head) * a.rows + r) * a.ld_logits;
+                        if (r0 + n * 8 + c4 * 2 + e < a.rows) {
 #pragma unroll
                             for (int t = 0; t < MT; ++t)
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const int j = j0 + t * 16 + h * 8 + g;
-                                    if (j < cur.end) row[j] = s[t][n][h * 2 + e];
-                                }
+                                for (int h = 0; h < 2; ++h)
+                                    if (j0 + t * 16 + h * 8 + g < cur.end) at[t * 16 + h * 8] = s[t][n][h * 2 + e];
                         }
+                        at += e == 0 ? a.ld_logits : 7 * a.ld_logits;
                     }
             }
             // ---- running maximum (rows 8 n + 2 c4, + 1: the same in all lanes of a column)
@@ -570,15 +600,15 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
                     for (int n = 0; n < NR; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
+                            // (selects: an index into s would move it to memory)
                             float p = 0.f;
 #pragma unroll
-                            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    if (at / 8 == t * 2 + h) {
-                                        p = s[t][n][h * 2 + e];
-                                        if ((at & 7) == g) s[t][n][h * 2 + e] = 0.f;
-                                    }
+                            for (int t = 0; t < MT; ++t) {
+                                const bool lower = at / 8 == t * 2, upper = at / 8 == t * 2 + 1, mine = (at & 7) == g;
+                                p = lower ? s[t][n][e] : upper ? s[t][n][2 + e] : p;
+                                s[t][n][e] = lower && mine ? 0.f : s[t][n][e];
+                                s[t][n][2 + e] = upper && mine ? 0.f : s[t][n][2 + e];
+                            }
                             p = __shfl_sync(0xFFFFFFFFu, p, (at & 7) * 4 + c4);
                             int begin, end;
                             row_range(a, r0 + n * 8 + c4 * 2 + e, cur.end, begin, end);
@@ -682,11 +712,9 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
         // that goes on after it in slot 1
         const bool began = was.tile <= done;
         const bool whole = began && ends;
-        const int head = (int)((uint32_t)was.hr / (uint32_t)a.row_tiles), r0 = (was.hr - head * a.row_tiles) * 8 * NR;
+        const int r0 = was.rt * 8 * NR;
         float *part = a.parts + (2 * (int64_t)blockIdx.x + began) * part_floats(D, NR);
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            float f[2], mt[2], lt[2];
+        auto joined = [&](int n, float (&mt)[2], float (&lt)[2]) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = n * 8 + c4 * 2 + e;
@@ -697,69 +725,98 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
                     if (sm_m[w][r] != kNone) lt[e] += sm_l[w][r] * ex2_approx(sm_m[w][r] - mt[e]);
-                f[e] = m[n][e] == kNone ? 0.f : ex2_approx(m[n][e] - mt[e]);
             }
-            // warps 2 and 3 hand over to 0 and 1, then 1 to 0, through the stage that each has just read
+        };
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            float mt[2], lt[2];
+            joined(n, mt, lt);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float f = m[n][e] == kNone ? 0.f : ex2_approx(m[n][e] - mt[e]);
+#pragma unroll
+                for (int i = 0; i < KS; ++i) o[n][i][e] *= f, o[n][i][2 + e] *= f;
+            }
+        }
+        // o' of an octet from one warp to another through the stage that the first has just read
+        auto put = [&](const float (&f)[KS][4]) {
 #pragma unroll
             for (int i = 0; i < KS; ++i)
+                sts128(read_stage + lane * 16 + i * 512,
+                       make_uint4(__float_as_uint(f[i][0]), __float_as_uint(f[i][1]), __float_as_uint(f[i][2]), __float_as_uint(f[i][3])));
+        };
+        auto add = [&](int from, float (&f)[KS][4]) {
+            const uint32_t at = sm_stage[from] + lane * 16;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) o[n][i][x] *= f[x & 1];
-            auto put = [&] {
+            for (int i = 0; i < KS; ++i) {
+                const uint4 t = lds128(at + i * 512);
+                f[i][0] += __uint_as_float(t.x), f[i][1] += __uint_as_float(t.y);
+                f[i][2] += __uint_as_float(t.z), f[i][3] += __uint_as_float(t.w);
+            }
+        };
+        auto write_out = [&](int n, const float (&f)[KS][4]) {
+            float mt[2], lt[2];
+            joined(n, mt, lt);
+            if (whole) {
 #pragma unroll
-                for (int i = 0; i < KS; ++i)
-                    sts128(read_stage + lane * 16 + i * 512, make_uint4(__float_as_uint(o[n][i][0]), __float_as_uint(o[n][i][1]), __float_as_uint(o[n][i][2]),
-                                                     __float_as_uint(o[n][i][3])));
-            };
-            auto add = [&](int from) {
-                const uint32_t at = sm_stage[from] + lane * 16;
+                for (int e = 0; e < 2; ++e) {
+                    const int r = r0 + n * 8 + c4 * 2 + e;
+                    if (r >= a.rows) continue;
+                    const int tok = (int)((uint32_t)r / (uint32_t)a.group);
+                    uint16_t *out = a.o + ((int64_t)was.b * a.n_q + tok) * a.ldo + (int64_t)(was.head * a.group + r - tok * a.group) * D;
+                    const float inv = lt[e] > 0.f || lt[e] != lt[e] ? a.v_scale / lt[e] : 0.f;
 #pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    const uint4 t = lds128(at + i * 512);
-                    o[n][i][0] += __uint_as_float(t.x), o[n][i][1] += __uint_as_float(t.y);
-                    o[n][i][2] += __uint_as_float(t.z), o[n][i][3] += __uint_as_float(t.w);
-                }
-            };
-            if (n > 0) __syncthreads();  // warp 1's stage has been read
-            if (warp >= 2) put();
-            __syncthreads();
-            if (warp < 2) add(warp + 2);
-            if (warp == 1) put();
-            __syncthreads();
-            if (warp == 0) {
-                add(1);
-                if (whole) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = r0 + n * 8 + c4 * 2 + e;
-                        if (r < a.rows) {
-                            const int tok = (int)((uint32_t)r / (uint32_t)a.group);
-                            uint16_t *out = a.o + ((int64_t)was.b * a.n_q + tok) * a.ldo + (int64_t)(head * a.group + r - tok * a.group) * D;
-                            const float inv = lt[e] > 0.f || lt[e] != lt[e] ? a.v_scale / lt[e] : 0.f;
-#pragma unroll
-                            for (int i = 0; i < KS; ++i) {
-                                if constexpr (C::E4M3) {
-                                    *reinterpret_cast<uint32_t *>(out + i * 16 + 2 * g) = pack_bf16(o[n][i][e] * inv, o[n][i][2 + e] * inv);
-                                } else {
-                                    const uint32_t t = pack_bf16(o[n][i][e] * inv, o[n][i][2 + e] * inv);
-                                    out[i * 16 + g] = (uint16_t)t;
-                                    out[i * 16 + 8 + g] = (uint16_t)(t >> 16);
-                                }
-                            }
-                            if (a.unit_ml && g == 0)
-                                a.unit_ml[((int64_t)was.b * a.unit_heads + was.hr) * 8 * NR + n * 8 + c4 * 2 + e] = make_float2(mt[e], lt[e]);
+                    for (int i = 0; i < KS; ++i) {
+                        const uint32_t t = pack_bf16(f[i][e] * inv, f[i][2 + e] * inv);
+                        if constexpr (C::E4M3) {
+                            *reinterpret_cast<uint32_t *>(out + i * 16 + 2 * g) = t;
+                        } else {
+                            out[i * 16 + g] = (uint16_t)t;
+                            out[i * 16 + 8 + g] = (uint16_t)(t >> 16);
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < KS; ++i)
-                        *reinterpret_cast<float4 *>(part + 16 * NR + ((n * KS + i) * 32 + lane) * 4) =
-                            make_float4(o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]);
-                    if (g == 0)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<float2 *>(part + 2 * (n * 8 + c4 * 2 + e)) = make_float2(mt[e], lt[e]);
+                    if (a.unit_ml && g == 0)
+                        a.unit_ml[((int64_t)was.b * a.unit_heads + was.head * a.row_tiles + was.rt) * 8 * NR + n * 8 + c4 * 2 + e] =
+                            make_float2(mt[e], lt[e]);
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+                    *reinterpret_cast<float4 *>(part + 16 * NR + ((n * KS + i) * 32 + lane) * 4) = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
+                if (g == 0)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<float2 *>(part + 2 * (n * 8 + c4 * 2 + e)) = make_float2(mt[e], lt[e]);
             }
+        };
+        if constexpr (NR == 1) {
+            // warps 2 and 3 to 0 and 1, then 1 to 0
+            if (warp >= 2) put(o[0]);
+            __syncthreads();
+            if (warp < 2) add(warp + 2, o[0]);
+            if (warp == 1) put(o[0]);
+            __syncthreads();
+            if (warp == 0) {
+                add(1, o[0]);
+                write_out(0, o[0]);
+            }
+        } else {
+            // warp n collects octet n: in round k from warp n + k
+#pragma unroll 1
+            for (int k = 1; k < kWarps; ++k) {
+                const int to = (warp - k) & (kWarps - 1);
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                    if (n == to) put(o[n]);
+                __syncthreads();
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                    if (n == warp) add((warp + k) & (kWarps - 1), o[n]);
+                __syncthreads();
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+                if (n == warp) write_out(n, o[n]);
         }
         __syncthreads();
         if (done + 1 < steps) {
@@ -776,16 +833,14 @@ struct Parts {
     int first, last;
     bool empty, whole;
 };
-__device__ __forceinline__ Parts parts_of(const AttnArgs &a, int64_t unit) {
-    const int b = (int)(unit / a.unit_heads), hr = (int)(unit - (int64_t)b * a.unit_heads);
+__device__ __forceinline__ Parts parts_of(const AttnArgs &a, int b, int hr) {
     const int64_t p0 = __ldg(a.prefix + b), p1 = __ldg(a.prefix + b + 1), total = __ldg(a.prefix + a.c.batch);
     Parts r = {0, 0, p0 == p1, false};
     if (!r.empty) {
-        const int64_t tiles = (p1 - p0) / a.unit_heads, t = p0 + hr * tiles;
-        // share i holds the tiles [total i / shares, total (i + 1) / shares)
-        const int64_t shares = min((int64_t)a.ctas, total);
-        r.first = (int)(((t + 1) * shares - 1) / total);
-        r.last = (int)(((t + tiles) * shares - 1) / total);
+        const int64_t all = p1 - p0;
+        const int64_t tiles = all >> 31 ? all / a.unit_heads : (uint32_t)all / (uint32_t)a.unit_heads, t = p0 + hr * tiles;
+        r.first = share_of(total, a.ctas, t);
+        r.last = share_of(total, a.ctas, t + tiles - 1);
         r.whole = r.first == r.last;
     }
     return r;
@@ -825,11 +880,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a) {
     pdl_trigger();
     const int D = a.c.dim, ks = D / 16, octets = a.tile_rows / 8;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
-    const int i = blockIdx.x % ks, n = blockIdx.x / ks % octets;
-    const int64_t unit = blockIdx.x / (ks * octets);
-    const Parts p = parts_of(a, unit);
+    const uint32_t unit = blockIdx.x / (uint32_t)(ks * octets), in_unit = blockIdx.x - unit * (uint32_t)(ks * octets);
+    const int n = (int)in_unit / ks, i = (int)in_unit - n * ks;
+    const int b = (int)(unit / (uint32_t)a.unit_heads), hr = (int)(unit - (uint32_t)b * (uint32_t)a.unit_heads);
+    const Parts p = parts_of(a, b, hr);
     if (p.whole) return;
-    const int b = (int)(unit / a.unit_heads), hr = (int)(unit % a.unit_heads), head = hr / a.row_tiles;
+    const int head = hr / a.row_tiles;
     const int r0 = hr % a.row_tiles * a.tile_rows + n * 8;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     float l[2] = {0.f, 0.f};
@@ -930,7 +986,7 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnArgs a, int c
     if (hi > begin)
         for (int rt = 0; rt < a.row_tiles; ++rt) {
             const int64_t unit = (int64_t)b * a.unit_heads + h * a.row_tiles + rt;
-            const Parts p = parts_of(a, unit);
+            const Parts p = parts_of(a, b, h * a.row_tiles + rt);
             for (int row = warp; row < a.tile_rows && rt * a.tile_rows + row < a.rows; row += kWarps) {
                 const float2 ml = join_ml(a, p, unit, row);
                 if (lane == 0) {
@@ -946,15 +1002,22 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnArgs a, int c
     float sum[kAt];
 #pragma unroll
     for (int x = 0; x < kAt; ++x) sum[x] = 0.f;
-    for (int r = 0; r < a.rows; ++r) {
-        const float m = sm_m[r], f = sm_r[r];
+    constexpr int kRowsAhead = 4;
+    for (int r0 = 0; r0 < a.rows; r0 += kRowsAhead) {
+        float s[kRowsAhead][kAt];  // all on their way before the first is used
 #pragma unroll
-        for (int x = 0; x < kAt; ++x) {
-            const int j = lo + x * kThreads + threadIdx.x;
-            if (j >= begin && j < hi) {
-                const float s = __ldg(z + r * a.ld_logits + j);
-                sum[x] = s == kNone ? sum[x] : fmaf(ex2_approx(s - m), f, sum[x]);
+        for (int y = 0; y < kRowsAhead; ++y)
+#pragma unroll
+            for (int x = 0; x < kAt; ++x) {
+                const int j = lo + x * kThreads + threadIdx.x;
+                s[y][x] = r0 + y < a.rows && j >= begin && j < hi ? __ldg(z + (r0 + y) * a.ld_logits + j) : kNone;
             }
+#pragma unroll
+        for (int y = 0; y < kRowsAhead; ++y) {
+            if (r0 + y >= a.rows) break;
+            const float m = sm_m[r0 + y], f = sm_r[r0 + y];
+#pragma unroll
+            for (int x = 0; x < kAt; ++x) sum[x] = s[y][x] == kNone ? sum[x] : fmaf(ex2_approx(s[y][x] - m), f, sum[x]);
         }
     }
 #pragma unroll
