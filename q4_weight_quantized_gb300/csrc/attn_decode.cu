@@ -16,8 +16,10 @@
 //     are the second product's B operand after one 8 x 8 transpose in registers.
 //   - The batch's work is one list of tiles (sequence, head, row tile, 4 steps of
 //     slots), cut into equal contiguous shares, one per CTA, whatever the lengths are:
-//     a share may end one unit, hold whole units and begin another.  Whole units are
-//     finished in place; parts leave (m, l, o') in the workspace for join_kernel.
+//     a share may end one unit, hold whole units and begin another.  After a unit's
+//     tiles the list holds kExtra places that stand for the time of ending one unit and
+//     beginning the next.  Whole units are finished in place; parts leave (m, l, o') in
+//     the workspace for join_kernel.
 //   - Each warp owns a ring of stages in shared memory and fills it with its own steps by
 //     16-byte asynchronous copies (any page size, any strides; one address for a step
 //     within a page), so no barrier lies in the main loop.  Rows lie RB + 16 bytes
@@ -40,6 +42,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -INFINITY;
 constexpr float kSlack = 8.f;       // how far (log2) a score may exceed the running maximum
+constexpr int kExtra = 2;           // places of the list after a unit's tiles
 
 // 16 bytes into shared memory, of which the last 16 - bytes become zeros
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
@@ -135,65 +138,75 @@ struct Cfg {
     static_assert(STAGES >= 3 && KS * 512 <= STAGE, "a stage holds a warp's fragments of one octet");
 };
 
-// A position in the list of tiles: tile `tile` of `tiles` of unit (sequence b, KV head, row
-// tile rt).
-struct Pos {
-    int b, head, rt, tile, tiles;
-    int begin, end;  // slots of the unit: the union of its rows' ranges
-};
-
 // Length of sequence b, cut to what table (and weights) can hold, and the slots its rows read.
 __device__ __forceinline__ void seq_range(const AttnArgs &a, int b, int &begin, int &len) {
     len = max(0, min(__ldg(a.seq_lens + b), a.cap));
     begin = 0;
     if (a.window > 0) begin = (int)max((int64_t)0, (int64_t)len - a.n_q + 1 - a.window);
 }
-__device__ __forceinline__ void enter(const AttnArgs &a, Pos &p, int ct) {
-    // the next sequence with slots; the list ends at a.c.batch
-    for (; p.b < a.c.batch; ++p.b) {
-        seq_range(a, p.b, p.begin, p.end);
-        p.tiles = (p.end - p.begin + ct - 1) / ct;
-        if (p.tiles > 0) return;
-    }
-}
-__device__ __forceinline__ void advance(const AttnArgs &a, Pos &p, int ct) {
-    if (++p.tile < p.tiles) return;
-    p.tile = 0;
-    if (++p.rt < a.row_tiles) return;
-    p.rt = 0;
-    if (++p.head < a.c.heads) return;
-    p.head = 0;
-    ++p.b;
-    enter(a, p, ct);
+// Places of one unit of n slots.
+template <int CT>
+__device__ __forceinline__ int places(int n) {
+    return n > 0 ? (n + CT - 1) / CT + kExtra : 0;
 }
 
-// Slots [begin, end) of row r (token-major: token r / group) of a sequence of length len.
-__device__ __forceinline__ void row_range(const AttnArgs &a, int r, int len, int &begin, int &end) {
-    if (r >= a.rows) {
-        begin = end = 0;
-        return;
+// A position in a share: tile `tile` of `tiles` of unit (sequence b, KV head, row tile rt).
+struct Pos {
+    int b, head, rt, tile, tiles;
+    int begin, end;  // slots of the unit: the union of its rows' ranges
+    int64_t left;    // places of the share from here on
+    // the next sequence with slots, if the share goes on
+    template <int CT>
+    __device__ __forceinline__ void enter(const AttnArgs &a) {
+        for (; left > 0 && b < a.c.batch; ++b) {
+            seq_range(a, b, begin, end);
+            tiles = (end - begin + CT - 1) / CT;
+            if (tiles > 0) return;
+        }
+        left = 0;
     }
-    end = max(0, len - a.n_q + 1 + r / a.group);
+    template <int CT>
+    __device__ __forceinline__ void next_unit(const AttnArgs &a) {
+        tile = 0;
+        if (++rt < a.row_tiles) return;
+        rt = 0;
+        if (++head < a.c.heads) return;
+        head = 0;
+        ++b;
+        enter<CT>(a);
+    }
+    template <int CT>
+    __device__ __forceinline__ void advance(const AttnArgs &a) {
+        --left;
+        if (++tile < tiles) return;
+        left -= kExtra;
+        next_unit<CT>(a);
+    }
+};
+
+// Slots [begin, end) of row r, of token `tok`, of a sequence of length len.
+__device__ __forceinline__ void row_range(const AttnArgs &a, int r, int tok, int len, int &begin, int &end) {
+    end = r < a.rows ? max(0, len - a.n_q + 1 + tok) : 0;
     begin = a.window > 0 ? (int)max((int64_t)0, (int64_t)end - a.window) : 0;
 }
 
-// The list's `total` tiles go to min(ctas, total) shares, none of them empty: share i is
-// [share_begin(i), share_begin(i + 1)), empty from there on.
+// The list's `total` places go to min(ctas, total) shares: share i is [share_begin(i),
+// share_begin(i + 1)), empty from there on.
 __device__ __forceinline__ int64_t share_begin(int64_t total, int ctas, int i) {
     if (total <= ctas) return min((int64_t)i, total);
     return total >> 22 ? total * i / ctas : (uint32_t)total * (uint32_t)i / (uint32_t)ctas;  // (ctas <= 2^9)
 }
-// The share that holds tile t.
+// The share that holds place t.
 __device__ __forceinline__ int share_of(int64_t total, int ctas, int64_t t) {
     if (total <= ctas) return (int)t;
     // the largest i with floor(total i / ctas) <= t
     return total >> 22 ? (int)(((t + 1) * ctas - 1) / total) : (int)(((uint32_t)(t + 1) * (uint32_t)ctas - 1) / (uint32_t)total);
 }
 
-// This CTA's share of the list, tiles [t0, t1), and where it begins (if it is not empty); CTA 0
-// also writes the prefix sums over the sequences for the joining kernel.
+// Where this CTA's share begins (left = 0: it is empty); CTA 0 also writes the places before
+// each sequence for the joining kernel.
 template <int CT>
-__device__ __forceinline__ void share_of_list(const AttnArgs &a, int64_t &t0, int64_t &t1, Pos &start, int64_t *scratch) {
+__device__ __forceinline__ void share_of_list(const AttnArgs &a, Pos &start, int64_t *scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.c.batch + kThreads - 1) / kThreads;
     const int lo = min(tid * per, a.c.batch), hi = min(lo + per, a.c.batch);
@@ -202,7 +215,7 @@ __device__ __forceinline__ void share_of_list(const AttnArgs &a, int64_t &t0, in
         int begin, len;
         if (blockIdx.x == 0 && __ldg(a.seq_lens + b) > a.cap) atomicOr(a.c.status, kDevIndex);
         seq_range(a, b, begin, len);
-        sum += (len - begin + CT - 1) / CT;
+        sum += places<CT>(len - begin);
     }
     sum *= a.unit_heads;
     int64_t inc = sum;
@@ -212,6 +225,7 @@ __device__ __forceinline__ void share_of_list(const AttnArgs &a, int64_t &t0, in
         if (lane >= o) inc += v;
     }
     if (lane == 31) scratch[warp] = inc;
+    if (tid == 0) start.left = 0;
     __syncthreads();
     int64_t before = inc - sum, total = 0;
 #pragma unroll
@@ -219,23 +233,29 @@ __device__ __forceinline__ void share_of_list(const AttnArgs &a, int64_t &t0, in
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
-    t0 = share_begin(total, a.ctas, blockIdx.x);
-    t1 = share_begin(total, a.ctas, blockIdx.x + 1);
+    const int64_t t0 = share_begin(total, a.ctas, blockIdx.x), t1 = share_begin(total, a.ctas, blockIdx.x + 1);
     if (t0 < t1 && before <= t0 && t0 < before + sum) {
-        // this thread's sequences hold the share's first tile
+        // this thread's sequences hold the share's first place
         Pos p;
         int64_t at = before;
+        int n = 0;
         for (p.b = lo;; ++p.b) {
             seq_range(a, p.b, p.begin, p.end);
-            p.tiles = (p.end - p.begin + CT - 1) / CT;
-            if (t0 < at + (int64_t)p.tiles * a.unit_heads) break;
-            at += (int64_t)p.tiles * a.unit_heads;
+            n = places<CT>(p.end - p.begin);
+            if (t0 < at + (int64_t)n * a.unit_heads) break;
+            at += (int64_t)n * a.unit_heads;
         }
         const int64_t in = t0 - at;  // (64-bit division is long: only where it must be)
-        const int hr = in >> 31 ? (int)(in / p.tiles) : (int)((uint32_t)in / (uint32_t)p.tiles);
-        p.tile = (int)(in - (int64_t)hr * p.tiles);
-        p.head = (int)((uint32_t)hr / (uint32_t)a.row_tiles);
+        const int hr = in >> 31 ? (int)(in / n) : (int)((uint32_t)in / (uint32_t)n);
+        p.tile = (int)(in - (int64_t)hr * n);
+        p.head = a.row_tiles == 1 ? hr : hr / a.row_tiles;
         p.rt = hr - p.head * a.row_tiles;
+        p.tiles = n - kExtra;
+        p.left = t1 - t0;
+        if (p.tile >= p.tiles) {  // it begins after a unit's tiles
+            p.left -= n - p.tile;
+            p.next_unit<CT>(a);
+        }
         start = p;
     }
     if (blockIdx.x == 0) {
@@ -244,7 +264,7 @@ __device__ __forceinline__ void share_of_list(const AttnArgs &a, int64_t &t0, in
             int begin, len;
             a.prefix[b] = at;
             seq_range(a, b, begin, len);
-            at += (int64_t)((len - begin + CT - 1) / CT) * a.unit_heads;
+            at += (int64_t)places<CT>(len - begin) * a.unit_heads;
         }
         if (tid == 0) a.prefix[a.c.batch] = total;
     }
@@ -259,46 +279,48 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
     __shared__ float sm_cs[8 * NR];
     __shared__ int64_t sm_scan[kWarps];
     __shared__ uint32_t sm_stage[kWarps];
+    __shared__ uint8_t sm_tok[kMaxAttnRows];  // token of a row: rows are token-major
+    __shared__ struct {
+        int64_t row;
+        float inv;
+    } sm_out[8 * NR];  // a row's place in o, and v_scale / l
     __shared__ Pos sm_pos;
     __shared__ uint32_t sm_mask[kWarps][C::STAGES];  // slots of a stage that are there
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c4 = lane & 3;
+    for (int r = tid; r < a.row_tiles * 8 * NR; r += kThreads) sm_tok[r] = (uint8_t)(min(r, a.rows - 1) / a.group);
     pdl_wait();
     pdl_trigger();
-    int64_t t0, t1;
-    share_of_list<C::CT>(a, t0, t1, sm_pos, sm_scan);
-    if (t0 >= t1) return;
+    share_of_list<C::CT>(a, sm_pos, sm_scan);
     Pos cur = sm_pos, nxt = cur;
+    if (cur.left <= 0) return;
+    bool began = cur.tile == 0;  // the unit begins in this share
 
     const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
     const uint32_t qs = smem_u32(smem) + C::RING;
 
     // ---- copies.  Lane i holds slot i of a step; the page ids of the step to be copied next are in
     // flight.
-    const int64_t steps = t1 - t0;
-    int64_t copied = 0;
-    int64_t fetched = 0;
     struct Fetched {
         int32_t page, head;
         uint32_t in_page;
-        bool in;
+        bool in, step;  // step: there is one
     };
     auto fetch_page = [&] {
-        Fetched f = {-1, 0, 0, false};
-        if (fetched < steps) {
+        Fetched f = {-1, 0, 0, false, nxt.left > 0};
+        if (f.step) {
             const int slot = nxt.begin + (nxt.tile * kWarps + warp) * TOK + (lane & (TOK - 1));
             const uint32_t pg = page_of(a.c, slot);
             f.in = slot < nxt.end;
             f.in_page = (uint32_t)slot - pg * a.c.page_size;
             f.head = nxt.head;
             if (f.in) f.page = __ldg(a.c.table + nxt.b * a.c.ld_table + pg);
-            ++fetched;
-            advance(a, nxt, C::CT);
+            nxt.advance<C::CT>(a);
         }
         return f;
     };
     auto copy_step = [&](int stage, const Fetched &f) {
-        if (copied < steps) {
+        if (f.step) {
             constexpr uint32_t kFull = TOK == 32 ? 0xFFFFFFFFu : (1u << TOK) - 1;
             constexpr int ROWS = 32 / C::CHUNKS;  // rows of a warp's copy instruction
             const bool ok = f.in && page_ok(a.c, f.page);
@@ -328,7 +350,6 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
                     cp_async16(to + (TOK + i * ROWS) * C::PITCH, a.c.v + o, n);
                 }
             }
-            ++copied;
         }
         cp_async_commit();
     };
@@ -344,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
     // those that ldmatrix leaves in this lane: 4 c4 .. 4 c4 + 3); e4m3: as f16, scaled by a power of two.
     auto query_octet = [&](const Pos &p, int n, uint32_t (&v)[KS][2]) {
         const int r = p.rt * 8 * NR + n * 8 + g;
-        const int tok = (int)((uint32_t)r / (uint32_t)a.group), hq = p.head * a.group + r - tok * a.group;
+        const int tok = sm_tok[r], hq = p.head * a.group + r - tok * a.group;
         const bool there = r < a.rows;
         const uint16_t *row = a.q + ((int64_t)p.b * a.n_q + (there ? tok : 0)) * a.ldq + (int64_t)(there ? hq : 0) * D;
 #pragma unroll
@@ -411,8 +432,9 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
         }
         // the first token's rows read the least at the end, the last one's at the begin
         int other;
-        row_range(a, r0, p.end, other, in_hi);
-        row_range(a, min(r0 + 8 * NR, a.rows) - 1, p.end, in_lo, other);
+        const int r1 = min(r0 + 8 * NR, a.rows) - 1;
+        row_range(a, r0, sm_tok[r0], p.end, other, in_hi);
+        row_range(a, r1, sm_tok[r1], p.end, in_lo, other);
     };
     load_queries(cur);
 #pragma unroll
@@ -421,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
     begin_unit(cur);
 
     int stage = 0;
-    for (int64_t done = 0; done < steps; ++done) {
+    while (true) {
         cp_async_wait<C::STAGES - 2>();
         __syncwarp();
         const uint32_t mask = sm_mask[warp][stage];
@@ -503,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         int begin, end;
-                        row_range(a, r0 + n * 8 + c4 * 2 + e, cur.end, begin, end);
+                        const int r = r0 + n * 8 + c4 * 2 + e;
+                        row_range(a, r, sm_tok[r], cur.end, begin, end);
 #pragma unroll
                         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -611,7 +634,8 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
                             }
                             p = __shfl_sync(0xFFFFFFFFu, p, (at & 7) * 4 + c4);
                             int begin, end;
-                            row_range(a, r0 + n * 8 + c4 * 2 + e, cur.end, begin, end);
+                            const int r = r0 + n * 8 + c4 * 2 + e;
+                            row_range(a, r, sm_tok[r], cur.end, begin, end);
                             if (j >= begin && j < end)
 #pragma unroll
                                 for (int i = 0; i < KS; ++i)
@@ -689,14 +713,16 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
         stage = stage + 1 == C::STAGES ? 0 : stage + 1;
 
         const bool ends = cur.tile + 1 == cur.tiles;
-        if (!ends && done + 1 < steps) {
+        if (!ends && cur.left > 1) {
+            --cur.left;
             ++cur.tile;
             continue;
         }
         // ---- the unit or the share ends: join the warps
-        Pos was = cur;
-        advance(a, cur, C::CT);
-        if (!C::QSMEM && done + 1 < steps) load_queries(cur);  // (on their way during what follows; cs is not needed any more)
+        const Pos was = cur;
+        cur.advance<C::CT>(a);
+        const bool more_units = cur.left > 0;
+        if (!C::QSMEM && more_units) load_queries(cur);  // (on their way during what follows; cs is not needed any more)
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -710,34 +736,34 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
         __syncthreads();
         // of its share's parts, a CTA leaves that of a unit begun before it in slot 0 and that of a unit
         // that goes on after it in slot 1
-        const bool began = was.tile <= done;
         const bool whole = began && ends;
-        const int r0 = was.rt * 8 * NR;
         float *part = a.parts + (2 * (int64_t)blockIdx.x + began) * part_floats(D, NR);
-        auto joined = [&](int n, float (&mt)[2], float (&lt)[2]) {
+        // thread r joins (m, l) of row r, for everybody
+        if (tid < 8 * NR) {
+            float mt = kNone, lt = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = n * 8 + c4 * 2 + e;
-                mt[e] = kNone;
-                lt[e] = 0.f;
+            for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, sm_m[w][tid]);
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) mt[e] = fmaxf(mt[e], sm_m[w][r]);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    if (sm_m[w][r] != kNone) lt[e] += sm_l[w][r] * ex2_approx(sm_m[w][r] - mt[e]);
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = sm_m[w][tid] == kNone ? 0.f : ex2_approx(sm_m[w][tid] - mt);
+                lt = fmaf(f, sm_l[w][tid], lt);
+                sm_l[w][tid] = f;
             }
-        };
+            const int r = was.rt * 8 * NR + tid, tok = sm_tok[r];
+            sm_out[tid].row = ((int64_t)was.b * a.n_q + tok) * a.ldo + (int64_t)(was.head * a.group + r - tok * a.group) * D;
+            sm_out[tid].inv = lt > 0.f || lt != lt ? a.v_scale / lt : 0.f;
+            if (!whole) *reinterpret_cast<float2 *>(part + 2 * tid) = make_float2(mt, lt);
+            else if (a.unit_ml) a.unit_ml[((int64_t)was.b * a.unit_heads + was.head * a.row_tiles) * 8 * NR + r] = make_float2(mt, lt);
+        }
+        __syncthreads();
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            float mt[2], lt[2];
-            joined(n, mt, lt);
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float f = m[n][e] == kNone ? 0.f : ex2_approx(m[n][e] - mt[e]);
+                const float f = sm_l[warp][n * 8 + c4 * 2 + e];
 #pragma unroll
                 for (int i = 0; i < KS; ++i) o[n][i][e] *= f, o[n][i][2 + e] *= f;
             }
-        }
         // o' of an octet from one warp to another through the stage that the first has just read
         auto put = [&](const float (&f)[KS][4]) {
 #pragma unroll
@@ -755,16 +781,13 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
             }
         };
         auto write_out = [&](int n, const float (&f)[KS][4]) {
-            float mt[2], lt[2];
-            joined(n, mt, lt);
             if (whole) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int r = r0 + n * 8 + c4 * 2 + e;
-                    if (r >= a.rows) continue;
-                    const int tok = (int)((uint32_t)r / (uint32_t)a.group);
-                    uint16_t *out = a.o + ((int64_t)was.b * a.n_q + tok) * a.ldo + (int64_t)(was.head * a.group + r - tok * a.group) * D;
-                    const float inv = lt[e] > 0.f || lt[e] != lt[e] ? a.v_scale / lt[e] : 0.f;
+                    const int r = n * 8 + c4 * 2 + e;
+                    if (was.rt * 8 * NR + r >= a.rows) continue;
+                    uint16_t *out = a.o + sm_out[r].row;
+                    const float inv = sm_out[r].inv;
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
                         const uint32_t t = pack_bf16(f[i][e] * inv, f[i][2 + e] * inv);
@@ -775,18 +798,11 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
                             out[i * 16 + 8 + g] = (uint16_t)(t >> 16);
                         }
                     }
-                    if (a.unit_ml && g == 0)
-                        a.unit_ml[((int64_t)was.b * a.unit_heads + was.head * a.row_tiles + was.rt) * 8 * NR + n * 8 + c4 * 2 + e] =
-                            make_float2(mt[e], lt[e]);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < KS; ++i)
                     *reinterpret_cast<float4 *>(part + 16 * NR + ((n * KS + i) * 32 + lane) * 4) = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
-                if (g == 0)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<float2 *>(part + 2 * (n * 8 + c4 * 2 + e)) = make_float2(mt[e], lt[e]);
             }
         };
         if constexpr (NR == 1) {
@@ -819,10 +835,10 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
                 if (n == warp) write_out(n, o[n]);
         }
         __syncthreads();
-        if (done + 1 < steps) {
-            if (C::QSMEM) load_queries(cur);
-            begin_unit(cur);
-        }
+        if (!more_units) break;
+        if (C::QSMEM) load_queries(cur);
+        begin_unit(cur);
+        began = true;
     }
     cp_async_wait<0>();
 }
@@ -838,9 +854,9 @@ __device__ __forceinline__ Parts parts_of(const AttnArgs &a, int b, int hr) {
     Parts r = {0, 0, p0 == p1, false};
     if (!r.empty) {
         const int64_t all = p1 - p0;
-        const int64_t tiles = all >> 31 ? all / a.unit_heads : (uint32_t)all / (uint32_t)a.unit_heads, t = p0 + hr * tiles;
+        const int64_t n = all >> 31 ? all / a.unit_heads : (uint32_t)all / (uint32_t)a.unit_heads, t = p0 + hr * n;
         r.first = share_of(total, a.ctas, t);
-        r.last = share_of(total, a.ctas, t + tiles - 1);
+        r.last = share_of(total, a.ctas, t + n - kExtra - 1);
         r.whole = r.first == r.last;
     }
     return r;

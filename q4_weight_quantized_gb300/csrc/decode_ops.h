@@ -33,7 +33,7 @@ struct AttnArgs {
     float *parts;                    // [2 * ctas] parts
     int32_t part_floats;
     float2 *unit_ml;                 // [batch * unit_heads][tile_rows]: (m, l) of units finished by one CTA; with weights only
-    int64_t *prefix;                 // [batch + 1]: tiles before each sequence
+    int64_t *prefix;                 // [batch + 1]: places of the list before each sequence
     int32_t ctas;
 };
 int attn_tile_rows(int D, int rows);
