@@ -3,23 +3,25 @@
 // The row's weights are whole numbers w = floor(2^(40 - d)), d = (z_max - z) / (T ln 2),
 // so sums are exact in any order and every decision (which tokens top-p keeps, which
 // one the random number falls on) is an integer comparison: the token does not depend
-// on how the work is split.  What is kept by top-k and top-p is a prefix in rank (logit
+// on how the work is split.  What top-k and top-p keep is a prefix in rank (logit
 // descending, index ascending), so all that has to be found is where it ends.
 //
 // A cluster of CTAs owns a row: each keeps its contiguous share of the logits in shared
 // memory, so the row is read from global memory once, and the CTAs exchange bins, sums
 // and cuts through distributed shared memory.
 //   1. load, largest logit;
-//   2. counts and weights per bin of d (monotone in the logit), at first only for d <
-//      kHead: the tail's weight, which rarely matters for the cut, is added up in
-//      registers without atomics; if the cut turns out to lie in the tail, again with
-//      all of d < 41;
-//   3. the bin in which top-k (then top-p) ends; its tokens, if few, are ranked against
-//      each other; if many, the bin is narrowed by histograms over their keys first;
-//      equal logits are counted off by index;
+//   2. the weight (and for top-k the count) of the tokens in bins of d, 2^s bins to an
+//      octave.  With top-k the cut is near the top: 64 bins to an octave of 16, and what
+//      lies below is not even weighed.  Otherwise 32 to an octave of 32; the rest is added
+//      up without bins.  If the cut turns out to lie below, again with all 41;
+//   3. the tokens of the bin in which top-k (then top-p) ends are ranked against each
+//      other if they are few; if many, the bin is first narrowed by histograms over their
+//      keys; equal logits are counted off by index;
 //   4. the sum of what is kept, the target, and the token by a scan in index order.
-// Bound by the arithmetic of the weights (about 40 instructions a logit) for many rows
-// and by the latency of the cluster's exchanges for one.
+// A bin never crosses an octave, so its tokens' weights have one scale: they are summed as
+// two 12-bit halves of a 24-bit number by 32-bit atomics without a result.
+// Bound by the arithmetic of the weights (some 70 instructions a logit in all, half of
+// them on two logits at once) for many rows, by the cluster's exchanges for one.
 #include <cuda_runtime.h>
 
 #include "decode_ops.h"
@@ -28,15 +30,15 @@
 namespace q4k {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
-constexpr int kList = 512;             // tokens of a bin that are ranked against each other
+constexpr int kList = 768;           // tokens of a bin that are ranked against each other
 constexpr int kMaxCluster = 8;
-constexpr int kCached = 19456;         // logits of a CTA that stay in shared memory with two CTAs on an SM
-constexpr float kHead = 12.f;          // d below which a token's bin is counted at once
-constexpr float kAll = 41.f;           // from here on the weight is 0
+constexpr int kCached = 19456;       // logits of a CTA that stay in shared memory with two CTAs on an SM
+constexpr float kAll = 41.f;         // from this d on the weight is 0
 constexpr uint32_t kOne = 1u << 24;
+constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 typedef unsigned long long u64;
 
@@ -44,20 +46,47 @@ __device__ __forceinline__ uint32_t key_of(float z) {
     const uint32_t u = __float_as_uint(z);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float clean(float z) { return z != z ? -INFINITY : z + 0.f; }  // NaN is -inf, -0 is +0
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k); }
+// The negative of a logit, as the row is kept: NaN counts as -inf, -0 as +0.
+__device__ __forceinline__ float stored(float z) { return z != z ? INFINITY : -(z + 0.f); }
 
-// 2^-1/2 (-ln 2)^i / i!: the series of 2^-f about f = 1/2
-__device__ __forceinline__ u64 weight_of(float d) {
-    const float n = floorf(d), f = __fsub_rn(__fsub_rn(d, n), 0.5f);
-    float p = -1.0785311133076902e-05f;
-    p = __fadd_rn(__fmul_rn(p, f), 0.00010891940473811701f);
-    p = __fadd_rn(__fmul_rn(p, f), -0.0009428249322809279f);
-    p = __fadd_rn(__fmul_rn(p, f), 0.006801044102758169f);
-    p = __fadd_rn(__fmul_rn(p, f), -0.03924733027815819f);
-    p = __fadd_rn(__fmul_rn(p, f), 0.16986578702926636f);
-    p = __fadd_rn(__fmul_rn(p, f), -0.4901290833950043f);
-    p = __fadd_rn(__fmul_rn(p, f), 0.7071067690849304f);
-    return ((u64)(uint32_t)__fmul_rn(p, 16777216.f) << 16) >> (int)n;
+// Two fp32 operations at once, each rounded on its own.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<u64 *>(&a)), "l"(*reinterpret_cast<u64 *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 sum2(float2 a, float2 b) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<u64 *>(&a)), "l"(*reinterpret_cast<u64 *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// floor(2^24 2^-f) and n of two distances 0 <= d < 2^22, n = floor(d), f = d - n: the series
+// of 2^-f about f = 1/2, coefficients 2^-1/2 (-ln 2)^i / i!.
+__device__ __forceinline__ void mantissa2(float2 d, uint32_t (&w)[2], uint32_t (&n)[2]) {
+    // 2^23 + d, rounded down, is 2^23 + n
+    const float2 t = make_float2(__fadd_rd(d.x, 8388608.f), __fadd_rd(d.y, 8388608.f));
+    n[0] = __float_as_uint(t.x) & 0x7FFFFF, n[1] = __float_as_uint(t.y) & 0x7FFFFF;
+    const float2 whole = sum2(t, both(-8388608.f));
+    const float2 f = sum2(sum2(d, make_float2(-whole.x, -whole.y)), both(-0.5f));
+    float2 p = both(-1.0785311133076902e-05f);
+    p = sum2(mul2(p, f), both(0.00010891940473811701f));
+    p = sum2(mul2(p, f), both(-0.0009428249322809279f));
+    p = sum2(mul2(p, f), both(0.006801044102758169f));
+    p = sum2(mul2(p, f), both(-0.03924733027815819f));
+    p = sum2(mul2(p, f), both(0.16986578702926636f));
+    p = sum2(mul2(p, f), both(-0.4901290833950043f));
+    p = sum2(mul2(p, f), both(0.7071067690849304f));
+    p = mul2(p, both(16777216.f));
+    w[0] = (uint32_t)p.x, w[1] = (uint32_t)p.y;
+}
+__device__ __forceinline__ u64 scaled(uint32_t w, uint32_t n) { return ((u64)w << 16) >> n; }
+__device__ __forceinline__ u64 weight_of(float d) {  // d < kAll
+    uint32_t w[2], n[2];
+    mantissa2(both(d), w, n);
+    return scaled(w[0], n[0]);
 }
 // floor(total * share / 2^24)
 __device__ __forceinline__ u64 part_of(u64 total, uint32_t share) {
@@ -70,22 +99,12 @@ __device__ __forceinline__ uint32_t share_of(float x, uint32_t none) {
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     return v;
 }
-template <typename T>
-__device__ __forceinline__ T peer(T *p, uint32_t rank) {
-    const uint32_t at = map_shared_rank(smem_u32(p), rank);
-    T v;
-    if constexpr (sizeof(T) == 8) {
-        u64 t;
-        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(t) : "r"(at) : "memory");
-        v = *reinterpret_cast<T *>(&t);
-    } else {
-        uint32_t t;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(t) : "r"(at) : "memory");
-        v = *reinterpret_cast<T *>(&t);
-    }
+__device__ __forceinline__ uint32_t peer(const uint32_t *p, uint32_t rank) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_shared_rank(smem_u32(p), rank)) : "memory");
     return v;
 }
 __device__ __forceinline__ void peer_store(u64 *p, uint32_t rank, u64 v) {
@@ -101,42 +120,65 @@ __device__ __forceinline__ uint32_t peer_add(uint32_t *p, uint32_t rank, uint32_
 }
 
 struct Shared {
-    uint32_t cnt[kBins], lo[kBins], hi[kBins];  // this CTA's bins: counts, and weights as two words carried by hand
+    uint32_t cnt[kBins], lo[kBins], hi[kBins];  // this CTA's bins: counts, and the halves of 24-bit weights
     uint32_t all_cnt[kBins];                    // the cluster's bins
     u64 all_sum[kBins];
     uint32_t list_key[kList], list_idx[kList];  // (CTA 0's are used)
     u64 list_w[kList];
-    uint32_t list_n;
-    uint32_t warp_u32[kWarps];
     u64 warp_u64[kWarps];
     u64 slot[2][kMaxCluster];  // exchanged values
     u64 found_sum, ranked_sum;
+    uint32_t warp_u32[kWarps];
+    uint32_t list_n[2];  // tokens that came for the list (CTA 0's are used): two counters in turn
     uint32_t found_bin, found_cnt, ranked_key, ranked_idx;
-    int has;
 };
 
-// A prefix in rank: the bins below `bin` whole, and of bin `bin` the keys above `key` and
-// those equal to it up to index `idx`.  bin = kBins + 1: no cut.
+// A prefix in rank: logits above z, and those equal to it up to index idx.
 struct Cut {
-    int bin;
-    uint32_t key, idx;
+    float z;
+    uint32_t idx;
     u64 sum;  // its weight
 };
 
 template <bool CACHED>
 struct Row {
     Shared &s;
-    const float *z;  // this CTA's share of the logits: in shared memory, or the row itself
-    uint32_t base;   // index of its first
-    int n;
+    const float *z;    // CACHED: this CTA's share in shared memory, negated, filled up with +inf to whole steps; else the row
+    uint32_t base;     // index of its first logit
+    int n, n4;         // its length; its groups of four logits
     uint32_t rank, ctas;
-    float top, c;    // largest logit; log2(e) / temperature
-    float span, scale;  // bins cover d < span
-    int turn;
+    float top, c;      // largest logit; log2(e) / temperature
+    bool odd;          // top or c is infinite: distances need care
+    int per_octave;    // log2 of the bins of an octave
+    float span;        // bins cover d < span
+    int turn, counter;
 
-    __device__ __forceinline__ float at(int i) const { return CACHED ? z[i] : clean(__ldg(z + i)); }
-    __device__ __forceinline__ float dist(float v) const { return v == top ? 0.f : __fmul_rn(__fsub_rn(top, v), c); }
-    __device__ __forceinline__ int bin_of(float d) const { return d < span ? min((int)(d * scale), kBins - 1) : kBins; }
+    // logits 4 i .. 4 i + 3, negated
+    __device__ __forceinline__ float4 four(int i) const {
+        if constexpr (CACHED) {
+            return reinterpret_cast<const float4 *>(z)[i];
+        } else {
+            float v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[x] = 4 * i + x < n ? stored(__ldg(z + 4 * i + x)) : INFINITY;
+            return make_float4(v[0], v[1], v[2], v[3]);
+        }
+    }
+    // distances of two negated logits; not < kAll (inf or NaN) for a weight of 0
+    __device__ __forceinline__ float2 dist2(float a, float b) const {
+        const float2 d = mul2(sum2(both(top), make_float2(a, b)), both(c));
+        return odd ? make_float2(-a == top ? 0.f : d.x, -b == top ? 0.f : d.y) : d;
+    }
+    __device__ __forceinline__ float dist(float a) const { return dist2(a, a).x; }
+    // floor(d 2^per_octave) for d < span (the sum has its last bit at 2^-per_octave)
+    __device__ __forceinline__ int bin_of(float d) const {
+        const float magic = __uint_as_float((uint32_t)(127 + 23 - per_octave) << 23);
+        return (int)(__float_as_uint(__fadd_rd(d, magic)) & 0x7FFFFF);
+    }
+    __device__ __forceinline__ void cover(int log_bins) {
+        per_octave = log_bins;
+        span = fminf(kAll, (float)(kBins >> log_bins));
+    }
 
     // Every CTA's value (its thread 0's) to all CTAs, by rank.  Two slots in turn, so one
     // barrier an exchange is enough.
@@ -152,7 +194,8 @@ struct Row {
         __syncthreads();
         if ((threadIdx.x & 31) == 0) s.warp_u64[threadIdx.x >> 5] = v;
         __syncthreads();
-        return warp_sum(s.warp_u64[threadIdx.x & 31]);
+        const int lane = threadIdx.x & 31;
+        return warp_sum(lane < kWarps ? s.warp_u64[lane] : 0);
     }
     __device__ __forceinline__ u64 cluster_sum(u64 v) {
         const u64 *all = exchange(block_sum(v));
@@ -161,43 +204,42 @@ struct Row {
         return t;
     }
     __device__ __forceinline__ uint32_t cluster_max(uint32_t v) {
-        v = __reduce_max_sync(0xFFFFFFFFu, v);
+        v = __reduce_max_sync(kFull, v);
         __syncthreads();
         if ((threadIdx.x & 31) == 0) s.warp_u32[threadIdx.x >> 5] = v;
         __syncthreads();
-        const u64 *all = exchange(__reduce_max_sync(0xFFFFFFFFu, s.warp_u32[threadIdx.x & 31]));
+        const int lane = threadIdx.x & 31;
+        const u64 *all = exchange(__reduce_max_sync(kFull, lane < kWarps ? s.warp_u32[lane] : 0));
         uint32_t t = 0;
         for (uint32_t r = 0; r < ctas; ++r) t = max(t, (uint32_t)all[r]);
         return t;
     }
 
-    // Counts and weights of the bins that pick(logit, bin, w) names (false: none), joined over
-    // the cluster into all_cnt and all_sum of every CTA.
-    template <typename Pick>
-    __device__ __forceinline__ void histogram(Pick &&pick) {
-        const int tid = threadIdx.x;
-        for (int i = tid; i < kBins; i += kThreads) s.cnt[i] = s.lo[i] = s.hi[i] = 0;
+    __device__ __forceinline__ void clear_bins() {
+        for (int i = threadIdx.x; i < kBins; i += kThreads) s.cnt[i] = s.lo[i] = s.hi[i] = 0;
         __syncthreads();
-        for (int i = tid; i < n; i += kThreads) {
-            int bin;
-            u64 w;
-            if (!pick(at(i), bin, w)) continue;
-            atomicAdd(&s.cnt[bin], 1u);
-            const uint32_t low = (uint32_t)w, old = atomicAdd(&s.lo[bin], low);
-            const uint32_t high = (uint32_t)(w >> 32) + (old + low < old ? 1u : 0u);
-            if (high) atomicAdd(&s.hi[bin], high);
-        }
+    }
+    template <bool COUNT>
+    __device__ __forceinline__ void into_bin(int bin, uint32_t w, uint32_t n) {
+        const uint32_t v = n <= 16 ? w : w >> (n - 16);
+        if (COUNT) atomicAdd(&s.cnt[bin], 1u);
+        atomicAdd(&s.lo[bin], v & 0xFFFu);
+        atomicAdd(&s.hi[bin], v >> 12);
+    }
+    // The CTAs' bins, joined, into all_cnt and all_sum of every CTA; octave(bin): n of its tokens.
+    template <typename Octave>
+    __device__ __forceinline__ void join_bins(Octave &&octave) {
         cluster_sync();
-        // CTA r joins bins [r, r + 1) * kBins / ctas and hands them to all
-        const int share = kBins / (int)ctas;
-        for (int i = tid; i < share; i += kThreads) {
+        const int share = kBins / (int)ctas;  // CTA r joins bins [r, r + 1) * share and hands them to all
+        for (int i = threadIdx.x; i < share; i += kThreads) {
             const int b = (int)rank * share + i;
             u64 w = 0;
             uint32_t k = 0;
             for (uint32_t r = 0; r < ctas; ++r) {
                 k += peer(&s.cnt[b], r);
-                w += ((u64)peer(&s.hi[b], r) << 32) + peer(&s.lo[b], r);
+                w += ((u64)peer(&s.hi[b], r) << 12) + peer(&s.lo[b], r);
             }
+            w <<= max(0, 16 - octave(b));
             for (uint32_t r = 0; r < ctas; ++r) {
                 peer_store(&s.all_cnt[b], r, k);
                 peer_store(&s.all_sum[b], r, w);
@@ -205,34 +247,64 @@ struct Row {
         }
         cluster_sync();
     }
+    // Bins of d < span over the row.  Returns this thread's part of the weight beyond (if TAIL).
+    template <bool COUNT, bool TAIL>
+    __device__ __forceinline__ u64 histogram() {
+        clear_bins();
+        u64 tail = 0;
+        for (int i = threadIdx.x; i < n4; i += kThreads) {
+            const float4 v = four(i);
+            const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int h = 0; h < 4; h += 2) {
+                const float2 d = dist2(x[h], x[h + 1]);
+                const float limit = TAIL ? kAll : span;
+                if (!(d.x < limit || d.y < limit)) continue;
+                uint32_t w[2], oct[2];
+                mantissa2(make_float2(d.x < kAll ? d.x : 0.f, d.y < kAll ? d.y : 0.f), w, oct);
+                const float dd[2] = {d.x, d.y};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (dd[e] < span) into_bin<COUNT>(bin_of(dd[e]), w[e], oct[e]);
+                    else if (TAIL && dd[e] < kAll) tail += scaled(w[e], oct[e]);
+                }
+            }
+        }
+        join_bins([&](int b) { return b >> per_octave; });
+        return tail;
+    }
 
     // The bin in which the running count (BY_SUM: weight), beginning with cnt (sum), reaches
     // `need`: its number, and the count and weight before it in cnt and sum.  -1: none does.
     template <bool BY_SUM>
     __device__ __forceinline__ int find_bin(u64 need, u64 &cnt, u64 &sum) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        static_assert(kBins == kThreads, "a bin per thread");
-        const uint32_t k = s.all_cnt[tid];
-        const u64 w = s.all_sum[tid];
-        uint32_t ki = k;
-        u64 wi = w;
+        static_assert(kBins == 2 * kThreads, "two bins a thread");
+        const uint32_t k[2] = {s.all_cnt[2 * tid], s.all_cnt[2 * tid + 1]};
+        const u64 w[2] = {s.all_sum[2 * tid], s.all_sum[2 * tid + 1]};
+        uint32_t ki = k[0] + k[1];
+        u64 wi = w[0] + w[1];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t kt = __shfl_up_sync(0xFFFFFFFFu, ki, o);
-            const u64 wt = __shfl_up_sync(0xFFFFFFFFu, wi, o);
+            const uint32_t kt = __shfl_up_sync(kFull, ki, o);
+            const u64 wt = __shfl_up_sync(kFull, wi, o);
             if (lane >= o) ki += kt, wi += wt;
         }
         __syncthreads();
         if (lane == 31) s.warp_u32[warp] = ki, s.warp_u64[warp] = wi;
         if (tid == 0) s.found_bin = kBins;
         __syncthreads();
-        const uint32_t kb = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s.warp_u32[lane] : 0u);
+        const uint32_t kb = __reduce_add_sync(kFull, lane < warp ? s.warp_u32[lane] : 0u);
         const u64 wb = warp_sum(lane < warp ? s.warp_u64[lane] : 0ull);
-        const u64 c1 = cnt + kb + ki, s1 = sum + wb + wi, c0 = c1 - k, s0 = s1 - w;
-        if (BY_SUM ? s0 < need && need <= s1 : c0 < need && need <= c1) {
-            s.found_bin = tid;
-            s.found_cnt = (uint32_t)c0;
-            s.found_sum = s0;
+        u64 c0 = cnt + kb + ki - k[0] - k[1], s0 = sum + wb + wi - w[0] - w[1];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (BY_SUM ? s0 < need && need <= s0 + w[x] : c0 < need && need <= c0 + k[x]) {
+                s.found_bin = 2 * tid + x;
+                s.found_cnt = (uint32_t)c0;
+                s.found_sum = s0;
+            }
+            c0 += k[x], s0 += w[x];
         }
         __syncthreads();
         const int bin = (int)s.found_bin;
@@ -242,15 +314,19 @@ struct Row {
         return bin;
     }
 
-    // Where, by index, the running sum of value(logit, index) over the whole row first exceeds
-    // target(total).  Returns true, in one warp of one CTA, with the index and its value.
+    // Where, by index, the running sum of value4(negated logits, index, values) over the whole row
+    // first exceeds target(total).  Returns true, in one warp of one CTA, with the index and its value.
     template <typename Value, typename Target>
-    __device__ __forceinline__ bool locate(Value &&value, Target &&target, uint32_t &idx, u64 &val, u64 &total) {
+    __device__ __forceinline__ bool locate(Value &&value4, Target &&target, uint32_t &idx, u64 &val, u64 &total) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const int per = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;  // a warp's run of indices
-        const int i0 = min(warp * per, n), i1 = min(i0 + per, n);
+        const int per = (n4 + kThreads - 1) / kThreads * 32;  // a warp's run of groups
+        const int i0 = min(warp * per, n4), i1 = min(i0 + per, n4);
         u64 sum = 0;
-        for (int i = i0 + lane; i < i1; i += 32) sum += value(at(i), base + i);
+        for (int i = i0 + lane; i < i1; i += 32) {
+            u64 v[4];
+            value4(four(i), base + 4 * i, v);
+            sum += v[0] + v[1] + v[2] + v[3];
+        }
         const u64 *all = exchange(block_sum(sum));
         u64 before = 0;
         total = 0;
@@ -264,21 +340,29 @@ struct Row {
         if (!(before <= goal && goal < before + mine)) return false;
         for (int j = i0; j < i1; j += 32) {
             const int i = j + lane;
-            const u64 v = i < i1 ? value(at(i), base + i) : 0;
-            u64 inc = v;
+            u64 v[4] = {0, 0, 0, 0};
+            if (i < i1) value4(four(i), base + 4 * i, v);
+            const u64 own = v[0] + v[1] + v[2] + v[3];
+            u64 inc = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const u64 t = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                const u64 t = __shfl_up_sync(kFull, inc, o);
                 if (lane >= o) inc += t;
             }
-            const uint32_t over = __ballot_sync(0xFFFFFFFFu, before + inc > goal);
+            const uint32_t over = __ballot_sync(kFull, before + inc > goal);
             if (over) {
+                u64 run = before + inc - own;
+                int x = 0;
+#pragma unroll
+                for (int y = 0; y < 3; ++y)
+                    if (x == y && run + v[y] <= goal) run += v[y], ++x;
+                const u64 mine_v = x == 0 ? v[0] : x == 1 ? v[1] : x == 2 ? v[2] : v[3];
                 const int l = __ffs(over) - 1;
-                idx = base + j + l;
-                val = __shfl_sync(0xFFFFFFFFu, v, l);
+                idx = __shfl_sync(kFull, base + 4 * i + x, l);
+                val = __shfl_sync(kFull, mine_v, l);
                 return true;
             }
-            before += __shfl_sync(0xFFFFFFFFu, inc, 31);
+            before += __shfl_sync(kFull, inc, 31);
         }
         return false;
     }
@@ -288,127 +372,138 @@ struct Row {
     template <bool BY_SUM>
     __device__ __forceinline__ Cut refine(int bin, u64 need, u64 cnt, u64 sum) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        uint32_t in = s.all_cnt[bin], lo = 0, hi = 0xFFFFFFFFu;
-        auto inside = [&](float v, uint32_t &key) {
-            const float d = dist(v);
-            key = key_of(v);
-            return d < kAll && bin_of(d) == bin && key >= lo && key <= hi;
+        const int octave = bin >> per_octave;
+        uint32_t lo = 0, hi = 0xFFFFFFFFu;  // keys of the bin that are left
+        // visit(negated logit, index, key, d) for these tokens
+        auto each = [&](auto &&visit) {
+            for (int i = tid; i < n4; i += kThreads) {
+                const float4 v = four(i);
+                const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int h = 0; h < 4; h += 2) {
+                    const float2 d = dist2(x[h], x[h + 1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float de = e ? d.y : d.x;
+                        if (!(de < span) || bin_of(de) != bin) continue;
+                        const uint32_t key = key_of(-x[h + e]);
+                        if (key >= lo && key <= hi) visit(x[h + e], base + 4 * i + h + e, key, de);
+                    }
+                }
+            }
         };
-        while (in > kList) {
-            // too many to be ranked: a histogram over their keys, from the largest down
-            uint32_t a = 0, b = 0, key;
-            for (int i = tid; i < n; i += kThreads)
-                if (inside(at(i), key)) a = max(a, key), b = max(b, ~key);
-            hi = cluster_max(a);
+        for (;;) {
+            // CTA 0 gathers the tokens if they are few
+            each([&](float, uint32_t idx, uint32_t key, float d) {
+                const uint32_t to = peer_add(&s.list_n[counter], 0, 1);
+                if (to < kList) {
+                    peer_store(&s.list_key[to], 0, key);
+                    peer_store(&s.list_idx[to], 0, idx);
+                    peer_store(&s.list_w[to], 0, weight_of(d));
+                }
+            });
+            cluster_sync();
+            const int m = (int)peer(&s.list_n[counter], 0);
+            counter ^= 1;  // the other one's readers are past the barrier, and its next users behind another
+            if (rank == 0 && tid == 0) s.list_n[counter] = 0;
+            if (m <= kList) {
+                // each warp ranks some of them against all
+                if (rank == 0)
+                    for (int i = warp; i < m; i += kWarps) {
+                        const uint32_t key = s.list_key[i], idx = s.list_idx[i];
+                        uint32_t k = 0;
+                        u64 w = 0;
+                        for (int j = lane; j < m; j += 32) {
+                            const uint32_t kj = s.list_key[j];
+                            if (kj > key || (kj == key && s.list_idx[j] < idx)) ++k, w += s.list_w[j];
+                        }
+                        k = __reduce_add_sync(kFull, k);
+                        w = warp_sum(w);
+                        const u64 w1 = sum + w + s.list_w[i];
+                        const bool is = BY_SUM ? sum + w < need && need <= w1 : cnt + k + 1 == need;
+                        if (is && (uint32_t)lane < ctas) {
+                            peer_store(&s.ranked_key, lane, key);
+                            peer_store(&s.ranked_idx, lane, idx);
+                            peer_store(&s.ranked_sum, lane, w1);
+                        }
+                    }
+                cluster_sync();
+                return {of_key(s.ranked_key), s.ranked_idx, s.ranked_sum};
+            }
+            // many: a histogram over their keys, from the largest down
+            uint32_t a = 0, b = 0;
+            each([&](float, uint32_t, uint32_t key, float) { a = max(a, key), b = max(b, ~key); });
+            a = cluster_max(a);
             lo = ~cluster_max(b);
+            hi = a;
             if (lo == hi) break;
             const int shift = max(0, 32 - __clz(hi - lo) - 10);
-            histogram([&](float v, int &to, u64 &w) {
-                uint32_t k;
-                if (!inside(v, k)) return false;
-                to = (int)((hi - k) >> shift);
-                w = weight_of(dist(v));
-                return true;
+            clear_bins();
+            each([&](float, uint32_t, uint32_t key, float d) {
+                uint32_t w[2], oct[2];
+                mantissa2(both(d), w, oct);
+                into_bin<true>((int)((hi - key) >> shift), w[0], oct[0]);
             });
+            join_bins([&](int) { return octave; });
             const uint32_t sub = (uint32_t)max(find_bin<BY_SUM>(need, cnt, sum), 0);
-            in = s.all_cnt[sub];
             hi -= sub << shift;
             lo = hi - min(hi - lo, (1u << shift) - 1);
         }
-        if (in > kList) {
-            // equal logits: the q-th by index
-            const float v0 = __uint_as_float(hi >> 31 ? hi ^ 0x80000000u : ~hi);
-            const u64 w = weight_of(dist(v0));
-            const u64 q = BY_SUM ? (need - sum + w - 1) / w : need - cnt;
-            uint32_t idx;
-            u64 val, total;
-            const bool here = locate([&](float v, uint32_t) { return (u64)(v == v0); }, [&](u64) { return q - 1; }, idx, val, total);
-            if (here && (uint32_t)lane < ctas) peer_store(&s.ranked_idx, lane, idx);
-            cluster_sync();
-            return {bin, hi, s.ranked_idx, sum + q * w};
-        }
-        // few: CTA 0 gathers them, and each warp ranks some of them against all
-        for (int i = tid; i < n; i += kThreads) {
-            uint32_t key;
-            const float v = at(i);
-            if (!inside(v, key)) continue;
-            const uint32_t to = peer_add(&s.list_n, 0, 1);
-            if (to < kList) {
-                peer_store(&s.list_key[to], 0, key);
-                peer_store(&s.list_idx[to], 0, base + i);
-                peer_store(&s.list_w[to], 0, weight_of(dist(v)));
-            }
-        }
+        // equal logits: the q-th by index
+        const float z0 = of_key(hi);
+        const u64 w = weight_of(dist(-z0));
+        const u64 q = BY_SUM ? (need - sum + w - 1) / w : need - cnt;
+        uint32_t idx;
+        u64 val, total;
+        const bool here = locate(
+            [&](float4 v, uint32_t, u64 (&is)[4]) { is[0] = -v.x == z0, is[1] = -v.y == z0, is[2] = -v.z == z0, is[3] = -v.w == z0; },
+            [&](u64) { return q - 1; }, idx, val, total);
+        if (here && (uint32_t)lane < ctas) peer_store(&s.ranked_idx, lane, idx);
         cluster_sync();
-        if (rank == 0) {
-            const int m = min((int)s.list_n, kList);
-            for (int i = warp; i < m; i += kWarps) {
-                const uint32_t key = s.list_key[i], idx = s.list_idx[i];
-                uint32_t k = 0;
-                u64 w = 0;
-                for (int j = lane; j < m; j += 32) {
-                    const uint32_t kj = s.list_key[j];
-                    if (kj > key || (kj == key && s.list_idx[j] < idx)) ++k, w += s.list_w[j];
-                }
-                k = __reduce_add_sync(0xFFFFFFFFu, k);
-                w = warp_sum(w);
-                const u64 w1 = sum + w + s.list_w[i];
-                const bool is = BY_SUM ? sum + w < need && need <= w1 : cnt + k + 1 == need;
-                if (is && (uint32_t)lane < ctas) {
-                    peer_store(&s.ranked_key, lane, key);
-                    peer_store(&s.ranked_idx, lane, idx);
-                    peer_store(&s.ranked_sum, lane, w1);
-                }
-            }
-            __syncthreads();
-            if (tid == 0) s.list_n = 0;
-        }
-        cluster_sync();
-        return {bin, s.ranked_key, s.ranked_idx, s.ranked_sum};
+        return {z0, s.ranked_idx, sum + q * w};
     }
 };
 
 template <bool CACHED>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, int per) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int per) {
     extern __shared__ __align__(16) uint8_t dyn[];
     Shared &s = *reinterpret_cast<Shared *>(dyn);
     float *own = reinterpret_cast<float *>(dyn + (sizeof(Shared) + 15) / 16 * 16);
-    pdl_wait();
-    pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31;
     const uint32_t rank = cluster_ctarank(), ctas = a.ctas;
+    if (tid == 0) s.list_n[0] = s.list_n[1] = 0;
+    cluster_arrive();  // (waited for before the first access to another CTA's memory)
+    pdl_wait();
+    pdl_trigger();
     const int64_t m = blockIdx.x / ctas;
     const int64_t i0 = min((int64_t)rank * per, (int64_t)a.V), i1 = min(i0 + per, (int64_t)a.V);
     const float *row = a.logits + m * a.ldl + i0;
-    Row<CACHED> r = {s, CACHED ? own : row, (uint32_t)i0, (int)(i1 - i0), rank, ctas, 0.f, 0.f, kHead, kBins / kHead, 0};
-    if (tid == 0) s.list_n = 0;
-    cluster_arrive();  // (waited for before the first access to another CTA's memory)
+    Row<CACHED> r = {s, CACHED ? own : row, (uint32_t)i0, (int)(i1 - i0), ((int)(i1 - i0) + 3) / 4, rank, ctas, 0.f, 0.f, false, 0, 0.f, 0, 0};
     // ---- load; the largest logit
-    uint32_t best = 0;
+    float best = INFINITY;  // (of the negated ones, the smallest)
     if (CACHED && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
         const float4 *row4 = reinterpret_cast<const float4 *>(row);
 #pragma unroll 4
         for (int i = tid; i < r.n / 4; i += kThreads) {
             float4 v = __ldg(row4 + i);
-            v.x = clean(v.x), v.y = clean(v.y), v.z = clean(v.z), v.w = clean(v.w);
+            v = make_float4(stored(v.x), stored(v.y), stored(v.z), stored(v.w));
             reinterpret_cast<float4 *>(own)[i] = v;
-            best = max(max(best, max(key_of(v.x), key_of(v.y))), max(key_of(v.z), key_of(v.w)));
+            best = fminf(fminf(best, fminf(v.x, v.y)), fminf(v.z, v.w));
         }
-        for (int i = r.n / 4 * 4 + tid; i < r.n; i += kThreads) {
-            own[i] = clean(__ldg(row + i));
-            best = max(best, key_of(own[i]));
+        for (int i = r.n / 4 * 4 + tid; i < r.n4 * 4; i += kThreads) {
+            own[i] = i < r.n ? stored(__ldg(row + i)) : INFINITY;
+            best = fminf(best, own[i]);
         }
     } else {
 #pragma unroll 8
-        for (int i = tid; i < r.n; i += kThreads) {
-            const float v = clean(__ldg(row + i));
+        for (int i = tid; i < (CACHED ? r.n4 * 4 : r.n); i += kThreads) {
+            const float v = i < r.n ? stored(__ldg(row + i)) : INFINITY;
             if (CACHED) own[i] = v;
-            best = max(best, key_of(v));
+            best = fminf(best, v);
         }
     }
     cluster_wait();
-    best = r.cluster_max(best);
-    r.top = __uint_as_float(best >> 31 ? best ^ 0x80000000u : ~best);
+    r.top = of_key(r.cluster_max(key_of(-best)));
     if (r.top == -INFINITY) {
         if (rank == 0 && tid == 0) {
             a.token[m] = -1;
@@ -421,91 +516,86 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, in
     const bool greedy = !(t > 0.f);
     if (greedy) t = 1.f;
     r.c = __fmul_rn(__fdiv_rn(1.f, t), 1.4426950408889634f);
+    r.odd = isinf(r.top) || isinf(r.c);
     const int64_t k = greedy ? 1 : a.top_k ? __ldg(a.top_k + m) : 0;
     const uint32_t p_share = greedy || !a.top_p ? kOne : share_of(__ldg(a.top_p + m), kOne);
     const uint32_t m_share = greedy || !a.min_p ? 0 : share_of(__ldg(a.min_p + m), 0);
     const uint32_t u = min(share_of(__ldg(a.u + m), 0), kOne - 1);
     const bool by_k = k > 0 && k < a.V, by_p = p_share < kOne;
     // ---- the cut
-    Cut cut = {kBins + 1, 0, 0xFFFFFFFFu, 0};
-    if (by_k || by_p) {
-        for (;;) {
-            u64 tail = 0;
-            r.histogram([&](float v, int &bin, u64 &w) {
-                const float d = r.dist(v);
-                if (!(d < kAll)) return false;
-                bin = r.bin_of(d);
-                if (bin < kBins) {
-                    w = weight_of(d);
-                    return true;
-                }
-                if (by_p && !by_k) tail += weight_of(d);
-                return false;
-            });
-            const bool all = r.span == kAll;
-            u64 sum = 0, cnt = 0;
-            cut.bin = kBins + 1;
-            if (by_k) {
-                const int bin = r.template find_bin<false>((u64)k, cnt, sum);
-                const bool many = bin >= 0 && s.all_cnt[bin] > kList;
-                if (bin >= 0) cut = r.template refine<false>(bin, (u64)k, cnt, sum);
-                else if (!all) {
-                    r.span = kAll, r.scale = kBins / kAll;
-                    continue;
-                }
-                if (by_p && many) {
-                    // the bins over keys have taken the place of those over d
-                    r.histogram([&](float v, int &to, u64 &w) {
-                        const float d = r.dist(v);
-                        to = r.bin_of(d);
-                        if (!(d < kAll) || to >= kBins) return false;
-                        w = weight_of(d);
-                        return true;
-                    });
-                }
-            }
-            if (by_p) {
-                u64 whole = cut.sum;
-                if (cut.bin > kBins) {
-                    u64 in_bins = 0;
-                    for (int i = tid; i < kBins; i += kThreads) in_bins += s.all_sum[i];
-                    // (the bins are the cluster's already: one CTA's sum of them is enough)
-                    whole = r.cluster_sum(tail + (rank == 0 ? in_bins : 0));
-                }
-                const u64 need = max(part_of(whole, p_share), (u64)1);
-                cnt = sum = 0;
-                const int bin = r.template find_bin<true>(need, cnt, sum);
-                if (bin < 0) {
-                    // beyond the bins (never once they cover every weight)
-                    if (all) break;
-                    r.span = kAll, r.scale = kBins / kAll;
-                    continue;
-                }
-                cut = r.template refine<true>(bin, need, cnt, sum);
-            }
-            break;
+    Cut cut = {-INFINITY, 0xFFFFFFFFu, 0};
+    if (by_k) {
+        bool cut_off = true;
+        u64 cnt = 0, sum = 0;
+        r.cover(6);
+        r.template histogram<true, false>();
+        int bin = r.template find_bin<false>((u64)k, cnt, sum);
+        if (bin < 0) {
+            r.cover(4);
+            r.template histogram<true, false>();
+            bin = r.template find_bin<false>((u64)k, cnt, sum);
+            cut_off = bin >= 0;  // fewer than k tokens have any weight
         }
+        bool kept_bins = true;
+        if (cut_off) {
+            kept_bins = s.all_cnt[bin] <= kList;  // otherwise bins over keys take their place
+            cut = r.template refine<false>(bin, (u64)k, cnt, sum);
+        }
+        if (by_p) {
+            if (!kept_bins) r.template histogram<true, false>();
+            u64 whole = cut.sum;
+            if (!cut_off) {
+                u64 part = 0;
+                if (rank == 0)
+                    for (int i = tid; i < kBins; i += kThreads) part += s.all_sum[i];
+                whole = r.cluster_sum(part);
+            }
+            cnt = sum = 0;
+            const u64 need = max(part_of(whole, p_share), (u64)1);
+            bin = r.template find_bin<true>(need, cnt, sum);
+            if (bin >= 0) cut = r.template refine<true>(bin, need, cnt, sum);
+        }
+    } else if (by_p) {
+        u64 need = 0, cnt = 0, sum = 0;
+        r.cover(5);
+        u64 part = r.template histogram<false, true>();
+        if (rank == 0)  // (the bins are the cluster's)
+            for (int i = tid; i < kBins; i += kThreads) part += s.all_sum[i];
+        need = max(part_of(r.cluster_sum(part), p_share), (u64)1);
+        int bin = r.template find_bin<true>(need, cnt, sum);
+        if (bin < 0) {
+            r.cover(4);
+            r.template histogram<false, true>();
+            bin = r.template find_bin<true>(need, cnt, sum);
+        }
+        if (bin >= 0) cut = r.template refine<true>(bin, need, cnt, sum);
     }
     // ---- the token
     const u64 least = part_of(weight_of(0.f), m_share);
     uint32_t idx;
     u64 w, total;
     const bool here = r.locate(
-        [&](float v, uint32_t i) -> u64 {
-            const float d = r.dist(v);
-            if (!(d < kAll)) return 0;
-            if (cut.bin <= kBins) {
-                const int bin = r.bin_of(d);
-                if (bin > cut.bin) return 0;
-                if (bin == cut.bin) {
-                    const uint32_t key = key_of(v);
-                    if (key < cut.key || (key == cut.key && i > cut.idx)) return 0;
+        [&](float4 v, uint32_t i, u64 (&x)[4]) {
+            const float z[4] = {v.x, v.y, v.z, v.w};
+            const float zc = -cut.z;
+#pragma unroll
+            for (int h = 0; h < 4; h += 2) {
+                x[h] = x[h + 1] = 0;
+                bool in[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) in[e] = z[h + e] < zc || (z[h + e] == zc && i + h + e <= cut.idx);
+                if (!(in[0] || in[1])) continue;
+                const float2 d = r.dist2(z[h], z[h + 1]);
+                uint32_t wm[2], n[2];
+                mantissa2(make_float2(d.x < kAll ? d.x : 0.f, d.y < kAll ? d.y : 0.f), wm, n);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const u64 we = scaled(wm[e], n[e]);
+                    if (in[e] && (e ? d.y : d.x) < kAll && we >= least) x[h + e] = we;
                 }
             }
-            const u64 x = weight_of(d);
-            return x >= least ? x : 0;
         },
-        [&](u64 sum) { return part_of(sum, u); }, idx, w, total);
+        [&](u64 all) { return part_of(all, u); }, idx, w, total);
     if (here && lane == 0) {
         a.token[m] = (int32_t)idx;
         if (a.prob) a.prob[m] = __fdiv_rn((float)w, (float)total);
