@@ -14,9 +14,10 @@
 //      octave.  With top-k the cut is near the top: 64 bins to an octave of 16, and what
 //      lies below is not even weighed.  Otherwise 32 to an octave of 32; the rest is added
 //      up without bins.  If the cut turns out to lie below, again with all 41;
-//   3. the tokens of the bin in which top-k (then top-p) ends are ranked against each
-//      other if they are few; if many, the bin is first narrowed by histograms over their
-//      keys; equal logits are counted off by index;
+//   3. the tokens of the bin in which top-k (then top-p) ends are gathered in one CTA, narrowed
+//      there by histograms over their keys, and the last few ranked against each other;
+//      if they are too many to be gathered, the whole cluster narrows them the same way
+//      first; equal logits are counted off by index;
 //   4. the sum of what is kept, the target, and the token by a scan in index order.
 // A bin never crosses an octave, so its tokens' weights have one scale: they are summed as
 // two 12-bit halves of a 24-bit number by 32-bit atomics without a result.
@@ -33,7 +34,8 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
-constexpr int kList = 768;           // tokens of a bin that are ranked against each other
+constexpr int kList = 768;           // tokens of a bin that one CTA gathers
+constexpr int kFew = 48;             // tokens that are ranked against each other
 constexpr int kMaxCluster = 8;
 constexpr int kCached = 19456;       // logits of a CTA that stay in shared memory with two CTAs on an SM
 constexpr float kAll = 41.f;         // from this d on the weight is 0
@@ -130,8 +132,10 @@ struct Shared {
     u64 found_sum, ranked_sum;
     uint32_t warp_u32[kWarps];
     uint32_t list_n[2];  // tokens that came for the list (CTA 0's are used): two counters in turn
-    uint32_t found_bin, found_cnt, ranked_key, ranked_idx;
+    uint32_t found_bin, found_cnt, found_in, ranked_key, ranked_idx;
 };
+
+static_assert(2 * (sizeof(Shared) + 4 * kCached + 1024) <= 233472, "two CTAs on an SM");
 
 // A prefix in rank: logits above z, and those equal to it up to index idx.
 struct Cut {
@@ -230,17 +234,25 @@ struct Row {
     template <typename Octave>
     __device__ __forceinline__ void join_bins(Octave &&octave) {
         cluster_sync();
-        const int share = kBins / (int)ctas;  // CTA r joins bins [r, r + 1) * share and hands them to all
-        for (int i = threadIdx.x; i < share; i += kThreads) {
+        // CTA r joins bins [r, r + 1) * share and hands them to all, some threads to a bin, each for
+        // some of the CTAs
+        const int share = kBins / (int)ctas, team = max(1, kThreads / share), mate = threadIdx.x % team;
+        for (int i = threadIdx.x / team; i < share; i += kThreads / team) {
             const int b = (int)rank * share + i;
             u64 w = 0;
             uint32_t k = 0;
-            for (uint32_t r = 0; r < ctas; ++r) {
-                k += peer(&s.cnt[b], r);
-                w += ((u64)peer(&s.hi[b], r) << 12) + peer(&s.lo[b], r);
+#pragma unroll 2
+            for (uint32_t r = mate; r < ctas; r += team) {
+                const uint32_t kr = peer(&s.cnt[b], r), hr = peer(&s.hi[b], r), lr = peer(&s.lo[b], r);
+                k += kr;
+                w += ((u64)hr << 12) + lr;
+            }
+            for (int o = 1; o < team; o <<= 1) {  // (teams lie within a warp, and all of them are here)
+                k += __shfl_xor_sync(kFull, k, o);
+                w += __shfl_xor_sync(kFull, w, o);
             }
             w <<= max(0, 16 - octave(b));
-            for (uint32_t r = 0; r < ctas; ++r) {
+            for (uint32_t r = mate; r < ctas; r += team) {
                 peer_store(&s.all_cnt[b], r, k);
                 peer_store(&s.all_sum[b], r, w);
             }
@@ -276,12 +288,18 @@ struct Row {
 
     // The bin in which the running count (BY_SUM: weight), beginning with cnt (sum), reaches
     // `need`: its number, and the count and weight before it in cnt and sum.  -1: none does.
-    template <bool BY_SUM>
-    __device__ __forceinline__ int find_bin(u64 need, u64 &cnt, u64 &sum) {
+    // OWN: of this CTA's bins (weights scaled by 2^up), otherwise of the cluster's.
+    template <bool BY_SUM, bool OWN = false>
+    __device__ __forceinline__ int find_bin(u64 need, u64 &cnt, u64 &sum, int up = 0) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         static_assert(kBins == 2 * kThreads, "two bins a thread");
-        const uint32_t k[2] = {s.all_cnt[2 * tid], s.all_cnt[2 * tid + 1]};
-        const u64 w[2] = {s.all_sum[2 * tid], s.all_sum[2 * tid + 1]};
+        uint32_t k[2];
+        u64 w[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            k[x] = OWN ? s.cnt[2 * tid + x] : s.all_cnt[2 * tid + x];
+            w[x] = OWN ? (((u64)s.hi[2 * tid + x] << 12) + s.lo[2 * tid + x]) << up : s.all_sum[2 * tid + x];
+        }
         uint32_t ki = k[0] + k[1];
         u64 wi = w[0] + w[1];
 #pragma unroll
@@ -302,6 +320,7 @@ struct Row {
             if (BY_SUM ? s0 < need && need <= s0 + w[x] : c0 < need && need <= c0 + k[x]) {
                 s.found_bin = 2 * tid + x;
                 s.found_cnt = (uint32_t)c0;
+                s.found_in = k[x];
                 s.found_sum = s0;
             }
             c0 += k[x], s0 += w[x];
@@ -407,15 +426,48 @@ struct Row {
             counter ^= 1;  // the other one's readers are past the barrier, and its next users behind another
             if (rank == 0 && tid == 0) s.list_n[counter] = 0;
             if (m <= kList) {
-                // each warp ranks some of them against all
-                if (rank == 0)
+                if (rank == 0) {
+                    const int up = max(0, 16 - octave);
+                    for (int left = m; left > kFew;) {
+                        // narrow by a histogram over the keys, from the largest down
+                        uint32_t a = 0, b = 0;
+                        for (int i = tid; i < m; i += kThreads) {
+                            const uint32_t key = s.list_key[i];
+                            if (key >= lo && key <= hi) a = max(a, key), b = max(b, ~key);
+                        }
+                        a = __reduce_max_sync(kFull, a), b = __reduce_max_sync(kFull, b);
+                        if (lane == 0) s.warp_u64[warp] = (u64)a << 32 | b;
+                        clear_bins();
+                        a = __reduce_max_sync(kFull, (uint32_t)(s.warp_u64[lane & (kWarps - 1)] >> 32));
+                        b = __reduce_max_sync(kFull, (uint32_t)s.warp_u64[lane & (kWarps - 1)]);
+                        hi = a, lo = ~b;
+                        if (lo == hi) break;  // equal logits: ranked by index below
+                        const int shift = max(0, 32 - __clz(hi - lo) - 10);
+                        for (int i = tid; i < m; i += kThreads) {
+                            const uint32_t key = s.list_key[i];
+                            if (key < lo || key > hi) continue;
+                            const int bin = (int)((hi - key) >> shift);
+                            const uint32_t v = (uint32_t)(s.list_w[i] >> up);
+                            atomicAdd(&s.cnt[bin], 1u);
+                            atomicAdd(&s.lo[bin], v & 0xFFFu);
+                            atomicAdd(&s.hi[bin], v >> 12);
+                        }
+                        __syncthreads();
+                        const uint32_t sub = (uint32_t)max((find_bin<BY_SUM, true>(need, cnt, sum, up)), 0);
+                        left = (int)s.found_in;
+                        hi -= sub << shift;
+                        lo = hi - min(hi - lo, (1u << shift) - 1);
+                        __syncthreads();  // (warp_u64 and found_in are written again)
+                    }
+                    // each warp ranks some of what is left against all of it
                     for (int i = warp; i < m; i += kWarps) {
                         const uint32_t key = s.list_key[i], idx = s.list_idx[i];
+                        if (key < lo || key > hi) continue;
                         uint32_t k = 0;
                         u64 w = 0;
                         for (int j = lane; j < m; j += 32) {
                             const uint32_t kj = s.list_key[j];
-                            if (kj > key || (kj == key && s.list_idx[j] < idx)) ++k, w += s.list_w[j];
+                            if (kj <= hi && (kj > key || (kj == key && s.list_idx[j] < idx))) ++k, w += s.list_w[j];
                         }
                         k = __reduce_add_sync(kFull, k);
                         w = warp_sum(w);
@@ -427,6 +479,7 @@ struct Row {
                             peer_store(&s.ranked_sum, lane, w1);
                         }
                     }
+                }
                 cluster_sync();
                 return {of_key(s.ranked_key), s.ranked_idx, s.ranked_sum};
             }
