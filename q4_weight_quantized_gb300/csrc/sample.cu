@@ -49,8 +49,12 @@ __device__ __forceinline__ uint32_t key_of(float z) {
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k); }
-// The negative of a logit, as the row is kept: NaN counts as -inf, -0 as +0.
-__device__ __forceinline__ float stored(float z) { return z != z ? INFINITY : -(z + 0.f); }
+// The negative of a logit, as the row is kept: that of NaN is +inf, that of either zero +0.
+__device__ __forceinline__ float stored(float z) { return fminf(0.f - z, INFINITY); }
+
+// Where the largest logit or 1 / temperature is infinite, every distance is 0 or infinite: the
+// row then counts as one of zeros and -inf.  least: the largest logit, negated.
+__device__ __forceinline__ float flat(float v, float least) { return v == least ? 0.f : INFINITY; }
 
 // Two fp32 operations at once, each rounded on its own.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -63,16 +67,20 @@ __device__ __forceinline__ float2 sum2(float2 a, float2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<u64 *>(&a)), "l"(*reinterpret_cast<u64 *>(&b)));
     return *reinterpret_cast<float2 *>(&r);
 }
+__device__ __forceinline__ float2 sum2_down(float2 a, float2 b) {
+    u64 r;
+    asm("add.rm.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<u64 *>(&a)), "l"(*reinterpret_cast<u64 *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // floor(2^24 2^-f) and n of two distances 0 <= d < 2^22, n = floor(d), f = d - n: the series
 // of 2^-f about f = 1/2, coefficients 2^-1/2 (-ln 2)^i / i!.
 __device__ __forceinline__ void mantissa2(float2 d, uint32_t (&w)[2], uint32_t (&n)[2]) {
     // 2^23 + d, rounded down, is 2^23 + n
-    const float2 t = make_float2(__fadd_rd(d.x, 8388608.f), __fadd_rd(d.y, 8388608.f));
+    const float2 t = sum2_down(d, both(8388608.f));
     n[0] = __float_as_uint(t.x) & 0x7FFFFF, n[1] = __float_as_uint(t.y) & 0x7FFFFF;
-    const float2 whole = sum2(t, both(-8388608.f));
-    const float2 f = sum2(sum2(d, make_float2(-whole.x, -whole.y)), both(-0.5f));
+    const float2 f = sum2(fma2(sum2(t, both(-8388608.f)), both(-1.f), d), both(-0.5f));  // (d - n is exact)
     float2 p = both(-1.0785311133076902e-05f);
     p = sum2(mul2(p, f), both(0.00010891940473811701f));
     p = sum2(mul2(p, f), both(-0.0009428249322809279f));
@@ -152,7 +160,7 @@ struct Row {
     int n, n4;         // its length; its groups of four logits
     uint32_t rank, ctas;
     float top, c;      // largest logit; log2(e) / temperature
-    bool odd;          // top or c is infinite: distances need care
+    float infinite;    // not CACHED: the row is to be flattened (see there) about this, unless NaN
     int per_octave;    // log2 of the bins of an octave
     float span;        // bins cover d < span
     int turn, counter;
@@ -164,14 +172,16 @@ struct Row {
         } else {
             float v[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) v[x] = 4 * i + x < n ? stored(__ldg(z + 4 * i + x)) : INFINITY;
+            for (int x = 0; x < 4; ++x) {
+                v[x] = 4 * i + x < n ? stored(__ldg(z + 4 * i + x)) : INFINITY;
+                if (infinite == infinite) v[x] = flat(v[x], infinite);
+            }
             return make_float4(v[0], v[1], v[2], v[3]);
         }
     }
     // distances of two negated logits; not < kAll (inf or NaN) for a weight of 0
     __device__ __forceinline__ float2 dist2(float a, float b) const {
-        const float2 d = mul2(sum2(both(top), make_float2(a, b)), both(c));
-        return odd ? make_float2(-a == top ? 0.f : d.x, -b == top ? 0.f : d.y) : d;
+        return mul2(sum2(both(top), make_float2(a, b)), both(c));
     }
     __device__ __forceinline__ float dist(float a) const { return dist2(a, a).x; }
     // floor(d 2^per_octave) for d < span (the sum has its last bit at 2^-per_octave)
@@ -223,10 +233,9 @@ struct Row {
         for (int i = threadIdx.x; i < kBins; i += kThreads) s.cnt[i] = s.lo[i] = s.hi[i] = 0;
         __syncthreads();
     }
-    template <bool COUNT>
-    __device__ __forceinline__ void into_bin(int bin, uint32_t w, uint32_t n) {
+    __device__ __forceinline__ void into_bin(bool count, int bin, uint32_t w, uint32_t n) {
         const uint32_t v = n <= 16 ? w : w >> (n - 16);
-        if (COUNT) atomicAdd(&s.cnt[bin], 1u);
+        if (count) atomicAdd(&s.cnt[bin], 1u);
         atomicAdd(&s.lo[bin], v & 0xFFFu);
         atomicAdd(&s.hi[bin], v >> 12);
     }
@@ -259,26 +268,25 @@ struct Row {
         }
         cluster_sync();
     }
-    // Bins of d < span over the row.  Returns this thread's part of the weight beyond (if TAIL).
-    template <bool COUNT, bool TAIL>
-    __device__ __forceinline__ u64 histogram() {
-        clear_bins();
+    // Bins of d < span over the row, from cleared ones.  Returns this thread's part of the weight beyond
+    // (if beyond).
+    __device__ __forceinline__ u64 histogram(bool count, bool beyond) {
         u64 tail = 0;
+        const float limit = beyond ? kAll : span;
         for (int i = threadIdx.x; i < n4; i += kThreads) {
             const float4 v = four(i);
             const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int h = 0; h < 4; h += 2) {
                 const float2 d = dist2(x[h], x[h + 1]);
-                const float limit = TAIL ? kAll : span;
                 if (!(d.x < limit || d.y < limit)) continue;
                 uint32_t w[2], oct[2];
                 mantissa2(make_float2(d.x < kAll ? d.x : 0.f, d.y < kAll ? d.y : 0.f), w, oct);
                 const float dd[2] = {d.x, d.y};
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    if (dd[e] < span) into_bin<COUNT>(bin_of(dd[e]), w[e], oct[e]);
-                    else if (TAIL && dd[e] < kAll) tail += scaled(w[e], oct[e]);
+                    if (dd[e] < span) into_bin(count, bin_of(dd[e]), w[e], oct[e]);
+                    else if (dd[e] < limit) tail += scaled(w[e], oct[e]);
                 }
             }
         }
@@ -286,19 +294,18 @@ struct Row {
         return tail;
     }
 
-    // The bin in which the running count (BY_SUM: weight), beginning with cnt (sum), reaches
+    // The bin in which the running count (by_sum: weight), beginning with cnt (sum), reaches
     // `need`: its number, and the count and weight before it in cnt and sum.  -1: none does.
-    // OWN: of this CTA's bins (weights scaled by 2^up), otherwise of the cluster's.
-    template <bool BY_SUM, bool OWN = false>
-    __device__ __forceinline__ int find_bin(u64 need, u64 &cnt, u64 &sum, int up = 0) {
+    // own: of this CTA's bins (weights scaled by 2^up), otherwise of the cluster's.
+    __device__ __forceinline__ int find_bin(bool by_sum, u64 need, u64 &cnt, u64 &sum, bool own = false, int up = 0) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         static_assert(kBins == 2 * kThreads, "two bins a thread");
         uint32_t k[2];
         u64 w[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            k[x] = OWN ? s.cnt[2 * tid + x] : s.all_cnt[2 * tid + x];
-            w[x] = OWN ? (((u64)s.hi[2 * tid + x] << 12) + s.lo[2 * tid + x]) << up : s.all_sum[2 * tid + x];
+            k[x] = own ? s.cnt[2 * tid + x] : s.all_cnt[2 * tid + x];
+            w[x] = own ? (((u64)s.hi[2 * tid + x] << 12) + s.lo[2 * tid + x]) << up : s.all_sum[2 * tid + x];
         }
         uint32_t ki = k[0] + k[1];
         u64 wi = w[0] + w[1];
@@ -317,7 +324,7 @@ struct Row {
         u64 c0 = cnt + kb + ki - k[0] - k[1], s0 = sum + wb + wi - w[0] - w[1];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            if (BY_SUM ? s0 < need && need <= s0 + w[x] : c0 < need && need <= c0 + k[x]) {
+            if (by_sum ? s0 < need && need <= s0 + w[x] : c0 < need && need <= c0 + k[x]) {
                 s.found_bin = 2 * tid + x;
                 s.found_cnt = (uint32_t)c0;
                 s.found_in = k[x];
@@ -388,8 +395,7 @@ struct Row {
 
     // The token of bin `bin` (of d) with which the running count (weight) reaches `need`, cnt and
     // sum being those before the bin.
-    template <bool BY_SUM>
-    __device__ __forceinline__ Cut refine(int bin, u64 need, u64 cnt, u64 sum) {
+    __device__ __forceinline__ Cut refine(bool by_sum, int bin, u64 need, u64 cnt, u64 sum) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         const int octave = bin >> per_octave;
         uint32_t lo = 0, hi = 0xFFFFFFFFu;  // keys of the bin that are left
@@ -453,7 +459,7 @@ struct Row {
                             atomicAdd(&s.hi[bin], v >> 12);
                         }
                         __syncthreads();
-                        const uint32_t sub = (uint32_t)max((find_bin<BY_SUM, true>(need, cnt, sum, up)), 0);
+                        const uint32_t sub = (uint32_t)max(find_bin(by_sum, need, cnt, sum, true, up), 0);
                         left = (int)s.found_in;
                         hi -= sub << shift;
                         lo = hi - min(hi - lo, (1u << shift) - 1);
@@ -472,7 +478,7 @@ struct Row {
                         k = __reduce_add_sync(kFull, k);
                         w = warp_sum(w);
                         const u64 w1 = sum + w + s.list_w[i];
-                        const bool is = BY_SUM ? sum + w < need && need <= w1 : cnt + k + 1 == need;
+                        const bool is = by_sum ? sum + w < need && need <= w1 : cnt + k + 1 == need;
                         if (is && (uint32_t)lane < ctas) {
                             peer_store(&s.ranked_key, lane, key);
                             peer_store(&s.ranked_idx, lane, idx);
@@ -495,17 +501,17 @@ struct Row {
             each([&](float, uint32_t, uint32_t key, float d) {
                 uint32_t w[2], oct[2];
                 mantissa2(both(d), w, oct);
-                into_bin<true>((int)((hi - key) >> shift), w[0], oct[0]);
+                into_bin(true, (int)((hi - key) >> shift), w[0], oct[0]);
             });
             join_bins([&](int) { return octave; });
-            const uint32_t sub = (uint32_t)max(find_bin<BY_SUM>(need, cnt, sum), 0);
+            const uint32_t sub = (uint32_t)max(find_bin(by_sum, need, cnt, sum), 0);
             hi -= sub << shift;
             lo = hi - min(hi - lo, (1u << shift) - 1);
         }
         // equal logits: the q-th by index
         const float z0 = of_key(hi);
         const u64 w = weight_of(dist(-z0));
-        const u64 q = BY_SUM ? (need - sum + w - 1) / w : need - cnt;
+        const u64 q = by_sum ? (need - sum + w - 1) / w : need - cnt;
         uint32_t idx;
         u64 val, total;
         const bool here = locate(
@@ -517,21 +523,98 @@ struct Row {
     }
 };
 
+struct Settings {
+    int64_t k;
+    uint32_t p_share, m_share, u;
+    bool by_k, by_p;
+};
+
+// The row's cut and its token, after the load.
+template <typename R>
+__device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, const Settings &set) {
+    Shared &s = r.s;
+    const int tid = threadIdx.x, lane = tid & 31;
+    Cut cut = {-INFINITY, 0xFFFFFFFFu, 0};
+    // First the cut of top-k, if any, then that of top-p: each phase's code is there once (inlined twice, a
+    // single row waits longer for instructions than for anything else).
+    bool by_sum = !set.by_k, bins = false, all = false;
+    u64 part = 0, whole = 0;  // whole: what top-k keeps
+    r.cover(set.by_k ? 6 : 5);
+    while (set.by_k || set.by_p) {
+        if (!bins) part = r.histogram(set.by_k, !set.by_k);
+        bins = true;
+        if (by_sum && whole == 0) {
+            if (r.rank == 0)  // (the bins are the cluster's)
+                for (int i = tid; i < kBins; i += kThreads) part += s.all_sum[i];
+            whole = r.cluster_sum(part);
+        }
+        const u64 need = by_sum ? max(part_of(whole, set.p_share), (u64)1) : (u64)set.k;
+        u64 cnt = 0, sum = 0;
+        const int bin = r.find_bin(by_sum, need, cnt, sum);
+        if (bin < 0 && !all) {
+            // beyond the bins: bins of every weight
+            all = true;
+            bins = false;
+            r.cover(4);
+            r.clear_bins();
+            continue;
+        }
+        if (bin >= 0) {  // (otherwise fewer than k tokens have any weight)
+            // where there are too many to gather, bins over keys take the place of those over d
+            bins = !by_sum && s.all_cnt[bin] <= kList;
+            cut = r.refine(by_sum, bin, need, cnt, sum);
+            whole = cut.sum;
+            if (!bins) r.clear_bins();
+        }
+        if (by_sum || !set.by_p) break;
+        by_sum = true;
+    }
+    // ---- the token
+    const u64 least = part_of(weight_of(0.f), set.m_share);
+    const float zc = -cut.z;
+    uint32_t idx;
+    u64 w, total;
+    const bool here = r.locate(
+        [&](float4 v, uint32_t i, u64 (&x)[4]) {
+            const float z[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int h = 0; h < 4; h += 2) {
+                x[h] = x[h + 1] = 0;
+                if (!(z[h] <= zc || z[h + 1] <= zc)) continue;
+                const float2 d = r.dist2(z[h], z[h + 1]);
+                uint32_t wm[2], n[2];
+                mantissa2(make_float2(d.x < kAll ? d.x : 0.f, d.y < kAll ? d.y : 0.f), wm, n);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const bool in = z[h + e] < zc || (z[h + e] == zc && i + h + e <= cut.idx);
+                    const u64 we = scaled(wm[e], n[e]);
+                    if (in && (e ? d.y : d.x) < kAll && we >= least) x[h + e] = we;
+                }
+            }
+        },
+        [&](u64 all) { return part_of(all, set.u); }, idx, w, total);
+    if (here && lane == 0) {
+        a.token[m] = (int32_t)idx;
+        if (a.prob) a.prob[m] = __fdiv_rn((float)w, (float)total);
+    }
+}
+
 template <bool CACHED>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int per) {
     extern __shared__ __align__(16) uint8_t dyn[];
     Shared &s = *reinterpret_cast<Shared *>(dyn);
     float *own = reinterpret_cast<float *>(dyn + (sizeof(Shared) + 15) / 16 * 16);
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
     const uint32_t rank = cluster_ctarank(), ctas = a.ctas;
     if (tid == 0) s.list_n[0] = s.list_n[1] = 0;
+    for (int i = tid; i < kBins; i += kThreads) s.cnt[i] = s.lo[i] = s.hi[i] = 0;
     cluster_arrive();  // (waited for before the first access to another CTA's memory)
     pdl_wait();
     pdl_trigger();
     const int64_t m = blockIdx.x / ctas;
     const int64_t i0 = min((int64_t)rank * per, (int64_t)a.V), i1 = min(i0 + per, (int64_t)a.V);
     const float *row = a.logits + m * a.ldl + i0;
-    Row<CACHED> r = {s, CACHED ? own : row, (uint32_t)i0, (int)(i1 - i0), ((int)(i1 - i0) + 3) / 4, rank, ctas, 0.f, 0.f, false, 0, 0.f, 0, 0};
+    Row<CACHED> r = {s, CACHED ? own : row, (uint32_t)i0, (int)(i1 - i0), ((int)(i1 - i0) + 3) / 4, rank, ctas, 0.f, 0.f, NAN, 0, 0.f, 0, 0};
     // ---- load; the largest logit
     float best = INFINITY;  // (of the negated ones, the smallest)
     if (CACHED && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
@@ -569,90 +652,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const bool greedy = !(t > 0.f);
     if (greedy) t = 1.f;
     r.c = __fmul_rn(__fdiv_rn(1.f, t), 1.4426950408889634f);
-    r.odd = isinf(r.top) || isinf(r.c);
-    const int64_t k = greedy ? 1 : a.top_k ? __ldg(a.top_k + m) : 0;
-    const uint32_t p_share = greedy || !a.top_p ? kOne : share_of(__ldg(a.top_p + m), kOne);
-    const uint32_t m_share = greedy || !a.min_p ? 0 : share_of(__ldg(a.min_p + m), 0);
-    const uint32_t u = min(share_of(__ldg(a.u + m), 0), kOne - 1);
-    const bool by_k = k > 0 && k < a.V, by_p = p_share < kOne;
-    // ---- the cut
-    Cut cut = {-INFINITY, 0xFFFFFFFFu, 0};
-    if (by_k) {
-        bool cut_off = true;
-        u64 cnt = 0, sum = 0;
-        r.cover(6);
-        r.template histogram<true, false>();
-        int bin = r.template find_bin<false>((u64)k, cnt, sum);
-        if (bin < 0) {
-            r.cover(4);
-            r.template histogram<true, false>();
-            bin = r.template find_bin<false>((u64)k, cnt, sum);
-            cut_off = bin >= 0;  // fewer than k tokens have any weight
-        }
-        bool kept_bins = true;
-        if (cut_off) {
-            kept_bins = s.all_cnt[bin] <= kList;  // otherwise bins over keys take their place
-            cut = r.template refine<false>(bin, (u64)k, cnt, sum);
-        }
-        if (by_p) {
-            if (!kept_bins) r.template histogram<true, false>();
-            u64 whole = cut.sum;
-            if (!cut_off) {
-                u64 part = 0;
-                if (rank == 0)
-                    for (int i = tid; i < kBins; i += kThreads) part += s.all_sum[i];
-                whole = r.cluster_sum(part);
-            }
-            cnt = sum = 0;
-            const u64 need = max(part_of(whole, p_share), (u64)1);
-            bin = r.template find_bin<true>(need, cnt, sum);
-            if (bin >= 0) cut = r.template refine<true>(bin, need, cnt, sum);
-        }
-    } else if (by_p) {
-        u64 need = 0, cnt = 0, sum = 0;
-        r.cover(5);
-        u64 part = r.template histogram<false, true>();
-        if (rank == 0)  // (the bins are the cluster's)
-            for (int i = tid; i < kBins; i += kThreads) part += s.all_sum[i];
-        need = max(part_of(r.cluster_sum(part), p_share), (u64)1);
-        int bin = r.template find_bin<true>(need, cnt, sum);
-        if (bin < 0) {
-            r.cover(4);
-            r.template histogram<false, true>();
-            bin = r.template find_bin<true>(need, cnt, sum);
-        }
-        if (bin >= 0) cut = r.template refine<true>(bin, need, cnt, sum);
+    Settings set;
+    set.k = greedy ? 1 : a.top_k ? __ldg(a.top_k + m) : 0;
+    set.p_share = greedy || !a.top_p ? kOne : share_of(__ldg(a.top_p + m), kOne);
+    set.m_share = greedy || !a.min_p ? 0 : share_of(__ldg(a.min_p + m), 0);
+    set.u = min(share_of(__ldg(a.u + m), 0), kOne - 1);
+    set.by_k = set.k > 0 && set.k < a.V;
+    set.by_p = set.p_share < kOne;
+    if (isinf(r.top) || isinf(r.c)) {
+        const float least = -r.top;
+        __syncthreads();
+        if (CACHED)
+            for (int i = tid; i < r.n4 * 4; i += kThreads) own[i] = flat(own[i], least);
+        else r.infinite = least;
+        r.top = 0.f, r.c = 1.f;
+        __syncthreads();
     }
-    // ---- the token
-    const u64 least = part_of(weight_of(0.f), m_share);
-    uint32_t idx;
-    u64 w, total;
-    const bool here = r.locate(
-        [&](float4 v, uint32_t i, u64 (&x)[4]) {
-            const float z[4] = {v.x, v.y, v.z, v.w};
-            const float zc = -cut.z;
-#pragma unroll
-            for (int h = 0; h < 4; h += 2) {
-                x[h] = x[h + 1] = 0;
-                bool in[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) in[e] = z[h + e] < zc || (z[h + e] == zc && i + h + e <= cut.idx);
-                if (!(in[0] || in[1])) continue;
-                const float2 d = r.dist2(z[h], z[h + 1]);
-                uint32_t wm[2], n[2];
-                mantissa2(make_float2(d.x < kAll ? d.x : 0.f, d.y < kAll ? d.y : 0.f), wm, n);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const u64 we = scaled(wm[e], n[e]);
-                    if (in[e] && (e ? d.y : d.x) < kAll && we >= least) x[h + e] = we;
-                }
-            }
-        },
-        [&](u64 all) { return part_of(all, u); }, idx, w, total);
-    if (here && lane == 0) {
-        a.token[m] = (int32_t)idx;
-        if (a.prob) a.prob[m] = __fdiv_rn((float)w, (float)total);
-    }
+    finish(r, a, m, set);
 }
 
 }  // namespace
