@@ -10,10 +10,10 @@
 // memory, so the row is read from global memory once, and the CTAs exchange bins, sums
 // and cuts through distributed shared memory.
 //   1. load, largest logit;
-//   2. the weight (and for top-k the count) of the tokens in bins of d, 2^s bins to an
-//      octave.  With top-k the cut is near the top: 64 bins to an octave of 16, and what
-//      lies below is not even weighed.  Otherwise 32 to an octave of 32; the rest is added
-//      up without bins.  If the cut turns out to lie below, again with all 41;
+//   2. the weight (and for top-k the count) of the tokens in bins of d.  With top-k the cut
+//      is near the top: 64 bins to each of 16 octaves, and what lies below is not even
+//      weighed.  Otherwise 32 to each of 32; the rest is added up without bins.  If the cut
+//      turns out to lie below, again with 16 bins to each of all 41 octaves;
 //   3. the tokens of the bin in which top-k (then top-p) ends are gathered in one CTA, narrowed
 //      there by histograms over their keys, and the last few ranked against each other;
 //      if they are too many to be gathered, the whole cluster narrows them the same way
@@ -35,7 +35,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kList = 768;           // tokens of a bin that one CTA gathers
-constexpr int kFew = 48;             // tokens that are ranked against each other
+constexpr int kFew = 256;            // tokens that are ranked against each other
 constexpr int kMaxCluster = 8;
 constexpr int kCached = 19456;       // logits of a CTA that stay in shared memory with two CTAs on an SM
 constexpr float kAll = 41.f;         // from this d on the weight is 0
@@ -123,6 +123,12 @@ __device__ __forceinline__ void peer_store(u64 *p, uint32_t rank, u64 v) {
 __device__ __forceinline__ void peer_store(uint32_t *p, uint32_t rank, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_shared_rank(smem_u32(p), rank)), "r"(v) : "memory");
 }
+__device__ __forceinline__ void peer_store(uint4 *p, uint32_t rank, uint4 v) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(map_shared_rank(smem_u32(p), rank)), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ u64 list_weight(uint4 t) { return (u64)t.w << 32 | t.z; }
 __device__ __forceinline__ uint32_t peer_add(uint32_t *p, uint32_t rank, uint32_t v) {
     uint32_t old;
     asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(map_shared_rank(smem_u32(p), rank)), "r"(v) : "memory");
@@ -133,14 +139,14 @@ struct Shared {
     uint32_t cnt[kBins], lo[kBins], hi[kBins];  // this CTA's bins: counts, and the halves of 24-bit weights
     uint32_t all_cnt[kBins];                    // the cluster's bins
     u64 all_sum[kBins];
-    uint32_t list_key[kList], list_idx[kList];  // (CTA 0's are used)
-    u64 list_w[kList];
+    uint4 list[kList];  // key, index, weight (CTA 0's is used)
     u64 warp_u64[kWarps];
     u64 slot[2][kMaxCluster];  // exchanged values
     u64 found_sum, ranked_sum;
     uint32_t warp_u32[kWarps];
     uint32_t list_n[2];  // tokens that came for the list (CTA 0's are used): two counters in turn
-    uint32_t found_bin, found_cnt, found_in, ranked_key, ranked_idx;
+    uint32_t list_left;
+    uint32_t found_bin, found_cnt, ranked_key, ranked_idx;
 };
 
 static_assert(2 * (sizeof(Shared) + 4 * kCached + 1024) <= 233472, "two CTAs on an SM");
@@ -276,6 +282,7 @@ struct Row {
         for (int i = threadIdx.x; i < n4; i += kThreads) {
             const float4 v = four(i);
             const float x[4] = {v.x, v.y, v.z, v.w};
+            uint32_t below = 0;
 #pragma unroll
             for (int h = 0; h < 4; h += 2) {
                 const float2 d = dist2(x[h], x[h + 1]);
@@ -286,9 +293,10 @@ struct Row {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (dd[e] < span) into_bin(count, bin_of(dd[e]), w[e], oct[e]);
-                    else if (dd[e] < limit) tail += scaled(w[e], oct[e]);
+                    else if (dd[e] < limit) below += w[e] >> (oct[e] - 16);  // (d >= span >= 16: 24 bits)
                 }
             }
+            tail += below;
         }
         join_bins([&](int b) { return b >> per_octave; });
         return tail;
@@ -327,7 +335,6 @@ struct Row {
             if (by_sum ? s0 < need && need <= s0 + w[x] : c0 < need && need <= c0 + k[x]) {
                 s.found_bin = 2 * tid + x;
                 s.found_cnt = (uint32_t)c0;
-                s.found_in = k[x];
                 s.found_sum = s0;
             }
             c0 += k[x], s0 += w[x];
@@ -400,6 +407,7 @@ struct Row {
         const int octave = bin >> per_octave;
         uint32_t lo = 0, hi = 0xFFFFFFFFu;  // keys of the bin that are left
         // visit(negated logit, index, key, d) for these tokens
+        const float from = ldexpf((float)bin, -per_octave), to = fminf(span, ldexpf((float)(bin + 1), -per_octave));
         auto each = [&](auto &&visit) {
             for (int i = tid; i < n4; i += kThreads) {
                 const float4 v = four(i);
@@ -410,7 +418,7 @@ struct Row {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float de = e ? d.y : d.x;
-                        if (!(de < span) || bin_of(de) != bin) continue;
+                        if (!(de >= from && de < to)) continue;
                         const uint32_t key = key_of(-x[h + e]);
                         if (key >= lo && key <= hi) visit(x[h + e], base + 4 * i + h + e, key, de);
                     }
@@ -422,23 +430,22 @@ struct Row {
             each([&](float, uint32_t idx, uint32_t key, float d) {
                 const uint32_t to = peer_add(&s.list_n[counter], 0, 1);
                 if (to < kList) {
-                    peer_store(&s.list_key[to], 0, key);
-                    peer_store(&s.list_idx[to], 0, idx);
-                    peer_store(&s.list_w[to], 0, weight_of(d));
+                    const u64 w = weight_of(d);
+                    peer_store(&s.list[to], 0, make_uint4(key, idx, (uint32_t)w, (uint32_t)(w >> 32)));
                 }
             });
             cluster_sync();
-            const int m = (int)peer(&s.list_n[counter], 0);
+            int m = (int)peer(&s.list_n[counter], 0);
             counter ^= 1;  // the other one's readers are past the barrier, and its next users behind another
             if (rank == 0 && tid == 0) s.list_n[counter] = 0;
             if (m <= kList) {
                 if (rank == 0) {
                     const int up = max(0, 16 - octave);
-                    for (int left = m; left > kFew;) {
+                    while (m > kFew) {
                         // narrow by a histogram over the keys, from the largest down
                         uint32_t a = 0, b = 0;
                         for (int i = tid; i < m; i += kThreads) {
-                            const uint32_t key = s.list_key[i];
+                            const uint32_t key = s.list[i].x;
                             if (key >= lo && key <= hi) a = max(a, key), b = max(b, ~key);
                         }
                         a = __reduce_max_sync(kFull, a), b = __reduce_max_sync(kFull, b);
@@ -450,40 +457,60 @@ struct Row {
                         if (lo == hi) break;  // equal logits: ranked by index below
                         const int shift = max(0, 32 - __clz(hi - lo) - 10);
                         for (int i = tid; i < m; i += kThreads) {
-                            const uint32_t key = s.list_key[i];
-                            if (key < lo || key > hi) continue;
-                            const int bin = (int)((hi - key) >> shift);
-                            const uint32_t v = (uint32_t)(s.list_w[i] >> up);
+                            const uint4 t = s.list[i];
+                            if (t.x < lo || t.x > hi) continue;
+                            const int bin = (int)((hi - t.x) >> shift);
+                            const uint32_t v = (uint32_t)(list_weight(t) >> up);
                             atomicAdd(&s.cnt[bin], 1u);
                             atomicAdd(&s.lo[bin], v & 0xFFFu);
                             atomicAdd(&s.hi[bin], v >> 12);
                         }
                         __syncthreads();
                         const uint32_t sub = (uint32_t)max(find_bin(by_sum, need, cnt, sum, true, up), 0);
-                        left = (int)s.found_in;
                         hi -= sub << shift;
                         lo = hi - min(hi - lo, (1u << shift) - 1);
-                        __syncthreads();  // (warp_u64 and found_in are written again)
+                        // the tokens of that bin alone stay in the list
+                        uint4 t[(kList + kThreads - 1) / kThreads];
+#pragma unroll
+                        for (int x = 0; x < (kList + kThreads - 1) / kThreads; ++x) t[x] = s.list[min(tid + x * kThreads, m - 1)];
+                        if (tid == 0) s.list_left = 0;
+                        __syncthreads();
+#pragma unroll
+                        for (int x = 0; x < (kList + kThreads - 1) / kThreads; ++x)
+                            if (tid + x * kThreads < m && t[x].x >= lo && t[x].x <= hi) s.list[atomicAdd(&s.list_left, 1u)] = t[x];
+                        __syncthreads();
+                        m = (int)s.list_left;
+                        __syncthreads();  // (list_left and warp_u64 are written again)
                     }
-                    // each warp ranks some of what is left against all of it
-                    for (int i = warp; i < m; i += kWarps) {
-                        const uint32_t key = s.list_key[i], idx = s.list_idx[i];
-                        if (key < lo || key > hi) continue;
+                    // what is left is ranked against all of it, a token by `team` neighbouring lanes
+                    int team = 1;
+                    while (team < 32 && 2 * team * m <= kThreads) team *= 2;
+                    const int mate = tid & (team - 1);
+                    for (int i0 = 0; i0 < m; i0 += kThreads / team) {
+                        const int i = i0 + tid / team;
+                        const uint4 me = s.list[min(i, m - 1)];
+                        const uint32_t key = me.x, idx = me.y;
                         uint32_t k = 0;
                         u64 w = 0;
-                        for (int j = lane; j < m; j += 32) {
-                            const uint32_t kj = s.list_key[j];
-                            if (kj <= hi && (kj > key || (kj == key && s.list_idx[j] < idx))) ++k, w += s.list_w[j];
+#pragma unroll 8
+                        for (int j = mate; j < m; j += team) {
+                            const uint4 t = s.list[j];
+                            const bool before = t.x > key || (t.x == key && t.y < idx);
+                            k += before ? 1u : 0u;
+                            w += before ? list_weight(t) : 0ull;
                         }
-                        k = __reduce_add_sync(kFull, k);
-                        w = warp_sum(w);
-                        const u64 w1 = sum + w + s.list_w[i];
-                        const bool is = by_sum ? sum + w < need && need <= w1 : cnt + k + 1 == need;
-                        if (is && (uint32_t)lane < ctas) {
-                            peer_store(&s.ranked_key, lane, key);
-                            peer_store(&s.ranked_idx, lane, idx);
-                            peer_store(&s.ranked_sum, lane, w1);
+                        for (int o = 1; o < team; o <<= 1) {
+                            k += __shfl_xor_sync(kFull, k, o);
+                            w += __shfl_xor_sync(kFull, w, o);
                         }
+                        if (i >= m || mate > 0) continue;
+                        const u64 w1 = sum + w + list_weight(me);
+                        if (by_sum ? sum + w < need && need <= w1 : cnt + k + 1 == need)
+                            for (uint32_t r = 0; r < ctas; ++r) {
+                                peer_store(&s.ranked_key, r, key);
+                                peer_store(&s.ranked_idx, r, idx);
+                                peer_store(&s.ranked_sum, r, w1);
+                            }
                     }
                 }
                 cluster_sync();
@@ -572,6 +599,8 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
     // ---- the token
     const u64 least = part_of(weight_of(0.f), set.m_share);
     const float zc = -cut.z;
+    // from this d on, w is below 2^(40 - limit) <= least / 2 (the series errs by far less than a factor 2)
+    const float limit = least > 0 ? fminf(kAll, 41.f - (float)(63 - __clzll((long long)least))) : kAll;
     uint32_t idx;
     u64 w, total;
     const bool here = r.locate(
@@ -580,15 +609,15 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
 #pragma unroll
             for (int h = 0; h < 4; h += 2) {
                 x[h] = x[h + 1] = 0;
-                if (!(z[h] <= zc || z[h + 1] <= zc)) continue;
                 const float2 d = r.dist2(z[h], z[h + 1]);
+                if (!((z[h] <= zc && d.x < limit) || (z[h + 1] <= zc && d.y < limit))) continue;
                 uint32_t wm[2], n[2];
                 mantissa2(make_float2(d.x < kAll ? d.x : 0.f, d.y < kAll ? d.y : 0.f), wm, n);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const bool in = z[h + e] < zc || (z[h + e] == zc && i + h + e <= cut.idx);
                     const u64 we = scaled(wm[e], n[e]);
-                    if (in && (e ? d.y : d.x) < kAll && we >= least) x[h + e] = we;
+                    if (in && (e ? d.y : d.x) < limit && we >= least) x[h + e] = we;
                 }
             }
         },
