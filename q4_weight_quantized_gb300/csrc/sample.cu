@@ -10,7 +10,7 @@
 // memory, so the row is read from global memory once, and the CTAs exchange bins, sums
 // and cuts through distributed shared memory.
 //   1. load, largest logit;
-//   2. the weight (and for top-k the count) of the tokens in bins of d.  With top-k the cut
+//   2. the number and the weight of the tokens in bins of d.  With top-k the cut
 //      is near the top: 64 bins to each of 16 octaves, and what lies below is not even
 //      weighed.  Otherwise 32 to each of 32; the rest is added up without bins.  If the cut
 //      turns out to lie below, again with 16 bins to each of all 41 octaves;
@@ -19,6 +19,8 @@
 //      if they are too many to be gathered, the whole cluster narrows them the same way
 //      first; equal logits are counted off by index;
 //   4. the sum of what is kept, the target, and the token by a scan in index order.
+// Where the tokens down to the first cut's bin are few, one CTA gathers them all after step
+// 2 and does the rest with them alone.
 // A bin never crosses an octave, so its tokens' weights have one scale: they are summed as
 // two 12-bit halves of a 24-bit number by 32-bit atomics without a result.
 // Bound by the arithmetic of the weights (some 70 instructions a logit in all, half of
@@ -239,9 +241,9 @@ struct Row {
         for (int i = threadIdx.x; i < kBins; i += kThreads) s.cnt[i] = s.lo[i] = s.hi[i] = 0;
         __syncthreads();
     }
-    __device__ __forceinline__ void into_bin(bool count, int bin, uint32_t w, uint32_t n) {
+    __device__ __forceinline__ void into_bin(int bin, uint32_t w, uint32_t n) {
         const uint32_t v = n <= 16 ? w : w >> (n - 16);
-        if (count) atomicAdd(&s.cnt[bin], 1u);
+        atomicAdd(&s.cnt[bin], 1u);
         atomicAdd(&s.lo[bin], v & 0xFFFu);
         atomicAdd(&s.hi[bin], v >> 12);
     }
@@ -276,7 +278,7 @@ struct Row {
     }
     // Bins of d < span over the row, from cleared ones.  Returns this thread's part of the weight beyond
     // (if beyond).
-    __device__ __forceinline__ u64 histogram(bool count, bool beyond) {
+    __device__ __forceinline__ u64 histogram(bool beyond) {
         u64 tail = 0;
         const float limit = beyond ? kAll : span;
         for (int i = threadIdx.x; i < n4; i += kThreads) {
@@ -292,7 +294,7 @@ struct Row {
                 const float dd[2] = {d.x, d.y};
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    if (dd[e] < span) into_bin(count, bin_of(dd[e]), w[e], oct[e]);
+                    if (dd[e] < span) into_bin(bin_of(dd[e]), w[e], oct[e]);
                     else if (dd[e] < limit) below += w[e] >> (oct[e] - 16);  // (d >= span >= 16: 24 bits)
                 }
             }
@@ -400,44 +402,78 @@ struct Row {
         return false;
     }
 
+    // Tokens from <= d < to, of a key in [lo, hi]: their number, and themselves in CTA 0's list as far as it
+    // holds them.  visit(index, key, d)
+    template <typename Visit>
+    __device__ __forceinline__ void each(float from, float to, uint32_t lo, uint32_t hi, Visit &&visit) {
+        for (int i = threadIdx.x; i < n4; i += kThreads) {
+            const float4 v = four(i);
+            const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int h = 0; h < 4; h += 2) {
+                const float2 d = dist2(x[h], x[h + 1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float de = e ? d.y : d.x;
+                    if (!(de >= from && de < to)) continue;
+                    const uint32_t key = key_of(-x[h + e]);
+                    if (key >= lo && key <= hi) visit(base + 4 * i + h + e, key, de);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ int gather(float from, float to, uint32_t lo, uint32_t hi) {
+        each(from, to, lo, hi, [&](uint32_t idx, uint32_t key, float d) {
+            const uint32_t at = peer_add(&s.list_n[counter], 0, 1);
+            if (at < kList) {
+                const u64 w = weight_of(d);
+                peer_store(&s.list[at], 0, make_uint4(key, idx, (uint32_t)w, (uint32_t)(w >> 32)));
+            }
+        });
+        cluster_sync();
+        const int m = (int)peer(&s.list_n[counter], 0);
+        counter ^= 1;  // the other one's readers are past the barrier, and its next users behind another
+        if (rank == 0 && threadIdx.x == 0) s.list_n[counter] = 0;
+        return m;
+    }
+    // Over the m tokens of CTA 0's list (m < 2^16; every thread of it calls): done(i, t, count, sum) for
+    // each token t, with the number and the weight of the tokens that before(other, t) names.  A token is
+    // the work of a few neighbouring lanes, one of which calls done.
+    template <typename Before, typename Done>
+    __device__ __forceinline__ void compare_all(int m, Before &&before, Done &&done) {
+        int team = 1;
+        while (team < 32 && 2 * team * m <= kThreads) team *= 2;
+        const int mate = threadIdx.x & (team - 1);
+        for (int i0 = 0; i0 < m; i0 += kThreads / team) {
+            const int i = i0 + threadIdx.x / team;
+            const uint4 me = s.list[min(i, m - 1)];
+            uint32_t k = 0;
+            u64 w = 0;
+#pragma unroll 8
+            for (int j = mate; j < m; j += team) {
+                const uint4 t = s.list[j];
+                const bool is = before(t, me);
+                k += is ? 1u : 0u;
+                w += is ? list_weight(t) : 0ull;
+            }
+            for (int o = 1; o < team; o <<= 1) {
+                k += __shfl_xor_sync(kFull, k, o);
+                w += __shfl_xor_sync(kFull, w, o);
+            }
+            if (i < m && mate == 0) done(i, me, k, w);
+        }
+    }
+    static __device__ __forceinline__ bool ranks_before(uint4 a, uint4 b) { return a.x > b.x || (a.x == b.x && a.y < b.y); }
+
     // The token of bin `bin` (of d) with which the running count (weight) reaches `need`, cnt and
     // sum being those before the bin.
     __device__ __forceinline__ Cut refine(bool by_sum, int bin, u64 need, u64 cnt, u64 sum) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         const int octave = bin >> per_octave;
         uint32_t lo = 0, hi = 0xFFFFFFFFu;  // keys of the bin that are left
-        // visit(negated logit, index, key, d) for these tokens
         const float from = ldexpf((float)bin, -per_octave), to = fminf(span, ldexpf((float)(bin + 1), -per_octave));
-        auto each = [&](auto &&visit) {
-            for (int i = tid; i < n4; i += kThreads) {
-                const float4 v = four(i);
-                const float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int h = 0; h < 4; h += 2) {
-                    const float2 d = dist2(x[h], x[h + 1]);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float de = e ? d.y : d.x;
-                        if (!(de >= from && de < to)) continue;
-                        const uint32_t key = key_of(-x[h + e]);
-                        if (key >= lo && key <= hi) visit(x[h + e], base + 4 * i + h + e, key, de);
-                    }
-                }
-            }
-        };
         for (;;) {
-            // CTA 0 gathers the tokens if they are few
-            each([&](float, uint32_t idx, uint32_t key, float d) {
-                const uint32_t to = peer_add(&s.list_n[counter], 0, 1);
-                if (to < kList) {
-                    const u64 w = weight_of(d);
-                    peer_store(&s.list[to], 0, make_uint4(key, idx, (uint32_t)w, (uint32_t)(w >> 32)));
-                }
-            });
-            cluster_sync();
-            int m = (int)peer(&s.list_n[counter], 0);
-            counter ^= 1;  // the other one's readers are past the barrier, and its next users behind another
-            if (rank == 0 && tid == 0) s.list_n[counter] = 0;
+            int m = gather(from, to, lo, hi);  // in CTA 0, if they are few
             if (m <= kList) {
                 if (rank == 0) {
                     const int up = max(0, 16 - octave);
@@ -482,53 +518,33 @@ struct Row {
                         m = (int)s.list_left;
                         __syncthreads();  // (list_left and warp_u64 are written again)
                     }
-                    // what is left is ranked against all of it, a token by `team` neighbouring lanes
-                    int team = 1;
-                    while (team < 32 && 2 * team * m <= kThreads) team *= 2;
-                    const int mate = tid & (team - 1);
-                    for (int i0 = 0; i0 < m; i0 += kThreads / team) {
-                        const int i = i0 + tid / team;
-                        const uint4 me = s.list[min(i, m - 1)];
-                        const uint32_t key = me.x, idx = me.y;
-                        uint32_t k = 0;
-                        u64 w = 0;
-#pragma unroll 8
-                        for (int j = mate; j < m; j += team) {
-                            const uint4 t = s.list[j];
-                            const bool before = t.x > key || (t.x == key && t.y < idx);
-                            k += before ? 1u : 0u;
-                            w += before ? list_weight(t) : 0ull;
-                        }
-                        for (int o = 1; o < team; o <<= 1) {
-                            k += __shfl_xor_sync(kFull, k, o);
-                            w += __shfl_xor_sync(kFull, w, o);
-                        }
-                        if (i >= m || mate > 0) continue;
-                        const u64 w1 = sum + w + list_weight(me);
+                    // what is left is ranked against all of it
+                    compare_all(m, ranks_before, [&](int, uint4 t, uint32_t k, u64 w) {
+                        const u64 w1 = sum + w + list_weight(t);
                         if (by_sum ? sum + w < need && need <= w1 : cnt + k + 1 == need)
                             for (uint32_t r = 0; r < ctas; ++r) {
-                                peer_store(&s.ranked_key, r, key);
-                                peer_store(&s.ranked_idx, r, idx);
+                                peer_store(&s.ranked_key, r, t.x);
+                                peer_store(&s.ranked_idx, r, t.y);
                                 peer_store(&s.ranked_sum, r, w1);
                             }
-                    }
+                    });
                 }
                 cluster_sync();
                 return {of_key(s.ranked_key), s.ranked_idx, s.ranked_sum};
             }
             // many: a histogram over their keys, from the largest down
             uint32_t a = 0, b = 0;
-            each([&](float, uint32_t, uint32_t key, float) { a = max(a, key), b = max(b, ~key); });
+            each(from, to, lo, hi, [&](uint32_t, uint32_t key, float) { a = max(a, key), b = max(b, ~key); });
             a = cluster_max(a);
             lo = ~cluster_max(b);
             hi = a;
             if (lo == hi) break;
             const int shift = max(0, 32 - __clz(hi - lo) - 10);
             clear_bins();
-            each([&](float, uint32_t, uint32_t key, float d) {
+            each(from, to, lo, hi, [&](uint32_t, uint32_t key, float d) {
                 uint32_t w[2], oct[2];
                 mantissa2(both(d), w, oct);
-                into_bin(true, (int)((hi - key) >> shift), w[0], oct[0]);
+                into_bin((int)((hi - key) >> shift), w[0], oct[0]);
             });
             join_bins([&](int) { return octave; });
             const uint32_t sub = (uint32_t)max(find_bin(by_sum, need, cnt, sum), 0);
@@ -556,6 +572,36 @@ struct Settings {
     bool by_k, by_p;
 };
 
+// The row's token from the tokens down to bin `bin` alone, which hold everything that top-k, or without
+// it top-p, keeps.  whole: without top-k, the weight of the row.
+template <typename R>
+__device__ __forceinline__ void finish_few(R &r, const SampleArgs &a, int64_t m, const Settings &set, int bin, u64 whole) {
+    Shared &s = r.s;
+    const int n = r.gather(0.f, fminf(r.span, ldexpf((float)(bin + 1), -r.per_octave)), 0, 0xFFFFFFFFu);
+    if (r.rank != 0) return;  // (no CTA touches another's memory from here on)
+    const u64 least = part_of(weight_of(0.f), set.m_share);
+    // each token's rank, and the weight before it; a thread has at most one token's
+    static_assert(kFew <= kThreads, "one token a thread");
+    int mine = -1;
+    uint32_t rank = 0;
+    u64 before = 0, weight = 0;
+    r.compare_all(n, R::ranks_before, [&](int i, uint4 t, uint32_t k, u64 w) { mine = i, rank = k, before = w, weight = list_weight(t); });
+    bool keep = mine >= 0 && (!set.by_k || rank < (uint32_t)min(set.k, (int64_t)kFew));
+    if (set.by_k) whole = r.block_sum(keep ? weight : 0);
+    if (set.by_p) keep = keep && before < max(part_of(whole, set.p_share), (u64)1);
+    keep = keep && weight >= least;
+    const u64 total = r.block_sum(keep ? weight : 0);  // (its barriers stand between the list's reads and writes)
+    if (mine >= 0 && !keep) s.list[mine].z = s.list[mine].w = 0;
+    __syncthreads();
+    const u64 goal = part_of(total, set.u);
+    r.compare_all(n, [](uint4 o, uint4 t) { return o.y < t.y; }, [&](int, uint4 t, uint32_t, u64 w) {
+        if (w <= goal && goal < w + list_weight(t)) {
+            a.token[m] = (int32_t)t.y;
+            if (a.prob) a.prob[m] = __fdiv_rn((float)list_weight(t), (float)total);
+        }
+    });
+}
+
 // The row's cut and its token, after the load.
 template <typename R>
 __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, const Settings &set) {
@@ -568,7 +614,7 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
     u64 part = 0, whole = 0;  // whole: what top-k keeps
     r.cover(set.by_k ? 6 : 5);
     while (set.by_k || set.by_p) {
-        if (!bins) part = r.histogram(set.by_k, !set.by_k);
+        if (!bins) part = r.histogram(!set.by_k);
         bins = true;
         if (by_sum && whole == 0) {
             if (r.rank == 0)  // (the bins are the cluster's)
@@ -585,6 +631,10 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
             r.cover(4);
             r.clear_bins();
             continue;
+        }
+        if (bin >= 0 && by_sum != set.by_k && cnt + s.all_cnt[bin] <= (u64)kFew) {
+            finish_few(r, a, m, set, bin, whole);
+            return;
         }
         if (bin >= 0) {  // (otherwise fewer than k tokens have any weight)
             // where there are too many to gather, bins over keys take the place of those over d
