@@ -7,11 +7,14 @@
 // never meet, so all moves run at once.
 //
 // select_kernel, a CTA per sequence and head: weights become order-preserving 32-bit
-// keys in shared memory; a histogram over the range of the keys that are left, narrowed
-// to the bin that holds the wanted rank, finds the cut in two or three rounds; then
-// each warp walks a contiguous run of slots, so ranks in slot order are prefix sums of
-// ballots.  Bound by latency (a few block-wide rounds); the reads are 8 bytes a slot.
-// move_kernel copies the rows, 16 bytes a lane: bound by HBM.
+// keys in shared memory.  A histogram over the range of the keys narrows it to the bin
+// that holds the wanted rank; once a few slots are left they are ranked against each
+// other, which also settles equal weights by slot.  The last pass takes the slots in
+// order, four to a thread, and numbers holes and fillers by one scan per tile.  Bound by
+// latency (some twenty block-wide steps; 256 threads for caches of up to 4096 slots, whose
+// steps would otherwise cost more in idle warps than in work); the reads are 8 bytes a slot.
+// move_kernel copies the rows, 16 bytes a lane: bound by HBM (two or four rows a thread cost
+// more in occupancy than their overlapping loads gave: 62 and 70 us against 59).
 #include <cuda_runtime.h>
 
 #include "decode_ops.h"
@@ -20,11 +23,11 @@
 namespace q4k {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kSmall = 4096;    // slots up to which 256 threads do
 constexpr int kCached = 20480;  // slots whose keys fit beside the histogram with two CTAs on an SM
+constexpr int kFew = 128;       // slots that are ranked against each other
 constexpr int kMoveThreads = 256;
+constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 // Order-preserving key: smaller weight, smaller key; -0 as +0; NaN above everything.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -33,41 +36,49 @@ __device__ __forceinline__ uint32_t key_of(float w) {
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t *scratch) {
-    v = __reduce_add_sync(0xFFFFFFFFu, v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return __reduce_add_sync(0xFFFFFFFFu, scratch[threadIdx.x & 31]);
-}
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *scratch) {
-    v = __reduce_max_sync(0xFFFFFFFFu, v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return __reduce_max_sync(0xFFFFFFFFu, scratch[threadIdx.x & 31]);
-}
-// Sum of the warps before this one of a value that every lane of a warp holds; *total
-// the sum of all.
-__device__ __forceinline__ uint32_t warps_before(uint32_t v, uint32_t *scratch, uint32_t *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    __syncthreads();
-    if (lane == 0) scratch[warp] = v;
-    __syncthreads();
-    const uint32_t w = scratch[lane];
-    *total = __reduce_add_sync(0xFFFFFFFFu, w);
-    return __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0u);
-}
+template <int THREADS>
+struct Block {
+    static constexpr int WARPS = THREADS / 32;
+    static __device__ __forceinline__ uint32_t sum(uint32_t v, uint32_t *scratch) {
+        v = __reduce_add_sync(kFull, v);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+        __syncthreads();
+        const int lane = threadIdx.x & 31;
+        return __reduce_add_sync(kFull, lane < WARPS ? scratch[lane] : 0u);
+    }
+    // Sum of a value over the threads before this one; total: over all.  Two scratch arrays in turn, so
+    // that one barrier a scan is enough.
+    static __device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t *scratch, uint32_t &total) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        uint32_t inc = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t t = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += t;
+        }
+        if (lane == 31) scratch[warp] = inc;
+        __syncthreads();
+        const uint32_t w = lane < WARPS ? scratch[lane] : 0u;
+        total = __reduce_add_sync(kFull, w);
+        return __reduce_add_sync(kFull, lane < warp ? w : 0u) + inc - v;
+    }
+};
 
 // CACHED: keys and protection bits lie in shared memory; otherwise both are formed
 // again from the arrays on every pass.
-template <bool CACHED>
-__global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
-    extern __shared__ uint32_t dyn[];
-    __shared__ uint32_t hist[kBins];
-    __shared__ uint32_t scratch[kWarps + 1];
-    __shared__ uint32_t found[2];
-    uint32_t *keys = dyn, *bits = dyn + kCached;  // [kCached], [kCached / 32]
+template <int THREADS, bool CACHED>
+__global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
+    using B = Block<THREADS>;
+    constexpr int BINS = 2 * THREADS, LOG_BINS = THREADS == 1024 ? 11 : 9;
+    constexpr int KEYS = CACHED ? (THREADS == 1024 ? kCached : kSmall) : 0;
+    static_assert(BINS == 1 << LOG_BINS, "two bins a thread");
+    extern __shared__ __align__(16) uint32_t dyn[];
+    __shared__ uint32_t hist[BINS];
+    __shared__ uint32_t scratch[2][32], red[5][32];
+    __shared__ uint2 list[kFew];
+    __shared__ uint32_t found[2], listed;
+    uint32_t *keys = dyn, *bits = dyn + KEYS;  // [KEYS], [KEYS / 32]
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -82,138 +93,232 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     if (n <= a.budget) {
         if (tid == 0) a.count[bh] = 0;
         if (w_out != w)
-            for (int j = tid; j < n; j += kThreads) w_out[j] = w[j];
+            for (int j = tid; j < n; j += THREADS) w_out[j] = w[j];
         if (p_out != p)
-            for (int j = tid; j < n; j += kThreads) p_out[j] = p[j];
+            for (int j = tid; j < n; j += THREADS) p_out[j] = p[j];
         return;
     }
-    // ---- newest position; positions as offset binary, so that the unsigned maximum serves
-    uint32_t top = 0;
-    for (int j = tid; j < n; j += kThreads) {
-        top = max(top, (uint32_t)p[j] ^ 0x80000000u);
-        if (CACHED) keys[j] = key_of(w[j]);
+    // ---- newest position (as offset binary, so that the unsigned maximum serves), and the keys; what
+    // stays below keep goes over at once, the holes among it are overwritten at the end.  CACHED: a
+    // thread holds slots tid, tid + THREADS, ... in registers, loaded before anything waits for one.
+    constexpr int PER = CACHED ? KEYS / THREADS : 1;
+    const bool copy_w = w_out != w, copy_p = p_out != p;
+    uint32_t top = 0, mine[PER];
+    int32_t pos[PER];
+    if constexpr (CACHED) {
+        float wj[PER];
+#pragma unroll
+        for (int x = 0; x < PER; ++x) {
+            if (x * THREADS >= n) break;
+            const int j = min(x * THREADS + tid, n - 1);
+            pos[x] = p[j], wj[x] = w[j];
+        }
+#pragma unroll
+        for (int x = 0; x < PER; ++x) {
+            if (x * THREADS >= n) break;
+            const int j = x * THREADS + tid;
+            top = max(top, (uint32_t)pos[x] ^ 0x80000000u);
+            mine[x] = key_of(wj[x]);
+            keys[j] = mine[x];  // (past n: never looked at)
+            if (copy_w && j < keep) w_out[j] = wj[x];
+            if (copy_p && j < keep) p_out[j] = pos[x];
+        }
+    } else {
+        for (int j = tid; j < n; j += THREADS) {
+            const int32_t pj = p[j];
+            top = max(top, (uint32_t)pj ^ 0x80000000u);
+            if (copy_w && j < keep) w_out[j] = w[j];
+            if (copy_p && j < keep) p_out[j] = pj;
+        }
     }
-    const int64_t newest = (int32_t)(block_max(top, scratch) ^ 0x80000000u);
+    top = __reduce_max_sync(kFull, top);
+    if (lane == 0) red[0][warp] = top;
+    __syncthreads();
+    const int64_t newest = (int32_t)(__reduce_max_sync(kFull, lane < B::WARPS ? red[0][lane] : 0u) ^ 0x80000000u);
     auto is_protected = [&](int32_t pos) { return pos < a.sinks || (int64_t)pos > newest - a.recent; };
     auto key_at = [&](int j) { return CACHED ? keys[j] : key_of(w[j]); };
     auto prot_at = [&](int j) { return CACHED ? (bits[j >> 5] >> (j & 31) & 1) != 0 : is_protected(p[j]); };
-    // ---- protected slots
-    uint32_t free_slots = 0;
-    for (int j0 = warp * 32; j0 < n; j0 += kThreads) {
-        const int j = j0 + lane;
-        const bool prot = j < n && is_protected(p[j]);
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, prot);
-        if (CACHED && lane == 0) bits[j0 >> 5] = m;
-        free_slots += j < n && !prot;
+    // ---- protected slots; number and range of the keys of either class
+    uint32_t free_slots = 0, low[2] = {kFull, kFull}, high[2] = {0, 0}, prots = 0;  // prots: of this thread's slots
+    auto of_either = [&](uint32_t k, bool prot) {
+        free_slots += !prot;
+        low[0] = prot ? low[0] : min(low[0], k), high[0] = prot ? high[0] : max(high[0], k);
+        low[1] = prot ? min(low[1], k) : low[1], high[1] = prot ? max(high[1], k) : high[1];
+    };
+    if constexpr (CACHED) {
+#pragma unroll
+        for (int x = 0; x < PER; ++x) {
+            if (x * THREADS >= n) break;
+            const int j = x * THREADS + tid;
+            const bool prot = is_protected(pos[x]);
+            const uint32_t m = __ballot_sync(kFull, prot);
+            if (lane == 0) bits[j >> 5] = m;
+            prots |= prot ? 1u << x : 0u;
+            if (j < n) of_either(mine[x], prot);
+        }
+    } else {
+        for (int j = tid; j < n; j += THREADS) of_either(key_of(w[j]), is_protected(p[j]));
     }
-    free_slots = block_sum(free_slots, scratch);  // (its barriers order the bits, too)
+    // visit(slot, key) for every slot of class `of` with a key in [lo, hi]
+    auto each = [&](bool of, uint32_t lo, uint32_t hi, auto &&visit) {
+        if constexpr (CACHED) {
+#pragma unroll
+            for (int x = 0; x < PER; ++x) {
+                if (x * THREADS >= n) break;
+                const int j = x * THREADS + tid;
+                if (j < n && mine[x] >= lo && mine[x] <= hi && ((prots >> x & 1) != 0) == of) visit(j, mine[x]);
+            }
+        } else {
+            for (int j = tid; j < n; j += THREADS) {
+                const uint32_t k = key_of(w[j]);
+                if (k >= lo && k <= hi && is_protected(p[j]) == of) visit(j, k);
+            }
+        }
+    };
+    free_slots = __reduce_add_sync(kFull, free_slots);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) low[x] = __reduce_min_sync(kFull, low[x]), high[x] = __reduce_max_sync(kFull, high[x]);
+    __syncthreads();
+    if (lane == 0) red[0][warp] = free_slots, red[1][warp] = low[0], red[2][warp] = high[0], red[3][warp] = low[1], red[4][warp] = high[1];
+    if (tid == 0) listed = 0;
+    __syncthreads();
+    const int rl = min(lane, B::WARPS - 1);
+    free_slots = __reduce_add_sync(kFull, lane < B::WARPS ? red[0][lane] : 0u);
     // ---- the class in which the cut lies: unprotected slots, or, if these are not enough, protected ones
-    uint32_t need = n - a.budget;
+    uint32_t need = n - a.budget, in = free_slots;
     const bool in_prot = need > free_slots;
-    if (in_prot) need -= free_slots;
-    // ---- the cut: in that class, keys < cut go, and the first `ties` slots of key == cut
-    uint32_t lo = 0xFFFFFFFFu, hi = 0;
-    for (int j = tid; j < n; j += kThreads)
-        if (prot_at(j) == in_prot) {
-            const uint32_t k = key_at(j);
-            lo = min(lo, k);
-            hi = max(hi, k);
-        }
-    lo = ~block_max(~lo, scratch);
-    hi = block_max(hi, scratch);
-    uint32_t cut, ties;
+    if (in_prot) need -= free_slots, in = n - free_slots;
+    uint32_t lo = __reduce_min_sync(kFull, red[in_prot ? 3 : 1][rl]), hi = __reduce_max_sync(kFull, red[in_prot ? 4 : 2][rl]);
+    // ---- the cut: of that class, slots with a smaller (key, slot) than (cut, cut_slot) go, and this one
+    uint32_t cut, cut_slot = kFull;
+    bool gathered = false;
+    if (need == 1) {  // one token more, one token less: the smallest key
+        hi = lo;
+        in = 1;  // (if only one slot has it; the list finds out)
+    }
     for (;;) {
-        const uint32_t width = hi - lo;
-        const int shift = max(0, 32 - __clz(width) - 11);  // at most 2048 bins
-        for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-        __syncthreads();
-        for (int j = tid; j < n; j += kThreads) {
-            const uint32_t k = key_at(j);
-            if (k >= lo && k <= hi && prot_at(j) == in_prot) atomicAdd(&hist[(k - lo) >> shift], 1u);
+        if (need == in && hi != lo) {  // all of them go
+            cut = hi;
+            break;
         }
+        if (in <= kFew && !gathered) {
+            gathered = true;
+            each(in_prot, lo, hi, [&](int j, uint32_t k) {
+                const uint32_t at = atomicAdd(&listed, 1u);
+                if (at < kFew) list[at] = make_uint2(k, j);
+            });
+            __syncthreads();
+            in = listed;
+            if (in <= kFew) {
+                // ranked against each other, a slot by a few neighbouring lanes
+                constexpr int TEAM = THREADS / kFew;
+                const uint2 me = list[min((uint32_t)(tid / TEAM), in - 1)];
+                uint32_t before = 0;
+                for (uint32_t i = tid % TEAM; i < in; i += TEAM) {
+                    const uint2 t = list[i];
+                    before += t.x < me.x || (t.x == me.x && t.y < me.y) ? 1u : 0u;
+                }
+#pragma unroll
+                for (int o = 1; o < TEAM; o <<= 1) before += __shfl_xor_sync(kFull, before, o);
+                if (tid / TEAM < in && tid % TEAM == 0 && before + 1 == need) found[0] = me.x, found[1] = me.y;
+                __syncthreads();
+                cut = found[0], cut_slot = found[1];
+                break;
+            }
+        }
+        if (lo == hi) {
+            // many equal keys: the need-th of them by slot
+            cut = lo;
+            uint32_t run = 0;
+            for (int j0 = 0, turn = 0; j0 < n; j0 += THREADS, turn ^= 1) {
+                const int j = j0 + tid;
+                const bool is = j < n && key_at(j) == cut && prot_at(j) == in_prot;
+                uint32_t total;
+                const uint32_t before = run + B::scan(is, scratch[turn], total);
+                if (is && before + 1 == need) found[0] = j;
+                run += total;
+            }
+            __syncthreads();
+            cut_slot = found[0];
+            break;
+        }
+        const int shift = max(0, 32 - __clz(hi - lo) - LOG_BINS);
+        for (int i = tid; i < BINS; i += THREADS) hist[i] = 0;
+        __syncthreads();
+        each(in_prot, lo, hi, [&](int, uint32_t k) { atomicAdd(&hist[(k - lo) >> shift], 1u); });
         __syncthreads();
         // bins 2 tid, 2 tid + 1: the one in which the need-th smallest key lies
         const uint32_t c0 = hist[2 * tid], c1 = hist[2 * tid + 1];
-        uint32_t inc = c0 + c1;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-            if (lane >= o) inc += v;
-        }
         uint32_t all;
-        const uint32_t before = warps_before(__shfl_sync(0xFFFFFFFFu, inc, 31), scratch, &all) + inc - c0 - c1;
+        const uint32_t before = B::scan(c0 + c1, scratch[0], all);
         if (before < need && need <= before + c0) found[0] = 2 * tid, found[1] = before;
         else if (before + c0 < need && need <= before + c0 + c1) found[0] = 2 * tid + 1, found[1] = before + c0;
         __syncthreads();
-        const uint32_t bin = found[0], left = need - found[1], in_bin = hist[bin];
+        const uint32_t bin = found[0];
+        need -= found[1];
+        in = hist[bin];
         lo += bin << shift;
         hi = lo + min(hi - lo, (1u << shift) - 1);
-        need = left;
-        if (shift == 0 || in_bin == left) {
-            // one key left, or the whole bin goes
-            cut = hi;
-            ties = in_bin == left ? 0xFFFFFFFFu : left;
-            break;
-        }
         __syncthreads();
     }
-    // ---- ranks in slot order: warp `warp` walks slots [s0, s1)
-    const int per = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int s0 = min(warp * per, n), s1 = min(s0 + per, n);
-    uint32_t all;
-    uint32_t tie0 = 0;
-    if (ties != 0xFFFFFFFFu) {
-        for (int j0 = s0; j0 < s1; j0 += 32) {
-            const int j = j0 + lane;
-            tie0 += __popc(__ballot_sync(0xFFFFFFFFu, j < s1 && key_at(j) == cut && prot_at(j) == in_prot));
-        }
-        tie0 = warps_before(tie0, scratch, &all);
-    }
-    auto walk = [&](auto &&visit) {
-        uint32_t tie = tie0;
-        for (int j0 = s0; j0 < s1; j0 += 32) {
-            const int j = j0 + lane;
-            bool gone = false, is_tie = false;
-            if (j < s1) {
-                const bool prot = prot_at(j);
-                const uint32_t k = key_at(j);
-                is_tie = prot == in_prot && k == cut;
-                gone = prot == in_prot ? k < cut || (is_tie && ties == 0xFFFFFFFFu) : in_prot;
-            }
-            const uint32_t m = __ballot_sync(0xFFFFFFFFu, is_tie);
-            if (is_tie && tie + __popc(m & ((1u << lane) - 1)) < ties) gone = true;
-            tie += __popc(m);
-            visit(j, gone);
-        }
-    };
-    uint32_t holes = 0, fill = 0;
-    walk([&](int j, bool gone) {
-        holes += __popc(__ballot_sync(0xFFFFFFFFu, j < s1 && gone && j < keep));
-        fill += __popc(__ballot_sync(0xFFFFFFFFu, j < s1 && !gone && j >= keep));
-    });
-    uint32_t moves;
-    uint32_t hole = warps_before(holes, scratch, &moves);
-    uint32_t from = warps_before(fill, scratch, &all);
-    int2 *list = a.moves + (int64_t)bh * a.max_moves;
-    walk([&](int j, bool gone) {
-        const bool to = j < s1 && gone && j < keep, src = j < s1 && !gone && j >= keep;
-        const uint32_t mt = __ballot_sync(0xFFFFFFFFu, to), ms = __ballot_sync(0xFFFFFFFFu, src), lt = (1u << lane) - 1;
-        if (to) list[hole + __popc(mt & lt)].x = j;
-        if (src) list[from + __popc(ms & lt)].y = j;
-        hole += __popc(mt);
-        from += __popc(ms);
-        if (j < s1 && j < keep && !gone) {
-            if (w_out != w) w_out[j] = w[j];
-            if (p_out != p) p_out[j] = p[j];
-        }
-    });
+    // ---- holes below keep and fillers from there on, numbered in slot order: tiles of four slots a thread
+    int2 *list_out = a.moves + (int64_t)bh * a.max_moves;
+    uint32_t holes = 0, fills = 0;
     __syncthreads();
-    for (uint32_t i = tid; i < moves; i += kThreads) {
-        const int2 m = list[i];
+    for (int j0 = 0, turn = 0; j0 < n; j0 += 4 * THREADS, turn ^= 1) {
+        const int j = j0 + 4 * tid;
+        uint32_t k[4] = {0, 0, 0, 0}, prot = 0;
+        if (j < n) {
+            if constexpr (CACHED) {
+                const uint4 t = *reinterpret_cast<const uint4 *>(keys + j);  // (past n: whatever is there)
+                k[0] = t.x, k[1] = t.y, k[2] = t.z, k[3] = t.w;
+                prot = bits[j >> 5] >> (j & 31);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (j + x < n) k[x] = key_of(w[j + x]), prot |= is_protected(p[j + x]) ? 1u << x : 0u;
+            }
+        }
+        uint32_t count = 0, mark = 0;  // holes, fillers << 16; slots of either kind
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const bool of_class = ((prot >> x & 1) != 0) == in_prot;
+            const bool gone = of_class ? k[x] < cut || (k[x] == cut && (uint32_t)(j + x) <= cut_slot) : in_prot;
+            const bool below = j + x < keep;
+            if (j + x < n && gone == below) mark |= 1u << x, count += below ? 1u : 1u << 16;
+        }
+        uint32_t total;
+        const uint32_t before = B::scan(count, scratch[turn], total);
+        uint32_t hole = holes + (before & 0xFFFF), fill = fills + (before >> 16);
+        if (j < n) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if (!(mark >> x & 1)) continue;
+                if (j + x < keep) list_out[hole++].x = j + x;
+                else list_out[fill++].y = j + x;
+            }
+        }
+        holes += total & 0xFFFF;
+        fills += total >> 16;
+    }
+    __syncthreads();
+    for (uint32_t i = tid; i < holes; i += THREADS) {
+        const int2 m = list_out[i];
         w_out[m.x] = w[m.y];
         p_out[m.x] = p[m.y];
     }
-    if (tid == 0) a.count[bh] = (int32_t)moves;
+    if (tid == 0) a.count[bh] = (int32_t)holes;
+}
+
+template <int THREADS, bool CACHED>
+cudaError_t launch_select(const EvictArgs &a, cudaStream_t s) {
+    auto kern = select_kernel<THREADS, CACHED>;
+    const int keys = CACHED ? (THREADS == 1024 ? kCached : kSmall) : 0, smem = (keys + keys / 32) * 4;
+    if (CACHED) {
+        const cudaError_t e = ensure_smem((const void *)kern, smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kern, dim3(a.c.batch * a.c.heads), dim3(THREADS), smem, s, dim3(1), a);
 }
 
 // `per_head` blocks for each sequence and head.  A row is `chunks` 16-byte chunks, a thread
@@ -247,15 +352,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
 }  // namespace
 
 cudaError_t launch_kv_evict(const DeviceInfo &di, const EvictArgs &a, cudaStream_t s) {
-    const bool cached = a.cap <= kCached;
-    const int smem = cached ? (kCached + kCached / 32) * 4 : 0;
-    auto kern = cached ? select_kernel<true> : select_kernel<false>;
-    cudaError_t e = cudaSuccess;
-    if (cached) e = ensure_smem((const void *)kern, smem);
+    cudaError_t e = a.cap <= kSmall    ? launch_select<256, true>(a, s)
+                    : a.cap <= kCached ? launch_select<1024, true>(a, s)
+                                       : launch_select<1024, false>(a, s);
     if (e != cudaSuccess) return e;
     const int bh = a.c.batch * a.c.heads;
-    e = launch_pdl(kern, dim3(bh), dim3(kThreads), smem, s, dim3(1), a);
-    if (e != cudaSuccess) return e;
     const int chunks = a.c.dim * (a.c.e4m3 ? 1 : 2) / 16, rows = kMoveThreads / chunks;
     // a few rounds of copies per block, but no more blocks than fill the GPU a few times over
     int64_t per_head = (a.max_moves + 4 * rows - 1) / (4 * rows);
