@@ -547,6 +547,42 @@ def test_norm(M, D, off, post, pre, gate, res, bias):
     assert (x[:, D:] == 0).all() and (r_out[:, D:] == 0).all()
 
 
+@pytest.mark.parametrize("D", [8, 64, 300, 768, 1000, 5120, 10240])
+@pytest.mark.parametrize("post,pre,gate,res,bias", [
+    ("rms", "rms", "row", BF, False), ("layer", "rms", None, torch.float32, True), ("none", "layer", "all", torch.float32, True),
+    ("rms", "none", "all", BF, True), ("rms", "layer", "row", torch.float32, True)])
+def test_norm_many_rows_are_each_row_alone(D, post, pre, gate, res, bias):
+    """Enough rows for every CTA to walk several: each equals the same row in a call of its own to a few roundings (the
+    orders of summation and of the factors differ), the outputs' own rounding aside; the last rows and r_out = r_in."""
+    g = gen_of(D)
+    M, kind = 1401, {"none": 0, "rms": 1, "layer": 2}
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    y, r0 = rnd(M, D) * 3, (rnd(M, D) * 2).to(res)
+    pw, qw = 1 + 0.2 * rnd(D), 1 + 0.2 * rnd(D)
+    pb, qb = (rnd(D), rnd(D)) if bias else (None, None)
+    gt = None if gate is None else rnd(1 if gate == "row" else M, D)
+    t = q4k.Q4K_RES_FP32 if res == torch.float32 else q4k.Q4K_RES_BF16
+
+    def call(y, gt, r, r_out, x):
+        q4k.q4k_norm_residual(y.shape[0], D, y, D, kind[post], pw, pb, 1e-5, gt, D if gate == "all" else 0, 0.7, r, r_out, D, t,
+                              kind[pre], qw, qb, 1e-6, x, D)
+
+    r, x = r0.clone(), torch.zeros(M, D, dtype=BF, device="cuda")
+    call(y, gt, r, r, x)
+    q4k.q4k_check_device()
+    for m in [0, 1, 303, 304, 700, M - 2, M - 1]:
+        r1, x1 = torch.zeros(1, D, dtype=res, device="cuda"), torch.zeros(1, D, dtype=BF, device="cuda")
+        call(y[m:m + 1], gt[m:m + 1] if gate == "all" else gt, r0[m:m + 1], r1, x1)
+        for got, want in ((r[m], r1[0]), (x[m], x1[0])):
+            scale = want.double().abs() + want.double().pow(2).mean().sqrt()
+            tol = scale * 100 * 2.0 ** -24 + (want.double().abs() * 2.0 ** -7 if want.dtype == BF else 0)  # (one step of bf16)
+            assert ((got.double() - want.double()).abs() <= tol).all()
+    full = R.norm_residual(np64(y), kind[post], np64(pw), None if pb is None else np64(pb), 1e-5, None if gt is None else np64(gt),
+                           0.7, np64(r0), kind[pre], np64(qw), None if qb is None else np64(qb), 1e-6)
+    for got, want in ((np64(r), full[0]), (np64(x), full[1])):
+        assert np.linalg.norm(got - want) <= np.linalg.norm(want) * (2.0 ** -9 + 1e-6)
+
+
 @pytest.mark.parametrize("res", [torch.float32, BF])
 @pytest.mark.parametrize("D", [96, 101, 20000])
 def test_norm_in_place_and_parts(res, D):
