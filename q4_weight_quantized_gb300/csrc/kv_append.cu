@@ -20,29 +20,26 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint16_t to_bf16(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
-// nearest e4m3, values beyond +-448 to +-448, NaN to NaN
-__device__ __forceinline__ uint8_t to_e4m3(float x) {
-    return x != x ? 0x7F : __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// nearest e4m3 of two values, beyond +-448 to +-448, NaN to NaN
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
-// Four consecutive values of a row: to bf16, or scaled to the cache's type.
-__device__ __forceinline__ void store4(void *row, int at, const float (&x)[4], bool e4m3) {
-    if (e4m3) {
-        uint32_t w = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w |= (uint32_t)to_e4m3(x[i]) << (8 * i);
-        reinterpret_cast<uint32_t *>(row)[at / 4] = w;
-    } else {
-        uint2 w;
-        w.x = to_bf16(x[0]) | (uint32_t)to_bf16(x[1]) << 16;
-        w.y = to_bf16(x[2]) | (uint32_t)to_bf16(x[3]) << 16;
-        reinterpret_cast<uint2 *>(row)[at / 4] = w;
-    }
+// Four consecutive values of a row, in the output's type.
+__device__ __forceinline__ void store4(void *row, int at, const float *x, bool e4m3) {
+    if (e4m3) reinterpret_cast<uint32_t *>(row)[at / 4] = pack_e4m3(x[0], x[1]) | pack_e4m3(x[2], x[3]) << 16;
+    else reinterpret_cast<uint2 *>(row)[at / 4] = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
 __device__ __forceinline__ void store1(void *row, int at, float x, bool e4m3) {
-    if (e4m3) static_cast<uint8_t *>(row)[at] = to_e4m3(x);
-    else static_cast<uint16_t *>(row)[at] = to_bf16(x);
+    if (e4m3) static_cast<uint8_t *>(row)[at] = (uint8_t)pack_e4m3(x, 0.f);
+    else static_cast<uint16_t *>(row)[at] = (uint16_t)pack_bf16(x, 0.f);
 }
 
 __device__ __forceinline__ void rotate(float &a, float &b, float c, float s) {
@@ -52,19 +49,21 @@ __device__ __forceinline__ void rotate(float &a, float &b, float c, float s) {
 }
 
 // Units of a head: VEC: eight values each; otherwise the rotary pairs, then single values.
+// n = id / per_token by one multiplication (id < 2^31, see KvView).
 template <bool VEC>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, int units, float k_inv, float v_inv) {
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, int64_t t0, uint32_t all, uint32_t per_token, uint32_t mul,
+                                                          uint32_t shift, uint32_t units, float k_inv, float v_inv) {
     pdl_wait();
     pdl_trigger();
     const int D = a.c.dim, half = a.rope_dim / 2;
-    const int heads = (a.q ? a.n_heads : 0) + 2 * a.c.heads;
-    const int64_t per_token = (int64_t)heads * units, all = a.T * per_token;
-    for (int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x; id < all; id += (int64_t)gridDim.x * kThreads) {
-        const int64_t t = id / per_token;
-        int head = (int)((id - t * per_token) / units);
-        const int u = (int)(id % units);
-        const int kind = !a.q || head >= a.n_heads ? (head - (a.q ? a.n_heads : 0) < a.c.heads ? 1 : 2) : 0;
-        if (kind) head -= (a.q ? a.n_heads : 0) + (kind == 2 ? a.c.heads : 0);
+    const int q_heads = a.q ? a.n_heads : 0;
+    for (uint32_t id = blockIdx.x * kThreads + threadIdx.x; id < all; id += gridDim.x * kThreads) {
+        const uint32_t nth = (uint32_t)(((uint64_t)id * mul) >> shift), in_token = id - nth * per_token;
+        const int64_t t = t0 + nth;
+        int head = (int)(VEC ? in_token >> (31 - __clz(units)) : in_token / units);  // (VEC: units is a power of two)
+        const int u = (int)(in_token - (uint32_t)head * units);
+        const int kind = head < q_heads ? 0 : head < q_heads + a.c.heads ? 1 : 2;  // query, key, value
+        if (kind) head -= q_heads + (kind == 2 ? a.c.heads : 0);
         // ---- where the token goes
         const int seq = __ldg(a.seq + t), slot = __ldg(a.slot + t), pos = __ldg(a.pos + t);
         bool ok = seq >= 0 && seq < a.c.batch && slot >= 0 && slot < a.c.capacity &&
@@ -97,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, in
         const bool turn = kind < 2 && ok;
         const float *cs = a.rope + (int64_t)pos * a.rope_dim;
         if constexpr (VEC) {
-            float x[8];
+            alignas(16) float x[8];
             const bool in_rope = u < a.rope_dim / 8;
             const bool split = in_rope && !a.pairs;  // four values and their partners
             const int at0 = split ? 4 * u : 8 * u, at1 = split ? half + 4 * u : 8 * u + 4;
@@ -115,14 +114,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, in
                     rotate(x[4], x[5], c.z, s.z), rotate(x[6], x[7], c.w, s.w);
                 }
             }
-            float lo[4], hi[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lo[i] = ok ? x[i] * scale : 0.f;
-                hi[i] = ok ? x[4 + i] * scale : 0.f;
-            }
-            store4(dst, at0, lo, e4m3);
-            store4(dst, at1, hi, e4m3);
+            for (int i = 0; i < 8; ++i) x[i] = ok ? x[i] * scale : 0.f;
+            store4(dst, at0, x, e4m3);
+            store4(dst, at1, x + 4, e4m3);
         } else {
             if (u < half) {
                 const int i = a.pairs ? 2 * u : u, j = a.pairs ? 2 * u + 1 : u + half;
@@ -146,13 +141,23 @@ cudaError_t launch_kv_append(const DeviceInfo &di, const AppendArgs &a, cudaStre
     const bool vec = (!a.q || (al16(a.q) && a.ldq % 4 == 0 && al16(a.q_out) && a.ldqo % 8 == 0)) && al16(a.k) &&
                      a.ldk % 4 == 0 && al16(a.v) && a.ldv % 4 == 0 && a.rope_dim % 8 == 0 && (a.rope_dim == 0 || al16(a.rope));
     const int D = a.c.dim, units = vec ? D / 8 : a.rope_dim / 2 + (D - a.rope_dim);
-    const int64_t all = a.T * ((a.q ? a.n_heads : 0) + 2 * a.c.heads) * units;
-    int64_t blocks = (all + kThreads - 1) / kThreads;
-    const int64_t cap = (int64_t)di.sm_count * 32;
-    if (blocks > cap) blocks = cap;
+    const int64_t per_token = ((a.q ? a.n_heads : 0) + 2 * a.c.heads) * (int64_t)units;
+    uint32_t l = 0;
+    while (((int64_t)1 << l) < per_token) ++l;
+    const uint32_t shift = 31 + l, mul = (uint32_t)((((uint64_t)1 << shift) + per_token - 1) / per_token);
     const float k_inv = 1.0f / a.c.k_scale, v_inv = 1.0f / a.c.v_scale;
-    return launch_pdl(vec ? append_kernel<true> : append_kernel<false>, dim3((unsigned)blocks), dim3(kThreads), 0, s, dim3(1), a,
-                      units, k_inv, v_inv);
+    // tokens of a launch: fewer than 2^31 units (a call of that size takes several)
+    const int64_t most = ((int64_t)1 << 30) / per_token;
+    for (int64_t t0 = 0; t0 < a.T; t0 += most) {
+        const int64_t all = (a.T - t0 < most ? a.T - t0 : most) * per_token;
+        int64_t blocks = (all + kThreads - 1) / kThreads;
+        const int64_t cap = (int64_t)di.sm_count * 64;
+        if (blocks > cap) blocks = cap;
+        const cudaError_t e = launch_pdl(vec ? append_kernel<true> : append_kernel<false>, dim3((unsigned)blocks), dim3(kThreads), 0, s, dim3(1),
+                                         a, t0, (uint32_t)all, (uint32_t)per_token, mul, shift, (uint32_t)units, k_inv, v_inv);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace q4k
