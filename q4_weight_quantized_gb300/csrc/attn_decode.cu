@@ -43,6 +43,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -INFINITY;
 constexpr float kSlack = 8.f;       // how far (log2) a score may exceed the running maximum
 constexpr int kExtra = 2;           // places of the list after a unit's tiles
+constexpr int kWaves = 3, kLong = 48;  // see shares_of
+static_assert(kWaves * kMaxAttnResident == kMaxAttnShares, "the workspace holds two parts for each share");
 
 // 16 bytes into shared memory, of which the last 16 - bytes become zeros
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
@@ -190,17 +192,20 @@ __device__ __forceinline__ void row_range(const AttnArgs &a, int r, int tok, int
     begin = a.window > 0 ? (int)max((int64_t)0, (int64_t)end - a.window) : 0;
 }
 
-// The list's `total` places go to min(ctas, total) shares: share i is [share_begin(i),
-// share_begin(i + 1)), empty from there on.
-__device__ __forceinline__ int64_t share_begin(int64_t total, int ctas, int i) {
-    if (total <= ctas) return min((int64_t)i, total);
-    return total >> 22 ? total * i / ctas : (uint32_t)total * (uint32_t)i / (uint32_t)ctas;  // (ctas <= 2^9)
+// The list's `total` places go to a number of shares: share i is [share_begin(i), share_begin(i + 1)).
+// One for each resident CTA, so that all run at once; long lists are cut into up to kWaves times as many
+// (of kLong places at least), which start as others end and even out how fast the SMs read.
+__device__ __forceinline__ int shares_of(int64_t total, int resident) {
+    const int64_t n = min(total / kLong, (int64_t)resident * kWaves);
+    return (int)min(total, max(n, (int64_t)resident));
 }
-// The share that holds place t.
-__device__ __forceinline__ int share_of(int64_t total, int ctas, int64_t t) {
-    if (total <= ctas) return (int)t;
-    // the largest i with floor(total i / ctas) <= t
-    return total >> 22 ? (int)(((t + 1) * ctas - 1) / total) : (int)(((uint32_t)(t + 1) * (uint32_t)ctas - 1) / (uint32_t)total);
+__device__ __forceinline__ int64_t share_begin(int64_t total, int shares, int i) {
+    if (i >= shares) return total;
+    return total >> 20 ? total * i / shares : (uint32_t)total * (uint32_t)i / (uint32_t)shares;  // (shares <= 2^11)
+}
+// The share that holds place t: the largest i with floor(total i / shares) <= t.
+__device__ __forceinline__ int share_of(int64_t total, int shares, int64_t t) {
+    return total >> 20 ? (int)(((t + 1) * shares - 1) / total) : (int)(((uint32_t)(t + 1) * (uint32_t)shares - 1) / (uint32_t)total);
 }
 
 // Where this CTA's share begins (left = 0: it is empty); CTA 0 also writes the places before
@@ -233,7 +238,8 @@ __device__ __forceinline__ void share_of_list(const AttnArgs &a, Pos &start, int
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
-    const int64_t t0 = share_begin(total, a.ctas, blockIdx.x), t1 = share_begin(total, a.ctas, blockIdx.x + 1);
+    const int shares = shares_of(total, a.resident);
+    const int64_t t0 = share_begin(total, shares, blockIdx.x), t1 = share_begin(total, shares, blockIdx.x + 1);
     if (t0 < t1 && before <= t0 && t0 < before + sum) {
         // this thread's sequences hold the share's first place
         Pos p;
@@ -855,8 +861,9 @@ __device__ __forceinline__ Parts parts_of(const AttnArgs &a, int b, int hr) {
     if (!r.empty) {
         const int64_t all = p1 - p0;
         const int64_t n = all >> 31 ? all / a.unit_heads : (uint32_t)all / (uint32_t)a.unit_heads, t = p0 + hr * n;
-        r.first = share_of(total, a.ctas, t);
-        r.last = share_of(total, a.ctas, t + n - kExtra - 1);
+        const int shares = shares_of(total, a.resident);
+        r.first = share_of(total, shares, t);
+        r.last = share_of(total, shares, t + n - kExtra - 1);
         r.whole = r.first == r.last;
     }
     return r;
@@ -886,105 +893,104 @@ __device__ __forceinline__ float2 join_ml(const AttnArgs &a, const Parts &p, int
     return make_float2(top, l);
 }
 
-// Units in several parts, and zeros for units without slots.  A block joins 16 values of the
-// 8 rows of an octet (one fragment: 32 lanes of float4), its warps taking every fourth part.
-__global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a) {
+// Units in several parts, and zeros for units without slots: `blocks` blocks a unit.  A warp quartet joins 16
+// values of the 8 rows of an octet at a time (one fragment: 32 lanes of float4), each warp taking every fourth
+// part.
+__global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a, int blocks) {
     __shared__ float4 sm[kWarps][32];
-    __shared__ float2 ml[kMaxAttnCtas][8];  // (m, l) of a part's rows, then (2^(m - M), -)
-    __shared__ float red[kWarps][8], sm_l[kWarps][8];
+    __shared__ float sm_m[kWarps][8], sm_l[kWarps][8];
     pdl_wait();
     pdl_trigger();
-    const int D = a.c.dim, ks = D / 16, octets = a.tile_rows / 8;
+    const int D = a.c.dim, ks = D / 16, fragments = a.tile_rows / 8 * ks;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
-    const uint32_t unit = blockIdx.x / (uint32_t)(ks * octets), in_unit = blockIdx.x - unit * (uint32_t)(ks * octets);
-    const int n = (int)in_unit / ks, i = (int)in_unit - n * ks;
+    const uint32_t unit = blockIdx.x / (uint32_t)blocks, block = blockIdx.x - unit * (uint32_t)blocks;
     const int b = (int)(unit / (uint32_t)a.unit_heads), hr = (int)(unit - (uint32_t)b * (uint32_t)a.unit_heads);
     const Parts p = parts_of(a, b, hr);
     if (p.whole) return;
-    const int head = hr / a.row_tiles;
-    const int r0 = hr % a.row_tiles * a.tile_rows + n * 8;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l[2] = {0.f, 0.f};
-    if (!p.empty) {
-        // (m, l) of the 8 rows of every part: thread x holds row x % 8 of every 16th part
-        const int parts = p.last - p.first + 1;
-        float top = kNone;
-        for (int x = tid; x < parts * 8; x += kThreads) {
-            const float2 t = *reinterpret_cast<const float2 *>(part_at(a, p, p.first + x / 8) + 2 * (n * 8 + x % 8));
-            ml[x / 8][x % 8] = t;
-            top = fmaxf(top, t.x);
-        }
-        // the fragments of this warp's parts are on their way meanwhile
-        constexpr int kAhead = 8;
-        float4 t[kAhead];
-        const int64_t at = 2 * a.tile_rows + ((n * ks + i) * 32 + lane) * 4;
+    const int head = hr / a.row_tiles, parts = p.last - p.first + 1;
+    for (int fragment = (int)block; fragment < fragments; fragment += blocks) {
+        const int n = fragment / ks, i = fragment - n * ks, r0 = (hr - head * a.row_tiles) * a.tile_rows + n * 8;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l[2] = {0.f, 0.f};
+        if (!p.empty) {
+            // the fragments of this warp's first parts are on their way during the join of (m, l)
+            constexpr int kAhead = 8;
+            float4 t[kAhead];
+            const int64_t at = 2 * a.tile_rows + (fragment * 32 + lane) * 4, at_ml = 2 * (n * 8 + c4 * 2);
 #pragma unroll
-        for (int y = 0; y < kAhead; ++y)
-            if (warp + y * kWarps < parts)
-                t[y] = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + warp + y * kWarps) + at);
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-        if (lane < 8) red[warp][lane] = top;
-        __syncthreads();
+            for (int y = 0; y < kAhead; ++y)
+                if (warp + y * kWarps < parts) t[y] = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + warp + y * kWarps) + at);
+            // thread x: row x % 8 of every 16th part
+            float top = kNone, sum = 0.f;
+            for (int x = tid; x < parts * 8; x += kThreads) {
+                const float2 ml = *reinterpret_cast<const float2 *>(part_at(a, p, p.first + x / 8) + 2 * (n * 8 + x % 8));
+                if (ml.x == kNone) continue;
+                const float m = fmaxf(top, ml.x);
+                sum = sum * ex2_approx(top - m) + ml.y * ex2_approx(ml.x - m);
+                top = m;
+            }
+            float m = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+            sum = top == kNone ? 0.f : sum * ex2_approx(top - m);
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+            __syncthreads();  // (the fragment before has been read)
+            if (lane < 8) sm_m[warp][lane] = m, sm_l[warp][lane] = sum;
+            __syncthreads();
+            float mt[2];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red[w][lane & 7]);
-        float sum = 0.f;
-        for (int x = tid; x < parts * 8; x += kThreads) {
-            const float2 t = ml[x / 8][x % 8];
-            const float f = t.x == kNone ? 0.f : ex2_approx(t.x - top);
-            ml[x / 8][x % 8].x = f;
-            sum = fmaf(f, t.y, sum);
-        }
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
-        if (lane < 8) sm_l[warp][lane] = sum;
-        __syncthreads();
+            for (int e = 0; e < 2; ++e) {
+                mt[e] = kNone;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+                for (int w = 0; w < kWarps; ++w) mt[e] = fmaxf(mt[e], sm_m[w][c4 * 2 + e]);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) l[e] += sm_l[w][c4 * 2 + e];
-        for (int x0 = warp; x0 < parts; x0 += kAhead * kWarps) {
+                for (int w = 0; w < kWarps; ++w)
+                    if (sm_m[w][c4 * 2 + e] != kNone) l[e] += sm_l[w][c4 * 2 + e] * ex2_approx(sm_m[w][c4 * 2 + e] - mt[e]);
+            }
+            for (int x0 = warp; x0 < parts; x0 += kAhead * kWarps) {
 #pragma unroll
-            for (int y = 0; y < kAhead; ++y) {
-                const int x = x0 + y * kWarps;
-                if (x < parts) {
-                    const float f0 = ml[x][c4 * 2].x, f1 = ml[x][c4 * 2 + 1].x;
-                    v.x = fmaf(f0, t[y].x, v.x), v.y = fmaf(f1, t[y].y, v.y);
-                    v.z = fmaf(f0, t[y].z, v.z), v.w = fmaf(f1, t[y].w, v.w);
-                    if (x + kAhead * kWarps < parts)
-                        t[y] = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + x + kAhead * kWarps) + at);
+                for (int y = 0; y < kAhead; ++y) {
+                    const int x = x0 + y * kWarps;
+                    if (x < parts) {
+                        const float4 ml = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + x) + at_ml);
+                        const float f0 = ml.x == kNone ? 0.f : ex2_approx(ml.x - mt[0]), f1 = ml.z == kNone ? 0.f : ex2_approx(ml.z - mt[1]);
+                        v.x = fmaf(f0, t[y].x, v.x), v.y = fmaf(f1, t[y].y, v.y);
+                        v.z = fmaf(f0, t[y].z, v.z), v.w = fmaf(f1, t[y].w, v.w);
+                        if (x + kAhead * kWarps < parts)
+                            t[y] = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + x + kAhead * kWarps) + at);
+                    }
                 }
             }
-        }
-        sm[warp][lane] = v;
-        __syncthreads();
-        if (warp > 0) return;
+            sm[warp][lane] = v;
+            __syncthreads();
+            if (warp > 0) continue;
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            const float4 x = sm[w][lane];
-            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            for (int w = 1; w < kWarps; ++w) {
+                const float4 x = sm[w][lane];
+                v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            }
+        } else if (warp > 0) {
+            continue;
         }
-    } else if (warp > 0) {
-        return;
-    }
-    const float lo[2] = {v.x, v.y}, hi[2] = {v.z, v.w};
+        const float lo[2] = {v.x, v.y}, hi[2] = {v.z, v.w};
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int r = r0 + c4 * 2 + e;
-        if (r >= a.rows) continue;
-        uint16_t *out = a.o + ((int64_t)b * a.n_q + r / a.group) * a.ldo + (int64_t)(head * a.group + r % a.group) * D + i * 16;
-        const float inv = l[e] > 0.f || l[e] != l[e] ? a.v_scale / l[e] : 0.f;
-        const uint32_t t = pack_bf16(lo[e] * inv, hi[e] * inv);
-        if (a.c.e4m3) {
-            *reinterpret_cast<uint32_t *>(out + 2 * g) = t;
-        } else {
-            out[g] = (uint16_t)t;
-            out[8 + g] = (uint16_t)(t >> 16);
+        for (int e = 0; e < 2; ++e) {
+            const int r = r0 + c4 * 2 + e;
+            if (r >= a.rows) continue;
+            uint16_t *out = a.o + ((int64_t)b * a.n_q + r / a.group) * a.ldo + (int64_t)(head * a.group + r % a.group) * D + i * 16;
+            const float inv = l[e] > 0.f || l[e] != l[e] ? a.v_scale / l[e] : 0.f;
+            const uint32_t t = pack_bf16(lo[e] * inv, hi[e] * inv);
+            if (a.c.e4m3) {
+                *reinterpret_cast<uint32_t *>(out + 2 * g) = t;
+            } else {
+                out[g] = (uint16_t)t;
+                out[8 + g] = (uint16_t)(t >> 16);
+            }
         }
     }
 }
 
-constexpr int kChunk = 1024;  // slots of a block that adds up weights
+constexpr int kChunk = 2048;  // slots of a block that adds up weights
 
 // A chunk of slots of one KV head's weights: weights <- decay * weights + sum of the rows'
 // 2^(s - m) / l.
@@ -1014,32 +1020,34 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnArgs a, int c
     __syncthreads();
     float *w = a.weights + bh * a.ld_weights;
     const float *z = a.logits + bh * a.rows * a.ld_logits;
-    constexpr int kAt = kChunk / kThreads;  // slots of a thread
-    float sum[kAt];
+    constexpr int kAt = 4, kRowsAhead = 4;  // slots of a thread at a time; rows whose scores are on their way at once
+    for (int j0 = lo + threadIdx.x; j0 < hi; j0 += kAt * kThreads) {
+        float sum[kAt], old[kAt];
 #pragma unroll
-    for (int x = 0; x < kAt; ++x) sum[x] = 0.f;
-    constexpr int kRowsAhead = 4;
-    for (int r0 = 0; r0 < a.rows; r0 += kRowsAhead) {
-        float s[kRowsAhead][kAt];  // all on their way before the first is used
-#pragma unroll
-        for (int y = 0; y < kRowsAhead; ++y)
-#pragma unroll
-            for (int x = 0; x < kAt; ++x) {
-                const int j = lo + x * kThreads + threadIdx.x;
-                s[y][x] = r0 + y < a.rows && j >= begin && j < hi ? __ldg(z + (r0 + y) * a.ld_logits + j) : kNone;
-            }
-#pragma unroll
-        for (int y = 0; y < kRowsAhead; ++y) {
-            if (r0 + y >= a.rows) break;
-            const float m = sm_m[r0 + y], f = sm_r[r0 + y];
-#pragma unroll
-            for (int x = 0; x < kAt; ++x) sum[x] = s[y][x] == kNone ? sum[x] : fmaf(ex2_approx(s[y][x] - m), f, sum[x]);
+        for (int x = 0; x < kAt; ++x) {
+            sum[x] = 0.f;
+            if (j0 + x * kThreads < hi) old[x] = w[j0 + x * kThreads];
         }
-    }
+        for (int r0 = 0; r0 < a.rows; r0 += kRowsAhead) {
+            float s[kRowsAhead][kAt];
 #pragma unroll
-    for (int x = 0; x < kAt; ++x) {
-        const int j = lo + x * kThreads + threadIdx.x;
-        if (j < hi) w[j] = fmaf(w[j], a.decay, sum[x]);
+            for (int y = 0; y < kRowsAhead; ++y)
+#pragma unroll
+                for (int x = 0; x < kAt; ++x) {
+                    const int j = j0 + x * kThreads;
+                    s[y][x] = r0 + y < a.rows && j >= begin && j < hi ? __ldg(z + (r0 + y) * a.ld_logits + j) : kNone;
+                }
+#pragma unroll
+            for (int y = 0; y < kRowsAhead; ++y) {
+                if (r0 + y >= a.rows) break;
+                const float m = sm_m[r0 + y], f = sm_r[r0 + y];
+#pragma unroll
+                for (int x = 0; x < kAt; ++x) sum[x] = s[y][x] == kNone ? sum[x] : fmaf(ex2_approx(s[y][x] - m), f, sum[x]);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kAt; ++x)
+            if (j0 + x * kThreads < hi) w[j0 + x * kThreads] = fmaf(old[x], a.decay, sum[x]);
     }
 }
 
@@ -1050,12 +1058,15 @@ cudaError_t launch(AttnArgs &a, const DeviceInfo &di, cudaStream_t s) {
     cudaError_t e = ensure_smem((const void *)kern, C::SMEM);
     if (e != cudaSuccess) return e;
     // as many CTAs as are resident at once
-    a.ctas = di.sm_count * C::PER_SM < kMaxAttnCtas ? di.sm_count * C::PER_SM : kMaxAttnCtas;
+    a.resident = di.sm_count * C::PER_SM < kMaxAttnResident ? di.sm_count * C::PER_SM : kMaxAttnResident;
     a.part_floats = part_floats(D, NR);
-    e = launch_pdl(kern, dim3(a.ctas), dim3(kThreads), C::SMEM, s, dim3(1), a);
+    e = launch_pdl(kern, dim3(a.resident * kWaves), dim3(kThreads), C::SMEM, s, dim3(1), a);
     if (e != cudaSuccess) return e;
-    const int64_t units = (int64_t)a.c.batch * a.unit_heads;
-    e = launch_pdl(join_kernel, dim3((unsigned)(units * NR * (D / 16))), dim3(kThreads), 0, s, dim3(1), a);
+    // a block a fragment where units are few; fewer where most units are whole and their blocks only find that out
+    const int64_t units = (int64_t)a.c.batch * a.unit_heads, fragments = NR * (D / 16);
+    int64_t blocks = (4 * di.sm_count + units - 1) / units;
+    if (blocks > fragments) blocks = fragments;
+    e = launch_pdl(join_kernel, dim3((unsigned)(units * blocks)), dim3(kThreads), 0, s, dim3(1), a, (int)blocks);
     if (e != cudaSuccess || !a.weights) return e;
     const int chunks = (a.cap + kChunk - 1) / kChunk;
     return launch_pdl(weigh_kernel, dim3((unsigned)((int64_t)a.c.batch * a.c.heads * chunks)), dim3(kThreads), 0, s, dim3(1), a,

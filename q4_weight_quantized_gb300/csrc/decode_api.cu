@@ -90,7 +90,7 @@ AttnLayout attn_layout(const q4k_kv_cache *c, int32_t n_heads, int32_t n_q, int6
     AttnLayout l;
     size_t at = 0;
     l.parts = at;
-    at += align256((size_t)2 * kMaxAttnCtas * attn_part_floats(c->head_dim, (int)tile) * 4);
+    at += align256((size_t)2 * kMaxAttnShares * attn_part_floats(c->head_dim, (int)tile) * 4);
     l.unit_ml = at;
     if (ld_weights > 0) at += align256(units * tile * sizeof(float2));
     l.prefix = at;

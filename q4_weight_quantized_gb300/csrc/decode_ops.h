@@ -8,7 +8,8 @@
 
 namespace q4k {
 
-constexpr int kMaxAttnCtas = 512;   // shares of an attention call (the workspace holds two parts for each)
+constexpr int kMaxAttnResident = 512;  // CTAs of an attention call that run at once, at most
+constexpr int kMaxAttnShares = 3 * kMaxAttnResident;  // shares of its work (the workspace holds two parts for each)
 constexpr int kMaxAttnRows = 1024;  // query rows of one KV head: n_q * group
 
 struct AttnArgs {
@@ -30,11 +31,11 @@ struct AttnArgs {
     // workspace
     float *logits;                   // [batch * heads][rows][ld_logits], with weights only
     int64_t ld_logits;
-    float *parts;                    // [2 * ctas] parts
+    float *parts;                    // [2 * shares] parts
     int32_t part_floats;
     float2 *unit_ml;                 // [batch * unit_heads][tile_rows]: (m, l) of units finished by one CTA; with weights only
     int64_t *prefix;                 // [batch + 1]: places of the list before each sequence
-    int32_t ctas;
+    int32_t resident;
 };
 int attn_tile_rows(int D, int rows);
 int attn_part_floats(int D, int tile_rows);
