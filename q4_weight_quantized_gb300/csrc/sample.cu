@@ -577,7 +577,7 @@ struct Settings {
 template <typename R>
 __device__ __forceinline__ void finish_few(R &r, const SampleArgs &a, int64_t m, const Settings &set, int bin, u64 whole) {
     Shared &s = r.s;
-    const int n = r.gather(0.f, fminf(r.span, ldexpf((float)(bin + 1), -r.per_octave)), 0, 0xFFFFFFFFu);
+    const int n = min(r.gather(0.f, fminf(r.span, ldexpf((float)(bin + 1), -r.per_octave)), 0, 0xFFFFFFFFu), kFew);
     if (r.rank != 0) return;  // (no CTA touches another's memory from here on)
     const u64 least = part_of(weight_of(0.f), set.m_share);
     // each token's rank, and the weight before it; a thread has at most one token's
