@@ -213,14 +213,14 @@ __device__ __forceinline__ int share_of(int64_t total, int shares, int64_t t) {
 template <int CT>
 __device__ __forceinline__ void share_of_list(const AttnArgs &a, Pos &start, int64_t *scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.c.batch + kThreads - 1) / kThreads;
+    const int per = (a.c.batch + kThreads - 1) / kThreads;  // sequences of a thread
     const int lo = min(tid * per, a.c.batch), hi = min(lo + per, a.c.batch);
     int64_t sum = 0;
-    for (int b = lo; b < hi; ++b) {
-        int begin, len;
-        if (blockIdx.x == 0 && __ldg(a.seq_lens + b) > a.cap) atomicOr(a.c.status, kDevIndex);
-        seq_range(a, b, begin, len);
-        sum += places<CT>(len - begin);
+    Pos p;  // the last of them; with one a thread, the only one
+    p.begin = p.end = 0;
+    for (p.b = lo; p.b < hi; ++p.b) {
+        seq_range(a, p.b, p.begin, p.end);
+        sum += places<CT>(p.end - p.begin);
     }
     sum *= a.unit_heads;
     int64_t inc = sum;
@@ -242,17 +242,26 @@ __device__ __forceinline__ void share_of_list(const AttnArgs &a, Pos &start, int
     const int64_t t0 = share_begin(total, shares, blockIdx.x), t1 = share_begin(total, shares, blockIdx.x + 1);
     if (t0 < t1 && before <= t0 && t0 < before + sum) {
         // this thread's sequences hold the share's first place
-        Pos p;
         int64_t at = before;
-        int n = 0;
-        for (p.b = lo;; ++p.b) {
-            seq_range(a, p.b, p.begin, p.end);
-            n = places<CT>(p.end - p.begin);
-            if (t0 < at + (int64_t)n * a.unit_heads) break;
-            at += (int64_t)n * a.unit_heads;
+        int n = places<CT>(p.end - p.begin);
+        p.b = lo;
+        if (per > 1)
+            for (;; ++p.b) {
+                seq_range(a, p.b, p.begin, p.end);
+                n = places<CT>(p.end - p.begin);
+                if (t0 < at + (int64_t)n * a.unit_heads) break;
+                at += (int64_t)n * a.unit_heads;
+            }
+        const int64_t in = t0 - at;
+        int hr;
+        if (in < 1 << 24) {
+            // (the quotient of two floats is off by one at most; whole-number division takes far longer)
+            hr = (int)__fdividef((float)in, (float)n);
+            const int rest = (int)in - hr * n;
+            hr += rest >= n ? 1 : rest < 0 ? -1 : 0;
+        } else {
+            hr = (int)(in / n);
         }
-        const int64_t in = t0 - at;  // (64-bit division is long: only where it must be)
-        const int hr = in >> 31 ? (int)(in / n) : (int)((uint32_t)in / (uint32_t)n);
         p.tile = (int)(in - (int64_t)hr * n);
         p.head = a.row_tiles == 1 ? hr : hr / a.row_tiles;
         p.rt = hr - p.head * a.row_tiles;
@@ -264,17 +273,18 @@ __device__ __forceinline__ void share_of_list(const AttnArgs &a, Pos &start, int
         }
         start = p;
     }
+    __syncthreads();
     if (blockIdx.x == 0) {
         int64_t at = before;
         for (int b = lo; b < hi; ++b) {
             int begin, len;
             a.prefix[b] = at;
+            if (__ldg(a.seq_lens + b) > a.cap) atomicOr(a.c.status, kDevIndex);
             seq_range(a, b, begin, len);
             at += (int64_t)places<CT>(len - begin) * a.unit_heads;
         }
         if (tid == 0) a.prefix[a.c.batch] = total;
     }
-    __syncthreads();
 }
 
 template <typename C>
@@ -871,34 +881,14 @@ __device__ __forceinline__ Parts parts_of(const AttnArgs &a, int b, int hr) {
 __device__ __forceinline__ const float *part_at(const AttnArgs &a, const Parts &p, int i) {
     return a.parts + (int64_t)(2 * i + (i == p.first)) * a.part_floats;
 }
-// (m, l) of one row over all its parts; every lane of the warp calls it and gets it.
-__device__ __forceinline__ float2 join_ml(const AttnArgs &a, const Parts &p, int64_t unit, int row) {
-    if (p.empty) return make_float2(kNone, 0.f);
-    if (p.whole) return a.unit_ml[unit * a.tile_rows + row];
-    const int lane = threadIdx.x & 31;
-    float m = kNone, l = 0.f;
-    for (int i = p.first + lane; i <= p.last; i += 32) {
-        const float2 ml = *reinterpret_cast<const float2 *>(part_at(a, p, i) + 2 * row);
-        if (ml.x == kNone) continue;
-        const float top = fmaxf(m, ml.x);
-        l = l * ex2_approx(m - top) + ml.y * ex2_approx(ml.x - top);
-        m = top;
-    }
-    float top = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if (m != kNone) l *= ex2_approx(m - top);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-    return make_float2(top, l);
-}
-
-// Units in several parts, and zeros for units without slots: `blocks` blocks a unit.  A warp quartet joins 16
-// values of the 8 rows of an octet at a time (one fragment: 32 lanes of float4), each warp taking every fourth
-// part.
-__global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a, int blocks) {
-    __shared__ float4 sm[kWarps][32];
-    __shared__ float sm_m[kWarps][8], sm_l[kWarps][8];
+// Units in several parts, and zeros for units without slots: `blocks` blocks a unit.  A block joins 16 values
+// of the 8 rows of an octet at a time (one fragment: 32 lanes of float4), its warps taking turns at the parts.
+// With weights it also leaves the unit's (m, l), as the CTAs that finished whole units did.
+constexpr int kJoinWarps = 16;  // of a block, at most
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a, int blocks) {
+    __shared__ float4 sm[kJoinWarps][32];
+    __shared__ float sm_m[kJoinWarps][8], sm_l[kJoinWarps][8];
+    const int warps = blockDim.x >> 5;
     pdl_wait();
     pdl_trigger();
     const int D = a.c.dim, ks = D / 16, fragments = a.tile_rows / 8 * ks;
@@ -914,15 +904,15 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a, int bl
         float l[2] = {0.f, 0.f};
         if (!p.empty) {
             // the fragments of this warp's first parts are on their way during the join of (m, l)
-            constexpr int kAhead = 8;
+            constexpr int kAhead = 4;
             float4 t[kAhead];
             const int64_t at = 2 * a.tile_rows + (fragment * 32 + lane) * 4, at_ml = 2 * (n * 8 + c4 * 2);
 #pragma unroll
             for (int y = 0; y < kAhead; ++y)
-                if (warp + y * kWarps < parts) t[y] = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + warp + y * kWarps) + at);
-            // thread x: row x % 8 of every 16th part
+                if (warp + y * warps < parts) t[y] = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + warp + y * warps) + at);
+            // thread x: row x % 8 of some of the parts
             float top = kNone, sum = 0.f;
-            for (int x = tid; x < parts * 8; x += kThreads) {
+            for (int x = tid; x < parts * 8; x += blockDim.x) {
                 const float2 ml = *reinterpret_cast<const float2 *>(part_at(a, p, p.first + x / 8) + 2 * (n * 8 + x % 8));
                 if (ml.x == kNone) continue;
                 const float m = fmaxf(top, ml.x);
@@ -941,31 +931,31 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a, int bl
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 mt[e] = kNone;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) mt[e] = fmaxf(mt[e], sm_m[w][c4 * 2 + e]);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
+                for (int w = 0; w < warps; ++w) mt[e] = fmaxf(mt[e], sm_m[w][c4 * 2 + e]);
+                for (int w = 0; w < warps; ++w)
                     if (sm_m[w][c4 * 2 + e] != kNone) l[e] += sm_l[w][c4 * 2 + e] * ex2_approx(sm_m[w][c4 * 2 + e] - mt[e]);
             }
-            for (int x0 = warp; x0 < parts; x0 += kAhead * kWarps) {
+            for (int x0 = warp; x0 < parts; x0 += kAhead * warps) {
 #pragma unroll
                 for (int y = 0; y < kAhead; ++y) {
-                    const int x = x0 + y * kWarps;
+                    const int x = x0 + y * warps;
                     if (x < parts) {
                         const float4 ml = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + x) + at_ml);
                         const float f0 = ml.x == kNone ? 0.f : ex2_approx(ml.x - mt[0]), f1 = ml.z == kNone ? 0.f : ex2_approx(ml.z - mt[1]);
                         v.x = fmaf(f0, t[y].x, v.x), v.y = fmaf(f1, t[y].y, v.y);
                         v.z = fmaf(f0, t[y].z, v.z), v.w = fmaf(f1, t[y].w, v.w);
-                        if (x + kAhead * kWarps < parts)
-                            t[y] = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + x + kAhead * kWarps) + at);
+                        if (x + kAhead * warps < parts)
+                            t[y] = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + x + kAhead * warps) + at);
                     }
                 }
             }
+            if (a.unit_ml && i == 0 && warp == 0 && g == 0)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) a.unit_ml[(int64_t)unit * a.tile_rows + n * 8 + c4 * 2 + e] = make_float2(mt[e], l[e]);
             sm[warp][lane] = v;
             __syncthreads();
             if (warp > 0) continue;
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
+            for (int w = 1; w < warps; ++w) {
                 const float4 x = sm[w][lane];
                 v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
             }
@@ -990,32 +980,24 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a, int bl
     }
 }
 
-constexpr int kChunk = 2048;  // slots of a block that adds up weights
-
 // A chunk of slots of one KV head's weights: weights <- decay * weights + sum of the rows'
 // 2^(s - m) / l.
-__global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnArgs a, int chunks) {
+__global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnArgs a, int chunks, int chunk) {
     __shared__ float sm_m[kMaxAttnRows], sm_r[kMaxAttnRows];
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t bh = blockIdx.x / chunks;
     const int b = (int)(bh / a.c.heads), h = (int)(bh - (int64_t)b * a.c.heads);
     int begin, len;
     seq_range(a, b, begin, len);
-    const int lo = (int)(blockIdx.x % chunks) * kChunk, hi = min(lo + kChunk, len);
+    const int lo = (int)(blockIdx.x - bh * chunks) * chunk, hi = min(lo + chunk, len);
     if (lo >= len) return;
     if (hi > begin)
-        for (int rt = 0; rt < a.row_tiles; ++rt) {
-            const int64_t unit = (int64_t)b * a.unit_heads + h * a.row_tiles + rt;
-            const Parts p = parts_of(a, b, h * a.row_tiles + rt);
-            for (int row = warp; row < a.tile_rows && rt * a.tile_rows + row < a.rows; row += kWarps) {
-                const float2 ml = join_ml(a, p, unit, row);
-                if (lane == 0) {
-                    sm_m[rt * a.tile_rows + row] = ml.x == kNone ? 0.f : ml.x;
-                    sm_r[rt * a.tile_rows + row] = ml.y > 0.f || ml.y != ml.y ? ex2_approx(lift(a.c.e4m3 != 0)) / ml.y : 0.f;
-                }
-            }
+        for (int r = threadIdx.x; r < a.rows; r += kThreads) {
+            const int rt = r / a.tile_rows;
+            const float2 ml = a.unit_ml[((int64_t)b * a.unit_heads + h * a.row_tiles + rt) * a.tile_rows + r - rt * a.tile_rows];
+            sm_m[r] = ml.x == kNone ? 0.f : ml.x;
+            sm_r[r] = ml.y > 0.f || ml.y != ml.y ? ex2_approx(lift(a.c.e4m3 != 0)) / ml.y : 0.f;
         }
     __syncthreads();
     float *w = a.weights + bh * a.ld_weights;
@@ -1060,17 +1042,28 @@ cudaError_t launch(AttnArgs &a, const DeviceInfo &di, cudaStream_t s) {
     // as many CTAs as are resident at once
     a.resident = di.sm_count * C::PER_SM < kMaxAttnResident ? di.sm_count * C::PER_SM : kMaxAttnResident;
     a.part_floats = part_floats(D, NR);
-    e = launch_pdl(kern, dim3(a.resident * kWaves), dim3(kThreads), C::SMEM, s, dim3(1), a);
+    const int64_t units = (int64_t)a.c.batch * a.unit_heads;
+    // no more CTAs than the list has places, were every length the largest
+    int64_t slots = a.cap;
+    if (a.window > 0 && a.window + a.n_q < slots) slots = a.window + a.n_q;
+    const int64_t most = units * ((slots + C::CT - 1) / C::CT + kExtra);
+    const int64_t ctas = most < (int64_t)a.resident * kWaves ? most : (int64_t)a.resident * kWaves;
+    e = launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), C::SMEM, s, dim3(1), a);
     if (e != cudaSuccess) return e;
     // a block a fragment where units are few; fewer where most units are whole and their blocks only find that out
-    const int64_t units = (int64_t)a.c.batch * a.unit_heads, fragments = NR * (D / 16);
-    int64_t blocks = (4 * di.sm_count + units - 1) / units;
+    const int64_t fragments = NR * (D / 16);
+    int64_t blocks = (16 * di.sm_count + units - 1) / units;
     if (blocks > fragments) blocks = fragments;
-    e = launch_pdl(join_kernel, dim3((unsigned)(units * blocks)), dim3(kThreads), 0, s, dim3(1), a, (int)blocks);
+    // a few units may be in hundreds of parts each
+    const int join_threads = units * 64 <= a.resident ? kJoinWarps * 32 : kThreads;
+    e = launch_pdl(join_kernel, dim3((unsigned)(units * blocks)), dim3(join_threads), 0, s, dim3(1), a, (int)blocks);
     if (e != cudaSuccess || !a.weights) return e;
-    const int chunks = (a.cap + kChunk - 1) / kChunk;
-    return launch_pdl(weigh_kernel, dim3((unsigned)((int64_t)a.c.batch * a.c.heads * chunks)), dim3(kThreads), 0, s, dim3(1), a,
-                      chunks);
+    // chunks of 2048 slots, which make the start of a block little work beside the rest, unless that leaves SMs idle
+    const int64_t heads = (int64_t)a.c.batch * a.c.heads;
+    int chunk = 2048;
+    while (chunk > 512 && heads * ((a.cap + chunk - 1) / chunk) < 4 * di.sm_count) chunk /= 2;
+    const int chunks = (a.cap + chunk - 1) / chunk;
+    return launch_pdl(weigh_kernel, dim3((unsigned)(heads * chunks)), dim3(kThreads), 0, s, dim3(1), a, chunks, chunk);
 }
 
 template <int D, bool E4M3>

@@ -191,7 +191,7 @@ q4k_status q4k_attn_decode(const q4k_kv_cache *cache, const int32_t *seq_lens, c
     a.row_tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
     a.unit_heads = cache->n_kv_heads * a.row_tiles;
     a.cap = weights && ld_weights < a.c.capacity ? (int32_t)ld_weights : a.c.capacity;
-    a.window = window;
+    a.window = window < kInt31 ? window : 0;  // no sequence is that long
     a.scale = scale * cache->k_scale;
     a.softcap = softcap;
     a.v_scale = cache->v_scale;

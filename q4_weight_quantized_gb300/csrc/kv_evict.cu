@@ -24,7 +24,8 @@ namespace q4k {
 namespace {
 
 constexpr int kSmall = 4096;    // slots up to which 256 threads do
-constexpr int kCached = 20480;  // slots whose keys fit beside the histogram with two CTAs on an SM
+constexpr int kHeld = 20480;    // slots that 1024 threads hold in registers, and whose keys leave room for two CTAs
+constexpr int kCached = 49152;  // slots whose keys fit in shared memory
 constexpr int kFew = 128;       // slots that are ranked against each other
 constexpr int kMoveThreads = 256;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
@@ -65,13 +66,14 @@ struct Block {
     }
 };
 
-// CACHED: keys and protection bits lie in shared memory; otherwise both are formed
-// again from the arrays on every pass.
-template <int THREADS, bool CACHED>
+// KEYS: the slots whose keys and protection bits lie in shared memory; 0: both are formed again from the
+// arrays on every pass.  HELD: a thread holds slots tid, tid + THREADS, ... in registers, too, loaded before
+// anything waits for one.
+template <int THREADS, int KEYS, bool HELD>
 __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
     using B = Block<THREADS>;
     constexpr int BINS = 2 * THREADS, LOG_BINS = THREADS == 1024 ? 11 : 9;
-    constexpr int KEYS = CACHED ? (THREADS == 1024 ? kCached : kSmall) : 0;
+    constexpr bool CACHED = KEYS > 0;
     static_assert(BINS == 1 << LOG_BINS, "two bins a thread");
     extern __shared__ __align__(16) uint32_t dyn[];
     __shared__ uint32_t hist[BINS];
@@ -99,13 +101,12 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
         return;
     }
     // ---- newest position (as offset binary, so that the unsigned maximum serves), and the keys; what
-    // stays below keep goes over at once, the holes among it are overwritten at the end.  CACHED: a
-    // thread holds slots tid, tid + THREADS, ... in registers, loaded before anything waits for one.
-    constexpr int PER = CACHED ? KEYS / THREADS : 1;
+    // stays below keep goes over at once, the holes among it are overwritten at the end
+    constexpr int PER = HELD ? KEYS / THREADS : 1;
     const bool copy_w = w_out != w, copy_p = p_out != p;
     uint32_t top = 0, mine[PER];
     int32_t pos[PER];
-    if constexpr (CACHED) {
+    if constexpr (HELD) {
         float wj[PER];
 #pragma unroll
         for (int x = 0; x < PER; ++x) {
@@ -124,11 +125,23 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
             if (copy_p && j < keep) p_out[j] = pos[x];
         }
     } else {
-        for (int j = tid; j < n; j += THREADS) {
-            const int32_t pj = p[j];
-            top = max(top, (uint32_t)pj ^ 0x80000000u);
-            if (copy_w && j < keep) w_out[j] = w[j];
-            if (copy_p && j < keep) p_out[j] = pj;
+        constexpr int kAhead = 8;  // loads before the first store
+        for (int j0 = tid; j0 < n; j0 += kAhead * THREADS) {
+            int32_t pj[kAhead];
+            float wj[kAhead];
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                const int j = min(j0 + x * THREADS, n - 1);
+                pj[x] = p[j], wj[x] = w[j];
+            }
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                const int j = j0 + x * THREADS;
+                top = max(top, (uint32_t)pj[x] ^ 0x80000000u);
+                if (CACHED && j < n) keys[j] = key_of(wj[x]);
+                if (copy_w && j < keep) w_out[j] = wj[x];
+                if (copy_p && j < keep) p_out[j] = pj[x];
+            }
         }
     }
     top = __reduce_max_sync(kFull, top);
@@ -145,7 +158,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
         low[0] = prot ? low[0] : min(low[0], k), high[0] = prot ? high[0] : max(high[0], k);
         low[1] = prot ? min(low[1], k) : low[1], high[1] = prot ? max(high[1], k) : high[1];
     };
-    if constexpr (CACHED) {
+    if constexpr (HELD) {
 #pragma unroll
         for (int x = 0; x < PER; ++x) {
             if (x * THREADS >= n) break;
@@ -157,11 +170,20 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
             if (j < n) of_either(mine[x], prot);
         }
     } else {
-        for (int j = tid; j < n; j += THREADS) of_either(key_of(w[j]), is_protected(p[j]));
+#pragma unroll 4
+        for (int j0 = 0; j0 < n; j0 += THREADS) {
+            const int j = j0 + tid;
+            const bool prot = j < n && is_protected(p[j]);
+            if (CACHED) {
+                const uint32_t m = __ballot_sync(kFull, prot);
+                if (lane == 0 && j < n) bits[j >> 5] = m;
+            }
+            if (j < n) of_either(CACHED ? keys[j] : key_of(w[j]), prot);
+        }
     }
     // visit(slot, key) for every slot of class `of` with a key in [lo, hi]
     auto each = [&](bool of, uint32_t lo, uint32_t hi, auto &&visit) {
-        if constexpr (CACHED) {
+        if constexpr (HELD) {
 #pragma unroll
             for (int x = 0; x < PER; ++x) {
                 if (x * THREADS >= n) break;
@@ -169,9 +191,10 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
                 if (j < n && mine[x] >= lo && mine[x] <= hi && ((prots >> x & 1) != 0) == of) visit(j, mine[x]);
             }
         } else {
+#pragma unroll 4
             for (int j = tid; j < n; j += THREADS) {
-                const uint32_t k = key_of(w[j]);
-                if (k >= lo && k <= hi && is_protected(p[j]) == of) visit(j, k);
+                const uint32_t k = key_at(j);
+                if (k >= lo && k <= hi && prot_at(j) == of) visit(j, k);
             }
         }
     };
@@ -310,11 +333,11 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
     if (tid == 0) a.count[bh] = (int32_t)holes;
 }
 
-template <int THREADS, bool CACHED>
+template <int THREADS, int KEYS, bool HELD>
 cudaError_t launch_select(const EvictArgs &a, cudaStream_t s) {
-    auto kern = select_kernel<THREADS, CACHED>;
-    const int keys = CACHED ? (THREADS == 1024 ? kCached : kSmall) : 0, smem = (keys + keys / 32) * 4;
-    if (CACHED) {
+    auto kern = select_kernel<THREADS, KEYS, HELD>;
+    constexpr int smem = (KEYS + KEYS / 32) * 4;
+    if (smem > 0) {
         const cudaError_t e = ensure_smem((const void *)kern, smem);
         if (e != cudaSuccess) return e;
     }
@@ -352,9 +375,10 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
 }  // namespace
 
 cudaError_t launch_kv_evict(const DeviceInfo &di, const EvictArgs &a, cudaStream_t s) {
-    cudaError_t e = a.cap <= kSmall    ? launch_select<256, true>(a, s)
-                    : a.cap <= kCached ? launch_select<1024, true>(a, s)
-                                       : launch_select<1024, false>(a, s);
+    cudaError_t e = a.cap <= kSmall    ? launch_select<256, kSmall, true>(a, s)
+                    : a.cap <= kHeld   ? launch_select<1024, kHeld, true>(a, s)
+                    : a.cap <= kCached ? launch_select<1024, kCached, false>(a, s)
+                                       : launch_select<1024, 0, false>(a, s);
     if (e != cudaSuccess) return e;
     const int bh = a.c.batch * a.c.heads;
     const int chunks = a.c.dim * (a.c.e4m3 ? 1 : 2) / 16, rows = kMoveThreads / chunks;

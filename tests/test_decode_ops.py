@@ -406,7 +406,9 @@ def run_evict(c, lens, budget, sinks, recent, w, p, in_place=False):
     (BF, 64, 16, "phsd", 1, [700, 40], 30, 10, 20, "equal"),
     (BF, 64, 64, "phsd", 2, [2000, 1999], 1, 0, 1, "random"),
     (BF, 64, 64, "phsd", 2, [2000, 900], 700, 0, 5, "odd"),              # infinities, NaN, signed zeros, negatives
-    (BF, 64, 128, "phsd", 1, [30000, 21000, 20480], 9000, 4, 100, "ties"),  # longer than the shared memory's keys
+    (BF, 64, 128, "phsd", 1, [30000, 21000, 20480], 9000, 4, 100, "ties"),  # longer than what a CTA's registers hold
+    (BF, 64, 128, "phsd", 1, [9000, 17001], 8192, 4, 100, "random"),
+    (BF, 64, 128, "phsd", 1, [60000, 49153], 30000, 4, 100, "random"),      # longer than the shared memory's keys
     (BF, 64, 16, "phsd", 1, [400], 200, 0, 50, "one position"),          # all protected: cut by weight all the same
 ])
 @pytest.mark.parametrize("in_place", [False, True])
