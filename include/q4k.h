@@ -496,8 +496,8 @@ q4k_status q4k_kv_append(const q4k_kv_cache *cache, int64_t T, int32_t n_heads, 
  *     slot j < len:  weights[b][h][j] = decay*weights[b][h][j] + sum of
  *     softmax(s[r])[j] over the rows r of head h.  len must be <= ld_weights.
  * Products are exact and sums, maxima and the joined softmax fp32; the weights p
- * enter the product with v as the sum of two 16-bit values (to about 2^-16), and o is
- * rounded once.  The length is split over the whole GPU by the lengths of the batch,
+ * enter the product with v as the sum of two bf16 values (to 2^-16), for an e4m3 cache
+ * as one f16 value (to 2^-12, and to 2^-32 of the largest), and o is rounded once.  The length is split over the whole GPU by the lengths of the batch,
  * and the parts are joined in slot order: the same call repeats its bits, but a
  * sequence's last bits may depend on the other lengths of its batch, also in
  * batch-invariant mode.

@@ -62,6 +62,8 @@ def kv_cache(k, v, page_table, k_scale: float = 1.0, v_scale: float = 1.0) -> Kv
     types = {torch.bfloat16: Q4K_KV_BF16, torch.float8_e4m3fn: Q4K_KV_E4M3}
     if k.dtype not in types or page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
         raise ValueError("k and v are bfloat16 or float8_e4m3fn, page_table int32 [batch][max_pages]")
+    if page_table.shape[0] > 1 and page_table.stride(0) < page_table.shape[1]:
+        raise ValueError("page_table's rows must not overlap")
     return KvCache(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), max(page_table.stride(0), page_table.shape[1]),
                    k.shape[0], k.stride(0), k.stride(1), k.stride(2), page_table.shape[0], page_table.shape[1],
                    k.shape[2], k.shape[1], k.shape[3], types[k.dtype], k_scale, v_scale)

@@ -914,14 +914,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a,
             float top = kNone, sum = 0.f;
             for (int x = tid; x < parts * 8; x += blockDim.x) {
                 const float2 ml = *reinterpret_cast<const float2 *>(part_at(a, p, p.first + x / 8) + 2 * (n * 8 + x % 8));
-                if (ml.x == kNone) continue;
+                if (ml.x == kNone) {
+                    sum += ml.y;  // 0, or NaN where every score is
+                    continue;
+                }
                 const float m = fmaxf(top, ml.x);
                 sum = sum * ex2_approx(top - m) + ml.y * ex2_approx(ml.x - m);
                 top = m;
             }
             float m = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-            sum = top == kNone ? 0.f : sum * ex2_approx(top - m);
+            if (top != kNone) sum *= ex2_approx(top - m);
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
             __syncthreads();  // (the fragment before has been read)
@@ -933,7 +936,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a,
                 mt[e] = kNone;
                 for (int w = 0; w < warps; ++w) mt[e] = fmaxf(mt[e], sm_m[w][c4 * 2 + e]);
                 for (int w = 0; w < warps; ++w)
-                    if (sm_m[w][c4 * 2 + e] != kNone) l[e] += sm_l[w][c4 * 2 + e] * ex2_approx(sm_m[w][c4 * 2 + e] - mt[e]);
+                    l[e] += sm_l[w][c4 * 2 + e] * (sm_m[w][c4 * 2 + e] == kNone ? 1.f : ex2_approx(sm_m[w][c4 * 2 + e] - mt[e]));
             }
             for (int x0 = warp; x0 < parts; x0 += kAhead * warps) {
 #pragma unroll

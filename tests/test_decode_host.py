@@ -142,3 +142,7 @@ def test_status_and_descriptor(lib):
     for bad in (dict(k=k.float()), dict(v=k[:3]), dict(t=torch.zeros(3, 2)), dict(t=torch.zeros(3, dtype=torch.int32))):
         with pytest.raises(ValueError):
             q4k.kv_cache(bad.get("k", k), bad.get("v", bad.get("k", k)), bad.get("t", torch.zeros(3, 2, dtype=torch.int32)))
+    with pytest.raises(ValueError):
+        q4k.kv_cache(k, k, torch.zeros(1, 2, dtype=torch.int32).expand(3, 2))  # one row for all sequences
+    wide = torch.zeros(3, 8, dtype=torch.int32)[:, :2]
+    assert q4k.kv_cache(k, k, wide).ld_table == 8

@@ -72,6 +72,12 @@ ATTN = [
     (256, F8, 16, "phsd", 1, 4, 1, [64, 65, 333], 0, 0.0, False),
     (128, F8, 5, "mixed", 1, 6, 4, [300, 2, 77], 40, 0.0, True),
     (256, F8, 16, "phsd", 1, 2, 3, [130, 40], 33, 3.0, True),
+    (64, BF, 16, "phsd", 1, 8, 3, [90, 200, 2], 0, 0.0, True),                      # 24 rows of one row tile
+    (64, F8, 16, "phsd", 2, 16, 2, [140, 33], 20, 0.0, True),                       # 32
+    (256, F8, 24, "pshd", 1, 16, 2, [100, 31], 0, 0.0, True),                       # two row tiles of 16
+    (256, BF, 16, "phsd", 2, 6, 7, [77, 300], 0, 0.0, False),                       # three
+    (128, F8, 16, "mixed", 1, 12, 6, [65, 500], 0, 0.0, True),                      # three of 32
+    (128, BF, 16, "phsd", 1, 1, 64, [64, 100], 0, 0.0, True),                       # the most new tokens
 ]
 
 
@@ -140,6 +146,37 @@ def test_attn_many_and_long(dtype):
         ref = R.attn_decode(np64(k), np64(v), table.cpu().numpy(), lens, np64(q), 1, D ** -0.5, weights=np.zeros(w.shape))
         check_attn(o, w, ref, D, max(lens))
     q4k.q4k_check_device()
+
+
+def test_attn_more_sequences_than_threads():
+    """Several sequences a thread when the work is shared out, many of them empty."""
+    g = gen_of(8)
+    B, Hkv, G, D, page, per = 700, 2, 3, 64, 8, 20
+    lens = [0 if i % 3 == 1 or 200 < i < 420 else (i * 37) % 157 for i in range(B)]
+    k, v = pool((B * per, Hkv, page, D), BF, "phsd", g)
+    table = table_of(B, per, B * per, g)
+    q = torch.randn(B, 1, Hkv * G, D, generator=g, device="cuda").to(BF)
+    w = torch.ones(B, Hkv, per * page, device="cuda")
+    o = run_attn(k, v, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), q, 1, D ** -0.5, weights=w, decay=0.5)
+    q4k.q4k_check_device()
+    check_attn(o, w, R.attn_decode(np64(k), np64(v), table.cpu().numpy(), lens, np64(q), 1, D ** -0.5, weights=np.ones(w.shape),
+                                   decay=0.5), D, 160)
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("n", [40, 5000])
+def test_attn_a_query_without_a_number_keeps_to_itself(dtype, n):
+    g = gen_of(9)
+    D, page, per = 128, 16, 320
+    k, v = pool((per, 1, page, D), dtype, "phsd", g)
+    table = table_of(1, per, per, g)
+    q = torch.randn(1, 1, 5, D, generator=g, device="cuda").to(BF)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    clean = run_attn(k, v, table, lens, q, 1, 0.1)
+    q[0, 0, 2] = float("nan")
+    o = run_attn(k, v, table, lens, q, 1, 0.1)
+    assert torch.isnan(o[0, 0, 2]).all()
+    assert torch.equal(o[0, 0, [0, 1, 3, 4]], clean[0, 0, [0, 1, 3, 4]])
 
 
 @pytest.mark.parametrize("dtype", [BF, F8])
