@@ -881,16 +881,113 @@ __device__ __forceinline__ Parts parts_of(const AttnArgs &a, int b, int hr) {
 __device__ __forceinline__ const float *part_at(const AttnArgs &a, const Parts &p, int i) {
     return a.parts + (int64_t)(2 * i + (i == p.first)) * a.part_floats;
 }
-// Units in several parts, and zeros for units without slots: `blocks` blocks a unit.  A block joins 16 values
-// of the 8 rows of an octet at a time (one fragment: 32 lanes of float4), its warps taking turns at the parts.
-// With weights it also leaves the unit's (m, l), as the CTAs that finished whole units did.
 constexpr int kJoinWarps = 16;  // of a block, at most
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a, int blocks) {
+
+// (m, l) of the 8 rows of octet n over the unit's parts; every thread of the block calls it.  Row lane % 8's come
+// back to every lane.  scratch: [2][kJoinWarps][8]
+__device__ __forceinline__ float2 join_ml(const AttnArgs &a, const Parts &p, int n, float (*scratch)[kJoinWarps][8]) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int parts = p.last - p.first + 1;
+    // thread x: row x % 8 of some of the parts
+    float top = kNone, sum = 0.f;
+    for (int x = tid; x < parts * 8; x += blockDim.x) {
+        const float2 ml = *reinterpret_cast<const float2 *>(part_at(a, p, p.first + x / 8) + 2 * (n * 8 + x % 8));
+        if (ml.x == kNone) {
+            sum += ml.y;  // 0, or NaN where every score is
+            continue;
+        }
+        const float m = fmaxf(top, ml.x);
+        sum = sum * ex2_approx(top - m) + ml.y * ex2_approx(ml.x - m);
+        top = m;
+    }
+    float m = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+    if (top != kNone) sum *= ex2_approx(top - m);
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+    __syncthreads();  // (what the scratch held has been read)
+    if (lane < 8) scratch[0][warp][lane] = m, scratch[1][warp][lane] = sum;
+    __syncthreads();
+    float mt = kNone, lt = 0.f;
+    for (int w = 0; w < warps; ++w) mt = fmaxf(mt, scratch[0][w][lane & 7]);
+    for (int w = 0; w < warps; ++w) {
+        const float mw = scratch[0][w][lane & 7];
+        lt += scratch[1][w][lane & 7] * (mw == kNone ? 1.f : ex2_approx(mw - mt));
+    }
+    return make_float2(mt, lt);
+}
+
+// A chunk of slots of one KV head's weights: weights <- decay * weights + sum of the rows' 2^(s - m) / l.
+__device__ __forceinline__ void weigh(const AttnArgs &a, uint32_t id, int chunks, int chunk, float *sm_m, float *sm_r,
+                                      float (*scratch)[kJoinWarps][8]) {
+    const uint32_t bh = id / (uint32_t)chunks;
+    const int b = (int)(bh / (uint32_t)a.c.heads), h = (int)(bh - (uint32_t)b * (uint32_t)a.c.heads);
+    int begin, len;
+    seq_range(a, b, begin, len);
+    const int lo = (int)(id - bh * (uint32_t)chunks) * chunk, hi = min(lo + chunk, len), threads = blockDim.x;
+    if (lo >= len) return;
+    if (hi > begin)
+        for (int rt = 0; rt < a.row_tiles; ++rt) {
+            const Parts p = parts_of(a, b, h * a.row_tiles + rt);
+            for (int n = 0; n < a.tile_rows / 8; ++n) {
+                const int r = rt * a.tile_rows + n * 8 + (threadIdx.x & 7);
+                const float2 ml = p.whole ? a.unit_ml[((int64_t)b * a.unit_heads + h * a.row_tiles) * a.tile_rows + r]
+                                          : join_ml(a, p, n, scratch);
+                if (threadIdx.x < 8 && r < a.rows) {
+                    sm_m[r] = ml.x == kNone ? 0.f : ml.x;
+                    sm_r[r] = ml.y > 0.f || ml.y != ml.y ? ex2_approx(lift(a.c.e4m3 != 0)) / ml.y : 0.f;
+                }
+            }
+        }
+    __syncthreads();
+    float *w = a.weights + (int64_t)bh * a.ld_weights;
+    const float *z = a.logits + (int64_t)bh * a.rows * a.ld_logits;
+    constexpr int kAt = 4, kRowsAhead = 4;  // slots of a thread at a time; rows whose scores are on their way at once
+    for (int j0 = lo + threadIdx.x; j0 < hi; j0 += kAt * threads) {
+        float sum[kAt], old[kAt];
+#pragma unroll
+        for (int x = 0; x < kAt; ++x) {
+            sum[x] = 0.f;
+            if (j0 + x * threads < hi) old[x] = w[j0 + x * threads];
+        }
+        for (int r0 = 0; r0 < a.rows; r0 += kRowsAhead) {
+            float s[kRowsAhead][kAt];
+#pragma unroll
+            for (int y = 0; y < kRowsAhead; ++y)
+#pragma unroll
+                for (int x = 0; x < kAt; ++x) {
+                    const int j = j0 + x * threads;
+                    s[y][x] = r0 + y < a.rows && j >= begin && j < hi ? __ldg(z + (r0 + y) * a.ld_logits + j) : kNone;
+                }
+#pragma unroll
+            for (int y = 0; y < kRowsAhead; ++y) {
+                if (r0 + y >= a.rows) break;
+                const float m = sm_m[r0 + y], f = sm_r[r0 + y];
+#pragma unroll
+                for (int x = 0; x < kAt; ++x) sum[x] = s[y][x] == kNone ? sum[x] : fmaf(ex2_approx(s[y][x] - m), f, sum[x]);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kAt; ++x)
+            if (j0 + x * threads < hi) w[j0 + x * threads] = fmaf(old[x], a.decay, sum[x]);
+    }
+}
+
+// The first join_blocks blocks: units in several parts, and zeros for units without slots, `blocks` blocks a unit.
+// A block joins 16 values of the 8 rows of an octet at a time (one fragment: 32 lanes of float4), its warps
+// taking turns at the parts.  The others add up weights; they join (m, l) for themselves, which costs less than
+// waiting for a kernel of its own.
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a, int blocks, uint32_t join_blocks, int chunks, int chunk) {
     __shared__ float4 sm[kJoinWarps][32];
-    __shared__ float sm_m[kJoinWarps][8], sm_l[kJoinWarps][8];
+    __shared__ float scratch[2][kJoinWarps][8];
+    __shared__ float sm_m[kMaxAttnRows], sm_r[kMaxAttnRows];
     const int warps = blockDim.x >> 5;
     pdl_wait();
     pdl_trigger();
+    if (blockIdx.x >= join_blocks) {
+        weigh(a, blockIdx.x - join_blocks, chunks, chunk, sm_m, sm_r, scratch);
+        return;
+    }
     const int D = a.c.dim, ks = D / 16, fragments = a.tile_rows / 8 * ks;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
     const uint32_t unit = blockIdx.x / (uint32_t)blocks, block = blockIdx.x - unit * (uint32_t)blocks;
@@ -910,34 +1007,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a,
 #pragma unroll
             for (int y = 0; y < kAhead; ++y)
                 if (warp + y * warps < parts) t[y] = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + warp + y * warps) + at);
-            // thread x: row x % 8 of some of the parts
-            float top = kNone, sum = 0.f;
-            for (int x = tid; x < parts * 8; x += blockDim.x) {
-                const float2 ml = *reinterpret_cast<const float2 *>(part_at(a, p, p.first + x / 8) + 2 * (n * 8 + x % 8));
-                if (ml.x == kNone) {
-                    sum += ml.y;  // 0, or NaN where every score is
-                    continue;
-                }
-                const float m = fmaxf(top, ml.x);
-                sum = sum * ex2_approx(top - m) + ml.y * ex2_approx(ml.x - m);
-                top = m;
-            }
-            float m = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-            if (top != kNone) sum *= ex2_approx(top - m);
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
-            __syncthreads();  // (the fragment before has been read)
-            if (lane < 8) sm_m[warp][lane] = m, sm_l[warp][lane] = sum;
-            __syncthreads();
+            const float2 own = join_ml(a, p, n, scratch);
             float mt[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                mt[e] = kNone;
-                for (int w = 0; w < warps; ++w) mt[e] = fmaxf(mt[e], sm_m[w][c4 * 2 + e]);
-                for (int w = 0; w < warps; ++w)
-                    l[e] += sm_l[w][c4 * 2 + e] * (sm_m[w][c4 * 2 + e] == kNone ? 1.f : ex2_approx(sm_m[w][c4 * 2 + e] - mt[e]));
-            }
+            for (int e = 0; e < 2; ++e) mt[e] = __shfl_sync(0xFFFFFFFFu, own.x, c4 * 2 + e), l[e] = __shfl_sync(0xFFFFFFFFu, own.y, c4 * 2 + e);
             for (int x0 = warp; x0 < parts; x0 += kAhead * warps) {
 #pragma unroll
                 for (int y = 0; y < kAhead; ++y) {
@@ -952,9 +1025,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a,
                     }
                 }
             }
-            if (a.unit_ml && i == 0 && warp == 0 && g == 0)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) a.unit_ml[(int64_t)unit * a.tile_rows + n * 8 + c4 * 2 + e] = make_float2(mt[e], l[e]);
             sm[warp][lane] = v;
             __syncthreads();
             if (warp > 0) continue;
@@ -983,59 +1053,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a,
     }
 }
 
-// A chunk of slots of one KV head's weights: weights <- decay * weights + sum of the rows'
-// 2^(s - m) / l.
-__global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnArgs a, int chunks, int chunk) {
-    __shared__ float sm_m[kMaxAttnRows], sm_r[kMaxAttnRows];
-    pdl_wait();
-    pdl_trigger();
-    const int64_t bh = blockIdx.x / chunks;
-    const int b = (int)(bh / a.c.heads), h = (int)(bh - (int64_t)b * a.c.heads);
-    int begin, len;
-    seq_range(a, b, begin, len);
-    const int lo = (int)(blockIdx.x - bh * chunks) * chunk, hi = min(lo + chunk, len);
-    if (lo >= len) return;
-    if (hi > begin)
-        for (int r = threadIdx.x; r < a.rows; r += kThreads) {
-            const int rt = r / a.tile_rows;
-            const float2 ml = a.unit_ml[((int64_t)b * a.unit_heads + h * a.row_tiles + rt) * a.tile_rows + r - rt * a.tile_rows];
-            sm_m[r] = ml.x == kNone ? 0.f : ml.x;
-            sm_r[r] = ml.y > 0.f || ml.y != ml.y ? ex2_approx(lift(a.c.e4m3 != 0)) / ml.y : 0.f;
-        }
-    __syncthreads();
-    float *w = a.weights + bh * a.ld_weights;
-    const float *z = a.logits + bh * a.rows * a.ld_logits;
-    constexpr int kAt = 4, kRowsAhead = 4;  // slots of a thread at a time; rows whose scores are on their way at once
-    for (int j0 = lo + threadIdx.x; j0 < hi; j0 += kAt * kThreads) {
-        float sum[kAt], old[kAt];
-#pragma unroll
-        for (int x = 0; x < kAt; ++x) {
-            sum[x] = 0.f;
-            if (j0 + x * kThreads < hi) old[x] = w[j0 + x * kThreads];
-        }
-        for (int r0 = 0; r0 < a.rows; r0 += kRowsAhead) {
-            float s[kRowsAhead][kAt];
-#pragma unroll
-            for (int y = 0; y < kRowsAhead; ++y)
-#pragma unroll
-                for (int x = 0; x < kAt; ++x) {
-                    const int j = j0 + x * kThreads;
-                    s[y][x] = r0 + y < a.rows && j >= begin && j < hi ? __ldg(z + (r0 + y) * a.ld_logits + j) : kNone;
-                }
-#pragma unroll
-            for (int y = 0; y < kRowsAhead; ++y) {
-                if (r0 + y >= a.rows) break;
-                const float m = sm_m[r0 + y], f = sm_r[r0 + y];
-#pragma unroll
-                for (int x = 0; x < kAt; ++x) sum[x] = s[y][x] == kNone ? sum[x] : fmaf(ex2_approx(s[y][x] - m), f, sum[x]);
-            }
-        }
-#pragma unroll
-        for (int x = 0; x < kAt; ++x)
-            if (j0 + x * kThreads < hi) w[j0 + x * kThreads] = fmaf(old[x], a.decay, sum[x]);
-    }
-}
-
 template <int D, bool E4M3, int NR>
 cudaError_t launch(AttnArgs &a, const DeviceInfo &di, cudaStream_t s) {
     using C = Cfg<D, E4M3, NR>;
@@ -1059,14 +1076,16 @@ cudaError_t launch(AttnArgs &a, const DeviceInfo &di, cudaStream_t s) {
     if (blocks > fragments) blocks = fragments;
     // a few units may be in hundreds of parts each
     const int join_threads = units * 64 <= a.resident ? kJoinWarps * 32 : kThreads;
-    e = launch_pdl(join_kernel, dim3((unsigned)(units * blocks)), dim3(join_threads), 0, s, dim3(1), a, (int)blocks);
-    if (e != cudaSuccess || !a.weights) return e;
-    // chunks of 2048 slots, which make the start of a block little work beside the rest, unless that leaves SMs idle
+    // weights: chunks of 2048 slots, which make the start of a block little work beside the rest, unless that leaves SMs
+    // idle
     const int64_t heads = (int64_t)a.c.batch * a.c.heads;
-    int chunk = 2048;
-    while (chunk > 512 && heads * ((a.cap + chunk - 1) / chunk) < 4 * di.sm_count) chunk /= 2;
-    const int chunks = (a.cap + chunk - 1) / chunk;
-    return launch_pdl(weigh_kernel, dim3((unsigned)(heads * chunks)), dim3(kThreads), 0, s, dim3(1), a, chunks, chunk);
+    int chunk = 2048, chunks = 0;
+    if (a.weights) {
+        while (chunk > 512 && heads * ((a.cap + chunk - 1) / chunk) < 4 * di.sm_count) chunk /= 2;
+        chunks = (a.cap + chunk - 1) / chunk;
+    }
+    return launch_pdl(join_kernel, dim3((unsigned)(units * blocks + heads * chunks)), dim3(join_threads), 0, s, dim3(1), a, (int)blocks,
+                      (uint32_t)(units * blocks), chunks > 0 ? chunks : 1, chunk);
 }
 
 template <int D, bool E4M3>

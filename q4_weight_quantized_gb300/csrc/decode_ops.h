@@ -33,7 +33,7 @@ struct AttnArgs {
     int64_t ld_logits;
     float *parts;                    // [2 * shares] parts
     int32_t part_floats;
-    float2 *unit_ml;                 // [batch * unit_heads][tile_rows]: (m, l) of every unit with slots; with weights only
+    float2 *unit_ml;                 // [batch * unit_heads][tile_rows]: (m, l) of units finished by one CTA; with weights only
     int64_t *prefix;                 // [batch + 1]: places of the list before each sequence
     int32_t resident;
 };
