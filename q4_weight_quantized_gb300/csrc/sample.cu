@@ -9,22 +9,29 @@
 // A cluster of CTAs owns a row: each keeps its contiguous share of the logits in shared
 // memory, so the row is read from global memory once, and the CTAs exchange bins, sums
 // and cuts through distributed shared memory.
-//   1. load, largest logit;
-//   2. the number and the weight of the tokens in bins of d.  With top-k the cut
-//      is near the top: 64 bins to each of 16 octaves, and what lies below is not even
-//      weighed.  Otherwise 32 to each of 32; the rest is added up without bins.  If the cut
+//   1. load, largest logits of 128 parts of the row: its largest, and a bound below the k-th
+//      (at least k logits are as large as the k-th of these);
+//   2. where top-k (k <= 96) or min-p can be seen to leave few tokens, those are gathered in
+//      one CTA, the row's weight is summed meanwhile if top-p asks for it, and that CTA ranks
+//      them and draws.  Otherwise:
+//   3. the number and the weight of the tokens in bins of d.  With top-k or min-p the cut
+//      is near the top: 64 bins to each of 16 octaves, and with top-k what lies below is not
+//      even weighed.  Otherwise 32 to each of 32; the rest is added up without bins.  If the cut
 //      turns out to lie below, again with 16 bins to each of all 41 octaves;
-//   3. the tokens of the bin in which top-k (then top-p) ends are gathered in one CTA, narrowed
+//   4. the tokens of the bin in which top-k (then top-p) ends are gathered in one CTA, narrowed
 //      there by histograms over their keys, and the last few ranked against each other;
 //      if they are too many to be gathered, the whole cluster narrows them the same way
 //      first; equal logits are counted off by index;
-//   4. the sum of what is kept, the target, and the token by a scan in index order.
+//   5. the sum of what is kept, the target, and the token by a scan in index order.
 // Where the tokens down to the first cut's bin are few, one CTA gathers them all after step
-// 2 and does the rest with them alone.
+// 3 and does the rest with them alone.
 // A bin never crosses an octave, so its tokens' weights have one scale: they are summed as
 // two 12-bit halves of a 24-bit number by 32-bit atomics without a result.
-// Bound by the arithmetic of the weights (some 70 instructions a logit in all, half of
-// them on two logits at once) for many rows, by the cluster's exchanges for one.
+// Bound for many rows by the arithmetic of the weights (half of it on two logits at once) and
+// the exchanges that two CTAs on an SM do not hide, for one row by the exchanges and the fetch
+// of instructions that are used once.  Measured: 9.4 us for a row of 128001 with top-k 50 and
+// top-p (13.1 without step 2), 149 us for 256 rows of 151936 with top-p and min-p (229).
+
 #include <cuda_runtime.h>
 
 #include "decode_ops.h"
@@ -39,7 +46,10 @@ constexpr int kBins = 1024;
 constexpr int kList = 768;           // tokens of a bin that one CTA gathers
 constexpr int kFew = 256;            // tokens that are ranked against each other
 constexpr int kMaxCluster = 8;
+constexpr int kBests = 128;          // parts of a row whose largest logits bound the k-th from below
+constexpr int kTop = 96;             // the largest k for that: some 180 of independent logits lie above the bound
 constexpr int kCached = 19456;       // logits of a CTA that stay in shared memory with two CTAs on an SM
+constexpr int kCachedOne = 47104;    // and with one
 constexpr float kAll = 41.f;         // from this d on the weight is 0
 constexpr uint32_t kOne = 1u << 24;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
@@ -53,6 +63,14 @@ __device__ __forceinline__ uint32_t key_of(float z) {
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k); }
 // The negative of a logit, as the row is kept: that of NaN is +inf, that of either zero +0.
 __device__ __forceinline__ float stored(float z) { return fminf(0.f - z, INFINITY); }
+
+// Logits 4 i .. 4 i + 3 of a row's part, negated; places outside head .. n - 1 count as -inf.
+__device__ __forceinline__ float4 fetch(const float *z, int i, int head, int n) {
+    float v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = 4 * i + x >= head && 4 * i + x < n ? stored(__ldg(z + 4 * i + x)) : INFINITY;
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
 
 // Where the largest logit or 1 / temperature is infinite, every distance is 0 or infinite: the
 // row then counts as one of zeros and -inf.  least: the largest logit, negated.
@@ -143,15 +161,17 @@ struct Shared {
     u64 all_sum[kBins];
     uint4 list[kList];  // key, index, weight (CTA 0's is used)
     u64 warp_u64[kWarps];
-    u64 slot[2][kMaxCluster];  // exchanged values
+    u64 slot[2][2 * kMaxCluster];  // exchanged values
+    alignas(16) uint32_t best[kBests];       // largest keys of parts of the row
     u64 found_sum, ranked_sum;
     uint32_t warp_u32[kWarps];
     uint32_t list_n[2];  // tokens that came for the list (CTA 0's are used): two counters in turn
-    uint32_t list_left;
+    uint32_t list_left, own_n;
     uint32_t found_bin, found_cnt, ranked_key, ranked_idx;
 };
 
 static_assert(2 * (sizeof(Shared) + 4 * kCached + 1024) <= 233472, "two CTAs on an SM");
+static_assert(sizeof(Shared) + 4 * kCachedOne + 1024 <= 233472, "one CTA on an SM");
 
 // A prefix in rank: logits above z, and those equal to it up to index idx.
 struct Cut {
@@ -163,9 +183,11 @@ struct Cut {
 template <bool CACHED>
 struct Row {
     Shared &s;
-    const float *z;    // CACHED: this CTA's share in shared memory, negated, filled up with +inf to whole steps; else the row
-    uint32_t base;     // index of its first logit
-    int n, n4;         // its length; its groups of four logits
+    // this CTA's share in groups of four, aligned as the row is in global memory: places outside head .. n - 1
+    // hold no logits.  CACHED: in shared memory, negated, +inf in those places
+    const float *z;
+    uint32_t base;     // index of place 0 (mod 2^32)
+    int head, n, n4;   // n4: groups
     uint32_t rank, ctas;
     float top, c;      // largest logit; log2(e) / temperature
     float infinite;    // not CACHED: the row is to be flattened (see there) about this, unless NaN
@@ -178,13 +200,9 @@ struct Row {
         if constexpr (CACHED) {
             return reinterpret_cast<const float4 *>(z)[i];
         } else {
-            float v[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                v[x] = 4 * i + x < n ? stored(__ldg(z + 4 * i + x)) : INFINITY;
-                if (infinite == infinite) v[x] = flat(v[x], infinite);
-            }
-            return make_float4(v[0], v[1], v[2], v[3]);
+            float4 v = fetch(z, i, head, n);
+            if (infinite == infinite) v = make_float4(flat(v.x, infinite), flat(v.y, infinite), flat(v.z, infinite), flat(v.w, infinite));
+            return v;
         }
     }
     // distances of two negated logits; not < kAll (inf or NaN) for a weight of 0
@@ -202,14 +220,48 @@ struct Row {
         span = fminf(kAll, (float)(kBins >> log_bins));
     }
 
-    // Every CTA's value (its thread 0's) to all CTAs, by rank.  Two slots in turn, so one
-    // barrier an exchange is enough.
-    __device__ __forceinline__ const u64 *exchange(u64 v) {
+    // Every CTA's value (or two) to all CTAs, by rank.  Two slots in turn, so one barrier an
+    // exchange is enough.
+    __device__ __forceinline__ const u64 *exchange(u64 v, u64 v2 = 0) {
         u64 *slot = s.slot[turn];
         turn ^= 1;
-        if (threadIdx.x < ctas) peer_store(slot + rank, threadIdx.x, v);
+        if (threadIdx.x < ctas) {
+            peer_store(slot + rank, threadIdx.x, v);
+            peer_store(slot + kMaxCluster + rank, threadIdx.x, v2);
+        }
         cluster_sync();
         return slot;
+    }
+    // The largest of all threads' keys; and those of kBests parts of the row, for kth_best.
+    __device__ __forceinline__ uint32_t cluster_best(uint32_t v) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        const int lanes = (int)ctas * (kThreads / kBests);  // of a part: 4 to 32
+        static_assert(kMaxCluster * (kThreads / kBests) == 32 && kBests == 128, "a part within a warp");
+        for (int o = 1; o < lanes; o <<= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+        const int mate = tid & (lanes - 1);
+        if (mate < (int)ctas) peer_store(&s.best[(rank * kThreads + tid) / lanes], mate, v);
+        cluster_sync();
+        const uint4 b = reinterpret_cast<const uint4 *>(s.best)[lane];
+        return __reduce_max_sync(kFull, max(max(b.x, b.y), max(b.z, b.w)));
+    }
+    // The k-th largest of the parts' largest keys, 0 < k <= kBests: at least k logits are as large.
+    __device__ __forceinline__ uint32_t kth_best(int k) {
+        constexpr int TEAM = kThreads / kBests;
+        const int i = threadIdx.x / TEAM, mate = threadIdx.x % TEAM;
+        const uint32_t me = s.best[i];
+        int before = 0;
+#pragma unroll
+        for (int x = 0; x < kBests / TEAM; x += 4) {
+            const int j = x * TEAM + 4 * mate;
+            const uint4 b = reinterpret_cast<const uint4 *>(s.best)[j / 4];
+            before += (b.x > me || (b.x == me && j < i)) + (b.y > me || (b.y == me && j + 1 < i)) +
+                      (b.z > me || (b.z == me && j + 2 < i)) + (b.w > me || (b.w == me && j + 3 < i));
+        }
+#pragma unroll
+        for (int o = 1; o < TEAM; o <<= 1) before += __shfl_xor_sync(kFull, before, o);
+        if (mate == 0 && before == k - 1) s.ranked_key = me;
+        __syncthreads();
+        return s.ranked_key;
     }
     __device__ __forceinline__ u64 block_sum(u64 v) {
         v = warp_sum(v);
@@ -276,15 +328,15 @@ struct Row {
         }
         cluster_sync();
     }
-    // Bins of d < span over the row, from cleared ones.  Returns this thread's part of the weight beyond
-    // (if beyond).
-    __device__ __forceinline__ u64 histogram(bool beyond) {
+    // Bins of d < edge (edge <= span) over the row, from cleared ones.  Returns this thread's part of the
+    // weight beyond (if beyond).
+    __device__ __forceinline__ u64 histogram(float edge, bool beyond) {
         u64 tail = 0;
-        const float limit = beyond ? kAll : span;
+        const float limit = beyond ? kAll : edge;
         for (int i = threadIdx.x; i < n4; i += kThreads) {
             const float4 v = four(i);
             const float x[4] = {v.x, v.y, v.z, v.w};
-            uint32_t below = 0;
+            u64 below = 0;
 #pragma unroll
             for (int h = 0; h < 4; h += 2) {
                 const float2 d = dist2(x[h], x[h + 1]);
@@ -294,8 +346,8 @@ struct Row {
                 const float dd[2] = {d.x, d.y};
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    if (dd[e] < span) into_bin(bin_of(dd[e]), w[e], oct[e]);
-                    else if (dd[e] < limit) below += w[e] >> (oct[e] - 16);  // (d >= span >= 16: 24 bits)
+                    if (dd[e] < edge) into_bin(bin_of(dd[e]), w[e], oct[e]);
+                    else if (dd[e] < limit) below += scaled(w[e], oct[e]);
                 }
             }
             tail += below;
@@ -305,9 +357,9 @@ struct Row {
     }
 
     // The bin in which the running count (by_sum: weight), beginning with cnt (sum), reaches
-    // `need`: its number, and the count and weight before it in cnt and sum.  -1: none does.
-    // own: of this CTA's bins (weights scaled by 2^up), otherwise of the cluster's.
-    __device__ __forceinline__ int find_bin(bool by_sum, u64 need, u64 &cnt, u64 &sum, bool own = false, int up = 0) {
+    // `need`, or bin `last` before that: its number, and the count and weight before it in cnt and sum.
+    // -1: none does.  own: of this CTA's bins (weights scaled by 2^up), otherwise of the cluster's.
+    __device__ __forceinline__ int find_bin(bool by_sum, u64 need, int last, u64 &cnt, u64 &sum, bool own = false, int up = 0) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         static_assert(kBins == 2 * kThreads, "two bins a thread");
         uint32_t k[2];
@@ -334,7 +386,8 @@ struct Row {
         u64 c0 = cnt + kb + ki - k[0] - k[1], s0 = sum + wb + wi - w[0] - w[1];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            if (by_sum ? s0 < need && need <= s0 + w[x] : c0 < need && need <= c0 + k[x]) {
+            const u64 at = by_sum ? s0 : c0, to = at + (by_sum ? w[x] : k[x]);
+            if (at < need && (2 * tid + x == last || (need <= to && 2 * tid + x < last))) {
                 s.found_bin = 2 * tid + x;
                 s.found_cnt = (uint32_t)c0;
                 s.found_sum = s0;
@@ -436,6 +489,47 @@ struct Row {
         if (rank == 0 && threadIdx.x == 0) s.list_n[counter] = 0;
         return m;
     }
+    // Tokens of d < to and no logit below -zc, into CTA 0's list if they are at most kFew: their number.
+    // weigh: the row's weight, too.
+    __device__ __forceinline__ int collect(float zc, float to, bool weigh, u64 &whole) {
+        u64 *own = s.all_sum;  // (not in use before the bins are joined)
+        u64 sum = 0;
+        for (int i = threadIdx.x; i < n4; i += kThreads) {
+            const float4 v = four(i);
+            const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int h = 0; h < 4; h += 2) {
+                const float2 d = dist2(x[h], x[h + 1]);
+                if (weigh && (d.x < kAll || d.y < kAll)) {
+                    uint32_t w[2], oct[2];
+                    mantissa2(make_float2(d.x < kAll ? d.x : 0.f, d.y < kAll ? d.y : 0.f), w, oct);
+                    sum += (d.x < kAll ? scaled(w[0], oct[0]) : 0) + (d.y < kAll ? scaled(w[1], oct[1]) : 0);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (!(x[h + e] <= zc && (e ? d.y : d.x) < to)) continue;
+                    const uint32_t at = atomicAdd(&s.own_n, 1u);
+                    if (at < kFew) own[at] = (u64)__float_as_uint(x[h + e]) << 32 | (base + 4 * i + h + e);
+                }
+            }
+        }
+        sum = block_sum(sum);
+        const u64 *all = exchange(sum, s.own_n);
+        int n = 0, at = 0;
+        for (uint32_t r = 0; r < ctas; ++r) {
+            if (r < rank) at += (int)all[kMaxCluster + r];
+            n += (int)all[kMaxCluster + r];
+            if (weigh) whole += all[r];
+        }
+        if (n > kFew) return n;
+        for (int i = threadIdx.x; i < (int)s.own_n; i += kThreads) {
+            const float x = __uint_as_float((uint32_t)(own[i] >> 32));
+            const u64 w = weight_of(dist(x));
+            peer_store(&s.list[at + i], 0, make_uint4(key_of(-x), (uint32_t)own[i], (uint32_t)w, (uint32_t)(w >> 32)));
+        }
+        cluster_sync();
+        return n;
+    }
     // Over the m tokens of CTA 0's list (m < 2^16; every thread of it calls): done(i, t, count, sum) for
     // each token t, with the number and the weight of the tokens that before(other, t) names.  A token is
     // the work of a few neighbouring lanes, one of which calls done.
@@ -502,7 +596,7 @@ struct Row {
                             atomicAdd(&s.hi[bin], v >> 12);
                         }
                         __syncthreads();
-                        const uint32_t sub = (uint32_t)max(find_bin(by_sum, need, cnt, sum, true, up), 0);
+                        const uint32_t sub = (uint32_t)max(find_bin(by_sum, need, kBins, cnt, sum, true, up), 0);
                         hi -= sub << shift;
                         lo = hi - min(hi - lo, (1u << shift) - 1);
                         // the tokens of that bin alone stay in the list
@@ -547,7 +641,7 @@ struct Row {
                 into_bin((int)((hi - key) >> shift), w[0], oct[0]);
             });
             join_bins([&](int) { return octave; });
-            const uint32_t sub = (uint32_t)max(find_bin(by_sum, need, cnt, sum), 0);
+            const uint32_t sub = (uint32_t)max(find_bin(by_sum, need, kBins, cnt, sum), 0);
             hi -= sub << shift;
             lo = hi - min(hi - lo, (1u << shift) - 1);
         }
@@ -567,26 +661,25 @@ struct Row {
 };
 
 struct Settings {
-    int64_t k;
+    int32_t k;
     uint32_t p_share, m_share, u;
     bool by_k, by_p;
 };
 
-// The row's token from the tokens down to bin `bin` alone, which hold everything that top-k, or without
-// it top-p, keeps.  whole: without top-k, the weight of the row.
+// The row's token from the n tokens of CTA 0's list alone, which hold everything that top-k, or without
+// it top-p, or min-p keeps.  whole: without top-k, the weight of the row.
 template <typename R>
-__device__ __forceinline__ void finish_few(R &r, const SampleArgs &a, int64_t m, const Settings &set, int bin, u64 whole) {
+__device__ __forceinline__ void finish_few(R &r, const SampleArgs &a, int64_t m, const Settings &set, int n, u64 whole, u64 least) {
     Shared &s = r.s;
-    const int n = min(r.gather(0.f, fminf(r.span, ldexpf((float)(bin + 1), -r.per_octave)), 0, 0xFFFFFFFFu), kFew);
     if (r.rank != 0) return;  // (no CTA touches another's memory from here on)
-    const u64 least = part_of(weight_of(0.f), set.m_share);
+    n = min(n, kFew);
     // each token's rank, and the weight before it; a thread has at most one token's
     static_assert(kFew <= kThreads, "one token a thread");
     int mine = -1;
     uint32_t rank = 0;
     u64 before = 0, weight = 0;
     r.compare_all(n, R::ranks_before, [&](int i, uint4 t, uint32_t k, u64 w) { mine = i, rank = k, before = w, weight = list_weight(t); });
-    bool keep = mine >= 0 && (!set.by_k || rank < (uint32_t)min(set.k, (int64_t)kFew));
+    bool keep = mine >= 0 && (!set.by_k || rank < (uint32_t)min(set.k, kFew));
     if (set.by_k) whole = r.block_sum(keep ? weight : 0);
     if (set.by_p) keep = keep && before < max(part_of(whole, set.p_share), (u64)1);
     keep = keep && weight >= least;
@@ -604,7 +697,7 @@ __device__ __forceinline__ void finish_few(R &r, const SampleArgs &a, int64_t m,
 
 // The row's cut and its token, after the load.
 template <typename R>
-__device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, const Settings &set) {
+__device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, const Settings &set, bool finite) {
     Shared &s = r.s;
     const int tid = threadIdx.x, lane = tid & 31;
     Cut cut = {-INFINITY, 0xFFFFFFFFu, 0};
@@ -612,9 +705,20 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
     // single row waits longer for instructions than for anything else).
     bool by_sum = !set.by_k, bins = false, all = false;
     u64 part = 0, whole = 0;  // whole: what top-k keeps
-    r.cover(set.by_k ? 6 : 5);
-    while (set.by_k || set.by_p) {
-        if (!bins) part = r.histogram(!set.by_k);
+    const u64 least = set.m_share > 0 ? part_of(weight_of(0.f), set.m_share) : 0;
+    // from this d on, w is below 2^(40 - limit) <= least / 2 (the series errs by far less than a factor 2)
+    const float limit = least > 0 ? fminf(kAll, 41.f - (float)(63 - __clzll((long long)least))) : kAll;
+    const bool bounded = limit < 16.f;
+    // Where top-k or min-p can be seen to leave few tokens, those alone.
+    int few = kFew + 1;
+    const bool by_best = finite && set.by_k && set.k <= kTop, last_k = !set.by_p, weigh = !set.by_k && set.by_p;
+    if (by_best || (bounded && !set.by_k))
+        few = r.collect(by_best ? -of_key(r.kth_best(set.k)) : INFINITY, weigh || last_k ? limit : kAll, weigh, whole);
+    r.cover(set.by_k || bounded ? 6 : 5);
+    while (few > kFew && (set.by_k || set.by_p)) {
+        // where the last cut lies beyond what min-p keeps, it need not be found
+        const int last = bounded && (by_sum || !set.by_p) ? r.bin_of(limit) : kBins;
+        if (!bins) part = r.histogram(fminf(r.span, ldexpf((float)(last + 1), -r.per_octave)), !set.by_k && whole == 0);
         bins = true;
         if (by_sum && whole == 0) {
             if (r.rank == 0)  // (the bins are the cluster's)
@@ -623,7 +727,7 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
         }
         const u64 need = by_sum ? max(part_of(whole, set.p_share), (u64)1) : (u64)set.k;
         u64 cnt = 0, sum = 0;
-        const int bin = r.find_bin(by_sum, need, cnt, sum);
+        const int bin = r.find_bin(by_sum, need, last, cnt, sum);
         if (bin < 0 && !all) {
             // beyond the bins: bins of every weight
             all = true;
@@ -633,10 +737,11 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
             continue;
         }
         if (bin >= 0 && by_sum != set.by_k && cnt + s.all_cnt[bin] <= (u64)kFew) {
-            finish_few(r, a, m, set, bin, whole);
-            return;
+            few = r.gather(0.f, fminf(r.span, ldexpf((float)(bin + 1), -r.per_octave)), 0, 0xFFFFFFFFu);
+            break;
         }
-        if (bin >= 0) {  // (otherwise fewer than k tokens have any weight)
+        // (-1: fewer than k tokens have any weight)
+        if (bin >= 0 && (by_sum ? sum + s.all_sum[bin] : cnt + s.all_cnt[bin]) >= need) {
             // where there are too many to gather, bins over keys take the place of those over d
             bins = !by_sum && s.all_cnt[bin] <= kList;
             cut = r.refine(by_sum, bin, need, cnt, sum);
@@ -646,11 +751,12 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
         if (by_sum || !set.by_p) break;
         by_sum = true;
     }
+    if (few <= kFew) {
+        finish_few(r, a, m, set, few, whole, least);
+        return;
+    }
     // ---- the token
-    const u64 least = part_of(weight_of(0.f), set.m_share);
     const float zc = -cut.z;
-    // from this d on, w is below 2^(40 - limit) <= least / 2 (the series errs by far less than a factor 2)
-    const float limit = least > 0 ? fminf(kAll, 41.f - (float)(63 - __clzll((long long)least))) : kAll;
     uint32_t idx;
     u64 w, total;
     const bool here = r.locate(
@@ -685,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     float *own = reinterpret_cast<float *>(dyn + (sizeof(Shared) + 15) / 16 * 16);
     const int tid = threadIdx.x;
     const uint32_t rank = cluster_ctarank(), ctas = a.ctas;
-    if (tid == 0) s.list_n[0] = s.list_n[1] = 0;
+    if (tid == 0) s.list_n[0] = s.list_n[1] = s.own_n = 0;
     for (int i = tid; i < kBins; i += kThreads) s.cnt[i] = s.lo[i] = s.hi[i] = 0;
     cluster_arrive();  // (waited for before the first access to another CTA's memory)
     pdl_wait();
@@ -693,39 +799,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const int64_t m = blockIdx.x / ctas;
     const int64_t i0 = min((int64_t)rank * per, (int64_t)a.V), i1 = min(i0 + per, (int64_t)a.V);
     const float *row = a.logits + m * a.ldl + i0;
-    Row<CACHED> r = {s, CACHED ? own : row, (uint32_t)i0, (int)(i1 - i0), ((int)(i1 - i0) + 3) / 4, rank, ctas, 0.f, 0.f, NAN, 0, 0.f, 0, 0};
-    // ---- load; the largest logit
-    float best = INFINITY;  // (of the negated ones, the smallest)
-    if (CACHED && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
-        const float4 *row4 = reinterpret_cast<const float4 *>(row);
-#pragma unroll 4
-        for (int i = tid; i < r.n / 4; i += kThreads) {
-            float4 v = __ldg(row4 + i);
-            v = make_float4(stored(v.x), stored(v.y), stored(v.z), stored(v.w));
-            reinterpret_cast<float4 *>(own)[i] = v;
-            best = fminf(fminf(best, fminf(v.x, v.y)), fminf(v.z, v.w));
-        }
-        for (int i = r.n / 4 * 4 + tid; i < r.n4 * 4; i += kThreads) {
-            own[i] = i < r.n ? stored(__ldg(row + i)) : INFINITY;
-            best = fminf(best, own[i]);
-        }
-    } else {
-#pragma unroll 8
-        for (int i = tid; i < (CACHED ? r.n4 * 4 : r.n); i += kThreads) {
-            const float v = i < r.n ? stored(__ldg(row + i)) : INFINITY;
-            if (CACHED) own[i] = v;
-            best = fminf(best, v);
-        }
-    }
-    cluster_wait();
-    r.top = of_key(r.cluster_max(key_of(-best)));
-    if (r.top == -INFINITY) {
-        if (rank == 0 && tid == 0) {
-            a.token[m] = -1;
-            if (a.prob) a.prob[m] = 0.f;
-        }
-        return;
-    }
+    const int head = (int)(reinterpret_cast<uintptr_t>(row) % 16 / 4), n = (int)(i1 - i0) + head;
+    row -= head;
+    Row<CACHED> r = {s, CACHED ? own : row, (uint32_t)i0 - head, head, n, (n + 3) / 4, rank, ctas, 0.f, 0.f, NAN, 0, 0.f, 0, 0};
     // ---- the row's settings
     float t = a.temperature ? __ldg(a.temperature + m) : 1.f;
     const bool greedy = !(t > 0.f);
@@ -738,7 +814,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     set.u = min(share_of(__ldg(a.u + m), 0), kOne - 1);
     set.by_k = set.k > 0 && set.k < a.V;
     set.by_p = set.p_share < kOne;
-    if (isinf(r.top) || isinf(r.c)) {
+    // ---- load; the largest logit
+    float best = INFINITY;  // (of the negated ones, the smallest)
+    auto take = [&](int i, float4 v) {
+        if (CACHED) reinterpret_cast<float4 *>(own)[i] = v;
+        best = fminf(fminf(best, fminf(v.x, v.y)), fminf(v.z, v.w));
+    };
+    const int whole0 = head > 0 ? 1 : 0, whole1 = n / 4;  // groups full of logits
+#pragma unroll 4
+    for (int i = whole0 + tid; i < whole1; i += kThreads) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(row) + i);
+        take(i, make_float4(stored(v.x), stored(v.y), stored(v.z), stored(v.w)));
+    }
+    if (tid < 2) {  // the first and the last group, where they are not
+        const int i = tid == 0 ? 0 : whole1;
+        if (tid == 0 ? whole0 > 0 : whole1 < r.n4) take(i, fetch(row, i, head, n));
+    }
+    cluster_wait();
+    r.top = of_key(r.cluster_best(key_of(-best)));
+    if (r.top == -INFINITY) {
+        if (rank == 0 && tid == 0) {
+            a.token[m] = -1;
+            if (a.prob) a.prob[m] = 0.f;
+        }
+        return;
+    }
+    const bool finite = !isinf(r.top) && !isinf(r.c);
+    if (!finite) {
         const float least = -r.top;
         __syncthreads();
         if (CACHED)
@@ -747,19 +849,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         r.top = 0.f, r.c = 1.f;
         __syncthreads();
     }
-    finish(r, a, m, set);
+    finish(r, a, m, set, finite);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const DeviceInfo &di, const SampleArgs &args, cudaStream_t s) {
-    (void)di;
     SampleArgs a = args;
-    // CTAs of a row: up to eight, a few thousand logits each at least
+    // CTAs of a row: up to eight, a few thousand logits each at least; fewer where the rows fill the
+    // device by themselves, as long as a row stays in shared memory
     a.ctas = a.V <= 4096 ? 1 : a.V <= 8192 ? 2 : a.V <= 16384 ? 4 : 8;
+    while (a.ctas > 1 && a.M * a.ctas > 2 * di.sm_count && a.V <= (int64_t)(a.ctas / 2) * (kCached - 8)) a.ctas /= 2;
     const int per = ((a.V + a.ctas - 1) / a.ctas + 3) / 4 * 4;
-    const bool cached = per <= kCached;
-    const int smem = (int)((sizeof(Shared) + 15) / 16 * 16) + (cached ? per * 4 : 0);
+    // A share stays in shared memory where that costs no CTA its place on an SM (the other way about, 10 rows
+    // of 164899 with top-k 400 took 44 us instead of 30, 174 of 176233 took 334 instead of 232).  It may
+    // begin inside a group.
+    const bool cached = per + 4 <= (a.M * a.ctas <= di.sm_count ? kCachedOne : kCached);
+    const int smem = (int)((sizeof(Shared) + 15) / 16 * 16) + (cached ? (per + 4) * 4 : 0);
     auto kern = cached ? sample_kernel<true> : sample_kernel<false>;
     cudaError_t e = ensure_smem((const void *)kern, smem);
     if (e != cudaSuccess) return e;

@@ -759,3 +759,68 @@ def test_sample_defaults_and_no_prob():
     token = torch.zeros(2, dtype=torch.int32, device="cuda")
     q4k.q4k_sample(z, 2, 3000, 3000, None, None, None, None, u, token)
     check_sample(z, None, None, None, None, u.tolist(), (token.tolist(), run_sample(z, u=u)[1]))
+
+
+@pytest.mark.parametrize("order", ["falling", "rising", "runs"])
+@pytest.mark.parametrize("V", [128, 1500, 6001, 40003])
+def test_sample_rows_in_order(order, V):
+    """Logits in order, so that the largest of a stretch say little about the k-th; k about the largest that they bound."""
+    g = gen_of(V + 2)
+    z = torch.sort(torch.randn(4, V, generator=g, device="cuda") * 2, dim=1, descending=order == "falling").values
+    if order == "runs":
+        z = z.view(4, -1).roll(V // 3, 1)
+    z = z.contiguous()
+    for k in (1, 2, 95, 96, 97, 128):
+        for p, m in ((1.0, 0.0), (0.9, 0.0), (0.97, 0.05), (1.0, 0.2)):
+            check_sample(z, [1.0, 0.5, 2.0, 0.9], k, p, m, [0.0, 0.4, 0.8, 1 - 2.0 ** -24])
+
+
+@pytest.mark.parametrize("near", [254, 255, 256, 257, 2000])
+def test_sample_tokens_that_min_p_keeps(near):
+    """As many tokens in reach of min-p as are ranked at once, one more, and many; top-p ends before, at and beyond them."""
+    V = 12007
+    g = gen_of(near)
+    for bulk in (-3.0, -9.0):
+        z = bulk + 0.1 * torch.randn(6, V, generator=g, device="cuda").clamp(-3, 3)
+        at = torch.randperm(V, generator=g, device="cuda")[:near + 1]
+        z[:, at] = -0.5 * torch.rand(6, near + 1, generator=g, device="cuda")
+        z[:, at[0]] = 0.0
+        z = z.contiguous()
+        u = [0.0, 0.2, 0.5, 0.7, 0.95, 1 - 2.0 ** -24]
+        for p in (0.05, 0.5, 0.9, 0.999, 1.0):
+            for k in (0, 60, near):
+                check_sample(z, 1.0, k, p, 0.3, u)
+
+
+@pytest.mark.parametrize("V", [4097, 9001, 17003, 39001, 80021])
+def test_sample_many_rows(V):
+    """So many rows that fewer CTAs share one."""
+    g = gen_of(V + 3)
+    M = 310 if V < 5000 else 160
+    z = torch.randn(M, V, generator=g, device="cuda") * 2.5
+    k = [(0, 50, 1, 300)[i % 4] for i in range(M)]
+    p = [(0.9, 1.0, 0.5)[i % 3] for i in range(M)]
+    m = [(0.0, 0.02, 0.0, 0.0, 0.1)[i % 5] for i in range(M)]
+    check_sample(z, 0.8, k, p, m, torch.rand(M, generator=g, device="cuda").tolist())
+
+
+@pytest.mark.parametrize("M,V", [(21, 156011), (2, 390001)])
+def test_sample_rows_beyond_shared_memory(M, V):
+    g = gen_of(V)
+    z = torch.randn(M, V, generator=g, device="cuda") * 2.2
+    k = [(50, 0, 3, 5000)[i % 4] for i in range(M)]
+    p = [(0.9, 0.95, 1.0)[i % 3] for i in range(M)]
+    m = [(0.0, 0.02)[i % 2] for i in range(M)]
+    check_sample(z, 1.0, k, p, m, torch.rand(M, generator=g, device="cuda").tolist())
+
+
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+def test_sample_rows_off_16_bytes(offset):
+    """What lies before and behind a row in its first and last 16 bytes is no part of it."""
+    g = gen_of(60 + offset)
+    for V in (1, 2, 3, 4, 5, 6, 7, 1030, 4098, 16391):
+        raw = torch.full((3, V + 8), float("inf"), device="cuda")
+        z = raw[:, offset:offset + V]
+        z.copy_(torch.randn(3, V, generator=g, device="cuda") * 2)
+        for k, p, m in ((0, 1.0, 0.0), (2, 1.0, 0.0), (0, 0.8, 0.0), (0, 0.9, 0.1)):
+            check_sample(z, 1.0, k, p, m, torch.rand(3, generator=g, device="cuda").tolist())
