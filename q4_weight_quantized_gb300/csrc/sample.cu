@@ -13,7 +13,8 @@
 //      (at least k logits are as large as the k-th of these);
 //   2. where top-k (k <= 96) or min-p can be seen to leave few tokens, those are gathered in
 //      one CTA, the row's weight is summed meanwhile if top-p asks for it, and that CTA ranks
-//      them and draws.  Otherwise:
+//      them and draws.  If they are many, but top-p ends beyond what min-p keeps, step 5
+//      follows.  Otherwise:
 //   3. the number and the weight of the tokens in bins of d.  With top-k or min-p the cut
 //      is near the top: 64 bins to each of 16 octaves, and with top-k what lies below is not
 //      even weighed.  Otherwise 32 to each of 32; the rest is added up without bins.  If the cut
@@ -29,8 +30,8 @@
 // two 12-bit halves of a 24-bit number by 32-bit atomics without a result.
 // Bound for many rows by the arithmetic of the weights (half of it on two logits at once) and
 // the exchanges that two CTAs on an SM do not hide, for one row by the exchanges and the fetch
-// of instructions that are used once.  Measured: 9.4 us for a row of 128001 with top-k 50 and
-// top-p (13.1 without step 2), 149 us for 256 rows of 151936 with top-p and min-p (229).
+// of instructions that are used once.  Measured: 9.6 us for a row of 128001 with top-k 50 and
+// top-p (13.1 without step 2), 131 us for 256 rows of 151936 with top-p and min-p (229).
 
 #include <cuda_runtime.h>
 
@@ -48,8 +49,8 @@ constexpr int kFew = 256;            // tokens that are ranked against each othe
 constexpr int kMaxCluster = 8;
 constexpr int kBests = 128;          // parts of a row whose largest logits bound the k-th from below
 constexpr int kTop = 96;             // the largest k for that: some 180 of independent logits lie above the bound
-constexpr int kCached = 19456;       // logits of a CTA that stay in shared memory with two CTAs on an SM
-constexpr int kCachedOne = 47104;    // and with one
+constexpr int kCached = 19328;       // logits of a CTA that stay in shared memory with two CTAs on an SM
+constexpr int kCachedOne = 47000;    // and with one
 constexpr float kAll = 41.f;         // from this d on the weight is 0
 constexpr uint32_t kOne = 1u << 24;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
@@ -95,7 +96,8 @@ __device__ __forceinline__ float2 sum2_down(float2 a, float2 b) {
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // floor(2^24 2^-f) and n of two distances 0 <= d < 2^22, n = floor(d), f = d - n: the series
-// of 2^-f about f = 1/2, coefficients 2^-1/2 (-ln 2)^i / i!.
+// of 2^-f about f = 1/2, coefficients 2^-1/2 (-ln 2)^i / i!.  It lies in [1/2, 1] for every f, where the
+// bits of an fp32 number p are 2^24 p + 0x3E800000.
 __device__ __forceinline__ void mantissa2(float2 d, uint32_t (&w)[2], uint32_t (&n)[2]) {
     // 2^23 + d, rounded down, is 2^23 + n
     const float2 t = sum2_down(d, both(8388608.f));
@@ -109,8 +111,7 @@ __device__ __forceinline__ void mantissa2(float2 d, uint32_t (&w)[2], uint32_t (
     p = sum2(mul2(p, f), both(0.16986578702926636f));
     p = sum2(mul2(p, f), both(-0.4901290833950043f));
     p = sum2(mul2(p, f), both(0.7071067690849304f));
-    p = mul2(p, both(16777216.f));
-    w[0] = (uint32_t)p.x, w[1] = (uint32_t)p.y;
+    w[0] = __float_as_uint(p.x) - 0x3E800000u, w[1] = __float_as_uint(p.y) - 0x3E800000u;
 }
 __device__ __forceinline__ u64 scaled(uint32_t w, uint32_t n) { return ((u64)w << 16) >> n; }
 __device__ __forceinline__ u64 weight_of(float d) {  // d < kAll
@@ -161,7 +162,7 @@ struct Shared {
     u64 all_sum[kBins];
     uint4 list[kList];  // key, index, weight (CTA 0's is used)
     u64 warp_u64[kWarps];
-    u64 slot[2][2 * kMaxCluster];  // exchanged values
+    u64 slot[2][3 * kMaxCluster];  // exchanged values
     alignas(16) uint32_t best[kBests];       // largest keys of parts of the row
     u64 found_sum, ranked_sum;
     uint32_t warp_u32[kWarps];
@@ -220,14 +221,15 @@ struct Row {
         span = fminf(kAll, (float)(kBins >> log_bins));
     }
 
-    // Every CTA's value (or two) to all CTAs, by rank.  Two slots in turn, so one barrier an
+    // Every CTA's value (or up to three) to all CTAs, by rank.  Two slots in turn, so one barrier an
     // exchange is enough.
-    __device__ __forceinline__ const u64 *exchange(u64 v, u64 v2 = 0) {
+    __device__ __forceinline__ const u64 *exchange(u64 v, u64 v2 = 0, u64 v3 = 0) {
         u64 *slot = s.slot[turn];
         turn ^= 1;
         if (threadIdx.x < ctas) {
             peer_store(slot + rank, threadIdx.x, v);
             peer_store(slot + kMaxCluster + rank, threadIdx.x, v2);
+            peer_store(slot + 2 * kMaxCluster + rank, threadIdx.x, v3);
         }
         cluster_sync();
         return slot;
@@ -490,36 +492,40 @@ struct Row {
         return m;
     }
     // Tokens of d < to and no logit below -zc, into CTA 0's list if they are at most kFew: their number.
-    // weigh: the row's weight, too.
-    __device__ __forceinline__ int collect(float zc, float to, bool weigh, u64 &whole) {
+    // weigh: their weight and the row's, too.
+    __device__ __forceinline__ int collect(float zc, float to, bool weigh, u64 &reach, u64 &whole) {
         u64 *own = s.all_sum;  // (not in use before the bins are joined)
-        u64 sum = 0;
+        u64 sum = 0, in = 0;
         for (int i = threadIdx.x; i < n4; i += kThreads) {
             const float4 v = four(i);
             const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int h = 0; h < 4; h += 2) {
                 const float2 d = dist2(x[h], x[h + 1]);
-                if (weigh && (d.x < kAll || d.y < kAll)) {
-                    uint32_t w[2], oct[2];
-                    mantissa2(make_float2(d.x < kAll ? d.x : 0.f, d.y < kAll ? d.y : 0.f), w, oct);
-                    sum += (d.x < kAll ? scaled(w[0], oct[0]) : 0) + (d.y < kAll ? scaled(w[1], oct[1]) : 0);
+                u64 w[2] = {0, 0};
+                if (weigh) {
+                    uint32_t wm[2], oct[2];
+                    mantissa2(make_float2(fminf(d.x, 60.f), fminf(d.y, 60.f)), wm, oct);  // (from kAll on, 0)
+                    w[0] = scaled(wm[0], oct[0]), w[1] = scaled(wm[1], oct[1]);
+                    sum += w[0] + w[1];
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (!(x[h + e] <= zc && (e ? d.y : d.x) < to)) continue;
                     const uint32_t at = atomicAdd(&s.own_n, 1u);
                     if (at < kFew) own[at] = (u64)__float_as_uint(x[h + e]) << 32 | (base + 4 * i + h + e);
+                    in += w[e];
                 }
             }
         }
         sum = block_sum(sum);
-        const u64 *all = exchange(sum, s.own_n);
+        if (weigh) in = block_sum(in);
+        const u64 *all = exchange(sum, s.own_n, in);
         int n = 0, at = 0;
         for (uint32_t r = 0; r < ctas; ++r) {
             if (r < rank) at += (int)all[kMaxCluster + r];
             n += (int)all[kMaxCluster + r];
-            if (weigh) whole += all[r];
+            if (weigh) whole += all[r], reach += all[2 * kMaxCluster + r];
         }
         if (n > kFew) return n;
         for (int i = threadIdx.x; i < (int)s.own_n; i += kThreads) {
@@ -704,8 +710,8 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
     // First the cut of top-k, if any, then that of top-p: each phase's code is there once (inlined twice, a
     // single row waits longer for instructions than for anything else).
     bool by_sum = !set.by_k, bins = false, all = false;
-    u64 part = 0, whole = 0;  // whole: what top-k keeps
-    const u64 least = set.m_share > 0 ? part_of(weight_of(0.f), set.m_share) : 0;
+    u64 part = 0, whole = 0, reach = 0;  // whole: what top-k keeps
+    const u64 least = (u64)set.m_share << 16;  // (the largest weight is 2^40)
     // from this d on, w is below 2^(40 - limit) <= least / 2 (the series errs by far less than a factor 2)
     const float limit = least > 0 ? fminf(kAll, 41.f - (float)(63 - __clzll((long long)least))) : kAll;
     const bool bounded = limit < 16.f;
@@ -713,9 +719,10 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
     int few = kFew + 1;
     const bool by_best = finite && set.by_k && set.k <= kTop, last_k = !set.by_p, weigh = !set.by_k && set.by_p;
     if (by_best || (bounded && !set.by_k))
-        few = r.collect(by_best ? -of_key(r.kth_best(set.k)) : INFINITY, weigh || last_k ? limit : kAll, weigh, whole);
+        few = r.collect(by_best ? -of_key(r.kth_best(set.k)) : INFINITY, weigh || last_k ? limit : kAll, weigh, reach, whole);
     r.cover(set.by_k || bounded ? 6 : 5);
-    while (few > kFew && (set.by_k || set.by_p)) {
+    // (nor need a cut of top-p be found that lies beyond what min-p keeps)
+    while (few > kFew && (set.by_k || (set.by_p && !(weigh && bounded && reach < part_of(whole, set.p_share))))) {
         // where the last cut lies beyond what min-p keeps, it need not be found
         const int last = bounded && (by_sum || !set.by_p) ? r.bin_of(limit) : kBins;
         if (!bins) part = r.histogram(fminf(r.span, ldexpf((float)(last + 1), -r.per_octave)), !set.by_k && whole == 0);

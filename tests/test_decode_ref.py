@@ -128,3 +128,12 @@ def test_sample_frequencies():
     got = np.bincount([R.sample(z, 0.8, 0, 1.0, 0.0, x)[0] for x in u], minlength=12) / 4000
     assert np.abs(got - p).max() <= 1 / 4000 + 1e-6
     assert math.isclose(sum(got), 1)
+
+
+def test_sample_weight_stays_in_its_octave():
+    """The series ends in [1/2, 1] for every fraction near 0 and near 1, so 24 bits hold it exactly."""
+    grid = np.arange(2 ** 22, dtype=np.float64)
+    for d in (grid * 2.0 ** -25, 0.75 + grid * 2.0 ** -24):
+        w = R.sample_weight(d.astype(np.float32))
+        assert w.min() >= 2 ** 39 and w.max() <= 2 ** 40
+    assert R.sample_weight(0.0) == 2 ** 40
