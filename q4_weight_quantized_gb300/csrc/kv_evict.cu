@@ -13,8 +13,11 @@
 // order, four to a thread, and numbers holes and fillers by one scan per tile.  Bound by
 // latency (some twenty block-wide steps; 256 threads for caches of up to 4096 slots, whose
 // steps would otherwise cost more in idle warps than in work); the reads are 8 bytes a slot.
-// move_kernel copies the rows, 16 bytes a lane: bound by HBM (two or four rows a thread cost
-// more in occupancy than their overlapping loads gave: 62 and 70 us against 59).
+// move_kernel copies the rows, 16 bytes a lane, and their weights and positions: bound by HBM (two or
+// four rows a thread cost more in occupancy than their overlapping loads gave: 62 and 70 us against 59).
+// Measured: 9.6 us for 32 caches of 8 heads with one slot over 2048 (7 of them the selection), 82 us for
+// 16 caches of 9001 to 16384 slots to 8192 (17 the selection, 59 the copies: 333 MB at 5.7 TB/s).
+
 #include <cuda_runtime.h>
 
 #include "decode_ops.h"
@@ -253,12 +256,16 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
             // many equal keys: the need-th of them by slot
             cut = lo;
             uint32_t run = 0;
-            for (int j0 = 0, turn = 0; j0 < n; j0 += THREADS, turn ^= 1) {
-                const int j = j0 + tid;
-                const bool is = j < n && key_at(j) == cut && prot_at(j) == in_prot;
-                uint32_t total;
-                const uint32_t before = run + B::scan(is, scratch[turn], total);
-                if (is && before + 1 == need) found[0] = j;
+            for (int j0 = 0, turn = 0; j0 < n && run < need; j0 += 4 * THREADS, turn ^= 1) {
+                const int j = j0 + 4 * tid;
+                uint32_t is = 0, total;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (j + x < n && key_at(j + x) == cut && prot_at(j + x) == in_prot) is |= 1u << x;
+                uint32_t before = run + B::scan(__popc(is), scratch[turn], total);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if ((is >> x & 1) && ++before == need) found[0] = j + x;
                 run += total;
             }
             __syncthreads();
@@ -324,12 +331,6 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
         holes += total & 0xFFFF;
         fills += total >> 16;
     }
-    __syncthreads();
-    for (uint32_t i = tid; i < holes; i += THREADS) {
-        const int2 m = list_out[i];
-        w_out[m.x] = w[m.y];
-        p_out[m.x] = p[m.y];
-    }
     if (tid == 0) a.count[bh] = (int32_t)holes;
 }
 
@@ -354,6 +355,13 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
     const int n = a.count[bh];
     const int2 *list = a.moves + (int64_t)bh * a.max_moves;
     const int32_t *table = a.c.table + b * a.c.ld_table;
+    // (here rather than at the end of the selection, which every head waits for)
+    const int64_t meta = (int64_t)bh * a.ld_meta;
+    for (int i = part * kMoveThreads + threadIdx.x; i < n; i += per_head * kMoveThreads) {
+        const int2 m = list[i];
+        a.weights_out[meta + m.x] = a.weights[meta + m.y];
+        a.positions_out[meta + m.x] = a.positions[meta + m.y];
+    }
     const int rows = kMoveThreads / chunks, ch = threadIdx.x % chunks;
     for (int i = part * rows + threadIdx.x / chunks; i < n; i += per_head * rows) {
         const int2 m = list[i];

@@ -493,6 +493,25 @@ def test_evict(dtype, D, page, layout, Hkv, lens, budget, sinks, recent, kind, i
             assert torch.equal(u8(now)[pg, :, j % page], u8(was)[pg, :, j % page])
 
 
+@pytest.mark.parametrize("n", [1100, 4090, 9001, 20011, 30001, 50021])
+@pytest.mark.parametrize("part", [0.01, 0.5, 0.99])
+def test_evict_equal_weights_over_many_slots(n, part):
+    """Far more equal weights than are ranked at once: those in the lowest slots go, however far in they end."""
+    g = gen_of(n)
+    page, D = 64, 64
+    per = -(-n // page)
+    k, v = pool((per, 1, page, D), BF, "phsd", g)
+    table = table_of(1, per, per, g)
+    ld = per * page
+    w = torch.floor(torch.rand(1, 1, ld, generator=g, device="cuda") * 1.5)  # two thirds 0
+    p = torch.randperm(ld, generator=g, device="cuda").view(1, 1, ld).int()
+    budget, was = n - max(1, int(part * 0.6 * n)), p[0, 0].tolist()
+    _, take = R.kv_evict([n], w.cpu().numpy(), p.cpu().numpy(), budget, 1, 5)
+    got, wo, po = run_evict(q4k.kv_cache(k, v, table), [n], budget, 1, 5, w, p, True)
+    q4k.q4k_check_device()
+    assert got.tolist() == [budget] and po[0, 0, :budget].tolist() == [was[j] for j in take[0][0]]
+
+
 def test_evict_bad_indices():
     g = gen_of(31)
     k, v = pool((4, 1, 16, 64), BF, "phsd", g)
