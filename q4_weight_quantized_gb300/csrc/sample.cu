@@ -12,8 +12,8 @@
 //   1. load, largest logits of 128 parts of the row: its largest, and a bound below the k-th
 //      (at least k logits are as large as the k-th of these);
 //   2. where top-k (k <= 96) or min-p can be seen to leave few tokens, those are gathered in
-//      one CTA, the row's weight is summed meanwhile if top-p asks for it, and that CTA ranks
-//      them and draws.  If they are many, but top-p ends beyond what min-p keeps, step 5
+//      one CTA by index, the row's weight is summed meanwhile if top-p asks for it, and that CTA
+//      ranks them, where a cut may lie among them, and draws.  If they are many, but top-p ends beyond what min-p keeps, step 5
 //      follows.  Otherwise:
 //   3. the number and the weight of the tokens in bins of d.  With top-k or min-p the cut
 //      is near the top: 64 bins to each of 16 octaves, and with top-k what lies below is not
@@ -31,7 +31,7 @@
 // Bound for many rows by the arithmetic of the weights (half of it on two logits at once) and
 // the exchanges that two CTAs on an SM do not hide, for one row by the exchanges and the fetch
 // of instructions that are used once.  Measured: 9.6 us for a row of 128001 with top-k 50 and
-// top-p (13.1 without step 2), 131 us for 256 rows of 151936 with top-p and min-p (229).
+// top-p (13.1 without step 2), 126 us for 256 rows of 151936 with top-p and min-p (229).
 
 #include <cuda_runtime.h>
 
@@ -491,10 +491,10 @@ struct Row {
         if (rank == 0 && threadIdx.x == 0) s.list_n[counter] = 0;
         return m;
     }
-    // Tokens of d < to and no logit below -zc, into CTA 0's list if they are at most kFew: their number.
-    // weigh: their weight and the row's, too.
+    // Tokens of d < to and no logit below -zc, into CTA 0's list by index, if they are at most kFew: their
+    // number.  weigh: their weight and the row's, too.
     __device__ __forceinline__ int collect(float zc, float to, bool weigh, u64 &reach, u64 &whole) {
-        u64 *own = s.all_sum;  // (not in use before the bins are joined)
+        u64 *own = s.all_sum;  // (not in use before the bins are joined, and after the last look at them)
         u64 sum = 0, in = 0;
         for (int i = threadIdx.x; i < n4; i += kThreads) {
             const float4 v = four(i);
@@ -520,7 +520,9 @@ struct Row {
         }
         sum = block_sum(sum);
         if (weigh) in = block_sum(in);
-        const u64 *all = exchange(sum, s.own_n, in);
+        const int m = (int)s.own_n;
+        const u64 *all = exchange(sum, m, in);
+        if (threadIdx.x == 0) s.own_n = 0;
         int n = 0, at = 0;
         for (uint32_t r = 0; r < ctas; ++r) {
             if (r < rank) at += (int)all[kMaxCluster + r];
@@ -528,10 +530,20 @@ struct Row {
             if (weigh) whole += all[r], reach += all[2 * kMaxCluster + r];
         }
         if (n > kFew) return n;
-        for (int i = threadIdx.x; i < (int)s.own_n; i += kThreads) {
-            const float x = __uint_as_float((uint32_t)(own[i] >> 32));
-            const u64 w = weight_of(dist(x));
-            peer_store(&s.list[at + i], 0, make_uint4(key_of(-x), (uint32_t)own[i], (uint32_t)w, (uint32_t)(w >> 32)));
+        int team = 1;  // neighbouring lanes that count the tokens before one
+        while (team < 32 && 2 * team * m <= kThreads) team *= 2;
+        const int mate = threadIdx.x & (team - 1), i = threadIdx.x / team;
+        static_assert(kFew <= kThreads, "one token a thread");
+        if (m > 0) {
+            const u64 me = own[min(i, m - 1)];
+            int before = 0;
+            for (int j = mate; j < m; j += team) before += (uint32_t)own[j] < (uint32_t)me ? 1 : 0;
+            for (int o = 1; o < team; o <<= 1) before += __shfl_xor_sync(kFull, before, o);
+            if (i < m && mate == 0) {
+                const float x = __uint_as_float((uint32_t)(me >> 32));
+                const u64 w = weight_of(dist(x));
+                peer_store(&s.list[at + before], 0, make_uint4(key_of(-x), (uint32_t)me, (uint32_t)w, (uint32_t)(w >> 32)));
+            }
         }
         cluster_sync();
         return n;
@@ -672,33 +684,40 @@ struct Settings {
     bool by_k, by_p;
 };
 
-// The row's token from the n tokens of CTA 0's list alone, which hold everything that top-k, or without
-// it top-p, or min-p keeps.  whole: without top-k, the weight of the row.
+// The row's token from the n tokens of CTA 0's list alone, which are in order and hold everything that
+// top-k, or without it top-p, or min-p keeps.  whole: without top-k, the weight of the row; reach: the
+// tokens' own, or 0.
 template <typename R>
-__device__ __forceinline__ void finish_few(R &r, const SampleArgs &a, int64_t m, const Settings &set, int n, u64 whole, u64 least) {
+__device__ __forceinline__ void finish_few(R &r, const SampleArgs &a, int64_t m, const Settings &set, int n, u64 whole, u64 reach, u64 least) {
     Shared &s = r.s;
     if (r.rank != 0) return;  // (no CTA touches another's memory from here on)
-    n = min(n, kFew);
-    // each token's rank, and the weight before it; a thread has at most one token's
-    static_assert(kFew <= kThreads, "one token a thread");
-    int mine = -1;
-    uint32_t rank = 0;
-    u64 before = 0, weight = 0;
-    r.compare_all(n, R::ranks_before, [&](int i, uint4 t, uint32_t k, u64 w) { mine = i, rank = k, before = w, weight = list_weight(t); });
-    bool keep = mine >= 0 && (!set.by_k || rank < (uint32_t)min(set.k, kFew));
-    if (set.by_k) whole = r.block_sum(keep ? weight : 0);
-    if (set.by_p) keep = keep && before < max(part_of(whole, set.p_share), (u64)1);
-    keep = keep && weight >= least;
-    const u64 total = r.block_sum(keep ? weight : 0);  // (its barriers stand between the list's reads and writes)
-    if (mine >= 0 && !keep) s.list[mine].z = s.list[mine].w = 0;
-    __syncthreads();
-    const u64 goal = part_of(total, set.u);
-    r.compare_all(n, [](uint4 o, uint4 t) { return o.y < t.y; }, [&](int, uint4 t, uint32_t, u64 w) {
-        if (w <= goal && goal < w + list_weight(t)) {
-            a.token[m] = (int32_t)t.y;
-            if (a.prob) a.prob[m] = __fdiv_rn((float)list_weight(t), (float)total);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint4 mine = s.list[min(tid, kList - 1)];
+    u64 weight = tid < n ? list_weight(mine) : 0;
+    // each token's rank, and the weight before it, where a cut may lie among them
+    u64 need = set.by_p ? max(part_of(whole, set.p_share), (u64)1) : 0;
+    if (set.by_k ? set.by_p || n > set.k : set.by_p && (reach == 0 || reach > need)) {
+        r.compare_all(n, R::ranks_before, [&](int i, uint4, uint32_t k, u64 w) { s.all_cnt[i] = k, s.all_sum[i] = w; });
+        __syncthreads();
+        if (set.by_k) {
+            if (tid < n && s.all_cnt[tid] >= (uint32_t)set.k) weight = 0;
+            if (set.by_p) need = max(part_of(r.block_sum(weight), set.p_share), (u64)1);
         }
-    });
+        if (set.by_p && tid < n && s.all_sum[tid] >= need) weight = 0;
+    }
+    if (weight < least) weight = 0;
+    const u64 total = r.block_sum(weight), goal = part_of(total, set.u);
+    u64 to = weight;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 t = __shfl_up_sync(kFull, to, o);
+        if (lane >= o) to += t;
+    }
+    to += warp_sum(lane < warp ? s.warp_u64[lane] : 0ull);
+    if (to - weight <= goal && goal < to) {
+        a.token[m] = (int32_t)mine.y;
+        if (a.prob) a.prob[m] = __fdiv_rn((float)weight, (float)total);
+    }
 }
 
 // The row's cut and its token, after the load.
@@ -744,7 +763,8 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
             continue;
         }
         if (bin >= 0 && by_sum != set.by_k && cnt + s.all_cnt[bin] <= (u64)kFew) {
-            few = r.gather(0.f, fminf(r.span, ldexpf((float)(bin + 1), -r.per_octave)), 0, 0xFFFFFFFFu);
+            reach = 0;
+            few = r.collect(INFINITY, fminf(r.span, ldexpf((float)(bin + 1), -r.per_octave)), false, reach, part);
             break;
         }
         // (-1: fewer than k tokens have any weight)
@@ -759,7 +779,7 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
         by_sum = true;
     }
     if (few <= kFew) {
-        finish_few(r, a, m, set, few, whole, least);
+        finish_few(r, a, m, set, few, whole, reach, least);
         return;
     }
     // ---- the token
