@@ -883,80 +883,81 @@ __device__ __forceinline__ const float *part_at(const AttnArgs &a, const Parts &
 }
 constexpr int kJoinWarps = 16;  // of a block, at most
 
-// (m, l) of the 8 rows of octet n over the unit's parts; every thread of the block calls it.  Row lane % 8's come
-// back to every lane.  scratch: [2][kJoinWarps][8]
-__device__ __forceinline__ float2 join_ml(const AttnArgs &a, const Parts &p, int n, float (*scratch)[kJoinWarps][8]) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+// (m, l) of row lane % 8 of octet n over the unit's parts x / 8, x = first, first + step, ... (multiples of 32 and
+// the lane), joined over the lanes of the row.  kAhead: loads on their way at once.
+template <int kAhead>
+__device__ __forceinline__ float2 join_parts(const AttnArgs &a, const Parts &p, int n, int first, int step) {
     const int parts = p.last - p.first + 1;
-    // thread x: row x % 8 of some of the parts
     float top = kNone, sum = 0.f;
-    for (int x = tid; x < parts * 8; x += blockDim.x) {
-        const float2 ml = *reinterpret_cast<const float2 *>(part_at(a, p, p.first + x / 8) + 2 * (n * 8 + x % 8));
-        if (ml.x == kNone) {
-            sum += ml.y;  // 0, or NaN where every score is
-            continue;
+    for (int x0 = first; x0 < parts * 8; x0 += kAhead * step) {
+        float2 ml[kAhead];
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            const int x = x0 + y * step;
+            ml[y] = x < parts * 8 ? *reinterpret_cast<const float2 *>(part_at(a, p, p.first + x / 8) + 2 * (n * 8 + x % 8)) : make_float2(kNone, 0.f);
         }
-        const float m = fmaxf(top, ml.x);
-        sum = sum * ex2_approx(top - m) + ml.y * ex2_approx(ml.x - m);
-        top = m;
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            if (ml[y].x == kNone) {
+                sum += ml[y].y;  // 0, or NaN where every score is
+                continue;
+            }
+            const float m = fmaxf(top, ml[y].x);
+            sum = sum * ex2_approx(top - m) + ml[y].y * ex2_approx(ml[y].x - m);
+            top = m;
+        }
     }
     float m = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
     m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
     if (top != kNone) sum *= ex2_approx(top - m);
     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
-    __syncthreads();  // (what the scratch held has been read)
-    if (lane < 8) scratch[0][warp][lane] = m, scratch[1][warp][lane] = sum;
-    __syncthreads();
+    return make_float2(m, sum);
+}
+// That of row `row` over warps w0, w0 + step, ... < w1, from scratch ([2][kJoinWarps][8]).
+__device__ __forceinline__ float2 join_warps(const float (*scratch)[kJoinWarps][8], int row, int w0, int w1, int step) {
     float mt = kNone, lt = 0.f;
-    for (int w = 0; w < warps; ++w) mt = fmaxf(mt, scratch[0][w][lane & 7]);
-    for (int w = 0; w < warps; ++w) {
-        const float mw = scratch[0][w][lane & 7];
-        lt += scratch[1][w][lane & 7] * (mw == kNone ? 1.f : ex2_approx(mw - mt));
+    for (int w = w0; w < w1; w += step) mt = fmaxf(mt, scratch[0][w][row]);
+    for (int w = w0; w < w1; w += step) {
+        const float mw = scratch[0][w][row];
+        lt += scratch[1][w][row] * (mw == kNone ? 1.f : ex2_approx(mw - mt));
     }
     return make_float2(mt, lt);
 }
-
-// A chunk of slots of one KV head's weights: weights <- decay * weights + sum of the rows' 2^(s - m) / l.
-__device__ __forceinline__ void weigh(const AttnArgs &a, uint32_t id, int chunks, int chunk, float *sm_m, float *sm_r,
-                                      float (*scratch)[kJoinWarps][8]) {
-    const uint32_t bh = id / (uint32_t)chunks;
-    const int b = (int)(bh / (uint32_t)a.c.heads), h = (int)(bh - (uint32_t)b * (uint32_t)a.c.heads);
-    int begin, len;
-    seq_range(a, b, begin, len);
-    const int lo = (int)(id - bh * (uint32_t)chunks) * chunk, hi = min(lo + chunk, len), threads = blockDim.x;
-    if (lo >= len) return;
-    if (hi > begin)
-        for (int rt = 0; rt < a.row_tiles; ++rt) {
-            const Parts p = parts_of(a, b, h * a.row_tiles + rt);
-            for (int n = 0; n < a.tile_rows / 8; ++n) {
-                const int r = rt * a.tile_rows + n * 8 + (threadIdx.x & 7);
-                const float2 ml = p.whole ? a.unit_ml[((int64_t)b * a.unit_heads + h * a.row_tiles) * a.tile_rows + r]
-                                          : join_ml(a, p, n, scratch);
-                if (threadIdx.x < 8 && r < a.rows) {
-                    sm_m[r] = ml.x == kNone ? 0.f : ml.x;
-                    sm_r[r] = ml.y > 0.f || ml.y != ml.y ? ex2_approx(lift(a.c.e4m3 != 0)) / ml.y : 0.f;
-                }
-            }
-        }
+// (m, l) of the 8 rows of octet n over all parts; every thread of the block calls it.  Row lane % 8's come back
+// to every lane.
+template <int kAhead>
+__device__ __forceinline__ float2 join_ml(const AttnArgs &a, const Parts &p, int n, float (*scratch)[kJoinWarps][8]) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const float2 own = join_parts<kAhead>(a, p, n, tid, blockDim.x);
+    __syncthreads();  // (what the scratch held has been read)
+    if (lane < 8) scratch[0][warp][lane] = own.x, scratch[1][warp][lane] = own.y;
     __syncthreads();
-    float *w = a.weights + (int64_t)bh * a.ld_weights;
-    const float *z = a.logits + (int64_t)bh * a.rows * a.ld_logits;
-    constexpr int kAt = 4, kRowsAhead = 4;  // slots of a thread at a time; rows whose scores are on their way at once
-    for (int j0 = lo + threadIdx.x; j0 < hi; j0 += kAt * threads) {
+    return join_warps(scratch, lane & 7, 0, warps, 1);
+}
+
+// Weights w of slots lo .. hi - 1 from the rows' scores z.  GROUPS: a chunk is fewer slots than the block takes at a
+// time, and its rows are dealt to groups of threads, whose sums are added in red.
+template <bool GROUPS, int kAt>
+__device__ __forceinline__ void add_up(const AttnArgs &a, float *w, const float *z, int begin, int lo, int hi, int chunk, const float *sm_m,
+                                       const float *sm_r, float *red) {
+    constexpr int kRowsAhead = 4;  // rows whose scores are on their way at once
+    const int groups = GROUPS ? kAt * blockDim.x / chunk : 1, per = blockDim.x / groups;
+    const int group = GROUPS ? threadIdx.x / per : 0, t = threadIdx.x - group * per;
+    for (int j0 = lo + t; GROUPS || j0 < hi; j0 += kAt * per) {
         float sum[kAt], old[kAt];
 #pragma unroll
         for (int x = 0; x < kAt; ++x) {
             sum[x] = 0.f;
-            if (j0 + x * threads < hi) old[x] = w[j0 + x * threads];
+            if (group == 0 && j0 + x * per < hi) old[x] = w[j0 + x * per];
         }
-        for (int r0 = 0; r0 < a.rows; r0 += kRowsAhead) {
+        for (int r0 = group * kRowsAhead; r0 < a.rows; r0 += groups * kRowsAhead) {
             float s[kRowsAhead][kAt];
 #pragma unroll
             for (int y = 0; y < kRowsAhead; ++y)
 #pragma unroll
                 for (int x = 0; x < kAt; ++x) {
-                    const int j = j0 + x * threads;
+                    const int j = j0 + x * per;
                     s[y][x] = r0 + y < a.rows && j >= begin && j < hi ? __ldg(z + (r0 + y) * a.ld_logits + j) : kNone;
                 }
 #pragma unroll
@@ -967,26 +968,80 @@ __device__ __forceinline__ void weigh(const AttnArgs &a, uint32_t id, int chunks
                 for (int x = 0; x < kAt; ++x) sum[x] = s[y][x] == kNone ? sum[x] : fmaf(ex2_approx(s[y][x] - m), f, sum[x]);
             }
         }
+        if constexpr (GROUPS) {
+            if (group > 0)
+#pragma unroll
+                for (int x = 0; x < kAt; ++x) red[(group - 1) * chunk + x * per + t] = sum[x];
+            __syncthreads();
+            if (group > 0) return;
+            for (int g = 0; g < groups - 1; ++g)
+#pragma unroll
+                for (int x = 0; x < kAt; ++x) sum[x] += red[g * chunk + x * per + t];
+        }
 #pragma unroll
         for (int x = 0; x < kAt; ++x)
-            if (j0 + x * threads < hi) w[j0 + x * threads] = fmaf(old[x], a.decay, sum[x]);
+            if (j0 + x * per < hi) w[j0 + x * per] = fmaf(old[x], a.decay, sum[x]);
+        if (GROUPS) return;  // (one turn covers the chunk)
     }
+}
+
+// A chunk of slots of one KV head's weights: weights <- decay * weights + sum of the rows' 2^(s - m) / l.
+__device__ __forceinline__ void weigh(const AttnArgs &a, uint32_t id, int chunks, int chunk, float *sm_m, float *sm_r,
+                                      float (*scratch)[kJoinWarps][8], float *red) {
+    const uint32_t bh = id / (uint32_t)chunks;
+    const int b = (int)(bh / (uint32_t)a.c.heads), h = (int)(bh - (uint32_t)b * (uint32_t)a.c.heads);
+    int begin, len;
+    seq_range(a, b, begin, len);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
+    const int lo = (int)(id - bh * (uint32_t)chunks) * chunk, hi = min(lo + chunk, len);
+    if (lo >= len) return;
+    if (hi > begin) {
+        // the octets' (m, l): `at_once` octets at a time, a team of warps each
+        const int octets = a.row_tiles * a.tile_rows / 8, at_once = min(octets, warps), team = warps / at_once;
+        for (int o0 = 0; o0 < octets; o0 += at_once) {
+            const int q = warp % at_once, o = o0 + q, mate = warp / at_once;
+            float2 ml = make_float2(kNone, 0.f);
+            if (o < octets && mate < team) {
+                const int rt = o * 8 / a.tile_rows, n = o - rt * (a.tile_rows / 8);
+                const Parts p = parts_of(a, b, h * a.row_tiles + rt);
+                if (!p.whole) ml = join_parts<4>(a, p, n, mate * 32 + lane, team * 32);
+                else if (mate == 0) ml = a.unit_ml[((int64_t)b * a.unit_heads + h * a.row_tiles) * a.tile_rows + o * 8 + (lane & 7)];
+            }
+            if (lane < 8) scratch[0][warp][lane] = ml.x, scratch[1][warp][lane] = ml.y;
+            __syncthreads();
+            const int r = o0 * 8 + tid;
+            if (tid < at_once * 8 && r < a.rows) {
+                const float2 all = join_warps(scratch, tid & 7, tid >> 3, team * at_once, at_once);
+                sm_m[r] = all.x == kNone ? 0.f : all.x;
+                sm_r[r] = all.y > 0.f || all.y != all.y ? ex2_approx(lift(a.c.e4m3 != 0)) / all.y : 0.f;
+            }
+            __syncthreads();
+        }
+    }
+    float *w = a.weights + (int64_t)bh * a.ld_weights;
+    const float *z = a.logits + (int64_t)bh * a.rows * a.ld_logits;
+    constexpr int kAt = 4;  // slots of a thread at a time
+    if (kAt * threads > chunk) add_up<true, kAt>(a, w, z, begin, lo, hi, chunk, sm_m, sm_r, red);
+    else add_up<false, kAt>(a, w, z, begin, lo, hi, chunk, sm_m, sm_r, red);
 }
 
 // The first join_blocks blocks: units in several parts, and zeros for units without slots, `blocks` blocks a unit.
 // A block joins 16 values of the 8 rows of an octet at a time (one fragment: 32 lanes of float4), its warps
 // taking turns at the parts.  The others add up weights; they join (m, l) for themselves, which costs less than
 // waiting for a kernel of its own.
+template <bool WEIGH>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a, int blocks, uint32_t join_blocks, int chunks, int chunk) {
     __shared__ float4 sm[kJoinWarps][32];
     __shared__ float scratch[2][kJoinWarps][8];
-    __shared__ float sm_m[kMaxAttnRows], sm_r[kMaxAttnRows];
     const int warps = blockDim.x >> 5;
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x >= join_blocks) {
-        weigh(a, blockIdx.x - join_blocks, chunks, chunk, sm_m, sm_r, scratch);
-        return;
+    if constexpr (WEIGH) {
+        __shared__ float sm_m[kMaxAttnRows], sm_r[kMaxAttnRows];
+        if (blockIdx.x >= join_blocks) {
+            weigh(a, blockIdx.x - join_blocks, chunks, chunk, sm_m, sm_r, scratch, reinterpret_cast<float *>(sm));
+            return;
+        }
     }
     const int D = a.c.dim, ks = D / 16, fragments = a.tile_rows / 8 * ks;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
@@ -1007,7 +1062,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnArgs a,
 #pragma unroll
             for (int y = 0; y < kAhead; ++y)
                 if (warp + y * warps < parts) t[y] = *reinterpret_cast<const float4 *>(part_at(a, p, p.first + warp + y * warps) + at);
-            const float2 own = join_ml(a, p, n, scratch);
+            const float2 own = join_ml<WEIGH ? 4 : 1>(a, p, n, scratch);  // (with WEIGH, the code that weigh has)
             float mt[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) mt[e] = __shfl_sync(0xFFFFFFFFu, own.x, c4 * 2 + e), l[e] = __shfl_sync(0xFFFFFFFFu, own.y, c4 * 2 + e);
@@ -1077,14 +1132,16 @@ cudaError_t launch(AttnArgs &a, const DeviceInfo &di, cudaStream_t s) {
     // a few units may be in hundreds of parts each
     const int join_threads = units * 64 <= a.resident ? kJoinWarps * 32 : kThreads;
     // weights: chunks of 2048 slots, which make the start of a block little work beside the rest, unless that leaves SMs
-    // idle
+    // idle; at the least 512, or 256 where more than 16 rows lengthen the rest (40 heads of one row over 32000 slots: 37 us
+    // with 256 and 35 with 512; 64 rows over 569 slots of 31 sequences: 52 and 54)
     const int64_t heads = (int64_t)a.c.batch * a.c.heads;
     int chunk = 2048, chunks = 0;
     if (a.weights) {
-        while (chunk > 512 && heads * ((a.cap + chunk - 1) / chunk) < 4 * di.sm_count) chunk /= 2;
+        const int least = a.rows > 16 ? 256 : 512;
+        while (chunk > least && heads * ((a.cap + chunk - 1) / chunk) < 4 * di.sm_count) chunk /= 2;
         chunks = (a.cap + chunk - 1) / chunk;
     }
-    return launch_pdl(join_kernel, dim3((unsigned)(units * blocks + heads * chunks)), dim3(join_threads), 0, s, dim3(1), a, (int)blocks,
+    return launch_pdl(a.weights ? join_kernel<true> : join_kernel<false>, dim3((unsigned)(units * blocks + heads * chunks)), dim3(join_threads), 0, s, dim3(1), a, (int)blocks,
                       (uint32_t)(units * blocks), chunks > 0 ? chunks : 1, chunk);
 }
 

@@ -131,6 +131,18 @@ def test_attn(D, dtype, page, layout, Hkv, G, n_q, lens, window, softcap, weigh)
     assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and (w is None or torch.equal(w, w2))
 
 
+@pytest.mark.parametrize("D,dtype,page,layout,Hkv,G,n_q,lens,window,softcap", [
+    (256, F8, 32, "phsd", 1, 16, 4, [83, 2793], 0, 0.0),      # 64 rows in four tiles, a few units in many parts
+    (64, BF, 16, "pshd", 2, 16, 4, [17, 569, 300], 0, 0.0),   # whole units, 64 rows
+    (128, BF, 16, "phsd", 1, 5, 1, [1500, 1025], 0, 0.0),
+    (128, F8, 24, "mixed", 1, 40, 3, [3000, 3, 517], 700, 30.0),  # 120 rows; chunks before the window's begin
+    (64, BF, 16, "phsd", 3, 7, 5, [257, 256, 255, 4097], 0, 0.0),
+])
+def test_attn_weights_of_many_rows(D, dtype, page, layout, Hkv, G, n_q, lens, window, softcap):
+    """Weights of few slots, whose rows are dealt to groups of threads, and (m, l) of several octets at once."""
+    test_attn(D, dtype, page, layout, Hkv, G, n_q, lens, window, softcap, True)
+
+
 @pytest.mark.parametrize("dtype", [BF, F8])
 def test_attn_many_and_long(dtype):
     """Ragged lengths over two orders of magnitude (units of one CTA, of many, of none), and one long sequence."""
