@@ -5,8 +5,12 @@
 // Bound by HBM for many rows (a row of y and r read, of r' and x written, each once)
 // and by latency for few.  A CTA holds a whole row in registers between the two norms,
 // up to 16384 values; only longer rows are read again.  A mean is
-// taken off before the squares are summed (two reductions over registers cost little,
-// and E[x^2] - E[x]^2 would cancel).  Everything is fp32 until the two outputs.
+// taken off before the squares are summed (E[x^2] - E[x]^2 would cancel): within a warp by
+// two sums over registers, over the warps by their means and squares, with one barrier.
+// Everything is fp32 until the two outputs.
+// Measured: 2.9 us for a row of 5120; 36 us for 4096 rows of 5120 (RMS, a gate, 16-bit residual:
+// 5.9 TB/s), 41 with two layer norms and biases.
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -21,19 +25,21 @@ namespace {
 constexpr int kMaxThreads = 1024;
 constexpr int kNone = 0, kLayer = 2;  // Q4K_NORM_NONE, Q4K_NORM_LAYER
 
-// Sum over the CTA, in the same order on every call; scratch holds 33 floats.
-__device__ __forceinline__ float block_sum(float v, float *scratch) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warps == 1) return v;
-    __syncthreads();  // the sum before has been read
-    if (lane == 0) scratch[warp] = v;
-    __syncthreads();
-    v = lane < warps ? scratch[lane] : 0.f;
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
+}
+// Sum over the CTA with one barrier, in the same order on every call: two scratch arrays in turn.
+__device__ __forceinline__ float turn_sum(float v, float2 (*scratch)[32], int &turn) {
+    v = warp_sum(v);
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warps == 1) return v;
+    if (lane == 0) scratch[turn][warp].x = v;
+    __syncthreads();
+    v = lane < warps ? scratch[turn][lane].x : 0.f;
+    turn ^= 1;
+    return warp_sum(v);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -44,20 +50,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // A row of D values over a CTA: thread t holds group i (of NV) of four values, elements
 // 4 (i threads + t) .. + 3 (VEC: 16-byte accesses), or i * 4 + x -> (4 i + x) threads + t.
-// Values past D are 0.
-template <int NV, bool VEC>
+// Values past D are 0; FULL: there are none.
+template <int NV, bool VEC, bool FULL = false>
 struct Slice {
     int D, tid, threads;
+    __device__ __forceinline__ bool in(int i, int x) const { return FULL || at(i, x) < D; }
     __device__ __forceinline__ int at(int i, int x) const { return VEC ? 4 * (i * threads + tid) + x : (4 * i + x) * threads + tid; }
     __device__ __forceinline__ void load(const float *p, float (&v)[4 * NV]) const {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if constexpr (VEC) {
-                const float4 t = at(i, 0) < D ? __ldg(reinterpret_cast<const float4 *>(p + at(i, 0))) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 t = in(i, 0) ? __ldg(reinterpret_cast<const float4 *>(p + at(i, 0))) : make_float4(0.f, 0.f, 0.f, 0.f);
                 v[4 * i] = t.x, v[4 * i + 1] = t.y, v[4 * i + 2] = t.z, v[4 * i + 3] = t.w;
             } else {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) v[4 * i + x] = at(i, x) < D ? __ldg(p + at(i, x)) : 0.f;
+                for (int x = 0; x < 4; ++x) v[4 * i + x] = in(i, x) ? __ldg(p + at(i, x)) : 0.f;
             }
         }
     }
@@ -65,12 +72,12 @@ struct Slice {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if constexpr (VEC) {
-                const uint2 t = at(i, 0) < D ? __ldg(reinterpret_cast<const uint2 *>(p + at(i, 0))) : make_uint2(0, 0);
+                const uint2 t = in(i, 0) ? __ldg(reinterpret_cast<const uint2 *>(p + at(i, 0))) : make_uint2(0, 0);
                 v[4 * i] = __uint_as_float(t.x << 16), v[4 * i + 1] = __uint_as_float(t.x & 0xFFFF0000u);
                 v[4 * i + 2] = __uint_as_float(t.y << 16), v[4 * i + 3] = __uint_as_float(t.y & 0xFFFF0000u);
             } else {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) v[4 * i + x] = at(i, x) < D ? __uint_as_float((uint32_t)__ldg(p + at(i, x)) << 16) : 0.f;
+                for (int x = 0; x < 4; ++x) v[4 * i + x] = in(i, x) ? __uint_as_float((uint32_t)__ldg(p + at(i, x)) << 16) : 0.f;
             }
         }
     }
@@ -78,11 +85,11 @@ struct Slice {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if constexpr (VEC) {
-                if (at(i, 0) < D) *reinterpret_cast<float4 *>(p + at(i, 0)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                if (in(i, 0)) *reinterpret_cast<float4 *>(p + at(i, 0)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             } else {
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    if (at(i, x) < D) p[at(i, x)] = v[4 * i + x];
+                    if (in(i, x)) p[at(i, x)] = v[4 * i + x];
             }
         }
     }
@@ -91,31 +98,64 @@ struct Slice {
         for (int i = 0; i < NV; ++i) {
             const uint2 t = make_uint2(pack_bf16(v[4 * i], v[4 * i + 1]), pack_bf16(v[4 * i + 2], v[4 * i + 3]));
             if constexpr (VEC) {
-                if (at(i, 0) < D) *reinterpret_cast<uint2 *>(p + at(i, 0)) = t;
+                if (in(i, 0)) *reinterpret_cast<uint2 *>(p + at(i, 0)) = t;
             } else {
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    if (at(i, x) < D) p[at(i, x)] = (uint16_t)((x < 2 ? t.x : t.y) >> (x & 1) * 16);
+                    if (in(i, x)) p[at(i, x)] = (uint16_t)((x < 2 ? t.x : t.y) >> (x & 1) * 16);
             }
         }
     }
-    // v <- norm(v)
-    __device__ __forceinline__ void norm(float (&v)[4 * NV], int kind, const float *w, const float *b, float eps, float *scratch) const {
-        float t[4 * NV];
-        if (w) load(w, t);  // (on its way during the sums)
-        const float inv = 1.f / (float)D;
+    // number of the row's values in warp w
+    __device__ __forceinline__ float values_of_warp(int w) const {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < NV * (VEC ? 1 : 4); ++i) n += min(max((VEC ? (D + 3) / 4 : D) - i * threads - 32 * w, 0), 32);
+        return (float)(VEC ? 4 * n : n);
+    }
+    __device__ __forceinline__ float inverse_of_warp() const { return 1.f / fmaxf(values_of_warp(tid >> 5), 1.f); }
+    // Takes the mean off (kind kLayer) and returns 1 / the norm.  Each warp knows the mean of its values and the
+    // squares about it before the one barrier; with n values each,
+    //     sum (v - mean)^2 = sum over warps of (squares + n (warp's mean - mean)^2).
+    // in_warp, in_lane: inverse_of_warp() and values_of_warp(lane).
+    __device__ __forceinline__ float scale_of(float (&v)[4 * NV], int kind, float eps, float inv, float in_warp, float in_lane,
+                                              float2 (*scratch)[32], int &turn) const {
         float sum = 0.f;
-        if (kind == kLayer) {
+        if (kind != kLayer) {
 #pragma unroll
-            for (int k = 0; k < 4 * NV; ++k) sum += v[k];
-            const float mean = block_sum(sum, scratch) * inv;
-#pragma unroll
-            for (int k = 0; k < 4 * NV; ++k) v[k] = at(k / 4, VEC ? 0 : k & 3) < D ? v[k] - mean : 0.f;
-            sum = 0.f;
+            for (int k = 0; k < 4 * NV; ++k) sum = fmaf(v[k], v[k], sum);
+            return 1.f / sqrtf(turn_sum(sum, scratch, turn) * inv + eps);
         }
 #pragma unroll
-        for (int k = 0; k < 4 * NV; ++k) sum = fmaf(v[k], v[k], sum);
-        const float f = 1.f / sqrtf(block_sum(sum, scratch) * inv + eps);
+        for (int k = 0; k < 4 * NV; ++k) sum += v[k];
+        float mean = warp_sum(sum) * in_warp, square = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4 * NV; ++k) {
+            const float d = v[k] - mean;
+            if (in(k / 4, VEC ? 0 : k & 3)) square = fmaf(d, d, square);
+        }
+        square = warp_sum(square);
+        const int warps = threads >> 5, lane = tid & 31;
+        if (warps > 1) {
+            if (lane == 0) scratch[turn][tid >> 5] = make_float2(mean, square);
+            __syncthreads();
+            const float2 of = lane < warps ? scratch[turn][lane] : make_float2(0.f, 0.f);
+            turn ^= 1;
+            const float n = lane < warps ? in_lane : 0.f;
+            mean = warp_sum(n * of.x) * inv;
+            const float d = of.x - mean;
+            square = warp_sum(lane < warps ? fmaf(n * d, d, of.y) : 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < 4 * NV; ++k) v[k] = in(k / 4, VEC ? 0 : k & 3) ? v[k] - mean : 0.f;
+        return 1.f / sqrtf(square * inv + eps);
+    }
+    // v <- norm(v)
+    __device__ __forceinline__ void norm(float (&v)[4 * NV], int kind, const float *w, const float *b, float eps, float2 (*scratch)[32],
+                                         int &turn) const {
+        float t[4 * NV];
+        if (w) load(w, t);  // (on its way during the sums)
+        const float f = scale_of(v, kind, eps, 1.f / (float)D, inverse_of_warp(), values_of_warp(tid & 31), scratch, turn);
 #pragma unroll
         for (int k = 0; k < 4 * NV; ++k) v[k] *= f;
         if (w) {
@@ -133,7 +173,8 @@ struct Slice {
 template <int NV, bool VEC, bool BF16>
 __global__ void __launch_bounds__(NV <= 2 ? kMaxThreads : 512) norm_kernel(const NormArgs a) {
     using Res = typename std::conditional<BF16, uint16_t, float>::type;
-    __shared__ float scratch[33];
+    __shared__ float2 scratch[2][32];
+    int turn = 0;
     pdl_wait();
     pdl_trigger();
     const int64_t row = blockIdx.x;
@@ -144,7 +185,7 @@ __global__ void __launch_bounds__(NV <= 2 ? kMaxThreads : 512) norm_kernel(const
         float y[4 * NV], t[4 * NV];
         s.load(a.y + row * a.ldy, y);
         if (a.gate) s.load(a.gate + row * a.ld_gate, t);
-        if (a.post != kNone) s.norm(y, a.post, a.post_w, a.post_b, a.post_eps, scratch);
+        if (a.post != kNone) s.norm(y, a.post, a.post_w, a.post_b, a.post_eps, scratch, turn);
         if (a.gate) {
 #pragma unroll
             for (int k = 0; k < 4 * NV; ++k) y[k] *= t[k];
@@ -154,29 +195,14 @@ __global__ void __launch_bounds__(NV <= 2 ? kMaxThreads : 512) norm_kernel(const
     }
     if (a.r_out) s.store(static_cast<Res *>(a.r_out) + row * a.ldr, h);
     if (!a.x) return;
-    if (a.pre != kNone) s.norm(h, a.pre, a.pre_w, a.pre_b, a.pre_eps, scratch);
+    if (a.pre != kNone) s.norm(h, a.pre, a.pre_w, a.pre_b, a.pre_eps, scratch, turn);
     s.store(a.x + row * a.ldx, h);
 }
 
-// Many rows: two CTAs an SM walk them, one row in registers while the next ones are copied into a ring in
-// shared memory, whole rows at a time.  What is the same for every row stays in registers; a CTA a row reads
-// it from L2 each time, as much again as the row itself.
-constexpr int kRing = 4;  // rows of the ring, at most
-
-// Sum over the CTA with one barrier: two scratch arrays in turn.
-__device__ __forceinline__ float turn_sum(float v, float (*scratch)[32], int &turn) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warps == 1) return v;
-    if (lane == 0) scratch[turn][warp] = v;
-    __syncthreads();
-    v = lane < warps ? scratch[turn][lane] : 0.f;
-    turn ^= 1;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-}
+// Many rows: a few CTAs an SM walk them, one row in registers while the next ones are copied into a ring in
+// shared memory, whole rows at a time.  What is the same for every row stays in registers and shared memory; a CTA
+// a row reads it from L2 each time, as much again as the row itself (4096 x 5120: 51 us against 36).
+constexpr int kRing = 8;  // rows of the ring, at most (8192 x 768: 15.7 us, with 4 18.0)
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
@@ -185,14 +211,14 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
 }
 
 // (640: 96 registers a thread, so that two CTAs of up to 320 threads share an SM)
-template <int NV, bool BF16>
-__global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int stages) {
+template <int NV, bool BF16, bool FULL>
+__global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int stages, uint32_t ring_bytes) {
     using Res = typename std::conditional<BF16, uint16_t, float>::type;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t bars[kRing];
-    __shared__ float scratch[2][32];
+    __shared__ float2 scratch[2][32];
     const int D = (int)a.D, tid = threadIdx.x;
-    const Slice<NV, true> s = {D, tid, (int)blockDim.x};
+    const Slice<NV, true, FULL> s = {D, tid, (int)blockDim.x};
     const bool gate_rows = a.y && a.gate && a.ld_gate != 0;
     const uint32_t y_bytes = a.y ? 4u * D : 0u, r_bytes = (uint32_t)sizeof(Res) * D, g_bytes = gate_rows ? 4u * D : 0u;
     const uint32_t stage_bytes = y_bytes + r_bytes + g_bytes;
@@ -222,27 +248,32 @@ __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int st
 #pragma unroll
         for (int k = 0; k < 4 * NV; ++k) w[k] *= t[k];
     };
-    const float *post_b = a.post != kNone ? a.post_b : nullptr, *pre_b = a.pre != kNone ? a.pre_b : nullptr;
-    if (a.y && a.post != kNone && a.post_w && !post_b) times(wy, a.post_w);
+    if (a.y && a.post != kNone && a.post_w) times(wy, a.post_w);
     if (a.y && a.gate && !gate_rows) times(wy, a.gate);
     if (a.x && a.pre != kNone && a.pre_w) times(wx, a.pre_w);
-    const float inv = 1.f / (float)D;
+    // and scale * gate * post_b and pre_b, in shared memory behind the ring (registers are short): each thread's own
+    const bool post_b = a.y && a.post != kNone && a.post_b, pre_b = a.x && a.pre != kNone && a.pre_b;
+    float *const by = reinterpret_cast<float *>(ring + ring_bytes), *const bx = by + (post_b ? D : 0);
+    if (post_b) {
+        float t[4 * NV];
+#pragma unroll
+        for (int k = 0; k < 4 * NV; ++k) t[k] = a.scale;
+        times(t, a.post_b);
+        if (a.gate && !gate_rows) times(t, a.gate);
+        s.store(by, t);
+    }
+    if (pre_b) {
+        float t[4 * NV];
+        s.load(a.pre_b, t);
+        s.store(bx, t);
+    }
+    // four values of one of them
+    auto four = [&](const float *p, int i) {
+        return s.in(i, 0) ? *reinterpret_cast<const float4 *>(p + s.at(i, 0)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    const float inv = 1.f / (float)D, in_warp = s.inverse_of_warp(), in_lane = s.values_of_warp(tid & 31);
     int turn = 0, stage = 0;
     uint32_t parity = 0;
-    auto scale_of = [&](float (&v)[4 * NV], int kind, float eps) {  // takes the mean off, returns 1 / the norm
-        float sum = 0.f;
-        if (kind == kLayer) {
-#pragma unroll
-            for (int k = 0; k < 4 * NV; ++k) sum += v[k];
-            const float mean = turn_sum(sum, scratch, turn) * inv;
-#pragma unroll
-            for (int k = 0; k < 4 * NV; ++k) v[k] = s.at(k / 4, 0) < D ? v[k] - mean : 0.f;
-            sum = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < 4 * NV; ++k) sum = fmaf(v[k], v[k], sum);
-        return 1.f / sqrtf(turn_sum(sum, scratch, turn) * inv + eps);
-    };
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
         if (!mbar_wait(smem_u32(&bars[stage]), parity, a.status)) {
             mbar_wait(smem_u32(&bars[stage]), parity, a.status);  // the copies may still land
@@ -250,12 +281,11 @@ __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int st
         }
         const uint8_t *at = ring + stage * stage_bytes;
         float v[4 * NV], h[4 * NV];
-        const bool gate_on = gate_rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = s.at(i, 0);
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f), r = y;
-            if (e < D) {
+            if (s.in(i, 0)) {
                 if (a.y) y = *reinterpret_cast<const float4 *>(at + 4 * e);
                 if constexpr (BF16) {
                     const uint2 t = *reinterpret_cast<const uint2 *>(at + y_bytes + 2 * e);
@@ -270,31 +300,24 @@ __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int st
         }
         if (a.y) {
             if (a.post != kNone) {
-                const float f = scale_of(v, a.post, a.post_eps);
+                const float f = s.scale_of(v, a.post, a.post_eps, inv, in_warp, in_lane, scratch, turn);
 #pragma unroll
                 for (int k = 0; k < 4 * NV; ++k) v[k] *= f;
-                if (post_b) {  // (then post_w is not among wy)
-                    float t[4 * NV];
-                    if (a.post_w) {
-                        s.load(a.post_w, t);
+            }
 #pragma unroll
-                        for (int k = 0; k < 4 * NV; ++k) v[k] *= t[k];
-                    }
-                    s.load(post_b, t);
+            for (int i = 0; i < NV; ++i) {
+                const float4 b = post_b ? four(by, i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float b4[4] = {b.x, b.y, b.z, b.w};
+                if (gate_rows) {
+                    const float4 t = four(reinterpret_cast<const float *>(at + y_bytes + r_bytes), i);
+                    const float t4[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-                    for (int k = 0; k < 4 * NV; ++k) v[k] += t[k];
+                    for (int x = 0; x < 4; ++x) h[4 * i + x] = fmaf(t4[x], fmaf(v[4 * i + x], wy[4 * i + x], b4[x]), h[4 * i + x]);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) h[4 * i + x] = fmaf(v[4 * i + x], wy[4 * i + x], h[4 * i + x]) + b4[x];
                 }
             }
-            if (gate_on) {
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (s.at(i, 0) < D) {
-                        const float4 t = *reinterpret_cast<const float4 *>(at + y_bytes + r_bytes + 4 * s.at(i, 0));
-                        v[4 * i] *= t.x, v[4 * i + 1] *= t.y, v[4 * i + 2] *= t.z, v[4 * i + 3] *= t.w;
-                    }
-            }
-#pragma unroll
-            for (int k = 0; k < 4 * NV; ++k) h[k] = fmaf(v[k], wy[k], h[k]);
         }
         __syncthreads();  // the stage has been read
         if (tid == 0 && row + (int64_t)stages * gridDim.x < a.M) copy(row + (int64_t)stages * gridDim.x, stage);
@@ -302,14 +325,13 @@ __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int st
         if (a.r_out) s.store(static_cast<Res *>(a.r_out) + row * a.ldr, h);
         if (!a.x) continue;
         if (a.pre != kNone) {
-            const float f = scale_of(h, a.pre, a.pre_eps);
+            const float f = s.scale_of(h, a.pre, a.pre_eps, inv, in_warp, in_lane, scratch, turn);
 #pragma unroll
-            for (int k = 0; k < 4 * NV; ++k) h[k] = h[k] * f * wx[k];
-            if (pre_b) {
-                float t[4 * NV];
-                s.load(pre_b, t);
+            for (int i = 0; i < NV; ++i) {
+                const float4 b = pre_b ? four(bx, i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float b4[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                for (int k = 0; k < 4 * NV; ++k) h[k] += t[k];
+                for (int x = 0; x < 4; ++x) h[4 * i + x] = fmaf(h[4 * i + x] * f, wx[4 * i + x], b4[x]);
             }
         }
         s.store(a.x + row * a.ldx, h);
@@ -319,7 +341,8 @@ __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int st
 // Rows too long for registers: every pass reads the row again and forms h anew; r_out
 // (which may be r_in) is written in the last one.
 __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a) {
-    __shared__ float scratch[33];
+    __shared__ float2 scratch[2][32];
+    int turn = 0;
     pdl_wait();
     pdl_trigger();
     const int64_t row = blockIdx.x, D = a.D;
@@ -329,7 +352,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a
     auto total = [&](auto &&value) {
         float s = 0.f;
         for (int64_t e = threadIdx.x; e < D; e += blockDim.x) s += value(e);
-        return block_sum(s, scratch);
+        return turn_sum(s, scratch, turn);
     };
     float y_mean = 0.f, y_f = 1.f;
     if (y && a.post != kNone) {
@@ -380,12 +403,13 @@ cudaError_t launch(const NormArgs &a, bool vec, int threads, cudaStream_t s) {
 }
 
 template <int NV>
-cudaError_t launch_rows(const NormArgs &a, int stages, int smem, int per_sm, int threads, int sm_count, cudaStream_t s) {
-    auto kern = a.bf16 ? norm_rows_kernel<NV, true> : norm_rows_kernel<NV, false>;
+cudaError_t launch_rows(const NormArgs &a, int stages, int ring, int smem, int per_sm, int threads, int sm_count, cudaStream_t s) {
+    auto kern = a.D == 4 * NV * threads ? (a.bf16 ? norm_rows_kernel<NV, true, true> : norm_rows_kernel<NV, false, true>)
+                                        : (a.bf16 ? norm_rows_kernel<NV, true, false> : norm_rows_kernel<NV, false, false>);
     cudaError_t e = ensure_smem((const void *)kern, smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = a.M < (int64_t)sm_count * per_sm ? a.M : (int64_t)sm_count * per_sm;
-    return launch_pdl(kern, dim3((unsigned)grid), dim3(threads), smem, s, dim3(1), a, stages);
+    return launch_pdl(kern, dim3((unsigned)grid), dim3(threads), smem, s, dim3(1), a, stages, (uint32_t)ring);
 }
 
 }  // namespace
@@ -403,23 +427,26 @@ cudaError_t launch_norm_residual(const DeviceInfo &di, const NormArgs &a, cudaSt
         const int threads = (int)(((quads + 7) / 8 + 31) / 32 * 32);
         return launch<8>(a, vec, threads, s);
     }
-    // many rows that can be copied whole: a ring of at least two rows a CTA (device time of one CTA a row
-    // against the ring at 4096 x 5120: 51 and 36 us)
+    // many rows that can be copied whole: a ring of at least two rows a CTA
     const int64_t row_bytes = a.D * ((a.y ? 4 : 0) + (a.bf16 ? 2 : 4) + (a.y && a.gate && a.ld_gate != 0 ? 4 : 0));
     const bool bulk = vec && a.D % 8 == 0 && al(a.r_in, 16) && (a.bf16 ? a.ldr % 8 == 0 : true);
-    const int nv = quads > 128 ? 4 : quads > 64 ? 2 : 1;
+    // values of a thread: as many as leave no thread without any (8192 x 768 with 16 a thread of two warps, a quarter of
+    // them idle: 19.3 us, with 8 of three: 17.8)
+    int nv = quads > 128 ? 4 : quads > 64 ? 2 : 1;
+    while (nv > 1 && quads % (32 * nv) != 0 && quads % 32 == 0 && quads <= 640 * (nv / 2)) nv /= 2;
     const int threads_many = (int)(((quads + nv - 1) / nv + 31) / 32 * 32);
     if (bulk && threads_many <= 640 && a.M >= 4 * di.sm_count) {
-        int per_sm = 640 / threads_many;
-        if (per_sm > 8) per_sm = 8;
-        while (per_sm > 1 && (220 * 1024) / per_sm < 2 * row_bytes + 1024) --per_sm;
-        int64_t stages = ((220 * 1024) / per_sm - 1024) / row_bytes;
+        const int64_t biases = 4 * a.D * ((a.y && a.post != kNone && a.post_b ? 1 : 0) + (a.x && a.pre != kNone && a.pre_b ? 1 : 0));
+        int per_sm = (nv == 4 ? 640 : 960) / threads_many;  // (as many as the registers allow)
+        if (per_sm > 10) per_sm = 10;
+        while (per_sm > 1 && (220 * 1024) / per_sm < 2 * row_bytes + biases + 1024) --per_sm;
+        int64_t stages = ((220 * 1024) / per_sm - 1024 - biases) / row_bytes;
         if (stages > kRing) stages = kRing;
         if (stages >= 2) {
-            const int smem = (int)(stages * row_bytes);
-            return nv == 4   ? launch_rows<4>(a, (int)stages, smem, per_sm, threads_many, di.sm_count, s)
-                   : nv == 2 ? launch_rows<2>(a, (int)stages, smem, per_sm, threads_many, di.sm_count, s)
-                             : launch_rows<1>(a, (int)stages, smem, per_sm, threads_many, di.sm_count, s);
+            const int ring = (int)(stages * row_bytes), smem = (int)(ring + biases);
+            return nv == 4   ? launch_rows<4>(a, (int)stages, ring, smem, per_sm, threads_many, di.sm_count, s)
+                   : nv == 2 ? launch_rows<2>(a, (int)stages, ring, smem, per_sm, threads_many, di.sm_count, s)
+                             : launch_rows<1>(a, (int)stages, ring, smem, per_sm, threads_many, di.sm_count, s);
         }
     }
     const int few = quads > kMaxThreads / 2 ? 2 : 1;

@@ -689,6 +689,29 @@ def test_norm_large_means_and_rows_without_a_number():
     assert torch.isnan(out[2]).all() and torch.isnan(out[3]).any()
 
 
+@pytest.mark.parametrize("D", [256, 776, 1536, 2048, 4096, 8192])
+@pytest.mark.parametrize("post,pre,gate,res,bias", [
+    ("layer", "layer", None, BF, True), ("layer", "rms", "all", BF, True), ("rms", "layer", "row", torch.float32, False)])
+def test_norm_many_rows_of_more_widths(D, post, pre, gate, res, bias):
+    """Widths that fill every thread and widths that do not; biases beside the ring, and rings that they leave no room for."""
+    test_norm_many_rows_are_each_row_alone(D, post, pre, gate, res, bias)
+
+
+@pytest.mark.parametrize("D", [768, 1000, 5120])
+def test_norm_many_rows_with_large_means(D):
+    """The mean is known to 2^-24 of itself and each addition on the way (up to 16 of a thread's values, 5 and 5 of a tree,
+    and as many for the warps' parts)."""
+    g = gen_of(42)
+    M, shift = 700, 1e4
+    y = torch.randn(M, D, generator=g, device="cuda") + shift
+    y[5, 0] = -3e5  # far from all others
+    r, x = torch.zeros(M, D, device="cuda"), torch.zeros(M, D, dtype=BF, device="cuda")
+    q4k.q4k_norm_residual(M, D, y, D, 2, None, None, 0.0, None, 0, 1.0, r, r, D, q4k.Q4K_RES_FP32, 0, None, None, 0.0, x, D)
+    want = R.norm_residual(np64(y), 2, None, None, 0.0, None, 1.0, np.zeros((M, D)), 0, None, None, 0)[0]
+    spread = np64(y).std(axis=1, keepdims=True)
+    assert (np.abs(np64(r) - want) * spread <= shift * 32 * 2.0 ** -24 + np.abs(want) * spread * 64 * 2.0 ** -24).all()
+
+
 # ---------------------------------------------------------------- sample
 
 def run_sample(z, t=None, k=None, p=None, m=None, u=None, ld=None):
