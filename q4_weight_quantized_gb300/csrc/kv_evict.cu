@@ -10,13 +10,13 @@
 // keys in shared memory.  A histogram over the range of the keys narrows it to the bin
 // that holds the wanted rank; once a few slots are left they are ranked against each
 // other, which also settles equal weights by slot.  The last pass takes the slots in
-// order, four to a thread, and numbers holes and fillers by one scan per tile.  Bound by
-// latency (some twenty block-wide steps; 256 threads for caches of up to 4096 slots, whose
+// order, a run to a thread, and numbers holes and fillers by one scan.  Bound by
+// latency (some fifteen block-wide steps; 256 threads for caches of up to 4096 slots, whose
 // steps would otherwise cost more in idle warps than in work); the reads are 8 bytes a slot.
 // move_kernel copies the rows, 16 bytes a lane, and their weights and positions: bound by HBM (two or
 // four rows a thread cost more in occupancy than their overlapping loads gave: 62 and 70 us against 59).
-// Measured: 9.6 us for 32 caches of 8 heads with one slot over 2048 (7 of them the selection), 82 us for
-// 16 caches of 9001 to 16384 slots to 8192 (17 the selection, 59 the copies: 333 MB at 5.7 TB/s).
+// Measured: 9.3 us for 32 caches of 8 heads with one slot over 2048 (5 of them the selection), 81 us for
+// 16 caches of 9001 to 16384 slots to 8192 (15 the selection, 59 the copies: 333 MB at 5.7 TB/s).
 
 #include <cuda_runtime.h>
 
@@ -291,14 +291,23 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
         hi = lo + min(hi - lo, (1u << shift) - 1);
         __syncthreads();
     }
-    // ---- holes below keep and fillers from there on, numbered in slot order: tiles of four slots a thread
+    // ---- holes below keep and fillers from there on, numbered in slot order: a run of slots a thread, so long that one
+    // scan is enough where 28 are (4, 12, 20 or 28: then the threads' 16-byte reads meet in no bank).  The list, at most
+    // half as many pairs as slots, then takes the keys' place, from where it goes out in whole sectors
     int2 *list_out = a.moves + (int64_t)bh * a.max_moves;
     uint32_t holes = 0, fills = 0;
+    const int per = CACHED ? min(((n + THREADS - 1) / THREADS + 3) / 8 * 8 + 4, 28) : 4;
+    const bool once = CACHED && n <= per * THREADS;
+    int2 *const moves = once ? reinterpret_cast<int2 *>(keys) : list_out;
     __syncthreads();
-    for (int j0 = 0, turn = 0; j0 < n; j0 += 4 * THREADS, turn ^= 1) {
-        const int j = j0 + 4 * tid;
-        uint32_t k[4] = {0, 0, 0, 0}, prot = 0;
-        if (j < n) {
+    for (int base = 0, turn = 0; base < n; base += per * THREADS, turn ^= 1) {
+        const int j0 = base + per * tid;
+        uint32_t count = 0, mark = 0;  // holes, fillers << 16; slots of either kind
+#pragma unroll
+        for (int q = 0; q < (CACHED ? 7 : 1); ++q) {
+            const int j = j0 + 4 * q;
+            if (4 * q >= per || j >= n) break;
+            uint32_t k[4] = {0, 0, 0, 0}, prot = 0;
             if constexpr (CACHED) {
                 const uint4 t = *reinterpret_cast<const uint4 *>(keys + j);  // (past n: whatever is there)
                 k[0] = t.x, k[1] = t.y, k[2] = t.z, k[3] = t.w;
@@ -308,28 +317,28 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
                 for (int x = 0; x < 4; ++x)
                     if (j + x < n) k[x] = key_of(w[j + x]), prot |= is_protected(p[j + x]) ? 1u << x : 0u;
             }
-        }
-        uint32_t count = 0, mark = 0;  // holes, fillers << 16; slots of either kind
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const bool of_class = ((prot >> x & 1) != 0) == in_prot;
-            const bool gone = of_class ? k[x] < cut || (k[x] == cut && (uint32_t)(j + x) <= cut_slot) : in_prot;
-            const bool below = j + x < keep;
-            if (j + x < n && gone == below) mark |= 1u << x, count += below ? 1u : 1u << 16;
+            for (int x = 0; x < 4; ++x) {
+                const bool of_class = ((prot >> x & 1) != 0) == in_prot;
+                const bool gone = of_class ? k[x] < cut || (k[x] == cut && (uint32_t)(j + x) <= cut_slot) : in_prot;
+                const bool below = j + x < keep;
+                if (j + x < n && gone == below) mark |= 1u << (4 * q + x), count += below ? 1u : 1u << 16;
+            }
         }
         uint32_t total;
         const uint32_t before = B::scan(count, scratch[turn], total);
         uint32_t hole = holes + (before & 0xFFFF), fill = fills + (before >> 16);
-        if (j < n) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                if (!(mark >> x & 1)) continue;
-                if (j + x < keep) list_out[hole++].x = j + x;
-                else list_out[fill++].y = j + x;
-            }
+        for (; mark != 0; mark &= mark - 1) {
+            const int slot = j0 + __ffs(mark) - 1;
+            if (slot < keep) moves[hole++].x = slot;
+            else moves[fill++].y = slot;
         }
         holes += total & 0xFFFF;
         fills += total >> 16;
+    }
+    if (once) {
+        __syncthreads();
+        for (uint32_t i = tid; i < holes; i += THREADS) list_out[i] = moves[i];
     }
     if (tid == 0) a.count[bh] = (int32_t)holes;
 }
