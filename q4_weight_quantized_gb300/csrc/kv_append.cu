@@ -9,6 +9,8 @@
 // on, so every access is 16 bytes (8 or 4 for the outputs) and neighbouring threads
 // touch neighbouring bytes; pointers, strides or widths that do not allow that take a
 // value (or pair) per thread.
+// Measured: 2.0 us for 16 tokens of 40 and 8 heads of 128; 43.5 us for 8191 tokens of 32 and 4 heads into an e4m3
+// cache, half the width rotated (245 MB at 5.6 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
