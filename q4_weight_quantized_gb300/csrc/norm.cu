@@ -171,7 +171,7 @@ struct Slice {
 };
 
 template <int NV, bool VEC, bool BF16>
-__global__ void __launch_bounds__(NV <= 2 ? kMaxThreads : 512) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
     using Res = typename std::conditional<BF16, uint16_t, float>::type;
     __shared__ float2 scratch[2][32];
     int turn = 0;
@@ -422,11 +422,6 @@ cudaError_t launch_norm_residual(const DeviceInfo &di, const NormArgs &a, cudaSt
                      (!a.x || (al(a.x, 8) && a.ldx % 4 == 0)) && al(a.post_w, 16) && al(a.post_b, 16) && al(a.pre_w, 16) &&
                      al(a.pre_b, 16);
     const int64_t quads = (a.D + 3) / 4;  // groups of four values
-    if (quads > 2 * kMaxThreads) {
-        if (quads > 8 * 512) return launch_pdl(norm_long_kernel, dim3((unsigned)a.M), dim3(kMaxThreads), 0, s, dim3(1), a);
-        const int threads = (int)(((quads + 7) / 8 + 31) / 32 * 32);
-        return launch<8>(a, vec, threads, s);
-    }
     // many rows that can be copied whole: a ring of at least two rows a CTA
     const int64_t row_bytes = a.D * ((a.y ? 4 : 0) + (a.bf16 ? 2 : 4) + (a.y && a.gate && a.ld_gate != 0 ? 4 : 0));
     const bool bulk = vec && a.D % 8 == 0 && al(a.r_in, 16) && (a.bf16 ? a.ldr % 8 == 0 : true);
@@ -449,9 +444,12 @@ cudaError_t launch_norm_residual(const DeviceInfo &di, const NormArgs &a, cudaSt
                              : launch_rows<1>(a, (int)stages, ring, smem, per_sm, threads_many, di.sm_count, s);
         }
     }
-    const int few = quads > kMaxThreads / 2 ? 2 : 1;
-    const int threads = (int)(((quads + few - 1) / few + 31) / 32 * 32);
-    return few == 2 ? launch<2>(a, vec, threads, s) : launch<1>(a, vec, threads, s);
+    // a CTA a row, values in registers: eight a thread, which leave registers for the loads ahead, up to 8192
+    // (2000 x 12375, which spills: 125 us; with 32 values of half as many threads 174)
+    if (quads > 4 * kMaxThreads) return launch_pdl(norm_long_kernel, dim3((unsigned)a.M), dim3(kMaxThreads), 0, s, dim3(1), a);
+    const int of_thread = quads > 2 * kMaxThreads ? 4 : quads > kMaxThreads / 2 ? 2 : 1;
+    const int threads = (int)(((quads + of_thread - 1) / of_thread + 31) / 32 * 32);
+    return of_thread == 4 ? launch<4>(a, vec, threads, s) : of_thread == 2 ? launch<2>(a, vec, threads, s) : launch<1>(a, vec, threads, s);
 }
 
 }  // namespace q4k
