@@ -47,7 +47,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -INFINITY;
 constexpr float kSlack = 8.f;       // how far (log2) a score may exceed the running maximum
 constexpr int kExtra = 2;           // places of the list after a unit's tiles
-constexpr int kWaves = 3, kLong = 48;  // see shares_of
+constexpr int kWaves = 3, kLong = 40;  // see shares_of
 static_assert(kWaves * kMaxAttnResident == kMaxAttnShares, "the workspace holds two parts for each share");
 
 // 16 bytes into shared memory, of which the last 16 - bytes become zeros
@@ -128,7 +128,7 @@ struct Cfg {
     static constexpr int RB = D * (E4M3 ? 1 : 2);              // bytes of a cached row
     static constexpr int PITCH = RB + 16;
     static constexpr int CHUNKS = RB / 16;                     // 16-byte chunks of a row
-    static constexpr int TOK = RB <= 128 && NR < 4 ? 32 : 16;  // slots of a step
+    static constexpr int TOK = RB <= 128 && (NR < 4 || D == 64) ? 32 : 16;  // slots of a step
     static constexpr int MT = TOK / 16;
     static constexpr int CT = kWarps * TOK;                    // slots of a tile
     static constexpr int STAGE = 2 * TOK * PITCH;              // bytes of a stage: keys, then values
@@ -197,11 +197,13 @@ __device__ __forceinline__ void row_range(const AttnArgs &a, int r, int tok, int
 }
 
 // The list's `total` places go to a number of shares: share i is [share_begin(i), share_begin(i + 1)).
-// One for each resident CTA, so that all run at once; long lists are cut into up to kWaves times as many
-// (of kLong places at least), which start as others end and even out how fast the SMs read.
+// One for each resident CTA, so that all run at once; long lists are cut into two or three times as many
+// (of kLong places at least), which start as others end and even out how fast the SMs read.  Not into any number
+// between: a few more than are resident run on their own at the end (8 sequences of 16384 slots on 344 shares
+// took 120 us, on 304 they take 96).
 __device__ __forceinline__ int shares_of(int64_t total, int resident) {
-    const int64_t n = min(total / kLong, (int64_t)resident * kWaves);
-    return (int)min(total, max(n, (int64_t)resident));
+    const int64_t waves = min(max(total / ((int64_t)kLong * resident), (int64_t)1), (int64_t)kWaves);
+    return (int)min(total, waves * resident);
 }
 __device__ __forceinline__ int64_t share_begin(int64_t total, int shares, int i) {
     if (i >= shares) return total;
