@@ -1138,13 +1138,14 @@ cudaError_t launch(AttnArgs &a, const DeviceInfo &di, cudaStream_t s) {
     // a few units may be in hundreds of parts each
     const int join_threads = units * 64 <= a.resident ? kJoinWarps * 32 : kThreads;
     // weights: chunks of 2048 slots, which make the start of a block little work beside the rest, unless that leaves SMs
-    // idle; at the least 512, or 256 where more than 16 rows lengthen the rest (40 heads of one row over 32000 slots: 37 us
-    // with 256 and 35 with 512; 64 rows over 569 slots of 31 sequences: 52 and 54)
+    // idle; at the least 512, or 256 and 128 where more than 16 and 32 rows lengthen the rest (64 heads of one row over 32000
+    // slots: 37 us with 256 and 35 with 512; 112 rows of 41 sequences of 45 to 91 slots: 36 with 512, 34 with 256, 31
+    // with 128)
     const int64_t heads = (int64_t)a.c.batch * a.c.heads;
     int chunk = 2048, chunks = 0;
     if (a.weights) {
-        const int least = a.rows > 16 ? 256 : 512;
-        while (chunk > least && heads * ((a.cap + chunk - 1) / chunk) < 4 * di.sm_count) chunk /= 2;
+        const int least = a.rows > 32 ? 128 : a.rows > 16 ? 256 : 512;
+        while (chunk > least && heads * ((slots + chunk - 1) / chunk) < 4 * di.sm_count) chunk /= 2;  // (of slots in the window)
         chunks = (a.cap + chunk - 1) / chunk;
     }
     return launch_pdl(a.weights ? join_kernel<true> : join_kernel<false>, dim3((unsigned)(units * blocks + heads * chunks)), dim3(join_threads), 0, s, dim3(1), a, (int)blocks,

@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
     int turn = 0;
     pdl_wait();
     pdl_trigger();
-    const int64_t row = blockIdx.x;
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;  // (several rows a CTA: a warp each, without barriers)
+    if (row >= a.M) return;
     const Slice<NV, VEC> s = {(int)a.D, (int)threadIdx.x, (int)blockDim.x};
     float h[4 * NV];
     s.load(static_cast<const Res *>(a.r_in) + row * a.ldr, h);  // (on its way during the first norm)
@@ -399,7 +400,9 @@ template <int NV>
 cudaError_t launch(const NormArgs &a, bool vec, int threads, cudaStream_t s) {
     auto kern = a.bf16 ? (vec ? norm_kernel<NV, true, true> : norm_kernel<NV, false, true>)
                        : (vec ? norm_kernel<NV, true, false> : norm_kernel<NV, false, false>);
-    return launch_pdl(kern, dim3((unsigned)a.M), dim3(threads), 0, s, dim3(1), a);
+    // rows of one warp: eight to a CTA where they are many (8038 x 65: 8.5 us with one, 5 with eight)
+    const int rows = threads == 32 && a.M >= 2048 ? 8 : 1;
+    return launch_pdl(kern, dim3((unsigned)((a.M + rows - 1) / rows)), dim3(threads, rows), 0, s, dim3(1), a);
 }
 
 template <int NV>
@@ -422,7 +425,8 @@ cudaError_t launch_norm_residual(const DeviceInfo &di, const NormArgs &a, cudaSt
                      (!a.x || (al(a.x, 8) && a.ldx % 4 == 0)) && al(a.post_w, 16) && al(a.post_b, 16) && al(a.pre_w, 16) &&
                      al(a.pre_b, 16);
     const int64_t quads = (a.D + 3) / 4;  // groups of four values
-    // many rows that can be copied whole: a ring of at least two rows a CTA
+    // many rows that can be copied whole: a ring of at least two rows a CTA (577 x 5120: 5.9 us, a CTA a row 9.5); those of
+    // one warp go to a warp each below (8038 x 64: 7.6 us with the ring)
     const int64_t row_bytes = a.D * ((a.y ? 4 : 0) + (a.bf16 ? 2 : 4) + (a.y && a.gate && a.ld_gate != 0 ? 4 : 0));
     const bool bulk = vec && a.D % 8 == 0 && al(a.r_in, 16) && (a.bf16 ? a.ldr % 8 == 0 : true);
     // values of a thread: as many as leave no thread without any (8192 x 768 with 16 a thread of two warps, a quarter of
@@ -430,7 +434,7 @@ cudaError_t launch_norm_residual(const DeviceInfo &di, const NormArgs &a, cudaSt
     int nv = quads > 128 ? 4 : quads > 64 ? 2 : 1;
     while (nv > 1 && quads % (32 * nv) != 0 && quads % 32 == 0 && quads <= 640 * (nv / 2)) nv /= 2;
     const int threads_many = (int)(((quads + nv - 1) / nv + 31) / 32 * 32);
-    if (bulk && threads_many <= 640 && a.M >= 4 * di.sm_count) {
+    if (bulk && threads_many > 32 && threads_many <= 640 && a.M >= di.sm_count) {
         const int64_t biases = 4 * a.D * ((a.y && a.post != kNone && a.post_b ? 1 : 0) + (a.x && a.pre != kNone && a.pre_b ? 1 : 0));
         int per_sm = (nv == 4 ? 640 : 960) / threads_many;  // (as many as the registers allow)
         if (per_sm > 10) per_sm = 10;
