@@ -11,14 +11,15 @@
 // that holds the wanted rank; once a few slots are left they are ranked against each
 // other, which also settles equal weights by slot.  The last pass takes the slots in
 // order, a run to a thread, and numbers holes and fillers by one scan.  Bound by
-// latency (some fifteen block-wide steps; 256 threads for caches of up to 4096 slots, whose
-// steps would otherwise cost more in idle warps than in work); the reads are 8 bytes a slot.
+// latency (some fifteen block-wide steps, which fewer threads take faster); the reads are 8 bytes a slot.
 // move_kernel copies the rows, 16 bytes a lane, and their weights and positions: bound by HBM (two or
 // four rows a thread cost more in occupancy than their overlapping loads gave: 62 and 70 us against 59).
-// Measured: 9.3 us for 32 caches of 8 heads with one slot over 2048 (5 of them the selection), 81 us for
+// Measured: 9.4 us for 32 caches of 8 heads with one slot over 2048 (5 of them the selection), 81 us for
 // 16 caches of 9001 to 16384 slots to 8192 (15 the selection, 59 the copies: 333 MB at 5.7 TB/s).
 
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "decode_ops.h"
 #include "q4k_ptx.cuh"
@@ -26,7 +27,8 @@
 namespace q4k {
 namespace {
 
-constexpr int kSmall = 4096;    // slots up to which 256 threads do
+constexpr int kSmall = 4096;    // slots that 256 threads hold in registers
+constexpr int kMid = 8192;      // 512 threads, of which two CTAs share an SM (256 caches of 8000: 20.6 us, with 1024 23.6)
 constexpr int kHeld = 20480;    // slots that 1024 threads hold in registers, and whose keys leave room for two CTAs
 constexpr int kCached = 49152;  // slots whose keys fit in shared memory
 constexpr int kFew = 128;       // slots that are ranked against each other
@@ -75,7 +77,7 @@ struct Block {
 template <int THREADS, int KEYS, bool HELD>
 __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
     using B = Block<THREADS>;
-    constexpr int BINS = 2 * THREADS, LOG_BINS = THREADS == 1024 ? 11 : 9;
+    constexpr int BINS = 2 * THREADS, LOG_BINS = THREADS == 1024 ? 11 : THREADS == 512 ? 10 : 9;
     constexpr bool CACHED = KEYS > 0;
     static_assert(BINS == 1 << LOG_BINS, "two bins a thread");
     extern __shared__ __align__(16) uint32_t dyn[];
@@ -173,15 +175,21 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
             if (j < n) of_either(mine[x], prot);
         }
     } else {
-#pragma unroll 4
-        for (int j0 = 0; j0 < n; j0 += THREADS) {
-            const int j = j0 + tid;
-            const bool prot = j < n && is_protected(p[j]);
-            if (CACHED) {
-                const uint32_t m = __ballot_sync(kFull, prot);
-                if (lane == 0 && j < n) bits[j >> 5] = m;
+        constexpr int kAhead = 8;  // loads before the first is looked at
+        for (int j0 = 0; j0 < n; j0 += kAhead * THREADS) {
+            int32_t pj[kAhead];
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) pj[x] = p[min(j0 + x * THREADS + tid, n - 1)];
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                const int j = j0 + x * THREADS + tid;
+                const bool prot = j < n && is_protected(pj[x]);
+                if (CACHED) {
+                    const uint32_t m = __ballot_sync(kFull, prot);
+                    if (lane == 0 && j < n) bits[j >> 5] = m;
+                }
+                if (j < n) of_either(CACHED ? keys[j] : key_of(w[j]), prot);
             }
-            if (j < n) of_either(CACHED ? keys[j] : key_of(w[j]), prot);
         }
     }
     // visit(slot, key) for every slot of class `of` with a key in [lo, hi]
@@ -192,6 +200,14 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
                 if (x * THREADS >= n) break;
                 const int j = x * THREADS + tid;
                 if (j < n && mine[x] >= lo && mine[x] <= hi && ((prots >> x & 1) != 0) == of) visit(j, mine[x]);
+            }
+        } else if constexpr (CACHED) {
+            for (int j = 4 * tid; j < n; j += 4 * THREADS) {
+                const uint4 t = *reinterpret_cast<const uint4 *>(keys + j);  // (past n: whatever is there)
+                const uint32_t k[4] = {t.x, t.y, t.z, t.w}, prot = bits[j >> 5] >> (j & 31);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (j + x < n && k[x] >= lo && k[x] <= hi && ((prot >> x & 1) != 0) == of) visit(j + x, k[x]);
             }
         } else {
 #pragma unroll 4
@@ -292,19 +308,22 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
         __syncthreads();
     }
     // ---- holes below keep and fillers from there on, numbered in slot order: a run of slots a thread, so long that one
-    // scan is enough where 28 are (4, 12, 20 or 28: then the threads' 16-byte reads meet in no bank).  The list, at most
-    // half as many pairs as slots, then takes the keys' place, from where it goes out in whole sectors
+    // scan is enough for the slots in shared memory (4, 12, 20, ...: then the threads' 16-byte reads meet in no bank).
+    // The list, at most half as many pairs as slots, then takes the keys' place, from where it goes out in whole sectors
     int2 *list_out = a.moves + (int64_t)bh * a.max_moves;
     uint32_t holes = 0, fills = 0;
-    const int per = CACHED ? min(((n + THREADS - 1) / THREADS + 3) / 8 * 8 + 4, 28) : 4;
-    const bool once = CACHED && n <= per * THREADS;
-    int2 *const moves = once ? reinterpret_cast<int2 *>(keys) : list_out;
+    const int per = CACHED ? ((n + THREADS - 1) / THREADS + 3) / 8 * 8 + 4 : 4;
+    constexpr int MOST = CACHED ? (KEYS / THREADS + 3) / 8 * 8 + 4 : 4;
+    using Mark = typename std::conditional<(MOST > 32), unsigned long long, uint32_t>::type;
+    static_assert(MOST <= 64 && MOST * THREADS < 65536, "marks of a thread in a word, counts of a block in 16 bits");
+    int2 *const moves = CACHED ? reinterpret_cast<int2 *>(keys) : list_out;
     __syncthreads();
     for (int base = 0, turn = 0; base < n; base += per * THREADS, turn ^= 1) {
         const int j0 = base + per * tid;
-        uint32_t count = 0, mark = 0;  // holes, fillers << 16; slots of either kind
+        uint32_t count = 0;  // holes, fillers << 16
+        Mark mark = 0;       // slots of either kind
 #pragma unroll
-        for (int q = 0; q < (CACHED ? 7 : 1); ++q) {
+        for (int q = 0; q < MOST / 4; ++q) {
             const int j = j0 + 4 * q;
             if (4 * q >= per || j >= n) break;
             uint32_t k[4] = {0, 0, 0, 0}, prot = 0;
@@ -322,21 +341,21 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
                 const bool of_class = ((prot >> x & 1) != 0) == in_prot;
                 const bool gone = of_class ? k[x] < cut || (k[x] == cut && (uint32_t)(j + x) <= cut_slot) : in_prot;
                 const bool below = j + x < keep;
-                if (j + x < n && gone == below) mark |= 1u << (4 * q + x), count += below ? 1u : 1u << 16;
+                if (j + x < n && gone == below) mark |= (Mark)1 << (4 * q + x), count += below ? 1u : 1u << 16;
             }
         }
         uint32_t total;
         const uint32_t before = B::scan(count, scratch[turn], total);
         uint32_t hole = holes + (before & 0xFFFF), fill = fills + (before >> 16);
         for (; mark != 0; mark &= mark - 1) {
-            const int slot = j0 + __ffs(mark) - 1;
+            const int slot = j0 + (MOST > 32 ? __ffsll((long long)mark) : __ffs((int)mark)) - 1;
             if (slot < keep) moves[hole++].x = slot;
             else moves[fill++].y = slot;
         }
         holes += total & 0xFFFF;
         fills += total >> 16;
     }
-    if (once) {
+    if (CACHED) {
         __syncthreads();
         for (uint32_t i = tid; i < holes; i += THREADS) list_out[i] = moves[i];
     }
@@ -392,12 +411,15 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
 }  // namespace
 
 cudaError_t launch_kv_evict(const DeviceInfo &di, const EvictArgs &a, cudaStream_t s) {
-    cudaError_t e = a.cap <= kSmall    ? launch_select<256, kSmall, true>(a, s)
+    const int bh = a.c.batch * a.c.heads;
+    // more short caches than SMs: small CTAs, of which more share one (256 heads with one slot over 2048: 9.4 us, with 512
+    // threads 10.9; 64 heads of 4096 to 2048: 30.1 and 27.4)
+    cudaError_t e = a.cap <= kSmall && bh > di.sm_count ? launch_select<256, kSmall, true>(a, s)
+                    : a.cap <= kMid    ? launch_select<512, kMid, true>(a, s)
                     : a.cap <= kHeld   ? launch_select<1024, kHeld, true>(a, s)
                     : a.cap <= kCached ? launch_select<1024, kCached, false>(a, s)
                                        : launch_select<1024, 0, false>(a, s);
     if (e != cudaSuccess) return e;
-    const int bh = a.c.batch * a.c.heads;
     const int chunks = a.c.dim * (a.c.e4m3 ? 1 : 2) / 16, rows = kMoveThreads / chunks;
     // a few rounds of copies per block, but no more blocks than fill the GPU a few times over
     int64_t per_head = (a.max_moves + 4 * rows - 1) / (4 * rows);
