@@ -524,6 +524,14 @@ def test_evict_equal_weights_over_many_slots(n, part):
     assert got.tolist() == [budget] and po[0, 0, :budget].tolist() == [was[j] for j in take[0][0]]
 
 
+@pytest.mark.parametrize("kind", ["random", "ties", "equal"])
+@pytest.mark.parametrize("most", [300, 4096])
+def test_evict_more_heads_than_sms(kind, most):
+    """More sequences and heads than a GPU has SMs, which smaller CTAs take."""
+    lens = [(37 * i) % 90 + 1 for i in range(78)] + [most, most - 1]
+    test_evict(BF, 64, 16, "phsd", 4, lens, 32, 2, 8, kind, True)
+
+
 def test_evict_bad_indices():
     g = gen_of(31)
     k, v = pool((4, 1, 16, 64), BF, "phsd", g)
