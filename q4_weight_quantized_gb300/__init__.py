@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libq4k.so")
@@ -125,6 +126,8 @@ def load(path: str | None = None):
                               st),
         "q4k_sample": ([P, i64, i64, i64, P, P, P, P, P, P, P, P], st),
     }
+    for name in _SLOTS:
+        sig[name + "_slots"] = ([ctypes.c_char_p], st)
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
         f.argtypes = args
@@ -139,6 +142,27 @@ def _ptr(a):
         return a
     return int(a) if isinstance(a, int) else a.data_ptr()
 
+
+# The arguments of the functions below in 8 bytes each, as their _slots forms take them: a foreign call converts every
+# argument on its own, and for these that took a quarter of a small call's host time.
+_SLOTS = {name: struct.Struct(form).pack for name, form in (
+    ("q4k_kv_append", "=22q"), ("q4k_attn_decode", "=6q2d5qd3q"), ("q4k_kv_evict", "=14q"),
+    ("q4k_norm_residual", "=7qd2qd7qd3q"), ("q4k_sample", "=12q"))}
+
+
+def _adr(a):
+    if type(a) is int:
+        return a
+    if a is None:
+        return 0
+    return int(a) if isinstance(a, int) else a.data_ptr()
+
+
+def _cache(c):
+    return 0 if c is None else ctypes.addressof(c)
+
+
+_pack_append, _pack_attn, _pack_evict, _pack_norm, _pack_sample = _SLOTS.values()
 
 _current_stream = None
 
@@ -315,9 +339,10 @@ def q4k_kv_append(cache, T: int, n_heads: int, q, ldq: int, k, ldk: int, v, ldv:
                   stream=None) -> None:
     """Rotary embedding of new queries and keys, and the write of new keys and values into the paged cache
     (a KvCache); q, k, v fp32, q_out bf16."""
-    _check(load().q4k_kv_append(cache, T, n_heads, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(seq),
-                                _ptr(slot), _ptr(pos), _ptr(rope), n_pos, rope_dim, rope_mode, _ptr(q_out), ldqo,
-                                _ptr(weights), _ptr(positions), ld_meta, _stream(stream)), "q4k_kv_append")
+    _check(load().q4k_kv_append_slots(_pack_append(
+        _cache(cache), T, n_heads, _adr(q), ldq, _adr(k), ldk, _adr(v), ldv, _adr(seq), _adr(slot), _adr(pos), _adr(rope),
+        n_pos, rope_dim, rope_mode, _adr(q_out), ldqo, _adr(weights), _adr(positions), ld_meta,
+        _adr(_stream(stream)))), "q4k_kv_append")
 
 
 def q4k_attn_decode_workspace_size(cache, n_heads: int, n_q: int, ld_weights: int = 0) -> int:
@@ -328,9 +353,9 @@ def q4k_attn_decode(cache, seq_lens, q, ldq: int, n_heads: int, n_q: int, scale:
                     o, ldo: int, weights, ld_weights: int, decay: float, ws, ws_bytes: int, stream=None) -> None:
     """Attention of the last n_q tokens of every sequence over its paged cache; q, o bf16 [batch*n_q][ld].  With
     `weights` (fp32 [batch][n_kv_heads][ld_weights]) it also adds up the weight each cached slot received."""
-    _check(load().q4k_attn_decode(cache, _ptr(seq_lens), _ptr(q), ldq, n_heads, n_q, scale, softcap, window,
-                                  _ptr(o), ldo, _ptr(weights), ld_weights, decay, _ptr(ws), ws_bytes,
-                                  _stream(stream)), "q4k_attn_decode")
+    _check(load().q4k_attn_decode_slots(_pack_attn(
+        _cache(cache), _adr(seq_lens), _adr(q), ldq, n_heads, n_q, scale, softcap, window, _adr(o), ldo, _adr(weights),
+        ld_weights, decay, _adr(ws), ws_bytes, _adr(_stream(stream)))), "q4k_attn_decode")
 
 
 def q4k_kv_evict_workspace_size(cache, ld_meta: int) -> int:
@@ -340,23 +365,25 @@ def q4k_kv_evict_workspace_size(cache, ld_meta: int) -> int:
 def q4k_kv_evict(cache, seq_lens, new_lens, budget: int, sinks: int, recent: int, weights, positions, weights_out,
                  positions_out, ld_meta: int, ws, ws_bytes: int, stream=None) -> None:
     """Cuts every sequence of the cache to at most `budget` slots, each KV head dropping its least attended ones."""
-    _check(load().q4k_kv_evict(cache, _ptr(seq_lens), _ptr(new_lens), budget, sinks, recent, _ptr(weights),
-                               _ptr(positions), _ptr(weights_out), _ptr(positions_out), ld_meta, _ptr(ws), ws_bytes,
-                               _stream(stream)), "q4k_kv_evict")
+    _check(load().q4k_kv_evict_slots(_pack_evict(
+        _cache(cache), _adr(seq_lens), _adr(new_lens), budget, sinks, recent, _adr(weights), _adr(positions),
+        _adr(weights_out), _adr(positions_out), ld_meta, _adr(ws), ws_bytes, _adr(_stream(stream)))), "q4k_kv_evict")
 
 
 def q4k_norm_residual(M: int, D: int, y, ldy: int, post: int, post_w, post_b, post_eps: float, gate, ld_gate: int,
                       scale: float, r_in, r_out, ldr: int, r_dtype: int, pre: int, pre_w, pre_b, pre_eps: float, x,
                       ldx: int, stream=None) -> None:
     """h = r_in + scale * gate * post(y); r_out = h; x = bf16(pre(h))."""
-    _check(load().q4k_norm_residual(M, D, _ptr(y), ldy, post, _ptr(post_w), _ptr(post_b), post_eps, _ptr(gate),
-                                    ld_gate, scale, _ptr(r_in), _ptr(r_out), ldr, r_dtype, pre, _ptr(pre_w),
-                                    _ptr(pre_b), pre_eps, _ptr(x), ldx, _stream(stream)), "q4k_norm_residual")
+    _check(load().q4k_norm_residual_slots(_pack_norm(
+        M, D, _adr(y), ldy, post, _adr(post_w), _adr(post_b), post_eps, _adr(gate), ld_gate, scale, _adr(r_in),
+        _adr(r_out), ldr, r_dtype, pre, _adr(pre_w), _adr(pre_b), pre_eps, _adr(x), ldx,
+        _adr(_stream(stream)))), "q4k_norm_residual")
 
 
 def q4k_sample(logits, M: int, V: int, ldl: int, temperature, top_k, top_p, min_p, u, token, prob=None,
                stream=None) -> None:
     """Draws a token for each row of fp32 logits [M][ldl] with the given random numbers u; per-row settings, each
     may be None."""
-    _check(load().q4k_sample(_ptr(logits), M, V, ldl, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
-                             _ptr(u), _ptr(token), _ptr(prob), _stream(stream)), "q4k_sample")
+    _check(load().q4k_sample_slots(_pack_sample(
+        _adr(logits), M, V, ldl, _adr(temperature), _adr(top_k), _adr(top_p), _adr(min_p), _adr(u), _adr(token), _adr(prob),
+        _adr(_stream(stream)))), "q4k_sample")

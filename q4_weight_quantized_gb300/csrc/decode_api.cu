@@ -2,6 +2,10 @@
 // validation, workspace layout and dispatch.  Their contract is in include/q4k.h.
 #include <cuda_runtime.h>
 
+#include <cstring>
+#include <type_traits>
+#include <utility>
+
 #include <cmath>
 
 #include "decode_ops.h"
@@ -67,6 +71,29 @@ KvView view(const q4k_kv_cache *c, const DeviceInfo &di) {
     v.v_scale = c->v_scale;
     v.status = di.status;
     return v;
+}
+
+// Argument of type T from 8 bytes.
+template <typename T>
+T argument(const char *slot) {
+    if constexpr (std::is_floating_point<T>::value) {
+        double v;
+        std::memcpy(&v, slot, 8);
+        return (T)v;
+    } else {
+        int64_t v;
+        std::memcpy(&v, slot, 8);
+        if constexpr (std::is_pointer<T>::value) return reinterpret_cast<T>(v);
+        else return static_cast<T>(v);
+    }
+}
+template <typename... Args, size_t... I>
+q4k_status call_each(q4k_status (*f)(Args...), const char *slots, std::index_sequence<I...>) {
+    return f(argument<Args>(slots + 8 * I)...);
+}
+template <typename... Args>
+q4k_status call(q4k_status (*f)(Args...), const void *slots) {
+    return call_each(f, static_cast<const char *>(slots), std::index_sequence_for<Args...>{});
 }
 
 q4k_status finish(cudaError_t e) { return e == cudaSuccess ? Q4K_OK : cuda_fail(e); }
@@ -297,5 +324,14 @@ q4k_status q4k_sample(const float *logits, int64_t M, int64_t V, int64_t ldl, co
     a.token = token, a.prob = prob;
     return finish(launch_sample(di, a, static_cast<cudaStream_t>(stream)));
 }
+
+// What the Python package calls: the same functions with their arguments one after the other in 8 bytes each (integers,
+// addresses, floats as doubles).  A foreign call from Python converts each argument on its own, which for twenty of
+// them takes longer than the rest of a small call on the host.
+q4k_status q4k_kv_append_slots(const void *slots) { return call(q4k_kv_append, slots); }
+q4k_status q4k_attn_decode_slots(const void *slots) { return call(q4k_attn_decode, slots); }
+q4k_status q4k_kv_evict_slots(const void *slots) { return call(q4k_kv_evict, slots); }
+q4k_status q4k_norm_residual_slots(const void *slots) { return call(q4k_norm_residual, slots); }
+q4k_status q4k_sample_slots(const void *slots) { return call(q4k_sample, slots); }
 
 }  // extern "C"
