@@ -495,6 +495,7 @@ q4k_status q4k_kv_append(const q4k_kv_cache *cache, int64_t T, int32_t n_heads, 
  *   weights (may be NULL): fp32 [batch][n_kv_heads][ld_weights], updated for every
  *     slot j < len:  weights[b][h][j] = decay*weights[b][h][j] + sum of
  *     softmax(s[r])[j] over the rows r of head h.  len must be <= ld_weights.
+ *     (A slot left out for its page: decay*weights alone.)
  * Products are exact and sums, maxima and the joined softmax fp32; the weights p
  * enter the product with v as the sum of two bf16 values (to 2^-16), for an e4m3 cache
  * as one f16 value (to 2^-12, and to 2^-32 of the largest), and o is rounded once.  The length is split over the whole GPU by the lengths of the batch,

@@ -729,6 +729,13 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
                     }
                 }
             }
+        } else if (a.logits) {
+            // none of the step's slots is there: no row has a score for them
+            const int r0 = cur.rt * 8 * NR, rows = min(8 * NR, a.rows - r0);
+            float *at = a.logits + (((int64_t)cur.b * a.c.heads + cur.head) * a.rows + r0) * a.ld_logits + j0 + lane;
+            if (lane < TOK && j0 + lane < cur.end)
+#pragma unroll 1
+                for (int r = 0; r < rows; ++r, at += a.ld_logits) *at = kNone;
         }
         __syncwarp();
         const uint32_t read_stage = ring + stage * C::STAGE;  // free until the next step
