@@ -521,6 +521,8 @@ q4k_status q4k_attn_decode(const q4k_kv_cache *cache, const int32_t *seq_lens, c
  * it, in increasing order; the other kept slots stay where they are.  So pages from
  * ceil(budget/page_size) on are free afterwards, and pages must not be shared between
  * sequences below that.
+ * A move from or to a page whose id is out of range is not made: the hole keeps the
+ * token that was to go, with its own weight and position, and the kept one is lost.
  *   weights, positions: [batch][n_kv_heads][ld_meta]; weights_out and positions_out
  *     receive the entries of the slots < new length (each may be the input array;
  *     otherwise they must not overlap it).

@@ -383,19 +383,26 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
     const int n = a.count[bh];
     const int2 *list = a.moves + (int64_t)bh * a.max_moves;
     const int32_t *table = a.c.table + b * a.c.ld_table;
+    // The ids of a move's two pages; if one is out of range, the move is not made: the hole keeps its token.
+    auto pages_of = [&](int2 m, uint32_t &pt, uint32_t &ps, int32_t &to, int32_t &from) {
+        pt = page_of(a.c, m.x), ps = page_of(a.c, m.y);
+        to = __ldg(table + pt), from = __ldg(table + ps);
+        return page_ok(a.c, to) && page_ok(a.c, from);
+    };
+    uint32_t pt, ps;
+    int32_t to, from;
     // (here rather than at the end of the selection, which every head waits for)
     const int64_t meta = (int64_t)bh * a.ld_meta;
     for (int i = part * kMoveThreads + threadIdx.x; i < n; i += per_head * kMoveThreads) {
         const int2 m = list[i];
+        if (!pages_of(m, pt, ps, to, from)) continue;
         a.weights_out[meta + m.x] = a.weights[meta + m.y];
         a.positions_out[meta + m.x] = a.positions[meta + m.y];
     }
     const int rows = kMoveThreads / chunks, ch = threadIdx.x % chunks;
     for (int i = part * rows + threadIdx.x / chunks; i < n; i += per_head * rows) {
         const int2 m = list[i];
-        const uint32_t pt = page_of(a.c, m.x), ps = page_of(a.c, m.y);
-        const int32_t to = __ldg(table + pt), from = __ldg(table + ps);
-        if (!page_ok(a.c, to) || !page_ok(a.c, from)) {
+        if (!pages_of(m, pt, ps, to, from)) {
             atomicOr(a.c.status, kDevIndex);
             continue;
         }

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import q4_weight_quantized_gb300 as q4k
-from tests.test_decode_ops import BF, F8, gen_of, np64, pool, run_attn, table_of
+from oracle import decode_ref as R
+from tests.test_decode_ops import BF, F8, gen_of, np64, pool, run_attn, run_evict, table_of
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +118,42 @@ def test_attn_scores_of_an_earlier_call_are_not_read(dtype):
     with pytest.raises(q4k.Q4KError):
         q4k.q4k_check_device()
     assert (w[0, 0, 2 * page:3 * page] == 0).all() and abs(float(w.sum()) - 4) < 1e-3
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dtype,D", [(BF, 64), (F8, 128)])
+@pytest.mark.parametrize("bad", ["from", "to", "both"])
+def test_evict_makes_a_move_whole_or_not_at_all(bad, dtype, D, in_place):
+    """A move between pages of which one is out of range is not made: the hole keeps its token, key, value, weight and
+    position alike, and every other move is made."""
+    g = gen_of(5)
+    B, Hkv, page, per, budget = 2, 2, 16, 20, 150
+    lens = [300, 290]
+    k, v = pool((B * per, Hkv, page, D), dtype, "phsd", g)
+    table = table_of(B, per, B * per, g)
+    if bad != "to":
+        table[0, 12], table[1, 15] = -1, B * per         # slots from the budget on: moves come from there
+    if bad != "from":
+        table[0, 3], table[1, 0] = 2 ** 31 - 1, -7       # slots below it: moves go there
+    w = torch.rand(B, Hkv, per * page, generator=g, device="cuda")
+    p = torch.stack([torch.randperm(per * page, generator=g, device="cuda") for _ in range(B * Hkv)]).view(B, Hkv, -1).int()
+    new, take = R.kv_evict(lens, w.cpu().numpy(), p.cpu().numpy(), budget, 4, 16)
+    u8 = lambda t: t.view(torch.uint8) if t.dtype == F8 else t  # noqa: E731
+    k0, v0, w0, p0 = u8(k).clone(), u8(v).clone(), w.clone(), p.clone()
+    got, wo, po = run_evict(q4k.kv_cache(k, v, table), lens, budget, 4, 16, w, p, in_place)
+    with pytest.raises(q4k.Q4KError) as err:
+        q4k.q4k_check_device()
+    assert err.value.status == q4k.Q4K_ERR_INDEX and got.tolist() == new.tolist()
+    ids, refused = table.cpu().numpy(), 0
+    for b in range(B):
+        for h in range(Hkv):
+            for i, j in enumerate(take[b][h]):
+                to, at = ids[b, i // page], ids[b, j // page]
+                ok = 0 <= to < B * per and 0 <= at < B * per
+                refused += not ok and i != j
+                j = j if ok else i
+                assert wo[b, h, i] == w0[b, h, j] and po[b, h, i] == p0[b, h, j], (b, h, i)
+                if 0 <= to < B * per:
+                    for now, was in ((u8(k), k0), (u8(v), v0)):
+                        assert torch.equal(now[to, h, i % page], was[ids[b, j // page], h, j % page]), (b, h, i)
+    assert refused > 4
