@@ -405,10 +405,10 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
                 for (int f = 0; f < 2; ++f) mx = fmaxf(mx, fmaxf(fabsf(lo_f32(v[ks][f])), fabsf(hi_f32(v[ks][f]))));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-            // 2^(14 - exponent of the largest): f16 then holds bf16's 8 bits of every value down to
-            // 2^-28 of the largest
+            // 2^(14 - exponent of the largest), at most 2^127: f16 then holds bf16's 8 bits of every value down to 2^-31
+            // of the largest, and a smaller one to 2^-39 of it
             const int e = (int)(__float_as_uint(mx) >> 23);
-            if (e > 14 && e < 255) up = __uint_as_float((uint32_t)min(127 + 14 + 127 - e, 254) << 23);
+            if (e < 255) up = __uint_as_float((uint32_t)min(127 + 14 + 127 - e, 254) << 23);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
