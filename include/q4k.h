@@ -137,6 +137,10 @@ int q4k_set_static_weights(int enable);
  *       GB300.
  * The boundary between the two paths stays: rows of calls with M <= 16 and
  * M > 16 differ in rounding (different kernels, each within its bar).
+ * Of the operators between a decode step's products, q4k_norm_residual follows the
+ * mode (about 0.15 us for a few rows), q4k_kv_append, q4k_kv_evict and q4k_sample give
+ * a token or sequence the same bits in either, and q4k_attn_decode is not
+ * batch-invariant in either: it splits its work by all lengths of the batch.
  * Process-wide; applies to calls enqueued after it returns.  Returns the previous
  * setting (0 or 1). */
 int q4k_set_batch_invariant(int enable);
@@ -551,7 +555,9 @@ q4k_status q4k_kv_evict(const q4k_kv_cache *cache, const int32_t *seq_lens, int3
  * NULL (1).  r_in and r_out [M][ldr] of type r_dtype; r_out may be r_in, or NULL (not
  * kept).  x bf16 [M][ldx], may be NULL if r_out is not (pre is then not computed).
  * Everything is fp32 until r_out and x are rounded once each; x comes from h before
- * r_out's rounding.  1 <= D <= 2^20; pointers aligned to their element. */
+ * r_out's rounding.  1 <= D <= 2^20; pointers aligned to their element.  A row's last
+ * bits depend on D, on how pointers and strides are aligned, and on whether M is below
+ * the number of SMs, but with q4k_set_batch_invariant(1) not on M. */
 q4k_status q4k_norm_residual(int64_t M, int64_t D, const float *y, int64_t ldy, int post, const float *post_w,
                              const float *post_b, float post_eps, const float *gate, int64_t ld_gate, float scale,
                              const void *r_in, void *r_out, int64_t ldr, int r_dtype, int pre, const float *pre_w,

@@ -50,6 +50,8 @@ q4k_status cuda_fail(cudaError_t e) {
     return Q4K_ERR_CUDA;
 }
 
+bool batch_invariant() { return g_batch_invariant.load(std::memory_order_relaxed) != 0; }
+
 unsigned long long context_id() {
     std::call_once(g_ctx_once, [] {
         void *fn = nullptr;
@@ -314,7 +316,7 @@ q4k_status q4k_gemm(const void *w, int64_t N, int64_t K, const uint16_t *x, int6
     // otherwise the tensor-core kernel, one CTA per output tile (with a cluster K
     // split when the tiles leave the GPU half idle)
     const bool early = g_static_weights.load(std::memory_order_relaxed) != 0;
-    const bool invariant = g_batch_invariant.load(std::memory_order_relaxed) != 0;
+    const bool invariant = batch_invariant();
     cudaError_t e;
     if (M == 1 && !invariant) {
         const unsigned long long lim = g_gemv_wait_ns.load(std::memory_order_relaxed);
@@ -364,7 +366,7 @@ q4k_status q4k_gemm_x8(const void *w, int64_t N, int64_t K, const int8_t *q, con
         e = launch_expand_x8(di, q, s, M, K, xh, cs);
         if (e == cudaSuccess)
             e = launch_gemm_tc(di, w, N, K, xh, M, K, y, ldy,
-                               g_batch_invariant.load(std::memory_order_relaxed) != 0, cs);
+                               batch_invariant(), cs);
     }
     return e == cudaSuccess ? Q4K_OK : cuda_fail(e);
 }
@@ -394,7 +396,7 @@ q4k_status q4k_nvfp4_gemm(const void *w, float g, int64_t N, int64_t K, const ui
                                                 g_static_weights.load(std::memory_order_relaxed) != 0,
                                                 static_cast<cudaStream_t>(stream))
                             : launch_gemm_tc_nvfp4(di, w, g, N, K, x, M, ldx, y, ldy,
-                                                   g_batch_invariant.load(std::memory_order_relaxed) != 0,
+                                                   batch_invariant(),
                                                    static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? Q4K_OK : cuda_fail(e);
 }

@@ -301,6 +301,7 @@ q4k_status q4k_norm_residual(int64_t M, int64_t D, const float *y, int64_t ldy, 
     a.r_in = r_in, a.r_out = r_out, a.ldr = ldr, a.bf16 = r_dtype == Q4K_RES_BF16;
     a.pre = pre, a.pre_w = pre_w, a.pre_b = pre_b, a.pre_eps = pre_eps;
     a.x = x, a.ldx = ldx;
+    a.invariant = batch_invariant();
     a.status = di.status;
     return finish(launch_norm_residual(di, a, static_cast<cudaStream_t>(stream)));
 }

@@ -94,6 +94,7 @@ struct NormArgs {
     float pre_eps;
     uint16_t *x;
     int64_t ldx;
+    int invariant;  // a row's bits must not depend on M
     unsigned int *status;
 };
 cudaError_t launch_norm_residual(const DeviceInfo &di, const NormArgs &a, cudaStream_t s);

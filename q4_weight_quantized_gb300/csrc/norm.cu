@@ -426,7 +426,9 @@ cudaError_t launch_norm_residual(const DeviceInfo &di, const NormArgs &a, cudaSt
                      al(a.pre_b, 16);
     const int64_t quads = (a.D + 3) / 4;  // groups of four values
     // many rows that can be copied whole: a ring of at least two rows a CTA (577 x 5120: 5.9 us, a CTA a row 9.5); those of
-    // one warp go to a warp each below (8038 x 64: 7.6 us with the ring)
+    // one warp go to a warp each below (8038 x 64: 7.6 us with the ring).  The two forms round in another order, so where a
+    // row's bits must not depend on M the ring takes few rows, too (one of 5120: 3.0 us, a CTA a row 2.9; the other way
+    // about, 4096 of them take 87 instead of 37)
     const int64_t row_bytes = a.D * ((a.y ? 4 : 0) + (a.bf16 ? 2 : 4) + (a.y && a.gate && a.ld_gate != 0 ? 4 : 0));
     const bool bulk = vec && a.D % 8 == 0 && al(a.r_in, 16) && (a.bf16 ? a.ldr % 8 == 0 : true);
     // values of a thread: as many as leave no thread without any (8192 x 768 with 16 a thread of two warps, a quarter of
@@ -434,7 +436,7 @@ cudaError_t launch_norm_residual(const DeviceInfo &di, const NormArgs &a, cudaSt
     int nv = quads > 128 ? 4 : quads > 64 ? 2 : 1;
     while (nv > 1 && quads % (32 * nv) != 0 && quads % 32 == 0 && quads <= 640 * (nv / 2)) nv /= 2;
     const int threads_many = (int)(((quads + nv - 1) / nv + 31) / 32 * 32);
-    if (bulk && threads_many > 32 && threads_many <= 640 && a.M >= di.sm_count) {
+    if (bulk && threads_many > 32 && threads_many <= 640 && (a.M >= di.sm_count || a.invariant)) {
         const int64_t biases = 4 * a.D * ((a.y && a.post != kNone && a.post_b ? 1 : 0) + (a.x && a.pre != kNone && a.pre_b ? 1 : 0));
         int per_sm = (nv == 4 ? 640 : 960) / threads_many;  // (as many as the registers allow)
         if (per_sm > 10) per_sm = 10;

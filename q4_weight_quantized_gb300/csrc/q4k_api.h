@@ -10,6 +10,9 @@ namespace q4k {
 // Q4K_OK if a compute capability 10.3 device is current (its properties in *di).
 q4k_status check_device(DeviceInfo *di);
 
+// The setting of q4k_set_batch_invariant.
+bool batch_invariant();
+
 // Records e for q4k_last_cuda_error and returns Q4K_ERR_CUDA.
 q4k_status cuda_fail(cudaError_t e);
 

@@ -35,3 +35,33 @@ def test_attn_e4m3_queries_down_to_the_smallest(e):
     assert (np.abs(np64(o) - want) <= mag * (2.2 * err + 2.0 ** -14 + 2.0 ** -11) + np.abs(want) * 2.0 ** -8 + 2.0 ** -20).all()
 
 
+@pytest.mark.parametrize("D", [8, 64, 300, 768, 1000, 5120, 10240, 12288])
+@pytest.mark.parametrize("post,pre,gate,res,bias", [
+    (1, 1, "row", BF, False), (2, 1, None, torch.float32, True), (0, 2, "all", torch.float32, True), (1, 0, "all", BF, True),
+    (1, 2, "row", torch.float32, True)])
+def test_norm_rows_do_not_depend_on_the_batch(D, post, pre, gate, res, bias):
+    """Batch-invariant mode: a row has the same bits alone and among many."""
+    g = gen_of(D)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    M = 2100 if D <= 1000 else 500
+    y, r = rnd(M, D) * 3, (rnd(M, D) * 2).to(res)
+    w1, w2 = 1 + 0.2 * rnd(D), 1 + 0.2 * rnd(D)
+    b1, b2 = (rnd(D), rnd(D)) if bias else (None, None)
+    gt = None if gate is None else rnd(1 if gate == "row" else M, D)
+    kind = q4k.Q4K_RES_FP32 if res == torch.float32 else q4k.Q4K_RES_BF16
+
+    def call(lo, hi):
+        out, x = torch.zeros(hi - lo, D, dtype=res, device="cuda"), torch.zeros(hi - lo, D, dtype=BF, device="cuda")
+        q4k.q4k_norm_residual(hi - lo, D, y[lo:hi], D, post, w1, b1, 1e-5, gt[lo:hi] if gate == "all" else gt,
+                              D if gate == "all" else 0, 0.7, r[lo:hi], out, D, kind, pre, w2, b2, 1e-6, x, D)
+        return out, x
+
+    was = q4k.q4k_set_batch_invariant(True)
+    try:
+        out, x = call(0, M)
+        for lo, hi in [(0, 1), (1, 2), (M - 1, M), (7, 24), (100, 251), (100, 252), (100, 253), (150, 453)]:
+            some, xs = call(lo, hi)
+            assert torch.equal(some, out[lo:hi]) and torch.equal(xs, x[lo:hi]), (lo, hi)
+    finally:
+        q4k.q4k_set_batch_invariant(was)
+    q4k.q4k_check_device()
