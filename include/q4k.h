@@ -150,11 +150,11 @@ int q4k_set_batch_invariant(int enable);
  * its work, wait for its own copies in flight, reach all of its barriers and
  * set a device status word that q4k_check_device reports as Q4K_ERR_TIMEOUT.
  * This sets the limit of the decode GEMV's main-loop waits (q4k_gemv, and
- * q4k_gemm with M = 1 outside batch-invariant mode) to `ns`, so that a test can
- * make that path run out without faulting or hanging anything; 0 restores the
- * standard limit.  Under 1000 ns a wait tests its copy once, without blocking,
- * and gives up at once if it has not landed.  A GEMV whose wait ran out leaves
- * its output undefined.
+ * q4k_gemm with M = 1 outside batch-invariant mode) and of q4k_norm_residual's
+ * waits for its ring of rows to `ns`, so that a test can make those paths run out
+ * without faulting or hanging anything; 0 restores the standard limit.  Under
+ * 1000 ns a wait tests its copy once, without blocking, and gives up at once if it
+ * has not landed.  A call whose wait ran out leaves its outputs undefined.
  * Process-wide; applies to calls enqueued after it returns.  Returns the
  * previous setting (0 = standard). */
 unsigned long long q4k_set_gemv_wait_limit_ns(unsigned long long ns);

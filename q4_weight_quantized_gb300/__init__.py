@@ -225,8 +225,8 @@ def q4k_set_static_weights(enable: bool) -> bool:
 
 
 def q4k_set_gemv_wait_limit_ns(ns: int) -> int:
-    """Test hook: the limit of the decode GEMV's main-loop waits in nanoseconds (0:
-    the standard 2 s); returns the previous setting.  See include/q4k.h."""
+    """Failure-detection test hook: limit (ns, 0 = standard) of the decode GEMV's main-loop waits and of
+    q4k_norm_residual's waits for its ring of rows.  Returns the previous setting."""
     return int(load().q4k_set_gemv_wait_limit_ns(int(ns)))
 
 

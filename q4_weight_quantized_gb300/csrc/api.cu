@@ -52,6 +52,11 @@ q4k_status cuda_fail(cudaError_t e) {
 
 bool batch_invariant() { return g_batch_invariant.load(std::memory_order_relaxed) != 0; }
 
+unsigned long long wait_limit_ns() {
+    const unsigned long long ns = g_gemv_wait_ns.load(std::memory_order_relaxed);
+    return ns ? ns : kWaitLimitNs;
+}
+
 unsigned long long context_id() {
     std::call_once(g_ctx_once, [] {
         void *fn = nullptr;
@@ -319,8 +324,7 @@ q4k_status q4k_gemm(const void *w, int64_t N, int64_t K, const uint16_t *x, int6
     const bool invariant = batch_invariant();
     cudaError_t e;
     if (M == 1 && !invariant) {
-        const unsigned long long lim = g_gemv_wait_ns.load(std::memory_order_relaxed);
-        e = launch_gemv(di, w, N, K, x, y, early, lim ? lim : kWaitLimitNs, s);
+        e = launch_gemv(di, w, N, K, x, y, early, wait_limit_ns(), s);
     }
     else if (M <= 16) e = launch_smallm(di, w, N, K, x, M, ldx, y, ldy, early, s);
     else e = launch_gemm_tc(di, w, N, K, x, M, ldx, y, ldy, invariant, s);

@@ -302,6 +302,7 @@ q4k_status q4k_norm_residual(int64_t M, int64_t D, const float *y, int64_t ldy, 
     a.pre = pre, a.pre_w = pre_w, a.pre_b = pre_b, a.pre_eps = pre_eps;
     a.x = x, a.ldx = ldx;
     a.invariant = batch_invariant();
+    a.wait_ns = wait_limit_ns();
     a.status = di.status;
     return finish(launch_norm_residual(di, a, static_cast<cudaStream_t>(stream)));
 }

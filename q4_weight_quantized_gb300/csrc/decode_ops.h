@@ -95,6 +95,7 @@ struct NormArgs {
     uint16_t *x;
     int64_t ldx;
     int invariant;  // a row's bits must not depend on M
+    unsigned long long wait_ns;  // limit of the ring's waits
     unsigned int *status;
 };
 cudaError_t launch_norm_residual(const DeviceInfo &di, const NormArgs &a, cudaStream_t s);

@@ -276,10 +276,7 @@ __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int st
     int turn = 0, stage = 0;
     uint32_t parity = 0;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
-        if (!mbar_wait(smem_u32(&bars[stage]), parity, a.status)) {
-            mbar_wait(smem_u32(&bars[stage]), parity, a.status);  // the copies may still land
-            return;  // (every thread waits for the same phase and gives up alike)
-        }
+        const bool landed = mbar_wait_limit(smem_u32(&bars[stage]), parity, a.status, a.wait_ns);
         const uint8_t *at = ring + stage * stage_bytes;
         float v[4 * NV], h[4 * NV];
 #pragma unroll
@@ -320,7 +317,15 @@ __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int st
                 }
             }
         }
-        __syncthreads();  // the stage has been read
+        // the stage has been read; or some thread gave up on it, and all leave (one may give up on what another has seen land)
+        if (__syncthreads_or(!landed)) {
+            // thread 0 has issued the copies of this row and of the next stages - 1
+            for (int i = 0; tid == 0 && i < stages && row + (int64_t)i * gridDim.x < a.M; ++i) {
+                const int of = stage + i < stages ? stage + i : stage + i - stages;
+                mbar_wait(smem_u32(&bars[of]), of < stage ? parity ^ 1 : parity, a.status);
+            }
+            return;
+        }
         if (tid == 0 && row + (int64_t)stages * gridDim.x < a.M) copy(row + (int64_t)stages * gridDim.x, stage);
         if (++stage == stages) stage = 0, parity ^= 1;
         if (a.r_out) s.store(static_cast<Res *>(a.r_out) + row * a.ldr, h);

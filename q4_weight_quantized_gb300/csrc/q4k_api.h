@@ -13,6 +13,9 @@ q4k_status check_device(DeviceInfo *di);
 // The setting of q4k_set_batch_invariant.
 bool batch_invariant();
 
+// The limit of the waits that q4k_set_gemv_wait_limit_ns can shorten.
+unsigned long long wait_limit_ns();
+
 // Records e for q4k_last_cuda_error and returns Q4K_ERR_CUDA.
 q4k_status cuda_fail(cudaError_t e);
 
