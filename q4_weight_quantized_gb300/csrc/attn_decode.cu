@@ -150,10 +150,16 @@ __device__ __forceinline__ void seq_range(const AttnArgs &a, int b, int &begin, 
     begin = 0;
     if (a.window > 0) begin = (int)max((int64_t)0, (int64_t)len - a.n_q + 1 - a.window);
 }
+// Tiles of n slots.  (A sequence has up to 2^31 - 1 slots, and its last tile and chunk may end beyond 2^31: slots that
+// are not known to be there are unsigned.)
+template <int CT>
+__device__ __forceinline__ int tiles_of(int n) {
+    return (int)(((uint32_t)n + CT - 1) / CT);
+}
 // Places of one unit of n slots.
 template <int CT>
 __device__ __forceinline__ int places(int n) {
-    return n > 0 ? (n + CT - 1) / CT + kExtra : 0;
+    return n > 0 ? tiles_of<CT>(n) + kExtra : 0;
 }
 
 // A position in a share: tile `tile` of `tiles` of unit (sequence b, KV head, row tile rt).
@@ -166,7 +172,7 @@ struct Pos {
     __device__ __forceinline__ void enter(const AttnArgs &a) {
         for (; left > 0 && b < a.c.batch; ++b) {
             seq_range(a, b, begin, end);
-            tiles = (end - begin + CT - 1) / CT;
+            tiles = end > begin ? tiles_of<CT>(end - begin) : 0;
             if (tiles > 0) return;
         }
         left = 0;
@@ -331,10 +337,10 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
     auto fetch_page = [&] {
         Fetched f = {-1, 0, 0, false, nxt.left > 0};
         if (f.step) {
-            const int slot = nxt.begin + (nxt.tile * kWarps + warp) * TOK + (lane & (TOK - 1));
+            const uint32_t slot = nxt.begin + (uint32_t)(nxt.tile * kWarps + warp) * TOK + (lane & (TOK - 1));
             const uint32_t pg = page_of(a.c, slot);
-            f.in = slot < nxt.end;
-            f.in_page = (uint32_t)slot - pg * a.c.page_size;
+            f.in = slot < (uint32_t)nxt.end;
+            f.in_page = slot - pg * a.c.page_size;
             f.head = nxt.head;
             if (f.in) f.page = __ldg(a.c.table + nxt.b * a.c.ld_table + pg);
             nxt.advance<C::CT>(a);
@@ -473,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
         copy_step(stage == 0 ? C::STAGES - 1 : stage - 1, next);
         next = fetch_page();
         const uint32_t k_at = ring + stage * C::STAGE, v_at = k_at + TOK * C::PITCH;
-        const int j0 = cur.begin + (cur.tile * kWarps + warp) * TOK;  // first slot of the step
+        const uint32_t j0 = cur.begin + (uint32_t)(cur.tile * kWarps + warp) * TOK;  // first slot of the step
         if (mask) {
             // ---- S^T = K Q^T: slots 16 t + g, + 8 by rows 8 n + 2 c4, + 1
             float s[MT][NR][4];
@@ -553,7 +559,8 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
                         for (int t = 0; t < MT; ++t)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const int at = t * 16 + h * 8 + g, j = j0 + at;
+                                const int at = t * 16 + h * 8 + g;
+                                const uint32_t j = j0 + at;
                                 if (!(mask >> at & 1) || j < begin || j >= end) s[t][n][h * 2 + e] = kNone;
                             }
                     }
@@ -628,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
             // is added row by row and then taken out of the product
             if (!inside && a.n_q > 1) {
                 for (int at = 0; at < TOK; ++at) {
-                    const int j = j0 + at;
+                    const uint32_t j = j0 + at;
                     if (!(mask >> at & 1) || (j >= in_lo && j < in_hi)) continue;
                     const uint32_t v_row = v_at + at * C::PITCH;
                     bool odd = false;
@@ -952,12 +959,12 @@ __device__ __forceinline__ float2 join_ml(const AttnArgs &a, const Parts &p, int
 // Weights w of slots lo .. hi - 1 from the rows' scores z.  GROUPS: a chunk is fewer slots than the block takes at a
 // time, and its rows are dealt to groups of threads, whose sums are added in red.
 template <bool GROUPS, int kAt>
-__device__ __forceinline__ void add_up(const AttnArgs &a, float *w, const float *z, int begin, int lo, int hi, int chunk, const float *sm_m,
+__device__ __forceinline__ void add_up(const AttnArgs &a, float *w, const float *z, uint32_t begin, uint32_t lo, uint32_t hi, int chunk, const float *sm_m,
                                        const float *sm_r, float *red) {
     constexpr int kRowsAhead = 4;  // rows whose scores are on their way at once
     const int groups = GROUPS ? kAt * blockDim.x / chunk : 1, per = blockDim.x / groups;
     const int group = GROUPS ? threadIdx.x / per : 0, t = threadIdx.x - group * per;
-    for (int j0 = lo + t; GROUPS || j0 < hi; j0 += kAt * per) {
+    for (uint32_t j0 = lo + t; GROUPS || j0 < hi; j0 += kAt * per) {
         float sum[kAt], old[kAt];
 #pragma unroll
         for (int x = 0; x < kAt; ++x) {
@@ -970,7 +977,7 @@ __device__ __forceinline__ void add_up(const AttnArgs &a, float *w, const float 
             for (int y = 0; y < kRowsAhead; ++y)
 #pragma unroll
                 for (int x = 0; x < kAt; ++x) {
-                    const int j = j0 + x * per;
+                    const uint32_t j = j0 + x * per;
                     s[y][x] = r0 + y < a.rows && j >= begin && j < hi ? __ldg(z + (r0 + y) * a.ld_logits + j) : kNone;
                 }
 #pragma unroll
@@ -1006,8 +1013,9 @@ __device__ __forceinline__ void weigh(const AttnArgs &a, uint32_t id, int chunks
     int begin, len;
     seq_range(a, b, begin, len);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
-    const int lo = (int)(id - bh * (uint32_t)chunks) * chunk, hi = min(lo + chunk, len);
+    const int lo = (int)(id - bh * (uint32_t)chunks) * chunk;
     if (lo >= len) return;
+    const int hi = lo + min(chunk, len - lo);
     if (hi > begin) {
         // the octets' (m, l): `at_once` octets at a time, a team of warps each
         const int octets = a.row_tiles * a.tile_rows / 8, at_once = min(octets, warps), team = warps / at_once;
@@ -1153,7 +1161,7 @@ cudaError_t launch(AttnArgs &a, const DeviceInfo &di, cudaStream_t s) {
     if (a.weights) {
         const int least = a.rows > 32 ? 128 : a.rows > 16 ? 256 : 512;
         while (chunk > least && heads * ((slots + chunk - 1) / chunk) < 4 * di.sm_count) chunk /= 2;  // (of slots in the window)
-        chunks = (a.cap + chunk - 1) / chunk;
+        chunks = (int)(((int64_t)a.cap + chunk - 1) / chunk);
     }
     return launch_pdl(a.weights ? join_kernel<true> : join_kernel<false>, dim3((unsigned)(units * blocks + heads * chunks)), dim3(join_threads), 0, s, dim3(1), a, (int)blocks,
                       (uint32_t)(units * blocks), chunks > 0 ? chunks : 1, chunk);
