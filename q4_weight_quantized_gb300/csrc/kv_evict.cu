@@ -95,14 +95,15 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
     float *w_out = a.weights_out + (int64_t)bh * a.ld_meta;
     int32_t *p_out = a.positions_out + (int64_t)bh * a.ld_meta;
     const int raw = a.seq_lens[b];
-    const int n = max(0, min(raw, a.cap)), keep = min(n, a.budget);
+    // (unsigned: of up to 2^31 - 1 slots, the last steps of a pass end beyond 2^31)
+    const uint32_t n = max(0, min(raw, a.cap)), keep = min(n, (uint32_t)a.budget);
     if (tid == 0 && raw > a.cap) atomicOr(a.c.status, kDevIndex);
-    if (n <= a.budget) {
+    if (n == keep) {
         if (tid == 0) a.count[bh] = 0;
         if (w_out != w)
-            for (int j = tid; j < n; j += THREADS) w_out[j] = w[j];
+            for (uint32_t j = tid; j < n; j += THREADS) w_out[j] = w[j];
         if (p_out != p)
-            for (int j = tid; j < n; j += THREADS) p_out[j] = p[j];
+            for (uint32_t j = tid; j < n; j += THREADS) p_out[j] = p[j];
         return;
     }
     // ---- newest position (as offset binary, so that the unsigned maximum serves), and the keys; what
@@ -116,13 +117,13 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
 #pragma unroll
         for (int x = 0; x < PER; ++x) {
             if (x * THREADS >= n) break;
-            const int j = min(x * THREADS + tid, n - 1);
+            const uint32_t j = min((uint32_t)(x * THREADS + tid), n - 1);
             pos[x] = p[j], wj[x] = w[j];
         }
 #pragma unroll
         for (int x = 0; x < PER; ++x) {
             if (x * THREADS >= n) break;
-            const int j = x * THREADS + tid;
+            const uint32_t j = x * THREADS + tid;
             top = max(top, (uint32_t)pos[x] ^ 0x80000000u);
             mine[x] = key_of(wj[x]);
             keys[j] = mine[x];  // (past n: never looked at)
@@ -131,17 +132,17 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
         }
     } else {
         constexpr int kAhead = 8;  // loads before the first store
-        for (int j0 = tid; j0 < n; j0 += kAhead * THREADS) {
+        for (uint32_t j0 = tid; j0 < n; j0 += kAhead * THREADS) {
             int32_t pj[kAhead];
             float wj[kAhead];
 #pragma unroll
             for (int x = 0; x < kAhead; ++x) {
-                const int j = min(j0 + x * THREADS, n - 1);
+                const uint32_t j = min(j0 + x * THREADS, n - 1);
                 pj[x] = p[j], wj[x] = w[j];
             }
 #pragma unroll
             for (int x = 0; x < kAhead; ++x) {
-                const int j = j0 + x * THREADS;
+                const uint32_t j = j0 + x * THREADS;
                 top = max(top, (uint32_t)pj[x] ^ 0x80000000u);
                 if (CACHED && j < n) keys[j] = key_of(wj[x]);
                 if (copy_w && j < keep) w_out[j] = wj[x];
@@ -154,8 +155,8 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
     __syncthreads();
     const int64_t newest = (int32_t)(__reduce_max_sync(kFull, lane < B::WARPS ? red[0][lane] : 0u) ^ 0x80000000u);
     auto is_protected = [&](int32_t pos) { return pos < a.sinks || (int64_t)pos > newest - a.recent; };
-    auto key_at = [&](int j) { return CACHED ? keys[j] : key_of(w[j]); };
-    auto prot_at = [&](int j) { return CACHED ? (bits[j >> 5] >> (j & 31) & 1) != 0 : is_protected(p[j]); };
+    auto key_at = [&](uint32_t j) { return CACHED ? keys[j] : key_of(w[j]); };
+    auto prot_at = [&](uint32_t j) { return CACHED ? (bits[j >> 5] >> (j & 31) & 1) != 0 : is_protected(p[j]); };
     // ---- protected slots; number and range of the keys of either class
     uint32_t free_slots = 0, low[2] = {kFull, kFull}, high[2] = {0, 0}, prots = 0;  // prots: of this thread's slots
     auto of_either = [&](uint32_t k, bool prot) {
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
 #pragma unroll
         for (int x = 0; x < PER; ++x) {
             if (x * THREADS >= n) break;
-            const int j = x * THREADS + tid;
+            const uint32_t j = x * THREADS + tid;
             const bool prot = is_protected(pos[x]);
             const uint32_t m = __ballot_sync(kFull, prot);
             if (lane == 0) bits[j >> 5] = m;
@@ -176,13 +177,13 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
         }
     } else {
         constexpr int kAhead = 8;  // loads before the first is looked at
-        for (int j0 = 0; j0 < n; j0 += kAhead * THREADS) {
+        for (uint32_t j0 = 0; j0 < n; j0 += kAhead * THREADS) {
             int32_t pj[kAhead];
 #pragma unroll
             for (int x = 0; x < kAhead; ++x) pj[x] = p[min(j0 + x * THREADS + tid, n - 1)];
 #pragma unroll
             for (int x = 0; x < kAhead; ++x) {
-                const int j = j0 + x * THREADS + tid;
+                const uint32_t j = j0 + x * THREADS + tid;
                 const bool prot = j < n && is_protected(pj[x]);
                 if (CACHED) {
                     const uint32_t m = __ballot_sync(kFull, prot);
@@ -198,11 +199,11 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
 #pragma unroll
             for (int x = 0; x < PER; ++x) {
                 if (x * THREADS >= n) break;
-                const int j = x * THREADS + tid;
+                const uint32_t j = x * THREADS + tid;
                 if (j < n && mine[x] >= lo && mine[x] <= hi && ((prots >> x & 1) != 0) == of) visit(j, mine[x]);
             }
         } else if constexpr (CACHED) {
-            for (int j = 4 * tid; j < n; j += 4 * THREADS) {
+            for (uint32_t j = 4 * tid; j < n; j += 4 * THREADS) {
                 const uint4 t = *reinterpret_cast<const uint4 *>(keys + j);  // (past n: whatever is there)
                 const uint32_t k[4] = {t.x, t.y, t.z, t.w}, prot = bits[j >> 5] >> (j & 31);
 #pragma unroll
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
             }
         } else {
 #pragma unroll 4
-            for (int j = tid; j < n; j += THREADS) {
+            for (uint32_t j = tid; j < n; j += THREADS) {
                 const uint32_t k = key_at(j);
                 if (k >= lo && k <= hi && prot_at(j) == of) visit(j, k);
             }
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
         }
         if (in <= kFew && !gathered) {
             gathered = true;
-            each(in_prot, lo, hi, [&](int j, uint32_t k) {
+            each(in_prot, lo, hi, [&](uint32_t j, uint32_t k) {
                 const uint32_t at = atomicAdd(&listed, 1u);
                 if (at < kFew) list[at] = make_uint2(k, j);
             });
@@ -272,8 +273,9 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
             // many equal keys: the need-th of them by slot
             cut = lo;
             uint32_t run = 0;
-            for (int j0 = 0, turn = 0; j0 < n && run < need; j0 += 4 * THREADS, turn ^= 1) {
-                const int j = j0 + 4 * tid;
+            int turn = 0;
+            for (uint32_t j0 = 0; j0 < n && run < need; j0 += 4 * THREADS, turn ^= 1) {
+                const uint32_t j = j0 + 4 * tid;
                 uint32_t is = 0, total;
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
         const int shift = max(0, 32 - __clz(hi - lo) - LOG_BINS);
         for (int i = tid; i < BINS; i += THREADS) hist[i] = 0;
         __syncthreads();
-        each(in_prot, lo, hi, [&](int, uint32_t k) { atomicAdd(&hist[(k - lo) >> shift], 1u); });
+        each(in_prot, lo, hi, [&](uint32_t, uint32_t k) { atomicAdd(&hist[(k - lo) >> shift], 1u); });
         __syncthreads();
         // bins 2 tid, 2 tid + 1: the one in which the need-th smallest key lies
         const uint32_t c0 = hist[2 * tid], c1 = hist[2 * tid + 1];
@@ -312,19 +314,20 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
     // The list, at most half as many pairs as slots, then takes the keys' place, from where it goes out in whole sectors
     int2 *list_out = a.moves + (int64_t)bh * a.max_moves;
     uint32_t holes = 0, fills = 0;
-    const int per = CACHED ? ((n + THREADS - 1) / THREADS + 3) / 8 * 8 + 4 : 4;
+    const uint32_t per = CACHED ? ((n + THREADS - 1) / THREADS + 3) / 8 * 8 + 4 : 4;
     constexpr int MOST = CACHED ? (KEYS / THREADS + 3) / 8 * 8 + 4 : 4;
     using Mark = typename std::conditional<(MOST > 32), unsigned long long, uint32_t>::type;
     static_assert(MOST <= 64 && MOST * THREADS < 65536, "marks of a thread in a word, counts of a block in 16 bits");
     int2 *const moves = CACHED ? reinterpret_cast<int2 *>(keys) : list_out;
     __syncthreads();
-    for (int base = 0, turn = 0; base < n; base += per * THREADS, turn ^= 1) {
-        const int j0 = base + per * tid;
+    int turn = 0;
+    for (uint32_t base = 0; base < n; base += per * THREADS, turn ^= 1) {
+        const uint32_t j0 = base + per * tid;
         uint32_t count = 0;  // holes, fillers << 16
         Mark mark = 0;       // slots of either kind
 #pragma unroll
         for (int q = 0; q < MOST / 4; ++q) {
-            const int j = j0 + 4 * q;
+            const uint32_t j = j0 + 4 * q;
             if (4 * q >= per || j >= n) break;
             uint32_t k[4] = {0, 0, 0, 0}, prot = 0;
             if constexpr (CACHED) {
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const bool of_class = ((prot >> x & 1) != 0) == in_prot;
-                const bool gone = of_class ? k[x] < cut || (k[x] == cut && (uint32_t)(j + x) <= cut_slot) : in_prot;
+                const bool gone = of_class ? k[x] < cut || (k[x] == cut && j + x <= cut_slot) : in_prot;
                 const bool below = j + x < keep;
                 if (j + x < n && gone == below) mark |= (Mark)1 << (4 * q + x), count += below ? 1u : 1u << 16;
             }
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const EvictArgs a) {
         const uint32_t before = B::scan(count, scratch[turn], total);
         uint32_t hole = holes + (before & 0xFFFF), fill = fills + (before >> 16);
         for (; mark != 0; mark &= mark - 1) {
-            const int slot = j0 + (MOST > 32 ? __ffsll((long long)mark) : __ffs((int)mark)) - 1;
+            const uint32_t slot = j0 + (MOST > 32 ? __ffsll((long long)mark) : __ffs((int)mark)) - 1;
             if (slot < keep) moves[hole++].x = slot;
             else moves[fill++].y = slot;
         }

@@ -71,3 +71,43 @@ def test_attn_over_the_longest_cache():
     v.view(torch.uint8)[1, 0, -1] = 0x7F             # NaN
     again = call()
     assert np.array_equal(again[0], got[0]) and np.isnan(again[1]).all()
+
+
+@pytest.mark.parametrize("equal", [False, True])
+def test_evict_from_the_longest_cache(equal):
+    """Three slots of no weight leave, the last one among them; and of equal weights, all but the last 4096 slots."""
+    g = gen_of(2)
+    D = 64
+    k, v = (torch.randn(2, 1, PAGE, D, generator=g, device="cuda").to(F8) for _ in range(2))
+    table = torch.zeros(1, PAGES, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    w = torch.ones(N + GUARD, device="cuda")
+    p = torch.full((N + GUARD,), -1, dtype=torch.int32, device="cuda")
+    p[:N] = torch.arange(N, dtype=torch.int32, device="cuda")
+    lens, new = torch.tensor([N], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    gone = [5, 123456789, N - 1]
+    budget = 4096 if equal else N - 3
+    if not equal:
+        w[torch.tensor(gone, device="cuda")] = 0.0
+    cache = q4k.kv_cache(k, v, table)
+    size = q4k.q4k_kv_evict_workspace_size(cache, N)
+    assert size >= 8 * (N // 2)
+    ws = torch.full((size + GUARD,), 0x5A, dtype=torch.uint8, device="cuda")
+    rows = k.view(torch.uint8).clone()
+    q4k.q4k_kv_evict(cache, lens, new, budget, 0, 0, w, p, w, p, N, ws, size)
+    q4k.q4k_check_device()
+    assert new.tolist() == [budget] and (ws[size:] == 0x5A).all()
+    del ws
+    want = torch.full((N + GUARD,), -1, dtype=torch.int32, device="cuda")
+    want[:N] = torch.arange(N, dtype=torch.int32, device="cuda")
+    weights = torch.ones(N + GUARD, device="cuda")
+    now = k.view(torch.uint8)
+    if equal:
+        want[:4096] = torch.arange(N - 4096, N, dtype=torch.int32, device="cuda")
+        assert torch.equal(now[0, 0, :4096], rows[1, 0, PAGE - 4096:])
+    else:
+        weights[torch.tensor(gone, device="cuda")] = 0.0
+        for at, j in zip(gone[:2], (N - 3, N - 2)):
+            want[at], weights[at] = j, 1.0
+            assert torch.equal(now[0, 0, at % PAGE], rows[1, 0, j % PAGE])
+    assert torch.equal(p, want) and torch.equal(w, weights)
