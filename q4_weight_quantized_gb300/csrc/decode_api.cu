@@ -98,10 +98,12 @@ q4k_status call(q4k_status (*f)(Args...), const void *slots) {
 
 q4k_status finish(cudaError_t e) { return e == cudaSuccess ? Q4K_OK : cuda_fail(e); }
 
-bool attn_shape_ok(const q4k_kv_cache *c, int32_t n_heads, int32_t n_q) {
+bool attn_shape_ok(const q4k_kv_cache *c, int32_t n_heads, int32_t n_q, int64_t ld_weights) {
     if (!cache_shape_ok(c) || n_heads < 1 || n_heads % c->n_kv_heads || n_q < 1 || n_q > 64) return false;
     const int64_t rows = (int64_t)n_q * (n_heads / c->n_kv_heads);
     if (rows > kMaxAttnRows) return false;
+    // the scores' bytes in the workspace
+    if ((double)c->batch * c->n_kv_heads * (double)rows * (double)ld_weights * 4 > 4e18) return false;
     const int tile = attn_tile_rows(c->head_dim, (int)rows);
     const int64_t units = (int64_t)c->batch * c->n_kv_heads * ((rows + tile - 1) / tile);
     // blocks of the joining kernel; tiles times shares in 64 bits
@@ -183,7 +185,7 @@ q4k_status q4k_kv_append(const q4k_kv_cache *cache, int64_t T, int32_t n_heads, 
 }
 
 size_t q4k_attn_decode_workspace_size(const q4k_kv_cache *cache, int32_t n_heads, int32_t n_q, int64_t ld_weights) {
-    if (!cache || ld_weights < 0 || ld_weights >= kInt31 || !attn_shape_ok(cache, n_heads, n_q)) return 0;
+    if (!cache || ld_weights < 0 || ld_weights >= kInt31 || !attn_shape_ok(cache, n_heads, n_q, ld_weights)) return 0;
     return attn_layout(cache, n_heads, n_q, ld_weights).total;
 }
 
@@ -194,7 +196,7 @@ q4k_status q4k_attn_decode(const q4k_kv_cache *cache, const int32_t *seq_lens, c
     q4k_status st = cache_check(cache);
     if (st != Q4K_OK) return st;
     if (!seq_lens || !q || !o || !ws) return Q4K_ERR_NULL;
-    if (!attn_shape_ok(cache, n_heads, n_q) || ldq < (int64_t)n_heads * cache->head_dim ||
+    if (!attn_shape_ok(cache, n_heads, n_q, weights ? ld_weights : 0) || ldq < (int64_t)n_heads * cache->head_dim ||
         ldo < (int64_t)n_heads * cache->head_dim || window < 0 || !std::isfinite(scale) || !(softcap >= 0.f) ||
         !std::isfinite(softcap))
         return Q4K_ERR_SHAPE;
