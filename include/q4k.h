@@ -587,6 +587,18 @@ q4k_status q4k_sample(const float *logits, int64_t M, int64_t V, int64_t ldl, co
                       const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *token,
                       float *prob, void *stream);
 
+/* The five calls above for callers whose foreign-function interface converts every
+ * argument on its own (from Python that takes longer than the rest of a small call on
+ * the host): `slots` holds the arguments of the call of the same name, in its order, 8
+ * bytes each in the machine's byte order - integers and addresses as int64 (a smaller
+ * integer parameter takes the low bits), floats as double, rounded to fp32.  The same
+ * checks, results and errors; slots = NULL gives Q4K_ERR_NULL. */
+q4k_status q4k_kv_append_slots(const void *slots);
+q4k_status q4k_attn_decode_slots(const void *slots);
+q4k_status q4k_kv_evict_slots(const void *slots);
+q4k_status q4k_norm_residual_slots(const void *slots);
+q4k_status q4k_sample_slots(const void *slots);
+
 #ifdef __cplusplus
 }
 #endif

@@ -37,6 +37,7 @@ EXPORTS = (
     "q4k_nvfp4_dequant", "q4k_nvfp4_gemm",
     "q4k_kv_append", "q4k_attn_decode_workspace_size", "q4k_attn_decode", "q4k_kv_evict_workspace_size", "q4k_kv_evict",
     "q4k_norm_residual", "q4k_sample",
+    "q4k_kv_append_slots", "q4k_attn_decode_slots", "q4k_kv_evict_slots", "q4k_norm_residual_slots", "q4k_sample_slots",
 )
 
 # fixed scratch capacity of q4k_moe_grouped_gemm_noalloc (Q4K_MOE_NOALLOC_SCRATCH_BYTES)

@@ -93,6 +93,7 @@ q4k_status call_each(q4k_status (*f)(Args...), const char *slots, std::index_seq
 }
 template <typename... Args>
 q4k_status call(q4k_status (*f)(Args...), const void *slots) {
+    if (!slots) return Q4K_ERR_NULL;
     return call_each(f, static_cast<const char *>(slots), std::index_sequence_for<Args...>{});
 }
 
@@ -329,9 +330,7 @@ q4k_status q4k_sample(const float *logits, int64_t M, int64_t V, int64_t ldl, co
     return finish(launch_sample(di, a, static_cast<cudaStream_t>(stream)));
 }
 
-// What the Python package calls: the same functions with their arguments one after the other in 8 bytes each (integers,
-// addresses, floats as doubles).  A foreign call from Python converts each argument on its own, which for twenty of
-// them takes longer than the rest of a small call on the host.
+// What the Python package calls.
 q4k_status q4k_kv_append_slots(const void *slots) { return call(q4k_kv_append, slots); }
 q4k_status q4k_attn_decode_slots(const void *slots) { return call(q4k_attn_decode, slots); }
 q4k_status q4k_kv_evict_slots(const void *slots) { return call(q4k_kv_evict, slots); }
