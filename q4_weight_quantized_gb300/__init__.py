@@ -59,15 +59,20 @@ def kv_cache(k, v, page_table, k_scale: float = 1.0, v_scale: float = 1.0) -> Kv
     strides with unit stride last, the same for both), page_table int32 [batch][max_pages].  It holds addresses only:
     the caller keeps the tensors."""
     import torch
-    if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4 or k.stride(3) != 1:
+    # (where a dimension has one element, its stride says nothing and may be anything)
+    def strides(t):
+        return [t.shape[3] if n == 1 else s for n, s in zip(t.shape, t.stride())]
+    if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4 or strides(k) != strides(v) or k.stride(3) != 1:
         raise ValueError("k and v must be 4-D with the same shape, strides and type, and unit stride last")
     types = {torch.bfloat16: Q4K_KV_BF16, torch.float8_e4m3fn: Q4K_KV_E4M3}
-    if k.dtype not in types or page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+    if k.dtype not in types or page_table.dtype != torch.int32 or page_table.dim() != 2 or (
+            page_table.shape[1] > 1 and page_table.stride(1) != 1):
         raise ValueError("k and v are bfloat16 or float8_e4m3fn, page_table int32 [batch][max_pages]")
     if page_table.shape[0] > 1 and page_table.stride(0) < page_table.shape[1]:
         raise ValueError("page_table's rows must not overlap")
+    page, head, slot, _ = strides(k)
     return KvCache(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), max(page_table.stride(0), page_table.shape[1]),
-                   k.shape[0], k.stride(0), k.stride(1), k.stride(2), page_table.shape[0], page_table.shape[1],
+                   k.shape[0], page, head, slot, page_table.shape[0], page_table.shape[1],
                    k.shape[2], k.shape[1], k.shape[3], types[k.dtype], k_scale, v_scale)
 
 
