@@ -45,14 +45,6 @@ __device__ __forceinline__ uint32_t key_of(float w) {
 template <int THREADS>
 struct Block {
     static constexpr int WARPS = THREADS / 32;
-    static __device__ __forceinline__ uint32_t sum(uint32_t v, uint32_t *scratch) {
-        v = __reduce_add_sync(kFull, v);
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-        __syncthreads();
-        const int lane = threadIdx.x & 31;
-        return __reduce_add_sync(kFull, lane < WARPS ? scratch[lane] : 0u);
-    }
     // Sum of a value over the threads before this one; total: over all.  Two scratch arrays in turn, so
     // that one barrier a scan is enough.
     static __device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t *scratch, uint32_t &total) {
