@@ -452,10 +452,10 @@ typedef struct {
     int32_t batch;             /* sequences, 1 .. 65535 */
     int32_t max_pages;         /* table entries per sequence; max_pages*page_size < 2^31 */
     int32_t page_size;         /* slots per page, >= 1 */
-    int32_t n_kv_heads;        /* 1 .. 1024 */
+    int32_t n_kv_heads;        /* 1 .. 1024; batch*n_kv_heads <= 2^24 */
     int32_t head_dim;          /* D: 64, 128 or 256 */
     int32_t dtype;             /* Q4K_KV_BF16 or Q4K_KV_E4M3 */
-    float k_scale, v_scale;    /* > 0; 1 for a plain cache */
+    float k_scale, v_scale;    /* > 0 and finite; 1 for a plain cache */
 } q4k_kv_cache;
 
 #define Q4K_ROPE_HALF 0  /* value i pairs with value i + rope_dim/2 */
@@ -477,6 +477,7 @@ typedef struct {
  *   q_out bf16 [T][ldqo].  q and q_out may both be NULL (keys and values only).
  *   weights, positions (each may be NULL): slot[t]'s entry of every head becomes
  *     0 and pos[t]; with either, slot[t] must be < ld_meta.
+ * T < 2^31; n_heads 1 .. 65536.
  * A token with an index out of range is recorded (Q4K_ERR_INDEX) and leaves the
  * cache, weights and positions alone; its q_out row becomes 0. */
 q4k_status q4k_kv_append(const q4k_kv_cache *cache, int64_t T, int32_t n_heads, const float *q, int64_t ldq,
@@ -495,19 +496,21 @@ q4k_status q4k_kv_append(const q4k_kv_cache *cache, int64_t T, int32_t n_heads, 
  * row's range has no part in it, whatever its key and value hold.
  *   q, o: bf16 [batch*n_q][ldq], [batch*n_q][ldo], row b*n_q + i, heads of D
  *     consecutive; 16-byte aligned, ldq and ldo multiples of 8.
- *   n_heads: a multiple of n_kv_heads; n_q 1 .. 64.
+ *   n_heads: a multiple of n_kv_heads; n_q 1 .. 64; rows of a KV head, n_q * n_heads /
+ *     n_kv_heads, 1 .. 1024.  (With many sequences, batch * n_kv_heads * D * these rows,
+ *     rounded up to whole tiles of 8, 16 or 32, must be below 2^38.)
  *   weights (may be NULL): fp32 [batch][n_kv_heads][ld_weights], updated for every
  *     slot j < len:  weights[b][h][j] = decay*weights[b][h][j] + sum of
  *     softmax(s[r])[j] over the rows r of head h.  len must be <= ld_weights.
  *     (A slot left out for its page: decay*weights alone.)
  * Products are exact and sums, maxima and the joined softmax fp32.  (For an e4m3 cache
  * a value of q below 2^-31 of the largest of its row is taken to 2^-39 of that one.)
- * The weights p
- * enter the product with v as the sum of two bf16 values (to 2^-16), for an e4m3 cache
- * as one f16 value (to 2^-12, and to 2^-32 of the largest), and o is rounded once.  The length is split over the whole GPU by the lengths of the batch,
- * and the parts are joined in slot order: the same call repeats its bits, but a
- * sequence's last bits may depend on the other lengths of its batch, also in
- * batch-invariant mode.
+ * The weights p enter the product with v as the sum of two bf16 values (to 2^-16), for
+ * an e4m3 cache as one f16 value (to 2^-11, and to 2^-32 of the largest), while the sum
+ * that divides them is that of the fp32 values; o is rounded once.  The length is split
+ * over the whole GPU by the lengths of the batch, and the parts are joined in slot
+ * order: the same call repeats its bits, but a sequence's last bits may depend on the
+ * other lengths of its batch, also in batch-invariant mode.
  * Workspace: q4k_attn_decode_workspace_size(cache, n_heads, n_q, ld_weights, or 0
  * without weights) bytes, 256-byte aligned; 0 is returned for arguments that the call
  * would refuse. */
@@ -555,7 +558,7 @@ q4k_status q4k_kv_evict(const q4k_kv_cache *cache, const int32_t *seq_lens, int3
  * NULL (1).  r_in and r_out [M][ldr] of type r_dtype; r_out may be r_in, or NULL (not
  * kept).  x bf16 [M][ldx], may be NULL if r_out is not (pre is then not computed).
  * Everything is fp32 until r_out and x are rounded once each; x comes from h before
- * r_out's rounding.  1 <= D <= 2^20; pointers aligned to their element.  A row's last
+ * r_out's rounding.  1 <= M < 2^31; 1 <= D <= 2^20; pointers aligned to their element.  A row's last
  * bits depend on D, on how pointers and strides are aligned, and on whether M is below
  * the number of SMs, but with q4k_set_batch_invariant(1) not on M. */
 q4k_status q4k_norm_residual(int64_t M, int64_t D, const float *y, int64_t ldy, int post, const float *post_w,
@@ -582,7 +585,7 @@ q4k_status q4k_norm_residual(int64_t M, int64_t D, const float *y, int64_t ldy, 
  *   temperature <= 0 or NaN: the first in rank, prob 1.  A row without any logit above
  *   -inf: token -1, prob 0.  top_p and min_p are clamped to [0, 1], u to [0, 1 -
  *   2^-24]; NaN counts as off (0 for u).
- * 1 <= V <= 2^22, ldl >= V; pointers aligned to their element. */
+ * 1 <= M <= 2^24, 1 <= V <= 2^22, ldl >= V; pointers aligned to their element. */
 q4k_status q4k_sample(const float *logits, int64_t M, int64_t V, int64_t ldl, const float *temperature,
                       const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *token,
                       float *prob, void *stream);

@@ -689,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnArg
                 }
             }
             // ---- O^T += V^T P^T.  bf16: p as the sum of two bf16 values (one alone would cost nearly as much
-            // as o's own rounding); e4m3: as one f16 value, 2^-12.
+            // as o's own rounding); e4m3: as one f16 value, to 2^-11 (over 200001 slots o is off by 1.7e-3 of its size, with
+            // 32 bits 1.6e-3: its own rounding)
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 uint32_t ph[NR][2], pl[NR][2];

@@ -14,8 +14,9 @@
 // latency (some fifteen block-wide steps, which fewer threads take faster); the reads are 8 bytes a slot.
 // move_kernel copies the rows, 16 bytes a lane, and their weights and positions: bound by HBM (two or
 // four rows a thread cost more in occupancy than their overlapping loads gave: 62 and 70 us against 59).
-// Measured: 9.4 us for 32 caches of 8 heads with one slot over 2048 (5 of them the selection), 81 us for
-// 16 caches of 9001 to 16384 slots to 8192 (15 the selection, 59 the copies: 333 MB at 5.7 TB/s).
+// Measured: 9.0 us for 32 caches of 8 heads with one slot over 2048 (5 of them the selection), 81 us for
+// 16 caches of 9001 to 16384 slots to 8192 (15 the selection, 59 the copies: 333 MB at 5.7 TB/s), 337 us for one of 8
+// heads of 200001 slots to half (beyond kCached, where every pass of a head's one CTA reads both arrays again).
 
 #include <cuda_runtime.h>
 
@@ -414,8 +415,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
 
 cudaError_t launch_kv_evict(const DeviceInfo &di, const EvictArgs &a, cudaStream_t s) {
     const int bh = a.c.batch * a.c.heads;
-    // more short caches than SMs: small CTAs, of which more share one (256 heads with one slot over 2048: 9.4 us, with 512
-    // threads 10.9; 64 heads of 4096 to 2048: 30.1 and 27.4)
+    // more short caches than SMs: small CTAs, of which more share one (the same cache again and
+    // again: 256 heads with one slot over 2048 8.0 us, with 512 threads 9.8; 64 heads of 4096 to 2048 23.6 and 20.7)
     cudaError_t e = a.cap <= kSmall && bh > di.sm_count ? launch_select<256, kSmall, true>(a, s)
                     : a.cap <= kMid    ? launch_select<512, kMid, true>(a, s)
                     : a.cap <= kHeld   ? launch_select<1024, kHeld, true>(a, s)
