@@ -506,7 +506,7 @@ q4k_status q4k_kv_append(const q4k_kv_cache *cache, int64_t T, int32_t n_heads, 
  * Products are exact and sums, maxima and the joined softmax fp32.  (For an e4m3 cache
  * a value of q below 2^-31 of the largest of its row is taken to 2^-39 of that one.)
  * The weights p enter the product with v as the sum of two bf16 values (to 2^-16), for
- * an e4m3 cache as one f16 value (to 2^-11, and to 2^-32 of the largest), while the sum
+ * an e4m3 cache of two f16 values (to 2^-22, and to 2^-32 of the largest), while the sum
  * that divides them is that of the fp32 values; o is rounded once.  The length is split
  * over the whole GPU by the lengths of the batch, and the parts are joined in slot
  * order: the same call repeats its bits, but a sequence's last bits may depend on the

@@ -65,3 +65,23 @@ def test_norm_rows_do_not_depend_on_the_batch(D, post, pre, gate, res, bias):
     finally:
         q4k.q4k_set_batch_invariant(was)
     q4k.q4k_check_device()
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("D,G,n", [(64, 4, 2), (64, 12, 6), (64, 32, 40), (128, 5, 4), (128, 9, 18), (128, 24, 2), (256, 8, 10), (256, 16, 64)])
+def test_attn_weights_keep_their_bits_in_the_second_product(dtype, D, G, n):
+    """Values of +1 and -1: what is left of a sum of weights that nearly cancel shows how far each is off.
+
+    Errors: a score by e (D additions of products that sum to big at most, the exponential), a weight then by e^(2 e), and by
+    2^-15 at most for its two 16-bit halves and the sums; o's own rounding is 2^-8 of what is left."""
+    g = gen_of(D + n)
+    B, Hkv, page = 24, 2, 16
+    per = -(-n // page)
+    k, v = pool((B * per, Hkv, page, D), dtype, "phsd", g)
+    v.copy_(torch.where(torch.rand(v.shape, generator=g, device="cuda") < 0.5, 1.0, -1.0))
+    table = table_of(B, per, B * per, g)
+    q = torch.randn(B, 1, Hkv * G, D, generator=g, device="cuda").to(BF)
+    o = run_attn(k, v, table, torch.full((B,), n, dtype=torch.int32, device="cuda"), q, 1, D ** -0.5)
+    want, _, mag, big = R.attn_decode(np64(k), np64(v), table.cpu().numpy(), [n] * B, np64(q), 1, D ** -0.5)
+    e = (D * 2.0 ** -24 + 2.0 ** -20) * big[..., None]
+    assert (np.abs(np64(o) - want) <= mag * (2.2 * e + 2.0 ** -15) + np.abs(want) * 2.0 ** -8 + 1e-30).all()
