@@ -104,6 +104,7 @@ struct SampleArgs {
     const float *logits;
     int64_t M, ldl;
     int32_t V, ctas;  // ctas of a row: chosen by the launcher
+    float one;        // 1: what no compiler knows (see the kernel)
     const float *temperature;
     const int32_t *top_k;
     const float *top_p, *min_p, *u;

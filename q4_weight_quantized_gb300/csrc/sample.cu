@@ -31,7 +31,7 @@
 // Bound for many rows by the arithmetic of the weights (half of it on two logits at once) and
 // the exchanges that two CTAs on an SM do not hide, for one row by the exchanges and the fetch
 // of instructions that are used once.  Measured: 9.6 us for a row of 128001 with top-k 50 and
-// top-p (13.1 without step 2), 126 us for 256 rows of 151936 with top-p and min-p (229).
+// top-p (13.1 without step 2), 133 us for 256 rows of 151936 with top-p and min-p.
 
 #include <cuda_runtime.h>
 
@@ -77,20 +77,26 @@ __device__ __forceinline__ float4 fetch(const float *z, int i, int head, int n) 
 // row then counts as one of zeros and -inf.  least: the largest logit, negated.
 __device__ __forceinline__ float flat(float v, float least) { return v == least ? 0.f : INFINITY; }
 
-// Two fp32 operations at once, each rounded on its own.
+// Two fp32 operations at once, each rounded on its own.  A packed product and a packed sum behind it would be compiled
+// into one fused operation, .rn or not, which rounds once: the sum of what may be a product is therefore itself written as
+// a fused operation, x * one + y, with a 1 that only the launch knows.  (256 rows of 151936 with top-p and min-p: 133 us;
+// 126 as it was compiled before, one weight in ten off by a unit; scalar operations, which the compiler leaves alone, take
+// 3 % longer than this.)
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     u64 r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<u64 *>(&a)), "l"(*reinterpret_cast<u64 *>(&b)));
     return *reinterpret_cast<float2 *>(&r);
 }
-__device__ __forceinline__ float2 sum2(float2 a, float2 b) {
+__device__ __forceinline__ float2 sum2(float2 a, float2 b) {  // (of no product)
     u64 r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<u64 *>(&a)), "l"(*reinterpret_cast<u64 *>(&b)));
     return *reinterpret_cast<float2 *>(&r);
 }
-__device__ __forceinline__ float2 sum2_down(float2 a, float2 b) {
+__device__ __forceinline__ float2 fma2_down(float2 a, float2 b, float2 c) {
     u64 r;
-    asm("add.rm.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<u64 *>(&a)), "l"(*reinterpret_cast<u64 *>(&b)));
+    asm("fma.rm.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<u64 *>(&a)), "l"(*reinterpret_cast<u64 *>(&b)), "l"(*reinterpret_cast<u64 *>(&c)));
     return *reinterpret_cast<float2 *>(&r);
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
@@ -98,25 +104,25 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // floor(2^24 2^-f) and n of two distances 0 <= d < 2^22, n = floor(d), f = d - n: the series
 // of 2^-f about f = 1/2, coefficients 2^-1/2 (-ln 2)^i / i!.  It lies in [1/2, 1] for every f, where the
 // bits of an fp32 number p are 2^24 p + 0x3E800000.
-__device__ __forceinline__ void mantissa2(float2 d, uint32_t (&w)[2], uint32_t (&n)[2]) {
+__device__ __forceinline__ void mantissa2(float2 d, float one, uint32_t (&w)[2], uint32_t (&n)[2]) {
     // 2^23 + d, rounded down, is 2^23 + n
-    const float2 t = sum2_down(d, both(8388608.f));
+    const float2 t = fma2_down(d, both(one), both(8388608.f));
     n[0] = __float_as_uint(t.x) & 0x7FFFFF, n[1] = __float_as_uint(t.y) & 0x7FFFFF;
     const float2 f = sum2(fma2(sum2(t, both(-8388608.f)), both(-1.f), d), both(-0.5f));  // (d - n is exact)
     float2 p = both(-1.0785311133076902e-05f);
-    p = sum2(mul2(p, f), both(0.00010891940473811701f));
-    p = sum2(mul2(p, f), both(-0.0009428249322809279f));
-    p = sum2(mul2(p, f), both(0.006801044102758169f));
-    p = sum2(mul2(p, f), both(-0.03924733027815819f));
-    p = sum2(mul2(p, f), both(0.16986578702926636f));
-    p = sum2(mul2(p, f), both(-0.4901290833950043f));
-    p = sum2(mul2(p, f), both(0.7071067690849304f));
+    p = fma2(mul2(p, f), both(one), both(0.00010891940473811701f));
+    p = fma2(mul2(p, f), both(one), both(-0.0009428249322809279f));
+    p = fma2(mul2(p, f), both(one), both(0.006801044102758169f));
+    p = fma2(mul2(p, f), both(one), both(-0.03924733027815819f));
+    p = fma2(mul2(p, f), both(one), both(0.16986578702926636f));
+    p = fma2(mul2(p, f), both(one), both(-0.4901290833950043f));
+    p = fma2(mul2(p, f), both(one), both(0.7071067690849304f));
     w[0] = __float_as_uint(p.x) - 0x3E800000u, w[1] = __float_as_uint(p.y) - 0x3E800000u;
 }
 __device__ __forceinline__ u64 scaled(uint32_t w, uint32_t n) { return ((u64)w << 16) >> n; }
-__device__ __forceinline__ u64 weight_of(float d) {  // d < kAll
+__device__ __forceinline__ u64 weight_of(float d, float one) {  // d < kAll
     uint32_t w[2], n[2];
-    mantissa2(both(d), w, n);
+    mantissa2(both(d), one, w, n);
     return scaled(w[0], n[0]);
 }
 // floor(total * share / 2^24)
@@ -191,6 +197,7 @@ struct Row {
     int head, n, n4;   // n4: groups
     uint32_t rank, ctas;
     float top, c;      // largest logit; log2(e) / temperature
+    float one;         // 1 (see mul2)
     float infinite;    // not CACHED: the row is to be flattened (see there) about this, unless NaN
     int per_octave;    // log2 of the bins of an octave
     float span;        // bins cover d < span
@@ -344,7 +351,7 @@ struct Row {
                 const float2 d = dist2(x[h], x[h + 1]);
                 if (!(d.x < limit || d.y < limit)) continue;
                 uint32_t w[2], oct[2];
-                mantissa2(make_float2(d.x < kAll ? d.x : 0.f, d.y < kAll ? d.y : 0.f), w, oct);
+                mantissa2(make_float2(d.x < kAll ? d.x : 0.f, d.y < kAll ? d.y : 0.f), one, w, oct);
                 const float dd[2] = {d.x, d.y};
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -481,7 +488,7 @@ struct Row {
         each(from, to, lo, hi, [&](uint32_t idx, uint32_t key, float d) {
             const uint32_t at = peer_add(&s.list_n[counter], 0, 1);
             if (at < kList) {
-                const u64 w = weight_of(d);
+                const u64 w = weight_of(d, one);
                 peer_store(&s.list[at], 0, make_uint4(key, idx, (uint32_t)w, (uint32_t)(w >> 32)));
             }
         });
@@ -505,7 +512,7 @@ struct Row {
                 u64 w[2] = {0, 0};
                 if (weigh) {
                     uint32_t wm[2], oct[2];
-                    mantissa2(make_float2(fminf(d.x, 60.f), fminf(d.y, 60.f)), wm, oct);  // (from kAll on, 0)
+                    mantissa2(make_float2(fminf(d.x, 60.f), fminf(d.y, 60.f)), one, wm, oct);  // (from kAll on, 0)
                     w[0] = scaled(wm[0], oct[0]), w[1] = scaled(wm[1], oct[1]);
                     sum += w[0] + w[1];
                 }
@@ -541,7 +548,7 @@ struct Row {
             for (int o = 1; o < team; o <<= 1) before += __shfl_xor_sync(kFull, before, o);
             if (i < m && mate == 0) {
                 const float x = __uint_as_float((uint32_t)(me >> 32));
-                const u64 w = weight_of(dist(x));
+                const u64 w = weight_of(dist(x), one);
                 peer_store(&s.list[at + before], 0, make_uint4(key_of(-x), (uint32_t)me, (uint32_t)w, (uint32_t)(w >> 32)));
             }
         }
@@ -655,7 +662,7 @@ struct Row {
             clear_bins();
             each(from, to, lo, hi, [&](uint32_t, uint32_t key, float d) {
                 uint32_t w[2], oct[2];
-                mantissa2(both(d), w, oct);
+                mantissa2(both(d), one, w, oct);
                 into_bin((int)((hi - key) >> shift), w[0], oct[0]);
             });
             join_bins([&](int) { return octave; });
@@ -665,7 +672,7 @@ struct Row {
         }
         // equal logits: the q-th by index
         const float z0 = of_key(hi);
-        const u64 w = weight_of(dist(-z0));
+        const u64 w = weight_of(dist(-z0), one);
         const u64 q = by_sum ? (need - sum + w - 1) / w : need - cnt;
         uint32_t idx;
         u64 val, total;
@@ -795,7 +802,7 @@ __device__ __forceinline__ void finish(R &r, const SampleArgs &a, int64_t m, con
                 const float2 d = r.dist2(z[h], z[h + 1]);
                 if (!((z[h] <= zc && d.x < limit) || (z[h + 1] <= zc && d.y < limit))) continue;
                 uint32_t wm[2], n[2];
-                mantissa2(make_float2(d.x < kAll ? d.x : 0.f, d.y < kAll ? d.y : 0.f), wm, n);
+                mantissa2(make_float2(d.x < kAll ? d.x : 0.f, d.y < kAll ? d.y : 0.f), r.one, wm, n);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const bool in = z[h + e] < zc || (z[h + e] == zc && i + h + e <= cut.idx);
@@ -828,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const float *row = a.logits + m * a.ldl + i0;
     const int head = (int)(reinterpret_cast<uintptr_t>(row) % 16 / 4), n = (int)(i1 - i0) + head;
     row -= head;
-    Row<CACHED> r = {s, CACHED ? own : row, (uint32_t)i0 - head, head, n, (n + 3) / 4, rank, ctas, 0.f, 0.f, NAN, 0, 0.f, 0, 0};
+    Row<CACHED> r = {s, CACHED ? own : row, (uint32_t)i0 - head, head, n, (n + 3) / 4, rank, ctas, 0.f, 0.f, a.one, NAN, 0, 0.f, 0, 0};
     // ---- the row's settings
     float t = a.temperature ? __ldg(a.temperature + m) : 1.f;
     const bool greedy = !(t > 0.f);
@@ -883,6 +890,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
 
 cudaError_t launch_sample(const DeviceInfo &di, const SampleArgs &args, cudaStream_t s) {
     SampleArgs a = args;
+    a.one = 1.f;
     // CTAs of a row: up to eight, a few thousand logits each at least; fewer where the rows fill the
     // device by themselves, as long as a row stays in shared memory
     a.ctas = a.V <= 4096 ? 1 : a.V <= 8192 ? 2 : a.V <= 16384 ? 4 : 8;
