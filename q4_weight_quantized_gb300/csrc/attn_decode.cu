@@ -29,7 +29,7 @@
 //   - The running maximum only moves when a score exceeds it by 2^8: until then no lane
 //     needs another's scores and o' is not rescaled.
 // Measured (with the join): 8.5 us for 40 heads over 8 KV heads of 128 and 1000 slots, 35 us for 16 sequences of
-// 33 to 6001 slots with 4 new tokens, 78 us for 200001 e4m3 slots (5.3 TB/s), 260 us for 64 sequences of 2000 to 8192
+// 33 to 6001 slots with 4 new tokens, 79 us for 200001 e4m3 slots (5.2 TB/s), 260 us for 64 sequences of 2000 to 8192
 // slots with weights (225 us in attn_kernel: 6.2 TB/s with the scores it writes).
 
 #include <cuda_fp16.h>
