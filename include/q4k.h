@@ -137,9 +137,9 @@ int q4k_set_static_weights(int enable);
  *       GB300.
  * The boundary between the two paths stays: rows of calls with M <= 16 and
  * M > 16 differ in rounding (different kernels, each within its bar).
- * Of the operators between a decode step's products, q4k_norm_residual follows the
- * mode (about 0.15 us for a few rows), q4k_kv_append, q4k_kv_evict and q4k_sample give
- * a token or sequence the same bits in either, and q4k_attn_decode is not
+ * Of the operators between a decode step's products, q4k_norm_residual and
+ * q4k_norm_residual_x8 follow the mode (about 0.15 us for a few rows), q4k_kv_append,
+ * q4k_kv_evict and q4k_sample give a token or sequence the same bits in either, and q4k_attn_decode is not
  * batch-invariant in either: it splits its work by all lengths of the batch.
  * Process-wide; applies to calls enqueued after it returns.  Returns the previous
  * setting (0 or 1). */
@@ -590,7 +590,85 @@ q4k_status q4k_sample(const float *logits, int64_t M, int64_t V, int64_t ldl, co
                       const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *token,
                       float *prob, void *stream);
 
-/* The five calls above for callers whose foreign-function interface converts every
+/* ---------------------------------------------------------------------------
+ * The operators of a step that runs chunks of prompts and decode tokens of many
+ * requests together: pages and slots for the new tokens (q4k_batch_plan), the norm
+ * between two blocks with 8-bit activations for the next product
+ * (q4k_norm_residual_x8), the requests' low-rank adapters beside a shared projection
+ * (q4k_lora_add) and the attention of chunks of any length over the paged cache
+ * (q4k_attn_chunk). */
+
+/* Gives every request of a batch its pages and every new token its slot.  Request b
+ * holds held[b] pages (the first entries of its row of cache->page_table, which this
+ * call writes) and seq_lens[b] slots in them, and brings n_new[b] tokens; a negative
+ * n_new[b] says that the request is over.  In this order, every sum over requests running
+ * in their order:
+ *   1. A request whose slots and tokens exceed max_pages*page_size brings none
+ *      (Q4K_ERR_INDEX is recorded).  Then those with which the running sum of tokens
+ *      exceeds T bring none in this step.
+ *   2. want = ceil((seq_lens[b] + tokens) / page_size), 0 for a request that is over.
+ *      Entries want .. held - 1 (after an eviction, or at the end) go back onto the free
+ *      list free_pages[0 .. *free_count), in order.
+ *   3. A request with want > held takes want - held pages from the list's end, if the
+ *      running sum of what requests lack, itself included, is at most what the list
+ *      holds now; otherwise it brings no tokens and keeps what it holds.
+ * Outputs: the table's entries, held_out[b], *count_out (the list's new length),
+ * after_lens[b] = seq_lens[b] + its tokens (0 if over), starts[0 .. batch] = running sum
+ * of tokens, and for each token t < starts[batch] its seq, slot and position pos[t] =
+ * first_pos[b] + i for the request's i-th (first_pos NULL: the slot): the inputs of
+ * q4k_kv_append and q4k_attn_chunk.  For starts[batch] <= t < T, seq = -1, slot = pos = 0.
+ *   All arrays int32 on the device, 4-byte aligned: seq_lens, n_new, first_pos, held,
+ *   held_out, after_lens [batch]; free_pages [n_pages]; seq, slot, pos [T]; starts
+ *   [batch + 1].  after_lens may be seq_lens, held_out held, count_out free_count; other
+ *   outputs overlap nothing.  1 <= T < 2^31.
+ * Lengths and held pages out of range count as clamped and are recorded, as is a page id
+ * out of range that changes hands (it is passed on as it is) and a page that the list
+ * (of n_pages entries) has no room for (it is dropped).
+ * Workspace: q4k_batch_plan_workspace_size(cache) bytes, 256-byte aligned. */
+size_t q4k_batch_plan_workspace_size(const q4k_kv_cache *cache);
+q4k_status q4k_batch_plan(const q4k_kv_cache *cache, const int32_t *seq_lens, const int32_t *n_new,
+                          const int32_t *first_pos, const int32_t *held, int32_t *held_out, int32_t *free_pages,
+                          const int32_t *free_count, int32_t *count_out, int64_t T, int32_t *after_lens,
+                          int32_t *starts, int32_t *seq, int32_t *slot, int32_t *pos, void *ws, size_t ws_bytes,
+                          void *stream);
+
+/* q4k_norm_residual whose output is (also) 8 bits wide, the input of q4k_gemm_x8: with
+ * v = pre(h) in fp32, for each 32 consecutive values of a row a = max |v|, s = a / 127,
+ * q = rint(v / s) (ties to even, at most 127 in magnitude), and q = 0, s = 0 where all
+ * are zero (q4k_quantize_x8's rule, applied to the fp32 values instead of their bf16
+ * roundings).  A block with a NaN gets s = NaN and q = 0, one with an infinity s = infinity
+ * and q = +-127 where |v| is infinite, 0 elsewhere.
+ *   q  int8 [M][D], dense, 4-byte aligned;  s  fp32 [M][D/32], dense
+ *   D a multiple of 32; x (bf16, for the other readers of v) and r_out may be NULL
+ * Everything else, the rows' bits included, is as in q4k_norm_residual. */
+q4k_status q4k_norm_residual_x8(int64_t M, int64_t D, const float *y, int64_t ldy, int post, const float *post_w,
+                                const float *post_b, float post_eps, const float *gate, int64_t ld_gate, float scale,
+                                const void *r_in, void *r_out, int64_t ldr, int r_dtype, int pre, const float *pre_w,
+                                const float *pre_b, float pre_eps, uint16_t *x, int64_t ldx, int8_t *q, float *s,
+                                void *stream);
+
+/* Adds to a projection's output what each token's low-rank adapter contributes:
+ *     y[t][n] += scales[a] * sum_{r < ranks[a]} b[a][n][r] * (sum_k a[a][r][k] * x[t][k]),
+ * a = ids[t].  Rows of tokens with a negative id are not touched (no adapter), nor those
+ * with an id >= n_adapters (Q4K_ERR_INDEX is recorded).  What lies beyond an adapter's
+ * rank has no part in it.
+ *   a  bf16 [n_adapters][R][K], b bf16 [n_adapters][N][R]: dense, 16-byte aligned
+ *   ranks  int32 [n_adapters] (NULL: R), clamped to 0 .. R;  scales  fp32 [n_adapters] (NULL: 1)
+ *   ids  int32 [T], in any order;  x  bf16 [T][ldx], 16-byte aligned, ldx % 8 == 0
+ *   y  fp32 [T][ldy], 4-byte aligned
+ *   1 <= n_adapters <= 1024; R a multiple of 8, 8 .. 128; K a multiple of 8; N, K <= 2^21;
+ *   T <= 2^23
+ * Products are exact and sums fp32; the inner sums, times the scale, enter the second
+ * product as the sum of three bf16 values, exactly.  A row's last bits do not depend on the
+ * other rows' adapters, but on K, R and T.
+ * Workspace: q4k_lora_add_workspace_size(...) bytes, 256-byte aligned; 0 is returned for
+ * arguments that the call would refuse. */
+size_t q4k_lora_add_workspace_size(int32_t n_adapters, int64_t N, int64_t K, int32_t R, int64_t T);
+q4k_status q4k_lora_add(int32_t n_adapters, int64_t N, int64_t K, int32_t R, const uint16_t *a, const uint16_t *b,
+                        const int32_t *ranks, const float *scales, const int32_t *ids, const uint16_t *x, int64_t T,
+                        int64_t ldx, float *y, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
+
+/* The eight calls above for callers whose foreign-function interface converts every
  * argument on its own (from Python that takes longer than the rest of a small call on
  * the host): `slots` holds the arguments of the call of the same name, in its order, 8
  * bytes each in the machine's byte order - integers and addresses as int64 (a smaller
@@ -601,6 +679,9 @@ q4k_status q4k_attn_decode_slots(const void *slots);
 q4k_status q4k_kv_evict_slots(const void *slots);
 q4k_status q4k_norm_residual_slots(const void *slots);
 q4k_status q4k_sample_slots(const void *slots);
+q4k_status q4k_batch_plan_slots(const void *slots);
+q4k_status q4k_norm_residual_x8_slots(const void *slots);
+q4k_status q4k_lora_add_slots(const void *slots);
 
 #ifdef __cplusplus
 }

@@ -37,7 +37,9 @@ EXPORTS = (
     "q4k_nvfp4_dequant", "q4k_nvfp4_gemm",
     "q4k_kv_append", "q4k_attn_decode_workspace_size", "q4k_attn_decode", "q4k_kv_evict_workspace_size", "q4k_kv_evict",
     "q4k_norm_residual", "q4k_sample",
+    "q4k_batch_plan_workspace_size", "q4k_batch_plan", "q4k_norm_residual_x8", "q4k_lora_add_workspace_size", "q4k_lora_add",
     "q4k_kv_append_slots", "q4k_attn_decode_slots", "q4k_kv_evict_slots", "q4k_norm_residual_slots", "q4k_sample_slots",
+    "q4k_batch_plan_slots", "q4k_norm_residual_x8_slots", "q4k_lora_add_slots",
 )
 
 # fixed scratch capacity of q4k_moe_grouped_gemm_noalloc (Q4K_MOE_NOALLOC_SCRATCH_BYTES)
@@ -131,6 +133,12 @@ def load(path: str | None = None):
         "q4k_norm_residual": ([i64, i64, P, i64, st, P, P, f32, P, i64, f32, P, P, i64, st, st, P, P, f32, P, i64, P],
                               st),
         "q4k_sample": ([P, i64, i64, i64, P, P, P, P, P, P, P, P], st),
+        "q4k_batch_plan_workspace_size": ([C], sz),
+        "q4k_batch_plan": ([C, P, P, P, P, P, P, P, P, i64, P, P, P, P, P, P, sz, P], st),
+        "q4k_norm_residual_x8": ([i64, i64, P, i64, st, P, P, f32, P, i64, f32, P, P, i64, st, st, P, P, f32, P, i64, P, P, P],
+                                 st),
+        "q4k_lora_add_workspace_size": ([i32, i64, i64, i32, i64], sz),
+        "q4k_lora_add": ([i32, i64, i64, i32, P, P, P, P, P, P, i64, i64, P, i64, P, sz, P], st),
     }
     for name in _SLOTS:
         sig[name + "_slots"] = ([ctypes.c_char_p], st)
@@ -153,7 +161,8 @@ def _ptr(a):
 # argument on its own, and for these that took a quarter of a small call's host time.
 _SLOTS = {name: struct.Struct(form).pack for name, form in (
     ("q4k_kv_append", "=22q"), ("q4k_attn_decode", "=6q2d5qd3q"), ("q4k_kv_evict", "=14q"),
-    ("q4k_norm_residual", "=7qd2qd7qd3q"), ("q4k_sample", "=12q"))}
+    ("q4k_norm_residual", "=7qd2qd7qd3q"), ("q4k_sample", "=12q"), ("q4k_batch_plan", "=18q"),
+    ("q4k_norm_residual_x8", "=7qd2qd7qd5q"), ("q4k_lora_add", "=17q"))}
 
 
 def _adr(a):
@@ -168,7 +177,7 @@ def _cache(c):
     return 0 if c is None else ctypes.addressof(c)
 
 
-_pack_append, _pack_attn, _pack_evict, _pack_norm, _pack_sample = _SLOTS.values()
+_pack_append, _pack_attn, _pack_evict, _pack_norm, _pack_sample, _pack_plan, _pack_norm8, _pack_lora = _SLOTS.values()
 
 _current_stream = None
 
@@ -393,3 +402,41 @@ def q4k_sample(logits, M: int, V: int, ldl: int, temperature, top_k, top_p, min_
     _check(load().q4k_sample_slots(_pack_sample(
         _adr(logits), M, V, ldl, _adr(temperature), _adr(top_k), _adr(top_p), _adr(min_p), _adr(u), _adr(token), _adr(prob),
         _adr(_stream(stream)))), "q4k_sample")
+
+
+def q4k_batch_plan_workspace_size(cache) -> int:
+    return load().q4k_batch_plan_workspace_size(cache)
+
+
+def q4k_batch_plan(cache, seq_lens, n_new, first_pos, held, held_out, free_pages, free_count, count_out, T: int, after_lens,
+                   starts, seq, slot, pos, ws, ws_bytes: int, stream=None) -> None:
+    """Gives each request of a batch its pages (written into the cache's page table, from and to a free list) and each of
+    its new tokens its sequence, slot and position; n_new < 0 ends a request."""
+    _check(load().q4k_batch_plan_slots(_pack_plan(
+        _cache(cache), _adr(seq_lens), _adr(n_new), _adr(first_pos), _adr(held), _adr(held_out), _adr(free_pages),
+        _adr(free_count), _adr(count_out), T, _adr(after_lens), _adr(starts), _adr(seq), _adr(slot), _adr(pos), _adr(ws),
+        ws_bytes, _adr(_stream(stream)))), "q4k_batch_plan")
+
+
+def q4k_norm_residual_x8(M: int, D: int, y, ldy: int, post: int, post_w, post_b, post_eps: float, gate, ld_gate: int,
+                         scale: float, r_in, r_out, ldr: int, r_dtype: int, pre: int, pre_w, pre_b, pre_eps: float, x,
+                         ldx: int, q, s, stream=None) -> None:
+    """q4k_norm_residual with pre(h) as int8 q [M][D] and fp32 scales s [M][D/32] (the input of q4k_gemm_x8); x, the same
+    in bf16, may be None."""
+    _check(load().q4k_norm_residual_x8_slots(_pack_norm8(
+        M, D, _adr(y), ldy, post, _adr(post_w), _adr(post_b), post_eps, _adr(gate), ld_gate, scale, _adr(r_in),
+        _adr(r_out), ldr, r_dtype, pre, _adr(pre_w), _adr(pre_b), pre_eps, _adr(x), ldx, _adr(q), _adr(s),
+        _adr(_stream(stream)))), "q4k_norm_residual_x8")
+
+
+def q4k_lora_add_workspace_size(n_adapters: int, N: int, K: int, R: int, T: int) -> int:
+    return load().q4k_lora_add_workspace_size(n_adapters, N, K, R, T)
+
+
+def q4k_lora_add(n_adapters: int, N: int, K: int, R: int, a, b, ranks, scales, ids, x, T: int, ldx: int, y, ldy: int, ws,
+                 ws_bytes: int, stream=None) -> None:
+    """y[t] += scales[i] * b[i] (a[i] x[t]), i = ids[t] (negative: none); a bf16 [n_adapters][R][K], b bf16
+    [n_adapters][N][R], x bf16, y fp32."""
+    _check(load().q4k_lora_add_slots(_pack_lora(
+        n_adapters, N, K, R, _adr(a), _adr(b), _adr(ranks), _adr(scales), _adr(ids), _adr(x), T, ldx, _adr(y), ldy, _adr(ws),
+        ws_bytes, _adr(_stream(stream)))), "q4k_lora_add")

@@ -1,4 +1,4 @@
-// C-ABI of the operators between a decode step's weight products: argument
+// C-ABI of the operators between a step's weight products: argument
 // validation, workspace layout and dispatch.  Their contract is in include/q4k.h.
 #include <cuda_runtime.h>
 
@@ -139,6 +139,68 @@ int64_t evict_max_moves(int64_t cap, int64_t budget) {
 int64_t evict_cap(const q4k_kv_cache *c, int64_t ld_meta) {
     const int64_t table = (int64_t)c->max_pages * c->page_size;
     return ld_meta < table ? ld_meta : table;
+}
+
+q4k_status norm_residual(int64_t M, int64_t D, const float *y, int64_t ldy, int post, const float *post_w,
+                          const float *post_b, float post_eps, const float *gate, int64_t ld_gate, float scale,
+                          const void *r_in, void *r_out, int64_t ldr, int r_dtype, int pre, const float *pre_w,
+                          const float *pre_b, float pre_eps, uint16_t *x, int64_t ldx, bool x8, int8_t *q,
+                          float *q_scale, void *stream) {
+    if (!r_in || (x8 ? !q || !q_scale : !r_out && !x)) return Q4K_ERR_NULL;
+    auto kind_ok = [](int k) { return k == Q4K_NORM_NONE || k == Q4K_NORM_RMS || k == Q4K_NORM_LAYER; };
+    if (M < 1 || M >= kInt31 || D < 1 || D > (1 << 20) || (y && ldy < D) || ldr < D || (x && ldx < D) ||
+        (gate && ld_gate != 0 && ld_gate < D) || !kind_ok(post) || !kind_ok(pre) ||
+        (r_dtype != Q4K_RES_FP32 && r_dtype != Q4K_RES_BF16) || !(post_eps >= 0.f) || !(pre_eps >= 0.f) || (x8 && D % 32))
+        return Q4K_ERR_SHAPE;
+    const uintptr_t ra = r_dtype == Q4K_RES_FP32 ? 4 : 2;
+    if (!aligned(y, 4) || !aligned(post_w, 4) || !aligned(post_b, 4) || !aligned(gate, 4) || !aligned(r_in, ra) ||
+        !aligned(r_out, ra) || !aligned(pre_w, 4) || !aligned(pre_b, 4) || !aligned(x, 2) || !aligned(q, 4) ||
+        !aligned(q_scale, 4))
+        return Q4K_ERR_ALIGN;
+    DeviceInfo di;
+    q4k_status st = check_device(&di);
+    if (st != Q4K_OK) return st;
+    NormArgs a = {};
+    a.M = M, a.D = D;
+    a.y = y, a.ldy = ldy;
+    a.post = post, a.post_w = post_w, a.post_b = post_b, a.post_eps = post_eps;
+    a.gate = gate, a.ld_gate = ld_gate, a.scale = scale;
+    a.r_in = r_in, a.r_out = r_out, a.ldr = ldr, a.bf16 = r_dtype == Q4K_RES_BF16;
+    a.pre = pre, a.pre_w = pre_w, a.pre_b = pre_b, a.pre_eps = pre_eps;
+    a.x = x, a.ldx = ldx;
+    a.q = q, a.q_scale = q_scale;
+    a.invariant = batch_invariant();
+    a.wait_ns = wait_limit_ns();
+    a.status = di.status;
+    return finish(launch_norm_residual(di, a, static_cast<cudaStream_t>(stream)));
+}
+
+// the running sums of pages, and the free list's lengths
+size_t plan_ws(const q4k_kv_cache *c) { return align256(((size_t)c->batch + 1) * 4) * 2 + 256; }
+
+bool lora_shape_ok(int32_t n_adapters, int64_t N, int64_t K, int32_t R, int64_t T) {
+    return n_adapters >= 1 && n_adapters <= 1024 && N >= 1 && N <= (1 << 21) && K >= 8 && K <= (1 << 21) && K % 8 == 0 && R >= 8 &&
+           R <= 128 && R % 8 == 0 && T >= 1 && T <= (1 << 23);
+}
+
+struct LoraLayout {
+    size_t part, offsets, perm, tiles, n_tiles, total;
+};
+LoraLayout lora_layout(int32_t n_adapters, int64_t K, int32_t R, int64_t T) {
+    LoraLayout l = {};
+    size_t at = align256((size_t)lora_split(K, T, n_adapters).splits * T * R * 4);
+    if (T > kLoraSmall) {
+        l.offsets = at;
+        at += align256(((size_t)n_adapters + 1) * 4);
+        l.perm = at;
+        at += align256((size_t)T * 4);
+        l.tiles = at;
+        at += align256((size_t)moe_max_tiles(n_adapters, T) * sizeof(int4));
+        l.n_tiles = at;
+        at += 256;
+    }
+    l.total = at;
+    return l;
 }
 
 }  // namespace
@@ -283,31 +345,17 @@ q4k_status q4k_norm_residual(int64_t M, int64_t D, const float *y, int64_t ldy, 
                              const float *post_b, float post_eps, const float *gate, int64_t ld_gate, float scale,
                              const void *r_in, void *r_out, int64_t ldr, int r_dtype, int pre, const float *pre_w,
                              const float *pre_b, float pre_eps, uint16_t *x, int64_t ldx, void *stream) {
-    if (!r_in || (!r_out && !x)) return Q4K_ERR_NULL;
-    auto kind_ok = [](int k) { return k == Q4K_NORM_NONE || k == Q4K_NORM_RMS || k == Q4K_NORM_LAYER; };
-    if (M < 1 || M >= kInt31 || D < 1 || D > (1 << 20) || (y && ldy < D) || ldr < D || (x && ldx < D) ||
-        (gate && ld_gate != 0 && ld_gate < D) || !kind_ok(post) || !kind_ok(pre) ||
-        (r_dtype != Q4K_RES_FP32 && r_dtype != Q4K_RES_BF16) || !(post_eps >= 0.f) || !(pre_eps >= 0.f))
-        return Q4K_ERR_SHAPE;
-    const uintptr_t ra = r_dtype == Q4K_RES_FP32 ? 4 : 2;
-    if (!aligned(y, 4) || !aligned(post_w, 4) || !aligned(post_b, 4) || !aligned(gate, 4) || !aligned(r_in, ra) ||
-        !aligned(r_out, ra) || !aligned(pre_w, 4) || !aligned(pre_b, 4) || !aligned(x, 2))
-        return Q4K_ERR_ALIGN;
-    DeviceInfo di;
-    q4k_status st = check_device(&di);
-    if (st != Q4K_OK) return st;
-    NormArgs a = {};
-    a.M = M, a.D = D;
-    a.y = y, a.ldy = ldy;
-    a.post = post, a.post_w = post_w, a.post_b = post_b, a.post_eps = post_eps;
-    a.gate = gate, a.ld_gate = ld_gate, a.scale = scale;
-    a.r_in = r_in, a.r_out = r_out, a.ldr = ldr, a.bf16 = r_dtype == Q4K_RES_BF16;
-    a.pre = pre, a.pre_w = pre_w, a.pre_b = pre_b, a.pre_eps = pre_eps;
-    a.x = x, a.ldx = ldx;
-    a.invariant = batch_invariant();
-    a.wait_ns = wait_limit_ns();
-    a.status = di.status;
-    return finish(launch_norm_residual(di, a, static_cast<cudaStream_t>(stream)));
+    return norm_residual(M, D, y, ldy, post, post_w, post_b, post_eps, gate, ld_gate, scale, r_in, r_out, ldr, r_dtype, pre, pre_w,
+                         pre_b, pre_eps, x, ldx, false, nullptr, nullptr, stream);
+}
+
+q4k_status q4k_norm_residual_x8(int64_t M, int64_t D, const float *y, int64_t ldy, int post, const float *post_w,
+                                const float *post_b, float post_eps, const float *gate, int64_t ld_gate, float scale,
+                                const void *r_in, void *r_out, int64_t ldr, int r_dtype, int pre, const float *pre_w,
+                                const float *pre_b, float pre_eps, uint16_t *x, int64_t ldx, int8_t *q, float *s,
+                                void *stream) {
+    return norm_residual(M, D, y, ldy, post, post_w, post_b, post_eps, gate, ld_gate, scale, r_in, r_out, ldr, r_dtype, pre, pre_w,
+                         pre_b, pre_eps, x, ldx, true, q, s, stream);
 }
 
 q4k_status q4k_sample(const float *logits, int64_t M, int64_t V, int64_t ldl, const float *temperature,
@@ -330,11 +378,84 @@ q4k_status q4k_sample(const float *logits, int64_t M, int64_t V, int64_t ldl, co
     return finish(launch_sample(di, a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t q4k_batch_plan_workspace_size(const q4k_kv_cache *cache) { return cache && cache_shape_ok(cache) ? plan_ws(cache) : 0; }
+
+q4k_status q4k_batch_plan(const q4k_kv_cache *cache, const int32_t *seq_lens, const int32_t *n_new,
+                          const int32_t *first_pos, const int32_t *held, int32_t *held_out, int32_t *free_pages,
+                          const int32_t *free_count, int32_t *count_out, int64_t T, int32_t *after_lens,
+                          int32_t *starts, int32_t *seq, int32_t *slot, int32_t *pos, void *ws, size_t ws_bytes,
+                          void *stream) {
+    q4k_status st = cache_check(cache);
+    if (st != Q4K_OK) return st;
+    if (!seq_lens || !n_new || !held || !held_out || !free_pages || !free_count || !count_out || !after_lens || !starts || !seq ||
+        !slot || !pos || !ws)
+        return Q4K_ERR_NULL;
+    if (T < 1 || T >= kInt31) return Q4K_ERR_SHAPE;
+    if (!aligned(seq_lens, 4) || !aligned(n_new, 4) || !aligned(first_pos, 4) || !aligned(held, 4) || !aligned(held_out, 4) ||
+        !aligned(free_pages, 4) || !aligned(free_count, 4) || !aligned(count_out, 4) || !aligned(after_lens, 4) ||
+        !aligned(starts, 4) || !aligned(seq, 4) || !aligned(slot, 4) || !aligned(pos, 4) || !aligned(ws, 256))
+        return Q4K_ERR_ALIGN;
+    if (ws_bytes < plan_ws(cache)) return Q4K_ERR_WORKSPACE;
+    DeviceInfo di;
+    if ((st = check_device(&di)) != Q4K_OK) return st;
+    PlanArgs a = {};
+    a.c = view(cache, di);
+    a.table = const_cast<int32_t *>(cache->page_table);
+    a.seq_lens = seq_lens, a.n_new = n_new, a.first_pos = first_pos, a.held = held, a.free_count = free_count;
+    a.held_out = held_out, a.free_pages = free_pages, a.count_out = count_out;
+    a.T = T;
+    a.after_lens = after_lens, a.starts = starts, a.seq = seq, a.slot = slot, a.pos = pos;
+    const size_t sums = align256(((size_t)cache->batch + 1) * 4);
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    a.back_at = reinterpret_cast<int32_t *>(base);
+    a.take_at = reinterpret_cast<int32_t *>(base + sums);
+    a.list = reinterpret_cast<int32_t *>(base + 2 * sums);
+    return finish(launch_batch_plan(di, a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t q4k_lora_add_workspace_size(int32_t n_adapters, int64_t N, int64_t K, int32_t R, int64_t T) {
+    return lora_shape_ok(n_adapters, N, K, R, T) ? lora_layout(n_adapters, K, R, T).total : 0;
+}
+
+q4k_status q4k_lora_add(int32_t n_adapters, int64_t N, int64_t K, int32_t R, const uint16_t *a, const uint16_t *b,
+                        const int32_t *ranks, const float *scales, const int32_t *ids, const uint16_t *x, int64_t T,
+                        int64_t ldx, float *y, int64_t ldy, void *ws, size_t ws_bytes, void *stream) {
+    if (!a || !b || !ids || !x || !y || !ws) return Q4K_ERR_NULL;
+    if (!lora_shape_ok(n_adapters, N, K, R, T) || ldx < K || ldy < N) return Q4K_ERR_SHAPE;
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(ranks, 4) || !aligned(scales, 4) || !aligned(ids, 4) || !aligned(x, 16) ||
+        ldx % 8 || !aligned(y, 4) || !aligned(ws, 256))
+        return Q4K_ERR_ALIGN;
+    const LoraLayout l = lora_layout(n_adapters, K, R, T);
+    if (ws_bytes < l.total) return Q4K_ERR_WORKSPACE;
+    DeviceInfo di;
+    const q4k_status st = check_device(&di);
+    if (st != Q4K_OK) return st;
+    LoraArgs c = {};
+    c.n_adapters = n_adapters, c.R = R, c.N = N, c.K = K;
+    c.a = a, c.b = b, c.ranks = ranks, c.scales = scales, c.ids = ids;
+    c.x = x, c.T = T, c.ldx = ldx, c.y = y, c.ldy = ldy;
+    c.status = di.status;
+    const LoraSplit split = lora_split(K, T, n_adapters);
+    c.k_chunk = (int32_t)split.k_chunk, c.splits = split.splits;
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    c.part = reinterpret_cast<float *>(base + l.part);
+    if (T > kLoraSmall) {
+        c.offsets = reinterpret_cast<int32_t *>(base + l.offsets);
+        c.perm = reinterpret_cast<int32_t *>(base + l.perm);
+        c.tiles = reinterpret_cast<int4 *>(base + l.tiles);
+        c.n_tiles = reinterpret_cast<int *>(base + l.n_tiles);
+    }
+    return finish(launch_lora_add(di, c, static_cast<cudaStream_t>(stream)));
+}
+
 // What the Python package calls.
 q4k_status q4k_kv_append_slots(const void *slots) { return call(q4k_kv_append, slots); }
 q4k_status q4k_attn_decode_slots(const void *slots) { return call(q4k_attn_decode, slots); }
 q4k_status q4k_kv_evict_slots(const void *slots) { return call(q4k_kv_evict, slots); }
 q4k_status q4k_norm_residual_slots(const void *slots) { return call(q4k_norm_residual, slots); }
 q4k_status q4k_sample_slots(const void *slots) { return call(q4k_sample, slots); }
+q4k_status q4k_batch_plan_slots(const void *slots) { return call(q4k_batch_plan, slots); }
+q4k_status q4k_norm_residual_x8_slots(const void *slots) { return call(q4k_norm_residual_x8, slots); }
+q4k_status q4k_lora_add_slots(const void *slots) { return call(q4k_lora_add, slots); }
 
 }  // extern "C"

@@ -94,6 +94,8 @@ struct NormArgs {
     float pre_eps;
     uint16_t *x;
     int64_t ldx;
+    int8_t *q;     // 8-bit output with its scales, or null
+    float *q_scale;
     int invariant;  // a row's bits must not depend on M
     unsigned long long wait_ns;  // limit of the ring's waits
     unsigned int *status;
@@ -112,5 +114,45 @@ struct SampleArgs {
     float *prob;
 };
 cudaError_t launch_sample(const DeviceInfo &di, const SampleArgs &a, cudaStream_t s);
+
+struct PlanArgs {
+    KvView c;
+    int32_t *table;  // c.table, to write
+    const int32_t *seq_lens, *n_new, *first_pos, *held, *free_count;
+    int32_t *held_out, *free_pages, *count_out;
+    int64_t T;
+    int32_t *after_lens, *starts, *seq, *slot, *pos;
+    // workspace
+    int32_t *back_at, *take_at;  // [batch + 1]: pages returned and taken before each request
+    int32_t *list;               // [2]: length of the free list before the call, and with the pages returned
+};
+cudaError_t launch_batch_plan(const DeviceInfo &di, const PlanArgs &a, cudaStream_t s);
+
+constexpr int kLoraSmall = 192;  // tokens of a call whose CTAs find their adapters' tokens themselves
+struct LoraArgs {
+    int32_t n_adapters, R;
+    int64_t N, K;
+    const uint16_t *a, *b;
+    const int32_t *ranks;
+    const float *scales;
+    const int32_t *ids;
+    const uint16_t *x;
+    int64_t T, ldx;
+    float *y;
+    int64_t ldy;
+    unsigned int *status;
+    int32_t k_chunk, splits;     // of the K axis
+    // workspace
+    float *part;                 // [splits][T][R]
+    int32_t *offsets, *perm;     // more than kLoraSmall tokens: sorted by adapter (else null)
+    int4 *tiles;
+    int *n_tiles;
+};
+struct LoraSplit {
+    int64_t k_chunk;
+    int splits;
+};
+LoraSplit lora_split(int64_t K, int64_t T, int n_adapters);
+cudaError_t launch_lora_add(const DeviceInfo &di, const LoraArgs &a, cudaStream_t s);
 
 }  // namespace q4k

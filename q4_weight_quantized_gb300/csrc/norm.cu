@@ -1,6 +1,6 @@
 // The end of one block and the start of the next in one pass:
 //     h = r + scale * gate * post(y),  r' = h,  x = bf16(pre(h))
-// post and pre being RMS or layer norms over a row.
+// post and pre being RMS or layer norms over a row; x may (also) be 8 bits a value, with a scale for each 32.
 //
 // Bound by HBM for many rows (a row of y and r read, of r' and x written, each once)
 // and by latency for few.  A CTA holds a whole row in registers between the two norms,
@@ -46,6 +46,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// v in 8 bits at the scale s = a / 127, a being the largest |v| of its block
+__device__ __forceinline__ float in_eight(float v, float s, float a) {
+    return a > 0.f ? copysignf(fminf(rintf(fabsf(v) / s), 127.f), v) : 0.f;
 }
 
 // A row of D values over a CTA: thread t holds group i (of NV) of four values, elements
@@ -103,6 +108,39 @@ struct Slice {
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     if (in(i, x)) p[at(i, x)] = (uint16_t)((x < 2 ? t.x : t.y) >> (x & 1) * 16);
+            }
+        }
+    }
+    // 8 bits a value, with a scale for each 32 consecutive ones (D % 32 == 0: a block lies in eight neighbouring threads'
+    // groups of four, VEC, or in a warp's single values, and is there as a whole or not at all):
+    //     s = max |v| / 127, q = rint(v / s), at most 127 in magnitude (so is an infinity's); 0 for a block of zeros or
+    // with a NaN
+    __device__ __forceinline__ void store8(int8_t *q, float *scale, const float (&v)[4 * NV]) const {
+        // |v| orders like its bits: the largest as whole numbers
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if constexpr (VEC) {
+                const uint32_t m01 = max(__float_as_uint(fabsf(v[4 * i])), __float_as_uint(fabsf(v[4 * i + 1])));
+                const uint32_t m23 = max(__float_as_uint(fabsf(v[4 * i + 2])), __float_as_uint(fabsf(v[4 * i + 3])));
+                uint32_t top = max(m01, m23);
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                const float a = __uint_as_float(top), s = a / 127.0f;
+                if (!in(i, 0)) continue;
+                uint32_t word = 0;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) word |= ((uint32_t)(int)in_eight(v[4 * i + x], s, a) & 0xFFu) << (8 * x);
+                *reinterpret_cast<uint32_t *>(q + at(i, 0)) = word;
+                if ((tid & 7) == 0) scale[at(i, 0) / 32] = s;
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v[4 * i + x]))));
+                    const float s = a / 127.0f;
+                    if (!in(i, x)) continue;
+                    q[at(i, x)] = (int8_t)(int)in_eight(v[4 * i + x], s, a);
+                    if ((tid & 31) == 0) scale[at(i, x) / 32] = s;
+                }
             }
         }
     }
@@ -170,7 +208,7 @@ struct Slice {
     }
 };
 
-template <int NV, bool VEC, bool BF16>
+template <int NV, bool VEC, bool BF16, bool X8>
 __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
     using Res = typename std::conditional<BF16, uint16_t, float>::type;
     __shared__ float2 scratch[2][32];
@@ -195,9 +233,10 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
         for (int k = 0; k < 4 * NV; ++k) h[k] = fmaf(a.scale, y[k], h[k]);
     }
     if (a.r_out) s.store(static_cast<Res *>(a.r_out) + row * a.ldr, h);
-    if (!a.x) return;
+    if (!X8 && !a.x) return;
     if (a.pre != kNone) s.norm(h, a.pre, a.pre_w, a.pre_b, a.pre_eps, scratch, turn);
-    s.store(a.x + row * a.ldx, h);
+    if (!X8 || a.x) s.store(a.x + row * a.ldx, h);
+    if constexpr (X8) s.store8(a.q + row * a.D, a.q_scale + row * (a.D / 32), h);
 }
 
 // Many rows: a few CTAs an SM walk them, one row in registers while the next ones are copied into a ring in
@@ -212,7 +251,7 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
 }
 
 // (640: 96 registers a thread, so that two CTAs of up to 320 threads share an SM)
-template <int NV, bool BF16, bool FULL>
+template <int NV, bool BF16, bool FULL, bool X8>
 __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int stages, uint32_t ring_bytes) {
     using Res = typename std::conditional<BF16, uint16_t, float>::type;
     extern __shared__ __align__(128) uint8_t ring[];
@@ -251,9 +290,10 @@ __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int st
     };
     if (a.y && a.post != kNone && a.post_w) times(wy, a.post_w);
     if (a.y && a.gate && !gate_rows) times(wy, a.gate);
-    if (a.x && a.pre != kNone && a.pre_w) times(wx, a.pre_w);
+    const bool out = X8 || a.x;  // is pre(h) wanted
+    if (out && a.pre != kNone && a.pre_w) times(wx, a.pre_w);
     // and scale * gate * post_b and pre_b, in shared memory behind the ring (registers are short): each thread's own
-    const bool post_b = a.y && a.post != kNone && a.post_b, pre_b = a.x && a.pre != kNone && a.pre_b;
+    const bool post_b = a.y && a.post != kNone && a.post_b, pre_b = out && a.pre != kNone && a.pre_b;
     float *const by = reinterpret_cast<float *>(ring + ring_bytes), *const bx = by + (post_b ? D : 0);
     if (post_b) {
         float t[4 * NV];
@@ -329,7 +369,7 @@ __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int st
         if (tid == 0 && row + (int64_t)stages * gridDim.x < a.M) copy(row + (int64_t)stages * gridDim.x, stage);
         if (++stage == stages) stage = 0, parity ^= 1;
         if (a.r_out) s.store(static_cast<Res *>(a.r_out) + row * a.ldr, h);
-        if (!a.x) continue;
+        if (!out) continue;
         if (a.pre != kNone) {
             const float f = s.scale_of(h, a.pre, a.pre_eps, inv, in_warp, in_lane, scratch, turn);
 #pragma unroll
@@ -340,7 +380,8 @@ __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int st
                 for (int x = 0; x < 4; ++x) h[4 * i + x] = fmaf(h[4 * i + x] * f, wx[4 * i + x], b4[x]);
             }
         }
-        s.store(a.x + row * a.ldx, h);
+        if (!X8 || a.x) s.store(a.x + row * a.ldx, h);
+        if constexpr (X8) s.store8(a.q + row * D, a.q_scale + row * (D / 32), h);
     }
 }
 
@@ -379,7 +420,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a
         return fmaf(a.scale, v, r);
     };
     float h_mean = 0.f, h_f = 1.f;
-    if (a.x && a.pre != kNone) {
+    if ((a.x || a.q) && a.pre != kNone) {
         if (a.pre == kLayer) h_mean = total(h_at) / n;
         h_f = 1.f / sqrtf(total([&](int64_t e) { const float d = h_at(e) - h_mean; return d * d; }) / n + a.pre_eps);
     }
@@ -389,22 +430,29 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a
             if (a.bf16) static_cast<uint16_t *>(a.r_out)[row * a.ldr + e] = __bfloat16_as_ushort(__float2bfloat16_rn(h));
             else static_cast<float *>(a.r_out)[row * a.ldr + e] = h;
         }
-        if (a.x) {
+        if (a.x || a.q) {
             float v = h;
             if (a.pre != kNone) {
                 v = (h - h_mean) * h_f;
                 if (a.pre_w) v *= __ldg(a.pre_w + e);
                 if (a.pre_b) v += __ldg(a.pre_b + e);
             }
-            a.x[row * a.ldx + e] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            if (a.x) a.x[row * a.ldx + e] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            if (a.q) {  // (D % 32 == 0: whole warps)
+                const float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v)))), s = top / 127.0f;
+                a.q[row * D + e] = (int8_t)(int)in_eight(v, s, top);
+                if ((threadIdx.x & 31) == 0) a.q_scale[row * (D / 32) + e / 32] = s;
+            }
         }
     }
 }
 
 template <int NV>
 cudaError_t launch(const NormArgs &a, bool vec, int threads, cudaStream_t s) {
-    auto kern = a.bf16 ? (vec ? norm_kernel<NV, true, true> : norm_kernel<NV, false, true>)
-                       : (vec ? norm_kernel<NV, true, false> : norm_kernel<NV, false, false>);
+    auto kern = a.q ? (a.bf16 ? (vec ? norm_kernel<NV, true, true, true> : norm_kernel<NV, false, true, true>)
+                              : (vec ? norm_kernel<NV, true, false, true> : norm_kernel<NV, false, false, true>))
+                    : (a.bf16 ? (vec ? norm_kernel<NV, true, true, false> : norm_kernel<NV, false, true, false>)
+                              : (vec ? norm_kernel<NV, true, false, false> : norm_kernel<NV, false, false, false>));
     // rows of one warp: eight to a CTA where they are many (8038 x 65: 8.5 us with one, 5 with eight)
     const int rows = threads == 32 && a.M >= 2048 ? 8 : 1;
     return launch_pdl(kern, dim3((unsigned)((a.M + rows - 1) / rows)), dim3(threads, rows), 0, s, dim3(1), a);
@@ -412,8 +460,11 @@ cudaError_t launch(const NormArgs &a, bool vec, int threads, cudaStream_t s) {
 
 template <int NV>
 cudaError_t launch_rows(const NormArgs &a, int stages, int ring, int smem, int per_sm, int threads, int sm_count, cudaStream_t s) {
-    auto kern = a.D == 4 * NV * threads ? (a.bf16 ? norm_rows_kernel<NV, true, true> : norm_rows_kernel<NV, false, true>)
-                                        : (a.bf16 ? norm_rows_kernel<NV, true, false> : norm_rows_kernel<NV, false, false>);
+    const bool full = a.D == 4 * NV * threads;
+    auto kern = a.q ? (full ? (a.bf16 ? norm_rows_kernel<NV, true, true, true> : norm_rows_kernel<NV, false, true, true>)
+                            : (a.bf16 ? norm_rows_kernel<NV, true, false, true> : norm_rows_kernel<NV, false, false, true>))
+                    : (full ? (a.bf16 ? norm_rows_kernel<NV, true, true, false> : norm_rows_kernel<NV, false, true, false>)
+                            : (a.bf16 ? norm_rows_kernel<NV, true, false, false> : norm_rows_kernel<NV, false, false, false>));
     cudaError_t e = ensure_smem((const void *)kern, smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = a.M < (int64_t)sm_count * per_sm ? a.M : (int64_t)sm_count * per_sm;
@@ -442,7 +493,7 @@ cudaError_t launch_norm_residual(const DeviceInfo &di, const NormArgs &a, cudaSt
     while (nv > 1 && quads % (32 * nv) != 0 && quads % 32 == 0 && quads <= 640 * (nv / 2)) nv /= 2;
     const int threads_many = (int)(((quads + nv - 1) / nv + 31) / 32 * 32);
     if (bulk && threads_many > 32 && threads_many <= 640 && (a.M >= di.sm_count || a.invariant)) {
-        const int64_t biases = 4 * a.D * ((a.y && a.post != kNone && a.post_b ? 1 : 0) + (a.x && a.pre != kNone && a.pre_b ? 1 : 0));
+        const int64_t biases = 4 * a.D * ((a.y && a.post != kNone && a.post_b ? 1 : 0) + ((a.x || a.q) && a.pre != kNone && a.pre_b ? 1 : 0));
         int per_sm = (nv == 4 ? 640 : 960) / threads_many;  // (as many as the registers allow)
         if (per_sm > 10) per_sm = 10;
         while (per_sm > 1 && (220 * 1024) / per_sm < 2 * row_bytes + biases + 1024) --per_sm;
