@@ -668,7 +668,36 @@ q4k_status q4k_lora_add(int32_t n_adapters, int64_t N, int64_t K, int32_t R, con
                         const int32_t *ranks, const float *scales, const int32_t *ids, const uint16_t *x, int64_t T,
                         int64_t ldx, float *y, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
 
-/* The eight calls above for callers whose foreign-function interface converts every
+/* Attention of a chunk of new tokens of every sequence over its cache: q4k_attn_decode's
+ * definition with a number of new tokens n_b = starts[b+1] - starts[b] of each sequence's
+ * own, from none to whole prompts.
+ *   s[r][j] = scale * k_scale * q[r] . k[j]   (with softcap c > 0: c*tanh(s/c))
+ *   o[r]    = v_scale * sum_j softmax_j(s[r])[j] * v[j]
+ * Row r is head hq of token i (0 <= i < n_b) of sequence b, which is row starts[b] + i of
+ * q and o; it reads KV head hq / (n_heads/n_kv_heads) at slots [max(0, e - window), e),
+ * e = seq_lens[b] - n_b + 1 + i (window 0: all of [0, e)).  seq_lens[b] counts the new
+ * tokens, which q4k_kv_append has written.  A row that reads nothing (e <= 0) gives 0; a
+ * slot outside a row's range has no part in it, whatever its key and value hold.
+ *   q, o: bf16 [T][ldq], [T][ldo], heads of D consecutive; 16-byte aligned, ldq and ldo
+ *     multiples of 8; they do not overlap.  Rows of o that belong to no sequence are not touched.
+ *   starts: int32 [batch + 1], not decreasing, 0 .. T; one that is out of order or range is recorded
+ *     (Q4K_ERR_INDEX) and counts as the nearest that is not.  starts[0] need not be 0.
+ *   n_heads: a multiple of n_kv_heads, n_heads / n_kv_heads <= 1024; T * n_heads < 2^31.
+ * Products are exact, sums and softmax fp32.  The weights enter the second product
+ * rounded to bf16 (each off by 2^-8 at most; for an e4m3 cache, whose values are exact in
+ * f16, to f16: by 2^-11, and 2^-32 of the largest), while the sum that divides them is that of the fp32 values: their
+ * errors, which add up at random, are of the size of o's own rounding.  (For an e4m3 cache a value of
+ * q below 2^-31 of the largest of its row is taken to 2^-39 of that one.)  The work is split over the whole GPU by all
+ * lengths, and split rows are joined in slot order: the same call repeats its bits, but a
+ * row's last bits may depend on the rest of the batch, also in batch-invariant mode.
+ * Workspace: q4k_attn_chunk_workspace_size(cache, T, n_heads) bytes, 256-byte aligned; 0
+ * is returned for arguments that the call would refuse. */
+size_t q4k_attn_chunk_workspace_size(const q4k_kv_cache *cache, int64_t T, int32_t n_heads);
+q4k_status q4k_attn_chunk(const q4k_kv_cache *cache, const int32_t *starts, const int32_t *seq_lens, const uint16_t *q,
+                          int64_t T, int64_t ldq, int32_t n_heads, float scale, float softcap, int64_t window,
+                          uint16_t *o, int64_t ldo, void *ws, size_t ws_bytes, void *stream);
+
+/* The nine calls above for callers whose foreign-function interface converts every
  * argument on its own (from Python that takes longer than the rest of a small call on
  * the host): `slots` holds the arguments of the call of the same name, in its order, 8
  * bytes each in the machine's byte order - integers and addresses as int64 (a smaller
@@ -682,6 +711,7 @@ q4k_status q4k_sample_slots(const void *slots);
 q4k_status q4k_batch_plan_slots(const void *slots);
 q4k_status q4k_norm_residual_x8_slots(const void *slots);
 q4k_status q4k_lora_add_slots(const void *slots);
+q4k_status q4k_attn_chunk_slots(const void *slots);
 
 #ifdef __cplusplus
 }

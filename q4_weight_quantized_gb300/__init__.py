@@ -38,8 +38,9 @@ EXPORTS = (
     "q4k_kv_append", "q4k_attn_decode_workspace_size", "q4k_attn_decode", "q4k_kv_evict_workspace_size", "q4k_kv_evict",
     "q4k_norm_residual", "q4k_sample",
     "q4k_batch_plan_workspace_size", "q4k_batch_plan", "q4k_norm_residual_x8", "q4k_lora_add_workspace_size", "q4k_lora_add",
+    "q4k_attn_chunk_workspace_size", "q4k_attn_chunk",
     "q4k_kv_append_slots", "q4k_attn_decode_slots", "q4k_kv_evict_slots", "q4k_norm_residual_slots", "q4k_sample_slots",
-    "q4k_batch_plan_slots", "q4k_norm_residual_x8_slots", "q4k_lora_add_slots",
+    "q4k_batch_plan_slots", "q4k_norm_residual_x8_slots", "q4k_lora_add_slots", "q4k_attn_chunk_slots",
 )
 
 # fixed scratch capacity of q4k_moe_grouped_gemm_noalloc (Q4K_MOE_NOALLOC_SCRATCH_BYTES)
@@ -138,6 +139,8 @@ def load(path: str | None = None):
         "q4k_norm_residual_x8": ([i64, i64, P, i64, st, P, P, f32, P, i64, f32, P, P, i64, st, st, P, P, f32, P, i64, P, P, P],
                                  st),
         "q4k_lora_add_workspace_size": ([i32, i64, i64, i32, i64], sz),
+        "q4k_attn_chunk_workspace_size": ([C, i64, i32], sz),
+        "q4k_attn_chunk": ([C, P, P, P, i64, i64, i32, f32, f32, i64, P, i64, P, sz, P], st),
         "q4k_lora_add": ([i32, i64, i64, i32, P, P, P, P, P, P, i64, i64, P, i64, P, sz, P], st),
     }
     for name in _SLOTS:
@@ -162,7 +165,7 @@ def _ptr(a):
 _SLOTS = {name: struct.Struct(form).pack for name, form in (
     ("q4k_kv_append", "=22q"), ("q4k_attn_decode", "=6q2d5qd3q"), ("q4k_kv_evict", "=14q"),
     ("q4k_norm_residual", "=7qd2qd7qd3q"), ("q4k_sample", "=12q"), ("q4k_batch_plan", "=18q"),
-    ("q4k_norm_residual_x8", "=7qd2qd7qd5q"), ("q4k_lora_add", "=17q"))}
+    ("q4k_norm_residual_x8", "=7qd2qd7qd5q"), ("q4k_lora_add", "=17q"), ("q4k_attn_chunk", "=7q2d6q"))}
 
 
 def _adr(a):
@@ -177,7 +180,8 @@ def _cache(c):
     return 0 if c is None else ctypes.addressof(c)
 
 
-_pack_append, _pack_attn, _pack_evict, _pack_norm, _pack_sample, _pack_plan, _pack_norm8, _pack_lora = _SLOTS.values()
+(_pack_append, _pack_attn, _pack_evict, _pack_norm, _pack_sample, _pack_plan, _pack_norm8, _pack_lora,
+ _pack_chunk) = _SLOTS.values()
 
 _current_stream = None
 
@@ -440,3 +444,16 @@ def q4k_lora_add(n_adapters: int, N: int, K: int, R: int, a, b, ranks, scales, i
     _check(load().q4k_lora_add_slots(_pack_lora(
         n_adapters, N, K, R, _adr(a), _adr(b), _adr(ranks), _adr(scales), _adr(ids), _adr(x), T, ldx, _adr(y), ldy, _adr(ws),
         ws_bytes, _adr(_stream(stream)))), "q4k_lora_add")
+
+
+def q4k_attn_chunk_workspace_size(cache, T: int, n_heads: int) -> int:
+    return load().q4k_attn_chunk_workspace_size(cache, T, n_heads)
+
+
+def q4k_attn_chunk(cache, starts, seq_lens, q, T: int, ldq: int, n_heads: int, scale: float, softcap: float, window: int, o,
+                   ldo: int, ws, ws_bytes: int, stream=None) -> None:
+    """Attention of a chunk of new tokens of every sequence (rows starts[b] .. starts[b+1] - 1 of q and o, bf16 [T][ld]) over
+    its paged cache."""
+    _check(load().q4k_attn_chunk_slots(_pack_chunk(
+        _cache(cache), _adr(starts), _adr(seq_lens), _adr(q), T, ldq, n_heads, scale, softcap, window, _adr(o), ldo, _adr(ws),
+        ws_bytes, _adr(_stream(stream)))), "q4k_attn_chunk")

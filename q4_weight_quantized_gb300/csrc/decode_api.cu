@@ -178,6 +178,35 @@ q4k_status norm_residual(int64_t M, int64_t D, const float *y, int64_t ldy, int 
 // the running sums of pages, and the free list's lengths
 size_t plan_ws(const q4k_kv_cache *c) { return align256(((size_t)c->batch + 1) * 4) * 2 + 256; }
 
+bool chunk_shape_ok(const q4k_kv_cache *c, int64_t T, int32_t n_heads) {
+    return cache_shape_ok(c) && n_heads >= 1 && n_heads % c->n_kv_heads == 0 && n_heads / c->n_kv_heads <= 1024 && T >= 1 &&
+           T < kInt31 && T * n_heads < kInt31;
+}
+
+struct ChunkLayout {
+    size_t seq_at, rt_at, rt_seq, place_at, head, parts, part_ml, total;
+};
+ChunkLayout chunk_layout(const q4k_kv_cache *c, int64_t T, int32_t n_heads) {
+    const size_t rows = (size_t)chunk_rows(c->head_dim);
+    const size_t tiles = (size_t)T * (n_heads / c->n_kv_heads) / rows + (size_t)(c->batch < T ? c->batch : T) + 1;
+    ChunkLayout l;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t from = at;
+        at += align256(bytes);
+        return from;
+    };
+    l.seq_at = take(((size_t)c->batch + 1) * 4);
+    l.rt_at = take(((size_t)c->batch + 1) * 4);
+    l.rt_seq = take(tiles * 4);
+    l.place_at = take((tiles + 1) * 8);
+    l.head = take(3 * 8);
+    l.part_ml = take((size_t)2 * kMaxChunkShares * rows * sizeof(float2));
+    l.parts = take((size_t)2 * kMaxChunkShares * rows * c->head_dim * 4);
+    l.total = at;
+    return l;
+}
+
 bool lora_shape_ok(int32_t n_adapters, int64_t N, int64_t K, int32_t R, int64_t T) {
     return n_adapters >= 1 && n_adapters <= 1024 && N >= 1 && N <= (1 << 21) && K >= 8 && K <= (1 << 21) && K % 8 == 0 && R >= 8 &&
            R <= 128 && R % 8 == 0 && T >= 1 && T <= (1 << 23);
@@ -448,6 +477,48 @@ q4k_status q4k_lora_add(int32_t n_adapters, int64_t N, int64_t K, int32_t R, con
     return finish(launch_lora_add(di, c, static_cast<cudaStream_t>(stream)));
 }
 
+size_t q4k_attn_chunk_workspace_size(const q4k_kv_cache *cache, int64_t T, int32_t n_heads) {
+    return cache && chunk_shape_ok(cache, T, n_heads) ? chunk_layout(cache, T, n_heads).total : 0;
+}
+
+q4k_status q4k_attn_chunk(const q4k_kv_cache *cache, const int32_t *starts, const int32_t *seq_lens, const uint16_t *q,
+                          int64_t T, int64_t ldq, int32_t n_heads, float scale, float softcap, int64_t window,
+                          uint16_t *o, int64_t ldo, void *ws, size_t ws_bytes, void *stream) {
+    q4k_status st = cache_check(cache);
+    if (st != Q4K_OK) return st;
+    if (!starts || !seq_lens || !q || !o || !ws) return Q4K_ERR_NULL;
+    if (!chunk_shape_ok(cache, T, n_heads) || ldq < (int64_t)n_heads * cache->head_dim || ldo < (int64_t)n_heads * cache->head_dim ||
+        window < 0 || !std::isfinite(scale) || !(softcap >= 0.f) || !std::isfinite(softcap))
+        return Q4K_ERR_SHAPE;
+    if (!aligned(starts, 4) || !aligned(seq_lens, 4) || !aligned(q, 16) || !aligned(o, 16) || ldq % 8 || ldo % 8 || !aligned(ws, 256))
+        return Q4K_ERR_ALIGN;
+    const ChunkLayout l = chunk_layout(cache, T, n_heads);
+    if (ws_bytes < l.total) return Q4K_ERR_WORKSPACE;
+    DeviceInfo di;
+    if ((st = check_device(&di)) != Q4K_OK) return st;
+    ChunkArgs a = {};
+    a.c = view(cache, di);
+    a.starts = starts, a.seq_lens = seq_lens;
+    a.q = q, a.T = T, a.ldq = ldq, a.o = o, a.ldo = ldo;
+    a.group = n_heads / cache->n_kv_heads;
+    a.window = window < kInt31 ? window : 0;  // no sequence is that long
+    a.q_sign = scale < 0.f ? 0x80008000u : 0u;
+    a.q_zero = scale == 0.f;
+    a.scale_log2 = a.q_zero ? 1.f : std::fabs(scale) * cache->k_scale * 1.4426950408889634f;
+    a.softcap = softcap;
+    a.cap_in = softcap > 0.f ? 2.f / softcap : 0.f;
+    a.v_scale = cache->v_scale;
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    a.seq_at = reinterpret_cast<int32_t *>(base + l.seq_at);
+    a.rt_at = reinterpret_cast<int32_t *>(base + l.rt_at);
+    a.rt_seq = reinterpret_cast<int32_t *>(base + l.rt_seq);
+    a.place_at = reinterpret_cast<int64_t *>(base + l.place_at);
+    a.head = reinterpret_cast<int64_t *>(base + l.head);
+    a.part_ml = reinterpret_cast<float2 *>(base + l.part_ml);
+    a.parts = reinterpret_cast<float *>(base + l.parts);
+    return finish(launch_attn_chunk(di, a, static_cast<cudaStream_t>(stream)));
+}
+
 // What the Python package calls.
 q4k_status q4k_kv_append_slots(const void *slots) { return call(q4k_kv_append, slots); }
 q4k_status q4k_attn_decode_slots(const void *slots) { return call(q4k_attn_decode, slots); }
@@ -457,5 +528,6 @@ q4k_status q4k_sample_slots(const void *slots) { return call(q4k_sample, slots);
 q4k_status q4k_batch_plan_slots(const void *slots) { return call(q4k_batch_plan, slots); }
 q4k_status q4k_norm_residual_x8_slots(const void *slots) { return call(q4k_norm_residual_x8, slots); }
 q4k_status q4k_lora_add_slots(const void *slots) { return call(q4k_lora_add, slots); }
+q4k_status q4k_attn_chunk_slots(const void *slots) { return call(q4k_attn_chunk, slots); }
 
 }  // extern "C"

@@ -128,6 +128,34 @@ struct PlanArgs {
 };
 cudaError_t launch_batch_plan(const DeviceInfo &di, const PlanArgs &a, cudaStream_t s);
 
+constexpr int kMaxChunkShares = 160;  // CTAs of an attention call over chunks, at most (the workspace holds two parts for each)
+struct ChunkArgs {
+    KvView c;
+    const int32_t *starts, *seq_lens;
+    const uint16_t *q;
+    int64_t T, ldq;
+    uint16_t *o;
+    int64_t ldo;
+    int32_t group;
+    int64_t window;
+    float scale_log2;             // |scale| * k_scale * log2(e)
+    uint32_t q_sign;              // flips the signs of a pair of 16-bit values, for a negative scale
+    int32_t q_zero;               // a scale of 0
+    float softcap, cap_in;        // and 2 / softcap
+    float v_scale;
+    int32_t shares;
+    // workspace
+    int32_t *seq_at;              // [batch + 1]: first row of each sequence
+    int32_t *rt_at;               // [batch + 1]: row tiles before each sequence
+    int32_t *rt_seq;              // [row tiles]
+    int64_t *place_at;            // [row tiles + 1]: places of the list before each row tile, of one KV head
+    int64_t *head;                // places, row tiles, shares
+    float *parts;                 // [2 * shares][rows][D]
+    float2 *part_ml;              // [2 * shares][rows]
+};
+int chunk_rows(int D);            // rows of a row tile
+cudaError_t launch_attn_chunk(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s);
+
 constexpr int kLoraSmall = 192;  // tokens of a call whose CTAs find their adapters' tokens themselves
 struct LoraArgs {
     int32_t n_adapters, R;

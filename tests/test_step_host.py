@@ -24,9 +24,26 @@ def lora(lib, n=4, N=64, K=64, R=16, a=A, b=A, ranks=A, scales=A, ids=A, x=A, T=
     return lib.q4k_lora_add(n, N, K, R, a, b, ranks, scales, ids, x, T, ldx, y, ldy, ws, ws_bytes, None)
 
 
+def chunk(lib, c=None, starts=A, lens=A, q=A, T=8, ldq=512, n_heads=4, scale=0.1, softcap=0.0, window=0, o=A, ldo=512, ws=A,
+          ws_bytes=1 << 30):
+    return lib.q4k_attn_chunk(ctypes.byref(c or cache()), starts, lens, q, T, ldq, n_heads, scale, softcap, window, o, ldo, ws,
+                              ws_bytes, None)
+
+
+@pytest.mark.parametrize("call", [plan, chunk])
 @pytest.mark.parametrize("change,status", BAD_CACHE)
-def test_bad_cache(lib, change, status):  # noqa: F811
-    assert plan(lib, c=cache(**change)) == status
+def test_bad_cache(lib, call, change, status):  # noqa: F811
+    assert call(lib, c=cache(**change)) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(starts=None), N), (dict(lens=None), N), (dict(q=None), N), (dict(o=None), N), (dict(ws=None), N), (dict(T=0), S),
+    (dict(T=1 << 31), S), (dict(T=1 << 29), S), (dict(n_heads=3), S), (dict(n_heads=0), S), (dict(ldq=511), S), (dict(ldo=504), S),
+    (dict(n_heads=2050, ldq=1 << 19, ldo=1 << 19), S), (dict(scale=float("nan")), S), (dict(softcap=-1.0), S),
+    (dict(softcap=float("inf")), S), (dict(window=-1), S), (dict(q=A + 8), L), (dict(o=A + 4), L), (dict(ldq=516), L),
+    (dict(ldo=514), L), (dict(ws=A + 16), L), (dict(lens=A + 1), L), (dict(starts=A + 2), L), (dict(ws_bytes=1000), W)])
+def test_chunk_refusals(lib, change, status):  # noqa: F811
+    assert chunk(lib, **change) == status
 
 
 @pytest.mark.parametrize("change,status", [
@@ -62,6 +79,12 @@ def test_workspaces(lib):  # noqa: F811
     assert lib.q4k_batch_plan_workspace_size(None) == 0
     assert lib.q4k_batch_plan_workspace_size(ctypes.byref(cache(head_dim=96))) == 0
     assert lib.q4k_batch_plan_workspace_size(ctypes.byref(cache())) % 256 == 0
+    c = ctypes.byref(cache())
+    a = lib.q4k_attn_chunk_workspace_size(c, 8, 4)
+    assert a > 0 and a % 256 == 0 and lib.q4k_attn_chunk_workspace_size(c, 1 << 20, 4) >= a + (1 << 20) * 2 // 256 * 12
+    for bad in ((0, 4), (8, 3), (1 << 31, 4), (8, 0)):
+        assert lib.q4k_attn_chunk_workspace_size(c, *bad) == 0
+    assert lib.q4k_attn_chunk_workspace_size(None, 8, 4) == 0
     assert lib.q4k_lora_add_workspace_size(4, 64, 64, 16, 8) >= 8 * 16 * 4
     assert lib.q4k_lora_add_workspace_size(4, 64, 64, 16, 1000) >= 1000 * (16 + 1) * 4
     for bad in ((0, 64, 64, 16, 8), (4, 0, 64, 16, 8), (4, 64, 60, 16, 8), (4, 64, 64, 15, 8), (4, 64, 64, 16, 0)):
@@ -69,6 +92,6 @@ def test_workspaces(lib):  # noqa: F811
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device status; a GPU is present")
-@pytest.mark.parametrize("call", [plan, norm8, lora])
+@pytest.mark.parametrize("call", [plan, norm8, lora, chunk])
 def test_no_device(lib, call):  # noqa: F811
     assert call(lib) == q4k.Q4K_ERR_DEVICE
