@@ -13,7 +13,8 @@
 //     lies in the cache: its slots are the K axis, so B is MN-major).  While one tile's warps do the softmax the tensor
 //     cores work for the other tile.
 //   - The running maximum moves only when a score exceeds it by 2^8; only then is O rescaled, by the softmax's own
-//     threads: S of a tile is there only after the O of the tile before.  (Heads of 256: one tile of rows, two buffers
+//     threads: S of a tile is there only after the O of the tile before.  So a tile's weights are taken by the maximum of
+//     the tiles before, in the one pass that finds its own maximum, which counts from the next tile on.  (Heads of 256: one tile of rows, two buffers
 //     of S instead; there the rare rescale waits for the product before.)
 //   - Work is one list of places (KV head, unit, tile of slots) cut into equal contiguous shares, one per CTA, whatever
 //     the lengths are; units that a share does not hold as a whole leave (m, l, o') in the workspace for join_kernel.
@@ -30,7 +31,7 @@
 namespace q4k {
 namespace {
 
-constexpr int kThreads = 512;          // warps 0-3 and 4-7: softmax of a tile of rows each; 8: MMA; 12-15: copies
+constexpr int kThreads = 512;          // warps 0-3 and 4-7: softmax of a tile of rows each; 8, 9: MMA; 12-15: copies
 constexpr int kMmaWarp = 8, kCopyWarp = 12, kCopyWarps = 4;
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // together those of the launch: 2 * (184 + 72) = 4 * 128
 constexpr int kPlanThreads = 1024;
@@ -38,7 +39,8 @@ constexpr int kJoinWarps = 8;
 constexpr int kMetaRing = 8;           // tiles whose page masks are kept: more than the ring holds
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;          // how far (log2) a score may exceed the running maximum
-constexpr int kMinPlaces = 2;          // tiles of a share, at least
+constexpr float kFar = 4194304.f;      // maxima (log2) from which on their product's rounding counts
+constexpr int kExtra = 1;              // places of the list after a unit's tiles: the time of ending it and beginning the next
 
 template <int D_, bool E4M3_>
 struct Cfg {
@@ -52,6 +54,8 @@ struct Cfg {
     static constexpr int LAG = NS - 2;                 // of which so many may be on their way
     // weights in f16 are kept as 2^7 p, in o' and l alike: at most 2^15, and what lies below 2^-32 of the largest is lost
     static constexpr float LIFT = E4M3 ? 7.f : 0.f;
+    // how far (log2) a score may exceed the maximum that its tile's weights are taken by: what their type holds
+    static constexpr float JUMP = E4M3 ? kSlack : 64.f;
     static constexpr int QBYTES = ROWS * D * 2;
     static constexpr int MISC = 1024;
     static constexpr int SMEM = QBYTES + NS * SLOT + MISC + 1024;  // (+ slack to align the base)
@@ -60,20 +64,16 @@ struct Cfg {
     static_assert(O_COL + NT * D <= COLS && SMEM <= 227 * 1024, "fits");
 };
 
-// What every role needs to know of a unit and of its share's part of it.
-struct Unit {
-    int b, h, n, e0;          // sequence, KV head, new tokens, end of token 0's slots
-    int64_t q0;               // first row of the sequence in q and o
-    int row0, rows;           // rows of the unit within the sequence
-    int64_t base;             // its first tile of slots
-    int64_t tiles, lo, hi;    // number of them, and the share's
-    int end, begin;           // slots that any row sees
+// What every role needs to know of a unit (ChunkRecord, made by plan_kernel), and of its share's part of it.
+struct Unit : ChunkRecord {
+    int h;        // KV head
+    int lo, hi;   // the share's tiles of slots
     bool whole;
 };
 
 struct Walk {
     int64_t at, hi, places;
-    int h, rt;
+    int h, rt, units;
 };
 
 __device__ __forceinline__ int64_t share_at(int64_t total, int shares, int s) { return total / shares * s + total % shares * s / shares; }
@@ -93,42 +93,37 @@ __device__ __forceinline__ Walk walk_of(const ChunkArgs &a, int share) {
     w.places = __ldg(a.head);
     const int shares = (int)__ldg(a.head + 2);
     const int64_t total = w.places * a.c.heads;
+    w.units = (int)__ldg(a.head + 1);
     w.at = share < shares ? share_at(total, shares, share) : 0;
     w.hi = share < shares ? share_at(total, shares, share + 1) : 0;
     w.h = w.places > 0 ? (int)(w.at / w.places) : 0;
-    w.rt = w.at < w.hi ? find_rt(a, (int)__ldg(a.head + 1), w.at - w.h * w.places) : 0;
+    w.rt = w.at < w.hi ? find_rt(a, w.units, w.at - w.h * w.places) : 0;
     return w;
 }
 
-// The unit of row tile rt: everything but the share's part.
-template <typename C>
-__device__ __forceinline__ void unit_of(const ChunkArgs &a, int rt, Unit &u) {
-    u.b = __ldg(a.rt_seq + rt);
-    const int s0 = __ldg(a.seq_at + u.b);
-    u.n = __ldg(a.seq_at + u.b + 1) - s0;
-    u.q0 = s0;
-    const int len = min(max(__ldg(a.seq_lens + u.b), 0), a.c.capacity);
-    u.e0 = len - u.n + 1;
-    u.row0 = (rt - __ldg(a.rt_at + u.b)) * C::ROWS;
-    u.rows = min(C::ROWS, u.n * a.group - u.row0);
-    u.end = max(0, u.e0 + (u.row0 + u.rows - 1) / a.group);
-    const int64_t begin = (int64_t)u.e0 + u.row0 / a.group - a.window;
-    u.begin = a.window > 0 && begin > 0 ? (int)begin : 0;
-    u.base = u.begin / C::BN;
-    u.tiles = max((int64_t)1, ((int64_t)u.end + C::BN - 1) / C::BN - u.base);
+__device__ __forceinline__ void load_record(const ChunkArgs &a, int rt, ChunkRecord &r) {
+    const int4 *p = reinterpret_cast<const int4 *>(a.records + rt);
+    const int4 x = __ldg(p), y = __ldg(p + 1), z = __ldg(p + 2);
+    r.b = x.x, r.q0 = x.y, r.e0 = x.z, r.row0 = x.w;
+    r.rows = y.x, r.begin = y.y, r.end = y.z, r.base = y.w;
+    r.tiles = z.x, r.all_end = z.y, r.all_begin = z.z, r.pad = 0;
 }
 
 template <typename C>
 __device__ __forceinline__ bool next_unit(const ChunkArgs &a, Walk &w, Unit &u) {
-    if (w.at >= w.hi) return false;
-    unit_of<C>(a, w.rt, u);
-    u.h = w.h;
-    u.lo = w.at - w.h * w.places - __ldg(a.place_at + w.rt);
-    u.hi = min(u.tiles, u.lo + (w.hi - w.at));
-    u.whole = u.lo == 0 && u.hi == u.tiles;
-    w.at += u.hi - u.lo;
-    if (u.hi == u.tiles && ++w.rt == (int)__ldg(a.head + 1)) w.rt = 0, ++w.h;
-    return true;
+    while (w.at < w.hi) {
+        const int64_t first = w.h * w.places + __ldg(a.place_at + w.rt);
+        load_record(a, w.rt, u);
+        u.h = w.h;
+        const int length = u.tiles + kExtra, lo = (int)(w.at - first);
+        const int hi = w.hi - first < length ? (int)(w.hi - first) : length;
+        w.at += hi - lo;
+        if (hi == length && ++w.rt == w.units) w.rt = 0, ++w.h;
+        u.lo = lo, u.hi = min(hi, u.tiles);
+        u.whole = lo == 0 && u.hi == u.tiles;
+        if (u.lo < u.hi) return true;
+    }
+    return false;
 }
 
 // ---------------------------------------------------------------- the list
@@ -223,29 +218,38 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ChunkArgs a) {
         }
         b = lo;
     }
-    auto places = [&](int rt, int &of) {
+    auto record = [&](int rt, int &of, ChunkRecord &r) {
         while (a.rt_at[of + 1] <= rt) ++of;
-        const int n = a.seq_at[of + 1] - a.seq_at[of], len = min(max(__ldg(a.seq_lens + of), 0), a.c.capacity), e0 = len - n + 1;
-        const int row0 = (rt - a.rt_at[of]) * C::ROWS, rows = min(C::ROWS, n * a.group - row0);
-        const int end = max(0, e0 + (row0 + rows - 1) / a.group);
-        const int64_t begin = (int64_t)e0 + row0 / a.group - a.window;
-        return max((int64_t)1, ((int64_t)end + C::BN - 1) / C::BN - (a.window > 0 && begin > 0 ? begin : 0) / C::BN);
+        const int n = a.seq_at[of + 1] - a.seq_at[of], len = min(max(__ldg(a.seq_lens + of), 0), a.c.capacity);
+        r.b = of, r.q0 = a.seq_at[of], r.e0 = len - n + 1;
+        r.row0 = (rt - a.rt_at[of]) * C::ROWS;
+        r.rows = min(C::ROWS, n * a.group - r.row0);
+        const int first = r.row0 / a.group, last = (r.row0 + r.rows - 1) / a.group;  // tokens
+        auto begin = [&](int tok) { return a.window > 0 && (int64_t)r.e0 + tok > a.window ? (int)(r.e0 + tok - a.window) : 0; };
+        r.begin = begin(first), r.end = max(0, r.e0 + last);
+        r.all_begin = begin(last), r.all_end = max(0, r.e0 + first);
+        r.base = r.begin / C::BN;
+        r.tiles = max(1, (int)(((int64_t)r.end + C::BN - 1) / C::BN) - r.base);
+        r.pad = 0;
+        return r.tiles + kExtra;
     };
     int64_t sum = 0, all;
     int of = b;
-    for (int rt = rt0; rt < rt1; ++rt) sum += places(rt, of);
+    ChunkRecord r;
+    for (int rt = rt0; rt < rt1; ++rt) sum += record(rt, of, r);
     sum = plan_scan(sum, all, scratch);
     of = b;
     for (int rt = rt0; rt < rt1; ++rt) {
         a.place_at[rt] = sum;
-        sum += places(rt, of);
-        a.rt_seq[rt] = of;
+        sum += record(rt, of, r);
+        a.records[rt] = r;
     }
     if (tid == 0) {
         a.place_at[R] = all;
         a.head[0] = all;
         a.head[1] = R;
-        const int64_t most = all * a.c.heads / kMinPlaces;
+        // as many shares as there are CTAs; for less work one a unit or two tiles
+        const int64_t units = (int64_t)R * a.c.heads, most = max(units, (all * a.c.heads - kExtra * units) / 2);
         a.head[2] = most < 1 ? 1 : most < a.shares ? most : a.shares;
     }
     if (bad) atomicOr(a.c.status, kDevIndex);
@@ -318,6 +322,73 @@ struct Bars {
     uint32_t full, empty, s_full, p_full, o_full, q_full, pv_done, done;
 };
 
+// A thread's row of a unit: where it is, what it sees, and its query on the way into shared memory.
+template <typename C>
+struct Row {
+    static constexpr int CHUNKS = C::D / 8;
+    static constexpr bool HELD = C::D <= 128;  // in registers from load() to store() (of 256 values: read by store())
+    uint4 v[HELD ? CHUNKS : 1];
+    const uint4 *src;
+    int64_t q_row;
+    int head, e, bgn;     // sees the slots [bgn, e)
+    bool real;            // (the last tile of a sequence may have fewer rows)
+    float cc;             // a score's factor, to log2
+
+    __device__ __forceinline__ void of(const ChunkArgs &a, const Unit &u, int t, int row_in) {
+        const int row = u.row0 + t * 128 + row_in;
+        real = t * 128 + row_in < u.rows;
+        const int tok = real ? row / a.group : 0;
+        q_row = (int64_t)u.q0 + tok;
+        head = u.h * a.group + (real ? row - tok * a.group : 0);
+        e = real ? u.e0 + tok : 0;
+        bgn = a.window > 0 && e > a.window ? (int)(e - a.window) : 0;
+        src = reinterpret_cast<const uint4 *>(a.q + q_row * a.ldq + (int64_t)head * C::D);
+    }
+    __device__ __forceinline__ void load(const ChunkArgs &, const Unit &) {
+        if constexpr (HELD) {
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) v[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    __device__ __forceinline__ uint4 chunk(int c) const {
+        if constexpr (HELD) return v[c];
+        else return real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+    }
+    // into the swizzled row at `dst`
+    __device__ __forceinline__ void store(const ChunkArgs &a, uint32_t dst, int swizzle) {
+        float up = 1.f;
+        cc = a.scale_log2;
+        if constexpr (C::E4M3) {
+            // f16: a power of two takes the row's largest value to [2^14, 2^15)
+            uint32_t top = 0;
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) {
+                const uint4 w = chunk(c);
+                top = max(top, max(max(w.x << 16 & 0x7FFFFFFFu, w.x & 0x7FFF0000u), max(w.y << 16 & 0x7FFFFFFFu, w.y & 0x7FFF0000u)));
+                top = max(top, max(max(w.z << 16 & 0x7FFFFFFFu, w.z & 0x7FFF0000u), max(w.w << 16 & 0x7FFFFFFFu, w.w & 0x7FFF0000u)));
+            }
+            const int ex = (int)(top >> 23);
+            // (a row that is not finite gives NaN either way)
+            const int shift = ex == 255 ? 0 : min(127 + 14 - ex, 126);
+            up = __uint_as_float((uint32_t)(127 + shift) << 23);
+            cc *= __uint_as_float((uint32_t)(127 - shift) << 23);
+        }
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            uint4 w = chunk(c);
+            if constexpr (C::E4M3) {
+                const float s = a.q_sign ? -up : up;
+                w.x = pack_f16(lo_f32(w.x) * s, hi_f32(w.x) * s), w.y = pack_f16(lo_f32(w.y) * s, hi_f32(w.y) * s);
+                w.z = pack_f16(lo_f32(w.z) * s, hi_f32(w.z) * s), w.w = pack_f16(lo_f32(w.w) * s, hi_f32(w.w) * s);
+            } else {
+                w.x ^= a.q_sign, w.y ^= a.q_sign, w.z ^= a.q_sign, w.w ^= a.q_sign;
+            }
+            if (a.q_zero) w = make_uint4(0, 0, 0, 0);
+            sts128(dst + (c / 8) * (128 * 128) + ((c % 8) ^ swizzle) * 16, w);
+        }
+    }
+};
+
 template <typename C>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
     constexpr int D = C::D, BN = C::BN, NT = C::NT, NS = C::NS;
@@ -327,10 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
     uint8_t *const misc_p = base + C::QBYTES + NS * C::SLOT;
     Bars bar;
     bar.full = misc, bar.empty = bar.full + 8 * NS, bar.s_full = bar.empty + 8 * NS, bar.p_full = bar.s_full + 16;
-    bar.o_full = bar.p_full + 16, bar.q_full = bar.o_full + 16, bar.pv_done = bar.q_full + 16, bar.done = bar.pv_done + 8;
+    bar.o_full = bar.p_full + 16, bar.q_full = bar.o_full + 16, bar.pv_done = bar.q_full + 16, bar.done = bar.pv_done + 16;
     uint32_t *const tmem_holder = reinterpret_cast<uint32_t *>(misc_p + 512);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc_p + 516);
-    volatile uint32_t *const bad_unit = reinterpret_cast<volatile uint32_t *>(misc_p + 544);       // [8]
+    volatile int *const bad_seen = reinterpret_cast<volatile int *>(misc_p + 520);  // a value that is not finite was taken out
     volatile uint32_t *const page_mask = reinterpret_cast<volatile uint32_t *>(misc_p + 640);      // [kMetaRing][4]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int *const status = a.c.status;
@@ -338,18 +409,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(bar.full + 8 * i, kCopyWarps);
-            mbar_init(bar.empty + 8 * i, 1);
+            mbar_init(bar.empty + 8 * i, NT);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar.s_full + 8 * t, 1);
             mbar_init(bar.p_full + 8 * t, 4);
             mbar_init(bar.o_full + 8 * t, 1);
             mbar_init(bar.q_full + 8 * t, 4);
+            mbar_init(bar.pv_done + 8 * t, 1);
         }
-        mbar_init(bar.pv_done, 1);
-        mbar_init(bar.done, 1);
+        mbar_init(bar.done, 2);
         *abort_flag = 0;
-        for (int i = 0; i < 8; ++i) bad_unit[i] = 0;
+        *bad_seen = 0;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -371,66 +442,64 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
         const int t = warp >> 2, row_in = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t o_col = tmem + lanes + C::O_COL + t * D;
-        uint32_t s_count = 0, unit_phase = 0, seq = 0;  // tiles and units that this tile of rows has had, units walked
-        int64_t tile_count = 0;  // tiles of slots walked (index into the page masks)
-        bool ok = t < NT;
-        for (; ok && next_unit<C>(a, walk, u); ++seq) {
-            if (t * 128 >= u.rows) {
-                tile_count += u.hi - u.lo;
-                continue;
+        uint32_t s_count = 0, unit_phase = 0;  // tiles and units that this tile of rows has had
+        uint32_t tile_count = 0;               // tiles of slots walked (index into the page masks)
+        bool ok = true;
+        // the next unit that has rows in this tile
+        auto advance = [&](Unit &n) {
+            while (next_unit<C>(a, walk, n)) {
+                if (t * 128 < n.rows) return true;
+                tile_count += (uint32_t)(n.hi - n.lo);
             }
-            // ---- the row, and Q into shared memory
-            const int row = u.row0 + t * 128 + row_in;
-            const bool real = t * 128 + row_in < u.rows;
-            const int tok = real ? row / a.group : 0;
-            const int64_t q_row = u.q0 + tok;
-            const int head = u.h * a.group + (real ? row - tok * a.group : 0);
-            const int e = real ? u.e0 + tok : 0;
-            const int bgn = a.window > 0 && e > a.window ? (int)(e - a.window) : 0;
-            float cc = a.scale_log2;
-            {
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + q_row * a.ldq + (int64_t)head * D);
-                const uint32_t dst = q_smem + t * (128 * D * 2) + row_in * 128;
-                float up = 1.f;
-                if constexpr (C::E4M3) {
-                    // f16: a power of two takes the row's largest value to [2^14, 2^15)
-                    uint32_t top = 0;
-                    if (real)
-#pragma unroll 4
-                        for (int c = 0; c < D / 8; ++c) {
-                            const uint4 v = __ldg(src + c);
-                            top = max(top, max(max(v.x << 16 & 0x7FFFFFFFu, v.x & 0x7FFF0000u), max(v.y << 16 & 0x7FFFFFFFu, v.y & 0x7FFF0000u)));
-                            top = max(top, max(max(v.z << 16 & 0x7FFFFFFFu, v.z & 0x7FFF0000u), max(v.w << 16 & 0x7FFFFFFFu, v.w & 0x7FFF0000u)));
-                        }
-                    const int ex = (int)(top >> 23);
-                    // (a row that is not finite gives NaN either way)
-                    const int shift = ex == 255 ? 0 : min(127 + 14 - ex, 126);
-                    up = __uint_as_float((uint32_t)(127 + shift) << 23);
-                    cc *= __uint_as_float((uint32_t)(127 - shift) << 23);
-                }
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    uint4 v = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                    if constexpr (C::E4M3) {
-                        const float f = a.q_sign ? -up : up;
-                        v.x = pack_f16(lo_f32(v.x) * f, hi_f32(v.x) * f), v.y = pack_f16(lo_f32(v.y) * f, hi_f32(v.y) * f);
-                        v.z = pack_f16(lo_f32(v.z) * f, hi_f32(v.z) * f), v.w = pack_f16(lo_f32(v.w) * f, hi_f32(v.w) * f);
-                    } else {
-                        v.x ^= a.q_sign, v.y ^= a.q_sign, v.z ^= a.q_sign, v.w ^= a.q_sign;
-                    }
-                    if (a.q_zero) v = make_uint4(0, 0, 0, 0);
-                    sts128(dst + (c / 8) * (128 * 128) + ((c % 8) ^ (row_in & 7)) * 16, v);
-                }
-            }
+            return false;
+        };
+        Row<C> r;
+        bool more = t < NT && advance(u);
+        if (more) {
+            r.of(a, u, t, row_in);
+            r.load(a, u);
+            r.store(a, q_smem + t * (128 * D * 2) + row_in * 128, row_in & 7);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar.q_full + 8 * t);
+        }
+        while (more) {
             // ---- what the tile's rows see
-            const int last_row = min(t * 128 + 127, u.rows - 1) + u.row0;
-            const int64_t all_end = (int64_t)u.e0 + (u.row0 + t * 128) / a.group;               // every row sees slots below this ...
-            const int64_t all_begin = a.window > 0 ? (int64_t)u.e0 + last_row / a.group - a.window : 0;  // ... and from this on
-            float m = -INFINITY, l = 0.f;
-            for (int64_t i = u.lo; i < u.hi; ++i, ++tile_count) {
+            // every row of the tile sees slots below all_end and from all_begin on
+            const int last_tok = (min(t * 128 + 127, u.rows - 1) + u.row0) / a.group;
+            const uint32_t all_end = (uint32_t)max(0, u.e0 + (u.row0 + t * 128) / a.group);
+            const uint32_t all_begin = a.window > 0 && (int64_t)u.e0 + last_tok > a.window ? (uint32_t)(u.e0 + last_tok - a.window) : 0u;
+            const float f = a.softcap > 0.f ? 1.f : r.cc;
+            // neg: -m f, or 0 where there is no maximum yet (rows that are not there have one: 0)
+            float m = r.real ? -INFINITY : 0.f, l = 0.f, m_next = m, neg = 0.f;
+            bool far = false;
+            // the running maximum becomes m_next; O and l follow
+            auto raise = [&](bool has_o) {
+                const float neg_new = m_next == -INFINITY ? 0.f : -m_next * f;
+                const float fac = m == m_next || m == -INFINITY ? 1.f : ex2_approx(neg_new - neg);
+                m = m_next, neg = neg_new;
+                far = __any_sync(0xFFFFFFFFu, fabsf(neg) > kFar);
+                l *= fac;
+                if (!has_o) return true;
+                if constexpr (NT == 1) {  // the product before must have ended
+                    const uint32_t before = s_count - 2;  // (s_count counts this tile already)
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar.pv_done + 8 * (before & 1), before >> 1 & 1, status))) return false;
+                    tc_fence_after();
+                }
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(o_col + 32 * c, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fac);
+                    tmem_st16(o_col + 32 * c, *reinterpret_cast<uint32_t(*)[16]>(o));
+                    tmem_st16(o_col + 32 * c + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
+                }
+                tmem_st_wait();
+                return true;
+            };
+            for (int i = u.lo; i < u.hi; ++i, ++tile_count) {
                 // heads of 256: the two buffers in turn, each with its barriers
                 const uint32_t odd = s_count & 1, at = NT == 2 ? (uint32_t)t : odd, phase = NT == 2 ? odd : s_count >> 1 & 1;
                 ++s_count;
@@ -440,109 +509,135 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                 }
                 tc_fence_after();
                 const uint32_t s_col = tmem + lanes + C::S_COL + at * BN;
-                float s[BN];
-#pragma unroll
-                for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
-                tmem_ld_wait();
-                const int64_t j0 = (u.base + i) * BN;
-                float f = cc;
-                if (a.softcap > 0.f) {
-                    // c tanh(s / c) = c (1 - 2 / (1 + e^(2 s / c))), in units of log2
-                    const float in = a.cap_in * cc, out = a.softcap * kLog2e;
-#pragma unroll
-                    for (int k = 0; k < BN; ++k) s[k] = fmaf(-2.f * out, rcp_approx(1.f + ex2_approx(s[k] * in)), out);
-                    f = 1.f;
-                }
+                const uint32_t j0 = (uint32_t)(u.base + i) * BN;
                 const volatile uint32_t *mask = page_mask + (tile_count & (kMetaRing - 1)) * 4;
-                uint32_t pages = 0xFFFFFFFFu;
+                uint32_t pages = mask[0];
 #pragma unroll
-                for (int w = 0; w < BN / 32; ++w) pages &= mask[w];
-                if (j0 + BN > all_end || j0 < all_begin || pages != 0xFFFFFFFFu) {
-                    const int from = (int)max((int64_t)0, bgn - j0), to = (int)min((int64_t)BN, e - j0);
-#pragma unroll
-                    for (int w = 0; w < BN / 32; ++w) {
-                        const uint32_t there = mask[w];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * w + k < from || 32 * w + k >= to || !(there >> k & 1u)) s[32 * w + k] = -INFINITY;
-                    }
+                for (int w = 1; w < BN / 32; ++w) pages &= mask[w];
+                const bool masked = j0 + BN > all_end || j0 < all_begin || pages != 0xFFFFFFFFu;
+                if (__any_sync(0xFFFFFFFFu, m_next != m) && !raise(i > u.lo)) {
+                    ok = false;
+                    break;
                 }
-                float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                for (int k = 4; k < BN; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
-                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                // a new maximum: rows that had none take theirs, others when it is 2^8 above
-                const bool up = m == -INFINITY ? mx > -INFINITY : (mx - m) * f > kSlack;
-                if (__any_sync(0xFFFFFFFFu, up)) {
-                    const float fac = !up ? 1.f : m == -INFINITY ? 0.f : ex2_approx((m - mx) * f);
-                    if (up) m = mx;
-                    l *= fac;
-                    if (i > u.lo) {
-                        if constexpr (NT == 1) {  // the product before must have ended (it is the pv_done phase before this tile's)
-                            if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar.pv_done, odd ^ 1, status))) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                        }
-#pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t o[16];
-                            asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                                         : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
-                                           "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                                         : "r"(o_col + 16 * c)
-                                         : "memory");
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fac);
-                            tmem_st16(o_col + 16 * c, o);
-                        }
-                        tmem_st_wait();
-                    }
-                }
-                const float m0 = m == -INFINITY ? 0.f : m, neg = -m0 * f;
-                if (__any_sync(0xFFFFFFFFu, fabsf(neg) > 65536.f)) {  // (m0 f's rounding would count)
-#pragma unroll
-                    for (int k = 0; k < BN; ++k) s[k] = ex2_approx(fmaf(s[k] - m0, f, C::LIFT));
-                } else {
+                // ---- the usual tile: weights by the maximum so far, in one pass; a larger one counts from the next tile on
+                bool done = false;
+                if (!masked && i > u.lo && a.softcap == 0.f && !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY)) {
+                    uint32_t p[BN / 2];
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    float top[2] = {-INFINITY, -INFINITY};
                     const float2 f2 = make_float2(f, f), n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
+                    uint32_t s[2][32];
+                    tmem_ld32(s_col, s[0]);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < BN; k += 2) {
-                        const float2 z = fma2(make_float2(s[k], s[k + 1]), f2, n2);
-                        s[k] = ex2_approx(z.x), s[k + 1] = ex2_approx(z.y);
+                    for (int c = 0; c < BN / 32; ++c) {
+                        if (c + 1 < BN / 32) tmem_ld32(s_col + 32 * (c + 1), s[(c + 1) & 1]);
+                        const uint32_t (&v)[32] = s[c & 1];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float x = __uint_as_float(v[k]), y = __uint_as_float(v[k + 1]);
+                            top[k / 2 & 1] = fmaxf(fmaxf(top[k / 2 & 1], x), y);
+                            const float2 z = fma2(make_float2(x, y), f2, n2);
+                            const float2 e = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+                            sum[k / 2 & 1] = add2(sum[k / 2 & 1], e);
+                            p[16 * c + k / 2] = C::E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+                        }
+                        if (c + 1 < BN / 32) tmem_ld_wait();
+                    }
+                    const float mx = fmaxf(top[0], top[1]), above = (mx - m) * f;
+                    done = !__any_sync(0xFFFFFFFFu, above > C::JUMP);
+                    if (done) {
+                        if (above > kSlack) m_next = mx;
+                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+#pragma unroll
+                        for (int c = 0; c < BN / 32; ++c) tmem_st16(s_col + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(p + 16 * c));
                     }
                 }
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                if (!done) {
+                    // ---- two passes: the maximum of what a row sees, then the weights
+                    const int from = (int)max((int64_t)0, (int64_t)r.bgn - j0), to = (int)min((int64_t)BN, (int64_t)r.e - j0);
+                    const float in = a.cap_in * r.cc, out = a.softcap * kLog2e;
+                    auto scores = [&](int c, float (&s)[32]) {
+                        tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s));
+                        uint32_t there = 0xFFFFFFFFu;
+                        if (masked) {
+                            there = mask[c];
+                            const int lo = from - 32 * c, hi = to - 32 * c;
+                            there &= lo <= 0 ? 0xFFFFFFFFu : lo >= 32 ? 0u : 0xFFFFFFFFu << lo;
+                            there &= hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
+                        }
+                        tmem_ld_wait();
+                        if (a.softcap > 0.f) {
+                            // c tanh(s / c) = c (1 - 2 / (1 + e^(2 s / c))), in units of log2
 #pragma unroll
-                for (int c = 0; c < BN / 32; ++c) {
-                    uint32_t p[16];
+                            for (int k = 0; k < 32; ++k) s[k] = fmaf(-2.f * out, rcp_approx(1.f + ex2_approx(s[k] * in)), out);
+                        }
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float x = s[32 * c + 2 * k], y = s[32 * c + 2 * k + 1];
-                        sum[k & 1] = add2(sum[k & 1], make_float2(x, y));
-                        p[k] = C::E4M3 ? pack_f16(x, y) : pack_bf16(x, y);
+                        for (int k = 0; k < 32; ++k) s[k] = there >> k & 1u ? s[k] : -INFINITY;
+                    };
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < BN / 32; ++c) {
+                        float s[32];
+                        scores(c, s);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) mx = fmaxf(fmaxf(mx, s[k]), s[k + 1]);
                     }
-                    tmem_st16(s_col + 16 * c, p);
+                    if (m == -INFINITY ? mx > -INFINITY : (mx - m) * f > kSlack) m_next = mx;
+                    if (__any_sync(0xFFFFFFFFu, m_next != m) && !raise(i > u.lo)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < BN / 32; ++c) {  // (a group's weights lie over scores that have been read)
+                        float s[32];
+                        uint32_t p[16];
+                        scores(c, s);
+                        const float m0 = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) s[k] = ex2_approx(far ? fmaf(s[k] - m0, f, C::LIFT) : fmaf(s[k], f, neg + C::LIFT));
+                        float part[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            part[0] += s[2 * k], part[1] += s[2 * k + 1];
+                            p[k] = C::E4M3 ? pack_f16(s[2 * k], s[2 * k + 1]) : pack_bf16(s[2 * k], s[2 * k + 1]);
+                        }
+                        l += part[0] + part[1];
+                        tmem_st16(s_col + 16 * c, p);
+                    }
                 }
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar.p_full + 8 * at);
             }
             if (!ok) break;
-            // ---- the unit's end
+            // ---- the unit's end; the next one's queries are on their way meanwhile, and its first scores
+            const Unit of = u;
+            const int64_t q_row = r.q_row;
+            const int head = r.head, e = r.e, bgn = r.bgn;
+            const bool real = r.real;
+            more = advance(u);
+            if (more) {
+                r.of(a, u, t, row_in);
+                r.load(a, u);
+            }
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar.o_full + 8 * t, unit_phase, status))) {
                 ok = false;
                 break;
             }
             unit_phase ^= 1;
             tc_fence_after();
-            const bool bad = bad_unit[seq & 7] == seq + 1;
+            if (more) {
+                r.store(a, q_smem + t * (128 * D * 2) + row_in * 128, row_in & 7);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar.q_full + 8 * t);
+            }
+            const bool bad = *bad_seen != 0;
             // a row that sees slots, all of them -infinity, has no weights: NaN, as 0 / 0 has it
             const float inv = e > bgn ? a.v_scale / l : 0.f;
-            float *const part = a.parts + ((int64_t)(2 * blockIdx.x + (u.lo > 0 ? 0 : 1)) * C::ROWS + t * 128 + row_in) * D;
+            const int64_t part_row = (int64_t)(2 * blockIdx.x + (of.lo > 0 ? 0 : 1)) * C::ROWS + t * 128 + row_in;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -550,17 +645,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                 tmem_ld_wait();
                 if (bad && real) {
                     // values that are not finite in tiles that not every row of the unit sees (the copies took them out)
-                    for (int64_t i = u.lo; i < u.hi; ++i) {
-                        const int64_t j0 = (u.base + i) * BN;
-                        const int64_t unit_end = (int64_t)u.e0 + u.row0 / a.group;
-                        const int64_t unit_begin = a.window > 0 ? (int64_t)u.e0 + (u.row0 + u.rows - 1) / a.group - a.window : 0;
-                        if (j0 + BN <= unit_end && j0 >= unit_begin) continue;
+                    for (int i = of.lo; i < of.hi; ++i) {
+                        const int64_t j0 = (int64_t)(of.base + i) * BN;
+                        if (j0 + BN <= of.all_end && j0 >= of.all_begin) continue;
                         const int64_t to = min((int64_t)e, j0 + BN);
                         for (int64_t j = max((int64_t)bgn, j0); j < to; ++j) {
                             const uint32_t pg = page_of(a.c, (uint32_t)j);
-                            const int32_t page = __ldg(a.c.table + u.b * a.c.ld_table + pg);
+                            const int32_t page = __ldg(a.c.table + of.b * a.c.ld_table + pg);
                             if (!page_ok(a.c, page)) continue;
-                            const uint8_t *v = a.c.v + row_bytes_at(a.c, page, u.h, (uint32_t)j - pg * a.c.page_size);
+                            const uint8_t *v = a.c.v + row_bytes_at(a.c, page, of.h, (uint32_t)j - pg * a.c.page_size);
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
                                 float x;
@@ -572,120 +665,127 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                     }
                 }
                 if (!real) continue;
-                if (u.whole) {
+                if (of.whole) {
                     uint4 *dst = reinterpret_cast<uint4 *>(a.o + q_row * a.ldo + (int64_t)head * D + 32 * c);
 #pragma unroll
                     for (int k = 0; k < 32; k += 8) {
                         uint32_t w[4];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const float p = __uint_as_float(o[k + 2 * x]) * inv, q = __uint_as_float(o[k + 2 * x + 1]) * inv;
-                            w[x] = e > bgn ? pack_bf16(p, q) : 0u;
+                            const float y = __uint_as_float(o[k + 2 * x]) * inv, z = __uint_as_float(o[k + 2 * x + 1]) * inv;
+                            w[x] = e > bgn ? pack_bf16(y, z) : 0u;
                         }
                         dst[k / 8] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(part + 32 * c);
+                    uint4 *dst = reinterpret_cast<uint4 *>(a.parts + part_row * D + 32 * c);
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) dst[k / 4] = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                 }
             }
-            if (!u.whole && real)
-                a.part_ml[(int64_t)(2 * blockIdx.x + (u.lo > 0 ? 0 : 1)) * C::ROWS + t * 128 + row_in] =
-                    make_float2(m == -INFINITY ? -INFINITY : m * (a.softcap > 0.f ? 1.f : cc), l);
+            if (!of.whole && real) a.part_ml[part_row] = make_float2(m == -INFINITY ? -INFINITY : -neg, l);
             tc_fence_before();
         }
-        if (!ok && t < NT && lane == 0) *abort_flag = 1;
+        if (!ok && lane == 0) *abort_flag = 1;
     } else if (warp < kCopyWarp) {
         set_regs_down<kOtherRegs>();
-        if (warp == kMmaWarp && lane == 0) {
+        if (warp < kMmaWarp + 2 && elect_one()) {
             // ---------------------------------------------------- MMA
+            // Two warps, as one thread does not issue fast enough for the tensor cores: one for each tile of rows, or,
+            // for heads of 256, one for each product.
             constexpr uint32_t kQk = idesc_of(128, BN, C::E4M3, false), kPv = idesc_of(128, D, C::E4M3, true);
-            uint32_t used = 0;               // tiles of the ring consumed or being consumed
-            uint32_t p_phase[2] = {0, 0};    // of the tiles of rows, or of the two buffers
-            uint32_t count = 0;              // tiles of slots walked
+            const int t = NT == 2 ? warp - kMmaWarp : 0;
+            const bool qks = NT == 2 || warp == kMmaWarp, pvs = NT == 2 || warp != kMmaWarp;
+            const uint64_t q_desc = umma_desc_sw128(q_smem + t * (128 * D * 2)), k_desc = umma_desc_sw128(ring), v_desc = desc_mn(ring, BN * 128);
+            const uint32_t s_at = tmem + C::S_COL + t * BN, o_at = tmem + C::O_COL + t * D;
+            uint32_t slot = 0, full_phase = 0;  // the ring tile that is next
+            uint32_t phase = 0, unit_phase = 0; // of p_full (NT 2); of q_full
+            uint32_t count = 0;                 // tiles of slots done (NT 1: buffers and their phases go by it)
             bool ok = true;
-            auto slot_of = [&](uint32_t n) { return n % NS; };
-            auto wait_full = [&](uint32_t n) {
-                const bool r = mbar_wait(bar.full + 8 * slot_of(n), (n / NS) & 1, status);
+            auto wait_full = [&] {
+                const bool r = mbar_wait(bar.full + 8 * slot, full_phase, status);
                 tc_fence_after();
                 return r;
             };
-            auto qk = [&](int t, uint32_t n, int s_at) {
-                const uint64_t qd = umma_desc_sw128(q_smem + t * (128 * D * 2)), kd = umma_desc_sw128(ring + slot_of(n) * C::SLOT);
+            auto free_slot = [&](bool used) {  // once what was issued has read it
+                if (used) umma_commit(bar.empty + 8 * slot);
+                else if (NT == 2) mbar_arrive(bar.empty + 8 * slot);
+                if (++slot == NS) slot = 0, full_phase ^= 1;
+            };
+            auto qk = [&](uint32_t buf) {
+                const uint64_t kd = k_desc + (uint64_t)(slot * (C::SLOT >> 4));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma_bf16(tmem + C::S_COL + s_at * BN, qd + (k / 4) * (128 * 128 >> 4) + 2 * (k % 4),
-                              kd + (k / 4) * (BN * 128 >> 4) + 2 * (k % 4), kQk, k != 0);
+                    umma_bf16(s_at + buf * BN, q_desc + (k / 4) * (128 * 128 >> 4) + 2 * (k % 4), kd + (k / 4) * (BN * 128 >> 4) + 2 * (k % 4),
+                              kQk, k != 0);
             };
-            auto pv = [&](int t, uint32_t n, int s_at, bool first) {
-                const uint64_t vd = desc_mn(ring + slot_of(n) * C::SLOT, BN * 128);
+            auto pv = [&](uint32_t buf, bool first) {
+                const uint64_t vd = v_desc + (uint64_t)(slot * (C::SLOT >> 4));
 #pragma unroll
                 for (int k = 0; k < BN / 16; ++k)
-                    umma_bf16_ts(tmem + C::O_COL + t * D, tmem + C::S_COL + s_at * BN + 8 * k, vd + k * (16 * 128 >> 4), kPv,
-                                 !first || k != 0);
+                    umma_bf16_ts(o_at, s_at + buf * BN + 8 * k, vd + k * (16 * 128 >> 4), kPv, !first || k != 0);
             };
-            uint32_t q_phase[2] = {0, 0};
             while (ok && next_unit<C>(a, walk, u)) {
-                const int nt = u.rows > 128 ? 2 : 1;
-                const int64_t tiles = u.hi - u.lo;
-                for (int t = 0; t < nt && ok; ++t) {
-                    ok = mbar_wait(bar.q_full + 8 * t, q_phase[t], status);
-                    q_phase[t] ^= 1;
-                }
-                if (!ok || !(ok = wait_full(used)) || *abort_flag) {
+                const int tiles = u.hi - u.lo;
+                if (*abort_flag) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                // the ring holds the unit's keys and values in turn: tile i at used + 2 i and used + 2 i + 1
-                for (int t = 0; t < nt; ++t) {
-                    const int at = NT == 2 ? t : (int)(count & 1);
-                    qk(t, used, at);
-                    umma_commit(bar.s_full + 8 * at);
+                if (NT == 2 && t * 128 >= u.rows) {  // no rows in this tile: its share of letting go of keys and values
+                    for (int i = 0; i < 2 * tiles && ok; ++i) {
+                        ok = wait_full();
+                        if (ok) free_slot(false);
+                    }
+                    continue;
                 }
-                umma_commit(bar.empty + 8 * slot_of(used));
-                for (int64_t i = 0; i < tiles && ok; ++i) {
-                    const uint32_t kn = used + 2 * (uint32_t)i + 2, vn = used + 2 * (uint32_t)i + 1;
-                    const bool more = i + 1 < tiles;
-                    if constexpr (NT == 1) {
-                        // the next scores into the other buffer, then this tile's product
-                        if (more) {
-                            if (!(ok = wait_full(kn))) break;
-                            const int next = (int)((count + i + 1) & 1);
-                            qk(0, kn, next);
-                            umma_commit(bar.s_full + 8 * next);
-                            umma_commit(bar.empty + 8 * slot_of(kn));
-                        }
-                        const int at = (int)((count + i) & 1);
-                        if (!(ok = mbar_wait(bar.p_full + 8 * at, p_phase[at], status)) || !(ok = wait_full(vn))) break;
-                        p_phase[at] ^= 1;
-                        pv(0, vn, at, i == 0);
-                        umma_commit(bar.pv_done);
-                        umma_commit(bar.empty + 8 * slot_of(vn));
-                        if (!more) umma_commit(bar.o_full);
-                    } else {
-                        for (int t = 0; t < nt && ok; ++t) {
-                            if (!(ok = mbar_wait(bar.p_full + 8 * t, p_phase[t], status))) break;
-                            p_phase[t] ^= 1;
-                            if (t == 0 && !(ok = wait_full(vn))) break;
+                if (qks) {
+                    if (!(ok = mbar_wait(bar.q_full + 8 * t, unit_phase, status))) break;
+                    unit_phase ^= 1;
+                }
+                if constexpr (NT == 2) {
+                    // the ring holds keys and values in turn: K(0) V(0) K(1) V(1) ...
+                    if (!(ok = wait_full())) break;
+                    qk(0);
+                    umma_commit(bar.s_full + 8 * t);
+                    free_slot(true);
+                    for (int i = 0; i < tiles; ++i) {
+                        if (!(ok = mbar_wait(bar.p_full + 8 * t, phase, status))) break;
+                        phase ^= 1;
+                        if (!(ok = wait_full())) break;
+                        pv(0, i == 0);
+                        if (i + 1 == tiles) umma_commit(bar.o_full + 8 * t);
+                        free_slot(true);
+                        if (i + 1 == tiles) break;
+                        if (!(ok = wait_full())) break;
+                        qk(0);
+                        umma_commit(bar.s_full + 8 * t);
+                        free_slot(true);
+                    }
+                } else {
+                    for (int i = 0; i < tiles; ++i, ++count) {
+                        const uint32_t buf = count & 1, of = count >> 1 & 1;
+                        if (qks) {
+                            if (!(ok = wait_full())) break;
+                            // the weights that lay in this buffer have been read
+                            if (count >= 2 && !(ok = mbar_wait(bar.pv_done + 8 * buf, of ^ 1, status))) break;
                             tc_fence_after();
-                            pv(t, vn, t, i == 0);
-                            if (more) {
-                                if (t == 0 && !(ok = wait_full(kn))) break;
-                                qk(t, kn, t);
-                                umma_commit(bar.s_full + 8 * t);
-                            } else {
-                                umma_commit(bar.o_full + 8 * t);
-                            }
+                            qk(buf);
+                            umma_commit(bar.s_full + 8 * buf);
+                            free_slot(true);
+                        } else if (++slot == NS) {
+                            slot = 0, full_phase ^= 1;
                         }
-                        if (!ok) break;
-                        umma_commit(bar.empty + 8 * slot_of(vn));
-                        if (more) umma_commit(bar.empty + 8 * slot_of(kn));
+                        if (pvs) {
+                            if (!(ok = mbar_wait(bar.p_full + 8 * buf, of, status)) || !(ok = wait_full())) break;
+                            pv(buf, i == 0);
+                            umma_commit(bar.pv_done + 8 * buf);
+                            if (i + 1 == tiles) umma_commit(bar.o_full);
+                            free_slot(true);
+                        } else if (++slot == NS) {
+                            slot = 0, full_phase ^= 1;
+                        }
                     }
                 }
-                used += 2 * (uint32_t)tiles;
-                count += (uint32_t)tiles;
             }
             if (!ok) *abort_flag = 1;
             umma_commit(bar.done);
@@ -694,26 +794,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
         // -------------------------------------------------------- copies
         set_regs_down<kOtherRegs>();
         const int w = warp - kCopyWarp;
-        constexpr int RB = D * (C::E4M3 ? 1 : 2);        // bytes of a cached row
-        constexpr int PER_ROW = RB / 16;                 // lanes of a row
-        constexpr int AT_ONCE = 32 / PER_ROW;            // rows of a warp's access
+        // A cached row is copied by as many lanes as 128 bytes of it have 16-byte pieces, block of 64 values after block, so
+        // that an access takes whole lines and a row's offset serves several.
+        constexpr int E = C::E4M3 ? 1 : 2;               // bytes of a value
+        constexpr int LANES = D * E < 128 ? D * E / 16 : 8;  // of a row
+        constexpr int PIECES = D * E / (16 * LANES);     // of a row, for a lane
+        constexpr int AT_ONCE = 32 / LANES;              // rows of a warp's access
         constexpr int WROWS = BN / kCopyWarps;           // rows of a warp
-        const int sub = lane / PER_ROW, chunk = lane % PER_ROW;
-        uint32_t issued = 0, shown = 0, seq = 0;
-        int64_t tile_count = 0;
-        bool ok = true;
+        constexpr int STEPS = WROWS / AT_ONCE;
+        const int sub = lane / LANES, chunk = lane % LANES;
+        uint32_t issued = 0, shown = 0;
+        uint32_t slot = 0, parity = 1;                   // where the next tile goes; its slot's phase before
+        uint32_t show_slot = 0;
+        uint32_t tile_count = 0;
         uint32_t edge_bits = 0;  // of the tiles on their way, newest in bit 0: values to be checked?
-        // this warp's part of ring tile n has landed: checked if need be, and shown to the MMAs
-        auto check = [&](uint32_t n, uint32_t of) {
-            const uint32_t at = ring + (n % NS) * C::SLOT;
+        // where 16-byte piece c of row r (of this warp's) lies in a tile
+        auto place = [&](int r, int c) {
+            const int row = w * WROWS + r;
+            return (uint32_t)((c / 8) * (BN * 128) + row * 128 + ((c ^ row) & 7) * 16);
+        };
+        // this warp's part of a tile has landed: checked if need be, and shown to the MMAs
+        auto check = [&](uint32_t at) {
             bool any = false;
 #pragma unroll 1
-            for (int r = 0; r < WROWS; r += AT_ONCE) {
-                const int slot = w * WROWS + r + sub;
+            for (int s = 0; s < STEPS; ++s) {
 #pragma unroll
-                for (int x = 0; x < (C::E4M3 ? 2 : 1); ++x) {
-                    const int c = (C::E4M3 ? 2 : 1) * chunk + x;
-                    const uint32_t p = at + (c / 8) * (BN * 128) + slot * 128 + ((c % 8) ^ (slot & 7)) * 16;
+                for (int x = 0; x < PIECES * (C::E4M3 ? 2 : 1); ++x) {
+                    const int c = C::E4M3 ? 2 * (chunk + LANES * (x / 2)) + (x & 1) : chunk + LANES * x;
+                    const uint32_t p = at + place(s * AT_ONCE + sub, c);
                     uint4 v = lds128(p);
                     const uint32_t b0 = not_finite<C::E4M3>(v.x), b1 = not_finite<C::E4M3>(v.y), b2 = not_finite<C::E4M3>(v.z),
                                    b3 = not_finite<C::E4M3>(v.w);
@@ -724,111 +832,107 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                     }
                 }
             }
-            if (any) bad_unit[of & 7] = of + 1;
+            if (any) *bad_seen = 1;
         };
-        uint32_t seq_of[NS];  // unit of each ring tile on its way
-#pragma unroll
-        for (int i = 0; i < NS; ++i) seq_of[i] = 0;
         auto show = [&](uint32_t upto) {
             while (shown != upto) {
-                const uint32_t back = issued - 1 - shown;
-                if (edge_bits >> back & 1u) {
-                    uint32_t of = 0;
-#pragma unroll
-                    for (int i = 0; i < NS; ++i)
-                        if (i == (int)(shown % NS)) of = seq_of[i];
-                    check(shown, of);
-                }
+                if (edge_bits >> (issued - 1 - shown) & 1u) check(ring + show_slot * C::SLOT);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar.full + 8 * (shown % NS));
+                if (lane == 0) mbar_arrive(bar.full + 8 * show_slot);
+                if (++show_slot == NS) show_slot = 0;
                 ++shown;
             }
         };
-        for (; ok && next_unit<C>(a, walk, u); ++seq) {
-            const int64_t unit_end = (int64_t)u.e0 + u.row0 / a.group;
-            const int64_t unit_begin = a.window > 0 ? (int64_t)u.e0 + (u.row0 + u.rows - 1) / a.group - a.window : 0;
-            for (int64_t i = u.lo; i < u.hi && ok; ++i, ++tile_count) {
-                const int64_t j0 = (u.base + i) * BN;
-                // where this lane's slot lies (lanes 0 .. WROWS - 1)
-                const int64_t j = j0 + w * WROWS + lane;
-                int64_t off = -1;
-                bool there = true;
-                if (lane < WROWS && j >= u.begin && j < u.end) {
-                    const uint32_t pg = page_of(a.c, (uint32_t)j);
-                    const int32_t page = __ldg(a.c.table + u.b * a.c.ld_table + pg);
-                    there = page_ok(a.c, page);
-                    if (there) off = row_bytes_at(a.c, page, u.h, (uint32_t)j - pg * a.c.page_size);
-                    else atomicOr(status, kDevIndex);
+        // the tile after this one: its page is looked up while this one is copied
+        int i = 0, page = 0;
+        uint32_t in_page = 0;
+        bool seen = false;       // does this lane's row hold a slot that some row of the unit sees?
+        auto look_up = [&] {
+            const uint32_t j = (uint32_t)(u.base + i) * BN + w * WROWS + lane;
+            seen = lane < WROWS && j >= (uint32_t)u.begin && j < (uint32_t)u.end;
+            if (seen) {
+                const uint32_t pg = page_of(a.c, j);
+                in_page = j - pg * a.c.page_size;
+                page = __ldg(a.c.table + u.b * a.c.ld_table + pg);
+            }
+        };
+        bool ok = true, more = next_unit<C>(a, walk, u);
+        if (more) {
+            i = u.lo;
+            look_up();
+        }
+        for (; more; ++tile_count) {
+            const bool there = !seen || page_ok(a.c, page);
+            if (!there) atomicOr(status, kDevIndex);
+            // this lane's row: its offset, or 1 (offsets are multiples of 16) where nothing is to be read
+            const int64_t off = seen && there ? row_bytes_at(a.c, page, u.h, in_page) : 1;
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
+            const uint32_t j0 = (uint32_t)(u.base + i) * BN;
+            const bool edge = j0 + BN > (uint32_t)u.all_end || j0 < (uint32_t)u.all_begin;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t eb = bar.empty + 8 * slot;
+                if (issued >= (uint32_t)NS && !__all_sync(0xFFFFFFFFu, mbar_test_wait(eb, parity))) {
+                    if constexpr (!C::E4M3) cp_async_wait<0>();  // nothing is held back while this waits
+                    show(issued);
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(eb, parity, status)) || *abort_flag) {
+                        ok = false;
+                        break;
+                    }
                 }
-                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
-                const bool edge = j0 + BN > unit_end || j0 < unit_begin;
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const uint32_t n = issued;
-                    if (n >= (uint32_t)NS) {
-                        const uint32_t eb = bar.empty + 8 * (n % NS), parity = (n / NS - 1) & 1;
-                        if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(eb, parity))) {
-                            cp_async_wait<0>();  // nothing is held back while this waits
-                            show(issued);
-                            if (!__all_sync(0xFFFFFFFFu, mbar_wait(eb, parity, status)) || *abort_flag) {
-                                ok = false;
-                                break;
-                            }
-                        }
-                    }
-                    if (kv == 0 && lane == 0) {  // (heads of 256: 16 slots a warp, two warps' bits in a word)
-                        if constexpr (WROWS == 32) page_mask[(tile_count & (kMetaRing - 1)) * 4 + w] = mask;
-                        else reinterpret_cast<volatile uint16_t *>(page_mask)[(tile_count & (kMetaRing - 1)) * 8 + w] = (uint16_t)mask;
-                    }
-                    const uint8_t *pool = kv == 0 ? a.c.k : a.c.v;
-                    const uint32_t at = ring + (n % NS) * C::SLOT;
-                    if constexpr (C::E4M3) {
-                        constexpr int STEP = 4;
+                if (kv == 0 && lane == 0) {  // (heads of 256: 16 slots a warp, two warps' bits in a word)
+                    if constexpr (WROWS == 32) page_mask[(tile_count & (kMetaRing - 1)) * 4 + w] = mask;
+                    else reinterpret_cast<volatile uint16_t *>(page_mask)[(tile_count & (kMetaRing - 1)) * 8 + w] = (uint16_t)mask;
+                }
+                const uint8_t *const pool = (kv == 0 ? a.c.k : a.c.v) + 16 * chunk;
+                const uint32_t at = ring + slot * C::SLOT;
+                if constexpr (C::E4M3) {
+                    constexpr int STEP = STEPS * PIECES < 4 ? STEPS * PIECES : 4;
 #pragma unroll 1
-                        for (int r = 0; r < WROWS; r += AT_ONCE * STEP) {
-                            uint4 v[STEP];
+                    for (int s = 0; s < STEPS * PIECES; s += STEP) {
+                        uint4 v[STEP];
 #pragma unroll
-                            for (int x = 0; x < STEP; ++x) {
-                                const int64_t o = __shfl_sync(0xFFFFFFFFu, off, (r + x * AT_ONCE + sub) & 31);
-                                v[x] = o >= 0 && r + x * AT_ONCE < WROWS ? __ldg(reinterpret_cast<const uint4 *>(pool + o) + chunk)
-                                                                       : make_uint4(0, 0, 0, 0);
-                            }
-#pragma unroll
-                            for (int x = 0; x < STEP; ++x) {
-                                if (r + x * AT_ONCE >= WROWS) continue;
-                                const int slot = w * WROWS + r + x * AT_ONCE + sub;
-                                const uint32_t row = at + (chunk / 4) * (BN * 128) + slot * 128;
-                                const int c = 2 * (chunk % 4);
-                                sts128(row + (c ^ (slot & 7)) * 16, make_uint4(e4m3x2_to_f16x2(v[x].x), e4m3x2_to_f16x2(v[x].x >> 16),
-                                                                               e4m3x2_to_f16x2(v[x].y), e4m3x2_to_f16x2(v[x].y >> 16)));
-                                sts128(row + ((c + 1) ^ (slot & 7)) * 16, make_uint4(e4m3x2_to_f16x2(v[x].z), e4m3x2_to_f16x2(v[x].z >> 16),
-                                                                                     e4m3x2_to_f16x2(v[x].w), e4m3x2_to_f16x2(v[x].w >> 16)));
-                            }
+                        for (int x = 0; x < STEP; ++x) {
+                            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, (s + x) / PIECES * AT_ONCE + sub);
+                            v[x] = o & 1 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4 *>(pool + o) + LANES * ((s + x) % PIECES));
                         }
-                    } else {
-#pragma unroll 4
-                        for (int r = 0; r < WROWS; r += AT_ONCE) {
-                            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r + sub);
-                            const int slot = w * WROWS + r + sub;
-                            cp_async16(at + (chunk / 8) * (BN * 128) + slot * 128 + ((chunk % 8) ^ (slot & 7)) * 16,
-                                       o >= 0 ? pool + o + chunk * 16 : pool, o >= 0 ? 16 : 0);
-                        }
-                        cp_async_commit();
-                    }
-                    ++issued;
-                    edge_bits = edge_bits << 1 | (uint32_t)(kv == 1 && edge);
 #pragma unroll
-                    for (int x = 0; x < NS; ++x)
-                        if (x == (int)(n % NS)) seq_of[x] = seq;
-                    if constexpr (C::E4M3) {
-                        show(issued);
-                    } else if (issued - shown > (uint32_t)C::LAG) {
-                        cp_async_wait<C::LAG>();
-                        show(issued - C::LAG);
+                        for (int x = 0; x < STEP; ++x) {
+                            const int r = (s + x) / PIECES * AT_ONCE + sub, c = 2 * (chunk + LANES * ((s + x) % PIECES));
+                            sts128(at + place(r, c), make_uint4(e4m3x2_to_f16x2(v[x].x), e4m3x2_to_f16x2(v[x].x >> 16),
+                                                                e4m3x2_to_f16x2(v[x].y), e4m3x2_to_f16x2(v[x].y >> 16)));
+                            sts128(at + place(r, c + 1), make_uint4(e4m3x2_to_f16x2(v[x].z), e4m3x2_to_f16x2(v[x].z >> 16),
+                                                                    e4m3x2_to_f16x2(v[x].w), e4m3x2_to_f16x2(v[x].w >> 16)));
+                        }
                     }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < STEPS; ++s) {
+                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, s * AT_ONCE + sub);
+                        const uint32_t bytes = o & 1 ? 0u : 16u;
+                        const uint8_t *const src = o & 1 ? pool : pool + o;
+#pragma unroll
+                        for (int x = 0; x < PIECES; ++x) cp_async16(at + place(s * AT_ONCE + sub, chunk + LANES * x), src + 16 * LANES * x, bytes);
+                    }
+                    cp_async_commit();
+                }
+                ++issued;
+                if (++slot == NS) slot = 0, parity ^= 1;
+                edge_bits = edge_bits << 1 | (uint32_t)(kv == 1 && edge);
+                if constexpr (C::E4M3) {
+                    show(issued);
+                } else if (issued - shown > (uint32_t)C::LAG) {
+                    cp_async_wait<C::LAG>();
+                    show(issued - C::LAG);
                 }
             }
+            if (!ok) break;
+            if (++i == u.hi) {
+                more = next_unit<C>(a, walk, u);
+                i = u.lo;
+            }
+            if (more) look_up();
         }
         cp_async_wait<0>();
         if (ok) show(issued);
@@ -860,10 +964,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const ChunkArgs a
     const int rt = find_rt(a, (int)__ldg(a.head + 1), in_head);
     const int64_t first = __ldg(a.place_at + rt);
     if (first == in_head) return;                                              // the boundary lies between units
-    const int64_t start = h * places + first, end = h * places + __ldg(a.place_at + rt + 1);
+    const int64_t start = h * places + first, end = h * places + __ldg(a.place_at + rt + 1) - kExtra;
+    if (cut >= end) return;                                                    // ... or behind the unit's tiles
     if (share_at(total, shares, s - 1) > start) return;                        // an earlier boundary cut it
-    Unit u;
-    unit_of<C>(a, rt, u);
+    ChunkRecord u;
+    load_record(a, rt, u);
     int last = s;                                                              // the share that holds its end
     while (last + 1 < shares && share_at(total, shares, last + 1) < end) ++last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -892,7 +997,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const ChunkArgs a
         const int row = u.row0 + row_in, tok = row / a.group, e = u.e0 + tok;
         const int bgn = a.window > 0 && e > a.window ? (int)(e - a.window) : 0;
         const float inv = a.v_scale / l;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + (u.q0 + tok) * a.ldo + (int64_t)(h * a.group + row - tok * a.group) * D + lane * PER);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + ((int64_t)u.q0 + tok) * a.ldo + (int64_t)(h * a.group + row - tok * a.group) * D + lane * PER);
 #pragma unroll
         for (int x = 0; x < PER; x += 2) dst[x / 2] = e > bgn ? pack_bf16(o[x] * inv, o[x + 1] * inv) : 0u;
     }

@@ -184,7 +184,7 @@ bool chunk_shape_ok(const q4k_kv_cache *c, int64_t T, int32_t n_heads) {
 }
 
 struct ChunkLayout {
-    size_t seq_at, rt_at, rt_seq, place_at, head, parts, part_ml, total;
+    size_t seq_at, rt_at, records, place_at, head, parts, part_ml, total;
 };
 ChunkLayout chunk_layout(const q4k_kv_cache *c, int64_t T, int32_t n_heads) {
     const size_t rows = (size_t)chunk_rows(c->head_dim);
@@ -198,7 +198,7 @@ ChunkLayout chunk_layout(const q4k_kv_cache *c, int64_t T, int32_t n_heads) {
     };
     l.seq_at = take(((size_t)c->batch + 1) * 4);
     l.rt_at = take(((size_t)c->batch + 1) * 4);
-    l.rt_seq = take(tiles * 4);
+    l.records = take(tiles * sizeof(ChunkRecord));
     l.place_at = take((tiles + 1) * 8);
     l.head = take(3 * 8);
     l.part_ml = take((size_t)2 * kMaxChunkShares * rows * sizeof(float2));
@@ -511,7 +511,7 @@ q4k_status q4k_attn_chunk(const q4k_kv_cache *cache, const int32_t *starts, cons
     uint8_t *base = static_cast<uint8_t *>(ws);
     a.seq_at = reinterpret_cast<int32_t *>(base + l.seq_at);
     a.rt_at = reinterpret_cast<int32_t *>(base + l.rt_at);
-    a.rt_seq = reinterpret_cast<int32_t *>(base + l.rt_seq);
+    a.records = reinterpret_cast<ChunkRecord *>(base + l.records);
     a.place_at = reinterpret_cast<int64_t *>(base + l.place_at);
     a.head = reinterpret_cast<int64_t *>(base + l.head);
     a.part_ml = reinterpret_cast<float2 *>(base + l.part_ml);

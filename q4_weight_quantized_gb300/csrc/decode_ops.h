@@ -129,6 +129,15 @@ struct PlanArgs {
 cudaError_t launch_batch_plan(const DeviceInfo &di, const PlanArgs &a, cudaStream_t s);
 
 constexpr int kMaxChunkShares = 160;  // CTAs of an attention call over chunks, at most (the workspace holds two parts for each)
+// A unit of rows (chunk_rows() of them at most) of a sequence, the same for every KV head.
+struct alignas(16) ChunkRecord {
+    int32_t b, q0, e0;          // sequence, its first row in q and o, the end of its first new token's slots
+    int32_t row0, rows;         // rows within the sequence
+    int32_t begin, end;         // slots that any row sees: [begin, end)
+    int32_t base, tiles;        // its tiles of slots: the first, their number
+    int32_t all_end, all_begin; // every row sees slots below all_end, and from all_begin on
+    int32_t pad;
+};
 struct ChunkArgs {
     KvView c;
     const int32_t *starts, *seq_lens;
@@ -147,7 +156,7 @@ struct ChunkArgs {
     // workspace
     int32_t *seq_at;              // [batch + 1]: first row of each sequence
     int32_t *rt_at;               // [batch + 1]: row tiles before each sequence
-    int32_t *rt_seq;              // [row tiles]
+    ChunkRecord *records;         // [row tiles]
     int64_t *place_at;            // [row tiles + 1]: places of the list before each row tile, of one KV head
     int64_t *head;                // places, row tiles, shares
     float *parts;                 // [2 * shares][rows][D]
