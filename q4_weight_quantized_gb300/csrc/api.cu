@@ -6,9 +6,11 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstring>
 #include <mutex>
 
 #include "q4k.h"
+#include "kv_cache.h"
 #include "q4k_api.h"
 #include "q4k_internal.h"
 #include "q4k_ptx.cuh"
@@ -148,6 +150,18 @@ struct TmapKey {
     }
 };
 
+static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    std::call_once(g_encode_once, [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    return g_encode;
+}
+
 static cudaError_t encode_cached(CUtensorMap *m, const TmapKey &k, CUtensorMapDataType dtype, CUtensorMapSwizzle sw) {
     constexpr int kSlots = 16;
     thread_local TmapKey keys[kSlots];
@@ -159,15 +173,7 @@ static cudaError_t encode_cached(CUtensorMap *m, const TmapKey &k, CUtensorMapDa
             *m = maps[i];
             return cudaSuccess;
         }
-    std::call_once(g_encode_once, [] {
-        void *fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    });
-    if (!g_encode) return cudaErrorNotSupported;
+    if (!encoder()) return cudaErrorNotSupported;
     cuuint64_t dims[2] = {(cuuint64_t)k.d0, (cuuint64_t)k.d1};
     cuuint64_t strides[1] = {(cuuint64_t)k.stride};
     cuuint32_t box[2] = {(cuuint32_t)k.box0, (cuuint32_t)k.box1};
@@ -209,6 +215,49 @@ cudaError_t make_bytes_tmap(CUtensorMap *m, const void *p, int64_t rows, int64_t
 cudaError_t make_act_tmap_sw128(CUtensorMap *m, const void *x, int64_t rows, int64_t K, int64_t ld, int box_rows) {
     const TmapKey k = {x, K, rows, ld * 2, 64, box_rows, 2};
     return encode_cached(m, k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// One pool of a paged cache as a 4-D tensor: D values, then slots and heads (the nearer first; *head_first tells which), then
+// pages; boxes of `box_values` values of `box_slots` slots, 128-byte swizzle if asked.  False where the pool has no such form.
+bool make_cache_tmap(CUtensorMap *m, const void *pool, const KvView &c, int box_values, int box_slots, bool swizzle, bool *head_first) {
+    struct Key {
+        const void *pool;
+        int64_t page, head, slot, pages;
+        int32_t size, heads, dim, e4m3, box0, box1, swizzle, unused;
+        bool operator==(const Key &o) const { return std::memcmp(this, &o, sizeof o) == 0; }
+    };
+    constexpr int kSlots = 16;
+    thread_local Key keys[kSlots];
+    thread_local CUtensorMap maps[kSlots];
+    thread_local int state[kSlots] = {};  // 1: a map, 2: there is none
+    thread_local int next = 0;
+    *head_first = c.head_bytes < c.slot_bytes;
+    const Key k = {pool, c.page_bytes, c.head_bytes, c.slot_bytes, c.n_pages, c.page_size, c.heads, c.dim, c.e4m3, box_values, box_slots,
+                   swizzle, 0};
+    for (int i = 0; i < kSlots; ++i)
+        if (state[i] && keys[i] == k) {
+            if (state[i] == 1) *m = maps[i];
+            return state[i] == 1;
+        }
+    bool ok = encoder() != nullptr && c.page_bytes < ((int64_t)1 << 40) && c.head_bytes < ((int64_t)1 << 40) &&
+              c.slot_bytes < ((int64_t)1 << 40);
+    if (ok) {
+        const bool hf = *head_first;
+        cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)(hf ? c.heads : c.page_size), (cuuint64_t)(hf ? c.page_size : c.heads),
+                              (cuuint64_t)c.n_pages};
+        cuuint64_t strides[3] = {(cuuint64_t)(hf ? c.head_bytes : c.slot_bytes), (cuuint64_t)(hf ? c.slot_bytes : c.head_bytes),
+                                 (cuuint64_t)c.page_bytes};
+        cuuint32_t box[4] = {(cuuint32_t)box_values, (cuuint32_t)(hf ? 1 : box_slots), (cuuint32_t)(hf ? box_slots : 1), 1};
+        cuuint32_t estr[4] = {1, 1, 1, 1};
+        ok = encoder()(m, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims,
+                       strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
+    keys[next] = k;
+    state[next] = ok ? 1 : 2;
+    if (ok) maps[next] = *m;
+    next = (next + 1) % kSlots;
+    return ok;
 }
 
 // Common device gate: a cc 10.3 device must be current.

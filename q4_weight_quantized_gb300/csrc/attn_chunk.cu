@@ -31,7 +31,7 @@
 namespace q4k {
 namespace {
 
-constexpr int kThreads = 512;          // warps 0-3 and 4-7: softmax of a tile of rows each; 8, 9: MMA; 12-15: copies
+constexpr int kThreads = 512;          // warps 0-3 and 4-7: softmax of a tile of rows each; 8 (9): MMA; 12-15: copies
 constexpr int kMmaWarp = 8, kCopyWarp = 12, kCopyWarps = 4;
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // together those of the launch: 2 * (184 + 72) = 4 * 128
 constexpr int kPlanThreads = 1024;
@@ -389,8 +389,18 @@ struct Row {
     }
 };
 
+// A tensor copy of box_slots slots of one head into shared memory, counted in bytes on `bar`; slots_at, head: its coordinates.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap &m, int value, int slot, int head, int page, bool head_first,
+                                         uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(&m)), "r"(value), "r"(head_first ? head : slot), "r"(head_first ? slot : head), "r"(page), "r"(bar)
+        : "memory");
+}
+
 template <typename C>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap k_map,
+                                                            const __grid_constant__ CUtensorMap v_map) {
     constexpr int D = C::D, BN = C::BN, NT = C::NT, NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -401,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
     bar.o_full = bar.p_full + 16, bar.q_full = bar.o_full + 16, bar.pv_done = bar.q_full + 16, bar.done = bar.pv_done + 16;
     uint32_t *const tmem_holder = reinterpret_cast<uint32_t *>(misc_p + 512);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc_p + 516);
+    volatile int *const bad_pages = reinterpret_cast<volatile int *>(misc_p + 524); // a page id was out of range
     volatile int *const bad_seen = reinterpret_cast<volatile int *>(misc_p + 520);  // a value that is not finite was taken out
     volatile uint32_t *const page_mask = reinterpret_cast<volatile uint32_t *>(misc_p + 640);      // [kMetaRing][4]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -409,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(bar.full + 8 * i, kCopyWarps);
-            mbar_init(bar.empty + 8 * i, NT);
+            mbar_init(bar.empty + 8 * i, 1);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar.s_full + 8 * t, 1);
@@ -418,9 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
             mbar_init(bar.q_full + 8 * t, 4);
             mbar_init(bar.pv_done + 8 * t, 1);
         }
-        mbar_init(bar.done, 2);
+        mbar_init(bar.done, NT == 2 ? 1 : 2);
         *abort_flag = 0;
         *bad_seen = 0;
+        *bad_pages = 0;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -472,13 +484,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
             const float f = a.softcap > 0.f ? 1.f : r.cc;
             // neg: -m f, or 0 where there is no maximum yet (rows that are not there have one: 0)
             float m = r.real ? -INFINITY : 0.f, l = 0.f, m_next = m, neg = 0.f;
-            bool far = false;
+            // what holds for all rows of the warp: a maximum is to be raised; each has one, and none is far from 0
+            bool pending = false, usual = false, far = false;
             // the running maximum becomes m_next; O and l follow
             auto raise = [&](bool has_o) {
                 const float neg_new = m_next == -INFINITY ? 0.f : -m_next * f;
                 const float fac = m == m_next || m == -INFINITY ? 1.f : ex2_approx(neg_new - neg);
                 m = m_next, neg = neg_new;
                 far = __any_sync(0xFFFFFFFFu, fabsf(neg) > kFar);
+                usual = usual && !far;
+                pending = false;
                 l *= fac;
                 if (!has_o) return true;
                 if constexpr (NT == 1) {  // the product before must have ended
@@ -509,25 +524,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                 }
                 tc_fence_after();
                 const uint32_t s_col = tmem + lanes + C::S_COL + at * BN;
+                uint32_t s[2][32];
+                tmem_ld32(s_col, s[0]);
                 const uint32_t j0 = (uint32_t)(u.base + i) * BN;
-                const volatile uint32_t *mask = page_mask + (tile_count & (kMetaRing - 1)) * 4;
-                uint32_t pages = mask[0];
-#pragma unroll
-                for (int w = 1; w < BN / 32; ++w) pages &= mask[w];
-                const bool masked = j0 + BN > all_end || j0 < all_begin || pages != 0xFFFFFFFFu;
-                if (__any_sync(0xFFFFFFFFu, m_next != m) && !raise(i > u.lo)) {
+                const bool pages = *bad_pages != 0, masked = j0 + BN > all_end || j0 < all_begin || pages;
+                if (pending && !raise(i > u.lo)) {
                     ok = false;
                     break;
                 }
                 // ---- the usual tile: weights by the maximum so far, in one pass; a larger one counts from the next tile on
                 bool done = false;
-                if (!masked && i > u.lo && a.softcap == 0.f && !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY)) {
+                if (!masked && usual) {
                     uint32_t p[BN / 2];
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     float top[2] = {-INFINITY, -INFINITY};
                     const float2 f2 = make_float2(f, f), n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
-                    uint32_t s[2][32];
-                    tmem_ld32(s_col, s[0]);
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < BN / 32; ++c) {
@@ -545,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                         if (c + 1 < BN / 32) tmem_ld_wait();
                     }
                     const float mx = fmaxf(top[0], top[1]), above = (mx - m) * f;
-                    done = !__any_sync(0xFFFFFFFFu, above > C::JUMP);
+                    pending = __any_sync(0xFFFFFFFFu, above > kSlack);
+                    done = !pending || !__any_sync(0xFFFFFFFFu, above > C::JUMP);
                     if (done) {
                         if (above > kSlack) m_next = mx;
                         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -554,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                     }
                 }
                 if (!done) {
+                    tmem_ld_wait();
                     // ---- two passes: the maximum of what a row sees, then the weights
                     const int from = (int)max((int64_t)0, (int64_t)r.bgn - j0), to = (int)min((int64_t)BN, (int64_t)r.e - j0);
                     const float in = a.cap_in * r.cc, out = a.softcap * kLog2e;
@@ -561,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                         tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s));
                         uint32_t there = 0xFFFFFFFFu;
                         if (masked) {
-                            there = mask[c];
+                            if (pages) there = page_mask[(tile_count & (kMetaRing - 1)) * 4 + c];
                             const int lo = from - 32 * c, hi = to - 32 * c;
                             there &= lo <= 0 ? 0xFFFFFFFFu : lo >= 32 ? 0u : 0xFFFFFFFFu << lo;
                             there &= hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
@@ -588,6 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                         ok = false;
                         break;
                     }
+                    pending = false;
+                    usual = a.softcap == 0.f && !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
 #pragma unroll 1
                     for (int c = 0; c < BN / 32; ++c) {  // (a group's weights lie over scores that have been read)
                         float s[32];
@@ -689,41 +704,40 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
         if (!ok && lane == 0) *abort_flag = 1;
     } else if (warp < kCopyWarp) {
         set_regs_down<kOtherRegs>();
-        if (warp < kMmaWarp + 2 && elect_one()) {
+        if (warp < kMmaWarp + (NT == 2 ? 1 : 2) && elect_one()) {
             // ---------------------------------------------------- MMA
-            // Two warps, as one thread does not issue fast enough for the tensor cores: one for each tile of rows, or,
-            // for heads of 256, one for each product.
+            // Two tiles of rows: one thread issues a tile's P V and next Q K^T, then the other's, so that while one's run the
+            // softmax of the other has the SM's other pipes for itself.  (Issued by two threads they interleave, both end
+            // together, and so do the two softmaxes that follow: 2.5 us for two tiles of 128 slots instead of 2.2.)  Heads of
+            // 256: a thread for each product.
             constexpr uint32_t kQk = idesc_of(128, BN, C::E4M3, false), kPv = idesc_of(128, D, C::E4M3, true);
-            const int t = NT == 2 ? warp - kMmaWarp : 0;
             const bool qks = NT == 2 || warp == kMmaWarp, pvs = NT == 2 || warp != kMmaWarp;
-            const uint64_t q_desc = umma_desc_sw128(q_smem + t * (128 * D * 2)), k_desc = umma_desc_sw128(ring), v_desc = desc_mn(ring, BN * 128);
-            const uint32_t s_at = tmem + C::S_COL + t * BN, o_at = tmem + C::O_COL + t * D;
-            uint32_t slot = 0, full_phase = 0;  // the ring tile that is next
-            uint32_t phase = 0, unit_phase = 0; // of p_full (NT 2); of q_full
-            uint32_t count = 0;                 // tiles of slots done (NT 1: buffers and their phases go by it)
+            const uint64_t q_desc = umma_desc_sw128(q_smem), k_desc = umma_desc_sw128(ring), v_desc = desc_mn(ring, BN * 128);
+            uint32_t slot = 0, full_phase = 0;     // the ring tile that is next
+            uint32_t phase = 0, unit_phase = 0;    // of p_full (NT 2), of q_full: a bit for each tile of rows
+            uint32_t count = 0;                    // tiles of slots done (NT 1: buffers and their phases go by it)
             bool ok = true;
             auto wait_full = [&] {
                 const bool r = mbar_wait(bar.full + 8 * slot, full_phase, status);
                 tc_fence_after();
                 return r;
             };
-            auto free_slot = [&](bool used) {  // once what was issued has read it
-                if (used) umma_commit(bar.empty + 8 * slot);
-                else if (NT == 2) mbar_arrive(bar.empty + 8 * slot);
+            auto next_slot = [&] {
                 if (++slot == NS) slot = 0, full_phase ^= 1;
             };
-            auto qk = [&](uint32_t buf) {
-                const uint64_t kd = k_desc + (uint64_t)(slot * (C::SLOT >> 4));
+            auto qk = [&](int t, uint32_t buf) {
+                const uint64_t kd = k_desc + (uint64_t)(slot * (C::SLOT >> 4)), qd = q_desc + (uint64_t)(t * (128 * D * 2 >> 4));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma_bf16(s_at + buf * BN, q_desc + (k / 4) * (128 * 128 >> 4) + 2 * (k % 4), kd + (k / 4) * (BN * 128 >> 4) + 2 * (k % 4),
-                              kQk, k != 0);
+                    umma_bf16(tmem + C::S_COL + buf * BN, qd + (k / 4) * (128 * 128 >> 4) + 2 * (k % 4),
+                              kd + (k / 4) * (BN * 128 >> 4) + 2 * (k % 4), kQk, k != 0);
+                umma_commit(bar.s_full + 8 * buf);
             };
-            auto pv = [&](uint32_t buf, bool first) {
-                const uint64_t vd = v_desc + (uint64_t)(slot * (C::SLOT >> 4));
+            auto pv = [&](int t, uint32_t buf, uint32_t of, bool first) {
+                const uint64_t vd = v_desc + (uint64_t)(of * (C::SLOT >> 4));
 #pragma unroll
                 for (int k = 0; k < BN / 16; ++k)
-                    umma_bf16_ts(o_at, s_at + buf * BN + 8 * k, vd + k * (16 * 128 >> 4), kPv, !first || k != 0);
+                    umma_bf16_ts(tmem + C::O_COL + t * D, tmem + C::S_COL + buf * BN + 8 * k, vd + k * (16 * 128 >> 4), kPv, !first || k != 0);
             };
             while (ok && next_unit<C>(a, walk, u)) {
                 const int tiles = u.hi - u.lo;
@@ -731,37 +745,48 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                     ok = false;
                     break;
                 }
-                if (NT == 2 && t * 128 >= u.rows) {  // no rows in this tile: its share of letting go of keys and values
-                    for (int i = 0; i < 2 * tiles && ok; ++i) {
-                        ok = wait_full();
-                        if (ok) free_slot(false);
-                    }
-                    continue;
-                }
-                if (qks) {
-                    if (!(ok = mbar_wait(bar.q_full + 8 * t, unit_phase, status))) break;
-                    unit_phase ^= 1;
-                }
                 if constexpr (NT == 2) {
+                    const int nt = u.rows > 128 ? 2 : 1;
                     // the ring holds keys and values in turn: K(0) V(0) K(1) V(1) ...
                     if (!(ok = wait_full())) break;
-                    qk(0);
-                    umma_commit(bar.s_full + 8 * t);
-                    free_slot(true);
-                    for (int i = 0; i < tiles; ++i) {
-                        if (!(ok = mbar_wait(bar.p_full + 8 * t, phase, status))) break;
-                        phase ^= 1;
-                        if (!(ok = wait_full())) break;
-                        pv(0, i == 0);
-                        if (i + 1 == tiles) umma_commit(bar.o_full + 8 * t);
-                        free_slot(true);
-                        if (i + 1 == tiles) break;
-                        if (!(ok = wait_full())) break;
-                        qk(0);
-                        umma_commit(bar.s_full + 8 * t);
-                        free_slot(true);
+                    for (int t = 0; t < nt && ok; ++t) {
+                        if (!(ok = mbar_wait(bar.q_full + 8 * t, unit_phase >> t & 1, status))) break;
+                        unit_phase ^= 1u << t;
+                        tc_fence_after();
+                        qk(t, t);
+                    }
+                    if (!ok) break;
+                    umma_commit(bar.empty + 8 * slot);
+                    next_slot();
+                    for (int i = 0; i < tiles && ok; ++i) {
+                        const uint32_t v_slot = slot;
+                        const bool last = i + 1 == tiles;
+                        for (int t = 0; t < nt; ++t) {
+                            if (t == 0 && !(ok = wait_full())) break;
+                            if (!(ok = mbar_wait(bar.p_full + 8 * t, phase >> t & 1, status))) break;
+                            phase ^= 1u << t;
+                            tc_fence_after();
+                            pv(t, t, v_slot, i == 0);
+                            if (last) {
+                                umma_commit(bar.o_full + 8 * t);
+                                continue;
+                            }
+                            if (t == 0) {
+                                next_slot();
+                                if (!(ok = wait_full())) break;
+                            }
+                            qk(t, t);
+                        }
+                        if (!ok) break;
+                        umma_commit(bar.empty + 8 * v_slot);
+                        if (!last) umma_commit(bar.empty + 8 * slot);
+                        next_slot();
                     }
                 } else {
+                    if (qks) {
+                        if (!(ok = mbar_wait(bar.q_full, unit_phase, status))) break;
+                        unit_phase ^= 1;
+                    }
                     for (int i = 0; i < tiles; ++i, ++count) {
                         const uint32_t buf = count & 1, of = count >> 1 & 1;
                         if (qks) {
@@ -769,21 +794,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                             // the weights that lay in this buffer have been read
                             if (count >= 2 && !(ok = mbar_wait(bar.pv_done + 8 * buf, of ^ 1, status))) break;
                             tc_fence_after();
-                            qk(buf);
-                            umma_commit(bar.s_full + 8 * buf);
-                            free_slot(true);
-                        } else if (++slot == NS) {
-                            slot = 0, full_phase ^= 1;
+                            qk(0, buf);
+                            umma_commit(bar.empty + 8 * slot);
                         }
+                        next_slot();
                         if (pvs) {
                             if (!(ok = mbar_wait(bar.p_full + 8 * buf, of, status)) || !(ok = wait_full())) break;
-                            pv(buf, i == 0);
+                            pv(0, buf, slot, i == 0);
                             umma_commit(bar.pv_done + 8 * buf);
                             if (i + 1 == tiles) umma_commit(bar.o_full);
-                            free_slot(true);
-                        } else if (++slot == NS) {
-                            slot = 0, full_phase ^= 1;
+                            umma_commit(bar.empty + 8 * slot);
                         }
+                        next_slot();
                     }
                 }
             }
@@ -834,12 +856,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
             }
             if (any) *bad_seen = 1;
         };
+        uint32_t box_bits = 0;   // of the tiles on their way, newest in bit 0: copied by the copy engine?
         auto show = [&](uint32_t upto) {
             while (shown != upto) {
-                if (edge_bits >> (issued - 1 - shown) & 1u) check(ring + show_slot * C::SLOT);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar.full + 8 * show_slot);
+                const uint32_t back = issued - 1 - shown;
+                if (!(box_bits >> back & 1u)) {  // (what the copy engine brings counts on the barrier by itself)
+                    if (edge_bits >> back & 1u) check(ring + show_slot * C::SLOT);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar.full + 8 * show_slot);
+                }
                 if (++show_slot == NS) show_slot = 0;
                 ++shown;
             }
@@ -864,12 +890,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
         }
         for (; more; ++tile_count) {
             const bool there = !seen || page_ok(a.c, page);
-            if (!there) atomicOr(status, kDevIndex);
+            if (!there) {
+                atomicOr(status, kDevIndex);
+                *bad_pages = 1;
+            }
             // this lane's row: its offset, or 1 (offsets are multiples of 16) where nothing is to be read
             const int64_t off = seen && there ? row_bytes_at(a.c, page, u.h, in_page) : 1;
             const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
             const uint32_t j0 = (uint32_t)(u.base + i) * BN;
             const bool edge = j0 + BN > (uint32_t)u.all_end || j0 < (uint32_t)u.all_begin;
+            // rows that are all there come by the copy engine, in boxes within a page (values only where every row sees them)
+            const bool boxes = a.box_slots > 0 && __all_sync(0xFFFFFFFFu, lane >= WROWS || (seen && there));
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
                 const uint32_t eb = bar.empty + 8 * slot;
@@ -906,6 +937,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                                                                     e4m3x2_to_f16x2(v[x].w), e4m3x2_to_f16x2(v[x].w >> 16)));
                         }
                     }
+                } else if (boxes && !(kv == 1 && edge)) {
+                    // lane x: block x % (D / 64) of box x / (D / 64)
+                    const int row = lane / (D / 64) * a.box_slots, block = lane % (D / 64);
+                    const int pg = __shfl_sync(0xFFFFFFFFu, page, row & 31), in = __shfl_sync(0xFFFFFFFFu, (int)in_page, row & 31);
+                    if (lane == 0) mbar_arrive_expect_tx(bar.full + 8 * slot, WROWS * D * 2);
+                    __syncwarp();
+                    if (row < WROWS)
+                        copy_box(at + block * (BN * 128) + (w * WROWS + row) * 128, kv == 0 ? k_map : v_map, 64 * block, in, u.h, pg,
+                                 a.head_first != 0, bar.full + 8 * slot);
+                    cp_async_commit();  // (an empty group: the count of those on their way is that of tiles)
                 } else {
 #pragma unroll
                     for (int s = 0; s < STEPS; ++s) {
@@ -920,6 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
                 ++issued;
                 if (++slot == NS) slot = 0, parity ^= 1;
                 edge_bits = edge_bits << 1 | (uint32_t)(kv == 1 && edge);
+                box_bits = box_bits << 1 | (uint32_t)(!C::E4M3 && boxes && !(kv == 1 && edge));
                 if constexpr (C::E4M3) {
                     show(issued);
                 } else if (issued - shown > (uint32_t)C::LAG) {
@@ -935,8 +977,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a) {
             if (more) look_up();
         }
         cp_async_wait<0>();
-        if (ok) show(issued);
-        else if (lane == 0) *abort_flag = 1;
+        if (ok) {
+            show(issued);
+        } else if (lane == 0) {
+            *abort_flag = 1;
+            // the copy engine's copies land before this CTA leaves (a barrier that others left short of arrivals runs out)
+            for (uint32_t n = issued > (uint32_t)NS ? issued - NS : 0; n < issued; ++n)
+                if (box_bits >> (issued - 1 - n) & 1u) (void)mbar_wait_limit(bar.full + 8 * (n % NS), n / NS & 1, status, 10000000ull);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -1015,7 +1063,15 @@ cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     a.shares = di.sm_count < kMaxChunkShares ? di.sm_count : kMaxChunkShares;
     if ((e = launch_pdl(plan_kernel<C>, dim3(1), dim3(kPlanThreads), 0, s, dim3(1), a)) != cudaSuccess) return e;
-    if ((e = launch_pdl(chunk_kernel<C>, dim3(a.shares), dim3(kThreads), C::SMEM, s, dim3(1), a)) != cudaSuccess) return e;
+    // boxes of what divides a page, of 8 (a swizzle atom) to 32 slots (a warp's rows; 16 of heads of 256)
+    CUtensorMap k_map = {}, v_map = {};
+    int box = 1;
+    while (box < C::BN / kCopyWarps && a.c.page_size % (2 * box) == 0) box *= 2;
+    bool head_first = false;
+    a.box_slots = !C::E4M3 && box >= 8 && make_cache_tmap(&k_map, a.c.k, a.c, 64, box, true, &head_first) &&
+                          make_cache_tmap(&v_map, a.c.v, a.c, 64, box, true, &head_first) ? box : 0;
+    a.head_first = head_first;
+    if ((e = launch_pdl(chunk_kernel<C>, dim3(a.shares), dim3(kThreads), C::SMEM, s, dim3(1), a, k_map, v_map)) != cudaSuccess) return e;
     // rows of a unit over 8 CTAs, fewer where the call has few rows
     const int64_t rows = a.T * a.group;
     const int y = rows <= kJoinWarps ? 1 : rows <= 4 * kJoinWarps ? 4 : 8;

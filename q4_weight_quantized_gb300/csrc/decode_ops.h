@@ -129,6 +129,9 @@ struct PlanArgs {
 cudaError_t launch_batch_plan(const DeviceInfo &di, const PlanArgs &a, cudaStream_t s);
 
 constexpr int kMaxChunkShares = 160;  // CTAs of an attention call over chunks, at most (the workspace holds two parts for each)
+// (api.cu; a map is kept for the pools that a thread used last)
+bool make_cache_tmap(CUtensorMap *m, const void *pool, const KvView &c, int box_values, int box_slots, bool swizzle, bool *head_first);
+
 // A unit of rows (chunk_rows() of them at most) of a sequence, the same for every KV head.
 struct alignas(16) ChunkRecord {
     int32_t b, q0, e0;          // sequence, its first row in q and o, the end of its first new token's slots
@@ -153,6 +156,8 @@ struct ChunkArgs {
     float softcap, cap_in;        // and 2 / softcap
     float v_scale;
     int32_t shares;
+    int32_t box_slots;            // slots of a tensor copy's box: what divides a page, up to 32; 0: none can be made
+    int32_t head_first;           // see make_cache_tmap
     // workspace
     int32_t *seq_at;              // [batch + 1]: first row of each sequence
     int32_t *rt_at;               // [batch + 1]: row tiles before each sequence
