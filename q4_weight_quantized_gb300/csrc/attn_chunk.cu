@@ -25,14 +25,16 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "decode_ops.h"
 #include "q4k_ptx.cuh"
 
 namespace q4k {
 namespace {
 
-constexpr int kThreads = 512;          // warps 0-3 and 4-7: softmax of a tile of rows each; 8 (9): MMA; 12-15: copies
-constexpr int kMmaWarp = 8, kCopyWarp = 12, kCopyWarps = 4;
+constexpr int kThreads = 512;          // warps 0-3 and 4-7: softmax of a tile of rows each; 8 (9): MMA; 10, 11: queries; 12-15: copies
+constexpr int kMmaWarp = 8, kQueryWarp = 10, kCopyWarp = 12, kCopyWarps = 4;
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // together those of the launch: 2 * (184 + 72) = 4 * 128
 constexpr int kPlanThreads = 1024;
 constexpr int kJoinWarps = 8;
@@ -50,14 +52,14 @@ struct Cfg {
     static constexpr int BN = D == 256 ? 64 : 128;     // slots of a tile
     static constexpr int ROWS = NT * 128;
     static constexpr int SLOT = BN * D * 2;            // bytes of a tile of keys or values in shared memory
-    static constexpr int NS = D == 64 ? 8 : 5;         // such tiles in the ring, keys and values in turn
+    static constexpr int NS = D == 64 ? 8 : E4M3 ? 4 : 5;         // such tiles in the ring, keys and values in turn
     static constexpr int LAG = NS - 2;                 // of which so many may be on their way
     // weights in f16 are kept as 2^7 p, in o' and l alike: at most 2^15, and what lies below 2^-32 of the largest is lost
     static constexpr float LIFT = E4M3 ? 7.f : 0.f;
     // how far (log2) a score may exceed the maximum that its tile's weights are taken by: what their type holds
     static constexpr float JUMP = E4M3 ? kSlack : 64.f;
     static constexpr int QBYTES = ROWS * D * 2;
-    static constexpr int MISC = 1024;
+    static constexpr int MISC = E4M3 ? 1024 + 2 * ROWS * 4 : 1024;    // barriers and flags; for an e4m3 cache the factors of two units' rows
     static constexpr int SMEM = QBYTES + NS * SLOT + MISC + 1024;  // (+ slack to align the base)
     static constexpr uint32_t S_COL = 0, O_COL = NT == 2 ? 2 * BN : 2 * BN;
     static constexpr uint32_t COLS = 512;
@@ -291,6 +293,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
 __device__ __forceinline__ float lo_f32(uint32_t bf16x2) { return __uint_as_float(bf16x2 << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t bf16x2) { return __uint_as_float(bf16x2 & 0xFFFF0000u); }
 
+// 16 consecutive fp32 columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+                   "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void set_regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -318,74 +329,42 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t pair) {
     return ((pair & kExp) == kExp ? 0x0000FFFFu : 0u) | ((pair >> 16 & kExp) == kExp ? 0xFFFF0000u : 0u);
 }
 
+// Four lanes' four 16-byte values, turned about: lane i of the four gets value i of lane k into w[k].
+__device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane) {
+    auto swap = [&](uint4 &x, uint4 &y, int bit) {  // lanes without the bit give y and get x's place
+        const bool up = lane & bit;
+        const uint4 s = up ? x : y;
+        uint4 g;
+        g.x = __shfl_xor_sync(0xFFFFFFFFu, s.x, bit), g.y = __shfl_xor_sync(0xFFFFFFFFu, s.y, bit);
+        g.z = __shfl_xor_sync(0xFFFFFFFFu, s.z, bit), g.w = __shfl_xor_sync(0xFFFFFFFFu, s.w, bit);
+        if (up) x = g;
+        else y = g;
+    };
+    swap(w[0], w[1], 1), swap(w[2], w[3], 1);
+    swap(w[0], w[2], 2), swap(w[1], w[3], 2);
+}
+
 struct Bars {
-    uint32_t full, empty, s_full, p_full, o_full, q_full, pv_done, done;
+    uint32_t full, empty, s_full, p_full, o_full, q_full, q_free, pv_done, done;
 };
 
-// A thread's row of a unit: where it is, what it sees, and its query on the way into shared memory.
-template <typename C>
+// row / group for 0 <= row < 2^31
+__device__ __forceinline__ int token_of(const ChunkArgs &a, int row) { return (int)(((uint64_t)(uint32_t)row * a.group_mul) >> a.group_shift); }
+
+// A row of a unit: where it is and what it sees.
 struct Row {
-    static constexpr int CHUNKS = C::D / 8;
-    static constexpr bool HELD = C::D <= 128;  // in registers from load() to store() (of 256 values: read by store())
-    uint4 v[HELD ? CHUNKS : 1];
-    const uint4 *src;
-    int64_t q_row;
+    int64_t q_row;        // of q and o
     int head, e, bgn;     // sees the slots [bgn, e)
     bool real;            // (the last tile of a sequence may have fewer rows)
-    float cc;             // a score's factor, to log2
-
-    __device__ __forceinline__ void of(const ChunkArgs &a, const Unit &u, int t, int row_in) {
-        const int row = u.row0 + t * 128 + row_in;
-        real = t * 128 + row_in < u.rows;
-        const int tok = real ? row / a.group : 0;
+    // row_in: of the unit
+    __device__ __forceinline__ void of(const ChunkArgs &a, const Unit &u, int row_in) {
+        const int row = u.row0 + row_in;
+        real = row_in < u.rows;
+        const int tok = real ? token_of(a, row) : 0;
         q_row = (int64_t)u.q0 + tok;
         head = u.h * a.group + (real ? row - tok * a.group : 0);
         e = real ? u.e0 + tok : 0;
         bgn = a.window > 0 && e > a.window ? (int)(e - a.window) : 0;
-        src = reinterpret_cast<const uint4 *>(a.q + q_row * a.ldq + (int64_t)head * C::D);
-    }
-    __device__ __forceinline__ void load(const ChunkArgs &, const Unit &) {
-        if constexpr (HELD) {
-#pragma unroll
-            for (int c = 0; c < CHUNKS; ++c) v[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        }
-    }
-    __device__ __forceinline__ uint4 chunk(int c) const {
-        if constexpr (HELD) return v[c];
-        else return real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-    }
-    // into the swizzled row at `dst`
-    __device__ __forceinline__ void store(const ChunkArgs &a, uint32_t dst, int swizzle) {
-        float up = 1.f;
-        cc = a.scale_log2;
-        if constexpr (C::E4M3) {
-            // f16: a power of two takes the row's largest value to [2^14, 2^15)
-            uint32_t top = 0;
-#pragma unroll
-            for (int c = 0; c < CHUNKS; ++c) {
-                const uint4 w = chunk(c);
-                top = max(top, max(max(w.x << 16 & 0x7FFFFFFFu, w.x & 0x7FFF0000u), max(w.y << 16 & 0x7FFFFFFFu, w.y & 0x7FFF0000u)));
-                top = max(top, max(max(w.z << 16 & 0x7FFFFFFFu, w.z & 0x7FFF0000u), max(w.w << 16 & 0x7FFFFFFFu, w.w & 0x7FFF0000u)));
-            }
-            const int ex = (int)(top >> 23);
-            // (a row that is not finite gives NaN either way)
-            const int shift = ex == 255 ? 0 : min(127 + 14 - ex, 126);
-            up = __uint_as_float((uint32_t)(127 + shift) << 23);
-            cc *= __uint_as_float((uint32_t)(127 - shift) << 23);
-        }
-#pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-            uint4 w = chunk(c);
-            if constexpr (C::E4M3) {
-                const float s = a.q_sign ? -up : up;
-                w.x = pack_f16(lo_f32(w.x) * s, hi_f32(w.x) * s), w.y = pack_f16(lo_f32(w.y) * s, hi_f32(w.y) * s);
-                w.z = pack_f16(lo_f32(w.z) * s, hi_f32(w.z) * s), w.w = pack_f16(lo_f32(w.w) * s, hi_f32(w.w) * s);
-            } else {
-                w.x ^= a.q_sign, w.y ^= a.q_sign, w.z ^= a.q_sign, w.w ^= a.q_sign;
-            }
-            if (a.q_zero) w = make_uint4(0, 0, 0, 0);
-            sts128(dst + (c / 8) * (128 * 128) + ((c % 8) ^ swizzle) * 16, w);
-        }
     }
 };
 
@@ -408,11 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
     uint8_t *const misc_p = base + C::QBYTES + NS * C::SLOT;
     Bars bar;
     bar.full = misc, bar.empty = bar.full + 8 * NS, bar.s_full = bar.empty + 8 * NS, bar.p_full = bar.s_full + 16;
-    bar.o_full = bar.p_full + 16, bar.q_full = bar.o_full + 16, bar.pv_done = bar.q_full + 16, bar.done = bar.pv_done + 16;
+    bar.o_full = bar.p_full + 16, bar.q_full = bar.o_full + 16, bar.q_free = bar.q_full + 16, bar.pv_done = bar.q_free + 16, bar.done = bar.pv_done + 16;
     uint32_t *const tmem_holder = reinterpret_cast<uint32_t *>(misc_p + 512);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc_p + 516);
     volatile int *const bad_pages = reinterpret_cast<volatile int *>(misc_p + 524); // a page id was out of range
     volatile int *const bad_seen = reinterpret_cast<volatile int *>(misc_p + 520);  // a value that is not finite was taken out
+    float *const q_factor = reinterpret_cast<float *>(misc_p + 1024);                               // [2][C::ROWS]
     volatile uint32_t *const page_mask = reinterpret_cast<volatile uint32_t *>(misc_p + 640);      // [kMetaRing][4]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int *const status = a.c.status;
@@ -426,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
             mbar_init(bar.s_full + 8 * t, 1);
             mbar_init(bar.p_full + 8 * t, 4);
             mbar_init(bar.o_full + 8 * t, 1);
-            mbar_init(bar.q_full + 8 * t, 4);
+            mbar_init(bar.q_full + 8 * t, NT == 2 ? 1 : 2);  // the warps that bring a tile's queries
+            mbar_init(bar.q_free + 8 * t, 1);
             mbar_init(bar.pv_done + 8 * t, 1);
         }
         mbar_init(bar.done, NT == 2 ? 1 : 2);
@@ -465,23 +446,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
             }
             return false;
         };
-        Row<C> r;
-        bool more = t < NT && advance(u);
-        if (more) {
-            r.of(a, u, t, row_in);
-            r.load(a, u);
-            r.store(a, q_smem + t * (128 * D * 2) + row_in * 128, row_in & 7);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar.q_full + 8 * t);
-        }
-        while (more) {
+        Row r;
+        uint32_t units = 0;
+        for (bool more = t < NT && advance(u); more; more = advance(u), ++units) {
+            r.of(a, u, t * 128 + row_in);
             // ---- what the tile's rows see
             // every row of the tile sees slots below all_end and from all_begin on
-            const int last_tok = (min(t * 128 + 127, u.rows - 1) + u.row0) / a.group;
-            const uint32_t all_end = (uint32_t)max(0, u.e0 + (u.row0 + t * 128) / a.group);
+            const int last_tok = token_of(a, min(t * 128 + 127, u.rows - 1) + u.row0);
+            const uint32_t all_end = (uint32_t)max(0, u.e0 + token_of(a, u.row0 + t * 128));
             const uint32_t all_begin = a.window > 0 && (int64_t)u.e0 + last_tok > a.window ? (uint32_t)(u.e0 + last_tok - a.window) : 0u;
-            const float f = a.softcap > 0.f ? 1.f : r.cc;
+            float cc = a.scale_log2, f = a.softcap > 0.f ? 1.f : cc;  // a score's factor, to log2
             // neg: -m f, or 0 where there is no maximum yet (rows that are not there have one: 0)
             float m = r.real ? -INFINITY : 0.f, l = 0.f, m_next = m, neg = 0.f;
             // what holds for all rows of the warp: a maximum is to be raised; each has one, and none is far from 0
@@ -523,63 +497,108 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                     break;
                 }
                 tc_fence_after();
+                if constexpr (C::E4M3) {
+                    if (i == u.lo) {  // (written before the tile's queries were there)
+                        cc = a.scale_log2 * q_factor[(units & 1) * C::ROWS + t * 128 + row_in];
+                        f = a.softcap > 0.f ? 1.f : cc;
+                    }
+                }
                 const uint32_t s_col = tmem + lanes + C::S_COL + at * BN;
-                uint32_t s[2][32];
-                tmem_ld32(s_col, s[0]);
+                uint32_t s[2][16];
+                tmem_ld16(s_col, s[0]);
                 const uint32_t j0 = (uint32_t)(u.base + i) * BN;
-                const bool pages = *bad_pages != 0, masked = j0 + BN > all_end || j0 < all_begin || pages;
+                const bool pages = *bad_pages != 0, masked = j0 + BN > all_end || j0 < all_begin, odd_tile = a.softcap > 0.f || a.odd_scale || far;
                 if (pending && !raise(i > u.lo)) {
                     ok = false;
                     break;
                 }
-                // ---- the usual tile: weights by the maximum so far, in one pass; a larger one counts from the next tile on
+                const int from = (int)max((int64_t)0, (int64_t)r.bgn - j0), to = (int)min((int64_t)BN, (int64_t)r.e - j0);
                 bool done = false;
-                if (!masked && usual) {
-                    uint32_t p[BN / 2];
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    float top[2] = {-INFINITY, -INFINITY};
-                    const float2 f2 = make_float2(f, f), n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
-                    tmem_ld_wait();
+                if (!odd_tile && !pages) {
+                    // ---- weights by the maximum so far, in one pass; a larger one counts from the next tile on
+                    auto one_pass = [&](auto masks) {
+                        constexpr bool MASK = decltype(masks)::value;
+                        uint32_t p[BN / 2];
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        float top[2] = {-INFINITY, -INFINITY};
+                        const float2 f2 = make_float2(f, f), n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < BN / 32; ++c) {
-                        if (c + 1 < BN / 32) tmem_ld32(s_col + 32 * (c + 1), s[(c + 1) & 1]);
-                        const uint32_t (&v)[32] = s[c & 1];
+                        for (int c = 0; c < BN / 16; ++c) {
+                            if (c + 1 < BN / 16) tmem_ld16(s_col + 16 * (c + 1), s[(c + 1) & 1]);
+                            const uint32_t (&v)[16] = s[c & 1];
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            const float x = __uint_as_float(v[k]), y = __uint_as_float(v[k + 1]);
-                            top[k / 2 & 1] = fmaxf(fmaxf(top[k / 2 & 1], x), y);
-                            const float2 z = fma2(make_float2(x, y), f2, n2);
-                            const float2 e = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-                            sum[k / 2 & 1] = add2(sum[k / 2 & 1], e);
-                            p[16 * c + k / 2] = C::E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+                            for (int k = 0; k < 16; k += 2) {
+                                float x = __uint_as_float(v[k]), y = __uint_as_float(v[k + 1]);
+                                if constexpr (MASK) {
+                                    x = 16 * c + k >= from && 16 * c + k < to ? x : -INFINITY;
+                                    y = 16 * c + k + 1 >= from && 16 * c + k + 1 < to ? y : -INFINITY;
+                                }
+                                top[k / 2 & 1] = fmaxf(fmaxf(top[k / 2 & 1], x), y);
+                                const float2 z = fma2(make_float2(x, y), f2, n2);
+                                const float2 e = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+                                sum[k / 2 & 1] = add2(sum[k / 2 & 1], e);
+                                p[8 * c + k / 2] = C::E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+                            }
+                            if (c + 1 < BN / 16) tmem_ld_wait();
                         }
-                        if (c + 1 < BN / 32) tmem_ld_wait();
-                    }
-                    const float mx = fmaxf(top[0], top[1]), above = (mx - m) * f;
-                    pending = __any_sync(0xFFFFFFFFu, above > kSlack);
-                    done = !pending || !__any_sync(0xFFFFFFFFu, above > C::JUMP);
-                    if (done) {
-                        if (above > kSlack) m_next = mx;
-                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                        const float mx = fmaxf(top[0], top[1]), above = (mx - m) * f;
+                        pending = __any_sync(0xFFFFFFFFu, above > kSlack);
+                        done = !pending || !__any_sync(0xFFFFFFFFu, above > C::JUMP);
+                        if (done) {
+                            if (above > kSlack) m_next = mx;
+                            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 #pragma unroll
-                        for (int c = 0; c < BN / 32; ++c) tmem_st16(s_col + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(p + 16 * c));
+                            for (int c = 0; c < BN / 32; ++c) tmem_st16(s_col + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(p + 16 * c));
+                        }
+                    };
+                    if (usual && !masked) one_pass(std::false_type{});
+                    if (!done) {
+                        // a first tile, rows without a maximum, a score far above it: the maximum of what a row sees first
+                        if (!usual || !masked) {
+                            float mx = -INFINITY;
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int c = 0; c < BN / 16; ++c) {
+                                if (c + 1 < BN / 16) tmem_ld16(s_col + 16 * (c + 1), s[(c + 1) & 1]);
+                                const uint32_t (&v)[16] = s[c & 1];
+#pragma unroll
+                                for (int k = 0; k < 16; k += 2) {
+                                    float x = __uint_as_float(v[k]), y = __uint_as_float(v[k + 1]);
+                                    x = 16 * c + k >= from && 16 * c + k < to ? x : -INFINITY;
+                                    y = 16 * c + k + 1 >= from && 16 * c + k + 1 < to ? y : -INFINITY;
+                                    mx = fmaxf(fmaxf(mx, x), y);
+                                }
+                                if (c + 1 < BN / 16) tmem_ld_wait();
+                            }
+                            if (m == -INFINITY ? mx > -INFINITY : (mx - m) * f > kSlack) m_next = mx;
+                            if (__any_sync(0xFFFFFFFFu, m_next != m) && !raise(i > u.lo)) {
+                                ok = false;
+                                break;
+                            }
+                            pending = false;
+                            usual = !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
+                            tmem_ld16(s_col, s[0]);
+                        }
+                        if (!far) one_pass(std::true_type{});
                     }
                 }
                 if (!done) {
                     tmem_ld_wait();
-                    // ---- two passes: the maximum of what a row sees, then the weights
-                    const int from = (int)max((int64_t)0, (int64_t)r.bgn - j0), to = (int)min((int64_t)BN, (int64_t)r.e - j0);
-                    const float in = a.cap_in * r.cc, out = a.softcap * kLog2e;
+                    // ---- soft caps, scales that are not positive, pages out of range, maxima far from 0: two passes, a group of 32 slots at a time
+                    const float in = a.cap_in * cc, out = a.softcap * kLog2e;
                     auto scores = [&](int c, float (&s)[32]) {
                         tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s));
                         uint32_t there = 0xFFFFFFFFu;
-                        if (masked) {
-                            if (pages) there = page_mask[(tile_count & (kMetaRing - 1)) * 4 + c];
-                            const int lo = from - 32 * c, hi = to - 32 * c;
-                            there &= lo <= 0 ? 0xFFFFFFFFu : lo >= 32 ? 0u : 0xFFFFFFFFu << lo;
-                            there &= hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
-                        }
+                        if (pages) there = page_mask[(tile_count & (kMetaRing - 1)) * 4 + c];
+                        const int lo = from - 32 * c, hi = to - 32 * c;
+                        there &= lo <= 0 ? 0xFFFFFFFFu : lo >= 32 ? 0u : 0xFFFFFFFFu << lo;
+                        there &= hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
                         tmem_ld_wait();
+                        if (a.odd_scale) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) s[k] *= a.score_sign;
+                        }
                         if (a.softcap > 0.f) {
                             // c tanh(s / c) = c (1 - 2 / (1 + e^(2 s / c))), in units of log2
 #pragma unroll
@@ -602,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                         break;
                     }
                     pending = false;
-                    usual = a.softcap == 0.f && !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
+                    usual = !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
 #pragma unroll 1
                     for (int c = 0; c < BN / 32; ++c) {  // (a group's weights lie over scores that have been read)
                         float s[32];
@@ -627,32 +646,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                 if (lane == 0) mbar_arrive(bar.p_full + 8 * at);
             }
             if (!ok) break;
-            // ---- the unit's end; the next one's queries are on their way meanwhile, and its first scores
-            const Unit of = u;
+            // ---- the unit's end
             const int64_t q_row = r.q_row;
             const int head = r.head, e = r.e, bgn = r.bgn;
             const bool real = r.real;
-            more = advance(u);
-            if (more) {
-                r.of(a, u, t, row_in);
-                r.load(a, u);
-            }
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar.o_full + 8 * t, unit_phase, status))) {
                 ok = false;
                 break;
             }
             unit_phase ^= 1;
             tc_fence_after();
-            if (more) {
-                r.store(a, q_smem + t * (128 * D * 2) + row_in * 128, row_in & 7);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar.q_full + 8 * t);
-            }
             const bool bad = *bad_seen != 0;
             // a row that sees slots, all of them -infinity, has no weights: NaN, as 0 / 0 has it
             const float inv = e > bgn ? a.v_scale / l : 0.f;
-            const int64_t part_row = (int64_t)(2 * blockIdx.x + (of.lo > 0 ? 0 : 1)) * C::ROWS + t * 128 + row_in;
+            const int64_t part_row = (int64_t)(2 * blockIdx.x + (u.lo > 0 ? 0 : 1)) * C::ROWS + t * 128 + row_in;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -660,15 +667,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                 tmem_ld_wait();
                 if (bad && real) {
                     // values that are not finite in tiles that not every row of the unit sees (the copies took them out)
-                    for (int i = of.lo; i < of.hi; ++i) {
-                        const int64_t j0 = (int64_t)(of.base + i) * BN;
-                        if (j0 + BN <= of.all_end && j0 >= of.all_begin) continue;
+                    for (int i = u.lo; i < u.hi; ++i) {
+                        const int64_t j0 = (int64_t)(u.base + i) * BN;
+                        if (j0 + BN <= u.all_end && j0 >= u.all_begin) continue;
                         const int64_t to = min((int64_t)e, j0 + BN);
                         for (int64_t j = max((int64_t)bgn, j0); j < to; ++j) {
                             const uint32_t pg = page_of(a.c, (uint32_t)j);
-                            const int32_t page = __ldg(a.c.table + of.b * a.c.ld_table + pg);
+                            const int32_t page = __ldg(a.c.table + u.b * a.c.ld_table + pg);
                             if (!page_ok(a.c, page)) continue;
-                            const uint8_t *v = a.c.v + row_bytes_at(a.c, page, of.h, (uint32_t)j - pg * a.c.page_size);
+                            const uint8_t *v = a.c.v + row_bytes_at(a.c, page, u.h, (uint32_t)j - pg * a.c.page_size);
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
                                 float x;
@@ -679,26 +686,44 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                         }
                     }
                 }
-                if (!real) continue;
-                if (of.whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.o + q_row * a.ldo + (int64_t)head * D + 32 * c);
+                // a thread has 32 values of its row; four lanes exchange theirs, so that they write four rows one after the
+                // other, 64 bytes (or 128) of each at a time instead of 16 bytes of 32 rows
+                if (u.whole) {
+                    uint4 w[4];
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
-                        uint32_t w[4];
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t x[4];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const float y = __uint_as_float(o[k + 2 * x]) * inv, z = __uint_as_float(o[k + 2 * x + 1]) * inv;
-                            w[x] = e > bgn ? pack_bf16(y, z) : 0u;
+                        for (int y = 0; y < 4; ++y) {
+                            const float lo = __uint_as_float(o[8 * k + 2 * y]) * inv, hi = __uint_as_float(o[8 * k + 2 * y + 1]) * inv;
+                            x[y] = e > bgn ? pack_bf16(lo, hi) : 0u;
                         }
-                        dst[k / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                        w[k] = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                    transpose4(w, lane);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int64_t to = __shfl_sync(0xFFFFFFFFu, real ? q_row * a.ldo + (int64_t)head * D : (int64_t)-1, (lane & ~3) + k);
+                        if (to >= 0) reinterpret_cast<uint4 *>(a.o + to + 32 * c)[lane & 3] = w[k];
                     }
                 } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.parts + part_row * D + 32 * c);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) dst[k / 4] = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    for (int half = 0; half < 2; ++half) {
+                        uint4 w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = make_uint4(o[16 * half + 4 * k], o[16 * half + 4 * k + 1], o[16 * half + 4 * k + 2], o[16 * half + 4 * k + 3]);
+                        transpose4(w, lane);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int row = t * 128 + (row_in & ~3) + k;
+                            if (row < u.rows)
+                                reinterpret_cast<uint4 *>(a.parts + (part_row - row_in - t * 128 + row) * D + 32 * c + 16 * half)[lane & 3] = w[k];
+                        }
+                    }
                 }
             }
-            if (!of.whole && real) a.part_ml[part_row] = make_float2(m == -INFINITY ? -INFINITY : -neg, l);
+            if (!u.whole && real) a.part_ml[part_row] = make_float2(m == -INFINITY ? -INFINITY : -neg, l);
             tc_fence_before();
         }
         if (!ok && lane == 0) *abort_flag = 1;
@@ -754,6 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                         unit_phase ^= 1u << t;
                         tc_fence_after();
                         qk(t, t);
+                        if (tiles == 1) umma_commit(bar.q_free + 8 * t);
                     }
                     if (!ok) break;
                     umma_commit(bar.empty + 8 * slot);
@@ -776,6 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                                 if (!(ok = wait_full())) break;
                             }
                             qk(t, t);
+                            if (i + 2 == tiles) umma_commit(bar.q_free + 8 * t);  // the unit's last scores
                         }
                         if (!ok) break;
                         umma_commit(bar.empty + 8 * v_slot);
@@ -795,6 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                             if (count >= 2 && !(ok = mbar_wait(bar.pv_done + 8 * buf, of ^ 1, status))) break;
                             tc_fence_after();
                             qk(0, buf);
+                            if (i + 1 == tiles) umma_commit(bar.q_free);
                             umma_commit(bar.empty + 8 * slot);
                         }
                         next_slot();
@@ -811,6 +839,61 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
             }
             if (!ok) *abort_flag = 1;
             umma_commit(bar.done);
+        } else if (warp >= kQueryWarp) {
+            // ---------------------------------------------------- queries
+            // A warp brings a tile's 128 rows (heads of 256: 64 of them each), as soon as the scores of the unit before are done.
+            constexpr int LANES = D / 8 < 32 ? D / 8 : 32, AT_ONCE = 32 / LANES;  // of a row, 16 bytes each; rows of an access
+            constexpr int ROWS = NT == 2 ? 128 : 64;
+            const int t = NT == 2 ? warp - kQueryWarp : 0, row0 = NT == 2 ? 0 : (warp - kQueryWarp) * 64;
+            const int c = lane % LANES;
+            const uint32_t dst = q_smem + t * (128 * D * 2) + (c / 8) * (128 * 128);
+            uint32_t units = 0;
+            bool ok = true;
+            while (ok && next_unit<C>(a, walk, u)) {
+                if (t * 128 >= u.rows) continue;
+                if (units > 0 && (!__all_sync(0xFFFFFFFFu, mbar_wait(bar.q_free + 8 * t, (units - 1) & 1, status)) || *abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                for (int r0 = row0; r0 < row0 + ROWS; r0 += 32) {
+                    Row r;
+                    r.of(a, u, t * 128 + r0 + lane);
+                    const int64_t at = r.real ? r.q_row * a.ldq + (int64_t)r.head * D : -1;
+#pragma unroll 4
+                    for (int s = 0; s < 32; s += AT_ONCE) {
+                        const int row = r0 + s + lane / LANES;
+                        const int64_t from = __shfl_sync(0xFFFFFFFFu, at, s + lane / LANES);
+                        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (from >= 0 ? from : 0)) + c;
+                        const uint32_t to = dst + row * 128 + ((c ^ row) & 7) * 16;
+                        if constexpr (C::E4M3) {
+                            // f16: a power of two takes the row's largest value to [2^14, 2^15)
+                            uint4 w = from >= 0 ? __ldg(src) : make_uint4(0, 0, 0, 0);
+                            uint32_t top = max(max(w.x << 16 & 0x7FFFFFFFu, w.x & 0x7FFF0000u), max(w.y << 16 & 0x7FFFFFFFu, w.y & 0x7FFF0000u));
+                            top = max(top, max(max(w.z << 16 & 0x7FFFFFFFu, w.z & 0x7FFF0000u), max(w.w << 16 & 0x7FFFFFFFu, w.w & 0x7FFF0000u)));
+#pragma unroll
+                            for (int o = LANES / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                            const int ex = (int)(top >> 23);
+                            // (a row that is not finite gives NaN either way)
+                            const int shift = ex == 255 ? 0 : min(127 + 14 - ex, 126);
+                            const float f = __uint_as_float((uint32_t)(127 + shift) << 23);
+                            w.x = pack_f16(lo_f32(w.x) * f, hi_f32(w.x) * f), w.y = pack_f16(lo_f32(w.y) * f, hi_f32(w.y) * f);
+                            w.z = pack_f16(lo_f32(w.z) * f, hi_f32(w.z) * f), w.w = pack_f16(lo_f32(w.w) * f, hi_f32(w.w) * f);
+                            sts128(to, w);
+                            // the way back, for the row's softmax (which has read those of two units before)
+                            if (c == 0) q_factor[(units & 1) * C::ROWS + t * 128 + row] = __uint_as_float((uint32_t)(127 - shift) << 23);
+                        } else {
+                            cp_async16(to, src, from >= 0 ? 16u : 0u);
+                        }
+                    }
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar.q_full + 8 * t);
+                ++units;
+            }
+            if (!ok && lane == 0) *abort_flag = 1;
         }
     } else {
         // -------------------------------------------------------- copies
@@ -838,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
         // this warp's part of a tile has landed: checked if need be, and shown to the MMAs
         auto check = [&](uint32_t at) {
             bool any = false;
-#pragma unroll 1
+#pragma unroll 2
             for (int s = 0; s < STEPS; ++s) {
 #pragma unroll
                 for (int x = 0; x < PIECES * (C::E4M3 ? 2 : 1); ++x) {
@@ -1019,12 +1102,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const ChunkArgs a
     load_record(a, rt, u);
     int last = s;                                                              // the share that holds its end
     while (last + 1 < shares && share_at(total, shares, last + 1) < end) ++last;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, parts = last - s + 2;
     for (int row_in = blockIdx.y * kJoinWarps + warp; row_in < u.rows; row_in += gridDim.y * kJoinWarps) {
-        auto part = [&](int k) { return (int64_t)(2 * k + (k == s - 1 ? 1 : 0)) * C::ROWS + row_in; };
-        float m = -INFINITY;
-        bool number = true;
-        for (int k = s - 1 + lane; k <= last; k += 32) {
+        // part k of the row: of share s - 1 + k
+        auto part = [&](int k) { return (int64_t)(2 * (s - 1 + k) + (k == 0 ? 1 : 0)) * C::ROWS + row_in; };
+        const float2 nothing = make_float2(-INFINITY, 0.f);
+        float2 own = lane < parts ? __ldcg(a.part_ml + part(lane)) : nothing;  // (a lane's first part stays at hand)
+        float m = own.x;
+        bool number = own.x == own.x;
+        for (int k = lane + 32; k < parts; k += 32) {
             const float x = __ldcg(a.part_ml + part(k)).x;
             m = fmaxf(m, x);
             if (x != x) number = false;
@@ -1033,14 +1119,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const ChunkArgs a
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         if (!__all_sync(0xFFFFFFFFu, number)) m = __uint_as_float(0x7FC00000u);
         float l = 0.f, o[PER] = {};
-        for (int k = s - 1; k <= last; ++k) {
-            const float2 ml = __ldcg(a.part_ml + part(k));
-            if (ml.x == -INFINITY && ml.y == 0.f) continue;  // it saw nothing
-            const float w = ex2_approx(ml.x - m);
-            l = fmaf(ml.y, w, l);
-            const float *p = a.parts + part(k) * D + lane * PER;
+        for (int k0 = 0; k0 < parts; k0 += 4) {  // four parts' values on their way at once
+            float x[4][PER], w[4];
 #pragma unroll
-            for (int x = 0; x < PER; ++x) o[x] = fmaf(__ldcg(p + x), w, o[x]);
+            for (int i = 0; i < 4; ++i) {
+                const int k = k0 + i;
+                float2 ml = make_float2(__shfl_sync(0xFFFFFFFFu, own.x, k & 31), __shfl_sync(0xFFFFFFFFu, own.y, k & 31));
+                if (k >= 32 && k < parts) ml = __ldcg(a.part_ml + part(k));
+                const bool there = k < parts && !(ml.x == -INFINITY && ml.y == 0.f);  // (it saw something)
+                w[i] = there ? ex2_approx(ml.x - m) : 0.f;
+                if (there) l = fmaf(ml.y, w[i], l);
+                const float2 *p = reinterpret_cast<const float2 *>(a.parts + part(there ? k : 0) * D + lane * PER);
+#pragma unroll
+                for (int y = 0; y < PER; y += 2) {
+                    const float2 t = there ? __ldcg(p + y / 2) : make_float2(0.f, 0.f);
+                    x[i][y] = t.x, x[i][y + 1] = t.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int y = 0; y < PER; ++y) o[y] = fmaf(x[i][y], w[i], o[y]);
         }
         const int row = u.row0 + row_in, tok = row / a.group, e = u.e0 + tok;
         const int bgn = a.window > 0 && e > a.window ? (int)(e - a.window) : 0;
@@ -1072,9 +1171,9 @@ cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
                           make_cache_tmap(&v_map, a.c.v, a.c, 64, box, true, &head_first) ? box : 0;
     a.head_first = head_first;
     if ((e = launch_pdl(chunk_kernel<C>, dim3(a.shares), dim3(kThreads), C::SMEM, s, dim3(1), a, k_map, v_map)) != cudaSuccess) return e;
-    // rows of a unit over 8 CTAs, fewer where the call has few rows
+    // rows of a unit over 16 CTAs, fewer where the call has few rows
     const int64_t rows = a.T * a.group;
-    const int y = rows <= kJoinWarps ? 1 : rows <= 4 * kJoinWarps ? 4 : 8;
+    const int y = rows <= kJoinWarps ? 1 : rows <= 4 * kJoinWarps ? 4 : 16;
     return launch_pdl(join_kernel<C>, dim3(a.shares, y), dim3(kJoinWarps * 32), 0, s, dim3(1), a);
 }
 

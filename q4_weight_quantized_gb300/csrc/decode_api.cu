@@ -45,6 +45,14 @@ q4k_status cache_check(const q4k_kv_cache *c) {
     return Q4K_OK;
 }
 
+// n / d = n * the result >> *shift for 0 <= n < 2^31
+uint32_t division(int32_t d, uint32_t *shift) {
+    uint32_t l = 0;
+    while (((uint64_t)1 << l) < (uint64_t)d) ++l;
+    *shift = 31 + l;
+    return (uint32_t)((((uint64_t)1 << *shift) + d - 1) / d);
+}
+
 KvView view(const q4k_kv_cache *c, const DeviceInfo &di) {
     const int64_t e = c->dtype == Q4K_KV_E4M3 ? 1 : 2;
     KvView v = {};
@@ -61,10 +69,7 @@ KvView view(const q4k_kv_cache *c, const DeviceInfo &di) {
     v.page_size = c->page_size;
     v.heads = c->n_kv_heads;
     v.capacity = c->max_pages * c->page_size;
-    uint32_t l = 0;
-    while (((uint64_t)1 << l) < (uint64_t)c->page_size) ++l;
-    v.div_shift = 31 + l;
-    v.div_mul = (uint32_t)((((uint64_t)1 << v.div_shift) + c->page_size - 1) / c->page_size);
+    v.div_mul = division(c->page_size, &v.div_shift);
     v.dim = c->head_dim;
     v.e4m3 = c->dtype == Q4K_KV_E4M3;
     v.k_scale = c->k_scale;
@@ -502,9 +507,10 @@ q4k_status q4k_attn_chunk(const q4k_kv_cache *cache, const int32_t *starts, cons
     a.q = q, a.T = T, a.ldq = ldq, a.o = o, a.ldo = ldo;
     a.group = n_heads / cache->n_kv_heads;
     a.window = window < kInt31 ? window : 0;  // no sequence is that long
-    a.q_sign = scale < 0.f ? 0x80008000u : 0u;
-    a.q_zero = scale == 0.f;
-    a.scale_log2 = a.q_zero ? 1.f : std::fabs(scale) * cache->k_scale * 1.4426950408889634f;
+    a.odd_scale = !(scale > 0.f);
+    a.score_sign = scale < 0.f ? -1.f : scale > 0.f ? 1.f : 0.f;
+    a.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * cache->k_scale * 1.4426950408889634f;
+    a.group_mul = division(a.group, &a.group_shift);
     a.softcap = softcap;
     a.cap_in = softcap > 0.f ? 2.f / softcap : 0.f;
     a.v_scale = cache->v_scale;

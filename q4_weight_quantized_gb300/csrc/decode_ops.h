@@ -151,8 +151,9 @@ struct ChunkArgs {
     int32_t group;
     int64_t window;
     float scale_log2;             // |scale| * k_scale * log2(e)
-    uint32_t q_sign;              // flips the signs of a pair of 16-bit values, for a negative scale
-    int32_t q_zero;               // a scale of 0
+    int32_t odd_scale;            // a scale that is not positive: scores times score_sign first
+    float score_sign;
+    uint32_t group_mul, group_shift;  // row / group for 0 <= row < 2^31 (see KvView)
     float softcap, cap_in;        // and 2 / softcap
     float v_scale;
     int32_t shares;
