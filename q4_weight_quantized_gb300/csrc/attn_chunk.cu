@@ -25,8 +25,6 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <type_traits>
-
 #include "decode_ops.h"
 #include "q4k_ptx.cuh"
 
@@ -293,15 +291,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
 __device__ __forceinline__ float lo_f32(uint32_t bf16x2) { return __uint_as_float(bf16x2 << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t bf16x2) { return __uint_as_float(bf16x2 & 0xFFFF0000u); }
 
-// 16 consecutive fp32 columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-                   "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                 : "r"(taddr)
-                 : "memory");
-}
-
 template <int N>
 __device__ __forceinline__ void set_regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -504,96 +493,63 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                     }
                 }
                 const uint32_t s_col = tmem + lanes + C::S_COL + at * BN;
-                uint32_t s[2][16];
-                tmem_ld16(s_col, s[0]);
+                uint32_t s[2][32];
+                tmem_ld32(s_col, s[0]);
                 const uint32_t j0 = (uint32_t)(u.base + i) * BN;
-                const bool pages = *bad_pages != 0, masked = j0 + BN > all_end || j0 < all_begin, odd_tile = a.softcap > 0.f || a.odd_scale || far;
+                const bool pages = *bad_pages != 0, masked = j0 + BN > all_end || j0 < all_begin;
                 if (pending && !raise(i > u.lo)) {
                     ok = false;
                     break;
                 }
-                const int from = (int)max((int64_t)0, (int64_t)r.bgn - j0), to = (int)min((int64_t)BN, (int64_t)r.e - j0);
                 bool done = false;
-                if (!odd_tile && !pages) {
+                if (usual && !masked && !pages) {
                     // ---- weights by the maximum so far, in one pass; a larger one counts from the next tile on
-                    auto one_pass = [&](auto masks) {
-                        constexpr bool MASK = decltype(masks)::value;
-                        uint32_t p[BN / 2];
-                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                        float top[2] = {-INFINITY, -INFINITY};
-                        const float2 f2 = make_float2(f, f), n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
-                        tmem_ld_wait();
+                    uint32_t p[BN / 2];
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    float top[2] = {-INFINITY, -INFINITY};
+                    const float2 f2 = make_float2(f, f), n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int c = 0; c < BN / 16; ++c) {
-                            if (c + 1 < BN / 16) tmem_ld16(s_col + 16 * (c + 1), s[(c + 1) & 1]);
-                            const uint32_t (&v)[16] = s[c & 1];
+                    for (int c = 0; c < BN / 32; ++c) {
+                        if (c + 1 < BN / 32) tmem_ld32(s_col + 32 * (c + 1), s[(c + 1) & 1]);
+                        const uint32_t (&v)[32] = s[c & 1];
 #pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                float x = __uint_as_float(v[k]), y = __uint_as_float(v[k + 1]);
-                                if constexpr (MASK) {
-                                    x = 16 * c + k >= from && 16 * c + k < to ? x : -INFINITY;
-                                    y = 16 * c + k + 1 >= from && 16 * c + k + 1 < to ? y : -INFINITY;
-                                }
-                                top[k / 2 & 1] = fmaxf(fmaxf(top[k / 2 & 1], x), y);
-                                const float2 z = fma2(make_float2(x, y), f2, n2);
-                                const float2 e = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-                                sum[k / 2 & 1] = add2(sum[k / 2 & 1], e);
-                                p[8 * c + k / 2] = C::E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
-                            }
-                            if (c + 1 < BN / 16) tmem_ld_wait();
+                        for (int k = 0; k < 32; k += 2) {
+                            const float x = __uint_as_float(v[k]), y = __uint_as_float(v[k + 1]);
+                            top[k / 2 & 1] = fmaxf(fmaxf(top[k / 2 & 1], x), y);
+                            const float2 z = fma2(make_float2(x, y), f2, n2);
+                            const float2 e = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+                            sum[k / 2 & 1] = add2(sum[k / 2 & 1], e);
+                            p[16 * c + k / 2] = C::E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
                         }
-                        const float mx = fmaxf(top[0], top[1]), above = (mx - m) * f;
-                        pending = __any_sync(0xFFFFFFFFu, above > kSlack);
-                        done = !pending || !__any_sync(0xFFFFFFFFu, above > C::JUMP);
-                        if (done) {
-                            if (above > kSlack) m_next = mx;
-                            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                        if (c + 1 < BN / 32) tmem_ld_wait();
+                    }
+                    const float mx = fmaxf(top[0], top[1]), above = (mx - m) * f;
+                    pending = __any_sync(0xFFFFFFFFu, above > kSlack);
+                    done = !pending || !__any_sync(0xFFFFFFFFu, above > C::JUMP);
+                    if (done) {
+                        if (above > kSlack) m_next = mx;
+                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 #pragma unroll
-                            for (int c = 0; c < BN / 32; ++c) tmem_st16(s_col + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(p + 16 * c));
-                        }
-                    };
-                    if (usual && !masked) one_pass(std::false_type{});
-                    if (!done) {
-                        // a first tile, rows without a maximum, a score far above it: the maximum of what a row sees first
-                        if (!usual || !masked) {
-                            float mx = -INFINITY;
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int c = 0; c < BN / 16; ++c) {
-                                if (c + 1 < BN / 16) tmem_ld16(s_col + 16 * (c + 1), s[(c + 1) & 1]);
-                                const uint32_t (&v)[16] = s[c & 1];
-#pragma unroll
-                                for (int k = 0; k < 16; k += 2) {
-                                    float x = __uint_as_float(v[k]), y = __uint_as_float(v[k + 1]);
-                                    x = 16 * c + k >= from && 16 * c + k < to ? x : -INFINITY;
-                                    y = 16 * c + k + 1 >= from && 16 * c + k + 1 < to ? y : -INFINITY;
-                                    mx = fmaxf(fmaxf(mx, x), y);
-                                }
-                                if (c + 1 < BN / 16) tmem_ld_wait();
-                            }
-                            if (m == -INFINITY ? mx > -INFINITY : (mx - m) * f > kSlack) m_next = mx;
-                            if (__any_sync(0xFFFFFFFFu, m_next != m) && !raise(i > u.lo)) {
-                                ok = false;
-                                break;
-                            }
-                            pending = false;
-                            usual = !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
-                            tmem_ld16(s_col, s[0]);
-                        }
-                        if (!far) one_pass(std::true_type{});
+                        for (int c = 0; c < BN / 32; ++c) tmem_st16(s_col + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(p + 16 * c));
                     }
                 }
                 if (!done) {
+                    // ---- a unit's first tile, its edges, a score far above the maximum, soft caps, scales that are not positive,
+                    // pages out of range, maxima far from 0: two passes, 32 slots at a time; slots that no row of the warp sees
+                    // are passed over
                     tmem_ld_wait();
-                    // ---- soft caps, scales that are not positive, pages out of range, maxima far from 0: two passes, a group of 32 slots at a time
+                    const int from = (int)max((int64_t)0, (int64_t)r.bgn - j0), to = (int)min((int64_t)BN, (int64_t)r.e - j0);
                     const float in = a.cap_in * cc, out = a.softcap * kLog2e;
-                    auto scores = [&](int c, float (&s)[32]) {
-                        tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s));
+                    auto seen = [&](int c) {  // a bit for each slot
                         uint32_t there = 0xFFFFFFFFu;
                         if (pages) there = page_mask[(tile_count & (kMetaRing - 1)) * 4 + c];
                         const int lo = from - 32 * c, hi = to - 32 * c;
                         there &= lo <= 0 ? 0xFFFFFFFFu : lo >= 32 ? 0u : 0xFFFFFFFFu << lo;
-                        there &= hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
+                        return there & (hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u);
+                    };
+                    auto scores = [&](int c, uint32_t there, float (&s)[32]) {
+                        tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s));
                         tmem_ld_wait();
                         if (a.odd_scale) {
 #pragma unroll
@@ -604,16 +560,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
 #pragma unroll
                             for (int k = 0; k < 32; ++k) s[k] = fmaf(-2.f * out, rcp_approx(1.f + ex2_approx(s[k] * in)), out);
                         }
+                        if (__any_sync(0xFFFFFFFFu, there != 0xFFFFFFFFu)) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) s[k] = there >> k & 1u ? s[k] : -INFINITY;
+                            for (int k = 0; k < 32; ++k) s[k] = there >> k & 1u ? s[k] : -INFINITY;
+                        }
                     };
                     float mx = -INFINITY;
 #pragma unroll 1
                     for (int c = 0; c < BN / 32; ++c) {
-                        float s[32];
-                        scores(c, s);
+                        const uint32_t there = seen(c);
+                        if (!__any_sync(0xFFFFFFFFu, there != 0)) continue;
+                        float s[32], top[2] = {mx, -INFINITY};
+                        scores(c, there, s);
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2) mx = fmaxf(fmaxf(mx, s[k]), s[k + 1]);
+                        for (int k = 0; k < 32; k += 2) top[k / 2 & 1] = fmaxf(fmaxf(top[k / 2 & 1], s[k]), s[k + 1]);
+                        mx = fmaxf(top[0], top[1]);
                     }
                     if (m == -INFINITY ? mx > -INFINITY : (mx - m) * f > kSlack) m_next = mx;
                     if (__any_sync(0xFFFFFFFFu, m_next != m) && !raise(i > u.lo)) {
@@ -621,22 +582,39 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                         break;
                     }
                     pending = false;
-                    usual = !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
+                    usual = a.softcap == 0.f && !a.odd_scale && !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
+                    const float2 f2 = make_float2(f, f), n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
 #pragma unroll 1
                     for (int c = 0; c < BN / 32; ++c) {  // (a group's weights lie over scores that have been read)
-                        float s[32];
+                        const uint32_t there = seen(c);
                         uint32_t p[16];
-                        scores(c, s);
-                        const float m0 = m == -INFINITY ? 0.f : m;
+                        if (!__any_sync(0xFFFFFFFFu, there != 0)) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) s[k] = ex2_approx(far ? fmaf(s[k] - m0, f, C::LIFT) : fmaf(s[k], f, neg + C::LIFT));
-                        float part[2] = {0.f, 0.f};
+                            for (int k = 0; k < 16; ++k) p[k] = 0;
+                            tmem_st16(s_col + 16 * c, p);
+                            continue;
+                        }
+                        float s[32];
+                        scores(c, there, s);
+                        if (far) {
+                            const float m0 = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) s[k] = fmaf(s[k] - m0, f, C::LIFT);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                const float2 z = fma2(make_float2(s[k], s[k + 1]), f2, n2);
+                                s[k] = z.x, s[k + 1] = z.y;
+                            }
+                        }
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            part[0] += s[2 * k], part[1] += s[2 * k + 1];
-                            p[k] = C::E4M3 ? pack_f16(s[2 * k], s[2 * k + 1]) : pack_bf16(s[2 * k], s[2 * k + 1]);
+                            const float2 e = make_float2(ex2_approx(s[2 * k]), ex2_approx(s[2 * k + 1]));
+                            sum[k & 1] = add2(sum[k & 1], e);
+                            p[k] = C::E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
                         }
-                        l += part[0] + part[1];
+                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                         tmem_st16(s_col + 16 * c, p);
                     }
                 }
