@@ -34,13 +34,13 @@ namespace {
 constexpr int kThreads = 512;          // warps 0-3 and 4-7: softmax of a tile of rows each; 8 (9): MMA; 10, 11: queries; 12-15: copies
 constexpr int kMmaWarp = 8, kQueryWarp = 10, kCopyWarp = 12, kCopyWarps = 4;
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // together those of the launch: 2 * (184 + 72) = 4 * 128
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kPlanBatch = 2048;  // sequences whose sums lie in shared memory, at most
 constexpr int kJoinWarps = 8;
 constexpr int kMetaRing = 8;           // tiles whose page masks are kept: more than the ring holds
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;          // how far (log2) a score may exceed the running maximum
 constexpr float kFar = 4194304.f;      // maxima (log2) from which on their product's rounding counts
-constexpr int kExtra = 1;              // places of the list after a unit's tiles: the time of ending it and beginning the next
+constexpr int kExtra = 5;              // places of the list after a unit's tiles: the time of ending it and beginning the next
 
 template <int D_, bool E4M3_>
 struct Cfg {
@@ -50,15 +50,16 @@ struct Cfg {
     static constexpr int BN = D == 256 ? 64 : 128;     // slots of a tile
     static constexpr int ROWS = NT * 128;
     static constexpr int SLOT = BN * D * 2;            // bytes of a tile of keys or values in shared memory
-    static constexpr int NS = D == 64 ? 8 : E4M3 ? 4 : 5;         // such tiles in the ring, keys and values in turn
+    static constexpr int NS = D == 64 ? 8 : E4M3 ? 4 : 5;  // such tiles in the ring, keys and values in turn
     static constexpr int LAG = NS - 2;                 // of which so many may be on their way
     // weights in f16 are kept as 2^7 p, in o' and l alike: at most 2^15, and what lies below 2^-32 of the largest is lost
     static constexpr float LIFT = E4M3 ? 7.f : 0.f;
     // how far (log2) a score may exceed the maximum that its tile's weights are taken by: what their type holds
     static constexpr float JUMP = E4M3 ? kSlack : 64.f;
     static constexpr int QBYTES = ROWS * D * 2;
-    static constexpr int MISC = E4M3 ? 1024 + 2 * ROWS * 4 : 1024;    // barriers and flags; for an e4m3 cache the factors of two units' rows
-    static constexpr int SMEM = QBYTES + NS * SLOT + MISC + 1024;  // (+ slack to align the base)
+    static constexpr int MISC = 768 + (E4M3 ? 2 * ROWS : 0);  // barriers and flags; for an e4m3 cache the factors of two units' rows
+    static constexpr int RAW = E4M3 ? BN * D : 0;      // bytes of a tile as it lies in an e4m3 cache: one of keys, one of values
+    static constexpr int SMEM = QBYTES + NS * SLOT + 2 * RAW + MISC + 1024;  // (+ slack to align the base)
     static constexpr uint32_t S_COL = 0, O_COL = NT == 2 ? 2 * BN : 2 * BN;
     static constexpr uint32_t COLS = 512;
     static_assert(O_COL + NT * D <= COLS && SMEM <= 227 * 1024, "fits");
@@ -66,7 +67,7 @@ struct Cfg {
 
 // What every role needs to know of a unit (ChunkRecord, made by plan_kernel), and of its share's part of it.
 struct Unit : ChunkRecord {
-    int h;        // KV head
+    int h, rt;    // KV head, row tile
     int lo, hi;   // the share's tiles of slots
     bool whole;
 };
@@ -78,12 +79,16 @@ struct Walk {
 
 __device__ __forceinline__ int64_t share_at(int64_t total, int shares, int s) { return total / shares * s + total % shares * s / shares; }
 
+// The row tile of a place: the last of n with place_at <= place, 32 probes at a time.  Whole warps.
 __device__ __forceinline__ int find_rt(const ChunkArgs &a, int n, int64_t place) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(a.place_at + mid) <= place) lo = mid;
-        else hi = mid;
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lo + lane * step;
+        const bool below = lane * step < n && __ldg(a.place_at + at) <= place;
+        const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, below));
+        lo += last * step;
+        n = min(step, n - last * step);
     }
     return lo;
 }
@@ -114,7 +119,7 @@ __device__ __forceinline__ bool next_unit(const ChunkArgs &a, Walk &w, Unit &u) 
     while (w.at < w.hi) {
         const int64_t first = w.h * w.places + __ldg(a.place_at + w.rt);
         load_record(a, w.rt, u);
-        u.h = w.h;
+        u.h = w.h, u.rt = w.rt;
         const int length = u.tiles + kExtra, lo = (int)(w.at - first);
         const int hi = w.hi - first < length ? (int)(w.hi - first) : length;
         w.at += hi - lo;
@@ -171,9 +176,11 @@ __device__ __forceinline__ int plan_max(int v, int *scratch) {
 template <typename C>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ChunkArgs a) {
     __shared__ int64_t scratch[32];
+    __shared__ int first_row[kPlanBatch + 1], first_tile[kPlanBatch + 1];
     pdl_wait();
     pdl_trigger();
     const int B = a.c.batch, tid = threadIdx.x;
+    int *const seq_at = B <= kPlanBatch ? first_row : a.seq_at, *const rt_at = B <= kPlanBatch ? first_tile : a.rt_at;
     bool bad = false;
     // chunks: starts, made to not decrease
     const int per = (B + kPlanThreads) / kPlanThreads;  // of batch + 1 values
@@ -186,11 +193,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ChunkArgs a) {
     };
     for (int b = first; b < last; ++b) top = max(top, min(max(__ldg(a.starts + b), 0), (int)a.T));
     top = plan_max(top, reinterpret_cast<int *>(scratch));
-    for (int b = first; b < last; ++b) a.seq_at[b] = start(b);
+    for (int b = first; b < last; ++b) seq_at[b] = start(b);
     __syncthreads();
     int64_t units = 0, all_units;
     auto units_of = [&](int b) {
-        const int64_t rows = (int64_t)(a.seq_at[b + 1] - a.seq_at[b]) * a.group;
+        const int64_t rows = (int64_t)(seq_at[b + 1] - seq_at[b]) * a.group;
         return (rows + C::ROWS - 1) / C::ROWS;
     };
     for (int b = first; b < min(last, B); ++b) {
@@ -200,10 +207,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ChunkArgs a) {
     }
     units = plan_scan(units, all_units, scratch);
     for (int b = first; b < min(last, B); ++b) {
-        a.rt_at[b] = (int)units;
+        rt_at[b] = (int)units;
         units += units_of(b);
     }
-    if (tid == 0) a.rt_at[B] = (int)all_units;
+    if (tid == 0) rt_at[B] = (int)all_units;
     __syncthreads();
     // places of each unit
     const int R = (int)all_units, per_rt = (R + kPlanThreads - 1) / kPlanThreads;
@@ -213,16 +220,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ChunkArgs a) {
         int lo = 0, hi = B;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (a.rt_at[mid] <= rt0) lo = mid;
+            if (rt_at[mid] <= rt0) lo = mid;
             else hi = mid;
         }
         b = lo;
     }
     auto record = [&](int rt, int &of, ChunkRecord &r) {
-        while (a.rt_at[of + 1] <= rt) ++of;
-        const int n = a.seq_at[of + 1] - a.seq_at[of], len = min(max(__ldg(a.seq_lens + of), 0), a.c.capacity);
-        r.b = of, r.q0 = a.seq_at[of], r.e0 = len - n + 1;
-        r.row0 = (rt - a.rt_at[of]) * C::ROWS;
+        while (rt_at[of + 1] <= rt) ++of;
+        const int n = seq_at[of + 1] - seq_at[of], len = min(max(__ldg(a.seq_lens + of), 0), a.c.capacity);
+        r.b = of, r.q0 = seq_at[of], r.e0 = len - n + 1;
+        r.row0 = (rt - rt_at[of]) * C::ROWS;
         r.rows = min(C::ROWS, n * a.group - r.row0);
         const int first = r.row0 / a.group, last = (r.row0 + r.rows - 1) / a.group;  // tokens
         auto begin = [&](int tok) { return a.window > 0 && (int64_t)r.e0 + tok > a.window ? (int)(r.e0 + tok - a.window) : 0; };
@@ -333,8 +340,16 @@ __device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane) {
     swap(w[0], w[2], 2), swap(w[1], w[3], 2);
 }
 
+// Takes the values that are not finite out of eight; were there any?
+template <bool F16>
+__device__ __forceinline__ bool finite_only(uint4 &v) {
+    const uint32_t b0 = not_finite<F16>(v.x), b1 = not_finite<F16>(v.y), b2 = not_finite<F16>(v.z), b3 = not_finite<F16>(v.w);
+    v.x &= ~b0, v.y &= ~b1, v.z &= ~b2, v.w &= ~b3;
+    return b0 | b1 | b2 | b3;
+}
+
 struct Bars {
-    uint32_t full, empty, s_full, p_full, o_full, q_full, q_free, pv_done, done;
+    uint32_t full, empty, s_full, p_full, o_full, q_full, q_free, pv_done, done, raw;
 };
 
 // row / group for 0 <= row < 2^31
@@ -372,16 +387,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
     constexpr int D = C::D, BN = C::BN, NT = C::NT, NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const uint32_t q_smem = smem_u32(base), ring = q_smem + C::QBYTES, misc = ring + NS * C::SLOT;
-    uint8_t *const misc_p = base + C::QBYTES + NS * C::SLOT;
+    const uint32_t q_smem = smem_u32(base), ring = q_smem + C::QBYTES, raw = ring + NS * C::SLOT, misc = raw + 2 * C::RAW;
+    uint8_t *const misc_p = base + C::QBYTES + NS * C::SLOT + 2 * C::RAW;
     Bars bar;
     bar.full = misc, bar.empty = bar.full + 8 * NS, bar.s_full = bar.empty + 8 * NS, bar.p_full = bar.s_full + 16;
-    bar.o_full = bar.p_full + 16, bar.q_full = bar.o_full + 16, bar.q_free = bar.q_full + 16, bar.pv_done = bar.q_free + 16, bar.done = bar.pv_done + 16;
+    bar.o_full = bar.p_full + 16, bar.q_full = bar.o_full + 16, bar.q_free = bar.q_full + 16, bar.pv_done = bar.q_free + 16, bar.done = bar.pv_done + 16, bar.raw = misc + 256;
     uint32_t *const tmem_holder = reinterpret_cast<uint32_t *>(misc_p + 512);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc_p + 516);
     volatile int *const bad_pages = reinterpret_cast<volatile int *>(misc_p + 524); // a page id was out of range
     volatile int *const bad_seen = reinterpret_cast<volatile int *>(misc_p + 520);  // a value that is not finite was taken out
-    float *const q_factor = reinterpret_cast<float *>(misc_p + 1024);                               // [2][C::ROWS]
+    volatile uint8_t *const q_factor = misc_p + 768;  // [2][C::ROWS]: exponents (biased by 127) of the factors
     volatile uint32_t *const page_mask = reinterpret_cast<volatile uint32_t *>(misc_p + 640);      // [kMetaRing][4]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int *const status = a.c.status;
@@ -400,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
             mbar_init(bar.pv_done + 8 * t, 1);
         }
         mbar_init(bar.done, NT == 2 ? 1 : 2);
+        for (int i = 0; i < 2 * kCopyWarps; ++i) mbar_init(bar.raw + 8 * i, 1);
         *abort_flag = 0;
         *bad_seen = 0;
         *bad_pages = 0;
@@ -437,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
         };
         Row r;
         uint32_t units = 0;
+        if (threadIdx.x == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
         for (bool more = t < NT && advance(u); more; more = advance(u), ++units) {
             r.of(a, u, t * 128 + row_in);
             // ---- what the tile's rows see
@@ -488,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                 tc_fence_after();
                 if constexpr (C::E4M3) {
                     if (i == u.lo) {  // (written before the tile's queries were there)
-                        cc = a.scale_log2 * q_factor[(units & 1) * C::ROWS + t * 128 + row_in];
+                        cc = a.scale_log2 * __uint_as_float((uint32_t)q_factor[(units & 1) * C::ROWS + t * 128 + row_in] << 23);
                         f = a.softcap > 0.f ? 1.f : cc;
                     }
                 }
@@ -701,6 +718,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                     }
                 }
             }
+            if (threadIdx.x == 0 && u.lo == 0 && !u.whole) {
+                // the share that begins a unit it does not end: join_kernel finds the parts from here
+                const int shares = (int)__ldg(a.head + 2);
+                const int64_t total = walk.places * a.c.heads, end = u.h * walk.places + __ldg(a.place_at + u.rt) + u.tiles;
+                int parts = 2;
+                while ((int)blockIdx.x + parts < shares && share_at(total, shares, blockIdx.x + parts) < end) ++parts;
+                a.joins[blockIdx.x] = make_int4(u.rt, u.h, parts, 0);
+            }
             if (!u.whole && real) a.part_ml[part_row] = make_float2(m == -INFINITY ? -INFINITY : -neg, l);
             tc_fence_before();
         }
@@ -858,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                             w.z = pack_f16(lo_f32(w.z) * f, hi_f32(w.z) * f), w.w = pack_f16(lo_f32(w.w) * f, hi_f32(w.w) * f);
                             sts128(to, w);
                             // the way back, for the row's softmax (which has read those of two units before)
-                            if (c == 0) q_factor[(units & 1) * C::ROWS + t * 128 + row] = __uint_as_float((uint32_t)(127 - shift) << 23);
+                            if (c == 0) q_factor[(units & 1) * C::ROWS + t * 128 + row] = (uint8_t)(127 - shift);
                         } else {
                             cp_async16(to, src, from >= 0 ? 16u : 0u);
                         }
@@ -902,14 +927,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
 #pragma unroll 2
             for (int s = 0; s < STEPS; ++s) {
 #pragma unroll
-                for (int x = 0; x < PIECES * (C::E4M3 ? 2 : 1); ++x) {
-                    const int c = C::E4M3 ? 2 * (chunk + LANES * (x / 2)) + (x & 1) : chunk + LANES * x;
-                    const uint32_t p = at + place(s * AT_ONCE + sub, c);
+                for (int x = 0; x < PIECES; ++x) {
+                    const uint32_t p = at + place(s * AT_ONCE + sub, chunk + LANES * x);
                     uint4 v = lds128(p);
-                    const uint32_t b0 = not_finite<C::E4M3>(v.x), b1 = not_finite<C::E4M3>(v.y), b2 = not_finite<C::E4M3>(v.z),
-                                   b3 = not_finite<C::E4M3>(v.w);
-                    if (b0 | b1 | b2 | b3) {
-                        v.x &= ~b0, v.y &= ~b1, v.z &= ~b2, v.w &= ~b3;
+                    if (finite_only<false>(v)) {
                         sts128(p, v);
                         any = true;
                     }
@@ -949,102 +970,206 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
             i = u.lo;
             look_up();
         }
-        for (; more; ++tile_count) {
-            const bool there = !seen || page_ok(a.c, page);
-            if (!there) {
-                atomicOr(status, kDevIndex);
-                *bad_pages = 1;
-            }
-            // this lane's row: its offset, or 1 (offsets are multiples of 16) where nothing is to be read
-            const int64_t off = seen && there ? row_bytes_at(a.c, page, u.h, in_page) : 1;
-            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
-            const uint32_t j0 = (uint32_t)(u.base + i) * BN;
-            const bool edge = j0 + BN > (uint32_t)u.all_end || j0 < (uint32_t)u.all_begin;
-            // rows that are all there come by the copy engine, in boxes within a page (values only where every row sees them)
-            const bool boxes = a.box_slots > 0 && __all_sync(0xFFFFFFFFu, lane >= WROWS || (seen && there));
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const uint32_t eb = bar.empty + 8 * slot;
-                if (issued >= (uint32_t)NS && !__all_sync(0xFFFFFFFFu, mbar_test_wait(eb, parity))) {
-                    if constexpr (!C::E4M3) cp_async_wait<0>();  // nothing is held back while this waits
-                    show(issued);
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(eb, parity, status)) || *abort_flag) {
-                        ok = false;
-                        break;
-                    }
-                }
-                if (kv == 0 && lane == 0) {  // (heads of 256: 16 slots a warp, two warps' bits in a word)
-                    if constexpr (WROWS == 32) page_mask[(tile_count & (kMetaRing - 1)) * 4 + w] = mask;
-                    else reinterpret_cast<volatile uint16_t *>(page_mask)[(tile_count & (kMetaRing - 1)) * 8 + w] = (uint16_t)mask;
-                }
-                const uint8_t *const pool = (kv == 0 ? a.c.k : a.c.v) + 16 * chunk;
-                const uint32_t at = ring + slot * C::SLOT;
-                if constexpr (C::E4M3) {
-                    constexpr int STEP = STEPS * PIECES < 4 ? STEPS * PIECES : 4;
-#pragma unroll 1
-                    for (int s = 0; s < STEPS * PIECES; s += STEP) {
-                        uint4 v[STEP];
-#pragma unroll
-                        for (int x = 0; x < STEP; ++x) {
-                            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, (s + x) / PIECES * AT_ONCE + sub);
-                            v[x] = o & 1 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4 *>(pool + o) + LANES * ((s + x) % PIECES));
-                        }
-#pragma unroll
-                        for (int x = 0; x < STEP; ++x) {
-                            const int r = (s + x) / PIECES * AT_ONCE + sub, c = 2 * (chunk + LANES * ((s + x) % PIECES));
-                            sts128(at + place(r, c), make_uint4(e4m3x2_to_f16x2(v[x].x), e4m3x2_to_f16x2(v[x].x >> 16),
-                                                                e4m3x2_to_f16x2(v[x].y), e4m3x2_to_f16x2(v[x].y >> 16)));
-                            sts128(at + place(r, c + 1), make_uint4(e4m3x2_to_f16x2(v[x].z), e4m3x2_to_f16x2(v[x].z >> 16),
-                                                                    e4m3x2_to_f16x2(v[x].w), e4m3x2_to_f16x2(v[x].w >> 16)));
-                        }
-                    }
-                } else if (boxes && !(kv == 1 && edge)) {
-                    // lane x: block x % (D / 64) of box x / (D / 64)
-                    const int row = lane / (D / 64) * a.box_slots, block = lane % (D / 64);
-                    const int pg = __shfl_sync(0xFFFFFFFFu, page, row & 31), in = __shfl_sync(0xFFFFFFFFu, (int)in_page, row & 31);
-                    if (lane == 0) mbar_arrive_expect_tx(bar.full + 8 * slot, WROWS * D * 2);
-                    __syncwarp();
-                    if (row < WROWS)
-                        copy_box(at + block * (BN * 128) + (w * WROWS + row) * 128, kv == 0 ? k_map : v_map, 64 * block, in, u.h, pg,
-                                 a.head_first != 0, bar.full + 8 * slot);
-                    cp_async_commit();  // (an empty group: the count of those on their way is that of tiles)
-                } else {
-#pragma unroll
-                    for (int s = 0; s < STEPS; ++s) {
-                        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, s * AT_ONCE + sub);
-                        const uint32_t bytes = o & 1 ? 0u : 16u;
-                        const uint8_t *const src = o & 1 ? pool : pool + o;
-#pragma unroll
-                        for (int x = 0; x < PIECES; ++x) cp_async16(at + place(s * AT_ONCE + sub, chunk + LANES * x), src + 16 * LANES * x, bytes);
-                    }
-                    cp_async_commit();
-                }
-                ++issued;
-                if (++slot == NS) slot = 0, parity ^= 1;
-                edge_bits = edge_bits << 1 | (uint32_t)(kv == 1 && edge);
-                box_bits = box_bits << 1 | (uint32_t)(!C::E4M3 && boxes && !(kv == 1 && edge));
-                if constexpr (C::E4M3) {
-                    show(issued);
-                } else if (issued - shown > (uint32_t)C::LAG) {
-                    cp_async_wait<C::LAG>();
-                    show(issued - C::LAG);
-                }
-            }
-            if (!ok) break;
+        auto step = [&] {  // to the next tile, whose page is looked up
             if (++i == u.hi) {
                 more = next_unit<C>(a, walk, u);
                 i = u.lo;
             }
             if (more) look_up();
-        }
-        cp_async_wait<0>();
-        if (ok) {
-            show(issued);
-        } else if (lane == 0) {
-            *abort_flag = 1;
-            // the copy engine's copies land before this CTA leaves (a barrier that others left short of arrivals runs out)
-            for (uint32_t n = issued > (uint32_t)NS ? issued - NS : 0; n < issued; ++n)
-                if (box_bits >> (issued - 1 - n) & 1u) (void)mbar_wait_limit(bar.full + 8 * (n % NS), n / NS & 1, status, 10000000ull);
+        };
+        if constexpr (C::E4M3) {
+            // ---- an e4m3 cache: a tile's bytes come into this warp's part of a buffer of their own, one tile ahead, by the copy
+            // engine where the rows are all there, and go from there, as f16, into the ring
+            struct Tile {
+                int64_t off;
+                int page, in, h;
+                uint32_t mask;
+                bool edge, boxes;
+            };
+            const uint32_t own = raw + w * (WROWS * D);
+            uint32_t raw_phase = 0;
+            auto tile_of = [&] {
+                Tile n;
+                const bool there = !seen || page_ok(a.c, page);
+                if (!there) {
+                    atomicOr(status, kDevIndex);
+                    *bad_pages = 1;
+                }
+                n.off = seen && there ? row_bytes_at(a.c, page, u.h, in_page) : 1;
+                n.page = page, n.in = (int)in_page, n.h = u.h;
+                n.mask = __ballot_sync(0xFFFFFFFFu, there);
+                const uint32_t j0 = (uint32_t)(u.base + i) * BN;
+                n.edge = j0 + BN > (uint32_t)u.all_end || j0 < (uint32_t)u.all_begin;
+                n.boxes = a.box_slots > 0 && __all_sync(0xFFFFFFFFu, lane >= WROWS || (seen && there));
+                return n;
+            };
+            auto fetch = [&](const Tile &n, int kv) {
+                const uint32_t to = own + kv * C::RAW;
+                if (n.boxes) {
+                    const int row = lane * a.box_slots;
+                    const int pg = __shfl_sync(0xFFFFFFFFu, n.page, row & 31), in = __shfl_sync(0xFFFFFFFFu, n.in, row & 31);
+                    const uint32_t rb = bar.raw + 8 * (2 * w + kv);
+                    if (lane == 0) mbar_arrive_expect_tx(rb, WROWS * D);
+                    __syncwarp();
+                    if (row < WROWS) copy_box(to + row * D, kv == 0 ? k_map : v_map, 0, in, n.h, pg, a.head_first != 0, rb);
+                } else {
+                    const uint8_t *const pool = (kv == 0 ? a.c.k : a.c.v) + 16 * chunk;
+#pragma unroll
+                    for (int s = 0; s < STEPS; ++s) {
+                        const int64_t o = __shfl_sync(0xFFFFFFFFu, n.off, s * AT_ONCE + sub);
+                        const uint32_t bytes = o & 1 ? 0u : 16u;
+                        const uint8_t *const src = o & 1 ? pool : pool + o;
+#pragma unroll
+                        for (int x = 0; x < PIECES; ++x)
+                            cp_async16(to + (s * AT_ONCE + sub) * D + 16 * (chunk + LANES * x), src + 16 * LANES * x, bytes);
+                    }
+                    cp_async_commit();
+                }
+            };
+            Tile now = {}, next = {};
+            bool flying[2] = {false, false};  // copies of the copy engine that have not been waited for
+            bool any = more;
+            if (more) {
+                now = tile_of();
+                fetch(now, 0), fetch(now, 1);
+                flying[0] = flying[1] = now.boxes;
+                step();
+            }
+            for (; any && ok; ++tile_count) {
+                const bool follows = more;
+                if (follows) {
+                    next = tile_of();
+                    step();
+                }
+                if (lane == 0) {
+                    if constexpr (WROWS == 32) page_mask[(tile_count & (kMetaRing - 1)) * 4 + w] = now.mask;
+                    else reinterpret_cast<volatile uint16_t *>(page_mask)[(tile_count & (kMetaRing - 1)) * 8 + w] = (uint16_t)now.mask;
+                }
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (issued >= (uint32_t)NS && (!__all_sync(0xFFFFFFFFu, mbar_wait(bar.empty + 8 * slot, parity, status)) || *abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (now.boxes) {
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar.raw + 8 * (2 * w + kv), raw_phase >> kv & 1, status))) {
+                            ok = false;
+                            break;
+                        }
+                        raw_phase ^= 1u << kv;
+                        flying[kv] = false;
+                    } else {
+                        cp_async_wait<0>();
+                    }
+                    const uint32_t from = own + kv * C::RAW + sub * D + 16 * chunk, at = ring + slot * C::SLOT;
+                    const bool check = kv == 1 && now.edge;
+                    bool odd = false;
+#pragma unroll
+                    for (int s = 0; s < STEPS; ++s) {
+#pragma unroll
+                        for (int x = 0; x < PIECES; ++x) {
+                            const uint4 v = lds128(from + s * AT_ONCE * D + 16 * LANES * x);
+                            uint4 lo = make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
+                            uint4 hi = make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
+                            if (check) odd |= finite_only<true>(lo) | finite_only<true>(hi);
+                            const int c = 2 * (chunk + LANES * x);
+                            sts128(at + place(s * AT_ONCE + sub, c), lo);
+                            sts128(at + place(s * AT_ONCE + sub, c + 1), hi);
+                        }
+                    }
+                    if (odd) *bad_seen = 1;
+                    fence_proxy_async_smem();  // for the MMAs, and for the copy engine, which may write what has been read
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar.full + 8 * slot);
+                    ++issued;
+                    if (++slot == NS) slot = 0, parity ^= 1;
+                    if (follows) {
+                        fetch(next, kv);
+                        flying[kv] = next.boxes;
+                    }
+                }
+                now = next;
+                any = follows;
+            }
+            cp_async_wait<0>();
+            if (!ok) {
+                if (lane == 0) *abort_flag = 1;
+                for (int kv = 0; kv < 2; ++kv)
+                    if (flying[kv]) (void)mbar_wait(bar.raw + 8 * (2 * w + kv), raw_phase >> kv & 1, status);
+            }
+        } else {
+            for (; more; ++tile_count) {
+                const bool there = !seen || page_ok(a.c, page);
+                if (!there) {
+                    atomicOr(status, kDevIndex);
+                    *bad_pages = 1;
+                }
+                // this lane's row: its offset, or 1 (offsets are multiples of 16) where nothing is to be read
+                const int64_t off = seen && there ? row_bytes_at(a.c, page, u.h, in_page) : 1;
+                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
+                const uint32_t j0 = (uint32_t)(u.base + i) * BN;
+                const bool edge = j0 + BN > (uint32_t)u.all_end || j0 < (uint32_t)u.all_begin;
+                // rows that are all there come by the copy engine, in boxes within a page (values only where every row sees them)
+                const bool boxes = a.box_slots > 0 && __all_sync(0xFFFFFFFFu, lane >= WROWS || (seen && there));
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t eb = bar.empty + 8 * slot;
+                    if (issued >= (uint32_t)NS && !__all_sync(0xFFFFFFFFu, mbar_test_wait(eb, parity))) {
+                        cp_async_wait<0>();  // nothing is held back while this waits
+                        show(issued);
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(eb, parity, status)) || *abort_flag) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    if (kv == 0 && lane == 0) {  // (heads of 256: 16 slots a warp, two warps' bits in a word)
+                        if constexpr (WROWS == 32) page_mask[(tile_count & (kMetaRing - 1)) * 4 + w] = mask;
+                        else reinterpret_cast<volatile uint16_t *>(page_mask)[(tile_count & (kMetaRing - 1)) * 8 + w] = (uint16_t)mask;
+                    }
+                    const uint8_t *const pool = (kv == 0 ? a.c.k : a.c.v) + 16 * chunk;
+                    const uint32_t at = ring + slot * C::SLOT;
+                    if (boxes && !(kv == 1 && edge)) {
+                        // lane x: block x % (D / 64) of box x / (D / 64)
+                        const int row = lane / (D / 64) * a.box_slots, block = lane % (D / 64);
+                        const int pg = __shfl_sync(0xFFFFFFFFu, page, row & 31), in = __shfl_sync(0xFFFFFFFFu, (int)in_page, row & 31);
+                        if (lane == 0) mbar_arrive_expect_tx(bar.full + 8 * slot, WROWS * D * 2);
+                        __syncwarp();
+                        if (row < WROWS)
+                            copy_box(at + block * (BN * 128) + (w * WROWS + row) * 128, kv == 0 ? k_map : v_map, 64 * block, in, u.h, pg,
+                                     a.head_first != 0, bar.full + 8 * slot);
+                        cp_async_commit();  // (an empty group: the count of those on their way is that of tiles)
+                    } else {
+#pragma unroll
+                        for (int s = 0; s < STEPS; ++s) {
+                            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, s * AT_ONCE + sub);
+                            const uint32_t bytes = o & 1 ? 0u : 16u;
+                            const uint8_t *const src = o & 1 ? pool : pool + o;
+#pragma unroll
+                            for (int x = 0; x < PIECES; ++x) cp_async16(at + place(s * AT_ONCE + sub, chunk + LANES * x), src + 16 * LANES * x, bytes);
+                        }
+                        cp_async_commit();
+                    }
+                    ++issued;
+                    if (++slot == NS) slot = 0, parity ^= 1;
+                    edge_bits = edge_bits << 1 | (uint32_t)(kv == 1 && edge);
+                    box_bits = box_bits << 1 | (uint32_t)(boxes && !(kv == 1 && edge));
+                    if (issued - shown > (uint32_t)C::LAG) {
+                        cp_async_wait<C::LAG>();
+                        show(issued - C::LAG);
+                    }
+                }
+                if (!ok) break;
+                step();
+            }
+            cp_async_wait<0>();
+            if (ok) {
+                show(issued);
+            } else if (lane == 0) {
+                *abort_flag = 1;
+                // the copy engine's copies land before this CTA leaves (a barrier that others left short of arrivals runs out)
+                for (uint32_t n = issued > (uint32_t)NS ? issued - NS : 0; n < issued; ++n)
+                    if (box_bits >> (issued - 1 - n) & 1u) (void)mbar_wait_limit(bar.full + 8 * (n % NS), n / NS & 1, status, 10000000ull);
+            }
         }
     }
     tc_fence_before();
@@ -1058,32 +1183,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
 
 // ---------------------------------------------------------------- joining
 
-// CTA (s, y): the unit that boundary s between shares is the first to cut, if there is one; each warp some of its rows.
+// CTA (s, y): the unit that share s begins and does not end, if there is one; each warp some of its rows.
 template <typename C>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const ChunkArgs a) {
     constexpr int D = C::D, PER = D / 32;
     pdl_wait();
     pdl_trigger();
-    const int64_t places = __ldg(a.head), total = places * a.c.heads;
-    const int shares = (int)__ldg(a.head + 2), s = blockIdx.x + 1;
-    if (s >= shares) return;
-    const int64_t cut = share_at(total, shares, s);
-    const int h = (int)(cut / places);
-    const int64_t in_head = cut - h * places;
-    const int rt = find_rt(a, (int)__ldg(a.head + 1), in_head);
-    const int64_t first = __ldg(a.place_at + rt);
-    if (first == in_head) return;                                              // the boundary lies between units
-    const int64_t start = h * places + first, end = h * places + __ldg(a.place_at + rt + 1) - kExtra;
-    if (cut >= end) return;                                                    // ... or behind the unit's tiles
-    if (share_at(total, shares, s - 1) > start) return;                        // an earlier boundary cut it
+    const int4 what = __ldg(a.joins + blockIdx.x);
+    const int s = blockIdx.x, h = what.y, parts = what.z;
+    if (parts == 0) return;
     ChunkRecord u;
-    load_record(a, rt, u);
-    int last = s;                                                              // the share that holds its end
-    while (last + 1 < shares && share_at(total, shares, last + 1) < end) ++last;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, parts = last - s + 2;
+    load_record(a, what.x, u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int row_in = blockIdx.y * kJoinWarps + warp; row_in < u.rows; row_in += gridDim.y * kJoinWarps) {
-        // part k of the row: of share s - 1 + k
-        auto part = [&](int k) { return (int64_t)(2 * (s - 1 + k) + (k == 0 ? 1 : 0)) * C::ROWS + row_in; };
+        // part k of the row: of share s + k
+        auto part = [&](int k) { return (int64_t)(2 * (s + k) + (k == 0 ? 1 : 0)) * C::ROWS + row_in; };
         const float2 nothing = make_float2(-INFINITY, 0.f);
         float2 own = lane < parts ? __ldcg(a.part_ml + part(lane)) : nothing;  // (a lane's first part stays at hand)
         float m = own.x;
@@ -1119,7 +1233,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const ChunkArgs a
 #pragma unroll
                 for (int y = 0; y < PER; ++y) o[y] = fmaf(x[i][y], w[i], o[y]);
         }
-        const int row = u.row0 + row_in, tok = row / a.group, e = u.e0 + tok;
+        const int row = u.row0 + row_in, tok = token_of(a, row), e = u.e0 + tok;
         const int bgn = a.window > 0 && e > a.window ? (int)(e - a.window) : 0;
         const float inv = a.v_scale / l;
         uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + ((int64_t)u.q0 + tok) * a.ldo + (int64_t)(h * a.group + row - tok * a.group) * D + lane * PER);
@@ -1140,18 +1254,21 @@ cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     a.shares = di.sm_count < kMaxChunkShares ? di.sm_count : kMaxChunkShares;
     if ((e = launch_pdl(plan_kernel<C>, dim3(1), dim3(kPlanThreads), 0, s, dim3(1), a)) != cudaSuccess) return e;
-    // boxes of what divides a page, of 8 (a swizzle atom) to 32 slots (a warp's rows; 16 of heads of 256)
+    // boxes of what divides a page, of 8 (a swizzle atom) to 32 slots (a warp's rows; 16 of heads of 256): blocks of 64 values,
+    // or whole rows of an e4m3 cache
     CUtensorMap k_map = {}, v_map = {};
     int box = 1;
     while (box < C::BN / kCopyWarps && a.c.page_size % (2 * box) == 0) box *= 2;
     bool head_first = false;
-    a.box_slots = !C::E4M3 && box >= 8 && make_cache_tmap(&k_map, a.c.k, a.c, 64, box, true, &head_first) &&
-                          make_cache_tmap(&v_map, a.c.v, a.c, 64, box, true, &head_first) ? box : 0;
+    const int values = C::E4M3 ? C::D : 64;
+    const bool maps = box >= 8 && make_cache_tmap(&k_map, a.c.k, a.c, values, box, !C::E4M3, &head_first) &&
+                      make_cache_tmap(&v_map, a.c.v, a.c, values, box, !C::E4M3, &head_first);
+    a.box_slots = maps ? box : 0;
     a.head_first = head_first;
     if ((e = launch_pdl(chunk_kernel<C>, dim3(a.shares), dim3(kThreads), C::SMEM, s, dim3(1), a, k_map, v_map)) != cudaSuccess) return e;
-    // rows of a unit over 16 CTAs, fewer where the call has few rows
+    // a warp a row
     const int64_t rows = a.T * a.group;
-    const int y = rows <= kJoinWarps ? 1 : rows <= 4 * kJoinWarps ? 4 : 16;
+    const int y = (int)(((rows < C::ROWS ? rows : C::ROWS) + kJoinWarps - 1) / kJoinWarps);
     return launch_pdl(join_kernel<C>, dim3(a.shares, y), dim3(kJoinWarps * 32), 0, s, dim3(1), a);
 }
 

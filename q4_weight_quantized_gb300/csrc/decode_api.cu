@@ -189,7 +189,7 @@ bool chunk_shape_ok(const q4k_kv_cache *c, int64_t T, int32_t n_heads) {
 }
 
 struct ChunkLayout {
-    size_t seq_at, rt_at, records, place_at, head, parts, part_ml, total;
+    size_t seq_at, rt_at, records, place_at, head, joins, parts, part_ml, total;
 };
 ChunkLayout chunk_layout(const q4k_kv_cache *c, int64_t T, int32_t n_heads) {
     const size_t rows = (size_t)chunk_rows(c->head_dim);
@@ -206,6 +206,7 @@ ChunkLayout chunk_layout(const q4k_kv_cache *c, int64_t T, int32_t n_heads) {
     l.records = take(tiles * sizeof(ChunkRecord));
     l.place_at = take((tiles + 1) * 8);
     l.head = take(3 * 8);
+    l.joins = take(kMaxChunkShares * sizeof(int4));
     l.part_ml = take((size_t)2 * kMaxChunkShares * rows * sizeof(float2));
     l.parts = take((size_t)2 * kMaxChunkShares * rows * c->head_dim * 4);
     l.total = at;
@@ -520,6 +521,7 @@ q4k_status q4k_attn_chunk(const q4k_kv_cache *cache, const int32_t *starts, cons
     a.records = reinterpret_cast<ChunkRecord *>(base + l.records);
     a.place_at = reinterpret_cast<int64_t *>(base + l.place_at);
     a.head = reinterpret_cast<int64_t *>(base + l.head);
+    a.joins = reinterpret_cast<int4 *>(base + l.joins);
     a.part_ml = reinterpret_cast<float2 *>(base + l.part_ml);
     a.parts = reinterpret_cast<float *>(base + l.parts);
     return finish(launch_attn_chunk(di, a, static_cast<cudaStream_t>(stream)));

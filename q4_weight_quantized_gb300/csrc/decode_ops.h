@@ -160,11 +160,11 @@ struct ChunkArgs {
     int32_t box_slots;            // slots of a tensor copy's box: what divides a page, up to 32; 0: none can be made
     int32_t head_first;           // see make_cache_tmap
     // workspace
-    int32_t *seq_at;              // [batch + 1]: first row of each sequence
-    int32_t *rt_at;               // [batch + 1]: row tiles before each sequence
+    int32_t *seq_at, *rt_at;      // [batch + 1]: first row of each sequence, row tiles before it (of many sequences)
     ChunkRecord *records;         // [row tiles]
     int64_t *place_at;            // [row tiles + 1]: places of the list before each row tile, of one KV head
     int64_t *head;                // places, row tiles, shares
+    int4 *joins;                  // [shares]: row tile, KV head and number of parts of the unit that a share begins and does not end
     float *parts;                 // [2 * shares][rows][D]
     float2 *part_ml;              // [2 * shares][rows]
 };
