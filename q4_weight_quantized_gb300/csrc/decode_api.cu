@@ -219,11 +219,11 @@ bool lora_shape_ok(int32_t n_adapters, int64_t N, int64_t K, int32_t R, int64_t 
 }
 
 struct LoraLayout {
-    size_t part, offsets, perm, tiles, n_tiles, total;
+    size_t v, offsets, perm, tiles, n_tiles, total;
 };
-LoraLayout lora_layout(int32_t n_adapters, int64_t K, int32_t R, int64_t T) {
+LoraLayout lora_layout(int32_t n_adapters, int32_t R, int64_t T) {
     LoraLayout l = {};
-    size_t at = align256((size_t)lora_split(K, T, n_adapters).splits * T * R * 4);
+    size_t at = align256((size_t)T * R * 4);
     if (T > kLoraSmall) {
         l.offsets = at;
         at += align256(((size_t)n_adapters + 1) * 4);
@@ -449,7 +449,7 @@ q4k_status q4k_batch_plan(const q4k_kv_cache *cache, const int32_t *seq_lens, co
 }
 
 size_t q4k_lora_add_workspace_size(int32_t n_adapters, int64_t N, int64_t K, int32_t R, int64_t T) {
-    return lora_shape_ok(n_adapters, N, K, R, T) ? lora_layout(n_adapters, K, R, T).total : 0;
+    return lora_shape_ok(n_adapters, N, K, R, T) ? lora_layout(n_adapters, R, T).total : 0;
 }
 
 q4k_status q4k_lora_add(int32_t n_adapters, int64_t N, int64_t K, int32_t R, const uint16_t *a, const uint16_t *b,
@@ -460,7 +460,7 @@ q4k_status q4k_lora_add(int32_t n_adapters, int64_t N, int64_t K, int32_t R, con
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(ranks, 4) || !aligned(scales, 4) || !aligned(ids, 4) || !aligned(x, 16) ||
         ldx % 8 || !aligned(y, 4) || !aligned(ws, 256))
         return Q4K_ERR_ALIGN;
-    const LoraLayout l = lora_layout(n_adapters, K, R, T);
+    const LoraLayout l = lora_layout(n_adapters, R, T);
     if (ws_bytes < l.total) return Q4K_ERR_WORKSPACE;
     DeviceInfo di;
     const q4k_status st = check_device(&di);
@@ -470,10 +470,8 @@ q4k_status q4k_lora_add(int32_t n_adapters, int64_t N, int64_t K, int32_t R, con
     c.a = a, c.b = b, c.ranks = ranks, c.scales = scales, c.ids = ids;
     c.x = x, c.T = T, c.ldx = ldx, c.y = y, c.ldy = ldy;
     c.status = di.status;
-    const LoraSplit split = lora_split(K, T, n_adapters);
-    c.k_chunk = (int32_t)split.k_chunk, c.splits = split.splits;
     uint8_t *base = static_cast<uint8_t *>(ws);
-    c.part = reinterpret_cast<float *>(base + l.part);
+    c.v = reinterpret_cast<float *>(base + l.v);
     if (T > kLoraSmall) {
         c.offsets = reinterpret_cast<int32_t *>(base + l.offsets);
         c.perm = reinterpret_cast<int32_t *>(base + l.perm);

@@ -184,18 +184,13 @@ struct LoraArgs {
     float *y;
     int64_t ldy;
     unsigned int *status;
-    int32_t k_chunk, splits;     // of the K axis
+    int32_t k_chunk;             // of the K axis, a CTA's
     // workspace
-    float *part;                 // [splits][T][R]
+    float *v;                    // [T][R]: the inner sums
     int32_t *offsets, *perm;     // more than kLoraSmall tokens: sorted by adapter (else null)
     int4 *tiles;
     int *n_tiles;
 };
-struct LoraSplit {
-    int64_t k_chunk;
-    int splits;
-};
-LoraSplit lora_split(int64_t K, int64_t T, int n_adapters);
-cudaError_t launch_lora_add(const DeviceInfo &di, const LoraArgs &a, cudaStream_t s);
+cudaError_t launch_lora_add(const DeviceInfo &di, LoraArgs &a, cudaStream_t s);
 
 }  // namespace q4k

@@ -2,16 +2,19 @@
 //     y[t] += c_a B_a (A_a x[t]),  a = ids[t].
 //
 // Two products over the tokens of one adapter at a time (a tile: an adapter and at most 192 of its tokens), the
-// inner sums v[t] = A_a x[t] between them in the workspace:
-//   shrink   v: m16n8k16 MMAs, 16 tokens by R, the K axis split over CTAs (few tiles must fill the GPU) and over the
-//            warps of a CTA.  Any pairing of k positions gives the same sum, so a lane's eight consecutive values of a
-//            row are its share of two MMA steps: operands come straight from global memory, 16 bytes at a time.
-//   expand   y: adds up the K parts in their order, multiplies by the adapter's scale, and splits the fp32 value into
-//            three bf16 pieces of 8 significant bits each (exact), so that the second product has exact products, too.
-//            Columns are dealt to MMA tiles so that a lane owns four consecutive ones: y is read and written 16 bytes
-//            at a time, the reads on their way before the inner sums are there.
-// Up to 192 tokens find their tile themselves: the CTA of a token that is its adapter's first gathers the
-// others.  More are sorted by adapter first (the experts' counting sort).
+// inner sums v[t] = c_a A_a x[t] between them in the workspace:
+//   shrink   v: m16n8k16 MMAs, 16 tokens by R.  The K axis is split over the warps of a CTA and the CTAs of a cluster (few
+//            tiles must fill the GPU), whose sums are added in their order through each other's shared memory.  Any
+//            pairing of k positions gives the same sum, so a lane's eight consecutive values of a row are its share of two
+//            MMA steps: operands come straight from global memory, 16 bytes at a time.
+//   expand   y: the fp32 inner sums are split into three bf16 pieces of 8 significant bits each (exact), so that the
+//            second product has exact products, too.  Columns are dealt to MMA tiles so that a lane owns four
+//            consecutive ones: y is read and written 16 bytes at a time.  Warps share nothing; a warp keeps its columns
+//            of B in registers and walks the tile's tokens, 16 at a time, the next ones' y on its way.
+// More than 192 tokens are sorted by adapter first (the experts' counting sort), then the two kernels run.  Up to 192 find their
+// tile themselves (an adapter, or a token that is its adapter's first where there are fewer tokens), and a cluster of
+// CTAs does both products of a tile in one launch, the inner sums staying in its shared memory; meanwhile its part of B
+// comes into L2.
 // Bound by HBM: of many tokens by y, read and written once, of few by the adapters' matrices and by latency.
 #include <cuda_runtime.h>
 
@@ -21,7 +24,8 @@
 namespace q4k {
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kWarps = 4, kThreads = kWarps * 32;  // of expand_kernel
+constexpr int kMaxCluster = 8;  // tile_kernel's clusters are of that many
 constexpr int kTileTokens = kMoeTileItems;
 static_assert(kLoraSmall <= kTileTokens, "the tokens of a small call fit in one tile");
 
@@ -29,113 +33,133 @@ struct Tile {
     int adapter, count, rank;
 };
 
-// The tile of CTA row `k`, its tokens in list[]; count 0: nothing to do.  Every thread calls it.
+// The tile `k`, its tokens in list[]; count 0: nothing to do.  Every thread of THREADS calls it.
+template <int THREADS>
 __device__ __forceinline__ Tile tile_of(const LoraArgs &a, int k, int *list, uint32_t *masks) {
+    constexpr int ROUNDS = (kLoraSmall + THREADS - 1) / THREADS, WARPS = THREADS / 32;
     Tile t = {-1, 0, 0};
     if (a.tiles) {
         if (k >= __ldg(a.n_tiles)) return t;
         const int4 r = __ldg(a.tiles + k);
         t.adapter = r.x, t.count = r.z;
-        for (int i = threadIdx.x; i < r.z; i += kThreads) list[i] = __ldg(a.perm + r.y + i);
-        __syncthreads();
+        for (int i = threadIdx.x; i < r.z; i += THREADS) list[i] = __ldg(a.perm + r.y + i);
     } else {
-        const int id = __ldg(a.ids + k), warp = threadIdx.x >> 5;
-        if (id < 0) return t;
-        if (id >= a.n_adapters) {
-            if (threadIdx.x == 0) atomicOr(a.status, kDevIndex);
-            return t;
-        }
-        bool mine[2];
+        const bool by_adapter = a.n_adapters <= a.T;
+        const int id = by_adapter ? k : __ldg(a.ids + k), warp = threadIdx.x >> 5;
+        bool mine[ROUNDS], over = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = i * kThreads + threadIdx.x;
-            mine[i] = at < a.T && __ldg(a.ids + at) == id;
+        for (int i = 0; i < ROUNDS; ++i) {
+            const int at = i * THREADS + threadIdx.x, of = at < a.T ? __ldg(a.ids + at) : -1;
+            mine[i] = of == id;
+            over |= of >= a.n_adapters;
             const uint32_t m = __ballot_sync(0xFFFFFFFFu, mine[i]);
-            if ((threadIdx.x & 31) == 0) masks[i * kWarps + warp] = m;
+            if ((threadIdx.x & 31) == 0) masks[i * WARPS + warp] = m;
         }
+        if (over && k == 0) atomicOr(a.status, kDevIndex);
         __syncthreads();
-        int first = -1, before[2] = {0, 0};
+        int first = -1, before[ROUNDS] = {};
 #pragma unroll
-        for (int w = 0; w < 2 * kWarps; ++w) {
+        for (int w = 0; w < ROUNDS * WARPS; ++w) {
             if (first < 0 && masks[w]) first = 32 * w + __ffs(masks[w]) - 1;
-            if (w < warp) before[0] += __popc(masks[w]);
-            if (w < kWarps + warp) before[1] += __popc(masks[w]);
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i)
+                if (w < i * WARPS + warp) before[i] += __popc(masks[w]);
             t.count += __popc(masks[w]);
         }
-        if (first != k) {
-            t.count = 0;
-            return t;
-        }
+        if (id < 0 || id >= a.n_adapters || (!by_adapter && first != k)) t.count = 0;
+        if (t.count == 0) return t;
         t.adapter = id;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < ROUNDS; ++i)
             if (mine[i])
-                list[before[i] + __popc(masks[i * kWarps + warp] & ((1u << (threadIdx.x & 31)) - 1u))] = i * kThreads + threadIdx.x;
-        __syncthreads();
+                list[before[i] + __popc(masks[i * WARPS + warp] & ((1u << (threadIdx.x & 31)) - 1u))] = i * THREADS + threadIdx.x;
     }
+    __syncthreads();
     t.rank = a.ranks ? min(max(__ldg(a.ranks + t.adapter), 0), a.R) : a.R;
     return t;
 }
 
 __device__ __forceinline__ uint4 ldg16(const uint16_t *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
 
-// NT: groups of eight inner values (R / 8, or the next power of two); U: steps of 32 k whose loads are in flight
-template <int NT, int U>
-__global__ void __launch_bounds__(kThreads) shrink_kernel(const LoraArgs a) {
-    pdl_wait();
-    pdl_trigger();
-    __shared__ int list[kTileTokens];
-    __shared__ uint32_t masks[2 * kWarps];
-    __shared__ float red[kWarps][16][NT * 8 + 1];
-    if (a.tiles) {  // (a small call's CTAs see the ids themselves)
-        const int64_t cta = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-        for (int64_t t = cta * kThreads + threadIdx.x; t < a.T; t += (int64_t)gridDim.x * gridDim.y * kThreads)
-            if (__ldg(a.ids + t) >= a.n_adapters) atomicOr(a.status, kDevIndex);
-    }
-    const Tile tile = tile_of(a, blockIdx.y, list, masks);
-    if (tile.count == 0) return;
+// The sums of tokens m0 .. m0 + 15 over this CTA's K chunk into red[0] (its warps' added), whole CTA.  U: steps of 32 k whose
+// loads are in flight.
+template <int NT, int U, int W>
+__device__ __forceinline__ void inner_sums(const LoraArgs &a, const Tile &tile, const int *list, int m0, float (*red)[16][NT * 8 + 1]) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
     const int k_end = (int)min((int64_t)(blockIdx.x + 1) * a.k_chunk, a.K);
     const uint16_t *rows = a.a + (int64_t)tile.adapter * a.R * a.K;
-    for (int m0 = 0; m0 < tile.count; m0 += 16) {
-        const uint16_t *x0 = m0 + g < tile.count ? a.x + list[m0 + g] * a.ldx : nullptr;
-        const uint16_t *x1 = m0 + g + 8 < tile.count ? a.x + list[m0 + g + 8] * a.ldx : nullptr;
-        float acc[NT][4] = {};
-        for (int k = blockIdx.x * a.k_chunk + 32 * warp + 8 * tq; k - 8 * tq < k_end; k += 32 * kWarps * U) {
-            uint4 xa[U], xb[U], w[U][NT];
+    const uint16_t *x0 = m0 + g < tile.count ? a.x + list[m0 + g] * a.ldx : nullptr;
+    const uint16_t *x1 = m0 + g + 8 < tile.count ? a.x + list[m0 + g + 8] * a.ldx : nullptr;
+    float acc[NT][4] = {};
+    for (int k = blockIdx.x * a.k_chunk + 32 * warp + 8 * tq; k - 8 * tq < k_end; k += 32 * W * U) {
+        uint4 xa[U], xb[U], w[U][NT];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int at = k + 32 * kWarps * u;
-                const bool in = at < k_end;
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                xa[u] = in && x0 ? ldg16(x0 + at) : zero;
-                xb[u] = in && x1 ? ldg16(x1 + at) : zero;
+        for (int u = 0; u < U; ++u) {
+            const int at = k + 32 * W * u;
+            const bool in = at < k_end;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            xa[u] = in && x0 ? ldg16(x0 + at) : zero;
+            xb[u] = in && x1 ? ldg16(x1 + at) : zero;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) w[u][n] = in && 8 * n + g < tile.rank ? ldg16(rows + (int64_t)(8 * n + g) * a.K + at) : zero;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t lo[4] = {xa[u].x, xb[u].x, xa[u].y, xb[u].y}, hi[4] = {xa[u].z, xb[u].z, xa[u].w, xb[u].w};
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma_bf16_16816(acc[n], lo, w[u][n].x, w[u][n].y, acc[n]);
-                    mma_bf16_16816(acc[n], hi, w[u][n].z, w[u][n].w, acc[n]);
-                }
-            }
+            for (int n = 0; n < NT; ++n) w[u][n] = in && 8 * n + g < tile.rank ? ldg16(rows + (int64_t)(8 * n + g) * a.K + at) : zero;
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            red[warp][g][8 * n + 2 * tq] = acc[n][0], red[warp][g][8 * n + 2 * tq + 1] = acc[n][1];
-            red[warp][g + 8][8 * n + 2 * tq] = acc[n][2], red[warp][g + 8][8 * n + 2 * tq + 1] = acc[n][3];
+        for (int u = 0; u < U; ++u) {
+            const uint32_t lo[4] = {xa[u].x, xb[u].x, xa[u].y, xb[u].y}, hi[4] = {xa[u].z, xb[u].z, xa[u].w, xb[u].w};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma_bf16_16816(acc[n], lo, w[u][n].x, w[u][n].y, acc[n]);
+                mma_bf16_16816(acc[n], hi, w[u][n].z, w[u][n].w, acc[n]);
+            }
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < 16 * a.R; i += kThreads) {
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        red[warp][g][8 * n + 2 * tq] = acc[n][0], red[warp][g][8 * n + 2 * tq + 1] = acc[n][1];
+        red[warp][g + 8][8 * n + 2 * tq] = acc[n][2], red[warp][g + 8][8 * n + 2 * tq + 1] = acc[n][3];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * a.R; i += W * 32) {
+        const int row = i / a.R, r = i - row * a.R;
+        float s = red[0][row][r];
+#pragma unroll
+        for (int w = 1; w < W; ++w) s += red[w][row][r];
+        red[0][row][r] = s;
+    }
+}
+
+// What the CTAs of the cluster have in `mine`, added in their order.
+__device__ __forceinline__ float cluster_total(const float *mine) {
+    float s = 0.f;
+    for (uint32_t c = 0; c < gridDim.x; ++c) s += ld_shared_cluster_f32(map_shared_rank(smem_u32(mine), c));
+    return s;
+}
+
+template <int NT, int U, int W>
+__global__ void __launch_bounds__(W * 32) shrink_kernel(const LoraArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    __shared__ int list[kTileTokens];
+    __shared__ uint32_t masks[8];
+    __shared__ float red[W][16][NT * 8 + 1];
+    const int64_t cta = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    for (int64_t t = cta * (W * 32) + threadIdx.x; t < a.T; t += (int64_t)gridDim.x * gridDim.y * gridDim.z * (W * 32))
+        if (__ldg(a.ids + t) >= a.n_adapters) atomicOr(a.status, kDevIndex);
+    const Tile tile = tile_of<W * 32>(a, blockIdx.y, list, masks);
+    const float scale = a.scales && tile.count > 0 ? __ldg(a.scales + tile.adapter) : 1.f;
+    // (the CTAs of a cluster have the same tile and tokens)
+    for (int m0 = 16 * blockIdx.z; m0 < tile.count; m0 += 16 * gridDim.z) {
+        inner_sums<NT, U, W>(a, tile, list, m0, red);
+        if (gridDim.x > 1) cluster_sync();
+        else __syncthreads();
+        for (int i = threadIdx.x; i < 16 * a.R; i += W * 32) {
             const int row = i / a.R, r = i - row * a.R;
-            if (m0 + row < tile.count)
-                a.part[((int64_t)blockIdx.x * a.T + list[m0 + row]) * a.R + r] =
-                    (red[0][row][r] + red[1][row][r]) + (red[2][row][r] + red[3][row][r]);
+            if (row % gridDim.x != blockIdx.x || m0 + row >= tile.count) continue;
+            const float s = gridDim.x > 1 ? cluster_total(&red[0][row][r]) : red[0][row][r];
+            a.v[(int64_t)list[m0 + row] * a.R + r] = r < tile.rank ? s * scale : 0.f;
         }
-        __syncthreads();
+        if (gridDim.x > 1) cluster_sync();  // the others have read this CTA's sums
+        else __syncthreads();
     }
 }
 
@@ -153,117 +177,228 @@ __device__ __forceinline__ void split3(float v, uint32_t (&piece)[3]) {
     piece[2] = __float_as_uint(r - __uint_as_float(__float_as_uint(r) & 0xFFFF0000u)) >> 16;
 }
 
+// KS steps of the first operand from 16 tokens' inner values: lane's rows g and g + 8 (null: no token), from value 4 tq on;
+// values beyond the rank are 0, those beyond R are not there.
+template <int KS>
+__device__ __forceinline__ void split_rows(const float4 (&t)[KS][2], uint32_t (&frag)[KS][3][4]) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t p0[3], p1[3], p2[3], p3[3];
+            split3(t[s][h].x, p0), split3(t[s][h].y, p1), split3(t[s][h].z, p2), split3(t[s][h].w, p3);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) frag[s][k][h] = p0[k] | p1[k] << 16, frag[s][k][2 + h] = p2[k] | p3[k] << 16;
+        }
+}
+
+// A group of 16 columns from n on.  B: column 2 j + e of MMA tile i is the group's column 4 j + 2 i + e; inner values 16 s + 4 tq .. + 3.
+template <int KS>
+__device__ __forceinline__ void load_b(const LoraArgs &a, const Tile &tile, int64_t n, uint32_t (&b)[2][KS][2]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t at = n + 4 * (g >> 1) + 2 * i + (g & 1);
+        const uint16_t *row = a.b + ((int64_t)tile.adapter * a.N + at) * a.R + 4 * tq;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const int left = tile.rank - (16 * s + 4 * tq);  // values within the rank
+            uint2 w = at < a.N && left > 0 ? __ldg(reinterpret_cast<const uint2 *>(row + 16 * s)) : make_uint2(0, 0);
+            if (left < 4) w.y &= left == 3 ? 0x0000FFFFu : 0u;
+            if (left < 2) w.x &= 0x0000FFFFu;
+            b[i][s][0] = w.x, b[i][s][1] = w.y;
+        }
+    }
+}
+// Four values of a row of y from column n on (row null: none)
+template <bool VEC>
+__device__ __forceinline__ float4 load_y(const LoraArgs &a, const float *row, int64_t n) {
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int64_t left = row ? a.N - n : 0;
+    if (VEC) {
+        if (left > 0) y = *reinterpret_cast<const float4 *>(row + n);
+    } else {
+        if (left > 0) y.x = row[n];
+        if (left > 1) y.y = row[n + 1];
+        if (left > 2) y.z = row[n + 2];
+        if (left > 3) y.w = row[n + 3];
+    }
+    return y;
+}
+template <bool VEC>
+__device__ __forceinline__ void store_y(const LoraArgs &a, float *row, int64_t n, float4 y) {
+    const int64_t left = row ? a.N - n : 0;
+    if (VEC) {
+        if (left > 0) *reinterpret_cast<float4 *>(row + n) = y;
+    } else {
+        if (left > 0) row[n] = y.x;
+        if (left > 1) row[n + 1] = y.y;
+        if (left > 2) row[n + 2] = y.z;
+        if (left > 3) row[n + 3] = y.w;
+    }
+}
+// acc += the group's products with step s of the tokens, the smallest pieces first
+template <int KS>
+__device__ __forceinline__ void multiply(float (&acc)[2][4], const uint32_t (&frag)[3][4], const uint32_t (&b)[2][KS][2], int s) {
+#pragma unroll
+    for (int k = 2; k >= 0; --k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) mma_bf16_16816(acc[i], frag[k], b[i][s][0], b[i][s][1], acc[i]);
+}
+__device__ __forceinline__ float4 plus(float4 y, const float (&acc)[2][4], int h) {
+    return make_float4(y.x + acc[0][2 * h], y.y + acc[0][2 * h + 1], y.z + acc[1][2 * h], y.w + acc[1][2 * h + 1]);
+}
+
 // KS: MMA steps over the inner values (R / 16, or the next power of two); CG: groups of 16 columns a warp
 template <int KS, int CG, bool VEC>
 __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
     __shared__ int list[kTileTokens];
-    __shared__ uint32_t masks[2 * kWarps];
-    __shared__ __align__(16) float v[16][KS * 16 + 4];
+    __shared__ uint32_t masks[8];
     // before the previous kernel has ended: what it does not write (it has itself waited for the writer of y and of the list)
-    const Tile tile = tile_of(a, blockIdx.y, list, masks);
+    const Tile tile = tile_of<kThreads>(a, blockIdx.y, list, masks);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+    const int64_t n0 = ((int64_t)blockIdx.x * kWarps + warp) * (16 * CG);
     if (tile.count == 0) {
         pdl_wait();
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-    const int64_t n0 = ((int64_t)blockIdx.x * kWarps + warp) * (16 * CG) + 4 * tq;
-    const float scale = a.scales ? __ldg(a.scales + tile.adapter) : 1.f;
-    // B: column 2 j + e of MMA tile i of a group is the group's column 4 j + 2 i + e; inner values 16 s + 4 tq .. + 3
     uint32_t b[CG][2][KS][2];
 #pragma unroll
-    for (int c = 0; c < CG; ++c)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t n = n0 - 4 * tq + 16 * c + 4 * (g >> 1) + 2 * i + (g & 1);
-            const uint16_t *row = a.b + ((int64_t)tile.adapter * a.N + n) * a.R + 4 * tq;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const int left = tile.rank - (16 * s + 4 * tq);  // values within the rank
-                uint2 w = n < a.N && left > 0 ? __ldg(reinterpret_cast<const uint2 *>(row + 16 * s)) : make_uint2(0, 0);
-                if (left < 4) w.y &= left == 3 ? 0x0000FFFFu : 0u;
-                if (left < 2) w.x &= 0x0000FFFFu;
-                b[c][i][s][0] = w.x, b[c][i][s][1] = w.y;
-            }
-        }
-    bool waited = false;
-    for (int m0 = 0; m0 < tile.count; m0 += 16) {
-        // y's values of rows g and g + 8
+    for (int c = 0; c < CG; ++c) load_b<KS>(a, tile, n0 + 16 * c, b[c]);
+    // y's values of rows m0 + g and m0 + g + 8 on their way
+    struct Rows {
+        float *at[2];
         float4 y[CG][2];
-        float *rows[2];
+    };
+    auto load = [&](int m0, Rows &r) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            rows[h] = m0 + g + 8 * h < tile.count ? a.y + list[m0 + g + 8 * h] * a.ldy + n0 : nullptr;
+            r.at[h] = m0 + g + 8 * h < tile.count ? a.y + list[m0 + g + 8 * h] * a.ldy : nullptr;
 #pragma unroll
-            for (int c = 0; c < CG; ++c) {
-                y[c][h] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (rows[h]) {
-                    const int64_t left = a.N - (n0 + 16 * c);
-                    const float *p = rows[h] + 16 * c;
-                    if (VEC) {
-                        if (left > 0) y[c][h] = *reinterpret_cast<const float4 *>(p);
-                    } else {
-                        if (left > 0) y[c][h].x = p[0];
-                        if (left > 1) y[c][h].y = p[1];
-                        if (left > 2) y[c][h].z = p[2];
-                        if (left > 3) y[c][h].w = p[3];
-                    }
-                }
-            }
+            for (int c = 0; c < CG; ++c) r.y[c][h] = load_y<VEC>(a, r.at[h], n0 + 16 * c + 4 * tq);
         }
-        if (!waited) {
-            pdl_wait();
-            pdl_trigger();
-        }
-        waited = true;
-        for (int i = threadIdx.x; i < 16 * KS * 16; i += kThreads) {
-            const int row = i / (KS * 16), r = i % (KS * 16);
-            float sum = 0.f;
-            if (m0 + row < tile.count && r < tile.rank) {
-                const float *p = a.part + (int64_t)list[m0 + row] * a.R + r;
-                for (int s = 0; s < a.splits; ++s) sum += __ldcg(p + (int64_t)s * a.T * a.R);
-            }
-            v[row][r] = sum * scale;
-        }
-        __syncthreads();
+    };
+    auto finish = [&](int m0, const Rows &r) {
         float acc[CG][2][4] = {};
+        const float *v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v[h] = m0 + g + 8 * h < tile.count ? a.v + (int64_t)list[m0 + g + 8 * h] * a.R + 4 * tq : nullptr;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            uint32_t frag[3][4];
+            float4 t[1][2];
+            uint32_t frag[1][3][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float4 t = *reinterpret_cast<const float4 *>(&v[g + 8 * h][16 * s + 4 * tq]);
-                uint32_t p0[3], p1[3], p2[3], p3[3];
-                split3(t.x, p0), split3(t.y, p1), split3(t.z, p2), split3(t.w, p3);
+            for (int h = 0; h < 2; ++h)
+                t[0][h] = v[h] && 16 * s + 4 * tq < a.R ? __ldcg(reinterpret_cast<const float4 *>(v[h] + 16 * s)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            split_rows<1>(t, frag);
 #pragma unroll
-                for (int k = 0; k < 3; ++k) frag[k][h] = p0[k] | p1[k] << 16, frag[k][2 + h] = p2[k] | p3[k] << 16;
-            }
-#pragma unroll
-            for (int k = 2; k >= 0; --k)
-#pragma unroll
-                for (int c = 0; c < CG; ++c)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) mma_bf16_16816(acc[c][i], frag[k], b[c][i][s][0], b[c][i][s][1], acc[c][i]);
+            for (int c = 0; c < CG; ++c) multiply<KS>(acc[c], frag[0], b[c], s);
         }
-        __syncthreads();  // v is free
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (!rows[h]) continue;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int c = 0; c < CG; ++c) {
-                const int64_t left = a.N - (n0 + 16 * c);
-                float *p = rows[h] + 16 * c;
-                const float4 t = make_float4(y[c][h].x + acc[c][0][2 * h], y[c][h].y + acc[c][0][2 * h + 1],
-                                             y[c][h].z + acc[c][1][2 * h], y[c][h].w + acc[c][1][2 * h + 1]);
-                if (VEC) {
-                    if (left > 0) *reinterpret_cast<float4 *>(p) = t;
-                } else {
-                    if (left > 0) p[0] = t.x;
-                    if (left > 1) p[1] = t.y;
-                    if (left > 2) p[2] = t.z;
-                    if (left > 3) p[3] = t.w;
-                }
+            for (int c = 0; c < CG; ++c) store_y<VEC>(a, r.at[h], n0 + 16 * c + 4 * tq, plus(r.y[c][h], acc[c], h));
+    };
+    // two sets in turn (copied from one to the other they would be waited for)
+    Rows even, odd;
+    load(0, even);
+    pdl_wait();
+    pdl_trigger();
+    for (int m0 = 0; m0 < tile.count; m0 += 32) {
+        if (m0 + 16 < tile.count) load(m0 + 16, odd);
+        finish(m0, even);
+        if (m0 + 16 >= tile.count) break;
+        if (m0 + 32 < tile.count) load(m0 + 32, even);
+        finish(m0 + 16, odd);
+    }
+}
+
+// Both products of a tile by one cluster: K and the columns are dealt to its CTAs.  G: groups of 16 columns on their way at once.
+template <int NT, int U, int W, int G, bool VEC>
+__global__ void __launch_bounds__(W * 32, NT <= 4 ? 2 : 1) tile_kernel(const LoraArgs a) {
+    constexpr int KS = NT == 1 ? 1 : NT / 2;
+    pdl_wait();
+    pdl_trigger();
+    __shared__ int list[kTileTokens];
+    __shared__ uint32_t masks[16];
+    extern __shared__ float red_smem[];
+    float (*const red)[16][NT * 8 + 1] = reinterpret_cast<float (*)[16][NT * 8 + 1]>(red_smem);  // [W]
+    __shared__ __align__(16) float v[16][KS * 16 + 4];
+    const Tile tile = tile_of<W * 32>(a, blockIdx.y, list, masks);
+    if (tile.count == 0) return;  // (so does the whole cluster)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+    const float scale = a.scales ? __ldg(a.scales + tile.adapter) : 1.f;
+    // this CTA's columns, whole groups
+    const int64_t per = ((a.N + gridDim.x - 1) / gridDim.x + 15) / 16 * 16, first = min(per * blockIdx.x, a.N), last = min(first + per, a.N);
+    if (threadIdx.x == 0 && last > first && 4 * tile.rank >= 3 * a.R) {  // (of lower ranks too much would not be read)
+        const uint16_t *from = a.b + ((int64_t)tile.adapter * a.N + first) * a.R;
+        const int64_t bytes = (last - first) * a.R * 2;
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(bytes < (1 << 19) ? bytes : 1 << 19)) : "memory");
+    }
+    for (int i = threadIdx.x; i < 16 * (KS * 16 + 4); i += W * 32) (&v[0][0])[i] = 0.f;  // (what lies beyond R)
+    struct Batch {
+        uint32_t b[G][2][KS][2];
+        float4 y[G][2];
+    };
+    for (int m0 = 0; m0 < tile.count; m0 += 16) {
+        float *rows[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) rows[h] = m0 + g + 8 * h < tile.count ? a.y + list[m0 + g + 8 * h] * a.ldy : nullptr;
+        auto load = [&](int64_t n, Batch &t) {
+#pragma unroll
+            for (int c = 0; c < G; ++c) {
+                const int64_t at = n + 16 * W * c;
+                load_b<KS>(a, tile, at < last ? at : a.N, t.b[c]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) t.y[c][h] = load_y<VEC>(a, at < last ? rows[h] : nullptr, at + 4 * tq);
             }
+        };
+        // (the first columns are on their way during the first product, the next ones always)
+        Batch even, odd;
+        load(first + 16 * warp, even);
+        inner_sums<NT, U, W>(a, tile, list, m0, red);
+        cluster_sync();
+        // each CTA adds up some of the tokens' sums, for all
+        for (int i = threadIdx.x; i < 16 * a.R; i += W * 32) {
+            const int row = i / a.R, r = i - row * a.R;
+            if (row % kMaxCluster != blockIdx.x) continue;
+            float part[kMaxCluster], s = 0.f;
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) part[c] = ld_shared_cluster_f32(map_shared_rank(smem_u32(&red[0][row][r]), c));
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) s += part[c];
+            s = r < tile.rank ? s * scale : 0.f;
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) st_shared_cluster_f32(map_shared_rank(smem_u32(&v[row][r]), c), s);
         }
+        cluster_sync();
+        float4 t[KS][2];
+        uint32_t frag[KS][3][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) t[s][h] = *reinterpret_cast<const float4 *>(&v[g + 8 * h][16 * s + 4 * tq]);
+        split_rows<KS>(t, frag);
+        auto finish = [&](int64_t n, const Batch &t) {
+#pragma unroll
+            for (int c = 0; c < G; ++c) {
+                const int64_t at = n + 16 * W * c;
+                float acc[2][4] = {};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) multiply<KS>(acc, frag[s], t.b[c], s);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) store_y<VEC>(a, at < last ? rows[h] : nullptr, at + 4 * tq, plus(t.y[c][h], acc, h));
+            }
+        };
+        constexpr int64_t STEP = 16 * W * G;
+        for (int64_t n = first + 16 * warp; n < last; n += 2 * STEP) {
+            if (n + STEP < last) load(n + STEP, odd);
+            finish(n, even);
+            if (n + STEP >= last) break;
+            if (n + 2 * STEP < last) load(n + 2 * STEP, even);
+            finish(n + STEP, odd);
+        }
+        // (v is written again only behind the next cluster barrier, which every warp reaches after it has read v)
     }
 }
 
@@ -274,34 +409,51 @@ cudaError_t launch_expand(const LoraArgs &a, bool vec, unsigned tiles, cudaStrea
                       dim3((unsigned)((a.N + columns - 1) / columns), tiles), dim3(kThreads), 0, s, dim3(1), a);
 }
 
-}  // namespace
-
-// (of sizes alone: the workspace is laid out by it)
-LoraSplit lora_split(int64_t K, int64_t T, int n_adapters) {
-    constexpr int kCtas = 4 * 152;  // four an SM, were every tile there
-    const int64_t tiles = T <= kLoraSmall ? T : moe_max_tiles(n_adapters, T);
-    int64_t splits = (kCtas + tiles - 1) / tiles;
-    const int64_t most = (K + 32 * kWarps - 1) / (32 * kWarps);
-    if (splits > most) splits = most;
-    LoraSplit r;
-    const int64_t unit = 32 * kWarps;
-    r.k_chunk = ((K + splits - 1) / splits + unit - 1) / unit * unit;
-    r.splits = (int)((K + r.k_chunk - 1) / r.k_chunk);
-    return r;
+// K over `splits` CTAs, in whole steps of a CTA's warps; returns how many have something to do
+unsigned split_k(LoraArgs &a, int64_t splits, int64_t unit) {
+    if (splits > kMaxCluster) splits = kMaxCluster;
+    if (splits > (a.K + unit - 1) / unit) splits = (a.K + unit - 1) / unit;
+    a.k_chunk = (int32_t)(((a.K + splits - 1) / splits + unit - 1) / unit * unit);
+    return (unsigned)((a.K + a.k_chunk - 1) / a.k_chunk);
 }
 
-cudaError_t launch_lora_add(const DeviceInfo &di, const LoraArgs &a, cudaStream_t s) {
-    unsigned tiles = (unsigned)a.T;
-    if (a.tiles) {
-        const cudaError_t e = launch_moe_route(a.ids, a.T, a.n_adapters, a.offsets, a.perm, false, a.tiles, a.n_tiles, s);
-        if (e != cudaSuccess) return e;
-        tiles = (unsigned)moe_max_tiles(a.n_adapters, a.T);
-    }
-    auto shrink = a.R <= 8 ? shrink_kernel<1, 4> : a.R <= 16 ? shrink_kernel<2, 4> : a.R <= 32 ? shrink_kernel<4, 2>
-                : a.R <= 64 ? shrink_kernel<8, 1> : shrink_kernel<16, 1>;
-    const cudaError_t e = launch_pdl(shrink, dim3((unsigned)a.splits, tiles), dim3(kThreads), 0, s, dim3(1), a);
+template <int NT, int U, int W>
+cudaError_t launch_shrink(LoraArgs &a, unsigned tiles, cudaStream_t s) {
+    // 16 tokens a CTA (the tokens of a tile over several), and CTAs enough for four an SM, were every tile full
+    constexpr int64_t kCtas = 4 * 152;
+    const unsigned z = kTileTokens / 16;
+    const unsigned splits = split_k(a, (kCtas + (int64_t)tiles * z - 1) / ((int64_t)tiles * z), 32 * W);
+    return launch_pdl(shrink_kernel<NT, U, W>, dim3(splits, tiles, z), dim3(W * 32), 0, s, dim3(splits), a);
+}
+
+template <int NT, int U, int W, int G>
+cudaError_t launch_tile(LoraArgs &a, bool vec, unsigned tiles, cudaStream_t s) {
+    const unsigned ctas = kMaxCluster;
+    a.k_chunk = (int32_t)(((a.K + ctas - 1) / ctas + 31) / 32 * 32);
+    auto kern = vec ? tile_kernel<NT, U, W, G, true> : tile_kernel<NT, U, W, G, false>;
+    constexpr int smem = W * 16 * (NT * 8 + 1) * 4;
+    const cudaError_t e = smem > 32 * 1024 ? ensure_smem((const void *)kern, smem) : cudaSuccess;
     if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(ctas, tiles), dim3(W * 32), smem, s, dim3(ctas), a);
+}
+
+}  // namespace
+
+cudaError_t launch_lora_add(const DeviceInfo &di, LoraArgs &a, cudaStream_t s) {
     const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.ldy % 4 == 0 && a.N % 4 == 0;
+    if (!a.tiles) {
+        const unsigned tiles = (unsigned)(a.n_adapters < a.T ? a.n_adapters : a.T);
+        return a.R <= 8 ? launch_tile<1, 4, 8, 2>(a, vec, tiles, s) : a.R <= 16 ? launch_tile<2, 4, 8, 2>(a, vec, tiles, s)
+             : a.R <= 32 ? launch_tile<4, 2, 8, 1>(a, vec, tiles, s) : a.R <= 64 ? launch_tile<8, 2, 8, 2>(a, vec, tiles, s)
+                         : launch_tile<16, 1, 8, 1>(a, vec, tiles, s);
+    }
+    cudaError_t e = launch_moe_route(a.ids, a.T, a.n_adapters, a.offsets, a.perm, false, a.tiles, a.n_tiles, s);
+    if (e != cudaSuccess) return e;
+    const unsigned tiles = (unsigned)moe_max_tiles(a.n_adapters, a.T);
+    e = a.R <= 8 ? launch_shrink<1, 4, 8>(a, tiles, s) : a.R <= 16 ? launch_shrink<2, 4, 8>(a, tiles, s)
+      : a.R <= 32 ? launch_shrink<4, 2, 8>(a, tiles, s) : a.R <= 64 ? launch_shrink<8, 2, 8>(a, tiles, s)
+                  : launch_shrink<16, 1, 4>(a, tiles, s);
+    if (e != cudaSuccess) return e;
     return a.R <= 16 ? launch_expand<1, 4>(a, vec, tiles, s) : a.R <= 32 ? launch_expand<2, 4>(a, vec, tiles, s)
          : a.R <= 64 ? launch_expand<4, 2>(a, vec, tiles, s) : launch_expand<8, 1>(a, vec, tiles, s);
 }
