@@ -192,24 +192,44 @@ __device__ __forceinline__ void split_rows(const float4 (&t)[KS][2], uint32_t (&
         }
 }
 
-// A group of 16 columns from n on.  B: column 2 j + e of MMA tile i is the group's column 4 j + 2 i + e; inner values 16 s + 4 tq .. + 3.
+// A lane's part of B's rows: inner values 16 s + 4 tq .. + 3, what lies beyond the rank taken out.  In a group of 16 columns,
+// column 2 j + e of MMA tile i is the group's column 4 j + 2 i + e.
 template <int KS>
-__device__ __forceinline__ void load_b(const LoraArgs &a, const Tile &tile, int64_t n, uint32_t (&b)[2][KS][2]) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t at = n + 4 * (g >> 1) + 2 * i + (g & 1);
-        const uint16_t *row = a.b + ((int64_t)tile.adapter * a.N + at) * a.R + 4 * tq;
+struct Columns {
+    const uint16_t *row;  // the lane's first column of group 0
+    int64_t left;         // columns from there on
+    int in;               // steps of which something lies within the rank
+    uint32_t mask[KS][2];
+    __device__ __forceinline__ Columns(const LoraArgs &a, const Tile &tile) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3, first = 4 * (g >> 1) + (g & 1);
+        row = a.b + ((int64_t)tile.adapter * a.N + first) * a.R + 4 * tq;
+        left = a.N - first;
+        in = (tile.rank - 4 * tq + 15) >> 4;  // (not positive: none)
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const int left = tile.rank - (16 * s + 4 * tq);  // values within the rank
-            uint2 w = at < a.N && left > 0 ? __ldg(reinterpret_cast<const uint2 *>(row + 16 * s)) : make_uint2(0, 0);
-            if (left < 4) w.y &= left == 3 ? 0x0000FFFFu : 0u;
-            if (left < 2) w.x &= 0x0000FFFFu;
-            b[i][s][0] = w.x, b[i][s][1] = w.y;
+            const int n = tile.rank - (16 * s + 4 * tq);
+            mask[s][0] = n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0x0000FFFFu : 0u;
+            mask[s][1] = n >= 4 ? 0xFFFFFFFFu : n == 3 ? 0x0000FFFFu : 0u;
         }
     }
-}
+    // the group that begins at column n (none: n beyond N)
+    __device__ __forceinline__ void load(int R, int64_t n, uint32_t (&b)[2][KS][2]) const {
+        const uint16_t *p = row + n * R;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const uint2 w = n + 2 * i < left && s < in ? __ldg(reinterpret_cast<const uint2 *>(p + 2 * i * R + 16 * s)) : make_uint2(0, 0);
+                b[i][s][0] = w.x, b[i][s][1] = w.y;
+            }
+    }
+    __device__ __forceinline__ void cut(uint32_t (&b)[2][KS][2]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) b[i][s][0] &= mask[s][0], b[i][s][1] &= mask[s][1];
+    }
+};
 // Four values of a row of y from column n on (row null: none)
 template <bool VEC>
 __device__ __forceinline__ float4 load_y(const LoraArgs &a, const float *row, int64_t n) {
@@ -262,9 +282,10 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
         pdl_wait();
         return;
     }
+    const Columns<KS> columns(a, tile);
     uint32_t b[CG][2][KS][2];
 #pragma unroll
-    for (int c = 0; c < CG; ++c) load_b<KS>(a, tile, n0 + 16 * c, b[c]);
+    for (int c = 0; c < CG; ++c) columns.load(a.R, n0 + 16 * c, b[c]);
     // y's values of rows m0 + g and m0 + g + 8 on their way
     struct Rows {
         float *at[2];
@@ -304,6 +325,8 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
     load(0, even);
     pdl_wait();
     pdl_trigger();
+#pragma unroll
+    for (int c = 0; c < CG; ++c) columns.cut(b[c]);
     for (int m0 = 0; m0 < tile.count; m0 += 32) {
         if (m0 + 16 < tile.count) load(m0 + 16, odd);
         finish(m0, even);
@@ -336,6 +359,7 @@ __global__ void __launch_bounds__(W * 32, NT <= 4 ? 2 : 1) tile_kernel(const Lor
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(bytes < (1 << 19) ? bytes : 1 << 19)) : "memory");
     }
     for (int i = threadIdx.x; i < 16 * (KS * 16 + 4); i += W * 32) (&v[0][0])[i] = 0.f;  // (what lies beyond R)
+    const Columns<KS> columns(a, tile);
     struct Batch {
         uint32_t b[G][2][KS][2];
         float4 y[G][2];
@@ -348,7 +372,7 @@ __global__ void __launch_bounds__(W * 32, NT <= 4 ? 2 : 1) tile_kernel(const Lor
 #pragma unroll
             for (int c = 0; c < G; ++c) {
                 const int64_t at = n + 16 * W * c;
-                load_b<KS>(a, tile, at < last ? at : a.N, t.b[c]);
+                columns.load(a.R, at < last ? at : a.N, t.b[c]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) t.y[c][h] = load_y<VEC>(a, at < last ? rows[h] : nullptr, at + 4 * tq);
             }
@@ -379,10 +403,11 @@ __global__ void __launch_bounds__(W * 32, NT <= 4 ? 2 : 1) tile_kernel(const Lor
 #pragma unroll
             for (int s = 0; s < KS; ++s) t[s][h] = *reinterpret_cast<const float4 *>(&v[g + 8 * h][16 * s + 4 * tq]);
         split_rows<KS>(t, frag);
-        auto finish = [&](int64_t n, const Batch &t) {
+        auto finish = [&](int64_t n, Batch &t) {
 #pragma unroll
             for (int c = 0; c < G; ++c) {
                 const int64_t at = n + 16 * W * c;
+                columns.cut(t.b[c]);
                 float acc[2][4] = {};
 #pragma unroll
                 for (int s = 0; s < KS; ++s) multiply<KS>(acc, frag[s], t.b[c], s);
