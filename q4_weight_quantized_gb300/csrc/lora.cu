@@ -479,7 +479,7 @@ cudaError_t launch_lora_add(const DeviceInfo &di, LoraArgs &a, cudaStream_t s) {
       : a.R <= 32 ? launch_shrink<4, 2, 8>(a, tiles, s) : a.R <= 64 ? launch_shrink<8, 2, 8>(a, tiles, s)
                   : launch_shrink<16, 1, 4>(a, tiles, s);
     if (e != cudaSuccess) return e;
-    return a.R <= 16 ? launch_expand<1, 4>(a, vec, tiles, s) : a.R <= 32 ? launch_expand<2, 4>(a, vec, tiles, s)
+    return a.R <= 16 ? launch_expand<1, 2>(a, vec, tiles, s) : a.R <= 32 ? launch_expand<2, 4>(a, vec, tiles, s)
          : a.R <= 64 ? launch_expand<4, 2>(a, vec, tiles, s) : launch_expand<8, 1>(a, vec, tiles, s);
 }
 

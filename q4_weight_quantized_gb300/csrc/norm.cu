@@ -49,8 +49,35 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // v in 8 bits at the scale s = a / 127, a being the largest |v| of its block
-__device__ __forceinline__ float in_eight(float v, float s, float a) {
-    return a > 0.f ? copysignf(fminf(rintf(fabsf(v) / s), 127.f), v) : 0.f;
+__device__ __forceinline__ int in_eight(float v, float s, float a) {
+    return a > 0.f ? (int)copysignf(fminf(rintf(fabsf(v) / s), 127.f), v) : 0;
+}
+// Four of them as bytes, and s.  For a of usual size s is a times the reciprocal of 127, corrected by its remainder (Markstein's
+// division: the nearest value), and v / s is v times the reciprocal of s, off by 2^-22 of it, 2^-15 at most: added to 3 * 2^22 it is
+// rounded to a whole number whose low byte lies in the sum's; where it lies within 10^-4 of the middle between two, the division
+// decides.  (A division for every value: 57.8 us for 4096 rows of 5120.)
+__device__ __forceinline__ uint32_t four_in_eight(const float *v, float a, float &s) {
+    constexpr float kInv = 1.0f / 127.0f, kMagic = 12582912.0f;
+    if (a > 1e-30f && a < 1e38f) {
+        s = a * kInv;
+        s = fmaf(fmaf(-127.0f, s, a), kInv, s);
+        const float inv = rcp_approx(s);
+        uint32_t b[4];
+        float off = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float u = fmaf(v[x], inv, kMagic);
+            b[x] = __float_as_uint(u);
+            off = fmaxf(off, fabsf(fmaf(v[x], inv, kMagic - u)));
+        }
+        if (off < 0.4999f) return prmt(prmt(b[0], b[1], 0x0040u), prmt(b[2], b[3], 0x0040u), 0x5410u);
+    } else {
+        s = a / 127.0f;
+    }
+    uint32_t word = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) word |= ((uint32_t)in_eight(v[x], s, a) & 0xFFu) << (8 * x);
+    return word;
 }
 
 // A row of D values over a CTA: thread t holds group i (of NV) of four values, elements
@@ -125,12 +152,9 @@ struct Slice {
                 uint32_t top = max(m01, m23);
 #pragma unroll
                 for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                const float a = __uint_as_float(top), s = a / 127.0f;
                 if (!in(i, 0)) continue;
-                uint32_t word = 0;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) word |= ((uint32_t)(int)in_eight(v[4 * i + x], s, a) & 0xFFu) << (8 * x);
-                *reinterpret_cast<uint32_t *>(q + at(i, 0)) = word;
+                float s;
+                *reinterpret_cast<uint32_t *>(q + at(i, 0)) = four_in_eight(v + 4 * i, __uint_as_float(top), s);
                 if ((tid & 7) == 0) scale[at(i, 0) / 32] = s;
             } else {
 #pragma unroll
@@ -138,7 +162,7 @@ struct Slice {
                     const float a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v[4 * i + x]))));
                     const float s = a / 127.0f;
                     if (!in(i, x)) continue;
-                    q[at(i, x)] = (int8_t)(int)in_eight(v[4 * i + x], s, a);
+                    q[at(i, x)] = (int8_t)in_eight(v[4 * i + x], s, a);
                     if ((tid & 31) == 0) scale[at(i, x) / 32] = s;
                 }
             }
@@ -440,7 +464,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a
             if (a.x) a.x[row * a.ldx + e] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
             if (a.q) {  // (D % 32 == 0: whole warps)
                 const float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v)))), s = top / 127.0f;
-                a.q[row * D + e] = (int8_t)(int)in_eight(v, s, top);
+                a.q[row * D + e] = (int8_t)in_eight(v, s, top);
                 if ((threadIdx.x & 31) == 0) a.q_scale[row * (D / 32) + e / 32] = s;
             }
         }

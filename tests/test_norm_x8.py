@@ -105,6 +105,30 @@ def test_eight_bits_of_zeros_and_of_no_numbers(D, pad):
     assert np.array_equal(q.cpu().numpy(), wq)
 
 
+@pytest.mark.parametrize("M,pad", [(4, 0), (4, 1), (800, 0)])
+def test_eight_bits_near_the_middle_and_over_all_sizes(M, pad):
+    """Values at, just below and just above the middle between two whole numbers of steps, at every power of two; scales of any
+    mantissa: the rule's bits."""
+    D, g = 4096, gen_of(6)
+    e = torch.randint(-140, 126, (M, D // 32, 1), generator=g, device="cuda").float()
+    top = (1 + torch.rand(M, D // 32, 1, generator=g, device="cuda")) * torch.exp2(e)
+    k = torch.randint(-127, 127, (M, D // 32, 32), generator=g, device="cuda").float()
+    near = torch.randint(-2, 3, (M, D // 32, 32), generator=g, device="cuda")
+    h = ((k + 0.5) * (top / 127.0))
+    h = (h.view(torch.int32) + near.to(torch.int32)).view(torch.float32)  # neighbours of the middle
+    h = torch.minimum(h.abs(), top) * torch.sign(h)
+    h[:, :, 7:8] = top
+    h[:, 0] = torch.where(near[:, 0] > 0, torch.full_like(k[:, 0], 127.0), k[:, 0] + 0.5)  # a scale of 1, exact ties
+    h[:, 0, 7] = 127.0
+    flat = torch.zeros(M, D + pad, device="cuda")
+    flat[:, :D] = h.reshape(M, D)
+    q, s = torch.zeros(M, D, dtype=torch.int8, device="cuda"), torch.zeros(M, D // 32, device="cuda")
+    q4k.q4k_norm_residual_x8(M, D, None, 0, 0, None, None, 0.0, None, 0, 1.0, flat, None, D + pad, q4k.Q4K_RES_FP32, 0, None, None, 0.0,
+                             None, 0, q, s)
+    wq, ws = step_ref.in_eight(flat[:, :D].cpu().numpy())
+    assert np.array_equal(s.cpu().numpy(), ws) and np.array_equal(q.cpu().numpy(), wq)
+
+
 def test_eight_bits_go_into_the_product(ref, syn):
     """The output is what q4k_gemm_x8 takes: the same product as with the rule's bits from the host."""
     M, D, N = 5, 1024, 256
