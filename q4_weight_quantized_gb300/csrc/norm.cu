@@ -52,32 +52,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ int in_eight(float v, float s, float a) {
     return a > 0.f ? (int)copysignf(fminf(rintf(fabsf(v) / s), 127.f), v) : 0;
 }
-// Four of them as bytes, and s.  For a of usual size s is a times the reciprocal of 127, corrected by its remainder (Markstein's
-// division: the nearest value), and v / s is v times the reciprocal of s, off by 2^-22 of it, 2^-15 at most: added to 3 * 2^22 it is
-// rounded to a whole number whose low byte lies in the sum's; where it lies within 10^-4 of the middle between two, the division
-// decides.  (A division for every value: 57.8 us for 4096 rows of 5120.)
-__device__ __forceinline__ uint32_t four_in_eight(const float *v, float a, float &s) {
+// Four of them as bytes, and s, for a of usual size; false where this may not be the rule's rounding.  s is a times the reciprocal
+// of 127, corrected by its remainder (Markstein's division: the nearest value), and v / s is v times the reciprocal of s, off by
+// 2^-22 of it, 2^-15 at most: added to 3 * 2^22 it is rounded to a whole number whose low byte lies in the sum's; not to be relied on
+// where it lies within 5 10^-5 of the middle between two.  (A division for every value: 57.8 us for 4096 rows of 5120.)
+__device__ __forceinline__ bool four_in_eight(const float *v, float a, float &s, uint32_t &word) {
     constexpr float kInv = 1.0f / 127.0f, kMagic = 12582912.0f;
-    if (a > 1e-30f && a < 1e38f) {
-        s = a * kInv;
-        s = fmaf(fmaf(-127.0f, s, a), kInv, s);
-        const float inv = rcp_approx(s);
-        uint32_t b[4];
-        float off = 0.f;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float u = fmaf(v[x], inv, kMagic);
-            b[x] = __float_as_uint(u);
-            off = fmaxf(off, fabsf(fmaf(v[x], inv, kMagic - u)));
-        }
-        if (off < 0.4999f) return prmt(prmt(b[0], b[1], 0x0040u), prmt(b[2], b[3], 0x0040u), 0x5410u);
-    } else {
-        s = a / 127.0f;
-    }
-    uint32_t word = 0;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) word |= ((uint32_t)in_eight(v[x], s, a) & 0xFFu) << (8 * x);
-    return word;
+    s = a * kInv;
+    s = fmaf(fmaf(-127.0f, s, a), kInv, s);
+    const float inv = rcp_approx(s);
+    const float2 i2 = make_float2(inv, inv), m2 = make_float2(kMagic, kMagic), none = make_float2(-1.f, -1.f);
+    const float2 x = make_float2(v[0], v[1]), y = make_float2(v[2], v[3]);
+    const float2 u = fma2(x, i2, m2), w = fma2(y, i2, m2);
+    const float2 du = fma2(x, i2, fma2(u, none, m2)), dw = fma2(y, i2, fma2(w, none, m2));
+    word = prmt(prmt(__float_as_uint(u.x), __float_as_uint(u.y), 0x0040u), prmt(__float_as_uint(w.x), __float_as_uint(w.y), 0x0040u), 0x5410u);
+    return fmaxf(fmaxf(fabsf(du.x), fabsf(du.y)), fmaxf(fabsf(dw.x), fabsf(dw.y))) < 0.49995f && a > 1e-30f && a < 1e38f;
 }
 
 // A row of D values over a CTA: thread t holds group i (of NV) of four values, elements
@@ -144,19 +133,40 @@ struct Slice {
     // with a NaN
     __device__ __forceinline__ void store8(int8_t *q, float *scale, const float (&v)[4 * NV]) const {
         // |v| orders like its bits: the largest as whole numbers
+        if constexpr (VEC) {
+            uint32_t top[NV], word[NV];
+            float s[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if constexpr (VEC) {
+            for (int i = 0; i < NV; ++i) {
                 const uint32_t m01 = max(__float_as_uint(fabsf(v[4 * i])), __float_as_uint(fabsf(v[4 * i + 1])));
                 const uint32_t m23 = max(__float_as_uint(fabsf(v[4 * i + 2])), __float_as_uint(fabsf(v[4 * i + 3])));
-                uint32_t top = max(m01, m23);
+                top[i] = max(m01, m23);
+            }
 #pragma unroll
-                for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) top[i] = max(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], o));
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const float a = __uint_as_float(top[i]);
+                if (four_in_eight(v + 4 * i, a, s[i], word[i])) continue;
+                s[i] = a / 127.0f;
+                word[i] = 0;
+#pragma unroll 1
+                for (int x = 0; x < 4; ++x)
+                    word[i] |= ((uint32_t)in_eight(x == 0 ? v[4 * i] : x == 1 ? v[4 * i + 1] : x == 2 ? v[4 * i + 2] : v[4 * i + 3], s[i], a) & 0xFFu) << (8 * x);
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
                 if (!in(i, 0)) continue;
-                float s;
-                *reinterpret_cast<uint32_t *>(q + at(i, 0)) = four_in_eight(v + 4 * i, __uint_as_float(top), s);
-                if ((tid & 7) == 0) scale[at(i, 0) / 32] = s;
-            } else {
+                *reinterpret_cast<uint32_t *>(q + at(i, 0)) = word[i];
+                if ((tid & 7) == 0) scale[at(i, 0) / 32] = s[i];
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if constexpr (!VEC) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const float a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v[4 * i + x]))));
