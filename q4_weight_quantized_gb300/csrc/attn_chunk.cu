@@ -298,6 +298,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
 __device__ __forceinline__ float lo_f32(uint32_t bf16x2) { return __uint_as_float(bf16x2 << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t bf16x2) { return __uint_as_float(bf16x2 & 0xFFFF0000u); }
 
+// 16 consecutive columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+                   "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void set_regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -467,10 +476,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
             // what holds for all rows of the warp: a maximum is to be raised; each has one, and none is far from 0
             bool pending = false, usual = false, far = false;
             // the running maximum becomes m_next; O and l follow
+            float raised = 1.f;  // by what the weights of before were multiplied
             auto raise = [&](bool has_o) {
                 const float neg_new = m_next == -INFINITY ? 0.f : -m_next * f;
                 const float fac = m == m_next || m == -INFINITY ? 1.f : ex2_approx(neg_new - neg);
-                m = m_next, neg = neg_new;
+                m = m_next, neg = neg_new, raised = fac;
                 far = __any_sync(0xFFFFFFFFu, fabsf(neg) > kFar);
                 usual = usual && !far;
                 pending = false;
@@ -553,8 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                 }
                 if (!done) {
                     // ---- a unit's first tile, its edges, a score far above the maximum, soft caps, scales that are not positive,
-                    // pages out of range, maxima far from 0: two passes, 32 slots at a time; slots that no row of the warp sees
-                    // are passed over
+                    // pages out of range, maxima far from 0: 32 slots at a time; slots that no row of the warp sees are passed over
                     tmem_ld_wait();
                     const int from = (int)max((int64_t)0, (int64_t)r.bgn - j0), to = (int)min((int64_t)BN, (int64_t)r.e - j0);
                     const float in = a.cap_in * cc, out = a.softcap * kLog2e;
@@ -582,25 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                             for (int k = 0; k < 32; ++k) s[k] = there >> k & 1u ? s[k] : -INFINITY;
                         }
                     };
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < BN / 32; ++c) {
-                        const uint32_t there = seen(c);
-                        if (!__any_sync(0xFFFFFFFFu, there != 0)) continue;
-                        float s[32], top[2] = {mx, -INFINITY};
-                        scores(c, there, s);
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) top[k / 2 & 1] = fmaxf(fmaxf(top[k / 2 & 1], s[k]), s[k + 1]);
-                        mx = fmaxf(top[0], top[1]);
-                    }
-                    if (m == -INFINITY ? mx > -INFINITY : (mx - m) * f > kSlack) m_next = mx;
-                    if (__any_sync(0xFFFFFFFFu, m_next != m) && !raise(i > u.lo)) {
-                        ok = false;
-                        break;
-                    }
-                    pending = false;
-                    usual = a.softcap == 0.f && !a.odd_scale && !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
-                    const float2 f2 = make_float2(f, f), n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
+                    float most = -INFINITY;
 #pragma unroll 1
                     for (int c = 0; c < BN / 32; ++c) {  // (a group's weights lie over scores that have been read)
                         const uint32_t there = seen(c);
@@ -613,11 +604,38 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                         }
                         float s[32];
                         scores(c, there, s);
+                        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) top[k / 2 & 1] = fmaxf(fmaxf(top[k / 2 & 1], s[k]), s[k + 1]);
+                        const float mx = fmaxf(top[0], top[1]);
+                        most = fmaxf(most, mx);
+                        // a maximum that cannot wait for the next tile: the weights of this one's groups before follow, too
+                        const bool now = m == -INFINITY ? mx > -INFINITY : (mx - m) * f > C::JUMP;
+                        if (__any_sync(0xFFFFFFFFu, now)) {
+                            if (now) m_next = mx;
+                            if (!(ok = raise(i > u.lo))) break;
+#pragma unroll 1
+                            for (int b = 0; b < c; ++b) {
+                                tmem_ld16(s_col + 16 * b, p);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) {
+                                    if constexpr (C::E4M3) {
+                                        const float2 w = __half22float2(*reinterpret_cast<const __half2 *>(&p[k]));
+                                        p[k] = pack_f16(w.x * raised, w.y * raised);
+                                    } else {
+                                        p[k] = pack_bf16(lo_f32(p[k]) * raised, hi_f32(p[k]) * raised);
+                                    }
+                                }
+                                tmem_st16(s_col + 16 * b, p);
+                            }
+                        }
                         if (far) {
                             const float m0 = m == -INFINITY ? 0.f : m;
 #pragma unroll
                             for (int k = 0; k < 32; ++k) s[k] = fmaf(s[k] - m0, f, C::LIFT);
                         } else {
+                            const float2 f2 = make_float2(f, f), n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
 #pragma unroll
                             for (int k = 0; k < 32; k += 2) {
                                 const float2 z = fma2(make_float2(s[k], s[k + 1]), f2, n2);
@@ -634,6 +652,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                         tmem_st16(s_col + 16 * c, p);
                     }
+                    if (!ok) break;
+                    const bool up = (most - m) * f > kSlack;
+                    if (up) m_next = most;
+                    pending = __any_sync(0xFFFFFFFFu, up);
+                    usual = a.softcap == 0.f && !a.odd_scale && !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -1008,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                 if (n.boxes) {
                     const int row = lane * a.box_slots;
                     const int pg = __shfl_sync(0xFFFFFFFFu, n.page, row & 31), in = __shfl_sync(0xFFFFFFFFu, n.in, row & 31);
-                    const uint32_t rb = bar.raw + 8 * (2 * w + kv);
+                    const uint32_t rb = bar.raw + 16 * w + 8 * kv;
                     if (lane == 0) mbar_arrive_expect_tx(rb, WROWS * D);
                     __syncwarp();
                     if (row < WROWS) copy_box(to + row * D, kv == 0 ? k_map : v_map, 0, in, n.h, pg, a.head_first != 0, rb);
@@ -1027,12 +1050,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                 }
             };
             Tile now = {}, next = {};
-            bool flying[2] = {false, false};  // copies of the copy engine that have not been waited for
+            bool flying = false;  // copies of the copy engine that have not been waited for
             bool any = more;
             if (more) {
                 now = tile_of();
                 fetch(now, 0), fetch(now, 1);
-                flying[0] = flying[1] = now.boxes;
+                flying = now.boxes;
                 step();
             }
             for (; any && ok; ++tile_count) {
@@ -1045,48 +1068,50 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                     if constexpr (WROWS == 32) page_mask[(tile_count & (kMetaRing - 1)) * 4 + w] = now.mask;
                     else reinterpret_cast<volatile uint16_t *>(page_mask)[(tile_count & (kMetaRing - 1)) * 8 + w] = (uint16_t)now.mask;
                 }
+                // keys and values together: what a wait, a fence or a copy's start costs is paid once
+                const uint32_t slot1 = slot + 1 < NS ? slot + 1 : 0, parity1 = slot + 1 < NS ? parity : parity ^ 1;
+                bool here = issued < (uint32_t)NS || (mbar_wait(bar.empty + 8 * slot, parity, status) && mbar_wait(bar.empty + 8 * slot1, parity1, status));
+                if (now.boxes) {
+                    here = here && mbar_wait(bar.raw + 16 * w, raw_phase, status) && mbar_wait(bar.raw + 16 * w + 8, raw_phase, status);
+                } else {
+                    cp_async_wait<0>();
+                }
+                if (!__all_sync(0xFFFFFFFFu, here) || *abort_flag) {
+                    ok = false;
+                    break;
+                }
+                if (now.boxes) raw_phase ^= 1, flying = false;
+                bool odd = false;
+                constexpr int GROUP = STEPS * PIECES < 4 ? STEPS * PIECES : 4;  // pieces read at a time
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    if (issued >= (uint32_t)NS && (!__all_sync(0xFFFFFFFFu, mbar_wait(bar.empty + 8 * slot, parity, status)) || *abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    if (now.boxes) {
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar.raw + 8 * (2 * w + kv), raw_phase >> kv & 1, status))) {
-                            ok = false;
-                            break;
-                        }
-                        raw_phase ^= 1u << kv;
-                        flying[kv] = false;
-                    } else {
-                        cp_async_wait<0>();
-                    }
-                    const uint32_t from = own + kv * C::RAW + sub * D + 16 * chunk, at = ring + slot * C::SLOT;
-                    const bool check = kv == 1 && now.edge;
-                    bool odd = false;
+                    const uint32_t from = own + kv * C::RAW + sub * D + 16 * chunk, at = ring + (kv == 0 ? slot : slot1) * C::SLOT;
 #pragma unroll
-                    for (int s = 0; s < STEPS; ++s) {
+                    for (int g = 0; g < STEPS * PIECES; g += GROUP) {
+                        uint4 v[GROUP];
 #pragma unroll
-                        for (int x = 0; x < PIECES; ++x) {
-                            const uint4 v = lds128(from + s * AT_ONCE * D + 16 * LANES * x);
-                            uint4 lo = make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
-                            uint4 hi = make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
-                            if (check) odd |= finite_only<true>(lo) | finite_only<true>(hi);
-                            const int c = 2 * (chunk + LANES * x);
-                            sts128(at + place(s * AT_ONCE + sub, c), lo);
-                            sts128(at + place(s * AT_ONCE + sub, c + 1), hi);
+                        for (int x = 0; x < GROUP; ++x) v[x] = lds128(from + (g + x) / PIECES * AT_ONCE * D + 16 * LANES * ((g + x) % PIECES));
+#pragma unroll
+                        for (int x = 0; x < GROUP; ++x) {
+                            uint4 lo = make_uint4(e4m3x2_to_f16x2(v[x].x), e4m3x2_to_f16x2(v[x].x >> 16), e4m3x2_to_f16x2(v[x].y), e4m3x2_to_f16x2(v[x].y >> 16));
+                            uint4 hi = make_uint4(e4m3x2_to_f16x2(v[x].z), e4m3x2_to_f16x2(v[x].z >> 16), e4m3x2_to_f16x2(v[x].w), e4m3x2_to_f16x2(v[x].w >> 16));
+                            if (kv == 1 && now.edge) odd |= finite_only<true>(lo) | finite_only<true>(hi);
+                            const int r = (g + x) / PIECES * AT_ONCE + sub, c = 2 * (chunk + LANES * ((g + x) % PIECES));
+                            sts128(at + place(r, c), lo);
+                            sts128(at + place(r, c + 1), hi);
                         }
                     }
-                    if (odd) *bad_seen = 1;
-                    fence_proxy_async_smem();  // for the MMAs, and for the copy engine, which may write what has been read
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar.full + 8 * slot);
-                    ++issued;
-                    if (++slot == NS) slot = 0, parity ^= 1;
-                    if (follows) {
-                        fetch(next, kv);
-                        flying[kv] = next.boxes;
-                    }
+                }
+                if (odd) *bad_seen = 1;
+                fence_proxy_async_smem();  // for the MMAs, and for the copy engine, which may write what has been read
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar.full + 8 * slot), mbar_arrive(bar.full + 8 * slot1);
+                issued += 2;
+                slot += 2;
+                if (slot >= (uint32_t)NS) slot -= NS, parity ^= 1;
+                if (follows) {
+                    fetch(next, 0), fetch(next, 1);
+                    flying = next.boxes;
                 }
                 now = next;
                 any = follows;
@@ -1094,8 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
             cp_async_wait<0>();
             if (!ok) {
                 if (lane == 0) *abort_flag = 1;
-                for (int kv = 0; kv < 2; ++kv)
-                    if (flying[kv]) (void)mbar_wait(bar.raw + 8 * (2 * w + kv), raw_phase >> kv & 1, status);
+                for (int kv = 0; kv < 2 && flying; ++kv) (void)mbar_wait(bar.raw + 16 * w + 8 * kv, raw_phase, status);
             }
         } else {
             for (; more; ++tile_count) {
