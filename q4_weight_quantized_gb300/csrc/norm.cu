@@ -312,6 +312,9 @@ __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int st
     if (tid == 0)
         for (int i = 0; i < stages; ++i)
             if (blockIdx.x + (int64_t)i * gridDim.x < a.M) copy(blockIdx.x + (int64_t)i * gridDim.x, i);
+    // a limit that only tests a copy (q4k_set_gemv_wait_limit_ns) tests the first row's here, where it is on its way for certain:
+    // behind the weights' loads a short row has mostly landed
+    const bool soon = a.wait_ns >= 1000ull || mbar_wait_limit(smem_u32(&bars[0]), 0, a.status, a.wait_ns);
     // scale * gate * post_w and pre_w
     float wy[4 * NV], wx[4 * NV];
 #pragma unroll
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(640) norm_rows_kernel(const NormArgs a, int st
     int turn = 0, stage = 0;
     uint32_t parity = 0;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
-        const bool landed = mbar_wait_limit(smem_u32(&bars[stage]), parity, a.status, a.wait_ns);
+        const bool landed = soon && mbar_wait_limit(smem_u32(&bars[stage]), parity, a.status, a.wait_ns);
         const uint8_t *at = ring + stage * stage_bytes;
         float v[4 * NV], h[4 * NV];
 #pragma unroll
