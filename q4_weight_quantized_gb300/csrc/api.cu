@@ -226,19 +226,19 @@ bool make_cache_tmap(CUtensorMap *m, const void *pool, const KvView &c, int box_
         int32_t size, heads, dim, e4m3, box0, box1, swizzle, unused;
         bool operator==(const Key &o) const { return std::memcmp(this, &o, sizeof o) == 0; }
     };
-    constexpr int kSlots = 16;
+    constexpr int kSlots = 256;  // by address: the pools of many layers
     thread_local Key keys[kSlots];
     thread_local CUtensorMap maps[kSlots];
     thread_local int state[kSlots] = {};  // 1: a map, 2: there is none
-    thread_local int next = 0;
     *head_first = c.head_bytes < c.slot_bytes;
     const Key k = {pool, c.page_bytes, c.head_bytes, c.slot_bytes, c.n_pages, c.page_size, c.heads, c.dim, c.e4m3, box_values, box_slots,
                    swizzle, 0};
-    for (int i = 0; i < kSlots; ++i)
-        if (state[i] && keys[i] == k) {
-            if (state[i] == 1) *m = maps[i];
-            return state[i] == 1;
-        }
+    const uint64_t address = reinterpret_cast<uintptr_t>(pool) >> 4;
+    const int at = (int)((address * 0x9E3779B97F4A7C15ull) >> 56);
+    if (state[at] && keys[at] == k) {
+        if (state[at] == 1) *m = maps[at];
+        return state[at] == 1;
+    }
     bool ok = encoder() != nullptr && c.page_bytes < ((int64_t)1 << 40) && c.head_bytes < ((int64_t)1 << 40) &&
               c.slot_bytes < ((int64_t)1 << 40);
     if (ok) {
@@ -253,10 +253,9 @@ bool make_cache_tmap(CUtensorMap *m, const void *pool, const KvView &c, int box_
                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     }
-    keys[next] = k;
-    state[next] = ok ? 1 : 2;
-    if (ok) maps[next] = *m;
-    next = (next + 1) % kSlots;
+    keys[at] = k;
+    state[at] = ok ? 1 : 2;
+    if (ok) maps[at] = *m;
     return ok;
 }
 

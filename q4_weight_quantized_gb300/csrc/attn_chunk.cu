@@ -54,8 +54,9 @@ struct Cfg {
     static constexpr int LAG = NS - 2;                 // of which so many may be on their way
     // weights in f16 are kept as 2^7 p, in o' and l alike: at most 2^15, and what lies below 2^-32 of the largest is lost
     static constexpr float LIFT = E4M3 ? 7.f : 0.f;
-    // how far (log2) a score may exceed the maximum that its tile's weights are taken by: what their type holds
-    static constexpr float JUMP = E4M3 ? kSlack : 64.f;
+    // how far (log2) a score may exceed the maximum that its tile's weights are taken by: what f16 holds, and what leaves O room
+    // for values up to 2^111
+    static constexpr float JUMP = E4M3 ? kSlack : 16.f;
     static constexpr int QBYTES = ROWS * D * 2;
     static constexpr int MISC = 768 + (E4M3 ? 2 * ROWS : 0);  // barriers and flags; for an e4m3 cache the factors of two units' rows
     static constexpr int RAW = E4M3 ? BN * D : 0;      // bytes of a tile as it lies in an e4m3 cache: one of keys, one of values
@@ -515,7 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                 tc_fence_after();
                 if constexpr (C::E4M3) {
                     if (i == u.lo) {  // (written before the tile's queries were there)
-                        cc = a.scale_log2 * __uint_as_float((uint32_t)q_factor[(units & 1) * C::ROWS + t * 128 + row_in] << 23);
+                        // (not 0, with which a masked score would give NaN)
+                        cc = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)q_factor[(units & 1) * C::ROWS + t * 128 + row_in] << 23), 1.17549435e-38f);
                         f = a.softcap > 0.f ? 1.f : cc;
                     }
                 }

@@ -508,10 +508,10 @@ q4k_status q4k_attn_chunk(const q4k_kv_cache *cache, const int32_t *starts, cons
     a.window = window < kInt31 ? window : 0;  // no sequence is that long
     a.odd_scale = !(scale > 0.f);
     a.score_sign = scale < 0.f ? -1.f : scale > 0.f ? 1.f : 0.f;
-    a.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * cache->k_scale * 1.4426950408889634f;
+    a.scale_log2 = scale == 0.f ? 1.f : std::fmax(std::fabs(scale) * cache->k_scale * 1.4426950408889634f, 1.17549435e-38f);
     a.group_mul = division(a.group, &a.group_shift);
     a.softcap = softcap;
-    a.cap_in = softcap > 0.f ? 2.f / softcap : 0.f;
+    a.cap_in = softcap > 0.f ? std::fmin(2.f / softcap, 3e38f) : 0.f;
     a.v_scale = cache->v_scale;
     uint8_t *base = static_cast<uint8_t *>(ws);
     a.seq_at = reinterpret_cast<int32_t *>(base + l.seq_at);

@@ -292,6 +292,28 @@ def test_chunk_e4m3_small_and_large_queries():
         assert torch.equal(run(k, v, table, starts, [128], q, 0.5 * 2.0 ** -e), one), e
 
 
+def test_chunk_tiny_queries_and_a_tiny_scale():
+    """Scores that are 0 to any precision: every slot that a row sees counts the same, masked ones not at all."""
+    g = gen_of(19)
+    for dtype in (BF, F8):
+        k, v, table, _, _, starts, q = make(128, dtype, 16, "phsd", 1, 3, [40], [170], g)
+        q = (q.float() * 2.0 ** -118).to(BF)
+        o = run(k, v, table, starts, [170], q, 1e-36)
+        ref = reference(k, v, table, starts, [170], q, 0.0)
+        check(o, ref, 128, dtype == F8)
+
+
+def test_chunk_values_of_any_size():
+    """A score far above those of the tiles before, and values near 2^100."""
+    g = gen_of(20)
+    k, v, table, _, _, starts, q = make(128, BF, 16, "phsd", 1, 2, [90], [700], g)
+    v *= 2.0 ** 100
+    for j, f in ((300, 3.0), (301, 5.0), (450, 9.0), (640, 40.0)):  # each above the one before by more than a step
+        k[int(table[0, j // 16]), 0, j % 16] *= f
+    o = run(k, v, table, starts, [700], q, 0.3)
+    check(o, reference(k, v, table, starts, [700], q, 0.3), 128, False)
+
+
 def test_chunk_bad_indices_are_reported_and_left_out():
     g = gen_of(15)
     D, page, n, L = 128, 16, 30, 200

@@ -70,7 +70,8 @@ SHAPES = [  # nA, N, K, R, T, ids, pads and offset of y
     (24, 512, 2048, 16, 32, "mixed", 0, 0, 0), (2, 1000, 520, 24, 33, 1, 16, 4, 0), (5, 300, 768, 32, 64, "runs", 0, 0, 0),
     (7, 129, 136, 48, 100, "mixed", 0, 3, 0), (3, 640, 512, 64, 191, "mixed", 0, 0, 0), (2, 200, 264, 128, 192, "mixed", 0, 0, 0),
     (2, 200, 264, 128, 193, "mixed", 0, 0, 0), (40, 100, 128, 16, 700, "mixed", 0, 0, 2), (3, 333, 256, 72, 1000, "runs", 0, 0, 0),
-    (1, 96, 5120, 16, 400, 0, 0, 0, 0), (1024, 64, 64, 8, 3000, "mixed", 0, 0, 0), (6, 17, 2048, 40, 500, "mixed", 0, 0, 0)]
+    (1, 96, 5120, 16, 400, 0, 0, 0, 0), (1024, 64, 64, 8, 3000, "mixed", 0, 0, 0),
+    (40, 100, 136, 16, 7, "mixed", 0, 0, 0), (1000, 48, 64, 64, 150, "mixed", 0, 0, 3), (3, 5120, 64, 16, 2, "mixed", 0, 0, 0), (6, 17, 2048, 40, 500, "mixed", 0, 0, 0)]
 
 
 @pytest.mark.parametrize("nA,N,K,R,T,ids,pad_x,pad_y,off_y", SHAPES)
@@ -81,6 +82,15 @@ def test_lora(nA, N, K, R, T, ids, pad_x, pad_y, off_y):
     q4k.q4k_check_device()
     check(p, got)
     assert torch.equal(call(p, copy_of(p["y"])), got)  # the same call, the same bits
+
+
+def test_lora_ids_out_of_range_with_more_adapters_than_tokens():
+    p = make(50, 64, 64, 8, 6, "mixed")
+    p["ids"][:] = torch.tensor([3, 50, 3, -1, 2 ** 31 - 1, 49], device="cuda")
+    check(p, call(p, p["y"].clone()))
+    with pytest.raises(q4k.Q4KError) as e:
+        q4k.q4k_check_device()
+    assert e.value.status == q4k.Q4K_ERR_INDEX
 
 
 @pytest.mark.parametrize("T", [40, 300])
