@@ -299,15 +299,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
 __device__ __forceinline__ float lo_f32(uint32_t bf16x2) { return __uint_as_float(bf16x2 << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t bf16x2) { return __uint_as_float(bf16x2 & 0xFFFF0000u); }
 
-// 16 consecutive columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-                   "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                 : "r"(taddr)
-                 : "memory");
-}
-
 template <int N>
 __device__ __forceinline__ void set_regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -477,11 +468,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
             // what holds for all rows of the warp: a maximum is to be raised; each has one, and none is far from 0
             bool pending = false, usual = false, far = false;
             // the running maximum becomes m_next; O and l follow
-            float raised = 1.f;  // by what the weights of before were multiplied
             auto raise = [&](bool has_o) {
                 const float neg_new = m_next == -INFINITY ? 0.f : -m_next * f;
                 const float fac = m == m_next || m == -INFINITY ? 1.f : ex2_approx(neg_new - neg);
-                m = m_next, neg = neg_new, raised = fac;
+                m = m_next, neg = neg_new;
                 far = __any_sync(0xFFFFFFFFu, fabsf(neg) > kFar);
                 usual = usual && !far;
                 pending = false;
@@ -530,13 +520,89 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                     ok = false;
                     break;
                 }
-                bool done = false;
-                if (usual && !masked && !pages) {
+                float2 f2 = make_float2(f, f), n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
+                bool prepare = masked || pages || !usual, fresh = true;
+                for (;;) {
+                    if (prepare) {
+                        // ---- a unit's first tile, its edges, a score far above the maximum, soft caps, scales that are not positive,
+                        // pages out of range, maxima far from 0: the scores as the weights' pass takes them, 32 slots at a time,
+                        // back in their place where they change, and their maximum
+                        tmem_ld_wait();
+                        const int from = (int)max((int64_t)0, (int64_t)r.bgn - j0), to = (int)min((int64_t)BN, (int64_t)r.e - j0);
+                        const float in = a.cap_in * cc, out = a.softcap * kLog2e;
+                        uint32_t(&v)[32] = s[0];
+                        float mx = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < BN / 32; ++c) {
+                            uint32_t there = 0xFFFFFFFFu;  // a bit for each slot that the row sees
+                            if (fresh && (masked || pages)) {
+                                if (pages) there = page_mask[(tile_count & (kMetaRing - 1)) * 4 + c];
+                                const int lo = from - 32 * c, hi = to - 32 * c;
+                                there &= lo <= 0 ? 0xFFFFFFFFu : lo >= 32 ? 0u : 0xFFFFFFFFu << lo;
+                                there &= hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
+                            }
+                            bool changed = __any_sync(0xFFFFFFFFu, there != 0xFFFFFFFFu);
+                            if (changed && !__any_sync(0xFFFFFFFFu, there != 0)) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = 0xFF800000u;
+                            } else {
+                                tmem_ld32(s_col + 32 * c, v);
+                                tmem_ld_wait();
+                                if (fresh && a.odd_scale) {
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * a.score_sign);
+                                    changed = true;
+                                }
+                                if (fresh && a.softcap > 0.f) {
+                                    // c tanh(s / c) = c (1 - 2 / (1 + e^(2 s / c))), in units of log2
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k)
+                                        v[k] = __float_as_uint(fmaf(-2.f * out, rcp_approx(1.f + ex2_approx(__uint_as_float(v[k]) * in)), out));
+                                    changed = true;
+                                }
+                                if (__any_sync(0xFFFFFFFFu, there != 0xFFFFFFFFu)) {
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k) v[k] = there >> k & 1u ? v[k] : 0xFF800000u;
+                                }
+                                float top[2] = {mx, -INFINITY};
+#pragma unroll
+                                for (int k = 0; k < 32; k += 2) top[k / 2 & 1] = fmaxf(fmaxf(top[k / 2 & 1], __uint_as_float(v[k])), __uint_as_float(v[k + 1]));
+                                mx = fmaxf(top[0], top[1]);
+                            }
+                            if (changed) {
+                                tmem_st16(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[16]>(v));
+                                tmem_st16(s_col + 32 * c + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+                            }
+                        }
+                        tmem_st_wait();
+                        if (m == -INFINITY ? mx > -INFINITY : (mx - m) * f > kSlack) m_next = mx;
+                        if (__any_sync(0xFFFFFFFFu, m_next != m) && !raise(i > u.lo)) {
+                            ok = false;
+                            break;
+                        }
+                        pending = false;
+                        usual = a.softcap == 0.f && !a.odd_scale && !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
+                        n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
+                        if (far) {  // the product of the maximum is not to be rounded by itself
+                            const float m0 = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+                            for (int c = 0; c < BN / 32; ++c) {
+                                tmem_ld32(s_col + 32 * c, v);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint((__uint_as_float(v[k]) - m0) * f);
+                                tmem_st16(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[16]>(v));
+                                tmem_st16(s_col + 32 * c + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+                            }
+                            tmem_st_wait();
+                            f2 = make_float2(1.f, 1.f), n2 = make_float2(C::LIFT, C::LIFT);
+                        }
+                        tmem_ld32(s_col, s[0]);
+                    }
                     // ---- weights by the maximum so far, in one pass; a larger one counts from the next tile on
                     uint32_t p[BN / 2];
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     float top[2] = {-INFINITY, -INFINITY};
-                    const float2 f2 = make_float2(f, f), n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < BN / 32; ++c) {
@@ -553,113 +619,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                         }
                         if (c + 1 < BN / 32) tmem_ld_wait();
                     }
-                    const float mx = fmaxf(top[0], top[1]), above = (mx - m) * f;
+                    const float mx = fmaxf(top[0], top[1]), above = far ? 0.f : (mx - m) * f;
                     pending = __any_sync(0xFFFFFFFFu, above > kSlack);
-                    done = !pending || !__any_sync(0xFFFFFFFFu, above > C::JUMP);
-                    if (done) {
-                        if (above > kSlack) m_next = mx;
-                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-#pragma unroll
-                        for (int c = 0; c < BN / 32; ++c) tmem_st16(s_col + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(p + 16 * c));
+                    if (pending && __any_sync(0xFFFFFFFFu, above > C::JUMP)) {  // the maximum first, then once more
+                        pending = false;
+                        fresh = fresh && !prepare;
+                        prepare = true;
+                        tmem_ld32(s_col, s[0]);
+                        continue;
                     }
+                    if (above > kSlack) m_next = mx;
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+#pragma unroll
+                    for (int c = 0; c < BN / 32; ++c) tmem_st16(s_col + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(p + 16 * c));
+                    break;
                 }
-                if (!done) {
-                    // ---- a unit's first tile, its edges, a score far above the maximum, soft caps, scales that are not positive,
-                    // pages out of range, maxima far from 0: 32 slots at a time; slots that no row of the warp sees are passed over
-                    tmem_ld_wait();
-                    const int from = (int)max((int64_t)0, (int64_t)r.bgn - j0), to = (int)min((int64_t)BN, (int64_t)r.e - j0);
-                    const float in = a.cap_in * cc, out = a.softcap * kLog2e;
-                    auto seen = [&](int c) {  // a bit for each slot
-                        uint32_t there = 0xFFFFFFFFu;
-                        if (pages) there = page_mask[(tile_count & (kMetaRing - 1)) * 4 + c];
-                        const int lo = from - 32 * c, hi = to - 32 * c;
-                        there &= lo <= 0 ? 0xFFFFFFFFu : lo >= 32 ? 0u : 0xFFFFFFFFu << lo;
-                        return there & (hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u);
-                    };
-                    auto scores = [&](int c, uint32_t there, float (&s)[32]) {
-                        tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s));
-                        tmem_ld_wait();
-                        if (a.odd_scale) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) s[k] *= a.score_sign;
-                        }
-                        if (a.softcap > 0.f) {
-                            // c tanh(s / c) = c (1 - 2 / (1 + e^(2 s / c))), in units of log2
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) s[k] = fmaf(-2.f * out, rcp_approx(1.f + ex2_approx(s[k] * in)), out);
-                        }
-                        if (__any_sync(0xFFFFFFFFu, there != 0xFFFFFFFFu)) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) s[k] = there >> k & 1u ? s[k] : -INFINITY;
-                        }
-                    };
-                    float most = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < BN / 32; ++c) {  // (a group's weights lie over scores that have been read)
-                        const uint32_t there = seen(c);
-                        uint32_t p[16];
-                        if (!__any_sync(0xFFFFFFFFu, there != 0)) {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) p[k] = 0;
-                            tmem_st16(s_col + 16 * c, p);
-                            continue;
-                        }
-                        float s[32];
-                        scores(c, there, s);
-                        float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) top[k / 2 & 1] = fmaxf(fmaxf(top[k / 2 & 1], s[k]), s[k + 1]);
-                        const float mx = fmaxf(top[0], top[1]);
-                        most = fmaxf(most, mx);
-                        // a maximum that cannot wait for the next tile: the weights of this one's groups before follow, too
-                        const bool now = m == -INFINITY ? mx > -INFINITY : (mx - m) * f > C::JUMP;
-                        if (__any_sync(0xFFFFFFFFu, now)) {
-                            if (now) m_next = mx;
-                            if (!(ok = raise(i > u.lo))) break;
-#pragma unroll 1
-                            for (int b = 0; b < c; ++b) {
-                                tmem_ld16(s_col + 16 * b, p);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) {
-                                    if constexpr (C::E4M3) {
-                                        const float2 w = __half22float2(*reinterpret_cast<const __half2 *>(&p[k]));
-                                        p[k] = pack_f16(w.x * raised, w.y * raised);
-                                    } else {
-                                        p[k] = pack_bf16(lo_f32(p[k]) * raised, hi_f32(p[k]) * raised);
-                                    }
-                                }
-                                tmem_st16(s_col + 16 * b, p);
-                            }
-                        }
-                        if (far) {
-                            const float m0 = m == -INFINITY ? 0.f : m;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) s[k] = fmaf(s[k] - m0, f, C::LIFT);
-                        } else {
-                            const float2 f2 = make_float2(f, f), n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
-#pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                const float2 z = fma2(make_float2(s[k], s[k + 1]), f2, n2);
-                                s[k] = z.x, s[k + 1] = z.y;
-                            }
-                        }
-                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float2 e = make_float2(ex2_approx(s[2 * k]), ex2_approx(s[2 * k + 1]));
-                            sum[k & 1] = add2(sum[k & 1], e);
-                            p[k] = C::E4M3 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
-                        }
-                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                        tmem_st16(s_col + 16 * c, p);
-                    }
-                    if (!ok) break;
-                    const bool up = (most - m) * f > kSlack;
-                    if (up) m_next = most;
-                    pending = __any_sync(0xFFFFFFFFu, up);
-                    usual = a.softcap == 0.f && !a.odd_scale && !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
-                }
+                if (!ok) break;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
