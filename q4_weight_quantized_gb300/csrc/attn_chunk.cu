@@ -33,7 +33,6 @@ namespace {
 
 constexpr int kThreads = 512;          // warps 0-3 and 4-7: softmax of a tile of rows each; 8 (9): MMA; 10, 11: queries; 12-15: copies
 constexpr int kMmaWarp = 8, kQueryWarp = 10, kCopyWarp = 12, kCopyWarps = 4;
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // together those of the launch: 2 * (184 + 72) = 4 * 128
 constexpr int kPlanThreads = 1024, kPlanBatch = 2048;  // sequences whose sums lie in shared memory, at most
 constexpr int kJoinWarps = 8;
 constexpr int kMetaRing = 8;           // tiles whose page masks are kept: more than the ring holds
@@ -51,18 +50,20 @@ struct Cfg {
     static constexpr int ROWS = NT * 128;
     static constexpr int SLOT = BN * D * 2;            // bytes of a tile of keys or values in shared memory
     static constexpr int NS = D == 64 ? 8 : E4M3 ? 4 : 5;  // such tiles in the ring, keys and values in turn
-    static constexpr int LAG = NS - 2;                 // of which so many may be on their way
     // weights in f16 are kept as 2^7 p, in o' and l alike: at most 2^15, and what lies below 2^-32 of the largest is lost
     static constexpr float LIFT = E4M3 ? 7.f : 0.f;
     // how far (log2) a score may exceed the maximum that its tile's weights are taken by: what f16 holds, and what leaves O room
     // for values up to 2^111
     static constexpr float JUMP = E4M3 ? kSlack : 16.f;
     static constexpr int QBYTES = ROWS * D * 2;
-    static constexpr int MISC = 768 + (E4M3 ? 2 * ROWS : 0);  // barriers and flags; for an e4m3 cache the factors of two units' rows
+    static constexpr int PLAN = 576, MISC = 768 + PLAN + (E4M3 ? 2 * ROWS : 0);  // barriers and flags, a small call's list, an e4m3
+                                                                                 // cache's factors of two units' rows
     static constexpr int RAW = E4M3 ? BN * D : 0;      // bytes of a tile as it lies in an e4m3 cache: one of keys, one of values
     static constexpr int SMEM = QBYTES + NS * SLOT + 2 * RAW + MISC + 1024;  // (+ slack to align the base)
     static constexpr uint32_t S_COL = 0, O_COL = NT == 2 ? 2 * BN : 2 * BN;
     static constexpr uint32_t COLS = 512;
+    // registers of a softmax thread and of the others, together those of the launch: 4 * 128 (an e4m3 cache's copies need more)
+    static constexpr int REGS = E4M3 ? 168 : 176, OTHER_REGS = 256 - REGS;
     static_assert(O_COL + NT * D <= COLS && SMEM <= 227 * 1024, "fits");
 };
 
@@ -73,10 +74,23 @@ struct Unit : ChunkRecord {
     bool whole;
 };
 
+// The list of a small call (few sequences and row tiles), which every CTA makes for itself.
+constexpr int kSmall = 32;
+struct SmallPlan {
+    int64_t places;                       // as ChunkArgs::head
+    int units, shares;
+    int place_at[kSmall + 1];
+    int seq_at[kSmall], len[kSmall], rt_at[kSmall];
+};
+
 struct Walk {
     int64_t at, hi, places;
-    int h, rt, units;
+    int h, rt, units, shares;
+    const SmallPlan *small;  // or null: the list is in the workspace
 };
+
+// row / group for 0 <= row < 2^31
+__device__ __forceinline__ int token_of(const ChunkArgs &a, int row) { return (int)(((uint64_t)(uint32_t)row * a.group_mul) >> a.group_shift); }
 
 __device__ __forceinline__ int64_t share_at(int64_t total, int shares, int s) { return total / shares * s + total % shares * s / shares; }
 
@@ -94,16 +108,22 @@ __device__ __forceinline__ int find_rt(const ChunkArgs &a, int n, int64_t place)
     return lo;
 }
 
-__device__ __forceinline__ Walk walk_of(const ChunkArgs &a, int share) {
+__device__ __forceinline__ Walk walk_of(const ChunkArgs &a, const SmallPlan *small, int share) {
     Walk w;
-    w.places = __ldg(a.head);
-    const int shares = (int)__ldg(a.head + 2);
+    w.small = small;
+    w.places = small ? small->places : __ldg(a.head);
+    const int shares = w.shares = small ? small->shares : (int)__ldg(a.head + 2);
     const int64_t total = w.places * a.c.heads;
-    w.units = (int)__ldg(a.head + 1);
+    w.units = small ? small->units : (int)__ldg(a.head + 1);
     w.at = share < shares ? share_at(total, shares, share) : 0;
     w.hi = share < shares ? share_at(total, shares, share + 1) : 0;
     w.h = w.places > 0 ? (int)(w.at / w.places) : 0;
-    w.rt = w.at < w.hi ? find_rt(a, w.units, w.at - w.h * w.places) : 0;
+    w.rt = 0;
+    if (w.at >= w.hi) return w;
+    const int64_t place = w.at - w.h * w.places;
+    if (!small) w.rt = find_rt(a, w.units, place);
+    else
+        while (w.rt + 1 < w.units && small->place_at[w.rt + 1] <= place) ++w.rt;
     return w;
 }
 
@@ -115,11 +135,34 @@ __device__ __forceinline__ void load_record(const ChunkArgs &a, int rt, ChunkRec
     r.tiles = z.x, r.all_end = z.y, r.all_begin = z.z, r.pad = 0;
 }
 
+// A row tile of sequence b, whose n new tokens' rows begin at q0.
+template <typename C>
+__device__ __forceinline__ void make_record(const ChunkArgs &a, int b, int q0, int n, int len, int tile, ChunkRecord &r) {
+    r.b = b, r.q0 = q0, r.e0 = len - n + 1;
+    r.row0 = tile * C::ROWS;
+    r.rows = min(C::ROWS, n * a.group - r.row0);
+    const int first = token_of(a, r.row0), last = token_of(a, r.row0 + r.rows - 1);  // tokens
+    auto begin = [&](int tok) { return a.window > 0 && (int64_t)r.e0 + tok > a.window ? (int)(r.e0 + tok - a.window) : 0; };
+    r.begin = begin(first), r.end = max(0, r.e0 + last);
+    r.all_begin = begin(last), r.all_end = max(0, r.e0 + first);
+    r.base = r.begin / C::BN;
+    r.tiles = max(1, (int)(((int64_t)r.end + C::BN - 1) / C::BN) - r.base);
+    r.pad = 0;
+}
+template <typename C>
+__device__ __forceinline__ void small_record(const ChunkArgs &a, const SmallPlan &p, int rt, ChunkRecord &r) {
+    int b = 0;
+    for (int i = 1; i < a.c.batch; ++i)
+        if (p.rt_at[i] <= rt) b = i;
+    make_record<C>(a, b, p.seq_at[b], p.seq_at[b + 1] - p.seq_at[b], p.len[b], rt - p.rt_at[b], r);
+}
+
 template <typename C>
 __device__ __forceinline__ bool next_unit(const ChunkArgs &a, Walk &w, Unit &u) {
     while (w.at < w.hi) {
-        const int64_t first = w.h * w.places + __ldg(a.place_at + w.rt);
-        load_record(a, w.rt, u);
+        const int64_t first = w.h * w.places + (w.small ? (int64_t)w.small->place_at[w.rt] : __ldg(a.place_at + w.rt));
+        if (w.small) small_record<C>(a, *w.small, w.rt, u);
+        else load_record(a, w.rt, u);
         u.h = w.h, u.rt = w.rt;
         const int length = u.tiles + kExtra, lo = (int)(w.at - first);
         const int hi = w.hi - first < length ? (int)(w.hi - first) : length;
@@ -133,6 +176,54 @@ __device__ __forceinline__ bool next_unit(const ChunkArgs &a, Walk &w, Unit &u) 
 }
 
 // ---------------------------------------------------------------- the list
+
+// As many shares as there are CTAs; for less work one a unit or two tiles.
+__device__ __forceinline__ int shares_of(const ChunkArgs &a, int row_tiles, int64_t places) {
+    const int64_t units = (int64_t)row_tiles * a.c.heads, most = max(units, (places * a.c.heads - kExtra * units) / 2);
+    return most < 1 ? 1 : most < a.shares ? (int)most : a.shares;
+}
+
+// The list of a small call by one warp; CTA 0's leaves the records for join_kernel.
+template <typename C>
+__device__ __forceinline__ void small_plan(const ChunkArgs &a, SmallPlan &p) {
+    const int lane = threadIdx.x & 31, B = a.c.batch;  // B < 32
+    auto sum_before = [&](int v, int &all) {
+        int s = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xFFFFFFFFu, s, o);
+            if (lane >= o) s += t;
+        }
+        all = __shfl_sync(0xFFFFFFFFu, s, 31);
+        return s - v;
+    };
+    const int raw = lane <= B ? __ldg(a.starts + lane) : 0, len = lane < B ? __ldg(a.seq_lens + lane) : 0;
+    int s = min(max(raw, 0), (int)a.T);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s = max(s, t);
+    }
+    const bool bad = (lane <= B && s != raw) || (lane < B && len > a.c.capacity);
+    const int next = __shfl_down_sync(0xFFFFFFFFu, s, 1), n = lane < B ? next - s : 0;
+    int R, all;
+    const int first = sum_before((int)(((int64_t)n * a.group + C::ROWS - 1) / C::ROWS), R);
+    if (lane <= B) p.seq_at[lane] = s;
+    if (lane < B) p.len[lane] = min(max(len, 0), a.c.capacity), p.rt_at[lane] = first;
+    __syncwarp();
+    ChunkRecord r = {};
+    if (lane < R) small_record<C>(a, p, lane, r);
+    const int at = sum_before(lane < R ? r.tiles + kExtra : 0, all);
+    if (lane < R) p.place_at[lane] = at;
+    if (lane == 0) {
+        p.place_at[R] = all;
+        p.places = all, p.units = R, p.shares = shares_of(a, R, all);
+    }
+    if (blockIdx.x == 0) {
+        if (lane < R) a.records[lane] = r;
+        if (bad) atomicOr(a.c.status, kDevIndex);
+    }
+}
 
 __device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t &total, int64_t *scratch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -228,17 +319,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ChunkArgs a) {
     }
     auto record = [&](int rt, int &of, ChunkRecord &r) {
         while (rt_at[of + 1] <= rt) ++of;
-        const int n = seq_at[of + 1] - seq_at[of], len = min(max(__ldg(a.seq_lens + of), 0), a.c.capacity);
-        r.b = of, r.q0 = seq_at[of], r.e0 = len - n + 1;
-        r.row0 = (rt - rt_at[of]) * C::ROWS;
-        r.rows = min(C::ROWS, n * a.group - r.row0);
-        const int first = r.row0 / a.group, last = (r.row0 + r.rows - 1) / a.group;  // tokens
-        auto begin = [&](int tok) { return a.window > 0 && (int64_t)r.e0 + tok > a.window ? (int)(r.e0 + tok - a.window) : 0; };
-        r.begin = begin(first), r.end = max(0, r.e0 + last);
-        r.all_begin = begin(last), r.all_end = max(0, r.e0 + first);
-        r.base = r.begin / C::BN;
-        r.tiles = max(1, (int)(((int64_t)r.end + C::BN - 1) / C::BN) - r.base);
-        r.pad = 0;
+        make_record<C>(a, of, seq_at[of], seq_at[of + 1] - seq_at[of], min(max(__ldg(a.seq_lens + of), 0), a.c.capacity), rt - rt_at[of], r);
         return r.tiles + kExtra;
     };
     int64_t sum = 0, all;
@@ -256,9 +337,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ChunkArgs a) {
         a.place_at[R] = all;
         a.head[0] = all;
         a.head[1] = R;
-        // as many shares as there are CTAs; for less work one a unit or two tiles
-        const int64_t units = (int64_t)R * a.c.heads, most = max(units, (all * a.c.heads - kExtra * units) / 2);
-        a.head[2] = most < 1 ? 1 : most < a.shares ? most : a.shares;
+        a.head[2] = shares_of(a, R, all);
     }
     if (bad) atomicOr(a.c.status, kDevIndex);
 }
@@ -353,9 +432,6 @@ struct Bars {
     uint32_t full, empty, s_full, p_full, o_full, q_full, q_free, pv_done, done, raw;
 };
 
-// row / group for 0 <= row < 2^31
-__device__ __forceinline__ int token_of(const ChunkArgs &a, int row) { return (int)(((uint64_t)(uint32_t)row * a.group_mul) >> a.group_shift); }
-
 // A row of a unit: where it is and what it sees.
 struct Row {
     int64_t q_row;        // of q and o
@@ -382,7 +458,7 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap &m, int
         : "memory");
 }
 
-template <typename C>
+template <typename C, bool SMALL>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap k_map,
                                                             const __grid_constant__ CUtensorMap v_map) {
     constexpr int D = C::D, BN = C::BN, NT = C::NT, NS = C::NS;
@@ -397,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc_p + 516);
     volatile int *const bad_pages = reinterpret_cast<volatile int *>(misc_p + 524); // a page id was out of range
     volatile int *const bad_seen = reinterpret_cast<volatile int *>(misc_p + 520);  // a value that is not finite was taken out
-    volatile uint8_t *const q_factor = misc_p + 768;  // [2][C::ROWS]: exponents (biased by 127) of the factors
+    volatile uint8_t *const q_factor = misc_p + 768 + C::PLAN;  // [2][C::ROWS]: exponents (biased by 127) of the factors
     volatile uint32_t *const page_mask = reinterpret_cast<volatile uint32_t *>(misc_p + 640);      // [kMetaRing][4]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int *const status = a.c.status;
@@ -422,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
         *bad_pages = 0;
         fence_mbar_init();
     }
+    static_assert(sizeof(SmallPlan) <= C::PLAN, "fits");
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_holder), C::COLS);
         tmem_relinquish();
@@ -432,12 +509,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
     const uint32_t tmem = *tmem_holder;
     pdl_wait();
     pdl_trigger();
-    Walk walk = walk_of(a, blockIdx.x);
+    SmallPlan *const small = SMALL ? reinterpret_cast<SmallPlan *>(misc_p + 768) : nullptr;
+    if constexpr (SMALL) {
+        __builtin_assume(small != nullptr);
+        if (warp == 0) small_plan<C>(a, *small);
+        __syncthreads();
+    }
+    Walk walk = walk_of(a, small, blockIdx.x);
     Unit u;
 
     if (warp < 8) {
         // -------------------------------------------------------- softmax, one row a thread
-        set_regs_up<kSoftmaxRegs>();
+        set_regs_up<C::REGS>();
         const int t = warp >> 2, row_in = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t o_col = tmem + lanes + C::O_COL + t * D;
@@ -720,8 +803,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
             }
             if (threadIdx.x == 0 && u.lo == 0 && !u.whole) {
                 // the share that begins a unit it does not end: join_kernel finds the parts from here
-                const int shares = (int)__ldg(a.head + 2);
-                const int64_t total = walk.places * a.c.heads, end = u.h * walk.places + __ldg(a.place_at + u.rt) + u.tiles;
+                const int shares = walk.shares;
+                const int64_t total = walk.places * a.c.heads;
+                const int64_t end = u.h * walk.places + (small ? (int64_t)small->place_at[u.rt] : __ldg(a.place_at + u.rt)) + u.tiles;
                 int parts = 2;
                 while ((int)blockIdx.x + parts < shares && share_at(total, shares, blockIdx.x + parts) < end) ++parts;
                 a.joins[blockIdx.x] = make_int4(u.rt, u.h, parts, 0);
@@ -731,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
         }
         if (!ok && lane == 0) *abort_flag = 1;
     } else if (warp < kCopyWarp) {
-        set_regs_down<kOtherRegs>();
+        set_regs_down<C::OTHER_REGS>();
         if (warp < kMmaWarp + (NT == 2 ? 1 : 2) && elect_one()) {
             // ---------------------------------------------------- MMA
             // Two tiles of rows: one thread issues a tile's P V and next Q K^T, then the other's, so that while one's run the
@@ -900,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
         }
     } else {
         // -------------------------------------------------------- copies
-        set_regs_down<kOtherRegs>();
+        set_regs_down<C::OTHER_REGS>();
         const int w = warp - kCopyWarp;
         // A cached row is copied by as many lanes as 128 bytes of it have 16-byte pieces, block of 64 values after block, so
         // that an access takes whole lines and a row's offset serves several.
@@ -1154,9 +1238,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                     if (++slot == NS) slot = 0, parity ^= 1;
                     edge_bits = edge_bits << 1 | (uint32_t)(kv == 1 && edge);
                     box_bits = box_bits << 1 | (uint32_t)(boxes && !(kv == 1 && edge));
-                    if (issued - shown > (uint32_t)C::LAG) {
-                        cp_async_wait<C::LAG>();
-                        show(issued - C::LAG);
+                    constexpr uint32_t kAhead = C::NS - 2;  // tiles on their way
+                    if (issued - shown > kAhead) {
+                        cp_async_wait<kAhead>();
+                        show(issued - kAhead);
                     }
                 }
                 if (!ok) break;
@@ -1243,18 +1328,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const ChunkArgs a
     }
 }
 
-template <typename C>
+template <typename C, bool SMALL>
 cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
     // setmaxnreg moves registers within what the launch holds: 128 a thread, or the split would wait forever
     static const bool fits = [] {
         cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, chunk_kernel<C>) == cudaSuccess && 4 * f.numRegs >= 2 * (kSoftmaxRegs + kOtherRegs);
+        return cudaFuncGetAttributes(&f, chunk_kernel<C, SMALL>) == cudaSuccess && 4 * f.numRegs >= 2 * (C::REGS + C::OTHER_REGS);
     }();
     if (!fits) return cudaErrorInvalidConfiguration;
-    cudaError_t e = ensure_smem((const void *)chunk_kernel<C>, C::SMEM);
+    cudaError_t e = ensure_smem((const void *)chunk_kernel<C, SMALL>, C::SMEM);
     if (e != cudaSuccess) return e;
     a.shares = di.sm_count < kMaxChunkShares ? di.sm_count : kMaxChunkShares;
-    if ((e = launch_pdl(plan_kernel<C>, dim3(1), dim3(kPlanThreads), 0, s, dim3(1), a)) != cudaSuccess) return e;
+    if (!SMALL && (e = launch_pdl(plan_kernel<C>, dim3(1), dim3(kPlanThreads), 0, s, dim3(1), a)) != cudaSuccess) return e;
     // boxes of what divides a page, of 8 (a swizzle atom) to 32 slots (a warp's rows; 16 of heads of 256): blocks of 64 values,
     // or whole rows of an e4m3 cache
     CUtensorMap k_map = {}, v_map = {};
@@ -1266,11 +1351,20 @@ cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
                       make_cache_tmap(&v_map, a.c.v, a.c, values, box, !C::E4M3, &head_first);
     a.box_slots = maps ? box : 0;
     a.head_first = head_first;
-    if ((e = launch_pdl(chunk_kernel<C>, dim3(a.shares), dim3(kThreads), C::SMEM, s, dim3(1), a, k_map, v_map)) != cudaSuccess) return e;
+    if ((e = launch_pdl(chunk_kernel<C, SMALL>, dim3(a.shares), dim3(kThreads), C::SMEM, s, dim3(1), a, k_map, v_map)) != cudaSuccess) return e;
     // a warp a row
     const int64_t rows = a.T * a.group;
     const int y = (int)(((rows < C::ROWS ? rows : C::ROWS) + kJoinWarps - 1) / kJoinWarps);
     return launch_pdl(join_kernel<C>, dim3(a.shares, y), dim3(kJoinWarps * 32), 0, s, dim3(1), a);
+}
+
+
+template <typename C>
+cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
+    // Few sequences and row tiles: every CTA lists them itself, a launch less (8 sequences of 1 to 3 tokens: 18.4 us, 20.3 with
+    // plan_kernel).  The branch inside one kernel costs the others 1 to 5 %: registers.
+    const bool small = a.c.batch < kSmall && a.T * a.group / C::ROWS + (a.c.batch < a.T ? a.c.batch : a.T) <= kSmall;
+    return small ? launch<C, true>(di, a, s) : launch<C, false>(di, a, s);
 }
 
 }  // namespace

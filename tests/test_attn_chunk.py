@@ -347,6 +347,42 @@ def test_chunk_bad_indices_are_reported_and_left_out():
     q4k.q4k_check_device()
 
 
+@pytest.mark.parametrize("D,G,new", [
+    (128, 8, [1] * 31), (128, 8, [1] * 32),                                # sequences
+    (128, 8, [31 * 32]), (128, 8, [31 * 32 + 1]),                          # row tiles
+    (128, 8, [1] * 16 + [15 * 32 + 15]), (128, 8, [1] * 16 + [16 * 32]),   # the bound on them from both
+    (256, 4, [1] * 31), (256, 4, [31 * 32 + 1]), (64, 1, [31 * 256]), (64, 1, [31 * 256, 0, 2]),
+])
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_chunk_either_side_of_a_small_call(dtype, D, G, new):
+    """Each CTA lists the work of a call with less than 32 sequences and at most 32 row tiles; a kernel does for more."""
+    g = gen_of(len(new) + D)
+    lens = [n + 41 * i % 199 for i, n in enumerate(new)]
+    k, v, table, ks, vs, starts, q = make(D, dtype, 16, "phsd", 1, G, new, lens, g)
+    ref = reference(k, v, table, starts, lens, q, D ** -0.5, 0.0, 0, ks, vs)
+    o = run(k, v, table, starts, lens, q, D ** -0.5, 0.0, 0, ks, vs)
+    q4k.q4k_check_device()
+    check(o, ref, D, dtype == F8)
+
+
+@pytest.mark.parametrize("B", [31, 32, 2100])
+def test_chunk_bad_starts_and_lengths_of_many_sequences(B):
+    g = gen_of(B)
+    D, page, L = 64, 8, 24
+    k, v, table, _, _, _, q = make(D, BF, page, "phsd", 1, 2, [2] * B, [L] * B, g, spare=0)
+    cap = table.shape[1] * page
+    starts, lens = [2 * b for b in range(B + 1)], [L] * B
+    starts[3], starts[7], starts[B] = 1, 2 ** 31 - 1, -5   # back; beyond T, so that all later ones go back; negative
+    lens[1], lens[2], lens[5] = cap + 1, -2 ** 31, 2 ** 31 - 1
+    o = run(k, v, table, starts, lens, q, 0.2)
+    with pytest.raises(q4k.Q4KError) as e:
+        q4k.q4k_check_device()
+    assert e.value.status == q4k.Q4K_ERR_INDEX
+    T = 2 * B
+    as_if = [0, 2, 4, 4, 8, 10, 12] + [T] * (B - 6)
+    check(o, reference(k, v, table, as_if, [min(max(n, 0), cap) for n in lens], q, 0.2), D, False)
+
+
 def test_chunk_rows_of_no_sequence_are_left_alone():
     g = gen_of(16)
     k, v, table, _, _, _, q = make(128, BF, 16, "phsd", 2, 2, [100], [100], g)
