@@ -137,10 +137,12 @@ int q4k_set_static_weights(int enable);
  *       GB300.
  * The boundary between the two paths stays: rows of calls with M <= 16 and
  * M > 16 differ in rounding (different kernels, each within its bar).
- * Of the operators between a decode step's products, q4k_norm_residual and
- * q4k_norm_residual_x8 follow the mode (about 0.15 us for a few rows), q4k_kv_append,
- * q4k_kv_evict and q4k_sample give a token or sequence the same bits in either, and q4k_attn_decode is not
- * batch-invariant in either: it splits its work by all lengths of the batch.
+ * Of the operators between the products, q4k_norm_residual and q4k_norm_residual_x8
+ * follow the mode (about 0.15 us for a few rows); q4k_kv_append, q4k_kv_evict, q4k_sample
+ * and q4k_batch_plan (whole numbers) give a token or sequence the same bits in either; a
+ * row of q4k_lora_add depends in either on T, not on the other rows; q4k_attn_decode and
+ * q4k_attn_chunk are not batch-invariant in either: they split their work by all lengths
+ * of the batch.
  * Process-wide; applies to calls enqueued after it returns.  Returns the previous
  * setting (0 or 1). */
 int q4k_set_batch_invariant(int enable);
@@ -150,9 +152,9 @@ int q4k_set_batch_invariant(int enable);
  * its work, wait for its own copies in flight, reach all of its barriers and
  * set a device status word that q4k_check_device reports as Q4K_ERR_TIMEOUT.
  * This sets the limit of the decode GEMV's main-loop waits (q4k_gemv, and
- * q4k_gemm with M = 1 outside batch-invariant mode) and of q4k_norm_residual's
- * waits for its ring of rows to `ns`, so that a test can make those paths run out
- * without faulting or hanging anything; 0 restores the standard limit.  Under
+ * q4k_gemm with M = 1 outside batch-invariant mode) and of q4k_norm_residual's and
+ * q4k_norm_residual_x8's waits for their ring of rows to `ns`, so that a test can make
+ * those paths run out without faulting or hanging anything; 0 restores the standard limit.  Under
  * 1000 ns a wait tests its copy once, without blocking, and gives up at once if it
  * has not landed.  A call whose wait ran out leaves its outputs undefined.
  * Process-wide; applies to calls enqueued after it returns.  Returns the

@@ -18,10 +18,19 @@
 //     of S instead; there the rare rescale waits for the product before.)
 //   - Work is one list of places (KV head, unit, tile of slots) cut into equal contiguous shares, one per CTA, whatever
 //     the lengths are; units that a share does not hold as a whole leave (m, l, o') in the workspace for join_kernel.
-//   - Four warps copy keys and values row by row, 16 bytes a lane, into the swizzled layout the MMAs read (any page
-//     size, any strides).  An e4m3 cache's values become f16 on the way, exactly, and Q f16 by a power of two a row.
+//   - Four warps bring keys and values into the swizzled layout the MMAs read.  Where every row sees a whole tile and pages
+//     have 8 slots or a multiple, the copy engine does (a box a page's part); else a lane copies 16 bytes at a time and
+//     fills what is not there with zeros (any page size, any strides).  An e4m3 cache's tiles are staged one ahead as
+//     they are and become f16, exactly, keys and values at once; Q becomes f16 by a power of two a row.
+//   - Scores that need more than the scale (a mask's edge, the softcap, maxima so large that the fused product's rounding
+//     counts) are prepared in their place in tensor memory first, so that the pass itself is the same for every tile.
 // A slot that some rows of a unit see and others do not may hold values that are not finite: those are taken out of the
 // product (0 * infinity would reach every row) and added to the rows that see them at the end.
+//
+// Measured, heads of 128, 40 of them on 8 KV heads: a prompt of 8192 in 515 us (1335 TFLOP/s), 512 tokens after 65536 in
+// 490 us (1410), from an e4m3 cache 640 us; with a softcap 570 TFLOP/s.  Two tiles of 128 rows and 128 slots take 1.8 us: 1.1 of
+// them (2048 cycles of MMAs) is the tensor cores'; softmax -> P V, Q K^T -> softmax of each tile is a chain that two tiles
+// cover to that extent.  A unit's end and start cost as much as 5 such places (kExtra; 3: 559 us for the prompt).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -62,7 +71,8 @@ struct Cfg {
     static constexpr int SMEM = QBYTES + NS * SLOT + 2 * RAW + MISC + 1024;  // (+ slack to align the base)
     static constexpr uint32_t S_COL = 0, O_COL = NT == 2 ? 2 * BN : 2 * BN;
     static constexpr uint32_t COLS = 512;
-    // registers of a softmax thread and of the others, together those of the launch: 4 * 128 (an e4m3 cache's copies need more)
+    // registers of a softmax thread and of the others, together those of the launch: 4 * 128.  (A prompt: 512 us,
+    // 517 by 192 and 64; an e4m3 cache, whose copies need more: 689 by 192 and 64, 651 by 176 and 80, 636 by 168 and 88.)
     static constexpr int REGS = E4M3 ? 168 : 176, OTHER_REGS = 256 - REGS;
     static_assert(O_COL + NT * D <= COLS && SMEM <= 227 * 1024, "fits");
 };
@@ -820,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
             // ---------------------------------------------------- MMA
             // Two tiles of rows: one thread issues a tile's P V and next Q K^T, then the other's, so that while one's run the
             // softmax of the other has the SM's other pipes for itself.  (Issued by two threads they interleave, both end
-            // together, and so do the two softmaxes that follow: 2.5 us for two tiles of 128 slots instead of 2.2.)  Heads of
+            // together, and so do the two softmaxes that follow: 4 % slower.)  Heads of
             // 256: a thread for each product.
             constexpr uint32_t kQk = idesc_of(128, BN, C::E4M3, false), kPv = idesc_of(128, D, C::E4M3, true);
             const bool qks = NT == 2 || warp == kMmaWarp, pvs = NT == 2 || warp != kMmaWarp;
@@ -952,29 +962,43 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                         const int64_t from = __shfl_sync(0xFFFFFFFFu, at, s + lane / LANES);
                         const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (from >= 0 ? from : 0)) + c;
                         const uint32_t to = dst + row * 128 + ((c ^ row) & 7) * 16;
-                        if constexpr (C::E4M3) {
-                            // f16: a power of two takes the row's largest value to [2^14, 2^15)
-                            uint4 w = from >= 0 ? __ldg(src) : make_uint4(0, 0, 0, 0);
-                            uint32_t top = max(max(w.x << 16 & 0x7FFFFFFFu, w.x & 0x7FFF0000u), max(w.y << 16 & 0x7FFFFFFFu, w.y & 0x7FFF0000u));
-                            top = max(top, max(max(w.z << 16 & 0x7FFFFFFFu, w.z & 0x7FFF0000u), max(w.w << 16 & 0x7FFFFFFFu, w.w & 0x7FFF0000u)));
-#pragma unroll
-                            for (int o = LANES / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                            const int ex = (int)(top >> 23);
-                            // (a row that is not finite gives NaN either way)
-                            const int shift = ex == 255 ? 0 : min(127 + 14 - ex, 126);
-                            const float f = __uint_as_float((uint32_t)(127 + shift) << 23);
-                            w.x = pack_f16(lo_f32(w.x) * f, hi_f32(w.x) * f), w.y = pack_f16(lo_f32(w.y) * f, hi_f32(w.y) * f);
-                            w.z = pack_f16(lo_f32(w.z) * f, hi_f32(w.z) * f), w.w = pack_f16(lo_f32(w.w) * f, hi_f32(w.w) * f);
-                            sts128(to, w);
-                            // the way back, for the row's softmax (which has read those of two units before)
-                            if (c == 0) q_factor[(units & 1) * C::ROWS + t * 128 + row] = (uint8_t)(127 - shift);
-                        } else {
-                            cp_async16(to, src, from >= 0 ? 16u : 0u);
-                        }
+                        cp_async16(to, src, from >= 0 ? 16u : 0u);
                     }
                 }
                 cp_async_commit();
                 cp_async_wait<0>();
+                if constexpr (C::E4M3) {
+                    // to f16 in their place, a lane a row: a power of two takes the row's largest value to [2^14, 2^15)
+                    __syncwarp();
+                    for (int r0 = row0; r0 < row0 + ROWS; r0 += 32) {
+                        const int row = r0 + lane;
+                        int shift = 126;
+                        if (t * 128 + r0 < u.rows) {  // (else all are 0)
+                            const uint32_t at = q_smem + t * (128 * D * 2) + row * 128;
+                            uint32_t top = 0;
+#pragma unroll
+                            for (int x = 0; x < D / 8; ++x) {
+                                const uint4 v = lds128(at + (x / 8) * (128 * 128) + ((x ^ row) & 7) * 16);
+                                const uint32_t p = max(max(v.x << 16 & 0x7FFFFFFFu, v.x & 0x7FFF0000u), max(v.y << 16 & 0x7FFFFFFFu, v.y & 0x7FFF0000u));
+                                top = max(max(top, p), max(max(v.z << 16 & 0x7FFFFFFFu, v.z & 0x7FFF0000u), max(v.w << 16 & 0x7FFFFFFFu, v.w & 0x7FFF0000u)));
+                            }
+                            const int ex = (int)(top >> 23);
+                            // (a row that is not finite gives NaN either way)
+                            shift = ex == 255 ? 0 : min(127 + 14 - ex, 126);
+                            const float f = __uint_as_float((uint32_t)(127 + shift) << 23);
+#pragma unroll
+                            for (int x = 0; x < D / 8; ++x) {
+                                const uint32_t to = at + (x / 8) * (128 * 128) + ((x ^ row) & 7) * 16;
+                                uint4 v = lds128(to);
+                                v.x = pack_f16(lo_f32(v.x) * f, hi_f32(v.x) * f), v.y = pack_f16(lo_f32(v.y) * f, hi_f32(v.y) * f);
+                                v.z = pack_f16(lo_f32(v.z) * f, hi_f32(v.z) * f), v.w = pack_f16(lo_f32(v.w) * f, hi_f32(v.w) * f);
+                                sts128(to, v);
+                            }
+                        }
+                        // the way back, for the row's softmax (which has read those of two units before)
+                        q_factor[(units & 1) * C::ROWS + t * 128 + row] = (uint8_t)(127 - shift);
+                    }
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar.q_full + 8 * t);
@@ -1068,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                 int64_t off;
                 int page, in, h;
                 uint32_t mask;
-                bool edge, boxes;
+                bool edge, boxes, first;  // first: of a unit's part
             };
             const uint32_t own = raw + w * (WROWS * D);
             uint32_t raw_phase = 0;
@@ -1081,6 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                 }
                 n.off = seen && there ? row_bytes_at(a.c, page, u.h, in_page) : 1;
                 n.page = page, n.in = (int)in_page, n.h = u.h;
+                n.first = i == u.lo;
                 n.mask = __ballot_sync(0xFFFFFFFFu, there);
                 const uint32_t j0 = (uint32_t)(u.base + i) * BN;
                 n.edge = j0 + BN > (uint32_t)u.all_end || j0 < (uint32_t)u.all_begin;
@@ -1129,7 +1154,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                     if constexpr (WROWS == 32) page_mask[(tile_count & (kMetaRing - 1)) * 4 + w] = now.mask;
                     else reinterpret_cast<volatile uint16_t *>(page_mask)[(tile_count & (kMetaRing - 1)) * 8 + w] = (uint16_t)now.mask;
                 }
-                // keys and values together: what a wait, a fence or a copy's start costs is paid once
+                // keys and values together: what a wait, a fence or a copy's start costs is paid once (but a unit's first scores
+                // do not wait for values)
                 const uint32_t slot1 = slot + 1 < NS ? slot + 1 : 0, parity1 = slot + 1 < NS ? parity : parity ^ 1;
                 bool here = issued < (uint32_t)NS || (mbar_wait(bar.empty + 8 * slot, parity, status) && mbar_wait(bar.empty + 8 * slot1, parity1, status));
                 if (now.boxes) {
@@ -1162,11 +1188,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                             sts128(at + place(r, c + 1), hi);
                         }
                     }
+                    if (kv == 0 && now.first) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar.full + 8 * slot);
+                    }
                 }
                 if (odd) *bad_seen = 1;
                 fence_proxy_async_smem();  // for the MMAs, and for the copy engine, which may write what has been read
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar.full + 8 * slot), mbar_arrive(bar.full + 8 * slot1);
+                if (lane == 0 && !now.first) mbar_arrive(bar.full + 8 * slot);
+                if (lane == 0) mbar_arrive(bar.full + 8 * slot1);
                 issued += 2;
                 slot += 2;
                 if (slot >= (uint32_t)NS) slot -= NS, parity ^= 1;
@@ -1361,7 +1393,7 @@ cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
 
 template <typename C>
 cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
-    // Few sequences and row tiles: every CTA lists them itself, a launch less (8 sequences of 1 to 3 tokens: 18.4 us, 20.3 with
+    // Few sequences and row tiles: every CTA lists them itself, a launch less (33 tokens of one sequence: 18.2 us, 20.3 with
     // plan_kernel).  The branch inside one kernel costs the others 1 to 5 %: registers.
     const bool small = a.c.batch < kSmall && a.T * a.group / C::ROWS + (a.c.batch < a.T ? a.c.batch : a.T) <= kSmall;
     return small ? launch<C, true>(di, a, s) : launch<C, false>(di, a, s);

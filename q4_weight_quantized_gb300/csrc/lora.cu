@@ -12,10 +12,13 @@
 //            consecutive ones: y is read and written 16 bytes at a time.  Warps share nothing; a warp keeps its columns
 //            of B in registers and walks the tile's tokens, 16 at a time, the next ones' y on its way.
 // More than 192 tokens are sorted by adapter first (the experts' counting sort), then the two kernels run.  Up to 192 find their
-// tile themselves (an adapter, or a token that is its adapter's first where there are fewer tokens), and a cluster of
-// CTAs does both products of a tile in one launch, the inner sums staying in its shared memory; meanwhile its part of B
-// comes into L2.
+// tiles themselves, and clusters of CTAs do both products in one launch, the inner sums staying in shared memory; meanwhile a
+// CTA's part of B comes into L2.  Where few adapters have tokens the clusters that the GPU holds are shared out to them: groups
+// of 16 tokens first, then columns, for which each makes the first product again.
 // Bound by HBM: of many tokens by y, read and written once, of few by the adapters' matrices and by latency.
+// Measured: 32 tokens, 24 adapters of rank 16, 5120 x 5120 9.7 us (11.1 as two launches); 64 tokens, 16 adapters of rank up
+// to 64, 5120 -> 17408 21 us (45 as two launches); 4096 tokens, 4 adapters of rank 16, 5120 -> 17408 125 us: 4.9 TB/s, of which
+// expand_kernel about 100 (5.7 TB/s).
 #include <cuda_runtime.h>
 
 #include "decode_ops.h"
@@ -33,49 +36,73 @@ struct Tile {
     int adapter, count, rank;
 };
 
-// The tile `k`, its tokens in list[]; count 0: nothing to do.  Every thread of THREADS calls it.
+// Tile `k` of the sorted tokens, these in list[]; count 0: nothing to do.  Every thread of THREADS calls it.
 template <int THREADS>
-__device__ __forceinline__ Tile tile_of(const LoraArgs &a, int k, int *list, uint32_t *masks) {
-    constexpr int ROUNDS = (kLoraSmall + THREADS - 1) / THREADS, WARPS = THREADS / 32;
+__device__ __forceinline__ Tile tile_of(const LoraArgs &a, int k, int *list) {
     Tile t = {-1, 0, 0};
-    if (a.tiles) {
-        if (k >= __ldg(a.n_tiles)) return t;
-        const int4 r = __ldg(a.tiles + k);
-        t.adapter = r.x, t.count = r.z;
-        for (int i = threadIdx.x; i < r.z; i += THREADS) list[i] = __ldg(a.perm + r.y + i);
-    } else {
-        const bool by_adapter = a.n_adapters <= a.T;
-        const int id = by_adapter ? k : __ldg(a.ids + k), warp = threadIdx.x >> 5;
-        bool mine[ROUNDS], over = false;
-#pragma unroll
-        for (int i = 0; i < ROUNDS; ++i) {
-            const int at = i * THREADS + threadIdx.x, of = at < a.T ? __ldg(a.ids + at) : -1;
-            mine[i] = of == id;
-            over |= of >= a.n_adapters;
-            const uint32_t m = __ballot_sync(0xFFFFFFFFu, mine[i]);
-            if ((threadIdx.x & 31) == 0) masks[i * WARPS + warp] = m;
-        }
-        if (over && k == 0) atomicOr(a.status, kDevIndex);
-        __syncthreads();
-        int first = -1, before[ROUNDS] = {};
-#pragma unroll
-        for (int w = 0; w < ROUNDS * WARPS; ++w) {
-            if (first < 0 && masks[w]) first = 32 * w + __ffs(masks[w]) - 1;
-#pragma unroll
-            for (int i = 0; i < ROUNDS; ++i)
-                if (w < i * WARPS + warp) before[i] += __popc(masks[w]);
-            t.count += __popc(masks[w]);
-        }
-        if (id < 0 || id >= a.n_adapters || (!by_adapter && first != k)) t.count = 0;
-        if (t.count == 0) return t;
-        t.adapter = id;
-#pragma unroll
-        for (int i = 0; i < ROUNDS; ++i)
-            if (mine[i])
-                list[before[i] + __popc(masks[i * WARPS + warp] & ((1u << (threadIdx.x & 31)) - 1u))] = i * THREADS + threadIdx.x;
-    }
+    if (k >= __ldg(a.n_tiles)) return t;
+    const int4 r = __ldg(a.tiles + k);
+    t.adapter = r.x, t.count = r.z;
+    for (int i = threadIdx.x; i < r.z; i += THREADS) list[i] = __ldg(a.perm + r.y + i);
     __syncthreads();
     t.rank = a.ranks ? min(max(__ldg(a.ranks + t.adapter), 0), a.R) : a.R;
+    return t;
+}
+
+// What cluster blockIdx.y of a small call does: an adapter's tokens (those with adapters at all, by their first token, have the
+// clusters dealt out to them evenly), of these every `stride`-th 16 from first_token on, and part `part` of `parts` of the columns.
+// first_at, one for each adapter, is kLoraSmall.
+struct Small : Tile {
+    int first_token, stride, part, parts;
+};
+template <int THREADS>
+__device__ __forceinline__ Small small_tile(const LoraArgs &a, int *list, uint32_t (*masks)[THREADS / 32], int *first_at) {
+    static_assert(kLoraSmall <= THREADS, "a token a thread");
+    constexpr int WARPS = THREADS / 32;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const uint32_t below = (1u << (tid & 31)) - 1u;
+    Small t = {};
+    const int id = tid < a.T ? __ldg(a.ids + tid) : -1;
+    const bool in = id >= 0 && id < a.n_adapters;
+    if (id >= a.n_adapters && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, kDevIndex);
+    if (in) atomicMin(first_at + id, tid);
+    __syncthreads();
+    const uint32_t first = __ballot_sync(0xFFFFFFFFu, in && first_at[id] == tid);
+    if ((tid & 31) == 0) masks[0][warp] = first;
+    __syncthreads();
+    int active = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) active += __popc(masks[0][w]);
+    if (active == 0) return t;
+    const int each = max(1, (int)gridDim.y / active), k = blockIdx.y / each;
+    if (k >= active) return t;
+    int left = k, at = 0;  // the k-th first token
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        const uint32_t m = masks[0][w], it = __ballot_sync(0xFFFFFFFFu, (m >> (tid & 31) & 1u) && __popc(m & below) == left);
+        if (it) at = 32 * w + __ffs(it) - 1;
+        left -= __popc(m);
+    }
+    t.adapter = __ldg(a.ids + at);
+    const uint32_t mine = __ballot_sync(0xFFFFFFFFu, id == t.adapter);
+    if ((tid & 31) == 0) masks[1][warp] = mine;
+    __syncthreads();
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += __popc(masks[1][w]);
+        t.count += __popc(masks[1][w]);
+    }
+    if (id == t.adapter) list[before + __popc(mine & below)] = tid;
+    __syncthreads();
+    t.rank = a.ranks ? min(max(__ldg(a.ranks + t.adapter), 0), a.R) : a.R;
+    // tokens first; columns as long as what each cluster does of them is not small beside the first product, which every one makes
+    const int share = blockIdx.y - k * each, groups = (t.count + 15) / 16;
+    t.stride = min(each, groups);
+    // (N, K <= 2^21)
+    t.parts = max(1, min(each / t.stride, (int)(8 * (uint32_t)a.N / (uint32_t)a.K)));
+    t.part = share / t.stride, t.first_token = share - t.part * t.stride;
+    if (t.part >= t.parts) t.count = 0;
     return t;
 }
 
@@ -140,12 +167,11 @@ __global__ void __launch_bounds__(W * 32) shrink_kernel(const LoraArgs a) {
     pdl_wait();
     pdl_trigger();
     __shared__ int list[kTileTokens];
-    __shared__ uint32_t masks[8];
     __shared__ float red[W][16][NT * 8 + 1];
     const int64_t cta = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
     for (int64_t t = cta * (W * 32) + threadIdx.x; t < a.T; t += (int64_t)gridDim.x * gridDim.y * gridDim.z * (W * 32))
         if (__ldg(a.ids + t) >= a.n_adapters) atomicOr(a.status, kDevIndex);
-    const Tile tile = tile_of<W * 32>(a, blockIdx.y, list, masks);
+    const Tile tile = tile_of<W * 32>(a, blockIdx.y, list);
     const float scale = a.scales && tile.count > 0 ? __ldg(a.scales + tile.adapter) : 1.f;
     // (the CTAs of a cluster have the same tile and tokens)
     for (int m0 = 16 * blockIdx.z; m0 < tile.count; m0 += 16 * gridDim.z) {
@@ -273,9 +299,8 @@ __device__ __forceinline__ float4 plus(float4 y, const float (&acc)[2][4], int h
 template <int KS, int CG, bool VEC>
 __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
     __shared__ int list[kTileTokens];
-    __shared__ uint32_t masks[8];
     // before the previous kernel has ended: what it does not write (it has itself waited for the writer of y and of the list)
-    const Tile tile = tile_of<kThreads>(a, blockIdx.y, list, masks);
+    const Tile tile = tile_of<kThreads>(a, blockIdx.y, list);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
     const int64_t n0 = ((int64_t)blockIdx.x * kWarps + warp) * (16 * CG);
     if (tile.count == 0) {
@@ -299,22 +324,15 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
             for (int c = 0; c < CG; ++c) r.y[c][h] = load_y<VEC>(a, r.at[h], n0 + 16 * c + 4 * tq);
         }
     };
-    auto finish = [&](int m0, const Rows &r) {
-        float acc[CG][2][4] = {};
-        const float *v[2];
+    // one step of 16 tokens' inner values, from value 16 s + 4 tq on
+    auto load_v = [&](int m0, int s, float4 (&t)[1][2]) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) v[h] = m0 + g + 8 * h < tile.count ? a.v + (int64_t)list[m0 + g + 8 * h] * a.R + 4 * tq : nullptr;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            float4 t[1][2];
-            uint32_t frag[1][3][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                t[0][h] = v[h] && 16 * s + 4 * tq < a.R ? __ldcg(reinterpret_cast<const float4 *>(v[h] + 16 * s)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            split_rows<1>(t, frag);
-#pragma unroll
-            for (int c = 0; c < CG; ++c) multiply<KS>(acc[c], frag[0], b[c], s);
+        for (int h = 0; h < 2; ++h) {
+            const float *v = m0 + g + 8 * h < tile.count ? a.v + (int64_t)list[m0 + g + 8 * h] * a.R + 4 * tq : nullptr;
+            t[0][h] = v && 16 * s + 4 * tq < a.R ? __ldcg(reinterpret_cast<const float4 *>(v + 16 * s)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+    };
+    auto store = [&](const Rows &r, const float (&acc)[CG][2][4]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -327,12 +345,74 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
     pdl_trigger();
 #pragma unroll
     for (int c = 0; c < CG; ++c) columns.cut(b[c]);
-    for (int m0 = 0; m0 < tile.count; m0 += 32) {
-        if (m0 + 16 < tile.count) load(m0 + 16, odd);
-        finish(m0, even);
-        if (m0 + 16 >= tile.count) break;
-        if (m0 + 32 < tile.count) load(m0 + 32, even);
-        finish(m0 + 16, odd);
+    if constexpr (KS == 1) {
+        auto finish = [&](int m0, const Rows &r) {
+            float acc[CG][2][4] = {};
+            float4 t[1][2];
+            uint32_t frag[1][3][4];
+            load_v(m0, 0, t);
+            split_rows<1>(t, frag);
+#pragma unroll
+            for (int c = 0; c < CG; ++c) multiply<KS>(acc[c], frag[0], b[c], 0);
+            store(r, acc);
+        };
+        for (int m0 = 0; m0 < tile.count; m0 += 32) {
+            if (m0 + 16 < tile.count) load(m0 + 16, odd);
+            finish(m0, even);
+            if (m0 + 16 >= tile.count) break;
+            if (m0 + 32 < tile.count) load(m0 + 32, even);
+            finish(m0 + 16, odd);
+        }
+    } else {
+        // higher ranks: the warps split the 16 tokens' inner values once for all of them, a step or more each, one group ahead
+        __shared__ __align__(16) uint4 pieces[2][KS][3][32];
+        constexpr int OWN = (KS + kWarps - 1) / kWarps;
+        float4 t[OWN][1][2];
+        auto fetch = [&](int m0) {
+#pragma unroll
+            for (int o = 0; o < OWN; ++o)
+                if (kWarps * o + warp < KS) load_v(m0, kWarps * o + warp, t[o]);
+        };
+        auto split = [&](int buf) {
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) {
+                uint32_t frag[1][3][4];
+                split_rows<1>(t[o], frag);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    if (kWarps * o + warp < KS)
+                        pieces[buf][kWarps * o + warp][k][lane] = make_uint4(frag[0][k][0], frag[0][k][1], frag[0][k][2], frag[0][k][3]);
+            }
+        };
+        auto finish = [&](int buf, const Rows &r) {
+            float acc[CG][2][4] = {};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                uint32_t frag[3][4];
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const uint4 f = pieces[buf][s][k][lane];
+                    frag[k][0] = f.x, frag[k][1] = f.y, frag[k][2] = f.z, frag[k][3] = f.w;
+                }
+#pragma unroll
+                for (int c = 0; c < CG; ++c) multiply<KS>(acc[c], frag, b[c], s);
+            }
+            store(r, acc);
+        };
+        fetch(0);
+        split(0);
+        __syncthreads();
+        for (int m0 = 0; m0 < tile.count; m0 += 32) {
+            if (m0 + 16 < tile.count) load(m0 + 16, odd), fetch(m0 + 16);
+            finish(0, even);
+            if (m0 + 16 >= tile.count) break;
+            split(1);
+            __syncthreads();
+            if (m0 + 32 < tile.count) load(m0 + 32, even), fetch(m0 + 32);
+            finish(1, odd);
+            if (m0 + 32 < tile.count) split(0);
+            __syncthreads();
+        }
     }
 }
 
@@ -340,19 +420,23 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
 template <int NT, int U, int W, int G, bool VEC>
 __global__ void __launch_bounds__(W * 32, NT <= 4 ? 2 : 1) tile_kernel(const LoraArgs a) {
     constexpr int KS = NT == 1 ? 1 : NT / 2;
+    __shared__ int list[kTileTokens];
+    __shared__ uint32_t masks[2][W];
+    extern __shared__ float red_smem[];
+    int *const first_at = reinterpret_cast<int *>(red_smem);
+    for (int i = threadIdx.x; i < a.n_adapters; i += W * 32) first_at[i] = kLoraSmall;
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
-    __shared__ int list[kTileTokens];
-    __shared__ uint32_t masks[16];
-    extern __shared__ float red_smem[];
     float (*const red)[16][NT * 8 + 1] = reinterpret_cast<float (*)[16][NT * 8 + 1]>(red_smem);  // [W]
     __shared__ __align__(16) float v[16][KS * 16 + 4];
-    const Tile tile = tile_of<W * 32>(a, blockIdx.y, list, masks);
+    const Small tile = small_tile<W * 32>(a, list, masks, first_at);
     if (tile.count == 0) return;  // (so does the whole cluster)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
     const float scale = a.scales ? __ldg(a.scales + tile.adapter) : 1.f;
     // this CTA's columns, whole groups
-    const int64_t per = ((a.N + gridDim.x - 1) / gridDim.x + 15) / 16 * 16, first = min(per * blockIdx.x, a.N), last = min(first + per, a.N);
+    const int ctas = kMaxCluster * tile.parts, per = ((uint32_t)(a.N + ctas - 1) / (uint32_t)ctas + 15) / 16 * 16;
+    const int64_t first = min((int64_t)per * (tile.part * kMaxCluster + blockIdx.x), a.N), last = min(first + per, a.N);
     if (threadIdx.x == 0 && last > first && 4 * tile.rank >= 3 * a.R) {  // (of lower ranks too much would not be read)
         const uint16_t *from = a.b + ((int64_t)tile.adapter * a.N + first) * a.R;
         const int64_t bytes = (last - first) * a.R * 2;
@@ -364,7 +448,7 @@ __global__ void __launch_bounds__(W * 32, NT <= 4 ? 2 : 1) tile_kernel(const Lor
         uint32_t b[G][2][KS][2];
         float4 y[G][2];
     };
-    for (int m0 = 0; m0 < tile.count; m0 += 16) {
+    for (int m0 = 16 * tile.first_token; m0 < tile.count; m0 += 16 * tile.stride) {
         float *rows[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) rows[h] = m0 + g + 8 * h < tile.count ? a.y + list[m0 + g + 8 * h] * a.ldy : nullptr;
@@ -456,10 +540,22 @@ cudaError_t launch_tile(LoraArgs &a, bool vec, unsigned tiles, cudaStream_t s) {
     const unsigned ctas = kMaxCluster;
     a.k_chunk = (int32_t)(((a.K + ctas - 1) / ctas + 31) / 32 * 32);
     auto kern = vec ? tile_kernel<NT, U, W, G, true> : tile_kernel<NT, U, W, G, false>;
-    constexpr int smem = W * 16 * (NT * 8 + 1) * 4;
+    constexpr int smem = W * 16 * (NT * 8 + 1) * 4;  // (the adapters' first tokens lie there first: 4 bytes for each of 1024)
+    static_assert(smem >= 4 * 1024, "fits");
     const cudaError_t e = smem > 32 * 1024 ? ensure_smem((const void *)kern, smem) : cudaSuccess;
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(ctas, tiles), dim3(W * 32), smem, s, dim3(ctas), a);
+    // clusters: one an adapter (a token, if there are fewer), and as many as the GPU holds, where few adapters can share them
+    static const unsigned resident = [] {
+        cudaLaunchAttribute of[1] = {};
+        of[0].id = cudaLaunchAttributeClusterDimension;
+        of[0].val.clusterDim = {kMaxCluster, 1, 1};
+        cudaLaunchConfig_t c = {};
+        c.gridDim = dim3(kMaxCluster), c.blockDim = dim3(W * 32), c.dynamicSmemBytes = smem, c.attrs = of, c.numAttrs = 1;
+        int n = 0;
+        return cudaOccupancyMaxActiveClusters(&n, tile_kernel<NT, U, W, G, false>, &c) == cudaSuccess && n > 0 ? (unsigned)n : 1u;
+    }();
+    const unsigned clusters = tiles > resident ? tiles : resident;
+    return launch_pdl(kern, dim3(ctas, clusters), dim3(W * 32), smem, s, dim3(ctas), a);
 }
 
 }  // namespace
@@ -480,7 +576,7 @@ cudaError_t launch_lora_add(const DeviceInfo &di, LoraArgs &a, cudaStream_t s) {
                   : launch_shrink<16, 1, 4>(a, tiles, s);
     if (e != cudaSuccess) return e;
     return a.R <= 16 ? launch_expand<1, 2>(a, vec, tiles, s) : a.R <= 32 ? launch_expand<2, 4>(a, vec, tiles, s)
-         : a.R <= 64 ? launch_expand<4, 2>(a, vec, tiles, s) : launch_expand<8, 1>(a, vec, tiles, s);
+         : a.R <= 64 ? launch_expand<4, 2>(a, vec, tiles, s) : launch_expand<8, 2>(a, vec, tiles, s);
 }
 
 }  // namespace q4k
