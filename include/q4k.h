@@ -140,7 +140,7 @@ int q4k_set_static_weights(int enable);
  * Of the operators between the products, q4k_norm_residual and q4k_norm_residual_x8
  * follow the mode (about 0.15 us for a few rows); q4k_kv_append, q4k_kv_evict, q4k_sample
  * and q4k_batch_plan (whole numbers) give a token or sequence the same bits in either; a
- * row of q4k_lora_add depends in either on T, not on the other rows; q4k_attn_decode and
+ * row of q4k_lora_add depends in either on T, not on the other rows' content; q4k_attn_decode and
  * q4k_attn_chunk are not batch-invariant in either: they split their work by all lengths
  * of the batch.
  * Process-wide; applies to calls enqueued after it returns.  Returns the previous
@@ -662,7 +662,7 @@ q4k_status q4k_norm_residual_x8(int64_t M, int64_t D, const float *y, int64_t ld
  *   T <= 2^23
  * Products are exact and sums fp32; the inner sums, times the scale, enter the second
  * product as the sum of three bf16 values, exactly.  A row's last bits do not depend on the
- * other rows' adapters, but on K, R and T.
+ * other rows' adapters, but on K, R, T and n_adapters.
  * Workspace: q4k_lora_add_workspace_size(...) bytes, 256-byte aligned; 0 is returned for
  * arguments that the call would refuse. */
 size_t q4k_lora_add_workspace_size(int32_t n_adapters, int64_t N, int64_t K, int32_t R, int64_t T);

@@ -16,9 +16,10 @@
 // CTA's part of B comes into L2.  Where few adapters have tokens the clusters that the GPU holds are shared out to them: groups
 // of 16 tokens first, then columns, for which each makes the first product again.
 // Bound by HBM: of many tokens by y, read and written once, of few by the adapters' matrices and by latency.
-// Measured: 32 tokens, 24 adapters of rank 16, 5120 x 5120 9.7 us (11.1 as two launches); 64 tokens, 16 adapters of rank up
-// to 64, 5120 -> 17408 21 us (45 as two launches); 4096 tokens, 4 adapters of rank 16, 5120 -> 17408 125 us: 4.9 TB/s, of which
-// expand_kernel about 100 (5.7 TB/s).
+// Measured: 32 tokens, 24 adapters of rank 16, 5120 x 5120 10 us (11.1 as two launches); 64 tokens, 16 adapters of rank up
+// to 64, 5120 -> 17408 22 us (45 as two launches); 83 tokens of one adapter of rank 16, 768 -> 6526 14 us (54 by one cluster);
+// 4096 tokens, 4 adapters of rank 16, 5120 -> 17408 124 us: 4.9 TB/s, of which expand_kernel about 100 (5.7 TB/s); 6944 tokens of
+// rank 128, 408 -> 5120 118 us, the issue of three products for one (302 with each warp splitting the inner sums for itself).
 #include <cuda_runtime.h>
 
 #include "decode_ops.h"
@@ -303,7 +304,9 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
     const Tile tile = tile_of<kThreads>(a, blockIdx.y, list);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
     const int64_t n0 = ((int64_t)blockIdx.x * kWarps + warp) * (16 * CG);
-    if (tile.count == 0) {
+    // this CTA's tokens of the tile
+    const int some = kTileTokens / gridDim.z, begin = some * blockIdx.z, end = min(begin + some, tile.count);
+    if (begin >= end) {
         pdl_wait();
         return;
     }
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
     auto load = [&](int m0, Rows &r) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            r.at[h] = m0 + g + 8 * h < tile.count ? a.y + list[m0 + g + 8 * h] * a.ldy : nullptr;
+            r.at[h] = m0 + g + 8 * h < end ? a.y + list[m0 + g + 8 * h] * a.ldy : nullptr;
 #pragma unroll
             for (int c = 0; c < CG; ++c) r.y[c][h] = load_y<VEC>(a, r.at[h], n0 + 16 * c + 4 * tq);
         }
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
     auto load_v = [&](int m0, int s, float4 (&t)[1][2]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float *v = m0 + g + 8 * h < tile.count ? a.v + (int64_t)list[m0 + g + 8 * h] * a.R + 4 * tq : nullptr;
+            const float *v = m0 + g + 8 * h < end ? a.v + (int64_t)list[m0 + g + 8 * h] * a.R + 4 * tq : nullptr;
             t[0][h] = v && 16 * s + 4 * tq < a.R ? __ldcg(reinterpret_cast<const float4 *>(v + 16 * s)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     };
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
     };
     // two sets in turn (copied from one to the other they would be waited for)
     Rows even, odd;
-    load(0, even);
+    load(begin, even);
     pdl_wait();
     pdl_trigger();
 #pragma unroll
@@ -356,11 +359,11 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
             for (int c = 0; c < CG; ++c) multiply<KS>(acc[c], frag[0], b[c], 0);
             store(r, acc);
         };
-        for (int m0 = 0; m0 < tile.count; m0 += 32) {
-            if (m0 + 16 < tile.count) load(m0 + 16, odd);
+        for (int m0 = begin; m0 < end; m0 += 32) {
+            if (m0 + 16 < end) load(m0 + 16, odd);
             finish(m0, even);
-            if (m0 + 16 >= tile.count) break;
-            if (m0 + 32 < tile.count) load(m0 + 32, even);
+            if (m0 + 16 >= end) break;
+            if (m0 + 32 < end) load(m0 + 32, even);
             finish(m0 + 16, odd);
         }
     } else {
@@ -399,18 +402,18 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
             }
             store(r, acc);
         };
-        fetch(0);
+        fetch(begin);
         split(0);
         __syncthreads();
-        for (int m0 = 0; m0 < tile.count; m0 += 32) {
-            if (m0 + 16 < tile.count) load(m0 + 16, odd), fetch(m0 + 16);
+        for (int m0 = begin; m0 < end; m0 += 32) {
+            if (m0 + 16 < end) load(m0 + 16, odd), fetch(m0 + 16);
             finish(0, even);
-            if (m0 + 16 >= tile.count) break;
+            if (m0 + 16 >= end) break;
             split(1);
             __syncthreads();
-            if (m0 + 32 < tile.count) load(m0 + 32, even), fetch(m0 + 32);
+            if (m0 + 32 < end) load(m0 + 32, even), fetch(m0 + 32);
             finish(1, odd);
-            if (m0 + 32 < tile.count) split(0);
+            if (m0 + 32 < end) split(0);
             __syncthreads();
         }
     }
@@ -513,9 +516,10 @@ __global__ void __launch_bounds__(W * 32, NT <= 4 ? 2 : 1) tile_kernel(const Lor
 
 template <int KS, int CG>
 cudaError_t launch_expand(const LoraArgs &a, bool vec, unsigned tiles, cudaStream_t s) {
-    const int64_t columns = kWarps * 16 * CG;
+    // (a tile's tokens over 2, 3 or 4 CTAs where that fills four an SM)
+    const int64_t columns = kWarps * 16 * CG, x = (a.N + columns - 1) / columns, z = 4 * 152 / (x * (a.T / kTileTokens + 1));
     return launch_pdl(vec ? expand_kernel<KS, CG, true> : expand_kernel<KS, CG, false>,
-                      dim3((unsigned)((a.N + columns - 1) / columns), tiles), dim3(kThreads), 0, s, dim3(1), a);
+                      dim3((unsigned)x, tiles, z < 1 ? 1 : z < 4 ? (unsigned)z : 4), dim3(kThreads), 0, s, dim3(1), a);
 }
 
 // K over `splits` CTAs, in whole steps of a CTA's warps; returns how many have something to do
@@ -528,11 +532,15 @@ unsigned split_k(LoraArgs &a, int64_t splits, int64_t unit) {
 
 template <int NT, int U, int W>
 cudaError_t launch_shrink(LoraArgs &a, unsigned tiles, cudaStream_t s) {
-    // 16 tokens a CTA (the tokens of a tile over several), and CTAs enough for four an SM, were every tile full
-    constexpr int64_t kCtas = 4 * 152;
+    // 16 tokens a CTA (the tokens of a tile over several); K over as many CTAs as an SM holds of them, each with a full round of
+    // loads at least (1028 tokens, 17408 -> 515, rank 8: 30 us, 48 by two; 955 tokens, 2048 -> 5120, rank 64: 29 us, 37 by eight)
+    constexpr int64_t kCtas = (NT <= 2 ? 4 : 2) * 152;
     const unsigned z = kTileTokens / 16;
-    const unsigned splits = split_k(a, (kCtas + (int64_t)tiles * z - 1) / ((int64_t)tiles * z), 32 * W);
-    return launch_pdl(shrink_kernel<NT, U, W>, dim3(splits, tiles, z), dim3(W * 32), 0, s, dim3(splits), a);
+    const int64_t groups = a.T / 16 + (a.n_adapters < a.T ? a.n_adapters : a.T);  // of 16 tokens, at most
+    int64_t splits = kCtas / groups, most = a.K / (32 * W * U);
+    if (splits > most) splits = most;
+    const unsigned n = split_k(a, splits > 1 ? splits : 1, 32 * W);
+    return launch_pdl(shrink_kernel<NT, U, W>, dim3(n, tiles, z), dim3(W * 32), 0, s, dim3(n), a);
 }
 
 template <int NT, int U, int W, int G>
