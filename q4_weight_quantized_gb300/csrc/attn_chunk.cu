@@ -22,13 +22,13 @@
 //     have 8 slots or a multiple, the copy engine does (a box a page's part); else a lane copies 16 bytes at a time and
 //     fills what is not there with zeros (any page size, any strides).  An e4m3 cache's tiles are staged one ahead as
 //     they are and become f16, exactly, keys and values at once; Q becomes f16 by a power of two a row.
-//   - Scores that need more than the scale (a mask's edge, the softcap, maxima so large that the fused product's rounding
+//   - Scores that need more than the scale (a mask's edge, a small call's softcap, maxima so large that the fused product's rounding
 //     counts) are prepared in their place in tensor memory first, so that the pass itself is the same for every tile.
 // A slot that some rows of a unit see and others do not may hold values that are not finite: those are taken out of the
 // product (0 * infinity would reach every row) and added to the rows that see them at the end.
 //
 // Measured, heads of 128, 40 of them on 8 KV heads: a prompt of 8192 in 515 us (1335 TFLOP/s), 512 tokens after 65536 in
-// 490 us (1410), from an e4m3 cache 640 us; with a softcap 570 TFLOP/s.  Two tiles of 128 rows and 128 slots take 1.8 us: 1.1 of
+// 490 us (1410), from an e4m3 cache 620 us; with a softcap 750 TFLOP/s.  Two tiles of 128 rows and 128 slots take 1.8 us: 1.1 of
 // them (2048 cycles of MMAs) is the tensor cores'; softmax -> P V, Q K^T -> softmax of each tile is a chain that two tiles
 // cover to that extent.  A unit's end and start cost as much as 5 such places (kExtra; 3: 559 us for the prompt).
 #include <cuda_fp16.h>
@@ -468,7 +468,9 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap &m, int
         : "memory");
 }
 
-template <typename C, bool SMALL>
+// SMALL: the CTAs list the work themselves.  CAP: a softcap, taken in the weights' pass (without it a softcap counts as a special
+// case, a pass of its own).
+template <typename C, bool SMALL, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap k_map,
                                                             const __grid_constant__ CUtensorMap v_map) {
     constexpr int D = C::D, BN = C::BN, NT = C::NT, NS = C::NS;
@@ -674,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                             break;
                         }
                         pending = false;
-                        usual = a.softcap == 0.f && !a.odd_scale && !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
+                        usual = (CAP || a.softcap == 0.f) && !a.odd_scale && !far && !__any_sync(0xFFFFFFFFu, m == -INFINITY);
                         n2 = make_float2(neg + C::LIFT, neg + C::LIFT);
                         if (far) {  // the product of the maximum is not to be rounded by itself
                             const float m0 = m == -INFINITY ? 0.f : m;
@@ -700,7 +702,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
 #pragma unroll
                     for (int c = 0; c < BN / 32; ++c) {
                         if (c + 1 < BN / 32) tmem_ld32(s_col + 32 * (c + 1), s[(c + 1) & 1]);
-                        const uint32_t (&v)[32] = s[c & 1];
+                        uint32_t (&v)[32] = s[c & 1];
+                        if constexpr (CAP) {
+                            if (!prepare) {
+                                const float2 in2 = make_float2(a.cap_in * cc, a.cap_in * cc), one = make_float2(1.f, 1.f);
+                                const float2 out2 = make_float2(a.softcap * kLog2e, a.softcap * kLog2e), less = make_float2(-2.f * out2.x, -2.f * out2.x);
+#pragma unroll
+                                for (int k = 0; k < 32; k += 2) {
+                                    const float2 e = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), in2, make_float2(0.f, 0.f));
+                                    const float2 d = add2(make_float2(ex2_approx(e.x), ex2_approx(e.y)), one);
+                                    const float2 x = fma2(make_float2(rcp_approx(d.x), rcp_approx(d.y)), less, out2);
+                                    v[k] = __float_as_uint(x.x), v[k + 1] = __float_as_uint(x.y);
+                                }
+                            }
+                        }
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
                             const float x = __uint_as_float(v[k]), y = __uint_as_float(v[k + 1]);
@@ -1360,15 +1375,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const ChunkArgs a
     }
 }
 
-template <typename C, bool SMALL>
+template <typename C, bool SMALL, bool CAP>
 cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
     // setmaxnreg moves registers within what the launch holds: 128 a thread, or the split would wait forever
     static const bool fits = [] {
         cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, chunk_kernel<C, SMALL>) == cudaSuccess && 4 * f.numRegs >= 2 * (C::REGS + C::OTHER_REGS);
+        return cudaFuncGetAttributes(&f, chunk_kernel<C, SMALL, CAP>) == cudaSuccess && 4 * f.numRegs >= 2 * (C::REGS + C::OTHER_REGS);
     }();
     if (!fits) return cudaErrorInvalidConfiguration;
-    cudaError_t e = ensure_smem((const void *)chunk_kernel<C, SMALL>, C::SMEM);
+    cudaError_t e = ensure_smem((const void *)chunk_kernel<C, SMALL, CAP>, C::SMEM);
     if (e != cudaSuccess) return e;
     a.shares = di.sm_count < kMaxChunkShares ? di.sm_count : kMaxChunkShares;
     if (!SMALL && (e = launch_pdl(plan_kernel<C>, dim3(1), dim3(kPlanThreads), 0, s, dim3(1), a)) != cudaSuccess) return e;
@@ -1383,7 +1398,7 @@ cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
                       make_cache_tmap(&v_map, a.c.v, a.c, values, box, !C::E4M3, &head_first);
     a.box_slots = maps ? box : 0;
     a.head_first = head_first;
-    if ((e = launch_pdl(chunk_kernel<C, SMALL>, dim3(a.shares), dim3(kThreads), C::SMEM, s, dim3(1), a, k_map, v_map)) != cudaSuccess) return e;
+    if ((e = launch_pdl(chunk_kernel<C, SMALL, CAP>, dim3(a.shares), dim3(kThreads), C::SMEM, s, dim3(1), a, k_map, v_map)) != cudaSuccess) return e;
     // a warp a row
     const int64_t rows = a.T * a.group;
     const int y = (int)(((rows < C::ROWS ? rows : C::ROWS) + kJoinWarps - 1) / kJoinWarps);
@@ -1395,8 +1410,15 @@ template <typename C>
 cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
     // Few sequences and row tiles: every CTA lists them itself, a launch less (33 tokens of one sequence: 18.2 us, 20.3 with
     // plan_kernel).  The branch inside one kernel costs the others 1 to 5 %: registers.
-    const bool small = a.c.batch < kSmall && a.T * a.group / C::ROWS + (a.c.batch < a.T ? a.c.batch : a.T) <= kSmall;
-    return small ? launch<C, true>(di, a, s) : launch<C, false>(di, a, s);
+    const int64_t units = a.T * a.group / C::ROWS + (a.c.batch < a.T ? a.c.batch : a.T);
+    bool small = a.c.batch < kSmall && units <= kSmall;
+    if (a.softcap > 0.f) {
+        // A soft cap within the weights' pass: 3.4 us for two tiles of 128 rows and 128 slots, 4.4 as a special case (heads of
+        // 128).  A small call's kernel has only the latter: where its CTAs may have more than a few tiles each, not that one.
+        if (units * a.c.heads * (a.c.capacity / C::BN) > 8 * (int64_t)di.sm_count) small = false;
+        if (!small) return launch<C, false, true>(di, a, s);
+    }
+    return small ? launch<C, true, false>(di, a, s) : launch<C, false, false>(di, a, s);
 }
 
 }  // namespace

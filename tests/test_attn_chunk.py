@@ -169,6 +169,24 @@ def test_chunk_long(D, dtype, page, Hkv, G, new, lens, window, softcap):
         assert torch.equal(run(k, v, table, starts, lens, q, D ** -0.5, softcap, window, ks, vs), o)
 
 
+@pytest.mark.parametrize("D,dtype,Hkv,G,new,lens,window,softcap", [
+    (128, BF, 2, 4, [900, 1], [3000, 500], 0, 15.0), (128, F8, 1, 5, [600, 3], [1000, 4000], 0, 4.0),
+    (64, BF, 2, 2, [1400], [2500], 700, 30.0), (64, F8, 1, 8, [300], [9000], 0, 8.0),
+    (256, BF, 1, 4, [700, 40], [1500, 2500], 0, 50.0), (256, F8, 2, 2, [500], [2000], 300, 2.0),
+    (128, BF, 4, 8, [20], [9000], 0, 10.0), (128, BF, 1, 1, [40] * 35, [200] * 35, 0, 6.0),
+])
+def test_chunk_softcap_in_the_weights_pass(D, dtype, Hkv, G, new, lens, window, softcap):
+    """Calls of more than a few tiles for a CTA, and small ones, with scores on both sides of the cap."""
+    g = gen_of(D + Hkv + len(new))
+    k, v, table, ks, vs, starts, q = make(D, dtype, 16, "phsd", Hkv, G, new, lens, g)
+    scale = 2.5 * D ** -0.5
+    ref = reference(k, v, table, starts, lens, q, scale, softcap, window, ks, vs)
+    o = run(k, v, table, starts, lens, q, scale, softcap, window, ks, vs)
+    q4k.q4k_check_device()
+    check(o, ref, D, dtype == F8)
+    assert torch.equal(run(k, v, table, starts, lens, q, scale, softcap, window, ks, vs), o)
+
+
 def test_chunk_many_sequences():
     """More sequences than threads of the CTA that lists them, many without new tokens."""
     g = gen_of(21)
