@@ -187,9 +187,9 @@ __device__ __forceinline__ bool next_unit(const ChunkArgs &a, Walk &w, Unit &u) 
 
 // ---------------------------------------------------------------- the list
 
-// As many shares as there are CTAs; for less work one a unit or two tiles.
+// As many shares as there are CTAs; for less work one a unit or tile.
 __device__ __forceinline__ int shares_of(const ChunkArgs &a, int row_tiles, int64_t places) {
-    const int64_t units = (int64_t)row_tiles * a.c.heads, most = max(units, (places * a.c.heads - kExtra * units) / 2);
+    const int64_t units = (int64_t)row_tiles * a.c.heads, most = max(units, places * a.c.heads - kExtra * units);
     return most < 1 ? 1 : most < a.shares ? (int)most : a.shares;
 }
 
@@ -552,6 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
         if (threadIdx.x == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
         for (bool more = t < NT && advance(u); more; more = advance(u), ++units) {
             r.of(a, u, t * 128 + row_in);
+            // no row of this warp is there: whatever its scores and weights are (of large calls too few units to look for it: 1 to 2 %)
+            const bool none = SMALL && t * 128 + (warp & 3) * 32 >= u.rows;
             // ---- what the tile's rows see
             // every row of the tile sees slots below all_end and from all_begin on
             const int last_tok = token_of(a, min(t * 128 + 127, u.rows - 1) + u.row0);
@@ -599,6 +601,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                     break;
                 }
                 tc_fence_after();
+                if (none) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar.p_full + 8 * at);
+                    continue;
+                }
                 if constexpr (C::E4M3) {
                     if (i == u.lo) {  // (written before the tile's queries were there)
                         // (not 0, with which a masked score would give NaN)
@@ -764,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
             const float inv = e > bgn ? a.v_scale / l : 0.f;
             const int64_t part_row = (int64_t)(2 * blockIdx.x + (u.lo > 0 ? 0 : 1)) * C::ROWS + t * 128 + row_in;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = none ? D / 32 : 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld32(o_col + 32 * c, o);
                 tmem_ld_wait();
@@ -967,7 +975,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                     ok = false;
                     break;
                 }
-                for (int r0 = row0; r0 < row0 + ROWS; r0 += 32) {
+                // (of a small call 32 rows of which none is there are left as they are: their softmax warp does not look at them)
+                const int end = SMALL ? min(row0 + ROWS, u.rows - t * 128) : row0 + ROWS;
+                for (int r0 = row0; r0 < end; r0 += 32) {
                     Row r;
                     r.of(a, u, t * 128 + r0 + lane);
                     const int64_t at = r.real ? r.q_row * a.ldq + (int64_t)r.head * D : -1;
@@ -985,30 +995,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                 if constexpr (C::E4M3) {
                     // to f16 in their place, a lane a row: a power of two takes the row's largest value to [2^14, 2^15)
                     __syncwarp();
-                    for (int r0 = row0; r0 < row0 + ROWS; r0 += 32) {
+                    for (int r0 = row0; r0 < end; r0 += 32) {
                         const int row = r0 + lane;
-                        int shift = 126;
-                        if (t * 128 + r0 < u.rows) {  // (else all are 0)
-                            const uint32_t at = q_smem + t * (128 * D * 2) + row * 128;
-                            uint32_t top = 0;
-#pragma unroll
-                            for (int x = 0; x < D / 8; ++x) {
-                                const uint4 v = lds128(at + (x / 8) * (128 * 128) + ((x ^ row) & 7) * 16);
-                                const uint32_t p = max(max(v.x << 16 & 0x7FFFFFFFu, v.x & 0x7FFF0000u), max(v.y << 16 & 0x7FFFFFFFu, v.y & 0x7FFF0000u));
-                                top = max(max(top, p), max(max(v.z << 16 & 0x7FFFFFFFu, v.z & 0x7FFF0000u), max(v.w << 16 & 0x7FFFFFFFu, v.w & 0x7FFF0000u)));
-                            }
-                            const int ex = (int)(top >> 23);
-                            // (a row that is not finite gives NaN either way)
-                            shift = ex == 255 ? 0 : min(127 + 14 - ex, 126);
-                            const float f = __uint_as_float((uint32_t)(127 + shift) << 23);
-#pragma unroll
-                            for (int x = 0; x < D / 8; ++x) {
-                                const uint32_t to = at + (x / 8) * (128 * 128) + ((x ^ row) & 7) * 16;
-                                uint4 v = lds128(to);
-                                v.x = pack_f16(lo_f32(v.x) * f, hi_f32(v.x) * f), v.y = pack_f16(lo_f32(v.y) * f, hi_f32(v.y) * f);
-                                v.z = pack_f16(lo_f32(v.z) * f, hi_f32(v.z) * f), v.w = pack_f16(lo_f32(v.w) * f, hi_f32(v.w) * f);
-                                sts128(to, v);
-                            }
+                        const uint32_t at = q_smem + t * (128 * D * 2) + row * 128;
+                        uint32_t top = 0;
+#pragma unroll 4
+                        for (int x = 0; x < D / 8; ++x) {
+                            const uint4 v = lds128(at + (x / 8) * (128 * 128) + ((x ^ row) & 7) * 16);
+                            const uint32_t p = max(max(v.x << 16 & 0x7FFFFFFFu, v.x & 0x7FFF0000u), max(v.y << 16 & 0x7FFFFFFFu, v.y & 0x7FFF0000u));
+                            top = max(max(top, p), max(max(v.z << 16 & 0x7FFFFFFFu, v.z & 0x7FFF0000u), max(v.w << 16 & 0x7FFFFFFFu, v.w & 0x7FFF0000u)));
+                        }
+                        const int ex = (int)(top >> 23);
+                        // (a row that is not finite gives NaN either way)
+                        const int shift = ex == 255 ? 0 : min(127 + 14 - ex, 126);
+                        const float f = __uint_as_float((uint32_t)(127 + shift) << 23);
+#pragma unroll 4
+                        for (int x = 0; x < D / 8; ++x) {
+                            const uint32_t to = at + (x / 8) * (128 * 128) + ((x ^ row) & 7) * 16;
+                            uint4 v = lds128(to);
+                            v.x = pack_f16(lo_f32(v.x) * f, hi_f32(v.x) * f), v.y = pack_f16(lo_f32(v.y) * f, hi_f32(v.y) * f);
+                            v.z = pack_f16(lo_f32(v.z) * f, hi_f32(v.z) * f), v.w = pack_f16(lo_f32(v.w) * f, hi_f32(v.w) * f);
+                            sts128(to, v);
                         }
                         // the way back, for the row's softmax (which has read those of two units before)
                         q_factor[(units & 1) * C::ROWS + t * 128 + row] = (uint8_t)(127 - shift);
