@@ -6,7 +6,6 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
-#include <cstring>
 #include <mutex>
 
 #include "q4k.h"
@@ -220,43 +219,18 @@ cudaError_t make_act_tmap_sw128(CUtensorMap *m, const void *x, int64_t rows, int
 // One pool of a paged cache as a 4-D tensor: D values, then slots and heads (the nearer first; *head_first tells which), then
 // pages; boxes of `box_values` values of `box_slots` slots, 128-byte swizzle if asked.  False where the pool has no such form.
 bool make_cache_tmap(CUtensorMap *m, const void *pool, const KvView &c, int box_values, int box_slots, bool swizzle, bool *head_first) {
-    struct Key {
-        const void *pool;
-        int64_t page, head, slot, pages;
-        int32_t size, heads, dim, e4m3, box0, box1, swizzle, unused;
-        bool operator==(const Key &o) const { return std::memcmp(this, &o, sizeof o) == 0; }
-    };
-    constexpr int kSlots = 256;  // by address: the pools of many layers
-    thread_local Key keys[kSlots];
-    thread_local CUtensorMap maps[kSlots];
-    thread_local int state[kSlots] = {};  // 1: a map, 2: there is none
-    *head_first = c.head_bytes < c.slot_bytes;
-    const Key k = {pool, c.page_bytes, c.head_bytes, c.slot_bytes, c.n_pages, c.page_size, c.heads, c.dim, c.e4m3, box_values, box_slots,
-                   swizzle, 0};
-    const uint64_t address = reinterpret_cast<uintptr_t>(pool) >> 4;
-    const int at = (int)((address * 0x9E3779B97F4A7C15ull) >> 56);
-    if (state[at] && keys[at] == k) {
-        if (state[at] == 1) *m = maps[at];
-        return state[at] == 1;
-    }
-    bool ok = encoder() != nullptr && c.page_bytes < ((int64_t)1 << 40) && c.head_bytes < ((int64_t)1 << 40) &&
-              c.slot_bytes < ((int64_t)1 << 40);
-    if (ok) {
-        const bool hf = *head_first;
-        cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)(hf ? c.heads : c.page_size), (cuuint64_t)(hf ? c.page_size : c.heads),
-                              (cuuint64_t)c.n_pages};
-        cuuint64_t strides[3] = {(cuuint64_t)(hf ? c.head_bytes : c.slot_bytes), (cuuint64_t)(hf ? c.slot_bytes : c.head_bytes),
-                                 (cuuint64_t)c.page_bytes};
-        cuuint32_t box[4] = {(cuuint32_t)box_values, (cuuint32_t)(hf ? 1 : box_slots), (cuuint32_t)(hf ? box_slots : 1), 1};
-        cuuint32_t estr[4] = {1, 1, 1, 1};
-        ok = encoder()(m, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims,
-                       strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    }
-    keys[at] = k;
-    state[at] = ok ? 1 : 2;
-    if (ok) maps[at] = *m;
-    return ok;
+    const bool hf = c.head_bytes < c.slot_bytes;
+    *head_first = hf;
+    if (!encoder() || c.page_bytes >= ((int64_t)1 << 40) || c.head_bytes >= ((int64_t)1 << 40) || c.slot_bytes >= ((int64_t)1 << 40)) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)(hf ? c.heads : c.page_size), (cuuint64_t)(hf ? c.page_size : c.heads),
+                          (cuuint64_t)c.n_pages};
+    cuuint64_t strides[3] = {(cuuint64_t)(hf ? c.head_bytes : c.slot_bytes), (cuuint64_t)(hf ? c.slot_bytes : c.head_bytes),
+                             (cuuint64_t)c.page_bytes};
+    cuuint32_t box[4] = {(cuuint32_t)box_values, (cuuint32_t)(hf ? 1 : box_slots), (cuuint32_t)(hf ? box_slots : 1), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return encoder()(m, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims,
+                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Common device gate: a cc 10.3 device must be current.
