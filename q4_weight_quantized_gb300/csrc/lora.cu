@@ -553,14 +553,15 @@ cudaError_t launch_tile(LoraArgs &a, bool vec, unsigned tiles, cudaStream_t s) {
     const cudaError_t e = smem > 32 * 1024 ? ensure_smem((const void *)kern, smem) : cudaSuccess;
     if (e != cudaSuccess) return e;
     // clusters: one an adapter (a token, if there are fewer), and as many as the GPU holds, where few adapters can share them
-    static const unsigned resident = [] {
+    static const unsigned resident = [&] {
         cudaLaunchAttribute of[1] = {};
         of[0].id = cudaLaunchAttributeClusterDimension;
         of[0].val.clusterDim = {kMaxCluster, 1, 1};
         cudaLaunchConfig_t c = {};
         c.gridDim = dim3(kMaxCluster), c.blockDim = dim3(W * 32), c.dynamicSmemBytes = smem, c.attrs = of, c.numAttrs = 1;
         int n = 0;
-        return cudaOccupancyMaxActiveClusters(&n, tile_kernel<NT, U, W, G, false>, &c) == cudaSuccess && n > 0 ? (unsigned)n : 1u;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &c) != cudaSuccess) (void)cudaGetLastError();
+        return n > 0 ? (unsigned)n : 1u;
     }();
     const unsigned clusters = tiles > resident ? tiles : resident;
     return launch_pdl(kern, dim3(ctas, clusters), dim3(W * 32), smem, s, dim3(ctas), a);

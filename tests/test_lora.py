@@ -4,6 +4,10 @@ Products are exact; a value is the sum of y, and of R inner values times b, each
 rounded to 2^-24 of a partial sum that is at most the sum of the magnitudes `mag`, and at most (K / 16 + R / 16 + 30) such
 additions on the way of a product (MMA steps, and the joins of warps, parts, pieces and y; the order inside an MMA step is
 counted as 16), the error is at most mag * (K / 16 + R + 60) * 2^-24."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -186,3 +190,35 @@ def test_lora_on_another_stream_in_a_graph_and_after_a_product(T, ref, syn):
         q4k.q4k_gemm(wd, N, K, p["x"], T, K, base, N, gws, size)
         check(dict(p, y=base), y)
     q4k.q4k_check_device()
+
+
+@pytest.mark.parametrize("nA,N,K,R,T,ids,pad_y,off_y", [
+    (1024, 300, 64, 16, 192, 1023, 0, 0), (1024, 72, 64, 8, 192, "runs", 0, 0), (40, 6526, 768, 16, 83, 5, 0, 0),
+    (10, 11559, 512, 128, 15, 3, 1, 0), (30, 20000, 64, 8, 3, "mixed", 0, 0), (8, 17, 4096, 64, 150, "runs", 0, 0),
+    (16, 1024, 264, 128, 100, "runs", 0, 0), (6, 2000, 96, 32, 190, "mixed", 4, 0), (9, 640, 8192, 64, 1, 8, 0, 0),
+    (1, 2048, 328, 128, 838, "runs", 0, 0), (3, 515, 4096, 8, 1028, "runs", 0, 1), (20, 333, 336, 64, 700, "mixed", 0, 0),
+    (2, 1030, 200, 32, 500, "mixed", 2, 0), (1, 128, 64, 40, 194, 0, 0, 0),
+])
+def test_few_adapters_share_the_gpu(nA, N, K, R, T, ids, pad_y, off_y):
+    """Clusters by groups of tokens and parts of the columns; tiles over several CTAs; pieces split once a CTA."""
+    p = make(nA, N, K, R, T, ids, pad_y=pad_y, off_y=off_y)
+    got = call(p, copy_of(p["y"]))
+    check(p, got)
+    assert torch.equal(call(p, copy_of(p["y"])), got)
+    q4k.q4k_check_device()
+
+
+def test_the_first_call_of_a_process_leaves_no_error_behind():
+    code = """
+import torch, q4_weight_quantized_gb300 as q4k
+for R in (128, 64, 32, 16, 8):
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+    y, ws = torch.ones(4, 64, device="cuda"), torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    q4k.q4k_lora_add(2, 64, 64, R, z(2, R, 64), z(2, 64, R), None, None, torch.zeros(4, dtype=torch.int32, device="cuda"), z(4, 64), 4, 64,
+                     y, 64, ws, ws.numel(), None)
+    assert float((y + 1).sum()) == 512  # (a launch that looks for errors)
+q4k.q4k_check_device()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
