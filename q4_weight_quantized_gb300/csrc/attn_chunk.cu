@@ -27,8 +27,8 @@
 // A slot that some rows of a unit see and others do not may hold values that are not finite: those are taken out of the
 // product (0 * infinity would reach every row) and added to the rows that see them at the end.
 //
-// Measured, heads of 128, 40 of them on 8 KV heads: a prompt of 8192 in 515 us (1335 TFLOP/s), 512 tokens after 65536 in
-// 490 us (1410), from an e4m3 cache 620 us; with a softcap 750 TFLOP/s.  Two tiles of 128 rows and 128 slots take 1.8 us: 1.1 of
+// Measured, heads of 128, 40 of them on 8 KV heads: a prompt of 8192 in 520 us (1320 TFLOP/s), 512 tokens after 65536 in
+// 485 us (1420), from an e4m3 cache 625 us; with a softcap 750 TFLOP/s.  Two tiles of 128 rows and 128 slots take 1.8 us: 1.1 of
 // them (2048 cycles of MMAs) is the tensor cores'; softmax -> P V, Q K^T -> softmax of each tile is a chain that two tiles
 // cover to that extent.  A unit's end and start cost as much as 5 such places (kExtra; 3: 559 us for the prompt).
 #include <cuda_fp16.h>
