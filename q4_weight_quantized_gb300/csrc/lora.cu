@@ -18,7 +18,7 @@
 // Bound by HBM: of many tokens by y, read and written once, of few by the adapters' matrices and by latency.
 // Measured: 32 tokens, 24 adapters of rank 16, 5120 x 5120 10 us (11.1 as two launches); 64 tokens, 16 adapters of rank up
 // to 64, 5120 -> 17408 22 us (45 as two launches); 83 tokens of one adapter of rank 16, 768 -> 6526 14 us (54 by one cluster);
-// 4096 tokens, 4 adapters of rank 16, 5120 -> 17408 124 us: 4.9 TB/s, of which expand_kernel about 100 (5.7 TB/s); 6944 tokens of
+// 4096 tokens, 4 adapters of rank 16, 5120 -> 17408 122 us: 5.0 TB/s, of which expand_kernel about 100 (5.7 TB/s); 6944 tokens of
 // rank 128, 408 -> 5120 118 us, the issue of three products for one (302 with each warp splitting the inner sums for itself).
 #include <cuda_runtime.h>
 
@@ -580,7 +580,7 @@ cudaError_t launch_lora_add(const DeviceInfo &di, LoraArgs &a, cudaStream_t s) {
     cudaError_t e = launch_moe_route(a.ids, a.T, a.n_adapters, a.offsets, a.perm, false, a.tiles, a.n_tiles, s);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)moe_max_tiles(a.n_adapters, a.T);
-    e = a.R <= 8 ? launch_shrink<1, 4, 8>(a, tiles, s) : a.R <= 16 ? launch_shrink<2, 4, 8>(a, tiles, s)
+    e = a.R <= 8 ? launch_shrink<1, 4, 8>(a, tiles, s) : a.R <= 16 ? launch_shrink<2, 2, 8>(a, tiles, s)
       : a.R <= 32 ? launch_shrink<4, 2, 8>(a, tiles, s) : a.R <= 64 ? launch_shrink<8, 2, 8>(a, tiles, s)
                   : launch_shrink<16, 1, 4>(a, tiles, s);
     if (e != cudaSuccess) return e;
