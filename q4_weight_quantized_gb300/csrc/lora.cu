@@ -19,7 +19,7 @@
 // Measured: 32 tokens, 24 adapters of rank 16, 5120 x 5120 10 us (11.1 as two launches); 64 tokens, 16 adapters of rank up
 // to 64, 5120 -> 17408 22 us (45 as two launches); 83 tokens of one adapter of rank 16, 768 -> 6526 14 us (54 by one cluster);
 // 4096 tokens, 4 adapters of rank 16, 5120 -> 17408 122 us: 5.0 TB/s, of which expand_kernel about 100 (5.7 TB/s); 6944 tokens of
-// rank 128, 408 -> 5120 118 us, the issue of three products for one (302 with each warp splitting the inner sums for itself).
+// rank 128, 408 -> 5120 111 us (118 with 32 columns a warp, 148 with 16), the issue of three products for one (302 with each warp splitting the inner sums for itself).
 #include <cuda_runtime.h>
 
 #include "decode_ops.h"
@@ -584,8 +584,8 @@ cudaError_t launch_lora_add(const DeviceInfo &di, LoraArgs &a, cudaStream_t s) {
       : a.R <= 32 ? launch_shrink<4, 2, 8>(a, tiles, s) : a.R <= 64 ? launch_shrink<8, 2, 8>(a, tiles, s)
                   : launch_shrink<16, 1, 4>(a, tiles, s);
     if (e != cudaSuccess) return e;
-    return a.R <= 16 ? launch_expand<1, 2>(a, vec, tiles, s) : a.R <= 32 ? launch_expand<2, 4>(a, vec, tiles, s)
-         : a.R <= 64 ? launch_expand<4, 2>(a, vec, tiles, s) : launch_expand<8, 2>(a, vec, tiles, s);
+    return a.R <= 16 ? launch_expand<1, 2>(a, vec, tiles, s) : a.R <= 32 ? launch_expand<2, 3>(a, vec, tiles, s)
+         : a.R <= 64 ? launch_expand<4, 2>(a, vec, tiles, s) : launch_expand<8, 3>(a, vec, tiles, s);
 }
 
 }  // namespace q4k
