@@ -53,6 +53,7 @@ def in_eight(v):
     s = (a / np.float32(127)).astype(np.float32)
     with np.errstate(all="ignore"):
         q = np.minimum(np.rint(np.abs(x) / s[..., None]), 127)
+    q = np.where(np.isinf(x), 127, q)
     q = np.where(a[..., None] > 0, np.copysign(q, x), 0)
     return q.reshape(v.shape).astype(np.int8), s
 
