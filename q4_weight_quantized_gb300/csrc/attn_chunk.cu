@@ -65,8 +65,13 @@ struct Cfg {
     // for values up to 2^111
     static constexpr float JUMP = E4M3 ? kSlack : 16.f;
     static constexpr int QBYTES = ROWS * D * 2;
-    static constexpr int PLAN = 576, MISC = 768 + PLAN + (E4M3 ? 2 * ROWS : 0);  // barriers and flags, a small call's list, an e4m3
-                                                                                 // cache's factors of two units' rows
+    // An e4m3 cache's factors of a unit's rows are written with its queries, once the last scores of the unit before are done, and
+    // read with its first scores.  Two tiles of rows: those scores are issued behind the weights of every unit before that one, so
+    // one unit's factors at most are unread.  One: scores wait for the products of two tiles before, so the weights may be behind by
+    // two whole units of one tile each, besides the one that is written (three, rounded up to a power of two).
+    static constexpr uint32_t FACTORS = NT == 2 ? 2 : 4;
+    static constexpr int PLAN = 576, MISC = 768 + PLAN + (E4M3 ? (int)FACTORS * ROWS : 0);  // barriers and flags, a small call's list, the
+                                                                                            // factors
     static constexpr int RAW = E4M3 ? BN * D : 0;      // bytes of a tile as it lies in an e4m3 cache: one of keys, one of values
     static constexpr int SMEM = QBYTES + NS * SLOT + 2 * RAW + MISC + 1024;  // (+ slack to align the base)
     static constexpr uint32_t S_COL = 0, O_COL = NT == 2 ? 2 * BN : 2 * BN;
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc_p + 516);
     volatile int *const bad_pages = reinterpret_cast<volatile int *>(misc_p + 524); // a page id was out of range
     volatile int *const bad_seen = reinterpret_cast<volatile int *>(misc_p + 520);  // a value that is not finite was taken out
-    volatile uint8_t *const q_factor = misc_p + 768 + C::PLAN;  // [2][C::ROWS]: exponents (biased by 127) of the factors
+    volatile uint8_t *const q_factor = misc_p + 768 + C::PLAN;  // [C::FACTORS][C::ROWS]: exponents (biased by 127) of the factors
     volatile uint32_t *const page_mask = reinterpret_cast<volatile uint32_t *>(misc_p + 640);      // [kMetaRing][4]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned int *const status = a.c.status;
@@ -610,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                 if constexpr (C::E4M3) {
                     if (i == u.lo) {  // (written before the tile's queries were there)
                         // (not 0, with which a masked score would give NaN)
-                        cc = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)q_factor[(units & 1) * C::ROWS + t * 128 + row_in] << 23), 1.17549435e-38f);
+                        cc = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)q_factor[units % C::FACTORS * C::ROWS + t * 128 + row_in] << 23), 1.17549435e-38f);
                         f = a.softcap > 0.f ? 1.f : cc;
                     }
                 }
@@ -1017,8 +1022,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                             v.z = pack_f16(lo_f32(v.z) * f, hi_f32(v.z) * f), v.w = pack_f16(lo_f32(v.w) * f, hi_f32(v.w) * f);
                             sts128(to, v);
                         }
-                        // the way back, for the row's softmax (which has read those of two units before)
-                        q_factor[(units & 1) * C::ROWS + t * 128 + row] = (uint8_t)(127 - shift);
+                        // the way back, for the row's softmax (which has read those that lay here, see FACTORS)
+                        q_factor[units % C::FACTORS * C::ROWS + t * 128 + row] = (uint8_t)(127 - shift);
                     }
                 }
                 fence_proxy_async_smem();
