@@ -64,6 +64,9 @@ struct Cfg {
     // how far (log2) a score may exceed the maximum that its tile's weights are taken by: what f16 holds, and what leaves O room
     // for values up to 2^111
     static constexpr float JUMP = E4M3 ? kSlack : 16.f;
+    // Soft caps from which on the short form of c tanh(s / c), off by 3 10^-7 c, adds more to a weight's error than a thirteenth of
+    // half a step of its 16 bits.
+    static constexpr float LARGE_CAP = E4M3 ? 64.f : 512.f;
     static constexpr int QBYTES = ROWS * D * 2;
     // An e4m3 cache's factors of a unit's rows are written with its queries, once the last scores of the unit before are done, and
     // read with its first scores.  Two tiles of rows: those scores are issued behind the weights of every unit before that one, so
@@ -473,6 +476,16 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap &m, int
         : "memory");
 }
 
+// c tanh(s / c) in units of log2 for a large cap c, s = score * cc / log2(e).  The form by the exponential is off by 3 10^-7 c (the roundings
+// of 1 + e^(2 s / c) and of its reciprocal), however small s is: it would lose scores far below the cap.  They have the odd series,
+// off by 2^-26 of s up to |s / c| = 1/4; above that 3 10^-7 c is 2^-19 of s.
+__device__ __forceinline__ float large_cap(float score, float cc, const ChunkArgs &a) {
+    const float t = score * (cc * a.cap_t), t2 = t * t;
+    const float series = fmaf(t2, fmaf(t2, fmaf(t2, fmaf(t2, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+    const float far = fmaf(-2.f, rcp_approx(1.f + ex2_approx(t * (2.f * kLog2e))), 1.f) * fminf(a.softcap * kLog2e, 3.4e38f);
+    return fabsf(t) < 0.25f ? score * cc * series : far;
+}
+
 // SMALL: the CTAs list the work themselves.  CAP: a softcap, taken in the weights' pass (without it a softcap counts as a special
 // case, a pass of its own).
 template <typename C, bool SMALL, bool CAP>
@@ -663,9 +676,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                                 }
                                 if (fresh && a.softcap > 0.f) {
                                     // c tanh(s / c) = c (1 - 2 / (1 + e^(2 s / c))), in units of log2
+                                    if (!SMALL && !CAP && a.large_cap) {
 #pragma unroll
-                                    for (int k = 0; k < 32; ++k)
-                                        v[k] = __float_as_uint(fmaf(-2.f * out, rcp_approx(1.f + ex2_approx(__uint_as_float(v[k]) * in)), out));
+                                        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(large_cap(__uint_as_float(v[k]), cc, a));
+                                    } else {
+#pragma unroll
+                                        for (int k = 0; k < 32; ++k)
+                                            v[k] = __float_as_uint(fmaf(-2.f * out, rcp_approx(1.f + ex2_approx(__uint_as_float(v[k]) * in)), out));
+                                    }
                                     changed = true;
                                 }
                                 if (__any_sync(0xFFFFFFFFu, there != 0xFFFFFFFFu)) {
@@ -1424,6 +1442,11 @@ cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
     // plan_kernel).  The branch inside one kernel costs the others 1 to 5 %: registers.
     const int64_t units = a.T * a.group / C::ROWS + (a.c.batch < a.T ? a.c.batch : a.T);
     bool small = a.c.batch < kSmall && units <= kSmall;
+    a.large_cap = a.softcap > C::LARGE_CAP;
+    a.cap_t = a.large_cap ? 0.69314718f / a.softcap : 0.f;
+    // A large cap is a special case of the kernel for large calls (5.4 us for two tiles of 128 rows and 128 slots): its code in the
+    // small calls' kernel costs each of them (512 tokens after 65536 from an e4m3 cache: 638 us instead of 624).
+    if (a.large_cap) return launch<C, false, false>(di, a, s);
     if (a.softcap > 0.f) {
         // A soft cap within the weights' pass: 3.4 us for two tiles of 128 rows and 128 slots, 4.4 as a special case (heads of
         // 128).  A small call's kernel has only the latter: where its CTAs may have more than a few tiles each, not that one.

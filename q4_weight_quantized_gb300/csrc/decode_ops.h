@@ -155,6 +155,8 @@ struct ChunkArgs {
     float score_sign;
     uint32_t group_mul, group_shift;  // row / group for 0 <= row < 2^31 (see KvView)
     float softcap, cap_in;        // and 2 / softcap
+    int32_t large_cap;            // a cap beside which scores may be very small,
+    float cap_t;                  // and ln 2 / softcap
     float v_scale;
     int32_t shares;
     int32_t box_slots;            // slots of a tensor copy's box: what divides a page, up to 32; 0: none can be made
