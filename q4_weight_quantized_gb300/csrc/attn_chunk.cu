@@ -629,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                     if (i == u.lo) {  // (written before the tile's queries were there)
                         // (not 0, with which a masked score would give NaN)
                         cc = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)q_factor[units % C::FACTORS * C::ROWS + t * 128 + row_in] << 23), 1.17549435e-38f);
+                        cc = fminf(cc, a.cc_max);
                         f = a.softcap > 0.f ? 1.f : cc;
                     }
                 }
@@ -1442,6 +1443,9 @@ cudaError_t launch(const DeviceInfo &di, ChunkArgs &a, cudaStream_t s) {
     // plan_kernel).  The branch inside one kernel costs the others 1 to 5 %: registers.
     const int64_t units = a.T * a.group / C::ROWS + (a.c.batch < a.T ? a.c.batch : a.T);
     bool small = a.c.batch < kSmall && units <= kSmall;
+    // (a factor of infinity would give no number for a score of 0)
+    a.cc_max = a.softcap > 0.f ? 3e38f / a.cap_in : INFINITY;
+    if (!C::E4M3) a.scale_log2 = a.scale_log2 < a.cc_max ? a.scale_log2 : a.cc_max;
     a.large_cap = a.softcap > C::LARGE_CAP;
     a.cap_t = a.large_cap ? 0.69314718f / a.softcap : 0.f;
     // A large cap is a special case of the kernel for large calls (5.4 us for two tiles of 128 rows and 128 slots): its code in the

@@ -155,6 +155,7 @@ struct ChunkArgs {
     float score_sign;
     uint32_t group_mul, group_shift;  // row / group for 0 <= row < 2^31 (see KvView)
     float softcap, cap_in;        // and 2 / softcap
+    float cc_max;                 // a score's factor, at most: cap_in times it is finite
     int32_t large_cap;            // a cap beside which scores may be very small,
     float cap_t;                  // and ln 2 / softcap
     float v_scale;

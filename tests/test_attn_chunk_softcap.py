@@ -38,3 +38,16 @@ def test_scores_on_both_sides_of_a_large_cap(dtype, softcap):
     o = run(k, v, table, starts, lens, q, scale, softcap, 0, ks, vs)
     q4k.q4k_check_device()
     check(o, reference(k, v, table, starts, lens, q, scale, softcap, 0, ks, vs), D, dtype == F8, norm=False)
+
+
+@pytest.mark.parametrize("new,lens", [([40], [170]), ([900, 1], [3000, 500])])
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_the_smallest_caps(new, lens, dtype):
+    """No score is left: every slot that a row sees counts the same, those of keys or queries of 0, too."""
+    g = gen_of(33)
+    k, v, table, _, _, starts, q = make(128, dtype, 16, "phsd", 2, 4, new, lens, g)
+    (k.view(torch.uint8) if dtype == F8 else k)[int(table[0, 2])] = 0
+    q[3] = 0
+    for softcap, scale in ((1e-38, 50.0), (1e-42, 50.0), (1e-38, -1e30)):
+        o = run(k, v, table, starts, lens, q, scale, softcap)
+        check(o, reference(k, v, table, starts, lens, q, 0.0), 128, dtype == F8)
