@@ -250,11 +250,30 @@ struct Columns {
                 b[i][s][0] = w.x, b[i][s][1] = w.y;
             }
     }
-    __device__ __forceinline__ void cut(uint32_t (&b)[2][KS][2]) const {
+    // (is any of the lane's values not finite?  0 times it is no number)
+    __device__ __forceinline__ bool cut(uint32_t (&b)[2][KS][2]) const {
+        uint32_t sum = 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int s = 0; s < KS; ++s) b[i][s][0] &= mask[s][0], b[i][s][1] &= mask[s][1];
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    b[i][s][x] &= mask[s][x];
+                    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(b[i][s][x]), "r"(0u));
+                }
+        return (sum & 0x7FFF7FFFu) != 0;
+    }
+    __device__ __forceinline__ void finite_only(uint32_t (&b)[2][KS][2]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t &p = b[i][s][x];
+                    p &= ((p & 0x7F80u) != 0x7F80u ? 0x0000FFFFu : 0u) | ((p & 0x7F800000u) != 0x7F800000u ? 0xFFFF0000u : 0u);
+                }
     }
 };
 // Four values of a row of y from column n on (row null: none)
@@ -291,6 +310,25 @@ __device__ __forceinline__ void multiply(float (&acc)[2][4], const uint32_t (&fr
     for (int k = 2; k >= 0; --k)
 #pragma unroll
         for (int i = 0; i < 2; ++i) mma_bf16_16816(acc[i], frag[k], b[i][s][0], b[i][s][1], acc[i]);
+}
+// Values of B that are not finite are taken out of the product: a piece of an inner value may be 0 where the value is not, and 0 *
+// infinity is no number.  What they add to columns n .. n + columns - 1 of rows list[begin .. end - 1], whose inner values v() gives,
+// by the warp that adds the product to them.
+template <typename V>
+__device__ __forceinline__ void add_infinite(const LoraArgs &a, const Tile &tile, int64_t n, int columns, const int *list, int begin, int end, V &&v) {
+    __syncwarp();
+#pragma unroll 1
+    for (int i = threadIdx.x & 31; i < columns && n + i < a.N; i += 32) {
+        const uint16_t *b = a.b + ((int64_t)tile.adapter * a.N + n + i) * a.R;
+#pragma unroll 1
+        for (int r = 0; r < tile.rank; ++r) {
+            const float x = __uint_as_float((uint32_t)__ldg(b + r) << 16);
+            if (isfinite(x)) continue;
+#pragma unroll 1
+            for (int m = begin; m < end; ++m) a.y[list[m] * a.ldy + n + i] += x * v(m, r);
+        }
+    }
+    __syncwarp();
 }
 __device__ __forceinline__ float4 plus(float4 y, const float (&acc)[2][4], int h) {
     return make_float4(y.x + acc[0][2 * h], y.y + acc[0][2 * h + 1], y.z + acc[1][2 * h], y.w + acc[1][2 * h + 1]);
@@ -346,25 +384,45 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
     load(begin, even);
     pdl_wait();
     pdl_trigger();
+    // values of B that are not finite: what they add comes first, then the products without them
+    auto cut = [&] {
+        bool infinite = false;
 #pragma unroll
-    for (int c = 0; c < CG; ++c) columns.cut(b[c]);
+        for (int c = 0; c < CG; ++c) infinite |= columns.cut(b[c]);
+        if (!__any_sync(0xFFFFFFFFu, infinite)) return;
+#pragma unroll
+        for (int c = 0; c < CG; ++c) columns.finite_only(b[c]);
+        add_infinite(a, tile, n0, 16 * CG, list, begin, end, [&](int m, int r) { return __ldcg(a.v + (int64_t)list[m] * a.R + r); });
+        load(begin, even);
+        if (KS == 1 && begin + 16 < end) load(begin + 16, odd);
+    };
     if constexpr (KS == 1) {
-        auto finish = [&](int m0, const Rows &r) {
+        auto finish = [&](const float4 (&t)[1][2], const Rows &r) {
             float acc[CG][2][4] = {};
-            float4 t[1][2];
             uint32_t frag[1][3][4];
-            load_v(m0, 0, t);
             split_rows<1>(t, frag);
 #pragma unroll
             for (int c = 0; c < CG; ++c) multiply<KS>(acc[c], frag[0], b[c], 0);
             store(r, acc);
         };
-        for (int m0 = begin; m0 < end; m0 += 32) {
-            if (m0 + 16 < end) load(m0 + 16, odd);
-            finish(m0, even);
+        auto rest = [&](int m0, const Rows &r) {
+            float4 t[1][2];
+            load_v(m0, 0, t);
+            finish(t, r);
+        };
+        {
+            float4 t[1][2];
+            if (begin + 16 < end) load(begin + 16, odd);
+            load_v(begin, 0, t);
+            cut();
+            finish(t, even);
+        }
+        for (int m0 = begin + 16; m0 < end; m0 += 32) {
+            if (m0 + 16 < end) load(m0 + 16, even);
+            rest(m0, odd);
             if (m0 + 16 >= end) break;
-            if (m0 + 32 < end) load(m0 + 32, even);
-            finish(m0 + 16, odd);
+            if (m0 + 32 < end) load(m0 + 32, odd);
+            rest(m0 + 16, even);
         }
     } else {
         // higher ranks: the warps split the 16 tokens' inner values once for all of them, a step or more each, one group ahead
@@ -403,6 +461,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const LoraArgs a) {
             store(r, acc);
         };
         fetch(begin);
+        cut();
         split(0);
         __syncthreads();
         for (int m0 = begin; m0 < end; m0 += 32) {
@@ -494,12 +553,14 @@ __global__ void __launch_bounds__(W * 32, NT <= 4 ? 2 : 1) tile_kernel(const Lor
 #pragma unroll
             for (int c = 0; c < G; ++c) {
                 const int64_t at = n + 16 * W * c;
-                columns.cut(t.b[c]);
+                const bool infinite = __any_sync(0xFFFFFFFFu, columns.cut(t.b[c]));
+                if (infinite) columns.finite_only(t.b[c]);
                 float acc[2][4] = {};
 #pragma unroll
                 for (int s = 0; s < KS; ++s) multiply<KS>(acc, frag[s], t.b[c], s);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) store_y<VEC>(a, at < last ? rows[h] : nullptr, at + 4 * tq, plus(t.y[c][h], acc, h));
+                if (infinite) add_infinite(a, tile, at, 16, list, m0, min(m0 + 16, tile.count), [&](int m, int r) { return v[m - m0][r]; });
             }
         };
         constexpr int64_t STEP = 16 * W * G;

@@ -222,3 +222,37 @@ q4k.q4k_check_device()
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("nA,N,K,R,T", [(2, 130, 64, 8, 5), (3, 300, 136, 16, 40), (2, 257, 64, 32, 100), (2, 96, 72, 64, 190), (1, 640, 64, 128, 33),
+                                        (3, 200, 64, 8, 500), (2, 333, 136, 16, 700), (2, 128, 64, 24, 400), (2, 260, 64, 64, 300), (3, 96, 72, 128, 600)])
+@pytest.mark.parametrize("whole", [False, True])
+def test_lora_infinities_within_the_rank(nA, N, K, R, T, whole):
+    """An infinite b times an inner value is infinite whatever the value's bits (so that parts of it may be 0); 0 * infinity is no
+    number; other columns are what they are without."""
+    p = make(nA, N, K, R, T, "mixed", seed=7)
+    p["ranks"][:] = R - 3
+    p["a"], p["b"] = (torch.nan_to_num(p[n], nan=0.5, posinf=0.25) for n in "ab")
+    p["scales"][:] = torch.tensor([1.0, -0.5, 2.0])[:nA]
+    if not whole:  # inner values of 8 bits: one product each
+        at = torch.arange(T, device="cuda") % K
+        value = torch.where(torch.arange(T, device="cuda") % 3 == 0, -2.0, 0.5)
+        p["x"].zero_()
+        p["x"][torch.arange(T, device="cuda"), at] = value.to(BF)
+        p["x"][T // 2] = 0
+    inf = float("inf")
+    for i, (n, r, v) in enumerate([(1, 0, inf), (2, R - 4, -inf), (N - 1, R // 2, inf), (N // 2, 1, float("nan")), (N // 2 + 3, 2, inf)]):
+        p["b"][i % nA, n, r] = v
+    p["b"][0, 17, 3:5] = torch.tensor([inf, -inf])
+    got = np64(call(p, p["y"].clone()))
+    f = lambda t: t.float().cpu().numpy()  # noqa: E731
+    with np.errstate(invalid="ignore"):
+        want = step_ref.lora_add(f(p["a"]), f(p["b"]), p["ranks"].tolist(), p["scales"].tolist(), p["ids"].tolist(), f(p["x"])[:, :K],
+                                 f(p["y"]))[0]
+    odd = ~np.isfinite(want)
+    assert odd.any() and np.isinf(want).any()
+    assert np.array_equal(np.nan_to_num(want[odd], nan=7.0, posinf=8.0, neginf=9.0), np.nan_to_num(got[odd], nan=7.0, posinf=8.0, neginf=9.0))
+    p["b"] = torch.nan_to_num(p["b"], nan=0.0, posinf=0.0, neginf=0.0)
+    clean = np64(call(p, p["y"].clone()))
+    assert np.array_equal(got[~odd], clean[~odd])
+    q4k.q4k_check_device()
