@@ -264,6 +264,8 @@ struct Columns {
                 }
         return (sum & 0x7FFF7FFFu) != 0;
     }
+    // in place of each such value 1 with its sign: what it adds has the sign of what the value itself adds later (an infinite inner
+    // value times 0 would be no number)
     __device__ __forceinline__ void finite_only(uint32_t (&b)[2][KS][2]) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -272,7 +274,8 @@ struct Columns {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     uint32_t &p = b[i][s][x];
-                    p &= ((p & 0x7F80u) != 0x7F80u ? 0x0000FFFFu : 0u) | ((p & 0x7F800000u) != 0x7F800000u ? 0xFFFF0000u : 0u);
+                    if ((p & 0x7F80u) == 0x7F80u) p = (p & 0xFFFF8000u) | 0x3F80u;
+                    if ((p & 0x7F800000u) == 0x7F800000u) p = (p & 0x8000FFFFu) | 0x3F800000u;
                 }
     }
 };
@@ -311,7 +314,7 @@ __device__ __forceinline__ void multiply(float (&acc)[2][4], const uint32_t (&fr
 #pragma unroll
         for (int i = 0; i < 2; ++i) mma_bf16_16816(acc[i], frag[k], b[i][s][0], b[i][s][1], acc[i]);
 }
-// Values of B that are not finite are taken out of the product: a piece of an inner value may be 0 where the value is not, and 0 *
+// Values of B that are not finite are no part of the product: a piece of an inner value may be 0 where the value is not, and 0 *
 // infinity is no number.  What they add to columns n .. n + columns - 1 of rows list[begin .. end - 1], whose inner values v() gives,
 // by the warp that adds the product to them.
 template <typename V>

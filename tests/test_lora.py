@@ -256,3 +256,23 @@ def test_lora_infinities_within_the_rank(nA, N, K, R, T, whole):
     clean = np64(call(p, p["y"].clone()))
     assert np.array_equal(got[~odd], clean[~odd])
     q4k.q4k_check_device()
+
+
+@pytest.mark.parametrize("R,T", [(8, 5), (16, 60), (64, 100), (128, 30), (8, 400), (16, 500), (32, 300), (128, 250)])
+def test_lora_infinite_inner_values_and_infinities(R, T):
+    """One infinite x and adapters of rank 1: infinity times each b, an infinite one or 0 included."""
+    p = make(2, 100, 64, R, T, "mixed", seed=9)
+    p["ranks"][:] = 1
+    p["a"][:, 0, 5], p["b"][:, 3, 0], p["b"][:, 4, 0] = 2.0, float("inf"), -float("inf")
+    p["b"][:, 5, 0], p["b"][0, 6, 0] = 0.0, float("nan")
+    p["x"][::3, 5] = float("inf")
+    p["x"][1::3, 5] = -float("inf")
+    got = np64(call(p, p["y"].clone()))
+    f = lambda t: t.float().cpu().numpy()  # noqa: E731
+    with np.errstate(invalid="ignore"):
+        want = step_ref.lora_add(f(p["a"]), f(p["b"]), [1, 1], p["scales"].tolist(), p["ids"].tolist(), f(p["x"])[:, :64], f(p["y"])[:, :100])[0]
+    odd = ~np.isfinite(want)
+    assert np.isinf(want[:, 3]).any() and np.isnan(want[:, 5]).any() and (~odd).any()
+    assert np.array_equal(np.isfinite(got), ~odd)
+    assert np.array_equal(np.nan_to_num(want[odd], nan=7.0, posinf=8.0, neginf=9.0), np.nan_to_num(got[odd], nan=7.0, posinf=8.0, neginf=9.0))
+    q4k.q4k_check_device()
