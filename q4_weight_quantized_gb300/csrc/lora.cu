@@ -22,6 +22,8 @@
 // rank 128, 408 -> 5120 111 us (118 with 32 columns a warp, 148 with 16), the issue of three products for one (302 with each warp splitting the inner sums for itself).
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "decode_ops.h"
 #include "q4k_ptx.cuh"
 
@@ -579,9 +581,9 @@ __global__ void __launch_bounds__(W * 32, NT <= 4 ? 2 : 1) tile_kernel(const Lor
 }
 
 template <int KS, int CG>
-cudaError_t launch_expand(const LoraArgs &a, bool vec, unsigned tiles, cudaStream_t s) {
+cudaError_t launch_expand(const DeviceInfo &di, const LoraArgs &a, bool vec, unsigned tiles, cudaStream_t s) {
     // (a tile's tokens over 2, 3 or 4 CTAs where that fills four an SM)
-    const int64_t columns = kWarps * 16 * CG, x = (a.N + columns - 1) / columns, z = 4 * 152 / (x * (a.T / kTileTokens + 1));
+    const int64_t columns = kWarps * 16 * CG, x = (a.N + columns - 1) / columns, z = 4 * di.sm_count / (x * (a.T / kTileTokens + 1));
     return launch_pdl(vec ? expand_kernel<KS, CG, true> : expand_kernel<KS, CG, false>,
                       dim3((unsigned)x, tiles, z < 1 ? 1 : z < 4 ? (unsigned)z : 4), dim3(kThreads), 0, s, dim3(1), a);
 }
@@ -595,40 +597,52 @@ unsigned split_k(LoraArgs &a, int64_t splits, int64_t unit) {
 }
 
 template <int NT, int U, int W>
-cudaError_t launch_shrink(LoraArgs &a, unsigned tiles, cudaStream_t s) {
+cudaError_t launch_shrink(const DeviceInfo &di, LoraArgs &a, unsigned tiles, cudaStream_t s) {
     // 16 tokens a CTA (the tokens of a tile over several); K over as many CTAs as an SM holds of them, each with a full round of
     // loads at least (1028 tokens, 17408 -> 515, rank 8: 30 us, 48 by two; 955 tokens, 2048 -> 5120, rank 64: 29 us, 37 by eight)
-    constexpr int64_t kCtas = (NT <= 2 ? 4 : 2) * 152;
+    const int64_t ctas = (NT <= 2 ? 4 : 2) * di.sm_count;
     const unsigned z = kTileTokens / 16;
     const int64_t groups = a.T / 16 + (a.n_adapters < a.T ? a.n_adapters : a.T);  // of 16 tokens, at most
-    int64_t splits = kCtas / groups, most = a.K / (32 * W * U);
+    int64_t splits = ctas / groups, most = a.K / (32 * W * U);
     if (splits > most) splits = most;
     const unsigned n = split_k(a, splits > 1 ? splits : 1, 32 * W);
     return launch_pdl(shrink_kernel<NT, U, W>, dim3(n, tiles, z), dim3(W * 32), 0, s, dim3(n), a);
 }
 
-template <int NT, int U, int W, int G>
-cudaError_t launch_tile(LoraArgs &a, bool vec, unsigned tiles, cudaStream_t s) {
-    const unsigned ctas = kMaxCluster;
-    a.k_chunk = (int32_t)(((a.K + ctas - 1) / ctas + 31) / 32 * 32);
-    auto kern = vec ? tile_kernel<NT, U, W, G, true> : tile_kernel<NT, U, W, G, false>;
+// Clusters of tile_kernel that the device holds at a time, asked once for each kernel and device (1, and asked again, if that fails).
+template <int NT, int U, int W, int G, bool VEC>
+unsigned resident_clusters(int device, int smem) {
+    constexpr int kDevices = 64;
+    static std::atomic<unsigned> kept[kDevices];
+    std::atomic<unsigned> *const at = device < kDevices ? &kept[device] : nullptr;
+    if (at && *at) return *at;
+    cudaLaunchAttribute of[1] = {};
+    of[0].id = cudaLaunchAttributeClusterDimension;
+    of[0].val.clusterDim = {kMaxCluster, 1, 1};
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(kMaxCluster), c.blockDim = dim3(W * 32), c.dynamicSmemBytes = smem, c.attrs = of, c.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, tile_kernel<NT, U, W, G, VEC>, &c) != cudaSuccess) (void)cudaGetLastError();
+    if (n < 1) return 1u;
+    if (at) *at = (unsigned)n;
+    return (unsigned)n;
+}
+
+template <int NT, int U, int W, int G, bool VEC>
+cudaError_t launch_tile(const DeviceInfo &di, const LoraArgs &a, unsigned tiles, cudaStream_t s) {
     constexpr int smem = W * 16 * (NT * 8 + 1) * 4;  // (the adapters' first tokens lie there first: 4 bytes for each of 1024)
     static_assert(smem >= 4 * 1024, "fits");
+    auto kern = tile_kernel<NT, U, W, G, VEC>;
     const cudaError_t e = smem > 32 * 1024 ? ensure_smem((const void *)kern, smem) : cudaSuccess;
     if (e != cudaSuccess) return e;
     // clusters: one an adapter (a token, if there are fewer), and as many as the GPU holds, where few adapters can share them
-    static const unsigned resident = [&] {
-        cudaLaunchAttribute of[1] = {};
-        of[0].id = cudaLaunchAttributeClusterDimension;
-        of[0].val.clusterDim = {kMaxCluster, 1, 1};
-        cudaLaunchConfig_t c = {};
-        c.gridDim = dim3(kMaxCluster), c.blockDim = dim3(W * 32), c.dynamicSmemBytes = smem, c.attrs = of, c.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &c) != cudaSuccess) (void)cudaGetLastError();
-        return n > 0 ? (unsigned)n : 1u;
-    }();
-    const unsigned clusters = tiles > resident ? tiles : resident;
-    return launch_pdl(kern, dim3(ctas, clusters), dim3(W * 32), smem, s, dim3(ctas), a);
+    const unsigned resident = resident_clusters<NT, U, W, G, VEC>(di.device, smem), clusters = tiles > resident ? tiles : resident;
+    return launch_pdl(kern, dim3(kMaxCluster, clusters), dim3(W * 32), smem, s, dim3(kMaxCluster), a);
+}
+template <int NT, int U, int W, int G>
+cudaError_t launch_tile(const DeviceInfo &di, LoraArgs &a, bool vec, unsigned tiles, cudaStream_t s) {
+    a.k_chunk = (int32_t)(((a.K + kMaxCluster - 1) / kMaxCluster + 31) / 32 * 32);
+    return vec ? launch_tile<NT, U, W, G, true>(di, a, tiles, s) : launch_tile<NT, U, W, G, false>(di, a, tiles, s);
 }
 
 }  // namespace
@@ -637,19 +651,19 @@ cudaError_t launch_lora_add(const DeviceInfo &di, LoraArgs &a, cudaStream_t s) {
     const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.ldy % 4 == 0 && a.N % 4 == 0;
     if (!a.tiles) {
         const unsigned tiles = (unsigned)(a.n_adapters < a.T ? a.n_adapters : a.T);
-        return a.R <= 8 ? launch_tile<1, 4, 8, 2>(a, vec, tiles, s) : a.R <= 16 ? launch_tile<2, 4, 8, 2>(a, vec, tiles, s)
-             : a.R <= 32 ? launch_tile<4, 2, 8, 1>(a, vec, tiles, s) : a.R <= 64 ? launch_tile<8, 2, 8, 2>(a, vec, tiles, s)
-                         : launch_tile<16, 1, 8, 1>(a, vec, tiles, s);
+        return a.R <= 8 ? launch_tile<1, 4, 8, 2>(di, a, vec, tiles, s) : a.R <= 16 ? launch_tile<2, 4, 8, 2>(di, a, vec, tiles, s)
+             : a.R <= 32 ? launch_tile<4, 2, 8, 1>(di, a, vec, tiles, s) : a.R <= 64 ? launch_tile<8, 2, 8, 2>(di, a, vec, tiles, s)
+                         : launch_tile<16, 1, 8, 1>(di, a, vec, tiles, s);
     }
     cudaError_t e = launch_moe_route(a.ids, a.T, a.n_adapters, a.offsets, a.perm, false, a.tiles, a.n_tiles, s);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)moe_max_tiles(a.n_adapters, a.T);
-    e = a.R <= 8 ? launch_shrink<1, 4, 8>(a, tiles, s) : a.R <= 16 ? launch_shrink<2, 2, 8>(a, tiles, s)
-      : a.R <= 32 ? launch_shrink<4, 2, 8>(a, tiles, s) : a.R <= 64 ? launch_shrink<8, 2, 8>(a, tiles, s)
-                  : launch_shrink<16, 1, 4>(a, tiles, s);
+    e = a.R <= 8 ? launch_shrink<1, 4, 8>(di, a, tiles, s) : a.R <= 16 ? launch_shrink<2, 2, 8>(di, a, tiles, s)
+      : a.R <= 32 ? launch_shrink<4, 2, 8>(di, a, tiles, s) : a.R <= 64 ? launch_shrink<8, 2, 8>(di, a, tiles, s)
+                  : launch_shrink<16, 1, 4>(di, a, tiles, s);
     if (e != cudaSuccess) return e;
-    return a.R <= 16 ? launch_expand<1, 2>(a, vec, tiles, s) : a.R <= 32 ? launch_expand<2, 3>(a, vec, tiles, s)
-         : a.R <= 64 ? launch_expand<4, 2>(a, vec, tiles, s) : launch_expand<8, 3>(a, vec, tiles, s);
+    return a.R <= 16 ? launch_expand<1, 2>(di, a, vec, tiles, s) : a.R <= 32 ? launch_expand<2, 3>(di, a, vec, tiles, s)
+         : a.R <= 64 ? launch_expand<4, 2>(di, a, vec, tiles, s) : launch_expand<8, 3>(di, a, vec, tiles, s);
 }
 
 }  // namespace q4k
