@@ -502,7 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
     uint32_t *const tmem_holder = reinterpret_cast<uint32_t *>(misc_p + 512);
     volatile int *const abort_flag = reinterpret_cast<volatile int *>(misc_p + 516);
     volatile int *const bad_pages = reinterpret_cast<volatile int *>(misc_p + 524); // a page id was out of range
-    volatile int *const bad_seen = reinterpret_cast<volatile int *>(misc_p + 520);  // a value that is not finite was taken out
+    // 1 + the last tile of slots walked in which a value that is not finite was taken out (0: none); of an e4m3 cache one for each
+    // copying warp (512 tokens after 65536: 624 us, 637 by an atomic maximum of one; a bf16 cache's mixed step: 78 us by that, 81 by four)
+    volatile int *const bad_seen = reinterpret_cast<volatile int *>(misc_p + 528);
     volatile uint8_t *const q_factor = misc_p + 768 + C::PLAN;  // [C::FACTORS][C::ROWS]: exponents (biased by 127) of the factors
     volatile uint32_t *const page_mask = reinterpret_cast<volatile uint32_t *>(misc_p + 640);      // [kMetaRing][4]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -524,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
         mbar_init(bar.done, NT == 2 ? 1 : 2);
         for (int i = 0; i < 2 * kCopyWarps; ++i) mbar_init(bar.raw + 8 * i, 1);
         *abort_flag = 0;
-        *bad_seen = 0;
+        for (int i = 0; i < kCopyWarps; ++i) bad_seen[i] = 0;
         *bad_pages = 0;
         fence_mbar_init();
     }
@@ -791,7 +793,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
             }
             unit_phase ^= 1;
             tc_fence_after();
-            const bool bad = *bad_seen != 0;
+            // in this unit's part, or one of a few that the copies are ahead
+            uint32_t mark = (uint32_t)bad_seen[0];
+            if constexpr (C::E4M3) {
+#pragma unroll
+                for (int i = 1; i < kCopyWarps; ++i) mark = max(mark, (uint32_t)bad_seen[i]);
+            }
+            const bool bad = mark > tile_count - (uint32_t)(u.hi - u.lo);
             // a row that sees slots, all of them -infinity, has no weights: NaN, as 0 / 0 has it
             const float inv = e > bgn ? a.v_scale / l : 0.f;
             const int64_t part_row = (int64_t)(2 * blockIdx.x + (u.lo > 0 ? 0 : 1)) * C::ROWS + t * 128 + row_in;
@@ -1090,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                     }
                 }
             }
-            if (any) *bad_seen = 1;
+            if (any) atomicMax(const_cast<int *>(bad_seen), (int)(shown / 2) + 1);  // (keys and values in turn)
         };
         uint32_t box_bits = 0;   // of the tiles on their way, newest in bit 0: copied by the copy engine?
         auto show = [&](uint32_t upto) {
@@ -1240,7 +1248,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkArgs a, c
                         if (lane == 0) mbar_arrive(bar.full + 8 * slot);
                     }
                 }
-                if (odd) *bad_seen = 1;
+                if (odd) bad_seen[w] = (int)tile_count + 1;
                 fence_proxy_async_smem();  // for the MMAs, and for the copy engine, which may write what has been read
                 __syncwarp();
                 if (lane == 0 && !now.first) mbar_arrive(bar.full + 8 * slot);
