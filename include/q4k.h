@@ -661,7 +661,8 @@ q4k_status q4k_norm_residual_x8(int64_t M, int64_t D, const float *y, int64_t ld
  *   1 <= n_adapters <= 1024; R a multiple of 8, 8 .. 128; K a multiple of 8; N, K <= 2^21;
  *   T <= 2^23
  * Products are exact and sums fp32; the inner sums, times the scale, enter the second
- * product as the sum of three bf16 values, exactly.  A row's last bits do not depend on the
+ * product as the sum of three bf16 values, exactly; a value of b that is not finite adds its own
+ * product with the inner sum.  A row's last bits do not depend on the
  * other rows' adapters, but on K, R, T and n_adapters.
  * Workspace: q4k_lora_add_workspace_size(...) bytes, 256-byte aligned; 0 is returned for
  * arguments that the call would refuse. */
@@ -689,7 +690,9 @@ q4k_status q4k_lora_add(int32_t n_adapters, int64_t N, int64_t K, int32_t R, con
  * rounded to bf16 (each off by 2^-8 at most; for an e4m3 cache, whose values are exact in
  * f16, to f16: by 2^-11, and 2^-32 of the largest), while the sum that divides them is that of the fp32 values: their
  * errors, which add up at random, are of the size of o's own rounding.  (For an e4m3 cache a value of
- * q below 2^-31 of the largest of its row is taken to 2^-39 of that one.)  The work is split over the whole GPU by all
+ * q below 2^-31 of the largest of its row is taken to 2^-39 of that one.)  A softcap may have any
+ * size; beyond its own fp32 roundings a capped score is off by 1.5e-4 at most (e4m3 cache: 2e-5), and by
+ * less for small caps.  The work is split over the whole GPU by all
  * lengths, and split rows are joined in slot order: the same call repeats its bits, but a
  * row's last bits may depend on the rest of the batch, also in batch-invariant mode.
  * Workspace: q4k_attn_chunk_workspace_size(cache, T, n_heads) bytes, 256-byte aligned; 0

@@ -22,13 +22,14 @@
 //     have 8 slots or a multiple, the copy engine does (a box a page's part); else a lane copies 16 bytes at a time and
 //     fills what is not there with zeros (any page size, any strides).  An e4m3 cache's tiles are staged one ahead as
 //     they are and become f16, exactly, keys and values at once; Q becomes f16 by a power of two a row.
-//   - Scores that need more than the scale (a mask's edge, a small call's softcap, maxima so large that the fused product's rounding
-//     counts) are prepared in their place in tensor memory first, so that the pass itself is the same for every tile.
+//   - Scores that need more than the scale (a mask's edge, a small call's softcap or a large one, maxima so large that the fused product's
+//     rounding counts) are prepared in their place in tensor memory first, so that the pass itself is the same for every tile.
 // A slot that some rows of a unit see and others do not may hold values that are not finite: those are taken out of the
 // product (0 * infinity would reach every row) and added to the rows that see them at the end.
 //
 // Measured, heads of 128, 40 of them on 8 KV heads: a prompt of 8192 in 520 us (1320 TFLOP/s), 512 tokens after 65536 in
-// 485 us (1420), from an e4m3 cache 625 us; with a softcap 750 TFLOP/s.  Two tiles of 128 rows and 128 slots take 1.8 us: 1.1 of
+// 487 us (1416), from an e4m3 cache 622 us; with a softcap 760 TFLOP/s, one above 512 (64 of an e4m3 cache) 465.  Heads of 256, 20 on 4: the same
+// chunk in 746 us (925), 966 from an e4m3 cache.  Two tiles of 128 rows and 128 slots take 1.8 us: 1.1 of
 // them (2048 cycles of MMAs) is the tensor cores'; softmax -> P V, Q K^T -> softmax of each tile is a chain that two tiles
 // cover to that extent.  A unit's end and start cost as much as 5 such places (kExtra; 3: 559 us for the prompt).
 #include <cuda_fp16.h>
@@ -77,7 +78,7 @@ struct Cfg {
                                                                                             // factors
     static constexpr int RAW = E4M3 ? BN * D : 0;      // bytes of a tile as it lies in an e4m3 cache: one of keys, one of values
     static constexpr int SMEM = QBYTES + NS * SLOT + 2 * RAW + MISC + 1024;  // (+ slack to align the base)
-    static constexpr uint32_t S_COL = 0, O_COL = NT == 2 ? 2 * BN : 2 * BN;
+    static constexpr uint32_t S_COL = 0, O_COL = 2 * BN;  // (two tiles of S, whatever NT)
     static constexpr uint32_t COLS = 512;
     // registers of a softmax thread and of the others, together those of the launch: 4 * 128.  (A prompt: 512 us,
     // 517 by 192 and 64; an e4m3 cache, whose copies need more: 689 by 192 and 64, 651 by 176 and 80, 636 by 168 and 88.)

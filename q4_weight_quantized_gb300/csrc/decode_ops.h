@@ -129,7 +129,7 @@ struct PlanArgs {
 cudaError_t launch_batch_plan(const DeviceInfo &di, const PlanArgs &a, cudaStream_t s);
 
 constexpr int kMaxChunkShares = 160;  // CTAs of an attention call over chunks, at most (the workspace holds two parts for each)
-// (api.cu; a map is kept for the pools that a thread used last)
+// (api.cu; made anew on each call, none is kept)
 bool make_cache_tmap(CUtensorMap *m, const void *pool, const KvView &c, int box_values, int box_slots, bool swizzle, bool *head_first);
 
 // A unit of rows (chunk_rows() of them at most) of a sequence, the same for every KV head.

@@ -15,6 +15,7 @@
 // tiles themselves, and clusters of CTAs do both products in one launch, the inner sums staying in shared memory; meanwhile a
 // CTA's part of B comes into L2.  Where few adapters have tokens the clusters that the GPU holds are shared out to them: groups
 // of 16 tokens first, then columns, for which each makes the first product again.
+// What is not finite in B is no part of the second product (a piece may be 0, and 0 * infinity is no number); it adds its own.
 // Bound by HBM: of many tokens by y, read and written once, of few by the adapters' matrices and by latency.
 // Measured: 32 tokens, 24 adapters of rank 16, 5120 x 5120 10 us (11.1 as two launches); 64 tokens, 16 adapters of rank up
 // to 64, 5120 -> 17408 22 us (45 as two launches); 83 tokens of one adapter of rank 16, 768 -> 6526 14 us (54 by one cluster);
