@@ -637,9 +637,9 @@ q4k_status q4k_batch_plan(const q4k_kv_cache *cache, const int32_t *seq_lens, co
 /* q4k_norm_residual whose output is (also) 8 bits wide, the input of q4k_gemm_x8: with
  * v = pre(h) in fp32, for each 32 consecutive values of a row a = max |v|, s = a / 127,
  * q = rint(v / s) (ties to even, at most 127 in magnitude), and q = 0, s = 0 where all
- * are zero (q4k_quantize_x8's rule, applied to the fp32 values instead of their bf16
- * roundings).  A block with a NaN gets s = NaN and q = 0, one with an infinity s = infinity
- * and q = +-127 where |v| is infinite, 0 elsewhere.
+ * are zero or a is so small that a / 127 is 0 (q4k_quantize_x8's rule, applied to the fp32
+ * values instead of their bf16 roundings).  A block with a NaN gets s = NaN and q = 0, one with
+ * an infinity s = infinity and q = +-127 where |v| is infinite, 0 elsewhere.
  *   q  int8 [M][D], dense, 4-byte aligned;  s  fp32 [M][D/32], dense
  *   D a multiple of 32; x (bf16, for the other readers of v) and r_out may be NULL
  * Everything else, the rows' bits included, is as in q4k_norm_residual. */

@@ -54,7 +54,7 @@ def in_eight(v):
     with np.errstate(all="ignore"):
         q = np.minimum(np.rint(np.abs(x) / s[..., None]), 127)
     q = np.where(np.isinf(x), 127, q)
-    q = np.where(a[..., None] > 0, np.copysign(q, x), 0)
+    q = np.where(s[..., None] > 0, np.copysign(q, x), 0)
     return q.reshape(v.shape).astype(np.int8), s
 
 

@@ -49,9 +49,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
-// v in 8 bits at the scale s = a / 127, a being the largest |v| of its block
-__device__ __forceinline__ int in_eight(float v, float s, float a) {
-    return a > 0.f ? (int)copysignf(fminf(rintf(fabsf(v) / s), 127.f), v) : 0;
+// v in 8 bits at the scale s = a / 127, a being the largest |v| of its block (so small that s is 0: 0)
+__device__ __forceinline__ int in_eight(float v, float s) {
+    return s > 0.f ? (int)copysignf(fminf(rintf(fabsf(v) / s), 127.f), v) : 0;
 }
 // Four of them as bytes, and s, for a of usual size; false where this may not be the rule's rounding.  s is a times the reciprocal
 // of 127, corrected by its remainder (Markstein's division: the nearest value), and v / s is v times the reciprocal of s, off by
@@ -155,7 +155,7 @@ struct Slice {
                 word[i] = 0;
 #pragma unroll 1
                 for (int x = 0; x < 4; ++x)
-                    word[i] |= ((uint32_t)in_eight(x == 0 ? v[4 * i] : x == 1 ? v[4 * i + 1] : x == 2 ? v[4 * i + 2] : v[4 * i + 3], s[i], a) & 0xFFu) << (8 * x);
+                    word[i] |= ((uint32_t)in_eight(x == 0 ? v[4 * i] : x == 1 ? v[4 * i + 1] : x == 2 ? v[4 * i + 2] : v[4 * i + 3], s[i]) & 0xFFu) << (8 * x);
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -173,7 +173,7 @@ struct Slice {
                     const float a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v[4 * i + x]))));
                     const float s = a / 127.0f;
                     if (!in(i, x)) continue;
-                    q[at(i, x)] = (int8_t)in_eight(v[4 * i + x], s, a);
+                    q[at(i, x)] = (int8_t)in_eight(v[4 * i + x], s);
                     if ((tid & 31) == 0) scale[at(i, x) / 32] = s;
                 }
             }
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_long_kernel(const NormArgs a
             if (a.x) a.x[row * a.ldx + e] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
             if (a.q) {  // (D % 32 == 0: whole warps)
                 const float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(v)))), s = top / 127.0f;
-                a.q[row * D + e] = (int8_t)in_eight(v, s, top);
+                a.q[row * D + e] = (int8_t)in_eight(v, s);
                 if ((threadIdx.x & 31) == 0) a.q_scale[row * (D / 32) + e / 32] = s;
             }
         }

@@ -105,6 +105,23 @@ def test_eight_bits_of_zeros_and_of_no_numbers(D, pad):
     assert np.array_equal(q.cpu().numpy(), wq)
 
 
+@pytest.mark.parametrize("M,D,pad", [(4, 128, 0), (4, 128, 1), (2, 17024, 0), (800, 4096, 0), (2100, 64, 0)])
+def test_eight_bits_of_the_smallest_values(M, D, pad):
+    """Blocks whose largest value is so small that its 127th part is 0: zeros, as blocks of zeros are; a little more, and they are there."""
+    k = torch.arange(M * D, device="cuda").view(M, D // 32, 32)
+    top = 60 + k[:, :, :1] // 32 % 9               # in steps of 2^-149: 60 .. 68 (64 / 127 is the first above a half)
+    h = (k * 37 % (2 * top + 1) - top).to(torch.int32)
+    h[:, :, 5], h[:, :, 9] = 0, top[:, :, 0].to(torch.int32)
+    flat = torch.zeros(M, D + pad, device="cuda")
+    flat[:, :D] = (h.abs() | (h < 0).to(torch.int32) << 31).view(torch.float32).reshape(M, D)
+    q, s = torch.full((M, D), 99, dtype=torch.int8, device="cuda"), torch.full((M, D // 32), -1.0, device="cuda")
+    q4k.q4k_norm_residual_x8(M, D, None, 0, 0, None, None, 0.0, None, 0, 1.0, flat, None, D + pad, q4k.Q4K_RES_FP32, 0, None, None, 0.0,
+                             None, 0, q, s)
+    steps = s.view(torch.int32)
+    assert torch.equal(steps, (top[:, :, 0] >= 64).to(torch.int32))
+    assert torch.equal(q.view(M, D // 32, 32).int(), torch.where((steps > 0)[:, :, None], h.clamp(-127, 127), 0))
+
+
 @pytest.mark.parametrize("M,pad", [(4, 0), (4, 1), (800, 0)])
 def test_eight_bits_near_the_middle_and_over_all_sizes(M, pad):
     """Values at, just below and just above the middle between two whole numbers of steps, at every power of two; scales of any
